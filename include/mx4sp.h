@@ -62,6 +62,8 @@ typedef enum {
 #define MX4_STATUS_BAD_INDEX 0x8u  /* top-k index outside [0, position] */
 #define MX4_STATUS_BAD_VALUE 0x10u /* non-finite fp32 input to mx4_insert */
 #define MX4_STATUS_TIMEOUT 0x20u   /* a kernel gave up a bounded wait (should not happen) */
+#define MX4_STATUS_NO_PAGES 0x40u  /* mx4_fork_pages: the free list ran out */
+#define MX4_STATUS_BAD_REF 0x80u   /* mx4_free_pages: a page that nobody holds */
 
 #define MX4_PAGE_TOKENS 128
 #define MX4_HEAD_DIM 128
@@ -418,6 +420,144 @@ int mx4_decode_steps(int64_t n_steps, const void *h_inputs, size_t h_inputs_stri
                      int64_t ld_scores, int32_t *d_topk_idx, void *topk_ws, size_t topk_ws_bytes,
                      void *dec_ws, size_t dec_ws_bytes, float *d_out, float *h_out,
                      size_t h_out_stride, void *stream, void *h2d_stream, void *d2h_stream);
+
+/* ---------------------------------------------------------------------------
+ * A speculative decode step.  A sequence's drafted tokens are n_nodes[s] <= N nodes
+ * (N <= 64; n_nodes NULL: N each), inserted by mx4_insert as the sequence's last
+ * n_nodes[s] cached tokens in node order: node j is cached token base + j with
+ * base = seq_lens[s] - n_nodes[s], and seq_lens counts them.  Node 0 is the root (the
+ * last token known to stand); a node's parent comes before it.  n_nodes[s] = 0 is an
+ * idle sequence.
+ *
+ * tree_paged_decode -- attention of all nodes of a step over the whole cache, or over
+ * a sliding window and the first tokens, with a tree mask.
+ *
+ * tree_mask[s*N + j] has bit i set where node j sees node i (its ancestors and itself;
+ * bits at or past n_nodes[s] are ignored); NULL is the chain, where j sees 0 .. j.
+ * Node j's depth is d_j = max(1, number of its bits) - 1 and its position base + d_j.
+ * Node j sees
+ *   - cached token i < base      if window == 0, or i > base + d_j - window, or i < sinks;
+ *   - node i, if its bit is set, if window == 0, or d_i > d_j - window, or base + d_i < sinks.
+ * With l_i = scale * q[s][j][h] . dequant(K_i) over the tokens i that it sees (KV head
+ * h / (H / Hkv)):
+ *     out[s][j][h][:] = sum_i softmax(l)_i dequant(V_i)[:],   lse[s][j][h] = ln sum_i e^{l_i}.
+ * A node that sees nothing, and rows j >= n_nodes[s], get zeros and -inf.  Tokens that
+ * a node does not see have no part in its result, whatever their rows hold (NaN too).
+ * N = 1 is the plain single-token decode step.
+ *
+ *   q            bf16 [B, N, H, 128], contiguous, 16-byte aligned
+ *   k_pages, v_pages  uint8 [num_pages, Hkv, 8704] at the given strides (the same for
+ *                both); 32-byte aligned, strides multiples of 32 (they are read by
+ *                tensor copies of the pool)
+ *   block_table  int32 [B, bt_width]; seq_lens int32 [B]; n_nodes int32 [B] or NULL
+ *   tree_mask    uint64 [B, N] or NULL
+ *   window, sinks  >= 0 (sinks counts only with a window)
+ *   out          bf16 [B, N, H, 128]; lse fp32 [B, N, H] or NULL (outputs; out 16-byte
+ *                aligned)
+ *   ws           tree_paged_decode_workspace(B, N, H, Hkv) bytes, 16-byte aligned; the
+ *                size depends on the current device's SM count
+ * Logits, softmax statistics and sums are fp32; the weights are rounded to bf16 for the
+ * product with V, as is the output.  1 <= N <= 64, 1 <= Hkv <= 8, H a multiple of Hkv,
+ * H <= 128, B <= 65535.  A bad length (seq_len < n_nodes, or beyond the block table) gives
+ * zeros and sets MX4_STATUS_BAD_LEN; tokens on a bad page are not seen
+ * (MX4_STATUS_BAD_PAGE).
+ * ------------------------------------------------------------------------- */
+int tree_paged_decode(const uint16_t *q, int64_t B, int N, int H, int Hkv,
+                      const uint8_t *k_pages, const uint8_t *v_pages, int64_t kv_page_stride,
+                      int64_t kv_head_stride, int64_t num_pages, const int32_t *block_table,
+                      int64_t bt_width, const int32_t *seq_lens, const int32_t *n_nodes,
+                      const uint64_t *tree_mask, int64_t window, int64_t sinks, float scale,
+                      uint16_t *out, float *lse, void *ws, size_t ws_bytes, void *stream);
+size_t tree_paged_decode_workspace(int64_t B, int N, int H, int Hkv);
+
+/* ---------------------------------------------------------------------------
+ * verify_drafts -- which drafted tokens stand, and the token after them, from the
+ * target's probabilities and given random numbers, such that the tokens follow the
+ * target's distribution (rejection sampling down the tree, children drawn from the
+ * draft's distribution after their parent).
+ *
+ * From cur = 0, W = target[s][0], T = 1, for j = 1 .. n-1 in order, wherever
+ * parents[s][j] == cur, with x = tokens[s][j] and q = draft[s][cur] (draft NULL: the
+ * one-hot distribution of x, for drafts that were looked up and not drawn):
+ *     if u_accept[s][j] * T * q(x) < W(x):  j stands; cur = j, W = target[s][j], T = 1
+ *     else:  W = max(W - T q, 0), T = sum W; if T is 0, W = target[s][cur] and no
+ *            further child of cur is tested.
+ * Then next_token[s] is the lowest v with W(0) + .. + W(v) > u_sample[s] * sum W.
+ * path[s] lists the nodes that stand (0 first), -1 padded, and n_accepted[s] counts
+ * them.  Sums are exact in units of 2^-62.
+ *
+ *   target       fp32, row of node j at target + s*t_batch_stride + j*t_node_stride
+ *                (elements), V values each; draft likewise, or NULL
+ *   tokens, parents  int32 [B, N]; u_accept fp32 [B, N]; u_sample fp32 [B] (in [0, 1));
+ *                tokens[s][0], parents[s][0] and u_accept[s][0] are not read
+ *   path int32 [B, N], n_accepted int32 [B], next_token int32 [B]  (outputs)
+ * 1 <= N <= 64, 1 <= V <= 2^24, B <= 65535.  A parent of -1 takes a node out; one that
+ * is not before its node, or a token outside [0, V), does too and sets
+ * MX4_STATUS_BAD_INDEX.  Probabilities that are NaN or negative count as 0 and ones
+ * above 1 set, like them, MX4_STATUS_BAD_VALUE; a row of zeros gives next_token -1.  An idle
+ * sequence (n_nodes 0) gets n_accepted 0 and next_token -1.
+ * ------------------------------------------------------------------------- */
+int verify_drafts(const float *target, int64_t t_batch_stride, int64_t t_node_stride,
+                  const float *draft, int64_t d_batch_stride, int64_t d_node_stride,
+                  const int32_t *tokens, const int32_t *parents, const float *u_accept,
+                  const float *u_sample, const int32_t *n_nodes, int64_t B, int N, int64_t V,
+                  int32_t *path, int32_t *n_accepted, int32_t *next_token, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * mx4_accept_rows -- the cache after verification: for every sequence, cached token
+ * base + i becomes base + path[s][i] for i < n_accepted[s] (K and V of every head, and
+ * the index key), and new_lens[s] = base + n_accepted[s].  The rows past the new length
+ * keep their bytes.
+ *
+ *   path int32 [B, N], ascending over its first n_accepted[s] entries;
+ *   n_accepted, seq_lens int32 [B]; n_nodes int32 [B] or NULL; block_table [B, bt_width]
+ *   k_pages, v_pages as mx4_insert; idx_pages index-K pages, MXFP4 (idx_fp8 = 0) or
+ *                fp8 (idx_fp8 = 1, 16384-byte pages), or NULL
+ *   new_lens     int32 [B] (output; not seq_lens itself)
+ * A path that does not ascend within the nodes (MX4_STATUS_BAD_INDEX), a bad length or
+ * count (MX4_STATUS_BAD_LEN) or a bad page (MX4_STATUS_BAD_PAGE) leaves the sequence's
+ * rows alone, with new_lens[s] = seq_lens[s].  The drafted rows' pages belong to this
+ * sequence alone (mx4_fork_pages copies the page that is being filled).
+ * 1 <= N <= 64, 1 <= Hkv <= 8.
+ * ------------------------------------------------------------------------- */
+int mx4_accept_rows(const int32_t *path, const int32_t *n_accepted, const int32_t *seq_lens,
+                    const int32_t *n_nodes, int64_t B, int N, const int32_t *block_table,
+                    int64_t bt_width, uint8_t *k_pages, uint8_t *v_pages, int64_t kv_page_stride,
+                    int64_t kv_head_stride, int Hkv, uint8_t *idx_pages, int64_t idx_page_stride,
+                    int idx_fp8, int64_t num_pages, int32_t *new_lens, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * mx4_fork_pages, mx4_free_pages -- sequences that branch and end.  ref_counts[p] is the
+ * number of table rows that hold page p; free page ids are a stack,
+ * free_list[0 .. *free_count).
+ *
+ * mx4_fork_pages: child i of table row r = rows[i] gets child_tables[i] = the full pages
+ * of r (one more reference each), then, where seq_lens[r] % 128 tokens are in r's last
+ * page, a page off the stack (reference 1) with those tokens' rows copied, then -1;
+ * child_lens[i] = seq_lens[r].  Children take pages in order, child 0 from the top.  A
+ * child that finds no page has length 0, a row of -1 and no references
+ * (MX4_STATUS_NO_PAGES); so has one of a bad row (MX4_STATUS_BAD_INDEX) or length.
+ *
+ * mx4_free_pages: every page of the rows' first ceil(lens / 128) entries loses a
+ * reference; pages that reach 0 go on the stack, ascending by id.  The table rows keep
+ * their bytes.  A page without references is left alone (MX4_STATUS_BAD_REF).
+ *
+ *   rows int32 [n]; block_table int32 [B, bt_width]; seq_lens int32 [B]
+ *   ref_counts int32 [num_pages], free_list int32 [num_pages], free_count int32 [1]
+ *   child_tables int32 [n, bt_width], child_lens int32 [n] (outputs; may not overlap
+ *                block_table and seq_lens)
+ *   pools        as mx4_accept_rows; free: tables int32 [n, bt_width], lens int32 [n]
+ * n <= 65535.
+ * ------------------------------------------------------------------------- */
+int mx4_fork_pages(const int32_t *rows, int64_t n, const int32_t *block_table, int64_t B,
+                   int64_t bt_width, const int32_t *seq_lens, int32_t *ref_counts,
+                   const int32_t *free_list, int32_t *free_count, uint8_t *k_pages,
+                   uint8_t *v_pages, int64_t kv_page_stride, int64_t kv_head_stride, int Hkv,
+                   uint8_t *idx_pages, int64_t idx_page_stride, int idx_fp8, int64_t num_pages,
+                   int32_t *child_tables, int32_t *child_lens, void *stream);
+int mx4_free_pages(const int32_t *tables, int64_t n, int64_t bt_width, const int32_t *lens,
+                   int32_t *ref_counts, int64_t num_pages, int32_t *free_list,
+                   int32_t *free_count, void *stream);
 
 /* ---------------------------------------------------------------------------
  * mx4_check_status -- synchronise `stream`, return MX4_OK if no kernel of this

@@ -22,7 +22,8 @@ __all__ = ["mx4_insert", "mx4_norm_rope_insert", "fp8_index_insert", "index_scor
            "index_topk", "index_topk_workspace", "topk_select", "sparse_paged_decode",
            "topk_select_workspace", "sparse_paged_decode_workspace", "mx4_check_status",
            "sparse_paged_decode_noalloc", "NOALLOC_SCRATCH_BYTES", "mx4_decode_step", "mx4_decode_steps",
-           "mx4_decode_step_input_layout",
+           "mx4_decode_step_input_layout", "tree_paged_decode", "tree_paged_decode_workspace",
+           "verify_drafts", "mx4_accept_rows", "mx4_fork_pages", "mx4_free_pages",
            "mx4_last_error", "mx4_page_bytes", "library_path", "Mx4Error", "PAGE_BYTES",
            "PAGE_TOKENS", "HEAD_DIM"]
 
@@ -38,7 +39,8 @@ _lock = threading.Lock()
 _lib = None
 
 STATUS_BITS = {0x1: "bad-slot", 0x2: "bad-page", 0x4: "bad-seq-len", 0x8: "bad-topk-index",
-               0x10: "non-finite-input"}
+               0x10: "non-finite-input", 0x20: "time-out", 0x40: "no-free-pages",
+               0x80: "bad-page-reference"}
 
 
 class Mx4Error(RuntimeError):
@@ -111,6 +113,22 @@ def _load():
         lib.mx4_decode_steps.argtypes = [i64, P, sz, i64, P, sz, P, P, i64, i64, P, i64, i64, P,
                                          i64, i64, P, i32, i32, ctypes.c_float, P, i64, P, P, sz,
                                          P, sz, P, P, sz, P, P, P]
+        lib.tree_paged_decode.restype = i32
+        lib.tree_paged_decode.argtypes = [P, i64, i32, i32, i32, P, P, i64, i64, i64, P, i64, P, P,
+                                          P, i64, i64, ctypes.c_float, P, P, P, sz, P]
+        lib.tree_paged_decode_workspace.restype = sz
+        lib.tree_paged_decode_workspace.argtypes = [i64, i32, i32, i32]
+        lib.verify_drafts.restype = i32
+        lib.verify_drafts.argtypes = [P, i64, i64, P, i64, i64, P, P, P, P, P, i64, i32, i64, P, P,
+                                      P, P]
+        lib.mx4_accept_rows.restype = i32
+        lib.mx4_accept_rows.argtypes = [P, P, P, P, i64, i32, P, i64, P, P, i64, i64, i32, P, i64,
+                                        i32, i64, P, P]
+        lib.mx4_fork_pages.restype = i32
+        lib.mx4_fork_pages.argtypes = [P, i64, P, i64, i64, P, P, P, P, P, P, i64, i64, i32, P,
+                                       i64, i32, i64, P, P, P]
+        lib.mx4_free_pages.restype = i32
+        lib.mx4_free_pages.argtypes = [P, i64, i64, P, P, i64, P, P, P]
         lib.mx4_check_status.restype = i32
         lib.mx4_check_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
         _lib = lib
@@ -541,6 +559,166 @@ def mx4_decode_steps(n_steps, h_inputs, n_new, d_staging, k_pages, v_pages, idx_
         n_steps, _host_ptr(h_inputs, "h_inputs"), in_stride, int(n_new), _ptr(d_staging),
         d_staging.numel(), *args, _ptr(d_out), _host_ptr(h_out, "h_out"), out_stride,
         _stream(stream), _stream(h2d_stream), _stream(d2h_stream)))
+
+
+def tree_paged_decode_workspace(B, N, H, Hkv) -> int:
+    return int(_load().tree_paged_decode_workspace(int(B), int(N), int(H), int(Hkv)))
+
+
+def _kv_pools(k_pages, v_pages):
+    _pages(k_pages, "k_pages", 3)
+    _pages(v_pages, "v_pages", 3)
+    if k_pages.stride() != v_pages.stride() or k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape and strides")
+
+
+def _int32(t, name, *sizes):
+    _need(t, torch.int32, name)
+    _dims(t, name, *sizes)
+
+
+def tree_paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, out, ws, tree_mask=None,
+                      n_nodes=None, window=0, sinks=0, lse=None, stream=None):
+    """Attention of a speculative step's nodes q bf16 [B, N, H, 128] (the last n_nodes[s]
+    cached tokens of each sequence; None: N) over the MXFP4 pages, out bf16 like q, lse
+    fp32 [B, N, H] or None.  tree_mask int64 [B, N]: bit i of word (s, j) set where node j
+    sees node i (None: a chain).  window > 0: only the last `window` positions and the
+    first `sinks` tokens.  N = 1 is the single-token decode step.  ws: uint8, at least
+    tree_paged_decode_workspace(B, N, H, Hkv) bytes (None when that is 0)."""
+    _need(q, torch.bfloat16, "q")
+    _need(out, torch.bfloat16, "out")
+    _kv_pools(k_pages, v_pages)
+    _dims(q, "q", None, None, None, HEAD_DIM)
+    B, N, H = (int(x) for x in q.shape[:3])
+    _dims(out, "out", B, N, H, HEAD_DIM)
+    _int32(block_table, "block_table", B, None)
+    _int32(seq_lens, "seq_lens", B)
+    if n_nodes is not None:
+        _int32(n_nodes, "n_nodes", B)
+    if tree_mask is not None:
+        _need(tree_mask, torch.int64, "tree_mask")
+        _dims(tree_mask, "tree_mask", B, N)
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        _dims(lse, "lse", B, N, H)
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(_load().tree_paged_decode(
+        _ptr(q), B, N, H, int(k_pages.shape[1]), _ptr(k_pages), _ptr(v_pages), k_pages.stride(0),
+        k_pages.stride(1), int(k_pages.shape[0]), _ptr(block_table), int(block_table.shape[1]),
+        _ptr(seq_lens), _ptr(n_nodes), _ptr(tree_mask), int(window), int(sinks), float(scale),
+        _ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def _prob_rows(t, name, B, N, V):
+    _need(t, torch.float32, name, contiguous=False)
+    _dims(t, name, B, N, V)
+    if V > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the vocabulary axis must be contiguous")
+
+
+def verify_drafts(target, draft, tokens, parents, u_accept, u_sample, path, n_accepted, next_token,
+                  n_nodes=None, stream=None):
+    """Which nodes of each sequence's tree of drafts stand, and the token after them: path
+    int32 [B, N] (accepted nodes, root first, -1 padded), n_accepted and next_token int32
+    [B], from the target's probabilities fp32 [B, N, V] after each node, the draft's (its
+    children were drawn from it; None: drafts that were looked up), tokens and parents
+    int32 [B, N] and the random numbers u_accept fp32 [B, N], u_sample fp32 [B]."""
+    _dims(target, "target", None, None, None)
+    B, N, V = (int(x) for x in target.shape)
+    _prob_rows(target, "target", B, N, V)
+    if draft is not None:
+        _prob_rows(draft, "draft", B, N, V)
+    _int32(tokens, "tokens", B, N)
+    _int32(parents, "parents", B, N)
+    _need(u_accept, torch.float32, "u_accept")
+    _dims(u_accept, "u_accept", B, N)
+    _need(u_sample, torch.float32, "u_sample")
+    _dims(u_sample, "u_sample", B)
+    _int32(path, "path", B, N)
+    _int32(n_accepted, "n_accepted", B)
+    _int32(next_token, "next_token", B)
+    if n_nodes is not None:
+        _int32(n_nodes, "n_nodes", B)
+    _check(_load().verify_drafts(
+        _ptr(target), target.stride(0), target.stride(1), _ptr(draft),
+        0 if draft is None else draft.stride(0), 0 if draft is None else draft.stride(1),
+        _ptr(tokens), _ptr(parents), _ptr(u_accept), _ptr(u_sample), _ptr(n_nodes), B, N, V,
+        _ptr(path), _ptr(n_accepted), _ptr(next_token), _stream(stream)))
+
+
+def _pool_args(k_pages, v_pages, idx_pages):
+    """The pools as the row and page calls take them (index pages MXFP4, fp8 or None)."""
+    _kv_pools(k_pages, v_pages)
+    fp8 = False
+    if idx_pages is not None:
+        fp8 = idx_pages.shape[-1] == FP8_PAGE_BYTES
+        if fp8:
+            _fp8_pages(idx_pages, "idx_pages")
+        else:
+            _pages(idx_pages, "idx_pages", 2)
+        if idx_pages.shape[0] != k_pages.shape[0]:
+            raise ValueError(f"idx_pages has {int(idx_pages.shape[0])} pages, k_pages "
+                             f"{int(k_pages.shape[0])}")
+    return (_ptr(k_pages), _ptr(v_pages), k_pages.stride(0), k_pages.stride(1),
+            int(k_pages.shape[1]), _ptr(idx_pages),
+            0 if idx_pages is None else idx_pages.stride(0), int(fp8), int(k_pages.shape[0]))
+
+
+def mx4_accept_rows(path, n_accepted, seq_lens, block_table, k_pages, v_pages, idx_pages, new_lens,
+                    n_nodes=None, stream=None):
+    """The cache after verify_drafts: the accepted nodes' rows (path int32 [B, N], ascending,
+    its first n_accepted[s] entries) become the sequence's first draft rows in every pool
+    (idx_pages MXFP4, fp8 or None); new_lens int32 [B] = seq_lens - n_nodes + n_accepted."""
+    _int32(path, "path", None, None)
+    B, N = int(path.shape[0]), int(path.shape[1])
+    _int32(n_accepted, "n_accepted", B)
+    _int32(seq_lens, "seq_lens", B)
+    _int32(block_table, "block_table", B, None)
+    _int32(new_lens, "new_lens", B)
+    if n_nodes is not None:
+        _int32(n_nodes, "n_nodes", B)
+    pools = _pool_args(k_pages, v_pages, idx_pages)
+    _check(_load().mx4_accept_rows(
+        _ptr(path), _ptr(n_accepted), _ptr(seq_lens), _ptr(n_nodes), B, N, _ptr(block_table),
+        int(block_table.shape[1]), *pools, _ptr(new_lens), _stream(stream)))
+
+
+def _free_state(ref_counts, free_list, free_count, P):
+    _int32(ref_counts, "ref_counts", P)
+    _int32(free_list, "free_list", P)
+    _int32(free_count, "free_count", 1)
+
+
+def mx4_fork_pages(rows, block_table, seq_lens, ref_counts, free_list, free_count, k_pages, v_pages,
+                   idx_pages, child_tables, child_lens, stream=None):
+    """Children of the table rows rows int32 [n]: child_tables int32 [n, W] shares the full
+    pages (ref_counts int32 [P] grows) and gets a copy of a partly filled last page on a
+    page off the stack free_list int32 [P], free_count int32 [1]; child_lens int32 [n]."""
+    _int32(rows, "rows", None)
+    n = int(rows.shape[0])
+    _int32(block_table, "block_table", None, None)
+    B, W = int(block_table.shape[0]), int(block_table.shape[1])
+    _int32(seq_lens, "seq_lens", B)
+    _int32(child_tables, "child_tables", n, W)
+    _int32(child_lens, "child_lens", n)
+    _free_state(ref_counts, free_list, free_count, int(k_pages.shape[0]))
+    pools = _pool_args(k_pages, v_pages, idx_pages)
+    _check(_load().mx4_fork_pages(
+        _ptr(rows), n, _ptr(block_table), B, W, _ptr(seq_lens), _ptr(ref_counts), _ptr(free_list),
+        _ptr(free_count), *pools, _ptr(child_tables), _ptr(child_lens), _stream(stream)))
+
+
+def mx4_free_pages(tables, lens, ref_counts, free_list, free_count, stream=None):
+    """The rows of tables int32 [n, W] (lens int32 [n] tokens each) give their pages back:
+    a reference less each, and pages without one go on the stack, ascending by id."""
+    _int32(tables, "tables", None, None)
+    n, W = int(tables.shape[0]), int(tables.shape[1])
+    _int32(lens, "lens", n)
+    _int32(ref_counts, "ref_counts", None)
+    P = int(ref_counts.shape[0])
+    _free_state(ref_counts, free_list, free_count, P)
+    _check(_load().mx4_free_pages(_ptr(tables), n, W, _ptr(lens), _ptr(ref_counts), P,
+                                  _ptr(free_list), _ptr(free_count), _stream(stream)))
 
 
 def mx4_check_status(stream=None) -> int:

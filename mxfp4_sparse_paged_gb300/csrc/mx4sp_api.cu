@@ -41,6 +41,23 @@ cudaError_t launch_fp8_index_insert(const float*, int64_t, const int64_t*, float
 cudaError_t launch_index_score_fp8(const uint16_t*, int, const uint8_t*, int64_t, int64_t,
                                    const int32_t*, int, int64_t, const int32_t*, float, float*,
                                    int64_t, uint32_t*, int, cudaStream_t);
+cudaError_t launch_tree_decode(const uint16_t*, int64_t, int, int, int, const uint8_t*,
+                               const uint8_t*, int64_t, int64_t, int64_t, const int32_t*, int64_t,
+                               const int32_t*, const int32_t*, const uint64_t*, int64_t, int64_t,
+                               float, uint16_t*, float*, void*, uint32_t*, int, cudaStream_t);
+size_t tree_decode_workspace_bytes(int64_t, int, int, int, int);
+cudaError_t launch_verify(const float*, const float*, const int64_t*, const int32_t*,
+                          const int32_t*, const float*, const float*, const int32_t*, int64_t, int,
+                          int, int32_t*, int32_t*, int32_t*, uint32_t*, int, cudaStream_t);
+cudaError_t launch_accept(const int32_t*, const int32_t*, const int32_t*, const int32_t*, int64_t,
+                          int, const int32_t*, int64_t, uint8_t*, uint8_t*, int64_t, int64_t, int,
+                          uint8_t*, int64_t, int, int64_t, int32_t*, uint32_t*, cudaStream_t);
+cudaError_t launch_fork(const int32_t*, int64_t, const int32_t*, int64_t, int64_t, const int32_t*,
+                        int32_t*, const int32_t*, int32_t*, uint8_t*, uint8_t*, int64_t, int64_t,
+                        int, uint8_t*, int64_t, int, int64_t, int32_t*, int32_t*, uint32_t*,
+                        cudaStream_t);
+cudaError_t launch_free(const int32_t*, int64_t, int64_t, const int32_t*, int32_t*, int64_t,
+                        int32_t*, int32_t*, uint32_t*, cudaStream_t);
 }  // namespace mx4
 
 // Device status word: kernels OR MX4_STATUS_* bits into it when they skip bad
@@ -447,12 +464,15 @@ int mx4_check_status(void* stream, uint32_t* bits) {
   if (e != cudaSuccess) return fail(MX4_ERR_CUDA, "mx4_check_status: %s", cudaGetErrorString(e));
   if (bits) *bits = h;
   if (h)
-    return fail(MX4_ERR_BOUNDS, "kernels skipped bad data: status bits 0x%x%s%s%s%s%s", h,
+    return fail(MX4_ERR_BOUNDS, "kernels skipped bad data: status bits 0x%x%s%s%s%s%s%s%s%s", h,
                 (h & MX4_STATUS_BAD_SLOT) ? " bad-slot" : "",
                 (h & MX4_STATUS_BAD_PAGE) ? " bad-page" : "",
                 (h & MX4_STATUS_BAD_LEN) ? " bad-seq-len" : "",
                 (h & MX4_STATUS_BAD_INDEX) ? " bad-topk-index" : "",
-                (h & MX4_STATUS_BAD_VALUE) ? " non-finite-input" : "");
+                (h & MX4_STATUS_BAD_VALUE) ? " non-finite-input" : "",
+                (h & MX4_STATUS_TIMEOUT) ? " time-out" : "",
+                (h & MX4_STATUS_NO_PAGES) ? " no-free-pages" : "",
+                (h & MX4_STATUS_BAD_REF) ? " bad-page-reference" : "");
   return ok();
 }
 
@@ -778,4 +798,204 @@ extern "C" int mx4_decode_steps(int64_t n_steps, const void* h_inputs, size_t h_
   if (e != cudaSuccess) return fail(MX4_ERR_CUDA, "%s: %s", kName, cudaGetErrorString(e));
   if (e2 != cudaSuccess) return fail(MX4_ERR_CUDA, "%s: %s", kName, cudaGetErrorString(e2));
   return ok();
+}
+
+// ---------------------------------------------------------------------------
+// A speculative decode step: tree_paged_decode, verify_drafts, mx4_accept_rows,
+// mx4_fork_pages, mx4_free_pages.
+
+namespace {
+
+constexpr int kMaxTreeNodes = 64;  // a node's mask is one 64-bit word
+
+int check_pools(const char* name, const uint8_t* k_pages, const uint8_t* v_pages,
+                int64_t kv_page_stride, int64_t kv_head_stride, int Hkv, const uint8_t* idx_pages,
+                int64_t idx_page_stride, int idx_fp8, int64_t num_pages) {
+  if (!k_pages || !v_pages) return fail(MX4_ERR_INVALID, "%s: NULL pages", name);
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(idx_pages, 16) ||
+      kv_page_stride % 16 || kv_head_stride % 16 || (idx_pages && idx_page_stride % 16))
+    return fail(MX4_ERR_INVALID, "%s: pages must be 16-byte aligned with 16-byte strides", name);
+  if (num_pages < 1 || num_pages > 0x7FFFFFFF || kv_page_stride < mx4::kPageBytes ||
+      (Hkv > 1 && kv_head_stride < mx4::kPageBytes) ||
+      (idx_pages && idx_page_stride < (idx_fp8 ? MX4_FP8_PAGE_BYTES : mx4::kPageBytes)))
+    return fail(MX4_ERR_INVALID, "%s: num_pages or a stride below a page", name);
+  return MX4_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// Limits of tree_paged_decode's sizes; 0 if they hold.
+int check_tree_sizes(const char* name, int64_t B, int N, int H, int Hkv) {
+  if (N < 1 || N > kMaxTreeNodes)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: N = %d (supported 1..64)", name, N);
+  if (Hkv < 1 || Hkv > 8 || H < 1 || H > 128 || H % Hkv)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: H = %d, Hkv = %d (H <= 128 a multiple of Hkv <= 8)", name,
+                H, Hkv);
+  if (B < 0 || B > 65535) return fail(MX4_ERR_UNSUPPORTED, "%s: B = %lld", name, (long long)B);
+  return MX4_OK;
+}
+
+}  // namespace
+
+extern "C" size_t tree_paged_decode_workspace(int64_t B, int N, int H, int Hkv) {
+  if (B < 1 || N < 1 || N > kMaxTreeNodes || Hkv < 1 || H < Hkv || H % Hkv) return 0;
+  return mx4::tree_decode_workspace_bytes(B, N, H, Hkv, current_sms());
+}
+
+extern "C" int tree_paged_decode(const uint16_t* q, int64_t B, int N, int H, int Hkv,
+                                 const uint8_t* k_pages, const uint8_t* v_pages,
+                                 int64_t kv_page_stride, int64_t kv_head_stride,
+                                 int64_t num_pages, const int32_t* block_table, int64_t bt_width,
+                                 const int32_t* seq_lens, const int32_t* n_nodes,
+                                 const uint64_t* tree_mask, int64_t window, int64_t sinks,
+                                 float scale, uint16_t* out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  static const char* kName = "tree_paged_decode";
+  if (int rc = check_tree_sizes(kName, B, N, H, Hkv)) return rc;
+  if (window < 0 || sinks < 0)
+    return fail(MX4_ERR_INVALID, "%s: window = %lld, sinks = %lld", kName, (long long)window,
+                (long long)sinks);
+  if (!(scale == scale) || scale == INFINITY || scale == -INFINITY)
+    return fail(MX4_ERR_INVALID, "%s: scale is not finite", kName);
+  const size_t need = tree_paged_decode_workspace(B, N, H, Hkv);
+  if (ws_bytes < need)
+    return fail(MX4_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", kName, ws_bytes, need);
+  if (B == 0) return ok();
+  if (!q || !block_table || !seq_lens || !out)
+    return fail(MX4_ERR_INVALID, "%s: NULL pointer", kName);
+  if (int rc = check_pools(kName, k_pages, v_pages, kv_page_stride, kv_head_stride, Hkv, nullptr,
+                           0, 0, num_pages))
+    return rc;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pages, 32) || !aligned(v_pages, 32) ||
+      kv_page_stride % 32 || (Hkv > 1 && kv_head_stride % 32) || !aligned(tree_mask, 8) ||
+      !aligned(lse, 4))
+    return fail(MX4_ERR_INVALID, "%s: misaligned buffer, or pages or strides not of 32 bytes",
+                kName);
+  if (need > 0 && (!ws || !aligned(ws, 16)))
+    return fail(MX4_ERR_INVALID, "%s: workspace NULL or not 16-byte aligned", kName);
+  if (bt_width < 1 || bt_width > (1 << 24)) return fail(MX4_ERR_INVALID, "%s: bt_width", kName);
+  DeviceInfo* d;
+  if (int rc = device_info(&d)) return rc;
+  return cuda_result(
+      mx4::launch_tree_decode(q, B, N, H, Hkv, k_pages, v_pages, kv_page_stride, kv_head_stride,
+                              num_pages, block_table, bt_width, seq_lens, n_nodes, tree_mask,
+                              window, sinks, scale, out, lse, ws, d->status, d->num_sms,
+                              static_cast<cudaStream_t>(stream)),
+      kName);
+}
+
+extern "C" int verify_drafts(const float* target, int64_t t_batch_stride, int64_t t_node_stride,
+                             const float* draft, int64_t d_batch_stride, int64_t d_node_stride,
+                             const int32_t* tokens, const int32_t* parents, const float* u_accept,
+                             const float* u_sample, const int32_t* n_nodes, int64_t B, int N,
+                             int64_t V, int32_t* path, int32_t* n_accepted, int32_t* next_token,
+                             void* stream) {
+  static const char* kName = "verify_drafts";
+  if (N < 1 || N > kMaxTreeNodes)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: N = %d (supported 1..64)", kName, N);
+  if (V < 1 || V > (1 << 24))
+    return fail(MX4_ERR_UNSUPPORTED, "%s: V = %lld (1..2^24)", kName, (long long)V);
+  if (B < 0 || B > 65535) return fail(MX4_ERR_UNSUPPORTED, "%s: B = %lld", kName, (long long)B);
+  if (B == 0) return ok();
+  if (!target || !tokens || !parents || !u_accept || !u_sample || !path || !n_accepted ||
+      !next_token)
+    return fail(MX4_ERR_INVALID, "%s: NULL pointer", kName);
+  if (!aligned(target, 4) || !aligned(draft, 4))
+    return fail(MX4_ERR_INVALID, "%s: misaligned probabilities", kName);
+  if ((N > 1 && t_node_stride < V) || (B > 1 && t_batch_stride < 0) || t_node_stride < 0 ||
+      (draft && (d_node_stride < 0 || d_batch_stride < 0 || (N > 1 && d_node_stride < V))))
+    return fail(MX4_ERR_INVALID, "%s: a stride below a row", kName);
+  const int64_t strides[4] = {t_batch_stride, t_node_stride, d_batch_stride, d_node_stride};
+  DeviceInfo* d;
+  if (int rc = device_info(&d)) return rc;
+  return cuda_result(mx4::launch_verify(target, draft, strides, tokens, parents, u_accept,
+                                        u_sample, n_nodes, B, N, (int)V, path, n_accepted,
+                                        next_token, d->status, d->num_sms,
+                                        static_cast<cudaStream_t>(stream)),
+                     kName);
+}
+
+extern "C" int mx4_accept_rows(const int32_t* path, const int32_t* n_accepted,
+                               const int32_t* seq_lens, const int32_t* n_nodes, int64_t B, int N,
+                               const int32_t* block_table, int64_t bt_width, uint8_t* k_pages,
+                               uint8_t* v_pages, int64_t kv_page_stride, int64_t kv_head_stride,
+                               int Hkv, uint8_t* idx_pages, int64_t idx_page_stride, int idx_fp8,
+                               int64_t num_pages, int32_t* new_lens, void* stream) {
+  static const char* kName = "mx4_accept_rows";
+  if (N < 1 || N > kMaxTreeNodes)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: N = %d (supported 1..64)", kName, N);
+  if (Hkv < 1 || Hkv > 8)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: Hkv = %d (supported 1..8)", kName, Hkv);
+  if (B < 0 || B > 0x7FFFFFFF)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: B = %lld", kName, (long long)B);
+  if (B == 0) return ok();
+  if (!path || !n_accepted || !seq_lens || !block_table || !new_lens)
+    return fail(MX4_ERR_INVALID, "%s: NULL pointer", kName);
+  if (int rc = check_pools(kName, k_pages, v_pages, kv_page_stride, kv_head_stride, Hkv, idx_pages,
+                           idx_page_stride, idx_fp8, num_pages))
+    return rc;
+  if (bt_width < 1) return fail(MX4_ERR_INVALID, "%s: bt_width < 1", kName);
+  if (overlap(new_lens, B * 4, seq_lens, B * 4) || overlap(new_lens, B * 4, n_accepted, B * 4) ||
+      (n_nodes && overlap(new_lens, B * 4, n_nodes, B * 4)))
+    return fail(MX4_ERR_INVALID, "%s: new_lens overlaps an input", kName);
+  DeviceInfo* d;
+  if (int rc = device_info(&d)) return rc;
+  return cuda_result(
+      mx4::launch_accept(path, n_accepted, seq_lens, n_nodes, B, N, block_table, bt_width, k_pages,
+                         v_pages, kv_page_stride, kv_head_stride, Hkv, idx_pages, idx_page_stride,
+                         idx_fp8 ? 1 : 0, num_pages, new_lens, d->status,
+                         static_cast<cudaStream_t>(stream)),
+      kName);
+}
+
+extern "C" int mx4_fork_pages(const int32_t* rows, int64_t n, const int32_t* block_table,
+                              int64_t B, int64_t bt_width, const int32_t* seq_lens,
+                              int32_t* ref_counts, const int32_t* free_list, int32_t* free_count,
+                              uint8_t* k_pages, uint8_t* v_pages, int64_t kv_page_stride,
+                              int64_t kv_head_stride, int Hkv, uint8_t* idx_pages,
+                              int64_t idx_page_stride, int idx_fp8, int64_t num_pages,
+                              int32_t* child_tables, int32_t* child_lens, void* stream) {
+  static const char* kName = "mx4_fork_pages";
+  if (Hkv < 1 || Hkv > 8)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: Hkv = %d (supported 1..8)", kName, Hkv);
+  if (n < 0 || n > 65535) return fail(MX4_ERR_UNSUPPORTED, "%s: n = %lld", kName, (long long)n);
+  if (n == 0) return ok();
+  if (!rows || !block_table || !seq_lens || !ref_counts || !free_list || !free_count ||
+      !child_tables || !child_lens)
+    return fail(MX4_ERR_INVALID, "%s: NULL pointer", kName);
+  if (B < 1 || bt_width < 1) return fail(MX4_ERR_INVALID, "%s: B or bt_width < 1", kName);
+  if (int rc = check_pools(kName, k_pages, v_pages, kv_page_stride, kv_head_stride, Hkv, idx_pages,
+                           idx_page_stride, idx_fp8, num_pages))
+    return rc;
+  if (overlap(child_tables, n * bt_width * 4, block_table, B * bt_width * 4) ||
+      overlap(child_lens, n * 4, seq_lens, B * 4) || overlap(child_lens, n * 4, rows, n * 4))
+    return fail(MX4_ERR_INVALID, "%s: an output overlaps an input", kName);
+  DeviceInfo* d;
+  if (int rc = device_info(&d)) return rc;
+  return cuda_result(
+      mx4::launch_fork(rows, n, block_table, B, bt_width, seq_lens, ref_counts, free_list,
+                       free_count, k_pages, v_pages, kv_page_stride, kv_head_stride, Hkv,
+                       idx_pages, idx_page_stride, idx_fp8 ? 1 : 0, num_pages, child_tables,
+                       child_lens, d->status, static_cast<cudaStream_t>(stream)),
+      kName);
+}
+
+extern "C" int mx4_free_pages(const int32_t* tables, int64_t n, int64_t bt_width,
+                              const int32_t* lens, int32_t* ref_counts, int64_t num_pages,
+                              int32_t* free_list, int32_t* free_count, void* stream) {
+  static const char* kName = "mx4_free_pages";
+  if (n < 0 || n > 65535) return fail(MX4_ERR_UNSUPPORTED, "%s: n = %lld", kName, (long long)n);
+  if (n == 0) return ok();
+  if (!tables || !lens || !ref_counts || !free_list || !free_count)
+    return fail(MX4_ERR_INVALID, "%s: NULL pointer", kName);
+  if (bt_width < 1 || num_pages < 1 || num_pages > 0x7FFFFFFF)
+    return fail(MX4_ERR_INVALID, "%s: bt_width or num_pages", kName);
+  DeviceInfo* d;
+  if (int rc = device_info(&d)) return rc;
+  return cuda_result(mx4::launch_free(tables, n, bt_width, lens, ref_counts, num_pages, free_list,
+                                      free_count, d->status, static_cast<cudaStream_t>(stream)),
+                     kName);
 }

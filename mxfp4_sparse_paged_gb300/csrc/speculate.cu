@@ -1,0 +1,670 @@
+// The steps around tree_paged_decode in a speculative decode step: which drafted
+// tokens stand (verify_drafts), the cache rows of the ones that do (accept_rows),
+// and sequences that branch and end (fork_pages, free_pages).
+//
+// Kernels that write lengths or block tables (accept, fork) do not signal their
+// dependents early: the library's other kernels read lengths and tables before they
+// wait for the kernel in front of them, so that kernel must have completed.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace mx4 {
+
+// ---------------------------------------------------------------------------
+// verify_drafts.  With p and q the target's and the draft's distributions after node
+// `cur`, the children x_1, x_2, ... of cur are tested in order against what is left of p:
+//   W_0 = p, T_0 = 1;   x_k stands iff  u T q(x_k) < W(x_k);   else
+//   W <- max(W - T q, 0), T <- sum W
+// (W / T is the residual distribution; kept unnormalised so nothing is divided), and
+// where no child stands the next token is drawn from W by its running sum.
+//
+// Sums are exact: probabilities are 64-bit integers in units of 2^-62 (fp32 values of
+// at least 2^-38 without any rounding), so no order of summation and no cluster size
+// changes a decision, and the only fp64 left is a few scalars (this GPU's fp64 rate is
+// a hundredth of its fp32 rate; the integer form costs some ten 32-bit operations a
+// value, below what the loads take).
+//
+// One cluster of CTAs per sequence, each CTA one contiguous part of the vocabulary.
+// What the walk looks up (parents, tokens, random numbers, p and q of each draft at its
+// parent) is loaded by all threads at once, so accepted drafts cost no dependent loads;
+// a rejection is one pass over the node's two rows and one exchange in the cluster.
+// Every thread runs the walk itself on the same numbers, so it needs no broadcast.
+constexpr int kMaxNodes = 64;
+constexpr int kVerThreads = 512;
+constexpr int kVerWarps = kVerThreads / 32;
+constexpr int kVerUnroll = 8;  // loads in flight per thread and row
+constexpr int kVerMaxCluster = 8;
+
+struct VerifyArgs {
+  const float* target;
+  const float* draft;  // NULL: given drafts
+  int64_t t_batch, t_node, d_batch, d_node;  // strides in elements
+  const int32_t* tokens;
+  const int32_t* parents;
+  const float* u_accept;
+  const float* u_sample;
+  const int32_t* n_nodes;  // NULL: all N
+  int N, V;
+  int32_t* path;
+  int32_t* n_accepted;
+  int32_t* next_token;
+  uint32_t* status;
+};
+
+// A probability in units of 2^-62 (truncated); a NaN or negative value counts as 0.
+__device__ __forceinline__ uint64_t to_fixed(float x) {
+  return __float2ull_rz(fminf(fmaxf(x, 0.f), 1.9999f) * 0x1p62f);
+}
+__device__ __forceinline__ bool prob_ok(float x) { return x >= 0.f && x <= 1.001f; }
+// a * b for a, b in units of 2^-62
+__device__ __forceinline__ uint64_t mul_fixed(uint64_t a, uint64_t b) {
+  return __umul64hi(a << 1, b << 1);
+}
+
+__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  return x;
+}
+
+// What is left of the target's distribution at the current node.
+struct Residual {
+  const float* p;       // the target's row
+  const float* q;       // the draft's row (NULL: one-hot drafts)
+  int k;                // rejections so far
+  const uint64_t* T;    // T_0 .. T_{k-1}
+  const int32_t* gone;  // the rejected tokens (one-hot drafts)
+  __device__ __forceinline__ uint64_t of(int v, float pv, float qv) const {
+    uint64_t w = to_fixed(pv);
+    if (k == 0) return w;
+    if (q) {
+      const uint64_t qf = to_fixed(qv);
+      for (int r = 0; r < k; ++r) {
+        const uint64_t t = r == 0 ? qf : mul_fixed(T[r], qf);
+        w = w > t ? w - t : 0;
+      }
+    } else {
+      for (int r = 0; r < k; ++r)
+        if (gone[r] == v) w = 0;
+    }
+    return w;
+  }
+};
+
+// Sum of the residual over v0 <= v < v1 by one warp (all lanes get it).
+__device__ __forceinline__ uint64_t warp_range_sum(const Residual& R, int v0, int v1, int lane,
+                                                   bool& bad) {
+  uint64_t s = 0;
+  const bool two = R.q != nullptr && R.k > 0;
+  for (int b = v0 + lane; b < v1; b += 32 * kVerUnroll) {
+    float pv[kVerUnroll], qv[kVerUnroll];
+#pragma unroll
+    for (int i = 0; i < kVerUnroll; ++i) {
+      const int v = b + 32 * i;
+      pv[i] = v < v1 ? R.p[v] : 0.f;
+      qv[i] = two && v < v1 ? R.q[v] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kVerUnroll; ++i) {
+      bad |= !prob_ok(pv[i]) || !prob_ok(qv[i]);
+      s += R.of(b + 32 * i, pv[i], qv[i]);
+    }
+  }
+  return warp_sum(s);
+}
+
+__global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t s = blockIdx.x / C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int32_t s_par[kMaxNodes], s_tok[kMaxNodes], s_gone[kMaxNodes], s_path[kMaxNodes];
+  __shared__ float s_u[kMaxNodes], s_p[kMaxNodes], s_q[kMaxNodes];
+  __shared__ uint64_t s_T[kMaxNodes + 1];
+  __shared__ uint64_t s_warp[2][kVerWarps];          // this CTA's warp sums, by pass parity
+  __shared__ uint64_t s_part[2][kVerMaxCluster];     // the cluster's CTA sums, by pass parity
+  __shared__ uint64_t s_sub[kVerWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int n = a.n_nodes ? min(max(a.n_nodes[s], 0), a.N) : a.N;
+  if (a.n_nodes && rank == 0 && tid == 0 && a.n_nodes[s] != n)
+    flag(a.status, MX4_STATUS_BAD_LEN);
+  if (n < 1) {  // an idle sequence (uniform over the cluster)
+    if (rank == 0) {
+      for (int j = tid; j < a.N; j += kVerThreads) a.path[s * a.N + j] = -1;
+      if (tid == 0) {
+        a.n_accepted[s] = 0;
+        a.next_token[s] = -1;
+      }
+    }
+    return;
+  }
+  const float* tgt = a.target + s * a.t_batch;
+  const float* drf = a.draft ? a.draft + s * a.d_batch : nullptr;
+  for (int j = tid; j < n; j += kVerThreads) {
+    int par = j == 0 ? -1 : a.parents[s * a.N + j];
+    const int tok = a.tokens[s * a.N + j];
+    if (j > 0 && par != -1 && (par < 0 || par >= j || tok < 0 || tok >= a.V)) {
+      flag(a.status, MX4_STATUS_BAD_INDEX);
+      par = -1;  // never tested
+    }
+    s_par[j] = par;
+    s_tok[j] = tok;
+    s_path[j] = -1;
+    s_u[j] = j > 0 ? a.u_accept[s * a.N + j] : 0.f;
+    s_p[j] = par >= 0 ? tgt[par * a.t_node + tok] : 0.f;
+    s_q[j] = par >= 0 ? (drf ? drf[par * a.d_node + tok] : 1.f) : 0.f;
+  }
+  cluster.sync();  // every CTA of the cluster runs: its shared memory may be written
+
+  // this CTA's part of the vocabulary, and this warp's part of that
+  const int c0 = (int)((int64_t)a.V * rank / C), c1 = (int)((int64_t)a.V * (rank + 1) / C);
+  auto warp_begin = [&](int w) { return c0 + (int)((int64_t)(c1 - c0) * w / kVerWarps); };
+  int pass = 0;
+  bool bad = false;
+  // one pass over the residual: T, with the warp and CTA sums left in parity `pass`
+  auto total = [&](const Residual& R) {
+    ++pass;
+    const uint64_t ws = warp_range_sum(R, warp_begin(warp), warp_begin(warp + 1), lane, bad);
+    if (lane == 0) s_warp[pass & 1][warp] = ws;
+    __syncthreads();
+    if (warp == 0) {
+      const uint64_t cs = warp_sum(lane < kVerWarps ? s_warp[pass & 1][lane] : 0);
+      if (lane < C) *cluster.map_shared_rank(&s_part[pass & 1][rank], lane) = cs;
+    }
+    cluster.sync();
+    uint64_t t = 0;
+    for (int i = 0; i < C; ++i) t += s_part[pass & 1][i];
+    return t;
+  };
+
+  int cur = 0, acc = 1;
+  bool shut = false, summed = false;  // summed: the last pass is of the current residual
+  uint64_t T = 1ull << 62;
+  Residual R{tgt, drf, 0, s_T, s_gone};
+  if (tid == 0) s_path[0] = 0;
+  for (int j = 1; j < n; ++j) {
+    if (s_par[j] != cur || shut) continue;
+    const float pv = s_p[j], qv = s_q[j];
+    bool ok;
+    if (R.k == 0) {
+      ok = (double)s_u[j] * (double)qv < (double)pv;
+    } else {
+      const double w = (double)R.of(s_tok[j], pv, qv);
+      ok = (double)s_u[j] * (double)T * (double)qv < w;
+    }
+    if (ok) {
+      cur = j;
+      R = Residual{tgt + (int64_t)j * a.t_node, drf ? drf + (int64_t)j * a.d_node : nullptr, 0,
+                   s_T, s_gone};
+      T = 1ull << 62;
+      summed = false;
+      if (tid == 0) s_path[acc] = j;
+      ++acc;
+      continue;
+    }
+    // rejected: T (of k rejections) is known; the residual of k + 1
+    __syncthreads();  // the walk above has read s_T and s_gone
+    if (tid == 0) {
+      s_T[R.k] = T;
+      s_gone[R.k] = s_tok[j];
+    }
+    ++R.k;
+    __syncthreads();
+    T = total(R);
+    summed = true;
+    if (T == 0) {  // nothing left (p <= q everywhere): draw from p itself
+      shut = true;
+      R.k = 0;
+      summed = false;
+    }
+  }
+  if (!summed) T = total(R);
+
+  // the next token: the first v whose running sum exceeds u T
+  const float us = a.u_sample[s];
+  const uint64_t ui = __double2ull_rz((double)fminf(fmaxf(us, 0.f), 0x1.fffffep-1f) * 0x1p64);
+  uint64_t left = __umul64hi(ui, T);
+  int at = -1;  // the CTA
+  uint64_t before = 0;
+  for (int i = 0; i < C; ++i) {
+    const uint64_t cs = s_part[pass & 1][i];
+    if (at < 0 && before + cs > left) at = i;
+    if (at < 0) before += cs;
+  }
+  if (T == 0) at = -1;  // a row of zeros: no token
+  if (at == rank) {
+    int w = 0;
+    for (; w < kVerWarps - 1; ++w) {
+      const uint64_t x = s_warp[pass & 1][w];
+      if (before + x > left) break;
+      before += x;
+    }
+    // the warp's part in sixteenths, then one warp's sixteenth 32 values at a time
+    const int w0 = warp_begin(w), w1 = warp_begin(w + 1);
+    auto sub = [&](int i) { return w0 + (int)((int64_t)(w1 - w0) * i / kVerWarps); };
+    const uint64_t x = warp_range_sum(R, sub(warp), sub(warp + 1), lane, bad);
+    if (lane == 0) s_sub[warp] = x;
+    __syncthreads();
+    int i = 0;
+    for (; i < kVerWarps - 1; ++i) {
+      if (before + s_sub[i] > left) break;
+      before += s_sub[i];
+    }
+    if (warp == 0) {
+      const bool two = R.q != nullptr && R.k > 0;
+      int found = sub(i + 1) - 1;
+      for (int b = sub(i); b < sub(i + 1); b += 32) {
+        const int v = b + lane;
+        const bool in = v < sub(i + 1);
+        uint64_t inc = in ? R.of(v, R.p[v], two ? R.q[v] : 0.f) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, in && before + inc > left);
+        if (hit) {
+          found = b + __ffs(hit) - 1;
+          break;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, inc, 31);
+      }
+      if (lane == 0) a.next_token[s] = found;
+    }
+  }
+  if (rank == 0) {
+    if (at < 0 && tid == 0) {
+      a.next_token[s] = -1;
+      flag(a.status, MX4_STATUS_BAD_VALUE);
+    }
+    if (tid == 0) a.n_accepted[s] = acc;
+    __syncthreads();
+    for (int j = tid; j < a.N; j += kVerThreads) a.path[s * a.N + j] = j < n ? s_path[j] : -1;
+  }
+  if (bad) flag(a.status, MX4_STATUS_BAD_VALUE);
+  cluster.sync();  // no CTA leaves while another may still write to its shared memory
+}
+
+cudaError_t launch_verify(const float* target, const float* draft, const int64_t* strides,
+                          const int32_t* tokens, const int32_t* parents, const float* u_accept,
+                          const float* u_sample, const int32_t* n_nodes, int64_t B, int N, int V,
+                          int32_t* path, int32_t* n_accepted, int32_t* next_token,
+                          uint32_t* status, int num_sms, cudaStream_t stream) {
+  VerifyArgs a{target, draft, strides[0], strides[1], strides[2], strides[3], tokens, parents,
+               u_accept, u_sample, n_nodes, N, V, path, n_accepted, next_token, status};
+  // CTAs a sequence: about four a SM in all, each with 2048 values or more
+  int C = kVerMaxCluster;
+  while (C > 1 && (B * C > 4 * (int64_t)num_sms || V / C < 2048)) C /= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(B * C));
+  cfg.blockDim = dim3(kVerThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_kernel, a);
+}
+
+// ---------------------------------------------------------------------------
+// Cache rows.  A pool is MXFP4 (64 data bytes and 4 scale bytes a row, head after head)
+// or the fp8 index pool (128 data bytes a row, no scales).
+struct Pools {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t kv_page, kv_head;
+  uint8_t* idx;  // NULL: none
+  int64_t idx_page;
+  int idx_fp8;
+  int Hkv;
+  int64_t num_pages;
+  __host__ __device__ int parts() const { return 2 * Hkv + (idx ? 1 : 0); }
+  // Part r of page p (K heads, V heads, the index key) and whether it is an fp8 one.
+  __device__ uint8_t* part(int r, int64_t p, bool& fp8) const {
+    fp8 = r == 2 * Hkv && idx_fp8;
+    if (r < Hkv) return k + p * kv_page + r * kv_head;
+    if (r < 2 * Hkv) return v + p * kv_page + (r - Hkv) * kv_head;
+    return idx + p * idx_page;
+  }
+};
+
+// accept_rows: the rows of the accepted nodes move to the sequence's first draft rows.
+// One CTA per (sequence, part).  Rows move towards lower places (path[i] >= i), so a
+// row's new place may be another's old one: every row is read into registers before
+// any is written.  16 bytes a thread and row piece, at most 8 pieces a row.
+constexpr int kAccThreads = 256;
+__global__ void __launch_bounds__(kAccThreads)
+accept_kernel(const int32_t* __restrict__ path, const int32_t* __restrict__ n_accepted,
+              const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ n_nodes, int N,
+              const int32_t* __restrict__ table, int64_t bt_width, Pools pools,
+              int32_t* __restrict__ new_lens, uint32_t* status) {
+  __shared__ int64_t s_src[kMaxNodes], s_dst[kMaxNodes];  // page * 128 + row; -1: stays
+  pdl_wait();
+  const int64_t s = blockIdx.x;
+  const int r = blockIdx.y, tid = threadIdx.x;
+  const int n = n_nodes ? n_nodes[s] : N;
+  const int64_t L = seq_lens[s];
+  const int acc = n_accepted[s];
+  bool ok = n >= 0 && n <= N && L >= n && L <= bt_width * kPageTokens && acc >= 0 && acc <= n;
+  const bool len_ok = ok;
+  const int64_t base = L - n;
+  int bad_page = 0;
+  if (ok && tid < kMaxNodes) {
+    int64_t src = -1, dst = -1;
+    if (tid < acc) {
+      const int32_t p = path[s * N + tid];
+      const int32_t prev = tid > 0 ? path[s * N + tid - 1] : -1;
+      if (p <= prev || p >= n) {
+        ok = false;
+      } else if (p > tid) {
+        const int64_t i = base + p, o = base + tid;
+        const int32_t sp = table[s * bt_width + i / kPageTokens];
+        const int32_t dp = table[s * bt_width + o / kPageTokens];
+        if (sp < 0 || sp >= pools.num_pages || dp < 0 || dp >= pools.num_pages) {
+          bad_page = 1;
+          ok = false;
+        } else {
+          src = (int64_t)sp * kPageTokens + i % kPageTokens;
+          dst = (int64_t)dp * kPageTokens + o % kPageTokens;
+        }
+      }
+    }
+    s_src[tid] = src;
+    s_dst[tid] = dst;
+  }
+  bad_page = __syncthreads_or(bad_page);
+  if (!__syncthreads_and(ok)) {  // the sequence is left as it is
+    if (r == 0 && tid == 0) {
+      flag(status, !len_ok ? MX4_STATUS_BAD_LEN : bad_page ? MX4_STATUS_BAD_PAGE
+                                                           : MX4_STATUS_BAD_INDEX);
+      new_lens[s] = (int32_t)L;
+    }
+    return;
+  }
+  if (r == 0 && tid == 0) new_lens[s] = (int32_t)(base + acc);
+  if (acc == 0) return;
+  // pieces: 8 a row of an fp8 part; of an MXFP4 part 4 of data and 1 of scales
+  uint4 x[2];
+  bool fp8;
+  pools.part(r, 0, fp8);
+  const int per = fp8 ? 8 : 5;
+  auto at = [&](int64_t slot, int piece) -> uint8_t* {
+    bool f;
+    uint8_t* b = pools.part(r, slot / kPageTokens, f);
+    const int row = (int)(slot % kPageTokens);
+    if (f) return b + row * 128 + piece * 16;
+    return piece < 4 ? b + row * kRowDataBytes + piece * 16
+                     : b + kScaleOffset + row * kRowScaleBytes;
+  };
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int e = tid + u * kAccThreads, i = e / per, piece = e % per;
+    if (i < acc && s_src[i] >= 0) {
+      if (!fp8 && piece == 4)
+        x[u].x = *reinterpret_cast<const uint32_t*>(at(s_src[i], piece));
+      else
+        x[u] = *reinterpret_cast<const uint4*>(at(s_src[i], piece));
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int e = tid + u * kAccThreads, i = e / per, piece = e % per;
+    if (i < acc && s_src[i] >= 0) {
+      if (!fp8 && piece == 4)
+        *reinterpret_cast<uint32_t*>(at(s_dst[i], piece)) = x[u].x;
+      else
+        *reinterpret_cast<uint4*>(at(s_dst[i], piece)) = x[u];
+    }
+  }
+}
+static_assert(2 * kAccThreads >= 8 * kMaxNodes, "a CTA's pieces");
+
+cudaError_t launch_accept(const int32_t* path, const int32_t* n_accepted, const int32_t* seq_lens,
+                          const int32_t* n_nodes, int64_t B, int N, const int32_t* table,
+                          int64_t bt_width, uint8_t* k, uint8_t* v, int64_t kv_page,
+                          int64_t kv_head, int Hkv, uint8_t* idx, int64_t idx_page, int idx_fp8,
+                          int64_t num_pages, int32_t* new_lens, uint32_t* status,
+                          cudaStream_t stream) {
+  const Pools pools{k, v, kv_page, kv_head, idx, idx_page, idx_fp8, Hkv, num_pages};
+  return launch_pdl(accept_kernel, dim3((unsigned)B, (unsigned)pools.parts()), dim3(kAccThreads),
+                    0, stream, path, n_accepted, seq_lens, n_nodes, N, table, bt_width, pools,
+                    new_lens, status);
+}
+
+// ---------------------------------------------------------------------------
+// fork_pages and free_pages.  Free page ids are a stack: free_list[0 .. free_count).
+//
+// fork: a child of table row r shares the full pages of r (one more reference each); its
+// partly filled last page is a page popped off the stack, with the used rows copied.
+// Child i's page is the one under those of the children before it, found by a running
+// count, so the outcome does not depend on scheduling.
+// Two kernels: one CTA does the counting and the popping (a serial dependence over the
+// children, of 4 bytes each); then one CTA per (child, part) copies rows, the first
+// part's CTA also the table row and the references.
+constexpr int kForkThreads = 1024;
+__global__ void __launch_bounds__(kForkThreads)
+fork_assign_kernel(const int32_t* __restrict__ rows, int64_t n, int64_t B, int64_t bt_width,
+                   const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ free_list,
+                   int32_t* free_count, int64_t num_pages, int32_t* __restrict__ child,
+                   int32_t* __restrict__ child_lens, uint32_t* status) {
+  __shared__ int s_warp[32];
+  __shared__ int s_taken;
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int have = (int)min((int64_t)max(*free_count, 0), num_pages);
+  if (tid == 0) s_taken = 0;
+  __syncthreads();
+  for (int64_t b = 0; b < n; b += kForkThreads) {
+    const int64_t i = b + tid;
+    int need = 0, L = 0;
+    if (i < n) {
+      const int r = rows[i];
+      if (r < 0 || r >= B) {
+        flag(status, MX4_STATUS_BAD_INDEX);
+      } else {
+        L = seq_lens[r];
+        if (L < 0 || L > bt_width * kPageTokens) {
+          flag(status, MX4_STATUS_BAD_LEN);
+          L = 0;
+        }
+      }
+      need = L % kPageTokens != 0;
+    }
+    int inc = need;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    int before = s_taken;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+    const int rank = before + inc - need;
+    if (i < n) {
+      if (need) {
+        int32_t page = rank < have ? free_list[have - 1 - rank] : -1;
+        if (page < 0 || page >= num_pages) {
+          flag(status, rank < have ? MX4_STATUS_BAD_PAGE : MX4_STATUS_NO_PAGES);
+          page = -1;
+          L = 0;  // no page: no child
+        }
+        child[i * bt_width + (L / kPageTokens)] = page;
+      }
+      child_lens[i] = L;
+    }
+    __syncthreads();
+    if (tid == kForkThreads - 1) s_taken = before + inc;
+    __syncthreads();
+  }
+  if (tid == 0) *free_count = have - min(s_taken, have);
+}
+
+constexpr int kCopyThreads = 128;
+__global__ void __launch_bounds__(kCopyThreads)
+fork_copy_kernel(const int32_t* __restrict__ rows, int64_t n, int64_t bt_width,
+                 const int32_t* __restrict__ table, int32_t* refs, Pools pools,
+                 int32_t* __restrict__ child, const int32_t* __restrict__ child_lens,
+                 uint32_t* status) {
+  pdl_wait();
+  const int64_t i = blockIdx.x;
+  const int r = blockIdx.y, tid = threadIdx.x;
+  const int L = child_lens[i];
+  const int full = L / kPageTokens, rem = L % kPageTokens;
+  const int32_t* src_row = table + (int64_t)(L > 0 ? rows[i] : 0) * bt_width;
+  int32_t* const row = child + i * bt_width;
+  if (r == 0) {
+    for (int64_t j = tid; j < bt_width; j += kCopyThreads) {
+      if (j < full) {
+        const int32_t p = src_row[j];
+        row[j] = p;
+        if (p >= 0 && p < pools.num_pages)
+          atomicAdd(refs + p, 1);
+        else
+          flag(status, MX4_STATUS_BAD_PAGE);
+      } else if (j > full || rem == 0) {
+        row[j] = -1;
+      } else {
+        refs[row[j]] = 1;  // the popped page
+      }
+    }
+  }
+  if (rem == 0) return;
+  const int32_t sp = src_row[full], dp = row[full];
+  if (sp < 0 || sp >= pools.num_pages) {
+    if (r == 0 && tid == 0) flag(status, MX4_STATUS_BAD_PAGE);
+    return;
+  }
+  bool fp8;
+  const uint8_t* from = pools.part(r, sp, fp8);
+  uint8_t* to = pools.part(r, dp, fp8);
+  const int pieces = rem * (fp8 ? 8 : 4);
+  for (int e = tid; e < pieces; e += kCopyThreads)
+    reinterpret_cast<uint4*>(to)[e] = reinterpret_cast<const uint4*>(from)[e];
+  if (!fp8)
+    for (int e = tid; e < rem; e += kCopyThreads)
+      reinterpret_cast<uint32_t*>(to + kScaleOffset)[e] =
+          reinterpret_cast<const uint32_t*>(from + kScaleOffset)[e];
+}
+
+cudaError_t launch_fork(const int32_t* rows, int64_t n, const int32_t* table, int64_t B,
+                        int64_t bt_width, const int32_t* seq_lens, int32_t* refs,
+                        const int32_t* free_list, int32_t* free_count, uint8_t* k, uint8_t* v,
+                        int64_t kv_page, int64_t kv_head, int Hkv, uint8_t* idx,
+                        int64_t idx_page, int idx_fp8, int64_t num_pages, int32_t* child,
+                        int32_t* child_lens, uint32_t* status, cudaStream_t stream) {
+  const Pools pools{k, v, kv_page, kv_head, idx, idx_page, idx_fp8, Hkv, num_pages};
+  cudaError_t e = launch_pdl(fork_assign_kernel, dim3(1), dim3(kForkThreads), 0, stream, rows, n,
+                             B, bt_width, seq_lens, free_list, free_count, num_pages, child,
+                             child_lens, status);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fork_copy_kernel, dim3((unsigned)n, (unsigned)pools.parts()),
+                    dim3(kCopyThreads), 0, stream, rows, n, bt_width, table, refs, pools, child,
+                    (const int32_t*)child_lens, status);
+}
+
+// free: one reference less for every page of the rows; a page whose count reaches 0 goes
+// back on the stack, ascending by id (whatever order the references went in).  The one
+// decrement that takes a count from 1 to 0 marks the page by -1 in its place; a second
+// kernel, one CTA, turns the marks into 0 and pushes them by a running count over the
+// ids: 4 bytes a page of the pool.
+constexpr int kFreeThreads = 256;
+constexpr int kFreed = -1;
+__global__ void __launch_bounds__(kFreeThreads)
+free_refs_kernel(const int32_t* __restrict__ table, int64_t n, int64_t bt_width,
+                 const int32_t* __restrict__ lens, int32_t* refs, int64_t num_pages,
+                 uint32_t* status) {
+  pdl_wait();
+  const int64_t s = blockIdx.x;
+  const int64_t L = lens[s];
+  if (L < 0 || L > bt_width * kPageTokens) {
+    if (threadIdx.x == 0) flag(status, MX4_STATUS_BAD_LEN);
+    return;
+  }
+  const int64_t pages = (L + kPageTokens - 1) / kPageTokens;
+  for (int64_t j = threadIdx.x; j < pages; j += kFreeThreads) {
+    const int32_t p = table[s * bt_width + j];
+    if (p < 0 || p >= num_pages) {
+      flag(status, MX4_STATUS_BAD_PAGE);
+      continue;
+    }
+    int32_t c = refs[p], seen;
+    for (;;) {
+      if (c <= 0) {  // a page that nobody holds (or that this call has already freed)
+        flag(status, MX4_STATUS_BAD_REF);
+        break;
+      }
+      seen = atomicCAS(refs + p, c, c == 1 ? kFreed : c - 1);
+      if (seen == c) break;
+      c = seen;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kForkThreads)
+free_push_kernel(int32_t* refs, int64_t num_pages, int32_t* __restrict__ free_list,
+                 int32_t* free_count, uint32_t* status) {
+  __shared__ int s_warp[32];
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t top = max(*free_count, 0);
+  constexpr int E = 8;  // ids a thread and round
+  for (int64_t b = 0; b < num_pages; b += (int64_t)kForkThreads * E) {
+    const int64_t p0 = b + (int64_t)tid * E;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (p0 + e < num_pages && refs[p0 + e] == kFreed) mine |= 1u << e;
+    int inc = __popc(mine);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before += s_warp[w];
+      all += s_warp[w];
+    }
+    int64_t to = top + before + inc - __popc(mine);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if ((mine >> e) & 1u) {
+        refs[p0 + e] = 0;
+        if (to < num_pages)
+          free_list[to] = (int32_t)(p0 + e);
+        else
+          flag(status, MX4_STATUS_BAD_REF);  // more free pages than pages
+        ++to;
+      }
+    top += all;
+    __syncthreads();
+  }
+  if (tid == 0) *free_count = (int32_t)min(top, num_pages);
+}
+
+cudaError_t launch_free(const int32_t* table, int64_t n, int64_t bt_width, const int32_t* lens,
+                        int32_t* refs, int64_t num_pages, int32_t* free_list,
+                        int32_t* free_count, uint32_t* status, cudaStream_t stream) {
+  cudaError_t e = launch_pdl(free_refs_kernel, dim3((unsigned)n), dim3(kFreeThreads), 0, stream,
+                             table, n, bt_width, lens, refs, num_pages, status);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(free_push_kernel, dim3(1), dim3(kForkThreads), 0, stream, refs, num_pages,
+                    free_list, free_count, status);
+}
+
+}  // namespace mx4
