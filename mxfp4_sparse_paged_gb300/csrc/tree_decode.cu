@@ -30,11 +30,12 @@
 // CTA.  A tile cut by a range's end leaves a partial record (O, reference, sum) in the
 // workspace, and a second kernel joins the records of each cut tile.
 //
-// Roles.  Warp 0 streams pages (tensor copy of K into the operand's swizzled layout, bulk
-// copies of scales and of V), warp 1 issues the MMAs, warps 4-7 do the softmax (one lane a
-// token; in the epilogue one lane a dim), warps 8-11 convert q and dequantise V.  All waits
-// are bounded; after one that runs out every role goes through its loop without waiting or
-// issuing, and the status word says so.
+// Roles.  Warps 0 and 3 stream the pages' K (tensor copies into the operand's swizzled
+// layout) and V (bulk copies), warps 1 and 2 issue the two products, then come the softmax
+// warps (groups of four, one lane a token, each group its own rows; in the epilogue one lane
+// a dim) and the warps that convert q and dequantise V.  All waits are bounded; after one
+// that runs out every role goes through its loop without waiting or issuing, and the status
+// word says so.
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
 #include <cuda_bf16.h>
 
@@ -46,13 +47,30 @@ namespace mx4 {
 
 namespace tree {
 
-constexpr int kThreads = 384;
-constexpr int kMaxSeq = 512;       // sequences per launch
+constexpr int kMaxSeq = 256;       // sequences per launch
 constexpr float kLazy = 12.f;      // log2 units a logit may lie above its row's reference
 constexpr float kUnset = -3e38f;   // the reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kKStage = 128 * 128 + 512;  // K operand tile, scales
+constexpr int kKTile = 128 * 128;  // K operand tile
 constexpr int kVTile = 128 * 128 * 2;
+
+// A configuration: NR rows a tile, SG softmax groups (of NR / SG rows), DW dequantising
+// warps, KS and VS stages of K and V pages, VB operand buffers of V and P, CTAs an SM.
+// Registers are dealt out by role (RC: control warps, RS: softmax, RD: dequantisation), in
+// place of the same number for all.
+template <int NR_, int SG_, int DW_, int KS_, int VS_, int VB_, int CTAS_, int RC_, int RS_, int RD_>
+struct Cfg {
+  static constexpr int NR = NR_, SG = SG_, DW = DW_, KS = KS_, VS = VS_, VB = VB_, CTAS = CTAS_;
+  static constexpr int RC = RC_, RS = RS_, RD = RD_;
+  static_assert(DW % 4 == 0 && NR % (16 * SG) == 0, "whole warpgroups, 16 rows at a time");
+  static constexpr int kRegs = 128 * (RC + SG * RS + DW / 4 * RD);  // all that the roles take
+  static constexpr int NC = NR / SG;
+  static constexpr int kThreads = 32 * (4 + 4 * SG + DW);
+  // hi and lo of q as one operand of 2 NR rows (K read once, their products added by the
+  // softmax) while that is cheap there
+  static constexpr bool kTwin = NR <= 32;
+  static constexpr int kScols = kTwin ? 2 * NR : NR;
+};
 
 struct Args {
   CUtensorMap tmap;  // the K pool
@@ -76,43 +94,47 @@ struct Args {
 };
 
 // Shared-memory layout, in bytes.
-template <int NR, int VB, int STG>
+template <class C>
 struct Lay {
-  static constexpr int kK = 0;                         // [STG] K operand | scales
-  static constexpr int kKPitch = (kKStage + 1023) / 1024 * 1024;
-  static constexpr int kVraw = kK + STG * kKPitch;     // [STG] V pages as stored
-  static constexpr int kV = kVraw + STG * kPageBytes;  // [VB] V operand
-  static constexpr int kP = kV + VB * kVTile;          // [VB] P operand
-  static constexpr int kQ = kP + VB * NR * 256;        // q operand: hi, lo
-  static constexpr int kSf = kQ + 2 * NR * 128;        // q scale words: hi, lo
-  static constexpr int kRef = kSf + 2 * NR * 4;        // [NR] references
-  static constexpr int kFac = kRef + NR * 4;           // [NR] rescaling factors, then 1 / sum
-  static constexpr int kWarp = kFac + NR * 4;          // [4][NR] per-warp maxima and sums
-  static constexpr int kNan = kWarp + 4 * NR * 4;      // [NR] dim blocks with a visible NaN
-  static constexpr int kNode = kNan + NR * 4;          // [NR] output row, -1 none
-  static constexpr int kDepth = kNode + NR * 4;        // [NR]
-  static constexpr int kMask = kDepth + NR * 4;        // [NR] u64: nodes that the row sees
-  static constexpr int kPref = kMask + NR * 8;         // [kMaxSeq] i64 page prefix
-  static constexpr int kLen = kPref + kMaxSeq * 8;     // [kMaxSeq]
-  static constexpr int kCnt = kLen + kMaxSeq * 4;      // [kMaxSeq] u8
-  static constexpr int kInfo = kCnt + kMaxSeq;         // [STG] valid tokens of the page
-  static constexpr int kBar = (kInfo + STG * 4 + 7) / 8 * 8;
-  static constexpr int kBars = 4 * STG + 4 + 3 * VB + 4;
-  static constexpr int kMisc = kBar + kBars * 8;       // abort, tmem address, scan space
-  static constexpr int kBytes = kMisc + 256 + 1024;    // + slack for the 1024-byte alignment
+  static constexpr int NR = C::NR;
+  static constexpr int kK = 0;                               // [KS] K operand
+  static constexpr int kKsc = kK + C::KS * kKTile;           // [KS] K scale words
+  static constexpr int kVraw = kKsc + C::KS * 512;           // [VS] V pages as stored
+  static constexpr int kV = kVraw + C::VS * kPageBytes;      // [VB] V operand
+  static constexpr int kP = kV + C::VB * kVTile;             // [VB] P operand
+  static constexpr int kQ = kP + C::VB * NR * 256;           // q operand: hi, lo
+  static constexpr int kSf = kQ + 2 * NR * 128;              // q scale words: hi, lo
+  static constexpr int kRef = kSf + 2 * NR * 4;              // [NR] minus the references
+  static constexpr int kFac = kRef + NR * 4;                 // [NR] rescaling factors, then 1 / sum
+  static constexpr int kWarp = kFac + NR * 4;                // [4][NR] per-warp maxima and sums
+  static constexpr int kNan = kWarp + 4 * NR * 4;            // [NR] dim blocks with a visible NaN
+  static constexpr int kNode = kNan + NR * 4;                // [NR] output row, -1 none
+  static constexpr int kLo = kNode + NR * 4;                 // [NR] first token of the window
+  static constexpr int kMask = kLo + NR * 4;                 // [NR] u64: nodes that the row sees
+  static constexpr int kPref = kMask + NR * 8;               // [kMaxSeq] i64 page prefix
+  static constexpr int kLen = kPref + kMaxSeq * 8;           // [kMaxSeq]
+  static constexpr int kCnt = kLen + kMaxSeq * 4;            // [kMaxSeq] u8
+  static constexpr int kInfo = kCnt + kMaxSeq;               // [VS] valid tokens of the page
+  static constexpr int kBar = (kInfo + C::VS * 4 + 7) / 8 * 8;
+  static constexpr int kBars = 2 * C::KS + 2 * C::VS + 4 + 3 * C::VB + 5;
+  static constexpr int kMisc = kBar + kBars * 8;             // abort, tmem address, scan space
+  static constexpr int kBytes = kMisc + 16 + 32 * 8 + 1024;  // + slack for the 1024-byte alignment
+  static_assert(kVraw % 16 == 0 && kV % 128 == 0 && kRef % 16 == 0 && kMask % 8 == 0, "alignment");
+  static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-template <int NR>
+template <class C>
 struct Tm {  // tensor-memory columns
   static constexpr int kS = 0;                    // two S buffers
-  static constexpr int kO = 2 * NR;
-  static constexpr int kSfa = 3 * NR;             // two sets of 4
-  static constexpr int kSfb = kSfa + 8;           // hi, lo
-  static constexpr int kSfbW = (NR + 31) / 32;    // columns of each, in a field of 4
-  static constexpr int kSfbPitch = 4;             // (scale fields start at multiples of 4)
-  static_assert(kSfbW <= kSfbPitch && kSfa % 4 == 0 && kSfb % 4 == 0, "scale fields");
-  static constexpr int kUsed = kSfb + 2 * kSfbPitch;
+  static constexpr int kO = 2 * C::kScols;
+  static constexpr int kSfa = kO + C::NR;         // two sets of 4 (scale fields start at
+  static constexpr int kSfb = kSfa + 8;           // multiples of 4)
+  static constexpr int kSfbRows = C::kTwin ? 2 * C::NR : C::NR;  // rows of one operand
+  static constexpr int kSfbW = (kSfbRows + 31) / 32;             // 32 rows a column
+  static constexpr int kUsed = kSfb + (C::kTwin ? 4 : 8);
+  static_assert(kSfbW <= 4 && kSfa % 4 == 0, "scale fields");
   static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= 512 && kCols * C::CTAS <= 512, "tensor memory");
 };
 
 __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -123,7 +145,7 @@ __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo, uint32_t s
   return d;
 }
 // S^T: A e2m1, B e4m3, UE8M0 scales, M = 128, scale byte kb of both words
-template <int NR>
+template <int NR>  // N
 __device__ constexpr uint32_t idesc_s(uint32_t kb) {
   return (kb << 4) | (5u << 7) | ((uint32_t)(NR >> 3) << 17) | (1u << 23) | (8u << 24) | (kb << 29);
 }
@@ -149,6 +171,14 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 }
 __device__ __forceinline__ void st1(uint32_t taddr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(v) : "memory");
+}
+// This warpgroup's registers a thread from here on.
+template <int kFrom, int kTo>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (kTo > kFrom)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kTo));
+  else if constexpr (kTo < kFrom)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kTo));
 }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
@@ -236,10 +266,11 @@ __host__ __device__ __forceinline__ int64_t range_begin(int64_t g, int64_t U, in
   return U * g / G;
 }
 
-template <int NR, int VB, int STG, int CTAS>
-__global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__ Args a) {
-  using L_ = Lay<NR, VB, STG>;
-  using T_ = Tm<NR>;
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_constant__ Args a) {
+  using L_ = Lay<C>;
+  using T_ = Tm<C>;
+  constexpr int NR = C::NR, NC = C::NC, SG = C::SG, DW = C::DW, KS = C::KS, VS = C::VS, VB = C::VB;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -251,32 +282,35 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
   volatile int* const s_info = reinterpret_cast<volatile int*>(sm + L_::kInfo);
   volatile int* const s_abort = reinterpret_cast<volatile int*>(sm + L_::kMisc);
   uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(sm + L_::kMisc + 4);
-  int64_t* const s_scan = reinterpret_cast<int64_t*>(sm + L_::kMisc + 16);  // [12]
+  int64_t* const s_scan = reinterpret_cast<int64_t*>(sm + L_::kMisc + 16);
   auto bar = [&](int i) { return sb + L_::kBar + 8u * i; };
-  const int kKFull = 0, kKEmpty = STG, kVFull = 2 * STG, kVEmpty = 3 * STG, kSFull = 4 * STG,
-            kSFree = kSFull + 2, kPFull = kSFree + 2, kVReady = kPFull + VB, kPvDone = kVReady + VB,
-            kQFull = kPvDone + VB, kQEmpty = kQFull + 1, kOFree = kQEmpty + 1, kDrain = kOFree + 1;
+  constexpr int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = kVFull + VS,
+                kSFull = kVEmpty + VS, kSFree = kSFull + 2, kPFull = kSFree + 2,
+                kVReady = kPFull + VB, kPvDone = kVReady + VB, kQFull = kPvDone + VB,
+                kQEmpty = kQFull + 1, kOFree = kQEmpty + 1, kDrain = kOFree + 1;  // two
 
   if (tid == 0) {
-    for (int i = 0; i < STG; ++i) {
+    for (int i = 0; i < KS; ++i) {
       mbar_init(bar(kKFull + i), 1);
       mbar_init(bar(kKEmpty + i), 1);
+    }
+    for (int i = 0; i < VS; ++i) {
       mbar_init(bar(kVFull + i), 1);
-      mbar_init(bar(kVEmpty + i), 8);  // four dequantising warps, four softmax warps
+      mbar_init(bar(kVEmpty + i), DW + 4 * SG);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kSFull + i), 1);
-      mbar_init(bar(kSFree + i), 4);
+      mbar_init(bar(kSFree + i), 4 * SG);
+      mbar_init(bar(kDrain + i), 1);
     }
     for (int i = 0; i < VB; ++i) {
-      mbar_init(bar(kPFull + i), 4);
-      mbar_init(bar(kVReady + i), 4);
+      mbar_init(bar(kPFull + i), 4 * SG);
+      mbar_init(bar(kVReady + i), DW);
       mbar_init(bar(kPvDone + i), 1);
     }
-    mbar_init(bar(kQFull), 4);
+    mbar_init(bar(kQFull), DW);
     mbar_init(bar(kQEmpty), 1);
-    mbar_init(bar(kOFree), 4);
-    mbar_init(bar(kDrain), 1);
+    mbar_init(bar(kOFree), 4 * SG);
     *s_abort = 0;
     fence_barrier_init();
   }
@@ -291,27 +325,21 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
   }
   // ---- pages a sequence and their prefix sum (a tile without pages counts as one)
   {
-    constexpr int per = (kMaxSeq + kThreads - 1) / kThreads;
-    int64_t mine[per], sum = 0;
-#pragma unroll
-    for (int i = 0; i < per; ++i) {
-      const int s = tid * per + i;
-      mine[i] = 0;
-      if (s < a.B) {
-        int64_t L = a.seq_lens[s];
-        int n = a.n_nodes ? a.n_nodes[s] : a.N;
-        if (n < 0 || n > a.N || L < n || L > a.bt_width * kPageTokens) {
-          if (blockIdx.x == 0) flag(a.status, MX4_STATUS_BAD_LEN);
-          n = 0;
-          L = 0;
-        }
-        s_len[s] = (int)L;
-        s_cnt[s] = (uint8_t)n;
-        mine[i] = max(1, span_of(L, n, a.window, a.sinks).np);
+    static_assert(kMaxSeq <= C::kThreads, "a thread a sequence");
+    int64_t mine = 0;
+    if (tid < a.B) {
+      int64_t L = a.seq_lens[tid];
+      int n = a.n_nodes ? a.n_nodes[tid] : a.N;
+      if (n < 0 || n > a.N || L < n || L > a.bt_width * kPageTokens) {
+        if (blockIdx.x == 0) flag(a.status, MX4_STATUS_BAD_LEN);
+        n = 0;
+        L = 0;
       }
-      sum += mine[i];
+      s_len[tid] = (int)L;
+      s_cnt[tid] = (uint8_t)n;
+      mine = max(1, span_of(L, n, a.window, a.sinks).np);
     }
-    int64_t inc = sum;
+    int64_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
@@ -319,13 +347,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
     }
     if (lane == 31) s_scan[warp] = inc;
     __syncthreads();
-    int64_t before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += s_scan[w];
-#pragma unroll
-    for (int i = 0; i < per; ++i) {
-      before += mine[i];
-      if (tid * per + i < a.B) s_pref[tid * per + i] = before;
-    }
+    for (int w = 0; w < warp; ++w) inc += s_scan[w];
+    if (tid < a.B) s_pref[tid] = inc;
   }
   fence_before();
   __syncthreads();
@@ -352,234 +375,295 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
     return false;
   };
 
-  // The tiles of this CTA's range, in order: f(tile number in the range, sequence, head,
-  // row tile, its span, its pages [e0, e1) of this range, begins, ends).
-  auto for_tiles = [&](auto&& f) {
-    int64_t u = u0;
-    int s = 0, ht = 0, count = 0;
-    int64_t e = 0;
-    if (u < u1) {
-      int lo = 0, hi = a.B - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s_pref[mid] * HT > u) hi = mid; else lo = mid + 1;
-      }
-      s = lo;
-      const int64_t p0 = s > 0 ? s_pref[s - 1] : 0, np = s_pref[s] - p0, r = u - p0 * HT;
-      ht = (int)(r / np);
-      e = r - ht * np;
+  // Page u of the list: sequence, tile of the sequence (head major), page of the tile.
+  struct At {
+    int s, ht;
+    int64_t e;
+  };
+  auto locate = [&](int64_t u) {
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_pref[mid] * HT > u) hi = mid; else lo = mid + 1;
     }
+    const int64_t p0 = lo > 0 ? s_pref[lo - 1] : 0, np = s_pref[lo] - p0, r = u - p0 * HT;
+    At x;
+    x.s = lo;
+    x.ht = (int)(r / np);
+    x.e = r - x.ht * np;
+    return x;
+  };
+  // The tiles of this CTA's range, in order: f(tile number among those with pages, sequence,
+  // head, row tile, its span, its pages [e0, e1) of this range).
+  auto for_tiles = [&](auto&& f) {
+    if (u0 >= u1) return;
+    int64_t u = u0;
+    At x = locate(u0);
+    int count = 0;
     while (u < u1) {
-      const int64_t np = s_pref[s] - (s > 0 ? s_pref[s - 1] : 0);
-      const int64_t e1 = min(np, e + (u1 - u));
-      const Span sp = span_of(s_len[s], s_cnt[s], a.window, a.sinks);
-      f(count, s, ht / a.tiles, ht % a.tiles, sp, (int)e, (int)e1, e == 0, e1 == np);
+      const int64_t np = s_pref[x.s] - (x.s > 0 ? s_pref[x.s - 1] : 0);
+      const int64_t e1 = min(np, x.e + (u1 - u));
+      const Span sp = span_of(s_len[x.s], s_cnt[x.s], a.window, a.sinks);
+      f(count, x.s, x.ht / a.tiles, x.ht % a.tiles, sp, (int)x.e, (int)e1);
       count += sp.np > 0;
-      u += e1 - e;
-      e = 0;
-      if (++ht == HT) {
-        ht = 0;
-        ++s;
+      u += e1 - x.e;
+      x.e = 0;
+      if (++x.ht == HT) {
+        x.ht = 0;
+        ++x.s;
       }
     }
   };
   auto page_no = [](const Span& sp, int e) { return e < sp.ns ? e : sp.first + (e - sp.ns); };
 
-  if (warp == 0) {
-    // ================= producer: one lane
-    if (lane == 0) {
-      int k = 0;
-      for_tiles([&](int, int s, int h, int, const Span& sp, int e0, int e1, bool, bool) {
-        if (sp.np == 0) return;
-        for (int e = e0; e < e1; ++e, ++k) {
-          const int pg = page_no(sp, e), st = k % STG, round = k / STG;
-          const int32_t pid = a.table[(int64_t)s * a.bt_width + pg];
+  constexpr int kLaunchRegs = 65536 / (C::CTAS * C::kThreads) / 8 * 8;
+  static_assert(C::kRegs <= kLaunchRegs * C::kThreads, "the roles' registers are the launch's");
+  if (warp < 4) {
+  set_regs<kLaunchRegs, C::RC>();  // (by the warpgroup as one)
+  if (warp == 0 || warp == 3) {
+    // ================= producers: K (warp 0) and V (warp 3).  The lanes look up the next 32
+    // pages' table entries at once, a batch ahead.
+    const bool isv = warp == 3;
+    struct Look {
+      int pid, h, live;  // live < 0: a tile without pages
+    };
+    auto look = [&](int64_t u) {
+      Look x{-1, 0, -1};
+      if (u < u1) {
+        const At y = locate(u);
+        const Span sp = span_of(s_len[y.s], s_cnt[y.s], a.window, a.sinks);
+        if (sp.np > 0) {
+          const int pg = page_no(sp, (int)y.e);
+          x.pid = a.table[(int64_t)y.s * a.bt_width + pg];
+          x.h = y.ht / a.tiles;
+          x.live = min(kPageTokens, sp.len - pg * kPageTokens);
+        }
+      }
+      return x;
+    };
+    int k = 0;
+    Look nxt = look(u0 + lane);
+    for (int64_t ub = u0; ub < u1; ub += 32) {
+      const Look cur = nxt;
+      nxt = look(ub + 32 + lane);
+      const int cnt = (int)min((int64_t)32, u1 - ub);
+      for (int i = 0; i < cnt; ++i) {
+        const int pid = __shfl_sync(0xFFFFFFFFu, cur.pid, i);
+        const int h = __shfl_sync(0xFFFFFFFFu, cur.h, i);
+        const int live = __shfl_sync(0xFFFFFFFFu, cur.live, i);
+        if (live < 0) continue;
+        if (lane == 0) {
           const bool ok = pid >= 0 && pid < a.num_pages;
-          if (!ok) flag(a.status, MX4_STATUS_BAD_PAGE);
-          bool go = !*s_abort;
-          if (round > 0) go = wait(kKEmpty + st, (round - 1) & 1) && go;
-          if (round > 0) go = wait(kVEmpty + st, (round - 1) & 1) && go;
-          if (!go) continue;
-          s_info[st] = ok ? min(kPageTokens, sp.len - pg * kPageTokens) : 0;
-          if (ok) {
-            const uint32_t kd = sb + L_::kK + st * L_::kKPitch, vd = sb + L_::kVraw + st * kPageBytes;
-            const int64_t off = (int64_t)pid * a.page_stride + (int64_t)h * a.head_stride;
-            mbar_arrive_expect_tx(bar(kKFull + st), kRowDataBytes * kPageTokens + 512);
-            asm volatile(
-                "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(kd),
-                "l"(reinterpret_cast<uint64_t>(&a.tmap)), "r"(0), "r"(0), "r"(0), "r"(h), "r"(pid),
-                "r"(bar(kKFull + st))
-                : "memory");
-            bulk_copy_g2s(kd + 128 * 128, a.k_pages + off + kScaleOffset, 512, bar(kKFull + st));
-            mbar_arrive_expect_tx(bar(kVFull + st), kPageBytes);
-            bulk_copy_g2s(vd, a.v_pages + off, kPageBytes, bar(kVFull + st));
+          const int64_t off = (int64_t)pid * a.page_stride + (int64_t)h * a.head_stride;
+          if (!isv) {
+            const int st = k % KS, round = k / KS;
+            bool go = !*s_abort;
+            if (round > 0) go = wait(kKEmpty + st, (round - 1) & 1) && go;
+            if (go && ok) {
+              const uint32_t kd = sb + L_::kK + st * kKTile, fb = bar(kKFull + st);
+              mbar_arrive_expect_tx(fb, kRowDataBytes * kPageTokens + 512);
+              asm volatile(
+                  "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                  "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(kd),
+                  "l"(reinterpret_cast<uint64_t>(&a.tmap)), "r"(0), "r"(0), "r"(0), "r"(h),
+                  "r"(pid), "r"(fb)
+                  : "memory");
+              bulk_copy_g2s(sb + L_::kKsc + st * 512, a.k_pages + off + kScaleOffset, 512, fb);
+            } else if (go) {
+              mbar_arrive(bar(kKFull + st));
+            }
           } else {
-            mbar_arrive(bar(kKFull + st));
-            mbar_arrive(bar(kVFull + st));
+            const int st = k % VS, round = k / VS;
+            if (!ok) flag(a.status, MX4_STATUS_BAD_PAGE);
+            bool go = !*s_abort;
+            if (round > 0) go = wait(kVEmpty + st, (round - 1) & 1) && go;
+            if (go) s_info[st] = ok ? live : 0;
+            if (go && ok) {
+              mbar_arrive_expect_tx(bar(kVFull + st), kPageBytes);
+              bulk_copy_g2s(sb + L_::kVraw + st * kPageBytes, a.v_pages + off, kPageBytes,
+                            bar(kVFull + st));
+            } else if (go) {
+              mbar_arrive(bar(kVFull + st));
+            }
           }
         }
-      });
-      // every copy has landed before the CTA ends
-      for (int i = max(0, k - STG); i < k; ++i) {
-        wait(kKFull + i % STG, (i / STG) & 1);
-        wait(kVFull + i % STG, (i / STG) & 1);
+        ++k;
       }
+      __syncwarp();
+    }
+    // every copy has landed before the CTA ends
+    if (lane == 0) {
+      const int S = isv ? VS : KS, full = isv ? kVFull : kKFull;
+      for (int i = max(0, k - S); i < k; ++i) wait(full + i % S, (i / S) & 1);
     }
   } else if (warp == 1) {
-    // ================= MMA issue: one lane
+    // ================= S^T = K q^T: one lane
     if (lane == 0) {
       int k = 0;
-      bool any = false;
-      // the page whose P V product is still to be issued
-      int pv = -1;
-      bool pv_first = false;
-      int pv_tile = 0;
-      auto issue_pv = [&]() {
-        const int b = pv % VB;
-        bool go = wait(kPFull + b, (pv / VB) & 1);
-        go = wait(kVReady + b, (pv / VB) & 1) && go;
-        if (pv_first && pv_tile > 0) go = wait(kOFree, (pv_tile - 1) & 1) && go;
-        if (!go || *s_abort) return;
-        fence_after();
-        const uint32_t va = sb + L_::kV + b * kVTile, pa = sb + L_::kP + b * NR * 256;
-#pragma unroll
-        for (uint32_t ks = 0; ks < 8; ++ks) {
-          const uint64_t ad = desc(va + ks * 256, 128, 2048), bd = desc(pa + ks * 256, 128, 2048);
-          asm volatile(
-              "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-              " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tm + T_::kO),
-              "l"(ad), "l"(bd), "r"(idesc_o<NR>()), "r"((uint32_t)(ks > 0 || !pv_first))
-              : "memory");
-        }
-        commit(bar(kPvDone + b));
-      };
-      for_tiles([&](int tile, int, int, int, const Span& sp, int e0, int e1, bool, bool) {
+      for_tiles([&](int tile, int, int, int, const Span& sp, int e0, int e1) {
         if (sp.np == 0) return;
-        any = true;
         for (int e = e0; e < e1; ++e, ++k) {
-          const int st = k % STG, b = k & 1;
+          const int st = k % KS, b = k & 1;
           bool go = true;
           if (e == e0) go = wait(kQFull, tile & 1);
-          go = wait(kKFull + st, (k / STG) & 1) && go;
+          go = wait(kKFull + st, (k / KS) & 1) && go;
           if (k >= 2) go = wait(kSFree + b, ((k >> 1) - 1) & 1) && go;
-          if (go && !*s_abort) {
-            fence_after();
-            const uint32_t ka = sb + L_::kK + st * L_::kKPitch, qa = sb + L_::kQ;
-            const uint32_t sfa = tm + T_::kSfa + 4u * b;
-            asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(sfa),
-                         "l"(desc(ka + 128 * 128, 16, 128))
-                         : "memory");
+          if (!go || *s_abort) continue;
+          fence_after();
+          const uint32_t ka = sb + L_::kK + st * kKTile, qa = sb + L_::kQ;
+          const uint32_t sfa = tm + T_::kSfa + 4u * b;
+          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(sfa),
+                       "l"(desc(sb + L_::kKsc + st * 512, 16, 128))
+                       : "memory");
 #pragma unroll
-            for (uint32_t part = 0; part < 2; ++part)
+          for (uint32_t part = 0; part < (C::kTwin ? 1 : 2); ++part)
 #pragma unroll
-              for (uint32_t kb = 0; kb < 4; ++kb) {
-                const uint64_t ad = desc(ka + kb * 32, 16, 1024) | ((uint64_t)2 << 61);
-                const uint64_t bd = desc(qa + part * NR * 128 + kb * 256, 128, 1024);
-                asm volatile(
-                    "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-                    " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, "
-                    "%2, %3, [%4], [%5], p;\n}\n" ::"r"(tm + T_::kS + b * NR),
-                    "l"(ad), "l"(bd), "r"(idesc_s<NR>(kb)), "r"(sfa),
-                    "r"(tm + T_::kSfb + part * T_::kSfbPitch), "r"(part + kb)
-                    : "memory");
-              }
-            commit(bar(kSFull + b));
-            commit(bar(kKEmpty + st));
-            if (e == e1 - 1) commit(bar(kQEmpty));
-          }
-          if (pv >= 0) issue_pv();
-          pv = k;
-          pv_first = e == e0;
-          pv_tile = tile;
+            for (uint32_t kb = 0; kb < 4; ++kb) {
+              const uint64_t ad = desc(ka + kb * 32, 16, 1024) | ((uint64_t)2 << 61);
+              const uint64_t bd = desc(qa + part * NR * 128 + kb * 256, 128, 1024);
+              asm volatile(
+                  "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+                  " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, "
+                  "%2, %3, [%4], [%5], p;\n}\n" ::"r"(tm + T_::kS + b * C::kScols),
+                  "l"(ad), "l"(bd), "r"(idesc_s<T_::kSfbRows>(kb)), "r"(sfa),
+                  "r"(tm + T_::kSfb + part * 4), "r"(part + kb)
+                  : "memory");
+            }
+          commit(bar(kSFull + b));
+          commit(bar(kKEmpty + st));
+          if (e == e1 - 1) commit(bar(kQEmpty));
         }
       });
-      if (pv >= 0) issue_pv();
-      if (any) {  // no MMA in flight when the tensor memory is freed
+      if (k > 0) {  // no MMA in flight when the tensor memory is freed
         commit(bar(kDrain));
         for (uint32_t p = 0; p < kWaitPolls; ++p)
           if (mbar_test(bar(kDrain), 0)) break;
       }
     }
-  } else if (warp >= 8) {
+  } else {
+    // ================= O^T += V^T P^T: one lane
+    if (lane == 0) {
+      int k = 0;
+      for_tiles([&](int tile, int, int, int, const Span& sp, int e0, int e1) {
+        if (sp.np == 0) return;
+        for (int e = e0; e < e1; ++e, ++k) {
+          const int b = k % VB;
+          bool go = true;
+          if (e == e0 && tile > 0) go = wait(kOFree, (tile - 1) & 1);
+          go = wait(kVReady + b, (k / VB) & 1) && go;
+          go = wait(kPFull + b, (k / VB) & 1) && go;
+          if (!go || *s_abort) continue;
+          fence_after();
+          const uint32_t va = sb + L_::kV + b * kVTile, pa = sb + L_::kP + b * NR * 256;
+#pragma unroll
+          for (uint32_t ks = 0; ks < 8; ++ks) {
+            const uint64_t ad = desc(va + ks * 256, 128, 2048), bd = desc(pa + ks * 256, 128, 2048);
+            asm volatile(
+                "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tm + T_::kO),
+                "l"(ad), "l"(bd), "r"(idesc_o<NR>()), "r"((uint32_t)(ks > 0 || e > e0))
+                : "memory");
+          }
+          commit(bar(kPvDone + b));
+        }
+      });
+      if (k > 0) {
+        commit(bar(kDrain + 1));
+        for (uint32_t p = 0; p < kWaitPolls; ++p)
+          if (mbar_test(bar(kDrain + 1), 0)) break;
+      }
+    }
+  }
+  } else if (warp >= 4 + 4 * SG) {
+    set_regs<kLaunchRegs, C::RD>();
     // ================= q conversion and V dequantisation
-    const int t = tid - 256, w = warp - 8;
+    const int t = tid - 32 * (4 + 4 * SG), w = t >> 5;
     const int r8 = lane & 7, blk = ((r8 >> 1) + (lane >> 3)) & 3;  // see below
     int k = 0;
-    for_tiles([&](int tile, int s, int h, int rt, const Span& sp, int e0, int e1, bool, bool) {
+    for_tiles([&](int tile, int s, int h, int rt, const Span& sp, int e0, int e1) {
       if (sp.np == 0) return;
-      if (tile > 0) wait(kQEmpty, (tile - 1) & 1);
       // 16 elements a thread: K-chunk j of row n; the two threads of a 32-block share its
-      // largest magnitude
-      for (int n = t >> 3; n < NR; n += 16) {
-        const int j = t & 7, row = rt * NR + n, node = row / a.G;
-        uint32_t wd[8] = {};
-        float amax = 0.f;
-        if (node < sp.n) {
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + (((int64_t)s * a.N + node) * a.H + h * a.G + row % a.G) * kHeadDim + 16 * j);
-          const uint4 x0 = src[0], x1 = src[1];
-          wd[0] = x0.x; wd[1] = x0.y; wd[2] = x0.z; wd[3] = x0.w;
-          wd[4] = x1.x; wd[5] = x1.y; wd[6] = x1.z; wd[7] = x1.w;
-        }
+      // largest magnitude.  The rows are on their way while the tile before finishes.
+      constexpr int kIt = (NR * 8 + DW * 32 - 1) / (DW * 32);
+      uint4 x0[kIt], x1[kIt];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_float(wd[i] & 0xFFFFu)),
-                                   fabsf(bf16_bits_to_float(wd[i] >> 16))));
+      for (int i = 0; i < kIt; ++i) {
+        const int n = (t >> 3) + i * DW * 4, row = rt * NR + n, node = row / a.G;
+        x0[i] = x1[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (n < NR && node < sp.n) {
+          const uint4* src = reinterpret_cast<const uint4*>(
+              a.q + (((int64_t)s * a.N + node) * a.H + h * a.G + row % a.G) * kHeadDim +
+              16 * (t & 7));
+          x0[i] = src[0];
+          x1[i] = src[1];
+        }
+      }
+      if (tile > 0) wait(kQEmpty, (tile - 1) & 1);
+#pragma unroll
+      for (int i = 0; i < kIt; ++i) {
+        const int n = (t >> 3) + i * DW * 4, j = t & 7;
+        const uint32_t wd[8] = {x0[i].x, x0[i].y, x0[i].z, x0[i].w, x1[i].x, x1[i].y, x1[i].z, x1[i].w};
+        float amax = 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_float(wd[u] & 0xFFFFu)),
+                                   fabsf(bf16_bits_to_float(wd[u] >> 16))));
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
         const int ef = min(254, (int)(__float_as_uint(amax) >> 23));
         const int E = amax == 0.f ? 0 : max(-122, ef - 127 - 7);
         const float inv = __uint_as_float((uint32_t)(127 - E) << 23);
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int u = 0; u < 4; ++u) {
           uint16_t hc[2], lc[2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t x2 = wd[2 * i + u];
-            float x0 = bf16_bits_to_float(x2 & 0xFFFFu), x1 = bf16_bits_to_float(x2 >> 16);
+          for (int v = 0; v < 2; ++v) {
+            const uint32_t x2 = wd[2 * u + v];
+            float y0 = bf16_bits_to_float(x2 & 0xFFFFu), y1 = bf16_bits_to_float(x2 >> 16);
             // an infinity has no E4M3 code: NaN, as its logits would be
-            x0 = isinf(x0) ? NAN : x0 * inv;
-            x1 = isinf(x1) ? NAN : x1 * inv;
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;\n" : "=h"(hc[u]) : "f"(x0), "f"(x1));
+            y0 = isinf(y0) ? NAN : y0 * inv;
+            y1 = isinf(y1) ? NAN : y1 * inv;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;\n" : "=h"(hc[v]) : "f"(y0), "f"(y1));
             uint32_t hf;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(hf) : "h"(hc[u]));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(hf) : "h"(hc[v]));
             const float h0 = __half2float(__ushort_as_half((unsigned short)(hf & 0xFFFFu)));
             const float h1 = __half2float(__ushort_as_half((unsigned short)(hf >> 16)));
             asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;\n"
-                : "=h"(lc[u])
-                : "f"((x0 - h0) * 32.f), "f"((x1 - h1) * 32.f));
+                : "=h"(lc[v])
+                : "f"((y0 - h0) * 32.f), "f"((y1 - h1) * 32.f));
           }
-          hi[i] = (uint32_t)hc[0] | ((uint32_t)hc[1] << 16);
-          lo[i] = (uint32_t)lc[0] | ((uint32_t)lc[1] << 16);
+          hi[u] = (uint32_t)hc[0] | ((uint32_t)hc[1] << 16);
+          lo[u] = (uint32_t)lc[0] | ((uint32_t)lc[1] << 16);
         }
-        uint8_t* dst = sm + L_::kQ + (n >> 3) * 1024 + j * 128 + (n & 7) * 16;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + NR * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        if ((j & 1) == 0) {
-          sm[L_::kSf + n * 4 + (j >> 1)] = (uint8_t)(E + 127);
-          sm[L_::kSf + (NR + n) * 4 + (j >> 1)] = (uint8_t)(E + 122);
+        if (n < NR) {
+          uint8_t* dst = sm + L_::kQ + (n >> 3) * 1024 + j * 128 + (n & 7) * 16;
+          *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(dst + NR * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if ((j & 1) == 0) {
+            sm[L_::kSf + n * 4 + (j >> 1)] = (uint8_t)(E + 127);
+            sm[L_::kSf + (NR + n) * 4 + (j >> 1)] = (uint8_t)(E + 122);
+          }
         }
       }
       fence_async();
-      asm volatile("bar.sync 2, 128;\n" ::: "memory");
-      // row n's scale word at lane n % 32 of every lane quarter, column n / 32
+      asm volatile("bar.sync 7, %0;\n" ::"n"(32 * DW) : "memory");
+      // operand row n's scale word at lane n % 32 of every lane quarter, column n / 32
+      if (w < 4) {
 #pragma unroll
-      for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < (C::kTwin ? 1 : 2); ++part)
 #pragma unroll
-        for (int c = 0; c < T_::kSfbW; ++c)
-          st1(tm + ((uint32_t)(32 * w) << 16) + T_::kSfb + part * T_::kSfbPitch + c,
-              *reinterpret_cast<const uint32_t*>(
-                  sm + L_::kSf + (part * NR + min(NR - 1, c * 32 + lane)) * 4));
-      wait_st();
+          for (int c = 0; c < T_::kSfbW; ++c)
+            st1(tm + ((uint32_t)(32 * w) << 16) + T_::kSfb + part * 4 + c,
+                *reinterpret_cast<const uint32_t*>(sm + L_::kSf + (part * NR + c * 32 + lane) * 4));
+        wait_st();
+      }
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kQFull));
 
       for (int e = e0; e < e1; ++e, ++k) {
-        const int st = k % STG, b = k % VB;
-        wait(kVFull + st, (k / STG) & 1);
-        if (k >= VB) wait(kPvDone + b, (k / VB - 1) & 1);
+        const int st = k % VS, b = k % VB;
+        wait(kVFull + st, (k / VS) & 1);
         const int live = s_info[st];
         const uint8_t* raw = sm + L_::kVraw + st * kPageBytes;
         uint8_t* const vb = sm + L_::kV + b * kVTile;
@@ -587,18 +671,24 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
         // tensor copy lays out K.  A warp's step: the 8 operand rows of one core matrix
         // (r8), lane >> 3 choosing which 32-dim block of each: 16 raw bytes a lane, four
         // 16-byte stores without bank conflicts.
+        constexpr int kIts = 16 / DW;
+        uint4 c4[kIts];
+        uint32_t sc[kIts];
+        bool use[kIts];
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const int m = (w * 4 + it) * 8 + r8;
-          const int tok = 4 * (m & 31) + (m >> 5);
-          const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tok * kRowDataBytes + blk * 16);
-          const uint32_t sc = raw[kScaleOffset + tok * kRowScaleBytes + blk];
-          const bool use = tok < live && sc != 255u;
+        for (int it = 0; it < kIts; ++it) {
+          const int m = (w * kIts + it) * 8 + r8, tok = 4 * (m & 31) + (m >> 5);
+          c4[it] = *reinterpret_cast<const uint4*>(raw + tok * kRowDataBytes + blk * 16);
+          sc[it] = raw[kScaleOffset + tok * kRowScaleBytes + blk];
+          use[it] = tok < live && sc[it] != 255u;
+        }
+        if (k >= VB) wait(kPvDone + b, (k / VB - 1) & 1);
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+          const int m = (w * kIts + it) * 8 + r8;
           // 2^(sc - 1), as two factors where it passes bf16's range
-          const uint32_t e1x = use ? min(sc + 126u, 254u) : 0u;
-          const uint32_t f1 = (e1x << 7) * 0x10001u;
-          const uint32_t f2 = ((127u + (sc > 128u ? sc - 128u : 0u)) << 7) * 0x10001u;
-          const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+          const uint32_t f1 = ((use[it] ? min(sc[it] + 126u, 254u) : 0u) << 7) * 0x10001u;
+          const uint32_t cw[4] = {c4[it].x, c4[it].y, c4[it].z, c4[it].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t x = cw[j];
@@ -610,9 +700,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
             y[3] = (x & 0x80008000u) | ((x >> 6) & 0x01C001C0u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = bf16_mul2(y[i], f1);
-            if (sc > 128u)
+            if (sc[it] > 128u) {
+              const uint32_t f2 = ((sc[it] - 1u) << 7) * 0x10001u;
 #pragma unroll
               for (int i = 0; i < 4; ++i) y[i] = bf16_mul2(y[i], f2);
+            }
             *reinterpret_cast<uint4*>(vb + (blk * 4 + j) * 2048 + (m >> 3) * 128 + r8 * 16) =
                 make_uint4(y[0], y[1], y[2], y[3]);
           }
@@ -625,40 +717,41 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
         }
       }
     });
-  } else if (warp >= 4) {
-    // ================= softmax
-    const int t = tid - 128, w = warp - 4;
+  } else {
+    set_regs<kLaunchRegs, C::RS>();
+    // ================= softmax: group sg has the rows c0 .. c0 + NC - 1 of a tile
+    const int sg = (warp - 4) >> 2, w = warp & 3, t = tid & 127, c0 = sg * NC;
     const uint32_t tl = tm + ((uint32_t)(32 * w) << 16);
-    float* const s_ref = reinterpret_cast<float*>(sm + L_::kRef);
-    float* const s_fac = reinterpret_cast<float*>(sm + L_::kFac);
-    float* const s_warp = reinterpret_cast<float*>(sm + L_::kWarp);
-    uint32_t* const s_nan = reinterpret_cast<uint32_t*>(sm + L_::kNan);
-    int* const s_node = reinterpret_cast<int*>(sm + L_::kNode);
-    int* const s_depth = reinterpret_cast<int*>(sm + L_::kDepth);
-    uint64_t* const s_mask = reinterpret_cast<uint64_t*>(sm + L_::kMask);
-    auto sync4 = []() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); };
-    auto any4 = [](bool v) {
+    float* const s_nref = reinterpret_cast<float*>(sm + L_::kRef) + c0;
+    float* const s_fac = reinterpret_cast<float*>(sm + L_::kFac) + c0;
+    float* const s_warp = reinterpret_cast<float*>(sm + L_::kWarp) + 4 * c0;  // [4][NC]
+    uint32_t* const s_nan = reinterpret_cast<uint32_t*>(sm + L_::kNan) + c0;
+    int* const s_node = reinterpret_cast<int*>(sm + L_::kNode) + c0;
+    int* const s_lo = reinterpret_cast<int*>(sm + L_::kLo) + c0;
+    uint32_t* const s_mask = reinterpret_cast<uint32_t*>(sm + L_::kMask) + 2 * c0;  // [NC][2]
+    auto sync4 = [&]() { asm volatile("bar.sync %0, 128;\n" ::"r"(sg + 1) : "memory"); };
+    auto any4 = [&](bool v) {
       uint32_t r;
       asm volatile(
           "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-          " barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+          " barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
           : "=r"(r)
-          : "r"((uint32_t)v)
+          : "r"((uint32_t)v), "r"(sg + 1)
           : "memory");
       return r != 0u;
     };
     const float cs = a.scale * kLog2e;
     const int tok = 4 * lane + w;  // this lane's token of a page
     int k = 0;
-    for_tiles([&](int tile, int s, int h, int rt, const Span& sp, int e0, int e1, bool begins,
-                  bool ends) {
+    for_tiles([&](int tile, int s, int h, int rt, const Span& sp, int e0, int e1) {
+      const bool begins = e0 == 0, ends = e1 >= sp.np;
       // ---- the tile's rows
       sync4();  // the tile before is written out
-      for (int c = t; c < NR; c += 128) {
-        const int row = rt * NR + c, node = row / a.G;
-        s_node[c] = node < a.N ? node * a.H + h * a.G + row % a.G : -1;
+      if (t < NC) {
+        const int row = rt * NR + c0 + t, node = row / a.G;
+        s_node[t] = node < a.N ? node * a.H + h * a.G + row % a.G : -1;
         uint64_t mk = 0;
-        int d = 0;
+        int lo = 0;
         if (node < sp.n) {
           const uint64_t all = sp.n < 64 ? (1ull << sp.n) - 1 : ~0ull;
           auto mask_of = [&](int j) {
@@ -666,31 +759,32 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
           };
           auto depth_of = [&](int j) { return max(1, __popcll(mask_of(j))) - 1; };
           mk = mask_of(node);
-          d = depth_of(node);
-          if (a.window > 0)
+          if (a.window > 0) {
+            const int d = depth_of(node);
+            lo = (int)max((int64_t)0, sp.base + d + 1 - a.window);
             for (int i = 0; i < sp.n; ++i)
               if ((mk >> i) & 1ull) {
                 const int di = depth_of(i);
                 if (!(di > d - a.window || sp.base + di < a.sinks)) mk &= ~(1ull << i);
               }
-        } else {
-          d = -1;  // no node: sees nothing, whatever is computed for it
+          }
         }
-        s_mask[c] = mk;
-        s_depth[c] = d;
-        s_ref[c] = kUnset;
-        s_nan[c] = 0;
+        s_mask[2 * t] = (uint32_t)mk;
+        s_mask[2 * t + 1] = (uint32_t)(mk >> 32);
+        s_lo[t] = lo;
+        s_nref[t] = -kUnset;
+        s_nan[t] = 0;
       }
       sync4();
-      float l[NR];
+      float l[NC];
 #pragma unroll
-      for (int c = 0; c < NR; ++c) l[c] = 0.f;
+      for (int c = 0; c < NC; ++c) l[c] = 0.f;
 
       if (sp.np > 0) {
         for (int e = e0; e < e1; ++e, ++k) {
-          const int st = k % STG, b = k & 1, pb = k % VB;
-          const int64_t first = (int64_t)page_no(sp, e) * kPageTokens, i_g = first + tok;
-          wait(kVFull + st, (k / STG) & 1);
+          const int st = k % VS, b = k & 1, pb = k % VB;
+          const int first = page_no(sp, e) * kPageTokens, i_g = first + tok;
+          wait(kVFull + st, (k / VS) & 1);
           const int live = s_info[st];
           uint32_t vw = *reinterpret_cast<const uint32_t*>(sm + L_::kVraw + st * kPageBytes +
                                                            kScaleOffset + tok * kRowScaleBytes);
@@ -701,96 +795,122 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
           const bool plain = live == kPageTokens && first + kPageTokens <= sp.base &&
                              (a.window == 0 || first > sp.base + 63 - a.window ||
                               first + kPageTokens <= a.sinks);
+          // a row sees a draft by its mask, an earlier token from the window's first on;
+          // rows without a node see what they like, their results are zeroed
+          const int nd = i_g - (int)sp.base;
           auto sees = [&](int c) {
-            if (tok >= live || s_depth[c] < 0) return false;
-            if (i_g >= sp.base) return ((s_mask[c] >> (int)(i_g - sp.base)) & 1ull) != 0;
-            return a.window == 0 || i_g > sp.base + s_depth[c] - a.window || i_g < a.sinks;
+            return nd >= 0 ? ((s_mask[2 * c + ((nd >> 5) & 1)] >> (nd & 31)) & 1u) != 0u
+                           : i_g >= s_lo[c] || i_g < a.sinks;
           };
           wait(kSFull + b, (k >> 1) & 1);
           fence_after();
-          float x[NR];
-          auto logits = [&]() {
+          float x[NC];
+          const uint32_t ts = tl + T_::kS + b * C::kScols + c0;
+          // S of 16 rows, hi and lo parts added where they are apart
+          auto s16 = [&](int c, float* v) {
+            ld16(ts + c, v);
+            if constexpr (C::kTwin) {
+              float y[16];
+              ld16(ts + NR + c, y);
+              wait_ld();
 #pragma unroll
-            for (int c = 0; c < NR; c += 16) ld16(tl + T_::kS + b * NR + c, x + c);
-            wait_ld();
-          };
-          auto hide = [&]() {  // -inf where not seen, whatever was computed there
-            if (!plain) {
-#pragma unroll
-              for (int c = 0; c < NR; ++c)
-                if (!sees(c)) x[c] = -INFINITY;
+              for (int i = 0; i < 16; ++i) v[i] += y[i];
+            } else {
+              wait_ld();
             }
           };
-          logits();
+          // -inf where not seen, whatever was computed there
+          auto hide16 = [&](int c, float* v) {
+            if (plain) return;
+            if (tok >= live) {
 #pragma unroll
-          for (int c = 0; c < NR; c += 4) {
-            const float4 rf = *reinterpret_cast<const float4*>(s_ref + c);
-            x[c] = fmaf(x[c], cs, -rf.x);
-            x[c + 1] = fmaf(x[c + 1], cs, -rf.y);
-            x[c + 2] = fmaf(x[c + 2], cs, -rf.z);
-            x[c + 3] = fmaf(x[c + 3], cs, -rf.w);
-          }
-          hide();
-          float top = -INFINITY;
+              for (int i = 0; i < 16; ++i) v[i] = -INFINITY;
+            } else if (nd >= 0 || a.window > 0) {
 #pragma unroll
-          for (int c = 0; c < NR; ++c) top = fmaxf(top, x[c]);
-          if (any4(top > kLazy)) {
-            // new references: the page's maximum of each row that has a larger one
-            logits();
-#pragma unroll
-            for (int c = 0; c < NR; ++c) x[c] = x[c] * cs;
-            hide();
-#pragma unroll
-            for (int c = 0; c < NR; c += 16) {
-              const float v = columns16(x + c, lane, [](float p, float q) { return fmaxf(p, q); });
-              if (lane < 16) s_warp[w * NR + c + lane] = v;
+              for (int i = 0; i < 16; ++i)
+                if (!sees(c + i)) v[i] = -INFINITY;
             }
-            if (k > 0 && e > e0) wait(kPvDone + (k - 1) % VB, ((k - 1) / VB) & 1);
+          };
+          for (bool again = false;; again = true) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < NC; c += 16) {
+              s16(c, x + c);
+#pragma unroll
+              for (int i = c; i < c + 16; i += 4) {
+                const float4 rf = *reinterpret_cast<const float4*>(s_nref + i);
+                x[i] = fmaf(x[i], cs, rf.x);
+                x[i + 1] = fmaf(x[i + 1], cs, rf.y);
+                x[i + 2] = fmaf(x[i + 2], cs, rf.z);
+                x[i + 3] = fmaf(x[i + 3], cs, rf.w);
+              }
+              hide16(c, x + c);
+              float m[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) m[i] = fmaxf(x[c + i], x[c + 8 + i]);
+#pragma unroll
+              for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < o; ++i) m[i] = fmaxf(m[i], m[i + o]);
+              top = fmaxf(top, m[0]);
+            }
+            if (again || !any4(top > kLazy)) break;
+            // new references: the page's maximum of each row that has a larger one; what was
+            // summed so far is brought to them, and the page's logits are taken once more
+#pragma unroll 1
+            for (int c = 0; c < NC; c += 16) {
+              float v[16];
+              s16(c, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] *= cs;
+              hide16(c, v);
+              const float mx = columns16(v, lane, [](float p, float q) { return fmaxf(p, q); });
+              if (lane < 16) s_warp[w * NC + c + lane] = mx;
+            }
+            if (e > e0) wait(kPvDone + (k - 1) % VB, ((k - 1) / VB) & 1);
             sync4();
-            for (int c = t; c < NR; c += 128) {
-              const float v = fmaxf(fmaxf(s_warp[c], s_warp[NR + c]),
-                                    fmaxf(s_warp[2 * NR + c], s_warp[3 * NR + c]));
-              const float old = s_ref[c], now = fmaxf(old, v);
-              s_fac[c] = old == kUnset ? 0.f : ex2(old - now);
-              s_ref[c] = now;
+            if (t < NC) {
+              const float v = fmaxf(fmaxf(s_warp[t], s_warp[NC + t]),
+                                    fmaxf(s_warp[2 * NC + t], s_warp[3 * NC + t]));
+              const float old = -s_nref[t], now = fmaxf(old, v);
+              s_fac[t] = old == kUnset ? 0.f : ex2(old - now);
+              s_nref[t] = -now;
             }
             sync4();
 #pragma unroll
-            for (int c = 0; c < NR; ++c) {
-              l[c] *= s_fac[c];
-              x[c] -= s_ref[c];
-            }
+            for (int c = 0; c < NC; ++c) l[c] *= s_fac[c];
             if (e > e0) {
               fence_after();
-#pragma unroll
-              for (int c = 0; c < NR; c += 16) {
+#pragma unroll 1
+              for (int c = 0; c < NC; c += 16) {
                 float o[16];
-                ld16(tl + T_::kO + c, o);
+                ld16(tl + T_::kO + c0 + c, o);
                 wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] *= s_fac[c + i];
-                st16(tl + T_::kO + c, o);
+                st16(tl + T_::kO + c0 + c, o);
               }
               wait_st();
             }
           }
-          // the accumulator has been read: the next page's product may go into it
+          // the accumulator has been read: a later page's product may go into it
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kSFree + b));
           if (vw != 0u) {
-            for (int c = 0; c < NR; ++c)
-              if (sees(c)) atomicOr(s_nan + c, vw);
+            for (int c = 0; c < NC; ++c)
+              if (tok < live && (plain || (nd < 0 && a.window == 0) || sees(c))) atomicOr(s_nan + c, vw);
           }
 #pragma unroll
-          for (int c = 0; c < NR; ++c) {
+          for (int c = 0; c < NC; ++c) {
             x[c] = ex2(x[c]);
             l[c] += x[c];
           }
           if (k >= VB) wait(kPvDone + pb, (k / VB - 1) & 1);
-          uint8_t* const pd = sm + L_::kP + pb * NR * 256 + (4 * w + (lane >> 3)) * 128 + (lane & 7) * 16;
+          uint8_t* const pd = sm + L_::kP + pb * NR * 256 + (c0 >> 3) * 2048 +
+                              (4 * w + (lane >> 3)) * 128 + (lane & 7) * 16;
 #pragma unroll
-          for (int c = 0; c < NR; c += 8)
+          for (int c = 0; c < NC; c += 8)
             *reinterpret_cast<uint4*>(pd + (c >> 3) * 2048) =
                 make_uint4(pack_bf16(x[c], x[c + 1]), pack_bf16(x[c + 2], x[c + 3]),
                            pack_bf16(x[c + 4], x[c + 5]), pack_bf16(x[c + 6], x[c + 7]));
@@ -799,32 +919,32 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
           if (lane == 0) mbar_arrive(bar(kPFull + pb));
         }
 #pragma unroll
-        for (int c = 0; c < NR; c += 16) {
+        for (int c = 0; c < NC; c += 16) {
           const float v = columns16(l + c, lane, [](float p, float q) { return p + q; });
-          if (lane < 16) s_warp[w * NR + c + lane] = v;
+          if (lane < 16) s_warp[w * NC + c + lane] = v;
         }
         wait(kPvDone + (k - 1) % VB, ((k - 1) / VB) & 1);
         sync4();
       } else {
-        for (int c = t; c < 4 * NR; c += 128) s_warp[c] = 0.f;
+        for (int c = t; c < 4 * NC; c += 128) s_warp[c] = 0.f;
         sync4();
       }
       // ---- the tile's result: this lane's dim of every row
       const bool whole = begins && ends;
       float* const rec = a.rec + (2 * g + (begins ? 1 : 0)) * (int64_t)(NR * 130);
-      for (int c = t; c < NR; c += 128) {
-        float sum = (s_warp[c] + s_warp[NR + c]) + (s_warp[2 * NR + c] + s_warp[3 * NR + c]);
-        if (s_depth[c] < 0) sum = 0.f;
-        const float rf = s_ref[c];
+      if (t < NC) {
+        float sum = (s_warp[t] + s_warp[NC + t]) + (s_warp[2 * NC + t] + s_warp[3 * NC + t]);
+        if ((rt * NR + c0 + t) / a.G >= sp.n) sum = 0.f;
+        const float rf = -s_nref[t];
         if (whole) {
-          s_fac[c] = sum == 0.f ? 0.f : 1.f / sum;
-          if (a.lse && s_node[c] >= 0)
-            a.lse[(int64_t)s * a.N * a.H + s_node[c]] =
+          s_fac[t] = sum == 0.f ? 0.f : 1.f / sum;
+          if (a.lse && s_node[t] >= 0)
+            a.lse[(int64_t)s * a.N * a.H + s_node[t]] =
                 sum == 0.f ? -INFINITY : (log2f(sum) + (rf == kUnset ? 0.f : rf)) * 0.6931471805599453f;
         } else {
-          s_fac[c] = sum == 0.f ? 0.f : 1.f;
-          rec[NR * 128 + c] = rf;
-          rec[NR * 129 + c] = sum;
+          s_fac[t] = sum == 0.f ? 0.f : 1.f;
+          rec[NR * 128 + c0 + t] = rf;
+          rec[NR * 129 + c0 + t] = sum;
         }
       }
       sync4();
@@ -832,27 +952,24 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
       // operand position -> dim: the codes of a word were paired i, i + 4
       const int dim = 32 * w + (lane & 24) + ((lane & 1) << 2) + ((lane & 7) >> 1);
       const uint32_t nb = 0x80u << (8 * w);
-      for (int c = 0; c < NR; c += 16) {
+#pragma unroll 1
+      for (int c = 0; c < NC; c += 16) {
         float o[16];
         if (sp.np > 0) {
-          ld16(tl + T_::kO + c, o);
+          ld16(tl + T_::kO + c0 + c, o);
           wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = 0.f;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float f = s_fac[c + i];
-          float v = f == 0.f ? 0.f : o[i] * f;
-          if (s_nan[c + i] & nb) v = NAN;
+          const float v = sp.np == 0 || f == 0.f ? 0.f : (s_nan[c + i] & nb) ? NAN : o[i] * f;
           if (whole) {
-            const int nd = s_node[c + i];
-            if (nd >= 0)
-              a.out[((int64_t)s * a.N * a.H + nd) * kHeadDim + dim] =
+            const int row = s_node[c + i];
+            if (row >= 0)
+              a.out[((int64_t)s * a.N * a.H + row) * kHeadDim + dim] =
                   __bfloat16_as_ushort(__float2bfloat16_rn(v));
           } else {
-            rec[(c + i) * 128 + dim] = v;
+            rec[(c0 + c + i) * 128 + dim] = v;
           }
         }
       }
@@ -861,33 +978,19 @@ __global__ void __launch_bounds__(kThreads, CTAS) kernel(const __grid_constant__
       if (sp.np > 0 && lane == 0) mbar_arrive(bar(kOFree));
       // a tile that began in a range before this one: if that range's end is the tile's
       // first cut, this CTA's place in the list says how many records join
-      if (t == 0 && !begins && e0 > 0) {
+      if (sg == 0 && t == 0 && !begins) {
         const int64_t start = u0 - e0, end = start + max(1, sp.np);
+        int parts = 0;
         if (range_begin(g - 1, U, Gd) <= start) {
-          int parts = 2;
+          parts = 2;
           while (g + parts - 1 < Gd && range_begin(g + parts - 1, U, Gd) < end) ++parts;
           a.meta[4 * g + 1] = s;
           a.meta[4 * g + 2] = h * a.tiles + rt;
-          a.meta[4 * g] = parts;
-        } else {
-          a.meta[4 * g] = 0;
         }
+        a.meta[4 * g] = parts;
       }
     });
-    // no cut tile at this range's start
-    if (t == 0) {
-      bool cut = false;
-      if (u0 < u1) {
-        int lo = 0, hi = a.B - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (s_pref[mid] * HT > u0) hi = mid; else lo = mid + 1;
-        }
-        const int64_t p0 = lo > 0 ? s_pref[lo - 1] : 0;
-        cut = (u0 - p0 * HT) % (s_pref[lo] - p0) != 0;
-      }
-      if (!cut) a.meta[4 * g] = 0;
-    }
+    if (sg == 0 && t == 0 && (u0 >= u1 || locate(u0).e == 0)) a.meta[4 * g] = 0;
   }
   fence_before();
   __syncthreads();
@@ -973,15 +1076,21 @@ static cudaError_t encode_pool(const uint8_t* pages, int64_t page_stride, int64_
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int NR, int VB, int STG, int CTAS>
+template <class C>
 cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
-  const int smem = Lay<NR, VB, STG>::kBytes;
-  auto kern = kernel<NR, VB, STG, CTAS>;
+  const int smem = Lay<C>::kBytes;
+  auto kern = kernel<C>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int grid = num_sms * CTAS;
-  a.tiles = (a.N * a.G + NR - 1) / NR;
-  a.meta = reinterpret_cast<int32_t*>(a.rec + (int64_t)grid * 2 * NR * 130);
+  // a block that was launched with fewer registers than its roles take would wait for them
+  static const int regs = [kern] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs * C::kThreads < C::kRegs) return cudaErrorInvalidConfiguration;
+  const int grid = num_sms * C::CTAS;
+  a.tiles = (a.N * a.G + C::NR - 1) / C::NR;
+  a.meta = reinterpret_cast<int32_t*>(a.rec + (int64_t)grid * 2 * C::NR * 130);
   const Args all = a;
   for (int64_t b0 = 0; b0 < B; b0 += kMaxSeq) {
     a = all;
@@ -993,9 +1102,9 @@ cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
     a.seq_lens += b0;
     if (a.n_nodes) a.n_nodes += b0;
     if (a.mask) a.mask += b0 * a.N;
-    e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, a);
+    e = launch_pdl(kern, dim3(grid), dim3(C::kThreads), smem, stream, a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(merge_kernel<NR>, dim3(grid, NR / 4), dim3(128), 0, stream, a);
+    e = launch_pdl(merge_kernel<C::NR>, dim3(grid, C::NR / 4), dim3(128), 0, stream, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -1003,11 +1112,15 @@ cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
 
 // Rows a tile: the smallest that holds all of a sequence's rows of one KV head, else the
 // largest.
+//               NR SG DW KS VS VB CTAs registers
+using C16 = Cfg<16, 1, 8, 2, 3, 1, 2, 40, 104, 56>;
+using C32 = Cfg<32, 2, 8, 4, 4, 2, 1, 48, 144, 72>;
+using C64 = Cfg<64, 2, 8, 3, 3, 2, 1, 48, 144, 72>;
 inline int rows_of(int N, int H, int Hkv) {
   const int rows = N * (H / Hkv);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
-inline int ctas_of(int nr) { return nr <= 32 ? 2 : 1; }
+inline int ctas_of(int nr) { return nr == 16 ? C16::CTAS : nr == 32 ? C32::CTAS : C64::CTAS; }
 
 }  // namespace tree
 
@@ -1052,9 +1165,9 @@ cudaError_t launch_tree_decode(const uint16_t* q, int64_t B, int N, int H, int H
   if (cudaError_t e = tree::encode_pool(k_pages, page_stride, head_stride, num_pages, Hkv, &a.tmap))
     return e;
   switch (tree::rows_of(N, H, Hkv)) {
-    case 16: return tree::launch<16, 1, 2, 2>(a, B, num_sms, stream);
-    case 32: return tree::launch<32, 1, 2, 2>(a, B, num_sms, stream);
-    default: return tree::launch<64, 2, 2, 1>(a, B, num_sms, stream);
+    case 16: return tree::launch<tree::C16>(a, B, num_sms, stream);
+    case 32: return tree::launch<tree::C32>(a, B, num_sms, stream);
+    default: return tree::launch<tree::C64>(a, B, num_sms, stream);
   }
 }
 
