@@ -876,7 +876,7 @@ extern "C" int tree_paged_decode(const uint16_t* q, int64_t B, int N, int H, int
                 kName);
   if (need > 0 && (!ws || !aligned(ws, 16)))
     return fail(MX4_ERR_INVALID, "%s: workspace NULL or not 16-byte aligned", kName);
-  if (bt_width < 1 || bt_width > (1 << 24)) return fail(MX4_ERR_INVALID, "%s: bt_width", kName);
+  if (bt_width < 1 || bt_width >= (1 << 23)) return fail(MX4_ERR_INVALID, "%s: bt_width", kName);
   DeviceInfo* d;
   if (int rc = device_info(&d)) return rc;
   return cuda_result(

@@ -52,7 +52,13 @@ constexpr float kLazy = 12.f;      // log2 units a logit may lie above its row's
 constexpr float kUnset = -3e38f;   // the reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKTile = 128 * 128;  // K operand tile
+// V operand: rows of 64 dims (128 bytes) a token, in 128-byte swizzle atoms of 8 tokens (the
+// 16-byte chunks of row r XOR-permuted by r % 8), 16 atoms, then the other 64 dims.
 constexpr int kVTile = 128 * 128 * 2;
+constexpr int kVHalf = kVTile / 2;
+// P operand: 16-byte chunks of 8 rows, the 128 tokens' chunks one after the other, the next
+// 8 rows kChunk bytes on (16 more than the chunks take, to change banks).
+constexpr int kChunk = 128 * 16 + 16;
 
 // A configuration: NR rows a tile, SG softmax groups (of NR / SG rows), DW dequantising
 // warps, KS and VS stages of K and V pages, VB operand buffers of V and P, CTAs an SM.
@@ -62,7 +68,7 @@ template <int NR_, int SG_, int DW_, int KS_, int VS_, int VB_, int CTAS_, int R
 struct Cfg {
   static constexpr int NR = NR_, SG = SG_, DW = DW_, KS = KS_, VS = VS_, VB = VB_, CTAS = CTAS_;
   static constexpr int RC = RC_, RS = RS_, RD = RD_;
-  static_assert(DW % 4 == 0 && NR % (16 * SG) == 0, "whole warpgroups, 16 rows at a time");
+  static_assert(VB <= 2 && NR <= 32 * SG && DW % 4 == 0 && NR % (16 * SG) == 0, "whole warpgroups, 16 rows at a time");
   static constexpr int kRegs = 128 * (RC + SG * RS + DW / 4 * RD);  // all that the roles take
   static constexpr int NC = NR / SG;
   static constexpr int kThreads = 32 * (4 + 4 * SG + DW);
@@ -83,7 +89,7 @@ struct Args {
   const int32_t* seq_lens;
   const int32_t* n_nodes;
   const uint64_t* mask;
-  int64_t window, sinks;
+  int window, sinks;  // (clamped below 2^30: no cached token lies further)
   float scale;
   uint16_t* out;
   float* lse;
@@ -98,11 +104,11 @@ template <class C>
 struct Lay {
   static constexpr int NR = C::NR;
   static constexpr int kK = 0;                               // [KS] K operand
-  static constexpr int kKsc = kK + C::KS * kKTile;           // [KS] K scale words
-  static constexpr int kVraw = kKsc + C::KS * 512;           // [VS] V pages as stored
-  static constexpr int kV = kVraw + C::VS * kPageBytes;      // [VB] V operand
-  static constexpr int kP = kV + C::VB * kVTile;             // [VB] P operand
-  static constexpr int kQ = kP + C::VB * NR * 256;           // q operand: hi, lo
+  static constexpr int kV = kK + C::KS * kKTile;             // [VB] V operand
+  static constexpr int kKsc = kV + C::VB * kVTile;           // [KS] scale words: K's, V's
+  static constexpr int kVraw = kKsc + C::KS * 1024;           // [VS] V pages as stored
+  static constexpr int kP = kVraw + C::VS * kPageBytes;      // [VB] P operand
+  static constexpr int kQ = (kP + C::VB * (NR / 8) * kChunk + 127) / 128 * 128;           // q operand: hi, lo
   static constexpr int kSf = kQ + 2 * NR * 128;              // q scale words: hi, lo
   static constexpr int kRef = kSf + 2 * NR * 4;              // [NR] minus the references
   static constexpr int kFac = kRef + NR * 4;                 // [NR] rescaling factors, then 1 / sum
@@ -115,11 +121,13 @@ struct Lay {
   static constexpr int kLen = kPref + kMaxSeq * 8;           // [kMaxSeq]
   static constexpr int kCnt = kLen + kMaxSeq * 4;            // [kMaxSeq] u8
   static constexpr int kInfo = kCnt + kMaxSeq;               // [VS] valid tokens of the page
-  static constexpr int kBar = (kInfo + C::VS * 4 + 7) / 8 * 8;
+  static constexpr int kKinfo = kInfo + C::VS * 4;           // [KS] the same
+  static constexpr int kBar = (kKinfo + C::KS * 4 + 7) / 8 * 8;
   static constexpr int kBars = 2 * C::KS + 2 * C::VS + 4 + 3 * C::VB + 5;
-  static constexpr int kMisc = kBar + kBars * 8;             // abort, tmem address, scan space
+  static constexpr int kStart = kBar + kBars * 8;            // where the range begins
+  static constexpr int kMisc = kStart + 24;                  // abort, tmem address, scan space
   static constexpr int kBytes = kMisc + 16 + 32 * 8 + 1024;  // + slack for the 1024-byte alignment
-  static_assert(kVraw % 16 == 0 && kV % 128 == 0 && kRef % 16 == 0 && kMask % 8 == 0, "alignment");
+  static_assert(kVraw % 16 == 0 && kV % 1024 == 0 && kP % 16 == 0 && kQ % 128 == 0 && kRef % 16 == 0 && kMask % 8 == 0, "alignment");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -172,6 +180,33 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 __device__ __forceinline__ void st1(uint32_t taddr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(v) : "memory");
 }
+// Wait for a phase: kSpins tries in a short loop (each sleeps in the hardware for a while).
+constexpr int kSpins = 4096, kWaits = 1024;
+__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "again:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra done;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra again;\n"
+      "done:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "n"(kSpins)
+      : "memory");
+  return ok != 0u;
+}
+// A ring position: slot and the parity of its use.
+template <int S>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == S) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 // This warpgroup's registers a thread from here on.
 template <int kFrom, int kTo>
 __device__ __forceinline__ void set_regs() {
@@ -247,18 +282,18 @@ __device__ __forceinline__ float columns16(const float* in, int lane, Op op) {
 // What a sequence's cached tokens give its tiles: pages 0 .. ns-1 hold the first
 // `sinks` tokens, pages first .. the window and the drafts.
 struct Span {
-  int64_t base;  // tokens before the drafts
+  int base;  // tokens before the drafts
   int len, n, ns, first, np;
 };
-__device__ __forceinline__ Span span_of(int64_t L, int n, int64_t window, int64_t sinks) {
+__device__ __forceinline__ Span span_of(int L, int n, int window, int sinks) {
   Span sp;
-  sp.len = (int)L;
+  sp.len = L;
   sp.n = n;
   sp.base = L - n;
-  const int64_t lo = window > 0 ? max((int64_t)0, sp.base + 1 - window) : 0;
-  sp.first = (int)(lo / kPageTokens);
-  sp.ns = (int)min((min(sinks, lo) + kPageTokens - 1) / kPageTokens, (int64_t)sp.first);
-  sp.np = n > 0 ? sp.ns + (int)((L + kPageTokens - 1) / kPageTokens) - sp.first : 0;
+  const int lo = window > 0 ? max(0, sp.base + 1 - window) : 0;
+  sp.first = lo >> 7;
+  sp.ns = min((min(sinks, lo) + kPageTokens - 1) >> 7, sp.first);
+  sp.np = n > 0 ? sp.ns + ((L + kPageTokens - 1) >> 7) - sp.first : 0;
   return sp;
 }
 
@@ -266,8 +301,15 @@ __host__ __device__ __forceinline__ int64_t range_begin(int64_t g, int64_t U, in
   return U * g / G;
 }
 
+// Where a CTA's range begins.
+struct Start {
+  int64_t pages;
+  int s, h, rt, e;
+};
+constexpr int kMinPages = 2;
+
 template <class C>
-__global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid_constant__ Args a) {
   using L_ = Lay<C>;
   using T_ = Tm<C>;
   constexpr int NR = C::NR, NC = C::NC, SG = C::SG, DW = C::DW, KS = C::KS, VS = C::VS, VB = C::VB;
@@ -280,6 +322,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
   int* const s_len = reinterpret_cast<int*>(sm + L_::kLen);
   uint8_t* const s_cnt = sm + L_::kCnt;
   volatile int* const s_info = reinterpret_cast<volatile int*>(sm + L_::kInfo);
+  volatile int* const s_kinfo = reinterpret_cast<volatile int*>(sm + L_::kKinfo);
   volatile int* const s_abort = reinterpret_cast<volatile int*>(sm + L_::kMisc);
   uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(sm + L_::kMisc + 4);
   int64_t* const s_scan = reinterpret_cast<int64_t*>(sm + L_::kMisc + 16);
@@ -292,11 +335,11 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < KS; ++i) {
       mbar_init(bar(kKFull + i), 1);
-      mbar_init(bar(kKEmpty + i), 1);
+      mbar_init(bar(kKEmpty + i), 1 + 4 * SG);
     }
     for (int i = 0; i < VS; ++i) {
       mbar_init(bar(kVFull + i), 1);
-      mbar_init(bar(kVEmpty + i), DW + 4 * SG);
+      mbar_init(bar(kVEmpty + i), DW);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kSFull + i), 1);
@@ -337,7 +380,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
       }
       s_len[tid] = (int)L;
       s_cnt[tid] = (uint8_t)n;
-      mine = max(1, span_of(L, n, a.window, a.sinks).np);
+      mine = max(1, span_of((int)L, n, a.window, a.sinks).np);
     }
     int64_t inc = mine;
 #pragma unroll
@@ -350,68 +393,96 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
     for (int w = 0; w < warp; ++w) inc += s_scan[w];
     if (tid < a.B) s_pref[tid] = inc;
   }
+  __syncthreads();
+  // ---- this CTA's range of pages, by one thread (all the divisions are here, once)
+  Start* const s_start = reinterpret_cast<Start*>(sm + L_::kStart);
+  if (tid == 0) {
+    const int HT = a.Hkv * a.tiles;
+    const int64_t U = s_pref[a.B - 1] * HT, g = blockIdx.x;
+    // few pages a CTA are not worth the records: at least kMinPages each
+    const int64_t Gd = max((int64_t)1, min((int64_t)gridDim.x, U / kMinPages));
+    Start x{};
+    int parts = 0;
+    if (g < Gd) {
+      const int64_t u0 = range_begin(g, U, Gd);
+      x.pages = range_begin(g + 1, U, Gd) - u0;
+      int lo = 0, hi = a.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s_pref[mid] * HT > u0) hi = mid; else lo = mid + 1;
+      }
+      const int64_t p0 = lo > 0 ? s_pref[lo - 1] : 0, np = s_pref[lo] - p0, r = u0 - p0 * HT;
+      const int ht = (int)(r / np);
+      x.s = lo;
+      x.h = ht / a.tiles;
+      x.rt = ht % a.tiles;
+      x.e = (int)(r - ht * np);
+      // a tile that began in the range before this one, and there alone: this CTA's place in
+      // the list says how many records join
+      const int64_t start = u0 - x.e, end = start + np;
+      if (x.e > 0 && range_begin(g - 1, U, Gd) <= start) {
+        parts = 2;
+        while (g + parts - 1 < Gd && range_begin(g + parts - 1, U, Gd) < end) ++parts;
+        a.meta[4 * g + 1] = x.s;
+        a.meta[4 * g + 2] = ht;
+      }
+    }
+    a.meta[4 * g] = parts;
+    *s_start = x;
+  }
   fence_before();
   __syncthreads();
   fence_after();
   pdl_launch_dependents();  // after this CTA has its tensor memory
 
   const uint32_t tm = *s_taddr;
-  const int HT = a.Hkv * a.tiles;
-  const int64_t U = s_pref[a.B - 1] * HT;
-  // few pages a CTA are not worth the records: at least kMinPages each
-  constexpr int kMinPages = 2;
-  const int64_t Gd = max((int64_t)1, min((int64_t)gridDim.x, U / kMinPages));
-  const int64_t g = blockIdx.x;
-  const int64_t u0 = g < Gd ? range_begin(g, U, Gd) : U, u1 = g < Gd ? range_begin(g + 1, U, Gd) : U;
 
   auto wait = [&](int i, uint32_t parity) -> bool {
     const uint32_t b = bar(i);
-    for (uint32_t p = 0; p < kWaitPolls; ++p) {
-      if (mbar_test(b, parity)) return true;
-      if ((p & 63u) == 63u && *s_abort) return false;
-    }
+    if (__builtin_expect(mbar_spin(b, parity), 1)) return true;
+    for (int j = 0; j < kWaits && !*s_abort; ++j)
+      if (mbar_spin(b, parity)) return true;
+    if (!*s_abort) flag(a.status, MX4_STATUS_TIMEOUT);
     *s_abort = 1;
-    flag(a.status, MX4_STATUS_TIMEOUT);
     return false;
   };
 
-  // Page u of the list: sequence, tile of the sequence (head major), page of the tile.
-  struct At {
-    int s, ht;
-    int64_t e;
+  // A place in the list of tiles, and the pages [e0, e1) of the tile in this CTA's range.
+  struct Cursor {
+    int64_t left;  // pages of the range from e0 on
+    int s, h, rt, e0, e1, np;  // np: the tile's places in the list (1 for a tile without pages)
+    Span sp;
   };
-  auto locate = [&](int64_t u) {
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s_pref[mid] * HT > u) hi = mid; else lo = mid + 1;
+  auto settle = [&](Cursor& c) {
+    if (c.left <= 0) return;
+    c.sp = span_of(s_len[c.s], s_cnt[c.s], a.window, a.sinks);
+    c.np = max(1, c.sp.np);
+    c.e1 = (int)min((int64_t)c.np, c.e0 + c.left);
+  };
+  auto begin = [&]() {
+    Cursor c{s_start->pages, s_start->s, s_start->h, s_start->rt, s_start->e, 0, 0, {}};
+    settle(c);
+    return c;
+  };
+  auto advance = [&](Cursor& c) {
+    c.left -= c.e1 - c.e0;
+    c.e0 = 0;
+    if (++c.rt == a.tiles) {
+      c.rt = 0;
+      if (++c.h == a.Hkv) {
+        c.h = 0;
+        ++c.s;
+      }
     }
-    const int64_t p0 = lo > 0 ? s_pref[lo - 1] : 0, np = s_pref[lo] - p0, r = u - p0 * HT;
-    At x;
-    x.s = lo;
-    x.ht = (int)(r / np);
-    x.e = r - x.ht * np;
-    return x;
+    settle(c);
   };
   // The tiles of this CTA's range, in order: f(tile number among those with pages, sequence,
   // head, row tile, its span, its pages [e0, e1) of this range).
   auto for_tiles = [&](auto&& f) {
-    if (u0 >= u1) return;
-    int64_t u = u0;
-    At x = locate(u0);
     int count = 0;
-    while (u < u1) {
-      const int64_t np = s_pref[x.s] - (x.s > 0 ? s_pref[x.s - 1] : 0);
-      const int64_t e1 = min(np, x.e + (u1 - u));
-      const Span sp = span_of(s_len[x.s], s_cnt[x.s], a.window, a.sinks);
-      f(count, x.s, x.ht / a.tiles, x.ht % a.tiles, sp, (int)x.e, (int)e1);
-      count += sp.np > 0;
-      u += e1 - x.e;
-      x.e = 0;
-      if (++x.ht == HT) {
-        x.ht = 0;
-        ++x.s;
-      }
+    for (Cursor c = begin(); c.left > 0; advance(c)) {
+      f(count, c.s, c.h, c.rt, c.sp, c.e0, c.e1);
+      count += c.sp.np > 0;
     }
   };
   auto page_no = [](const Span& sp, int e) { return e < sp.ns ? e : sp.first + (e - sp.ns); };
@@ -421,75 +492,70 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
   if (warp < 4) {
   set_regs<kLaunchRegs, C::RC>();  // (by the warpgroup as one)
   if (warp == 0 || warp == 3) {
-    // ================= producers: K (warp 0) and V (warp 3).  The lanes look up the next 32
-    // pages' table entries at once, a batch ahead.
+    // ================= producers: K (warp 0) and V (warp 3).  The lanes look up 32 pages of a
+    // tile at once, the next ones before the present ones' copies.
     const bool isv = warp == 3;
-    struct Look {
-      int pid, h, live;  // live < 0: a tile without pages
-    };
-    auto look = [&](int64_t u) {
-      Look x{-1, 0, -1};
-      if (u < u1) {
-        const At y = locate(u);
-        const Span sp = span_of(s_len[y.s], s_cnt[y.s], a.window, a.sinks);
-        if (sp.np > 0) {
-          const int pg = page_no(sp, (int)y.e);
-          x.pid = a.table[(int64_t)y.s * a.bt_width + pg];
-          x.h = y.ht / a.tiles;
-          x.live = min(kPageTokens, sp.len - pg * kPageTokens);
-        }
-      }
-      return x;
-    };
     int k = 0;
-    Look nxt = look(u0 + lane);
-    for (int64_t ub = u0; ub < u1; ub += 32) {
-      const Look cur = nxt;
-      nxt = look(ub + 32 + lane);
-      const int cnt = (int)min((int64_t)32, u1 - ub);
+    Ring<KS> kr;
+    Ring<VS> vr;
+    Cursor c = begin();
+    auto look = [&](const Cursor& x) {
+      const int e = x.e0 + lane;
+      return x.left > 0 && x.sp.np > 0 && e < x.e1
+                 ? a.table[(int64_t)x.s * a.bt_width + page_no(x.sp, e)]
+                 : -1;
+    };
+    int pid_n = look(c);
+    while (c.left > 0) {
+      const Cursor cur = c;
+      const int pid_c = pid_n;
+      const int cnt = min(32, cur.e1 - cur.e0);
+      if (cnt < cur.e1 - cur.e0) {
+        c.e0 += 32;
+        c.left -= 32;
+      } else {
+        advance(c);
+      }
+      pid_n = look(c);
+      if (cur.sp.np == 0) continue;
+#pragma unroll 1
       for (int i = 0; i < cnt; ++i) {
-        const int pid = __shfl_sync(0xFFFFFFFFu, cur.pid, i);
-        const int h = __shfl_sync(0xFFFFFFFFu, cur.h, i);
-        const int live = __shfl_sync(0xFFFFFFFFu, cur.live, i);
-        if (live < 0) continue;
+        const int pid = __shfl_sync(0xFFFFFFFFu, pid_c, i);
         if (lane == 0) {
           const bool ok = pid >= 0 && pid < a.num_pages;
-          const int64_t off = (int64_t)pid * a.page_stride + (int64_t)h * a.head_stride;
-          if (!isv) {
-            const int st = k % KS, round = k / KS;
-            bool go = !*s_abort;
-            if (round > 0) go = wait(kKEmpty + st, (round - 1) & 1) && go;
-            if (go && ok) {
-              const uint32_t kd = sb + L_::kK + st * kKTile, fb = bar(kKFull + st);
-              mbar_arrive_expect_tx(fb, kRowDataBytes * kPageTokens + 512);
+          const int live = min(kPageTokens, cur.sp.len - page_no(cur.sp, cur.e0 + i) * kPageTokens);
+          const int64_t off = (int64_t)pid * a.page_stride + (int64_t)cur.h * a.head_stride;
+          const int st = isv ? vr.slot : kr.slot;
+          const uint32_t fb = bar((isv ? kVFull : kKFull) + st);
+          bool go = !*s_abort;
+          if (k >= (isv ? VS : KS))
+            go = wait((isv ? kVEmpty : kKEmpty) + st, (isv ? vr.phase : kr.phase) ^ 1u) && go;
+          if (go) {
+            if (isv) s_info[st] = ok ? live : 0; else s_kinfo[st] = ok ? live : 0;
+            if (!ok) {
+              flag(a.status, MX4_STATUS_BAD_PAGE);
+              mbar_arrive(fb);
+            } else if (isv) {
+              mbar_arrive_expect_tx(fb, kPageBytes);
+              bulk_copy_g2s(sb + L_::kVraw + st * kPageBytes, a.v_pages + off, kPageBytes, fb);
+            } else {
+              mbar_arrive_expect_tx(fb, kRowDataBytes * kPageTokens + 1024);
               asm volatile(
                   "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                  "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(kd),
-                  "l"(reinterpret_cast<uint64_t>(&a.tmap)), "r"(0), "r"(0), "r"(0), "r"(h),
+                  "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(sb + L_::kK + st * kKTile),
+                  "l"(reinterpret_cast<uint64_t>(&a.tmap)), "r"(0), "r"(0), "r"(0), "r"(cur.h),
                   "r"(pid), "r"(fb)
                   : "memory");
-              bulk_copy_g2s(sb + L_::kKsc + st * 512, a.k_pages + off + kScaleOffset, 512, fb);
-            } else if (go) {
-              mbar_arrive(bar(kKFull + st));
-            }
-          } else {
-            const int st = k % VS, round = k / VS;
-            if (!ok) flag(a.status, MX4_STATUS_BAD_PAGE);
-            bool go = !*s_abort;
-            if (round > 0) go = wait(kVEmpty + st, (round - 1) & 1) && go;
-            if (go) s_info[st] = ok ? live : 0;
-            if (go && ok) {
-              mbar_arrive_expect_tx(bar(kVFull + st), kPageBytes);
-              bulk_copy_g2s(sb + L_::kVraw + st * kPageBytes, a.v_pages + off, kPageBytes,
-                            bar(kVFull + st));
-            } else if (go) {
-              mbar_arrive(bar(kVFull + st));
+              bulk_copy_g2s(sb + L_::kKsc + st * 1024, a.k_pages + off + kScaleOffset, 512, fb);
+              bulk_copy_g2s(sb + L_::kKsc + st * 1024 + 512, a.v_pages + off + kScaleOffset, 512, fb);
             }
           }
         }
+        __syncwarp();
         ++k;
+        kr.next();
+        vr.next();
       }
-      __syncwarp();
     }
     // every copy has landed before the CTA ends
     if (lane == 0) {
@@ -500,35 +566,36 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
     // ================= S^T = K q^T: one lane
     if (lane == 0) {
       int k = 0;
+      Ring<KS> kr;
+      Ring<2> sr;
+      const uint64_t ad0 = desc(sb + L_::kK, 16, 1024) | ((uint64_t)2 << 61);
+      const uint64_t sd0 = desc(sb + L_::kKsc, 16, 128), bd0 = desc(sb + L_::kQ, 128, 1024);
       for_tiles([&](int tile, int, int, int, const Span& sp, int e0, int e1) {
         if (sp.np == 0) return;
-        for (int e = e0; e < e1; ++e, ++k) {
-          const int st = k % KS, b = k & 1;
-          bool go = true;
-          if (e == e0) go = wait(kQFull, tile & 1);
-          go = wait(kKFull + st, (k / KS) & 1) && go;
-          if (k >= 2) go = wait(kSFree + b, ((k >> 1) - 1) & 1) && go;
-          if (!go || *s_abort) continue;
+        wait(kQFull, tile & 1);
+        for (int e = e0; e < e1; ++e, ++k, kr.next(), sr.next()) {
+          const int st = kr.slot, b = sr.slot;
+          wait(kKFull + st, kr.phase);
+          if (k >= 2) wait(kSFree + b, sr.phase ^ 1u);
+          if (*s_abort) continue;
           fence_after();
-          const uint32_t ka = sb + L_::kK + st * kKTile, qa = sb + L_::kQ;
           const uint32_t sfa = tm + T_::kSfa + 4u * b;
+          const uint64_t ad = ad0 + st * (kKTile >> 4);
           asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(sfa),
-                       "l"(desc(sb + L_::kKsc + st * 512, 16, 128))
+                       "l"(sd0 + st * (1024 >> 4))
                        : "memory");
 #pragma unroll
           for (uint32_t part = 0; part < (C::kTwin ? 1 : 2); ++part)
 #pragma unroll
-            for (uint32_t kb = 0; kb < 4; ++kb) {
-              const uint64_t ad = desc(ka + kb * 32, 16, 1024) | ((uint64_t)2 << 61);
-              const uint64_t bd = desc(qa + part * NR * 128 + kb * 256, 128, 1024);
+            for (uint32_t kb = 0; kb < 4; ++kb)
               asm volatile(
                   "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
                   " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, "
                   "%2, %3, [%4], [%5], p;\n}\n" ::"r"(tm + T_::kS + b * C::kScols),
-                  "l"(ad), "l"(bd), "r"(idesc_s<T_::kSfbRows>(kb)), "r"(sfa),
-                  "r"(tm + T_::kSfb + part * 4), "r"(part + kb)
+                  "l"(ad + kb * (32 >> 4)), "l"(bd0 + ((part * NR * 128 + kb * 256) >> 4)),
+                  "r"(idesc_s<T_::kSfbRows>(kb)), "r"(sfa), "r"(tm + T_::kSfb + part * 4),
+                  "r"(part + kb)
                   : "memory");
-            }
           commit(bar(kSFull + b));
           commit(bar(kKEmpty + st));
           if (e == e1 - 1) commit(bar(kQEmpty));
@@ -544,26 +611,27 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
     // ================= O^T += V^T P^T: one lane
     if (lane == 0) {
       int k = 0;
+      Ring<VB> br;
+      const uint64_t ad0 = desc(sb + L_::kV, kVHalf, 1024) | ((uint64_t)2 << 61);
+      const uint64_t bd0 = desc(sb + L_::kP, 128, kChunk);
       for_tiles([&](int tile, int, int, int, const Span& sp, int e0, int e1) {
         if (sp.np == 0) return;
-        for (int e = e0; e < e1; ++e, ++k) {
-          const int b = k % VB;
-          bool go = true;
-          if (e == e0 && tile > 0) go = wait(kOFree, (tile - 1) & 1);
-          go = wait(kVReady + b, (k / VB) & 1) && go;
-          go = wait(kPFull + b, (k / VB) & 1) && go;
-          if (!go || *s_abort) continue;
+        if (tile > 0) wait(kOFree, (tile - 1) & 1);
+        for (int e = e0; e < e1; ++e, ++k, br.next()) {
+          const int b = br.slot;
+          wait(kVReady + b, br.phase);
+          wait(kPFull + b, br.phase);
+          if (*s_abort) continue;
           fence_after();
-          const uint32_t va = sb + L_::kV + b * kVTile, pa = sb + L_::kP + b * NR * 256;
+          const uint64_t ad = ad0 + b * (kVTile >> 4), bd = bd0 + b * ((NR / 8) * kChunk >> 4);
 #pragma unroll
-          for (uint32_t ks = 0; ks < 8; ++ks) {
-            const uint64_t ad = desc(va + ks * 256, 128, 2048), bd = desc(pa + ks * 256, 128, 2048);
+          for (uint32_t ks = 0; ks < 8; ++ks)
             asm volatile(
                 "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tm + T_::kO),
-                "l"(ad), "l"(bd), "r"(idesc_o<NR>()), "r"((uint32_t)(ks > 0 || e > e0))
+                "l"(ad + ks * (2048 >> 4)), "l"(bd + ks * (256 >> 4)), "r"(idesc_o<NR>()),
+                "r"((uint32_t)(ks > 0 || e > e0))
                 : "memory");
-          }
           commit(bar(kPvDone + b));
         }
       });
@@ -580,6 +648,8 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
     const int t = tid - 32 * (4 + 4 * SG), w = t >> 5;
     const int r8 = lane & 7, blk = ((r8 >> 1) + (lane >> 3)) & 3;  // see below
     int k = 0;
+    Ring<VS> vr;
+    Ring<VB> br;
     for_tiles([&](int tile, int s, int h, int rt, const Span& sp, int e0, int e1) {
       if (sp.np == 0) return;
       // 16 elements a thread: K-chunk j of row n; the two threads of a 32-block share its
@@ -661,34 +731,29 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kQFull));
 
-      for (int e = e0; e < e1; ++e, ++k) {
-        const int st = k % VS, b = k % VB;
-        wait(kVFull + st, (k / VS) & 1);
+      for (int e = e0; e < e1; ++e, ++k, vr.next(), br.next()) {
+        const int st = vr.slot, b = br.slot;
+        wait(kVFull + st, vr.phase);
         const int live = s_info[st];
-        const uint8_t* raw = sm + L_::kVraw + st * kPageBytes;
-        uint8_t* const vb = sm + L_::kV + b * kVTile;
         // Operand row (K index) m holds token 4 (m % 32) + m / 32, the order in which the
-        // tensor copy lays out K.  A warp's step: the 8 operand rows of one core matrix
-        // (r8), lane >> 3 choosing which 32-dim block of each: 16 raw bytes a lane, four
-        // 16-byte stores without bank conflicts.
+        // tensor copy lays out K.  A warp's step: 8 operand rows (r8), lane >> 3 choosing
+        // which 32-dim block of each: 16 raw bytes a lane, four 16-byte stores without bank
+        // conflicts.  A short loop: the roles' code together must stay near the warps.
+        const uint8_t* raw = sm + L_::kVraw + st * kPageBytes;
+        if (k >= VB) wait(kPvDone + b, br.phase ^ 1u);
         constexpr int kIts = 16 / DW;
-        uint4 c4[kIts];
-        uint32_t sc[kIts];
-        bool use[kIts];
-#pragma unroll
+#pragma unroll 1
         for (int it = 0; it < kIts; ++it) {
           const int m = (w * kIts + it) * 8 + r8, tok = 4 * (m & 31) + (m >> 5);
-          c4[it] = *reinterpret_cast<const uint4*>(raw + tok * kRowDataBytes + blk * 16);
-          sc[it] = raw[kScaleOffset + tok * kRowScaleBytes + blk];
-          use[it] = tok < live && sc[it] != 255u;
-        }
-        if (k >= VB) wait(kPvDone + b, (k / VB - 1) & 1);
-#pragma unroll
-        for (int it = 0; it < kIts; ++it) {
-          const int m = (w * kIts + it) * 8 + r8;
+          const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tok * kRowDataBytes + blk * 16);
+          const uint32_t sc = raw[kScaleOffset + tok * kRowScaleBytes + blk];
           // 2^(sc - 1), as two factors where it passes bf16's range
-          const uint32_t f1 = ((use[it] ? min(sc[it] + 126u, 254u) : 0u) << 7) * 0x10001u;
-          const uint32_t cw[4] = {c4[it].x, c4[it].y, c4[it].z, c4[it].w};
+          const uint32_t f1 =
+              ((tok < live && sc != 255u ? min(sc + 126u, 254u) : 0u) << 7) * 0x10001u;
+          const bool big = __any_sync(0xFFFFFFFFu, sc > 128u);
+          const uint32_t f2 = ((sc > 128u ? sc - 1u : 127u) << 7) * 0x10001u;
+          uint8_t* const dst = sm + L_::kV + b * kVTile + (blk >> 1) * kVHalf + (m >> 3) * 1024 + r8 * 128;
+          const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t x = cw[j];
@@ -700,12 +765,11 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
             y[3] = (x & 0x80008000u) | ((x >> 6) & 0x01C001C0u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = bf16_mul2(y[i], f1);
-            if (sc[it] > 128u) {
-              const uint32_t f2 = ((sc[it] - 1u) << 7) * 0x10001u;
+            if (big) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) y[i] = bf16_mul2(y[i], f2);
             }
-            *reinterpret_cast<uint4*>(vb + (blk * 4 + j) * 2048 + (m >> 3) * 128 + r8 * 16) =
+            *reinterpret_cast<uint4*>(dst + ((((blk & 1) * 4 + j) ^ r8) << 4)) =
                 make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
@@ -743,6 +807,9 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
     const float cs = a.scale * kLog2e;
     const int tok = 4 * lane + w;  // this lane's token of a page
     int k = 0;
+    Ring<KS> kr;
+    Ring<2> sr;
+    Ring<VB> br;
     for_tiles([&](int tile, int s, int h, int rt, const Span& sp, int e0, int e1) {
       const bool begins = e0 == 0, ends = e1 >= sp.np;
       // ---- the tile's rows
@@ -761,7 +828,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
           mk = mask_of(node);
           if (a.window > 0) {
             const int d = depth_of(node);
-            lo = (int)max((int64_t)0, sp.base + d + 1 - a.window);
+            lo = max(0, sp.base + d + 1 - a.window);
             for (int i = 0; i < sp.n; ++i)
               if ((mk >> i) & 1ull) {
                 const int di = depth_of(i);
@@ -781,15 +848,16 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
       for (int c = 0; c < NC; ++c) l[c] = 0.f;
 
       if (sp.np > 0) {
-        for (int e = e0; e < e1; ++e, ++k) {
-          const int st = k % VS, b = k & 1, pb = k % VB;
-          const int first = page_no(sp, e) * kPageTokens, i_g = first + tok;
-          wait(kVFull + st, (k / VS) & 1);
-          const int live = s_info[st];
-          uint32_t vw = *reinterpret_cast<const uint32_t*>(sm + L_::kVraw + st * kPageBytes +
-                                                           kScaleOffset + tok * kRowScaleBytes);
+        for (int e = e0; e < e1; ++e, ++k, kr.next(), sr.next(), br.next()) {
+          const int st = kr.slot, b = sr.slot, pb = br.slot;
+          const int first = page_no(sp, e) * kPageTokens;
+          wait(kKFull + st, kr.phase);
+          const int live = s_kinfo[st];
+          uint32_t vw = *reinterpret_cast<const uint32_t*>(sm + L_::kKsc + st * 1024 + 512 + tok * 4);
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kVEmpty + st));
+          if (lane == 0) mbar_arrive(bar(kKEmpty + st));
+          wait(kSFull + b, sr.phase);
+          fence_after();
           // dim blocks of this token's V row that are NaN
           vw = ((vw & 0x7F7F7F7Fu) + 0x01010101u) & vw & 0x80808080u;
           const bool plain = live == kPageTokens && first + kPageTokens <= sp.base &&
@@ -797,13 +865,19 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
                               first + kPageTokens <= a.sinks);
           // a row sees a draft by its mask, an earlier token from the window's first on;
           // rows without a node see what they like, their results are zeroed
-          const int nd = i_g - (int)sp.base;
-          auto sees = [&](int c) {
-            return nd >= 0 ? ((s_mask[2 * c + ((nd >> 5) & 1)] >> (nd & 31)) & 1u) != 0u
-                           : i_g >= s_lo[c] || i_g < a.sinks;
-          };
-          wait(kSFull + b, (k >> 1) & 1);
-          fence_after();
+          uint32_t vis = ~0u;
+          if (!plain) {
+            vis = 0u;
+            const int i_g = first + tok, nd = i_g - sp.base;
+            if (tok < live) {
+#pragma unroll 1
+              for (int c = 0; c < NC; ++c) {
+                const bool see = nd >= 0 ? ((s_mask[2 * c + ((nd >> 5) & 1)] >> (nd & 31)) & 1u) != 0u
+                                         : i_g >= s_lo[c] || i_g < a.sinks;
+                vis |= (uint32_t)see << c;
+              }
+            }
+          }
           float x[NC];
           const uint32_t ts = tl + T_::kS + b * C::kScols + c0;
           // S of 16 rows, hi and lo parts added where they are apart
@@ -822,14 +896,9 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
           // -inf where not seen, whatever was computed there
           auto hide16 = [&](int c, float* v) {
             if (plain) return;
-            if (tok >= live) {
+            const uint32_t vb = vis >> c;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = -INFINITY;
-            } else if (nd >= 0 || a.window > 0) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (!sees(c + i)) v[i] = -INFINITY;
-            }
+            for (int i = 0; i < 16; ++i) v[i] = (vb >> i) & 1u ? v[i] : -INFINITY;
           };
           for (bool again = false;; again = true) {
             float top = -INFINITY;
@@ -867,7 +936,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
               const float mx = columns16(v, lane, [](float p, float q) { return fmaxf(p, q); });
               if (lane < 16) s_warp[w * NC + c + lane] = mx;
             }
-            if (e > e0) wait(kPvDone + (k - 1) % VB, ((k - 1) / VB) & 1);
+            if (e > e0) wait(kPvDone + (VB == 1 ? 0 : pb ^ 1), VB == 1 || pb == 0 ? br.phase ^ 1u : br.phase);
             sync4();
             if (t < NC) {
               const float v = fmaxf(fmaxf(s_warp[t], s_warp[NC + t]),
@@ -898,20 +967,21 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kSFree + b));
           if (vw != 0u) {
+#pragma unroll 1
             for (int c = 0; c < NC; ++c)
-              if (tok < live && (plain || (nd < 0 && a.window == 0) || sees(c))) atomicOr(s_nan + c, vw);
+              if ((vis >> c) & 1u) atomicOr(s_nan + c, vw);
           }
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             x[c] = ex2(x[c]);
             l[c] += x[c];
           }
-          if (k >= VB) wait(kPvDone + pb, (k / VB - 1) & 1);
-          uint8_t* const pd = sm + L_::kP + pb * NR * 256 + (c0 >> 3) * 2048 +
+          if (k >= VB) wait(kPvDone + pb, br.phase ^ 1u);
+          uint8_t* const pd = sm + L_::kP + (pb * (NR / 8) + (c0 >> 3)) * kChunk +
                               (4 * w + (lane >> 3)) * 128 + (lane & 7) * 16;
 #pragma unroll
           for (int c = 0; c < NC; c += 8)
-            *reinterpret_cast<uint4*>(pd + (c >> 3) * 2048) =
+            *reinterpret_cast<uint4*>(pd + (c >> 3) * kChunk) =
                 make_uint4(pack_bf16(x[c], x[c + 1]), pack_bf16(x[c + 2], x[c + 3]),
                            pack_bf16(x[c + 4], x[c + 5]), pack_bf16(x[c + 6], x[c + 7]));
           fence_async();
@@ -923,7 +993,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
           const float v = columns16(l + c, lane, [](float p, float q) { return p + q; });
           if (lane < 16) s_warp[w * NC + c + lane] = v;
         }
-        wait(kPvDone + (k - 1) % VB, ((k - 1) / VB) & 1);
+        wait(kPvDone + (VB == 1 ? 0 : br.slot ^ 1), VB == 1 || br.slot == 0 ? br.phase ^ 1u : br.phase);
         sync4();
       } else {
         for (int c = t; c < 4 * NC; c += 128) s_warp[c] = 0.f;
@@ -931,7 +1001,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
       }
       // ---- the tile's result: this lane's dim of every row
       const bool whole = begins && ends;
-      float* const rec = a.rec + (2 * g + (begins ? 1 : 0)) * (int64_t)(NR * 130);
+      float* const rec = a.rec + (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * (int64_t)(NR * 130);
       if (t < NC) {
         float sum = (s_warp[t] + s_warp[NC + t]) + (s_warp[2 * NC + t] + s_warp[3 * NC + t]);
         if ((rt * NR + c0 + t) / a.G >= sp.n) sum = 0.f;
@@ -976,21 +1046,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
       fence_before();
       __syncwarp();
       if (sp.np > 0 && lane == 0) mbar_arrive(bar(kOFree));
-      // a tile that began in a range before this one: if that range's end is the tile's
-      // first cut, this CTA's place in the list says how many records join
-      if (sg == 0 && t == 0 && !begins) {
-        const int64_t start = u0 - e0, end = start + max(1, sp.np);
-        int parts = 0;
-        if (range_begin(g - 1, U, Gd) <= start) {
-          parts = 2;
-          while (g + parts - 1 < Gd && range_begin(g + parts - 1, U, Gd) < end) ++parts;
-          a.meta[4 * g + 1] = s;
-          a.meta[4 * g + 2] = h * a.tiles + rt;
-        }
-        a.meta[4 * g] = parts;
-      }
     });
-    if (sg == 0 && t == 0 && (u0 >= u1 || locate(u0).e == 0)) a.meta[4 * g] = 0;
   }
   fence_before();
   __syncthreads();
@@ -1003,7 +1059,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) kernel(const __grid_cons
 // Joins the records of a cut tile: block x = the range after its first cut, a warp a row,
 // a lane four dims: out = sum_r O_r 2^(m_r - M) / sum_r l_r 2^(m_r - M).
 template <int NR>
-__global__ void __launch_bounds__(128) merge_kernel(const Args a) {
+__global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
   pdl_launch_dependents();
   pdl_wait();
   const int64_t g = blockIdx.x;
@@ -1079,7 +1135,7 @@ static cudaError_t encode_pool(const uint8_t* pages, int64_t page_stride, int64_
 template <class C>
 cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
   const int smem = Lay<C>::kBytes;
-  auto kern = kernel<C>;
+  auto kern = tree_kernel<C>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // a block that was launched with fewer registers than its roles take would wait for them
@@ -1104,7 +1160,7 @@ cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
     if (a.mask) a.mask += b0 * a.N;
     e = launch_pdl(kern, dim3(grid), dim3(C::kThreads), smem, stream, a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(merge_kernel<C::NR>, dim3(grid, C::NR / 4), dim3(128), 0, stream, a);
+    e = launch_pdl(tree_merge_kernel<C::NR>, dim3(grid, C::NR / 4), dim3(128), 0, stream, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -1148,8 +1204,8 @@ cudaError_t launch_tree_decode(const uint16_t* q, int64_t B, int N, int H, int H
   a.seq_lens = seq_lens;
   a.n_nodes = n_nodes;
   a.mask = mask;
-  a.window = window;
-  a.sinks = sinks;
+  a.window = (int)std::min<int64_t>(window, 1 << 30);
+  a.sinks = (int)std::min<int64_t>(sinks, 1 << 30);
   a.scale = scale;
   a.out = out;
   a.lse = lse;
