@@ -30,12 +30,15 @@
 // CTA.  A tile cut by a range's end leaves a partial record (O, reference, sum) in the
 // workspace, and a second kernel joins the records of each cut tile.
 //
-// Roles.  Warps 0 and 3 stream the pages' K (tensor copies into the operand's swizzled
-// layout) and V (bulk copies), warps 1 and 2 issue the two products, then come the softmax
-// warps (groups of four, one lane a token, each group its own rows; in the epilogue one lane
-// a dim) and the warps that convert q and dequantise V.  All waits are bounded; after one
-// that runs out every role goes through its loop without waiting or issuing, and the status
-// word says so.
+// One CTA of 8 warps goes through its pages in order, every warp doing the same: softmax of
+// page k (two groups of four warps, each half of the rows; one lane a token), a sixteenth of
+// V's dequantisation, one barrier.  Copies and MMAs are asynchronous, each issued by one
+// thread: K and V of the pages to come, S of page k + 1 as soon as S of page k is in registers,
+// P V of page k after the barrier; two CTAs an SM fill each other's waits.  (Warps of fixed
+// roles handing pages to each other by barriers, 12 to 20 a CTA, took 217 to 304 us and 1120 us
+// on the first and last cases named below: each hand-over cost a few hundred cycles.)
+// All waits are bounded; after one that runs out the CTA goes through its loop without waiting
+// or issuing, and the status word says so.
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
 #include <cuda_bf16.h>
 
@@ -51,31 +54,26 @@ constexpr int kMaxSeq = 256;       // sequences per launch
 constexpr float kLazy = 12.f;      // log2 units a logit may lie above its row's reference
 constexpr float kUnset = -3e38f;   // the reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 256;
 constexpr int kKTile = 128 * 128;  // K operand tile
 // V operand: rows of 64 dims (128 bytes) a token, in 128-byte swizzle atoms of 8 tokens (the
 // 16-byte chunks of row r XOR-permuted by r % 8), 16 atoms, then the other 64 dims.
 constexpr int kVTile = 128 * 128 * 2;
 constexpr int kVHalf = kVTile / 2;
 // P operand: 16-byte chunks of 8 rows, the 128 tokens' chunks one after the other, the next
-// 8 rows kChunk bytes on (16 more than the chunks take, to change banks).
-constexpr int kChunk = 128 * 16 + 16;
+// 8 rows kChunk bytes on.
+constexpr int kChunk = 128 * 16;
 
-// A configuration: NR rows a tile, SG softmax groups (of NR / SG rows), DW dequantising
-// warps, KS and VS stages of K and V pages, VB operand buffers of V and P, CTAs an SM.
-// Registers are dealt out by role (RC: control warps, RS: softmax, RD: dequantisation), in
-// place of the same number for all.
-template <int NR_, int SG_, int DW_, int KS_, int VS_, int VB_, int CTAS_, int RC_, int RS_, int RD_>
+// A configuration: NR rows a tile, KS and VS stages of K and V pages, CTAs an SM.
+template <int NR_, int KS_, int VS_, int CTAS_>
 struct Cfg {
-  static constexpr int NR = NR_, SG = SG_, DW = DW_, KS = KS_, VS = VS_, VB = VB_, CTAS = CTAS_;
-  static constexpr int RC = RC_, RS = RS_, RD = RD_;
-  static_assert(VB <= 2 && NR <= 32 * SG && DW % 4 == 0 && NR % (16 * SG) == 0, "whole warpgroups, 16 rows at a time");
-  static constexpr int kRegs = 128 * (RC + SG * RS + DW / 4 * RD);  // all that the roles take
-  static constexpr int NC = NR / SG;
-  static constexpr int kThreads = 32 * (4 + 4 * SG + DW);
+  static constexpr int NR = NR_, KS = KS_, VS = VS_, CTAS = CTAS_;
+  static constexpr int NC = NR / 2;  // rows of a softmax group
   // hi and lo of q as one operand of 2 NR rows (K read once, their products added by the
   // softmax) while that is cheap there
   static constexpr bool kTwin = NR <= 32;
   static constexpr int kScols = kTwin ? 2 * NR : NR;
+  static_assert(NC == 8 || NC == 16 || NC == 32, "rows");
 };
 
 struct Args {
@@ -104,12 +102,12 @@ template <class C>
 struct Lay {
   static constexpr int NR = C::NR;
   static constexpr int kK = 0;                               // [KS] K operand
-  static constexpr int kV = kK + C::KS * kKTile;             // [VB] V operand
-  static constexpr int kKsc = kV + C::VB * kVTile;           // [KS] scale words: K's, V's
-  static constexpr int kVraw = kKsc + C::KS * 1024;           // [VS] V pages as stored
-  static constexpr int kP = kVraw + C::VS * kPageBytes;      // [VB] P operand
-  static constexpr int kQ = (kP + C::VB * (NR / 8) * kChunk + 127) / 128 * 128;           // q operand: hi, lo
-  static constexpr int kSf = kQ + 2 * NR * 128;              // q scale words: hi, lo
+  static constexpr int kV = kK + C::KS * kKTile;             // V operand
+  static constexpr int kP = kV + kVTile;                     // P operand
+  static constexpr int kQ = kP + NR / 8 * kChunk;            // q operand: hi, lo
+  static constexpr int kKsc = kQ + 2 * NR * 128;             // [KS] K scale words
+  static constexpr int kVraw = kKsc + C::KS * 512;           // [VS] V pages as stored
+  static constexpr int kSf = kVraw + C::VS * kPageBytes;     // q scale words: hi, lo
   static constexpr int kRef = kSf + 2 * NR * 4;              // [NR] minus the references
   static constexpr int kFac = kRef + NR * 4;                 // [NR] rescaling factors, then 1 / sum
   static constexpr int kWarp = kFac + NR * 4;                // [4][NR] per-warp maxima and sums
@@ -117,26 +115,27 @@ struct Lay {
   static constexpr int kNode = kNan + NR * 4;                // [NR] output row, -1 none
   static constexpr int kLo = kNode + NR * 4;                 // [NR] first token of the window
   static constexpr int kMask = kLo + NR * 4;                 // [NR] u64: nodes that the row sees
-  static constexpr int kPref = kMask + NR * 8;               // [kMaxSeq] i64 page prefix
-  static constexpr int kLen = kPref + kMaxSeq * 8;           // [kMaxSeq]
+  static constexpr int kPref = kMask + NR * 8;               // [kMaxSeq] u32 page prefix
+  static constexpr int kLen = kPref + kMaxSeq * 4;           // [kMaxSeq]
   static constexpr int kCnt = kLen + kMaxSeq * 4;            // [kMaxSeq] u8
-  static constexpr int kInfo = kCnt + kMaxSeq;               // [VS] valid tokens of the page
-  static constexpr int kKinfo = kInfo + C::VS * 4;           // [KS] the same
-  static constexpr int kBar = (kKinfo + C::KS * 4 + 7) / 8 * 8;
-  static constexpr int kBars = 2 * C::KS + 2 * C::VS + 4 + 3 * C::VB + 5;
+  static constexpr int kOff = kCnt + kMaxSeq;                // [4] i64: page offsets of loads
+  static constexpr int kBar = kOff + 4 * 8;
+  static constexpr int kBars = C::KS + C::VS + 2;
   static constexpr int kStart = kBar + kBars * 8;            // where the range begins
-  static constexpr int kMisc = kStart + 24;                  // abort, tmem address, scan space
-  static constexpr int kBytes = kMisc + 16 + 32 * 8 + 1024;  // + slack for the 1024-byte alignment
-  static_assert(kVraw % 16 == 0 && kV % 1024 == 0 && kP % 16 == 0 && kQ % 128 == 0 && kRef % 16 == 0 && kMask % 8 == 0, "alignment");
-  static_assert(kBytes <= 227 * 1024, "shared memory");
+  static constexpr int kInfo = kStart + 24;                  // [4] valid tokens of loaded pages
+  static constexpr int kMisc = kInfo + 16;                   // abort, tmem address, scan space
+  static constexpr int kBytes = kMisc + 8 + 8 * 4 + 1024;    // + slack for the 1024-byte alignment
+  static_assert(kV % 1024 == 0 && kVraw % 16 == 0 && kRef % 16 == 0 && kMask % 8 == 0 &&
+                kOff % 8 == 0, "alignment");
+  static_assert(C::CTAS * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
 template <class C>
 struct Tm {  // tensor-memory columns
-  static constexpr int kS = 0;                    // two S buffers
-  static constexpr int kO = 2 * C::kScols;
-  static constexpr int kSfa = kO + C::NR;         // two sets of 4 (scale fields start at
-  static constexpr int kSfb = kSfa + 8;           // multiples of 4)
+  static constexpr int kS = 0;
+  static constexpr int kO = C::kScols;
+  static constexpr int kSfa = kO + C::NR;         // (scale fields start at multiples of 4)
+  static constexpr int kSfb = kSfa + 4;           // hi, lo
   static constexpr int kSfbRows = C::kTwin ? 2 * C::NR : C::NR;  // rows of one operand
   static constexpr int kSfbW = (kSfbRows + 31) / 32;             // 32 rows a column
   static constexpr int kUsed = kSfb + (C::kTwin ? 4 : 8);
@@ -194,27 +193,6 @@ __device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0u;
 }
-// A ring position: slot and the parity of its use.
-template <int S>
-struct Ring {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == S) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
-};
-
-// This warpgroup's registers a thread from here on.
-template <int kFrom, int kTo>
-__device__ __forceinline__ void set_regs() {
-  if constexpr (kTo > kFrom)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kTo));
-  else if constexpr (kTo < kFrom)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kTo));
-}
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
@@ -244,6 +222,33 @@ __device__ __forceinline__ void st16(uint32_t taddr, const float* x) {
       : "memory");
 }
 
+__device__ __forceinline__ void ld8(uint32_t taddr, float* x) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void st8(uint32_t taddr, const float* x) {
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(x[i]);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+template <int W>
+__device__ __forceinline__ void ldw(uint32_t taddr, float* x) {
+  if constexpr (W == 8) ld8(taddr, x); else ld16(taddr, x);
+}
+template <int W>
+__device__ __forceinline__ void stw(uint32_t taddr, const float* x) {
+  if constexpr (W == 8) st8(taddr, x); else st16(taddr, x);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -260,15 +265,15 @@ __device__ __forceinline__ uint32_t bf16_mul2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Column sums (maxima) over a warp's lanes of 16 values a lane: lane l returns column
-// l % 16's.  Each step halves the columns a lane holds: 16 shuffles, not 80.
-template <class Op>
-__device__ __forceinline__ float columns16(const float* in, int lane, Op op) {
-  float v[16];
+// Column sums (maxima) over a warp's lanes of W values a lane: lane l returns column l % W's.
+// Each step halves the columns a lane holds: about W shuffles, not 5 W.
+template <int W, class Op>
+__device__ __forceinline__ float columns(const float* in, int lane, Op op) {
+  float v[W];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = in[i];
+  for (int i = 0; i < W; ++i) v[i] = in[i];
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  for (int o = W / 2; o > 0; o >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -276,7 +281,9 @@ __device__ __forceinline__ float columns16(const float* in, int lane, Op op) {
       v[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, o));
     }
   }
-  return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 16));
+#pragma unroll
+  for (int o = W; o < 32; o <<= 1) v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
+  return v[0];
 }
 
 // What a sequence's cached tokens give its tiles: pages 0 .. ns-1 hold the first
@@ -309,51 +316,29 @@ struct Start {
 constexpr int kMinPages = 2;
 
 template <class C>
-__global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_constant__ Args a) {
   using L_ = Lay<C>;
   using T_ = Tm<C>;
-  constexpr int NR = C::NR, NC = C::NC, SG = C::SG, DW = C::DW, KS = C::KS, VS = C::VS, VB = C::VB;
+  constexpr int NR = C::NR, NC = C::NC, KS = C::KS, VS = C::VS, W = NC < 16 ? NC : 16;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_addr(sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t* const s_pref = reinterpret_cast<int64_t*>(sm + L_::kPref);
+  uint32_t* const s_pref = reinterpret_cast<uint32_t*>(sm + L_::kPref);
   int* const s_len = reinterpret_cast<int*>(sm + L_::kLen);
   uint8_t* const s_cnt = sm + L_::kCnt;
-  volatile int* const s_info = reinterpret_cast<volatile int*>(sm + L_::kInfo);
-  volatile int* const s_kinfo = reinterpret_cast<volatile int*>(sm + L_::kKinfo);
+  int64_t* const s_off = reinterpret_cast<int64_t*>(sm + L_::kOff);
+  int* const s_info = reinterpret_cast<int*>(sm + L_::kInfo);
+  Start* const s_start = reinterpret_cast<Start*>(sm + L_::kStart);
   volatile int* const s_abort = reinterpret_cast<volatile int*>(sm + L_::kMisc);
   uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(sm + L_::kMisc + 4);
-  int64_t* const s_scan = reinterpret_cast<int64_t*>(sm + L_::kMisc + 16);
+  uint32_t* const s_scan = reinterpret_cast<uint32_t*>(sm + L_::kMisc + 8);
   auto bar = [&](int i) { return sb + L_::kBar + 8u * i; };
-  constexpr int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = kVFull + VS,
-                kSFull = kVEmpty + VS, kSFree = kSFull + 2, kPFull = kSFree + 2,
-                kVReady = kPFull + VB, kPvDone = kVReady + VB, kQFull = kPvDone + VB,
-                kQEmpty = kQFull + 1, kOFree = kQEmpty + 1, kDrain = kOFree + 1;  // two
+  constexpr int kKFull = 0, kVFull = KS, kSFull = KS + VS, kPvDone = kSFull + 1;
 
   if (tid == 0) {
-    for (int i = 0; i < KS; ++i) {
-      mbar_init(bar(kKFull + i), 1);
-      mbar_init(bar(kKEmpty + i), 1 + 4 * SG);
-    }
-    for (int i = 0; i < VS; ++i) {
-      mbar_init(bar(kVFull + i), 1);
-      mbar_init(bar(kVEmpty + i), DW);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kSFull + i), 1);
-      mbar_init(bar(kSFree + i), 4 * SG);
-      mbar_init(bar(kDrain + i), 1);
-    }
-    for (int i = 0; i < VB; ++i) {
-      mbar_init(bar(kPFull + i), 4 * SG);
-      mbar_init(bar(kVReady + i), DW);
-      mbar_init(bar(kPvDone + i), 1);
-    }
-    mbar_init(bar(kQFull), DW);
-    mbar_init(bar(kQEmpty), 1);
-    mbar_init(bar(kOFree), 4 * SG);
+    for (int i = 0; i < L_::kBars; ++i) mbar_init(bar(i), 1);
     *s_abort = 0;
     fence_barrier_init();
   }
@@ -367,9 +352,9 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
   // ---- pages a sequence and their prefix sum (a tile without pages counts as one)
+  static_assert(kMaxSeq <= kThreads && (int64_t)kMaxSeq << 23 <= 0xFFFFFFFFll, "a thread a sequence");
   {
-    static_assert(kMaxSeq <= C::kThreads, "a thread a sequence");
-    int64_t mine = 0;
+    uint32_t mine = 0;
     if (tid < a.B) {
       int64_t L = a.seq_lens[tid];
       int n = a.n_nodes ? a.n_nodes[tid] : a.N;
@@ -382,10 +367,10 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
       s_cnt[tid] = (uint8_t)n;
       mine = max(1, span_of((int)L, n, a.window, a.sinks).np);
     }
-    int64_t inc = mine;
+    uint32_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
       if (lane >= o) inc += y;
     }
     if (lane == 31) s_scan[warp] = inc;
@@ -395,10 +380,9 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
   }
   __syncthreads();
   // ---- this CTA's range of pages, by one thread (all the divisions are here, once)
-  Start* const s_start = reinterpret_cast<Start*>(sm + L_::kStart);
   if (tid == 0) {
     const int HT = a.Hkv * a.tiles;
-    const int64_t U = s_pref[a.B - 1] * HT, g = blockIdx.x;
+    const int64_t U = (int64_t)s_pref[a.B - 1] * HT, g = blockIdx.x;
     // few pages a CTA are not worth the records: at least kMinPages each
     const int64_t Gd = max((int64_t)1, min((int64_t)gridDim.x, U / kMinPages));
     Start x{};
@@ -409,7 +393,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
       int lo = 0, hi = a.B - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (s_pref[mid] * HT > u0) hi = mid; else lo = mid + 1;
+        if ((int64_t)s_pref[mid] * HT > u0) hi = mid; else lo = mid + 1;
       }
       const int64_t p0 = lo > 0 ? s_pref[lo - 1] : 0, np = s_pref[lo] - p0, r = u0 - p0 * HT;
       const int ht = (int)(r / np);
@@ -436,7 +420,6 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
   pdl_launch_dependents();  // after this CTA has its tensor memory
 
   const uint32_t tm = *s_taddr;
-
   auto wait = [&](int i, uint32_t parity) -> bool {
     const uint32_t b = bar(i);
     if (__builtin_expect(mbar_spin(b, parity), 1)) return true;
@@ -476,203 +459,164 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
     }
     settle(c);
   };
-  // The tiles of this CTA's range, in order: f(tile number among those with pages, sequence,
-  // head, row tile, its span, its pages [e0, e1) of this range).
-  auto for_tiles = [&](auto&& f) {
-    int count = 0;
-    for (Cursor c = begin(); c.left > 0; advance(c)) {
-      f(count, c.s, c.h, c.rt, c.sp, c.e0, c.e1);
-      count += c.sp.np > 0;
-    }
-  };
   auto page_no = [](const Span& sp, int e) { return e < sp.ns ? e : sp.first + (e - sp.ns); };
 
-  constexpr int kLaunchRegs = 65536 / (C::CTAS * C::kThreads) / 8 * 8;
-  static_assert(C::kRegs <= kLaunchRegs * C::kThreads, "the roles' registers are the launch's");
-  if (warp < 4) {
-  set_regs<kLaunchRegs, C::RC>();  // (by the warpgroup as one)
-  if (warp == 0 || warp == 3) {
-    // ================= producers: K (warp 0) and V (warp 3).  The lanes look up 32 pages of a
-    // tile at once, the next ones before the present ones' copies.
-    const bool isv = warp == 3;
-    int k = 0;
-    Ring<KS> kr;
-    Ring<VS> vr;
-    Cursor c = begin();
-    auto look = [&](const Cursor& x) {
-      const int e = x.e0 + lane;
-      return x.left > 0 && x.sp.np > 0 && e < x.e1
-                 ? a.table[(int64_t)x.s * a.bt_width + page_no(x.sp, e)]
-                 : -1;
-    };
-    int pid_n = look(c);
-    while (c.left > 0) {
-      const Cursor cur = c;
-      const int pid_c = pid_n;
-      const int cnt = min(32, cur.e1 - cur.e0);
-      if (cnt < cur.e1 - cur.e0) {
-        c.e0 += 32;
-        c.left -= 32;
-      } else {
-        advance(c);
-      }
-      pid_n = look(c);
-      if (cur.sp.np == 0) continue;
+  // ---- loads, by one thread: page ki of the range is the next K to load, vi the next V.
+  // The table entry of page ki is read a page ahead.  A page's offset and its number of valid
+  // tokens (0: a bad page, not loaded) are left for V's load and the softmax.
+  constexpr int kLoader = 128;
+  Cursor lc = begin();
+  int ki = 0, vi = 0, le = lc.e0, lpid = -1;
+  auto look = [&]() {  // the next page that there is
+    while (lc.left > 0 && (le >= lc.e1 || lc.sp.np == 0)) {
+      advance(lc);
+      le = 0;
+    }
+    if (lc.left > 0) lpid = a.table[(int64_t)lc.s * a.bt_width + page_no(lc.sp, le)];
+  };
+  auto load_k = [&]() {
+    if (lc.left <= 0 || *s_abort) return;
+    const int st = ki % KS;
+    const bool ok = lpid >= 0 && lpid < a.num_pages;
+    const int64_t off = (int64_t)lpid * a.page_stride + (int64_t)lc.h * a.head_stride;
+    s_off[ki & 3] = ok ? off : -1;
+    s_info[ki & 3] = ok ? min(kPageTokens, lc.sp.len - page_no(lc.sp, le) * kPageTokens) : 0;
+    const uint32_t fb = bar(kKFull + st);
+    if (ok) {
+      mbar_arrive_expect_tx(fb, kRowDataBytes * kPageTokens + 512);
+      asm volatile(
+          "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+          "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(sb + L_::kK + st * kKTile),
+          "l"(reinterpret_cast<uint64_t>(&a.tmap)), "r"(0), "r"(0), "r"(0), "r"(lc.h), "r"(lpid),
+          "r"(fb)
+          : "memory");
+      bulk_copy_g2s(sb + L_::kKsc + st * 512, a.k_pages + off + kScaleOffset, 512, fb);
+    } else {
+      flag(a.status, MX4_STATUS_BAD_PAGE);
+      mbar_arrive(fb);
+    }
+    ++ki;
+    ++le;
+    look();
+  };
+  auto load_v = [&]() {
+    if (vi >= ki || *s_abort) return;
+    const int st = vi % VS;
+    const int64_t off = s_off[vi & 3];
+    if (off >= 0) {
+      mbar_arrive_expect_tx(bar(kVFull + st), kPageBytes);
+      bulk_copy_g2s(sb + L_::kVraw + st * kPageBytes, a.v_pages + off, kPageBytes, bar(kVFull + st));
+    } else {
+      mbar_arrive(bar(kVFull + st));
+    }
+    ++vi;
+  };
+  if (tid == kLoader) {
+    look();
+    for (int i = 0; i < KS; ++i) load_k();
+    for (int i = 0; i < VS; ++i) load_v();
+  }
+
+  // ---- MMAs, by one thread
+  // S^T = K q^T of page k (K landed: kKFull), fence_after() before
+  auto issue_s = [&](int k) {
+    const int st = k % KS;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(tm + T_::kSfa),
+                 "l"(desc(sb + L_::kKsc + st * 512, 16, 128))
+                 : "memory");
+    const uint64_t ad = desc(sb + L_::kK + st * kKTile, 16, 1024) | ((uint64_t)2 << 61);
+    const uint64_t bd = desc(sb + L_::kQ, 128, 1024);
+#pragma unroll
+    for (uint32_t part = 0; part < (C::kTwin ? 1 : 2); ++part)
+#pragma unroll
+      for (uint32_t kb = 0; kb < 4; ++kb)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, "
+            "%2, %3, [%4], [%5], p;\n}\n" ::"r"(tm + T_::kS),
+            "l"(ad + kb * (32 >> 4)), "l"(bd + ((part * NR * 128 + kb * 256) >> 4)),
+            "r"(idesc_s<T_::kSfbRows>(kb)), "r"(tm + T_::kSfa), "r"(tm + T_::kSfb + part * 4),
+            "r"(part + kb)
+            : "memory");
+    commit(bar(kSFull));
+  };
+  // O^T (+)= V^T P^T
+  auto issue_pv = [&](bool first) {
+    const uint64_t ad = desc(sb + L_::kV, kVHalf, 1024) | ((uint64_t)2 << 61);
+    const uint64_t bd = desc(sb + L_::kP, 128, kChunk);
+#pragma unroll
+    for (uint32_t ks = 0; ks < 8; ++ks)
+      asm volatile(
+          "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+          " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tm + T_::kO),
+          "l"(ad + ks * (2048 >> 4)), "l"(bd + ks * (256 >> 4)), "r"(idesc_o<NR>()),
+          "r"((uint32_t)(ks > 0 || !first))
+          : "memory");
+    commit(bar(kPvDone));
+  };
+
+  // ---- the softmax group's rows c0 .. c0 + NC - 1 of a tile
+  const int w = warp & 3, t = tid & 127, c0 = (warp >> 2) * NC;
+  const uint32_t tl = tm + ((uint32_t)(32 * w) << 16);
+  float* const s_nref = reinterpret_cast<float*>(sm + L_::kRef) + c0;
+  float* const s_fac = reinterpret_cast<float*>(sm + L_::kFac) + c0;
+  float* const s_warp = reinterpret_cast<float*>(sm + L_::kWarp) + 4 * c0;  // [4][NC]
+  uint32_t* const s_nan = reinterpret_cast<uint32_t*>(sm + L_::kNan) + c0;
+  int* const s_node = reinterpret_cast<int*>(sm + L_::kNode) + c0;
+  int* const s_lo = reinterpret_cast<int*>(sm + L_::kLo) + c0;
+  uint32_t* const s_mask = reinterpret_cast<uint32_t*>(sm + L_::kMask) + 2 * c0;  // [NC][2]
+  const float cs = a.scale * kLog2e;
+  const int tok = 4 * lane + w;  // this lane's token of a page
+  // dequantisation: see below
+  const int r8 = lane & 7, blk = ((r8 >> 1) + (lane >> 3)) & 3;
+
+  int k = 0;  // pages done
+  for (Cursor cu = begin(); cu.left > 0; advance(cu)) {
+    const Span sp = cu.sp;
+    const bool begins = cu.e0 == 0, ends = cu.e1 >= sp.np;
+    __syncthreads();  // the tile before is written out
+    // ---- the tile's rows
+    if (t < NC) {
+      const int row = cu.rt * NR + c0 + t, node = row / a.G;
+      s_node[t] = node < a.N ? node * a.H + cu.h * a.G + row % a.G : -1;
+      uint64_t mk = 0;
+      int lo = 0;
+      if (node < sp.n) {
+        const uint64_t all = sp.n < 64 ? (1ull << sp.n) - 1 : ~0ull;
+        auto mask_of = [&](int j) {
+          return (a.mask ? a.mask[(int64_t)cu.s * a.N + j] : (2ull << j) - 1) & all;
+        };
+        mk = mask_of(node);
+        if (a.window > 0) {
+          const int d = max(1, __popcll(mk)) - 1;
+          lo = max(0, sp.base + d + 1 - a.window);
 #pragma unroll 1
-      for (int i = 0; i < cnt; ++i) {
-        const int pid = __shfl_sync(0xFFFFFFFFu, pid_c, i);
-        if (lane == 0) {
-          const bool ok = pid >= 0 && pid < a.num_pages;
-          const int live = min(kPageTokens, cur.sp.len - page_no(cur.sp, cur.e0 + i) * kPageTokens);
-          const int64_t off = (int64_t)pid * a.page_stride + (int64_t)cur.h * a.head_stride;
-          const int st = isv ? vr.slot : kr.slot;
-          const uint32_t fb = bar((isv ? kVFull : kKFull) + st);
-          bool go = !*s_abort;
-          if (k >= (isv ? VS : KS))
-            go = wait((isv ? kVEmpty : kKEmpty) + st, (isv ? vr.phase : kr.phase) ^ 1u) && go;
-          if (go) {
-            if (isv) s_info[st] = ok ? live : 0; else s_kinfo[st] = ok ? live : 0;
-            if (!ok) {
-              flag(a.status, MX4_STATUS_BAD_PAGE);
-              mbar_arrive(fb);
-            } else if (isv) {
-              mbar_arrive_expect_tx(fb, kPageBytes);
-              bulk_copy_g2s(sb + L_::kVraw + st * kPageBytes, a.v_pages + off, kPageBytes, fb);
-            } else {
-              mbar_arrive_expect_tx(fb, kRowDataBytes * kPageTokens + 1024);
-              asm volatile(
-                  "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                  "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(sb + L_::kK + st * kKTile),
-                  "l"(reinterpret_cast<uint64_t>(&a.tmap)), "r"(0), "r"(0), "r"(0), "r"(cur.h),
-                  "r"(pid), "r"(fb)
-                  : "memory");
-              bulk_copy_g2s(sb + L_::kKsc + st * 1024, a.k_pages + off + kScaleOffset, 512, fb);
-              bulk_copy_g2s(sb + L_::kKsc + st * 1024 + 512, a.v_pages + off + kScaleOffset, 512, fb);
-            }
+          for (int i = 0; i < sp.n; ++i) {
+            const int di = max(1, __popcll(mask_of(i))) - 1;
+            if (!(di > d - a.window || sp.base + di < a.sinks)) mk &= ~(1ull << i);
           }
         }
-        __syncwarp();
-        ++k;
-        kr.next();
-        vr.next();
       }
+      s_mask[2 * t] = (uint32_t)mk;
+      s_mask[2 * t + 1] = (uint32_t)(mk >> 32);
+      s_lo[t] = lo;
+      s_nref[t] = -kUnset;
+      s_nan[t] = 0;
     }
-    // every copy has landed before the CTA ends
-    if (lane == 0) {
-      const int S = isv ? VS : KS, full = isv ? kVFull : kKFull;
-      for (int i = max(0, k - S); i < k; ++i) wait(full + i % S, (i / S) & 1);
-    }
-  } else if (warp == 1) {
-    // ================= S^T = K q^T: one lane
-    if (lane == 0) {
-      int k = 0;
-      Ring<KS> kr;
-      Ring<2> sr;
-      const uint64_t ad0 = desc(sb + L_::kK, 16, 1024) | ((uint64_t)2 << 61);
-      const uint64_t sd0 = desc(sb + L_::kKsc, 16, 128), bd0 = desc(sb + L_::kQ, 128, 1024);
-      for_tiles([&](int tile, int, int, int, const Span& sp, int e0, int e1) {
-        if (sp.np == 0) return;
-        wait(kQFull, tile & 1);
-        for (int e = e0; e < e1; ++e, ++k, kr.next(), sr.next()) {
-          const int st = kr.slot, b = sr.slot;
-          wait(kKFull + st, kr.phase);
-          if (k >= 2) wait(kSFree + b, sr.phase ^ 1u);
-          if (*s_abort) continue;
-          fence_after();
-          const uint32_t sfa = tm + T_::kSfa + 4u * b;
-          const uint64_t ad = ad0 + st * (kKTile >> 4);
-          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(sfa),
-                       "l"(sd0 + st * (1024 >> 4))
-                       : "memory");
-#pragma unroll
-          for (uint32_t part = 0; part < (C::kTwin ? 1 : 2); ++part)
-#pragma unroll
-            for (uint32_t kb = 0; kb < 4; ++kb)
-              asm volatile(
-                  "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-                  " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, "
-                  "%2, %3, [%4], [%5], p;\n}\n" ::"r"(tm + T_::kS + b * C::kScols),
-                  "l"(ad + kb * (32 >> 4)), "l"(bd0 + ((part * NR * 128 + kb * 256) >> 4)),
-                  "r"(idesc_s<T_::kSfbRows>(kb)), "r"(sfa), "r"(tm + T_::kSfb + part * 4),
-                  "r"(part + kb)
-                  : "memory");
-          commit(bar(kSFull + b));
-          commit(bar(kKEmpty + st));
-          if (e == e1 - 1) commit(bar(kQEmpty));
-        }
-      });
-      if (k > 0) {  // no MMA in flight when the tensor memory is freed
-        commit(bar(kDrain));
-        for (uint32_t p = 0; p < kWaitPolls; ++p)
-          if (mbar_test(bar(kDrain), 0)) break;
-      }
-    }
-  } else {
-    // ================= O^T += V^T P^T: one lane
-    if (lane == 0) {
-      int k = 0;
-      Ring<VB> br;
-      const uint64_t ad0 = desc(sb + L_::kV, kVHalf, 1024) | ((uint64_t)2 << 61);
-      const uint64_t bd0 = desc(sb + L_::kP, 128, kChunk);
-      for_tiles([&](int tile, int, int, int, const Span& sp, int e0, int e1) {
-        if (sp.np == 0) return;
-        if (tile > 0) wait(kOFree, (tile - 1) & 1);
-        for (int e = e0; e < e1; ++e, ++k, br.next()) {
-          const int b = br.slot;
-          wait(kVReady + b, br.phase);
-          wait(kPFull + b, br.phase);
-          if (*s_abort) continue;
-          fence_after();
-          const uint64_t ad = ad0 + b * (kVTile >> 4), bd = bd0 + b * ((NR / 8) * kChunk >> 4);
-#pragma unroll
-          for (uint32_t ks = 0; ks < 8; ++ks)
-            asm volatile(
-                "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tm + T_::kO),
-                "l"(ad + ks * (2048 >> 4)), "l"(bd + ks * (256 >> 4)), "r"(idesc_o<NR>()),
-                "r"((uint32_t)(ks > 0 || e > e0))
-                : "memory");
-          commit(bar(kPvDone + b));
-        }
-      });
-      if (k > 0) {
-        commit(bar(kDrain + 1));
-        for (uint32_t p = 0; p < kWaitPolls; ++p)
-          if (mbar_test(bar(kDrain + 1), 0)) break;
-      }
-    }
-  }
-  } else if (warp >= 4 + 4 * SG) {
-    set_regs<kLaunchRegs, C::RD>();
-    // ================= q conversion and V dequantisation
-    const int t = tid - 32 * (4 + 4 * SG), w = t >> 5;
-    const int r8 = lane & 7, blk = ((r8 >> 1) + (lane >> 3)) & 3;  // see below
-    int k = 0;
-    Ring<VS> vr;
-    Ring<VB> br;
-    for_tiles([&](int tile, int s, int h, int rt, const Span& sp, int e0, int e1) {
-      if (sp.np == 0) return;
-      // 16 elements a thread: K-chunk j of row n; the two threads of a 32-block share its
-      // largest magnitude.  The rows are on their way while the tile before finishes.
-      constexpr int kIt = (NR * 8 + DW * 32 - 1) / (DW * 32);
-      uint4 x0[kIt], x1[kIt];
-#pragma unroll
-      for (int i = 0; i < kIt; ++i) {
-        const int n = (t >> 3) + i * DW * 4, row = rt * NR + n, node = row / a.G;
-        x0[i] = x1[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (n < NR && node < sp.n) {
+    // ---- q: 16 elements a thread, K-chunk j of row n; the two threads of a 32-block share
+    // its largest magnitude
+    if (sp.np > 0) {
+#pragma unroll 1
+      for (int n = tid >> 3; n < NR; n += kThreads / 8) {
+        const int j = tid & 7, row = cu.rt * NR + n, node = row / a.G;
+        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+        if (node < sp.n) {
           const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + (((int64_t)s * a.N + node) * a.H + h * a.G + row % a.G) * kHeadDim +
-              16 * (t & 7));
-          x0[i] = src[0];
-          x1[i] = src[1];
+              a.q + (((int64_t)cu.s * a.N + node) * a.H + cu.h * a.G + row % a.G) * kHeadDim + 16 * j);
+          x0 = src[0];
+          x1 = src[1];
         }
-      }
-      if (tile > 0) wait(kQEmpty, (tile - 1) & 1);
-#pragma unroll
-      for (int i = 0; i < kIt; ++i) {
-        const int n = (t >> 3) + i * DW * 4, j = t & 7;
-        const uint32_t wd[8] = {x0[i].x, x0[i].y, x0[i].z, x0[i].w, x1[i].x, x1[i].y, x1[i].z, x1[i].w};
+        const uint32_t wd[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
         float amax = 0.f;
 #pragma unroll
         for (int u = 0; u < 8; ++u)
@@ -685,7 +629,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          uint16_t hc[2], lc[2];
+          uint16_t hc[2], lc2[2];
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const uint32_t x2 = wd[2 * u + v];
@@ -699,70 +643,205 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
             const float h0 = __half2float(__ushort_as_half((unsigned short)(hf & 0xFFFFu)));
             const float h1 = __half2float(__ushort_as_half((unsigned short)(hf >> 16)));
             asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;\n"
-                : "=h"(lc[v])
+                : "=h"(lc2[v])
                 : "f"((y0 - h0) * 32.f), "f"((y1 - h1) * 32.f));
           }
           hi[u] = (uint32_t)hc[0] | ((uint32_t)hc[1] << 16);
-          lo[u] = (uint32_t)lc[0] | ((uint32_t)lc[1] << 16);
+          lo[u] = (uint32_t)lc2[0] | ((uint32_t)lc2[1] << 16);
         }
-        if (n < NR) {
-          uint8_t* dst = sm + L_::kQ + (n >> 3) * 1024 + j * 128 + (n & 7) * 16;
-          *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(dst + NR * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          if ((j & 1) == 0) {
-            sm[L_::kSf + n * 4 + (j >> 1)] = (uint8_t)(E + 127);
-            sm[L_::kSf + (NR + n) * 4 + (j >> 1)] = (uint8_t)(E + 122);
-          }
+        uint8_t* dst = sm + L_::kQ + (n >> 3) * 1024 + j * 128 + (n & 7) * 16;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + NR * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if ((j & 1) == 0) {
+          sm[L_::kSf + n * 4 + (j >> 1)] = (uint8_t)(E + 127);
+          sm[L_::kSf + (NR + n) * 4 + (j >> 1)] = (uint8_t)(E + 122);
         }
       }
       fence_async();
-      asm volatile("bar.sync 7, %0;\n" ::"n"(32 * DW) : "memory");
+    }
+    __syncthreads();
+    float l[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) l[c] = 0.f;
+
+    if (sp.np > 0) {
       // operand row n's scale word at lane n % 32 of every lane quarter, column n / 32
-      if (w < 4) {
+      if (warp < 4) {
 #pragma unroll
         for (int part = 0; part < (C::kTwin ? 1 : 2); ++part)
 #pragma unroll
           for (int c = 0; c < T_::kSfbW; ++c)
-            st1(tm + ((uint32_t)(32 * w) << 16) + T_::kSfb + part * 4 + c,
+            st1(tl + T_::kSfb + part * 4 + c,
                 *reinterpret_cast<const uint32_t*>(sm + L_::kSf + (part * NR + c * 32 + lane) * 4));
         wait_st();
       }
       fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kQFull));
-
-      for (int e = e0; e < e1; ++e, ++k, vr.next(), br.next()) {
-        const int st = vr.slot, b = br.slot;
-        wait(kVFull + st, vr.phase);
-        const int live = s_info[st];
-        // Operand row (K index) m holds token 4 (m % 32) + m / 32, the order in which the
-        // tensor copy lays out K.  A warp's step: 8 operand rows (r8), lane >> 3 choosing
-        // which 32-dim block of each: 16 raw bytes a lane, four 16-byte stores without bank
-        // conflicts.  A short loop: the roles' code together must stay near the warps.
-        const uint8_t* raw = sm + L_::kVraw + st * kPageBytes;
-        if (k >= VB) wait(kPvDone + b, br.phase ^ 1u);
-        constexpr int kIts = 16 / DW;
+      __syncthreads();
+      if (tid == 0) {
+        wait(kKFull + k % KS, (k / KS) & 1);
+        if (!*s_abort) {
+          fence_after();
+          issue_s(k);
+        }
+      }
 #pragma unroll 1
-        for (int it = 0; it < kIts; ++it) {
-          const int m = (w * kIts + it) * 8 + r8, tok = 4 * (m & 31) + (m >> 5);
-          const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tok * kRowDataBytes + blk * 16);
-          const uint32_t sc = raw[kScaleOffset + tok * kRowScaleBytes + blk];
+      for (int e = cu.e0; e < cu.e1; ++e, ++k) {
+        // ---- logits in log2 units relative to the rows' references
+        const int first = page_no(sp, e) * kPageTokens, live = s_info[k & 3];
+        const bool plain = live == kPageTokens && first + kPageTokens <= sp.base &&
+                           (a.window == 0 || first > sp.base + 63 - a.window ||
+                            first + kPageTokens <= a.sinks);
+        // a row sees a draft by its mask, an earlier token from the window's first on; rows
+        // without a node see what they like, their results are zeroed
+        uint32_t vis = ~0u;
+        if (!plain) {
+          vis = 0u;
+          const int i_g = first + tok, nd = i_g - sp.base;
+          if (tok < live) {
+#pragma unroll 1
+            for (int c = 0; c < NC; ++c) {
+              const bool see = nd >= 0 ? ((s_mask[2 * c + ((nd >> 5) & 1)] >> (nd & 31)) & 1u) != 0u
+                                       : i_g >= s_lo[c] || i_g < a.sinks;
+              vis |= (uint32_t)see << c;
+            }
+          }
+        }
+        wait(kSFull, k & 1);
+        fence_after();
+        float x[NC];
+        const uint32_t ts = tl + T_::kS + c0;
+        // S of W rows, hi and lo parts added where they are apart
+        auto s_of = [&](int c, float* v) {
+          ldw<W>(ts + c, v);
+          if constexpr (C::kTwin) {
+            float y[W];
+            ldw<W>(ts + NR + c, y);
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] += y[i];
+          } else {
+            wait_ld();
+          }
+        };
+        // -inf where not seen, whatever was computed there
+        auto hide = [&](int c, float* v) {
+          if (plain) return;
+          const uint32_t vb = vis >> c;
+#pragma unroll
+          for (int i = 0; i < W; ++i) v[i] = (vb >> i) & 1u ? v[i] : -INFINITY;
+        };
+        bool moved = false;  // new references were set on this page
+        for (;; moved = true) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < NC; c += W) {
+            s_of(c, x + c);
+#pragma unroll
+            for (int i = c; i < c + W; i += 4) {
+              const float4 rf = *reinterpret_cast<const float4*>(s_nref + i);
+              x[i] = fmaf(x[i], cs, rf.x);
+              x[i + 1] = fmaf(x[i + 1], cs, rf.y);
+              x[i + 2] = fmaf(x[i + 2], cs, rf.z);
+              x[i + 3] = fmaf(x[i + 3], cs, rf.w);
+            }
+            hide(c, x + c);
+            float m[W / 2];
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) m[i] = fmaxf(x[c + i], x[c + W / 2 + i]);
+#pragma unroll
+            for (int o = W / 4; o > 0; o >>= 1)
+#pragma unroll
+              for (int i = 0; i < o; ++i) m[i] = fmaxf(m[i], m[i + o]);
+            top = fmaxf(top, m[0]);
+          }
+          fence_before();
+          if (moved || !__syncthreads_or(top > kLazy)) break;
+          // new references: the page's maximum of each row that has a larger one; what was
+          // summed so far is brought to them, and the page's logits are taken once more
+#pragma unroll 1
+          for (int c = 0; c < NC; c += W) {
+            float v[W];
+            s_of(c, v);
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] *= cs;
+            hide(c, v);
+            const float mx = columns<W>(v, lane, [](float p, float q) { return fmaxf(p, q); });
+            if (lane < W) s_warp[w * NC + c + lane] = mx;
+          }
+          if (e > cu.e0) wait(kPvDone, (k - 1) & 1);
+          __syncthreads();
+          if (t < NC) {
+            const float v = fmaxf(fmaxf(s_warp[t], s_warp[NC + t]),
+                                  fmaxf(s_warp[2 * NC + t], s_warp[3 * NC + t]));
+            const float old = -s_nref[t], now = fmaxf(old, v);
+            s_fac[t] = old == kUnset ? 0.f : ex2(old - now);
+            s_nref[t] = -now;
+          }
+          __syncthreads();
+#pragma unroll
+          for (int c = 0; c < NC; ++c) l[c] *= s_fac[c];
+          if (e > cu.e0) {
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < NC; c += W) {
+              float o[W];
+              ldw<W>(tl + T_::kO + c0 + c, o);
+              wait_ld();
+#pragma unroll
+              for (int i = 0; i < W; ++i) o[i] *= s_fac[c + i];
+              stw<W>(tl + T_::kO + c0 + c, o);
+            }
+            wait_st();
+          }
+        }
+        // S is in registers everywhere (the vote's barrier): the next page's may replace it, if
+        // its K is there
+        bool ahead = false;
+        if (tid == 0 && !moved && e + 1 < cu.e1 && !*s_abort &&
+            mbar_test(bar(kKFull + (k + 1) % KS), ((k + 1) / KS) & 1)) {
+          fence_after();
+          issue_s(k + 1);
+          ahead = true;
+        }
+        // ---- weights
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          x[c] = ex2(x[c]);
+          l[c] += x[c];
+        }
+        if (k > 0) wait(kPvDone, (k - 1) & 1);  // the operands' buffers are free
+        uint8_t* const pd = sm + L_::kP + (c0 >> 3) * kChunk + (4 * w + (lane >> 3)) * 128 + (lane & 7) * 16;
+#pragma unroll
+        for (int c = 0; c < NC; c += 8)
+          *reinterpret_cast<uint4*>(pd + (c >> 3) * kChunk) =
+              make_uint4(pack_bf16(x[c], x[c + 1]), pack_bf16(x[c + 2], x[c + 3]),
+                         pack_bf16(x[c + 4], x[c + 5]), pack_bf16(x[c + 6], x[c + 7]));
+        // ---- V.  Operand row (K index) m holds token 4 (m % 32) + m / 32, the order in which
+        // the tensor copy lays out K.  A warp's step: 8 operand rows (r8), lane >> 3 choosing
+        // which 32-dim block of each: 16 raw bytes a lane, four 16-byte stores without bank
+        // conflicts.
+        wait(kVFull + k % VS, (k / VS) & 1);
+        const uint8_t* raw = sm + L_::kVraw + (k % VS) * kPageBytes;
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+          const int m = (warp * 2 + it) * 8 + r8, tk = 4 * (m & 31) + (m >> 5);
+          const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tk * kRowDataBytes + blk * 16);
+          const uint32_t sc = raw[kScaleOffset + tk * kRowScaleBytes + blk];
           // 2^(sc - 1), as two factors where it passes bf16's range
-          const uint32_t f1 =
-              ((tok < live && sc != 255u ? min(sc + 126u, 254u) : 0u) << 7) * 0x10001u;
+          const uint32_t f1 = ((tk < live && sc != 255u ? min(sc + 126u, 254u) : 0u) << 7) * 0x10001u;
           const bool big = __any_sync(0xFFFFFFFFu, sc > 128u);
           const uint32_t f2 = ((sc > 128u ? sc - 1u : 127u) << 7) * 0x10001u;
-          uint8_t* const dst = sm + L_::kV + b * kVTile + (blk >> 1) * kVHalf + (m >> 3) * 1024 + r8 * 128;
+          uint8_t* const dst = sm + L_::kV + (blk >> 1) * kVHalf + (m >> 3) * 1024 + r8 * 128;
           const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t x = cw[j];
+            const uint32_t v = cw[j];
             // codes i and i + 4 of the word as one pair
             uint32_t y[4];
-            y[0] = ((x << 12) & 0x80008000u) | ((x << 6) & 0x01C001C0u);
-            y[1] = ((x << 8) & 0x80008000u) | ((x << 2) & 0x01C001C0u);
-            y[2] = ((x << 4) & 0x80008000u) | ((x >> 2) & 0x01C001C0u);
-            y[3] = (x & 0x80008000u) | ((x >> 6) & 0x01C001C0u);
+            y[0] = ((v << 12) & 0x80008000u) | ((v << 6) & 0x01C001C0u);
+            y[1] = ((v << 8) & 0x80008000u) | ((v << 2) & 0x01C001C0u);
+            y[2] = ((v << 4) & 0x80008000u) | ((v >> 2) & 0x01C001C0u);
+            y[3] = (v & 0x80008000u) | ((v >> 6) & 0x01C001C0u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = bf16_mul2(y[i], f1);
             if (big) {
@@ -773,280 +852,101 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
                 make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
+        // NaN dim blocks of this lane's token: the rows that see it get them at the end
+        uint32_t vw = *reinterpret_cast<const uint32_t*>(raw + kScaleOffset + tok * kRowScaleBytes);
+        vw = ((vw & 0x7F7F7F7Fu) + 0x01010101u) & vw & 0x80808080u;
+        if (vw != 0u && tok < live) {
+#pragma unroll 1
+          for (int c = 0; c < NC; ++c)
+            if ((vis >> c) & 1u) atomicOr(s_nan + c, vw);
+        }
         fence_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kVReady + b));
-          mbar_arrive(bar(kVEmpty + st));
-        }
-      }
-    });
-  } else {
-    set_regs<kLaunchRegs, C::RS>();
-    // ================= softmax: group sg has the rows c0 .. c0 + NC - 1 of a tile
-    const int sg = (warp - 4) >> 2, w = warp & 3, t = tid & 127, c0 = sg * NC;
-    const uint32_t tl = tm + ((uint32_t)(32 * w) << 16);
-    float* const s_nref = reinterpret_cast<float*>(sm + L_::kRef) + c0;
-    float* const s_fac = reinterpret_cast<float*>(sm + L_::kFac) + c0;
-    float* const s_warp = reinterpret_cast<float*>(sm + L_::kWarp) + 4 * c0;  // [4][NC]
-    uint32_t* const s_nan = reinterpret_cast<uint32_t*>(sm + L_::kNan) + c0;
-    int* const s_node = reinterpret_cast<int*>(sm + L_::kNode) + c0;
-    int* const s_lo = reinterpret_cast<int*>(sm + L_::kLo) + c0;
-    uint32_t* const s_mask = reinterpret_cast<uint32_t*>(sm + L_::kMask) + 2 * c0;  // [NC][2]
-    auto sync4 = [&]() { asm volatile("bar.sync %0, 128;\n" ::"r"(sg + 1) : "memory"); };
-    auto any4 = [&](bool v) {
-      uint32_t r;
-      asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-          " barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-          : "=r"(r)
-          : "r"((uint32_t)v), "r"(sg + 1)
-          : "memory");
-      return r != 0u;
-    };
-    const float cs = a.scale * kLog2e;
-    const int tok = 4 * lane + w;  // this lane's token of a page
-    int k = 0;
-    Ring<KS> kr;
-    Ring<2> sr;
-    Ring<VB> br;
-    for_tiles([&](int tile, int s, int h, int rt, const Span& sp, int e0, int e1) {
-      const bool begins = e0 == 0, ends = e1 >= sp.np;
-      // ---- the tile's rows
-      sync4();  // the tile before is written out
-      if (t < NC) {
-        const int row = rt * NR + c0 + t, node = row / a.G;
-        s_node[t] = node < a.N ? node * a.H + h * a.G + row % a.G : -1;
-        uint64_t mk = 0;
-        int lo = 0;
-        if (node < sp.n) {
-          const uint64_t all = sp.n < 64 ? (1ull << sp.n) - 1 : ~0ull;
-          auto mask_of = [&](int j) {
-            return (a.mask ? a.mask[(int64_t)s * a.N + j] : (2ull << j) - 1) & all;
-          };
-          auto depth_of = [&](int j) { return max(1, __popcll(mask_of(j))) - 1; };
-          mk = mask_of(node);
-          if (a.window > 0) {
-            const int d = depth_of(node);
-            lo = max(0, sp.base + d + 1 - a.window);
-            for (int i = 0; i < sp.n; ++i)
-              if ((mk >> i) & 1ull) {
-                const int di = depth_of(i);
-                if (!(di > d - a.window || sp.base + di < a.sinks)) mk &= ~(1ull << i);
-              }
-          }
-        }
-        s_mask[2 * t] = (uint32_t)mk;
-        s_mask[2 * t + 1] = (uint32_t)(mk >> 32);
-        s_lo[t] = lo;
-        s_nref[t] = -kUnset;
-        s_nan[t] = 0;
-      }
-      sync4();
-      float l[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) l[c] = 0.f;
-
-      if (sp.np > 0) {
-        for (int e = e0; e < e1; ++e, ++k, kr.next(), sr.next(), br.next()) {
-          const int st = kr.slot, b = sr.slot, pb = br.slot;
-          const int first = page_no(sp, e) * kPageTokens;
-          wait(kKFull + st, kr.phase);
-          const int live = s_kinfo[st];
-          uint32_t vw = *reinterpret_cast<const uint32_t*>(sm + L_::kKsc + st * 1024 + 512 + tok * 4);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kKEmpty + st));
-          wait(kSFull + b, sr.phase);
+        fence_before();
+        __syncthreads();
+        if (tid == 0 && !*s_abort) {
           fence_after();
-          // dim blocks of this token's V row that are NaN
-          vw = ((vw & 0x7F7F7F7Fu) + 0x01010101u) & vw & 0x80808080u;
-          const bool plain = live == kPageTokens && first + kPageTokens <= sp.base &&
-                             (a.window == 0 || first > sp.base + 63 - a.window ||
-                              first + kPageTokens <= a.sinks);
-          // a row sees a draft by its mask, an earlier token from the window's first on;
-          // rows without a node see what they like, their results are zeroed
-          uint32_t vis = ~0u;
-          if (!plain) {
-            vis = 0u;
-            const int i_g = first + tok, nd = i_g - sp.base;
-            if (tok < live) {
-#pragma unroll 1
-              for (int c = 0; c < NC; ++c) {
-                const bool see = nd >= 0 ? ((s_mask[2 * c + ((nd >> 5) & 1)] >> (nd & 31)) & 1u) != 0u
-                                         : i_g >= s_lo[c] || i_g < a.sinks;
-                vis |= (uint32_t)see << c;
-              }
-            }
+          issue_pv(e == cu.e0);
+          if (!ahead && e + 1 < cu.e1 && wait(kKFull + (k + 1) % KS, ((k + 1) / KS) & 1)) {
+            fence_after();
+            issue_s(k + 1);
           }
-          float x[NC];
-          const uint32_t ts = tl + T_::kS + b * C::kScols + c0;
-          // S of 16 rows, hi and lo parts added where they are apart
-          auto s16 = [&](int c, float* v) {
-            ld16(ts + c, v);
-            if constexpr (C::kTwin) {
-              float y[16];
-              ld16(ts + NR + c, y);
-              wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] += y[i];
-            } else {
-              wait_ld();
-            }
-          };
-          // -inf where not seen, whatever was computed there
-          auto hide16 = [&](int c, float* v) {
-            if (plain) return;
-            const uint32_t vb = vis >> c;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = (vb >> i) & 1u ? v[i] : -INFINITY;
-          };
-          for (bool again = false;; again = true) {
-            float top = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < NC; c += 16) {
-              s16(c, x + c);
-#pragma unroll
-              for (int i = c; i < c + 16; i += 4) {
-                const float4 rf = *reinterpret_cast<const float4*>(s_nref + i);
-                x[i] = fmaf(x[i], cs, rf.x);
-                x[i + 1] = fmaf(x[i + 1], cs, rf.y);
-                x[i + 2] = fmaf(x[i + 2], cs, rf.z);
-                x[i + 3] = fmaf(x[i + 3], cs, rf.w);
-              }
-              hide16(c, x + c);
-              float m[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) m[i] = fmaxf(x[c + i], x[c + 8 + i]);
-#pragma unroll
-              for (int o = 4; o > 0; o >>= 1)
-#pragma unroll
-                for (int i = 0; i < o; ++i) m[i] = fmaxf(m[i], m[i + o]);
-              top = fmaxf(top, m[0]);
-            }
-            if (again || !any4(top > kLazy)) break;
-            // new references: the page's maximum of each row that has a larger one; what was
-            // summed so far is brought to them, and the page's logits are taken once more
-#pragma unroll 1
-            for (int c = 0; c < NC; c += 16) {
-              float v[16];
-              s16(c, v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] *= cs;
-              hide16(c, v);
-              const float mx = columns16(v, lane, [](float p, float q) { return fmaxf(p, q); });
-              if (lane < 16) s_warp[w * NC + c + lane] = mx;
-            }
-            if (e > e0) wait(kPvDone + (VB == 1 ? 0 : pb ^ 1), VB == 1 || pb == 0 ? br.phase ^ 1u : br.phase);
-            sync4();
-            if (t < NC) {
-              const float v = fmaxf(fmaxf(s_warp[t], s_warp[NC + t]),
-                                    fmaxf(s_warp[2 * NC + t], s_warp[3 * NC + t]));
-              const float old = -s_nref[t], now = fmaxf(old, v);
-              s_fac[t] = old == kUnset ? 0.f : ex2(old - now);
-              s_nref[t] = -now;
-            }
-            sync4();
-#pragma unroll
-            for (int c = 0; c < NC; ++c) l[c] *= s_fac[c];
-            if (e > e0) {
-              fence_after();
-#pragma unroll 1
-              for (int c = 0; c < NC; c += 16) {
-                float o[16];
-                ld16(tl + T_::kO + c0 + c, o);
-                wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] *= s_fac[c + i];
-                st16(tl + T_::kO + c0 + c, o);
-              }
-              wait_st();
-            }
-          }
-          // the accumulator has been read: a later page's product may go into it
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kSFree + b));
-          if (vw != 0u) {
-#pragma unroll 1
-            for (int c = 0; c < NC; ++c)
-              if ((vis >> c) & 1u) atomicOr(s_nan + c, vw);
-          }
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            x[c] = ex2(x[c]);
-            l[c] += x[c];
-          }
-          if (k >= VB) wait(kPvDone + pb, br.phase ^ 1u);
-          uint8_t* const pd = sm + L_::kP + (pb * (NR / 8) + (c0 >> 3)) * kChunk +
-                              (4 * w + (lane >> 3)) * 128 + (lane & 7) * 16;
-#pragma unroll
-          for (int c = 0; c < NC; c += 8)
-            *reinterpret_cast<uint4*>(pd + (c >> 3) * kChunk) =
-                make_uint4(pack_bf16(x[c], x[c + 1]), pack_bf16(x[c + 2], x[c + 3]),
-                           pack_bf16(x[c + 4], x[c + 5]), pack_bf16(x[c + 6], x[c + 7]));
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kPFull + pb));
         }
-#pragma unroll
-        for (int c = 0; c < NC; c += 16) {
-          const float v = columns16(l + c, lane, [](float p, float q) { return p + q; });
-          if (lane < 16) s_warp[w * NC + c + lane] = v;
+        if (tid == kLoader) {  // S of page k is done with its K, everyone with its V
+          load_k();
+          load_v();
         }
-        wait(kPvDone + (VB == 1 ? 0 : br.slot ^ 1), VB == 1 || br.slot == 0 ? br.phase ^ 1u : br.phase);
-        sync4();
+      }
+#pragma unroll
+      for (int c = 0; c < NC; c += W) {
+        const float v = columns<W>(l + c, lane, [](float p, float q) { return p + q; });
+        if (lane < W) s_warp[w * NC + c + lane] = v;
+      }
+      wait(kPvDone, (k - 1) & 1);
+    } else {
+      for (int c = t; c < 4 * NC; c += 128) s_warp[c] = 0.f;
+    }
+    __syncthreads();
+    // ---- the tile's result: this lane's dim of every row
+    const bool whole = begins && ends;
+    float* const rec = a.rec + (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * (int64_t)(NR * 130);
+    if (t < NC) {
+      float sum = (s_warp[t] + s_warp[NC + t]) + (s_warp[2 * NC + t] + s_warp[3 * NC + t]);
+      if ((cu.rt * NR + c0 + t) / a.G >= sp.n) sum = 0.f;
+      const float rf = -s_nref[t];
+      if (whole) {
+        s_fac[t] = sum == 0.f ? 0.f : 1.f / sum;
+        if (a.lse && s_node[t] >= 0)
+          a.lse[(int64_t)cu.s * a.N * a.H + s_node[t]] =
+              sum == 0.f ? -INFINITY : (log2f(sum) + (rf == kUnset ? 0.f : rf)) * 0.6931471805599453f;
       } else {
-        for (int c = t; c < 4 * NC; c += 128) s_warp[c] = 0.f;
-        sync4();
+        s_fac[t] = sum == 0.f ? 0.f : 1.f;
+        rec[NR * 128 + c0 + t] = rf;
+        rec[NR * 129 + c0 + t] = sum;
       }
-      // ---- the tile's result: this lane's dim of every row
-      const bool whole = begins && ends;
-      float* const rec = a.rec + (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * (int64_t)(NR * 130);
-      if (t < NC) {
-        float sum = (s_warp[t] + s_warp[NC + t]) + (s_warp[2 * NC + t] + s_warp[3 * NC + t]);
-        if ((rt * NR + c0 + t) / a.G >= sp.n) sum = 0.f;
-        const float rf = -s_nref[t];
-        if (whole) {
-          s_fac[t] = sum == 0.f ? 0.f : 1.f / sum;
-          if (a.lse && s_node[t] >= 0)
-            a.lse[(int64_t)s * a.N * a.H + s_node[t]] =
-                sum == 0.f ? -INFINITY : (log2f(sum) + (rf == kUnset ? 0.f : rf)) * 0.6931471805599453f;
-        } else {
-          s_fac[t] = sum == 0.f ? 0.f : 1.f;
-          rec[NR * 128 + c0 + t] = rf;
-          rec[NR * 129 + c0 + t] = sum;
-        }
-      }
-      sync4();
-      fence_after();
-      // operand position -> dim: the codes of a word were paired i, i + 4
-      const int dim = 32 * w + (lane & 24) + ((lane & 1) << 2) + ((lane & 7) >> 1);
-      const uint32_t nb = 0x80u << (8 * w);
+    }
+    __syncthreads();
+    fence_after();
+    // operand position -> dim: the codes of a word were paired i, i + 4
+    const int dim = 32 * w + (lane & 24) + ((lane & 1) << 2) + ((lane & 7) >> 1);
+    const uint32_t nb = 0x80u << (8 * w);
 #pragma unroll 1
-      for (int c = 0; c < NC; c += 16) {
-        float o[16];
-        if (sp.np > 0) {
-          ld16(tl + T_::kO + c0 + c, o);
-          wait_ld();
-        }
+    for (int c = 0; c < NC; c += W) {
+      float o[W];
+      if (sp.np > 0) {
+        ldw<W>(tl + T_::kO + c0 + c, o);
+        wait_ld();
+      }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float f = s_fac[c + i];
-          const float v = sp.np == 0 || f == 0.f ? 0.f : (s_nan[c + i] & nb) ? NAN : o[i] * f;
-          if (whole) {
-            const int row = s_node[c + i];
-            if (row >= 0)
-              a.out[((int64_t)s * a.N * a.H + row) * kHeadDim + dim] =
-                  __bfloat16_as_ushort(__float2bfloat16_rn(v));
-          } else {
-            rec[(c0 + c + i) * 128 + dim] = v;
-          }
+      for (int i = 0; i < W; ++i) {
+        const float f = s_fac[c + i];
+        const float v = sp.np == 0 || f == 0.f ? 0.f : (s_nan[c + i] & nb) ? NAN : o[i] * f;
+        if (whole) {
+          const int row = s_node[c + i];
+          if (row >= 0)
+            a.out[((int64_t)cu.s * a.N * a.H + row) * kHeadDim + dim] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        } else {
+          rec[(c0 + c + i) * 128 + dim] = v;
         }
       }
-      fence_before();
-      __syncwarp();
-      if (sp.np > 0 && lane == 0) mbar_arrive(bar(kOFree));
-    });
+    }
+    fence_before();
+  }
+  // After a time-out copies and MMAs may be under way: none is when the CTA ends.
+  if (*s_abort) {
+    if (tid == kLoader) {
+      for (int i = max(0, ki - KS); i < ki; ++i)
+        for (int j = 0; j < kWaits && !mbar_spin(bar(kKFull + i % KS), (i / KS) & 1); ++j) {}
+      for (int i = max(0, vi - VS); i < vi; ++i)
+        for (int j = 0; j < kWaits && !mbar_spin(bar(kVFull + i % VS), (i / VS) & 1); ++j) {}
+    }
+    if (tid == 0) {  // a commit follows all MMAs issued so far
+      const uint32_t b = smem_addr(s_scan);
+      mbar_init(b, 1);
+      fence_barrier_init();
+      commit(b);
+      for (int j = 0; j < kWaits && !mbar_spin(b, 0); ++j) {}
+    }
   }
   fence_before();
   __syncthreads();
@@ -1138,12 +1038,6 @@ cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
   auto kern = tree_kernel<C>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // a block that was launched with fewer registers than its roles take would wait for them
-  static const int regs = [kern] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
-  }();
-  if (regs * C::kThreads < C::kRegs) return cudaErrorInvalidConfiguration;
   const int grid = num_sms * C::CTAS;
   a.tiles = (a.N * a.G + C::NR - 1) / C::NR;
   a.meta = reinterpret_cast<int32_t*>(a.rec + (int64_t)grid * 2 * C::NR * 130);
@@ -1158,7 +1052,7 @@ cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
     a.seq_lens += b0;
     if (a.n_nodes) a.n_nodes += b0;
     if (a.mask) a.mask += b0 * a.N;
-    e = launch_pdl(kern, dim3(grid), dim3(C::kThreads), smem, stream, a);
+    e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, a);
     if (e != cudaSuccess) return e;
     e = launch_pdl(tree_merge_kernel<C::NR>, dim3(grid, C::NR / 4), dim3(128), 0, stream, a);
     if (e != cudaSuccess) return e;
@@ -1168,10 +1062,10 @@ cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
 
 // Rows a tile: the smallest that holds all of a sequence's rows of one KV head, else the
 // largest.
-//               NR SG DW KS VS VB CTAs registers
-using C16 = Cfg<16, 1, 8, 2, 3, 1, 2, 40, 104, 56>;
-using C32 = Cfg<32, 2, 8, 4, 4, 2, 1, 48, 144, 72>;
-using C64 = Cfg<64, 2, 8, 3, 3, 2, 1, 48, 144, 72>;
+//               NR KS VS CTAs
+using C16 = Cfg<16, 2, 2, 2>;
+using C32 = Cfg<32, 2, 2, 2>;
+using C64 = Cfg<64, 2, 1, 2>;
 inline int rows_of(int N, int H, int Hkv) {
   const int rows = N * (H / Hkv);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
