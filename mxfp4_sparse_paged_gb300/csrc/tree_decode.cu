@@ -30,13 +30,13 @@
 // CTA.  A tile cut by a range's end leaves a partial record (O, reference, sum) in the
 // workspace, and a second kernel joins the records of each cut tile.
 //
-// One CTA of 8 warps goes through its pages in order, every warp doing the same: softmax of
-// page k (two groups of four warps, each half of the rows; one lane a token), a sixteenth of
-// V's dequantisation, one barrier.  Copies and MMAs are asynchronous, each issued by one
-// thread: K and V of the pages to come, S of page k + 1 as soon as S of page k is in registers,
-// P V of page k after the barrier; two CTAs an SM fill each other's waits.  (Warps of fixed
-// roles handing pages to each other by barriers, 12 to 20 a CTA, took 217 to 304 us and 1120 us
-// on the first and last cases named below: each hand-over cost a few hundred cycles.)
+// A CTA goes through its pages in order, eight warps doing the same: a sixteenth of V's
+// dequantisation each half warp, then the softmax (two groups of four warps, each half of the
+// rows; one lane a token), one barrier a page.  A ninth warp issues all that is asynchronous:
+// P V of the page before, S of the page ahead (two accumulators), copies of the pages to come.
+// Two CTAs an SM fill each other's waits.  (Warps of fixed roles handing pages to each other by
+// barriers, 12 to 20 a CTA, took two to three times as long: each hand-over cost a few hundred
+// cycles.)
 // All waits are bounded; after one that runs out the CTA goes through its loop without waiting
 // or issuing, and the status word says so.
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
@@ -54,7 +54,8 @@ constexpr int kMaxSeq = 256;       // sequences per launch
 constexpr float kLazy = 12.f;      // log2 units a logit may lie above its row's reference
 constexpr float kUnset = -3e38f;   // the reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 256;
+constexpr int kWorkers = 256;            // the eight warps that compute
+constexpr int kThreads = kWorkers + 32;  // and the one that issues
 constexpr int kKTile = 128 * 128;  // K operand tile
 // V operand: rows of 64 dims (128 bytes) a token, in 128-byte swizzle atoms of 8 tokens (the
 // 16-byte chunks of row r XOR-permuted by r % 8), 16 atoms, then the other 64 dims.
@@ -120,11 +121,12 @@ struct Lay {
   static constexpr int kCnt = kLen + kMaxSeq * 4;            // [kMaxSeq] u8
   static constexpr int kOff = kCnt + kMaxSeq;                // [4] i64: page offsets of loads
   static constexpr int kBar = kOff + 4 * 8;
-  static constexpr int kBars = C::KS + C::VS + 2;
+  static constexpr int kBars = C::KS + C::VS + 3;
   static constexpr int kStart = kBar + kBars * 8;            // where the range begins
   static constexpr int kInfo = kStart + 24;                  // [4] valid tokens of loaded pages
-  static constexpr int kMisc = kInfo + 16;                   // abort, tmem address, scan space
-  static constexpr int kBytes = kMisc + 8 + 8 * 4 + 1024;    // + slack for the 1024-byte alignment
+  static constexpr int kMore = kInfo + 16;                   // [3] a page asks for new references
+  static constexpr int kMisc = kMore + 16;                   // abort, tmem address, scan space
+  static constexpr int kBytes = kMisc + 8 + 10 * 4 + 1024;    // + slack for the 1024-byte alignment
   static_assert(kV % 1024 == 0 && kVraw % 16 == 0 && kRef % 16 == 0 && kMask % 8 == 0 &&
                 kOff % 8 == 0, "alignment");
   static_assert(C::CTAS * (kBytes + 1024) <= 228 * 1024, "shared memory");
@@ -132,10 +134,10 @@ struct Lay {
 
 template <class C>
 struct Tm {  // tensor-memory columns
-  static constexpr int kS = 0;
-  static constexpr int kO = C::kScols;
-  static constexpr int kSfa = kO + C::NR;         // (scale fields start at multiples of 4)
-  static constexpr int kSfb = kSfa + 4;           // hi, lo
+  static constexpr int kS = 0;                    // two S buffers
+  static constexpr int kO = 2 * C::kScols;
+  static constexpr int kSfa = kO + C::NR;         // two sets (scale fields start at multiples of 4)
+  static constexpr int kSfb = kSfa + 8;           // hi, lo
   static constexpr int kSfbRows = C::kTwin ? 2 * C::NR : C::NR;  // rows of one operand
   static constexpr int kSfbW = (kSfbRows + 31) / 32;             // 32 rows a column
   static constexpr int kUsed = kSfb + (C::kTwin ? 4 : 8);
@@ -321,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
   using T_ = Tm<C>;
   constexpr int NR = C::NR, NC = C::NC, KS = C::KS, VS = C::VS, W = NC < 16 ? NC : 16;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
-  uint8_t* const sm = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
+  // (by an offset, not by rounding the pointer: it stays a pointer to shared memory)
+  uint8_t* const sm = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
   const uint32_t sb = smem_addr(sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t* const s_pref = reinterpret_cast<uint32_t*>(sm + L_::kPref);
@@ -335,11 +337,13 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
   uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(sm + L_::kMisc + 4);
   uint32_t* const s_scan = reinterpret_cast<uint32_t*>(sm + L_::kMisc + 8);
   auto bar = [&](int i) { return sb + L_::kBar + 8u * i; };
-  constexpr int kKFull = 0, kVFull = KS, kSFull = KS + VS, kPvDone = kSFull + 1;
+  volatile int* const s_more = reinterpret_cast<volatile int*>(sm + L_::kMore);
+  constexpr int kKFull = 0, kVFull = KS, kSFull = KS + VS, kPvDone = kSFull + 2;
 
   if (tid == 0) {
     for (int i = 0; i < L_::kBars; ++i) mbar_init(bar(i), 1);
     *s_abort = 0;
+    s_more[0] = s_more[1] = s_more[2] = 0;
     fence_barrier_init();
   }
   // The kernel in front may hold tensor memory that this one would wait for: its end first.
@@ -430,6 +434,9 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     return false;
   };
 
+  // (the two branches below pass the same barriers in the same order)
+  auto sync_all = []() { asm volatile("bar.sync 1, %0;\n" ::"n"(kThreads) : "memory"); };
+
   // A place in the list of tiles, and the pages [e0, e1) of the tile in this CTA's range.
   struct Cursor {
     int64_t left;  // pages of the range from e0 on
@@ -461,10 +468,11 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
   };
   auto page_no = [](const Span& sp, int e) { return e < sp.ns ? e : sp.first + (e - sp.ns); };
 
+  if (tid >= kWorkers) {
+  // ================= the issuing warp (one lane; all keep step with the barriers)
   // ---- loads, by one thread: page ki of the range is the next K to load, vi the next V.
   // The table entry of page ki is read a page ahead.  A page's offset and its number of valid
   // tokens (0: a bad page, not loaded) are left for V's load and the softmax.
-  constexpr int kLoader = 128;
   Cursor lc = begin();
   int ki = 0, vi = 0, le = lc.e0, lpid = -1;
   auto look = [&]() {  // the next page that there is
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     }
     ++vi;
   };
-  if (tid == kLoader) {
+  if (lane == 0) {
     look();
     for (int i = 0; i < KS; ++i) load_k();
     for (int i = 0; i < VS; ++i) load_v();
@@ -521,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
   // S^T = K q^T of page k (K landed: kKFull), fence_after() before
   auto issue_s = [&](int k) {
     const int st = k % KS;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(tm + T_::kSfa),
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(tm + T_::kSfa + 4 * (k & 1)),
                  "l"(desc(sb + L_::kKsc + st * 512, 16, 128))
                  : "memory");
     const uint64_t ad = desc(sb + L_::kK + st * kKTile, 16, 1024) | ((uint64_t)2 << 61);
@@ -533,12 +541,12 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
         asm volatile(
             "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
             " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, "
-            "%2, %3, [%4], [%5], p;\n}\n" ::"r"(tm + T_::kS),
+            "%2, %3, [%4], [%5], p;\n}\n" ::"r"(tm + T_::kS + (k & 1) * C::kScols),
             "l"(ad + kb * (32 >> 4)), "l"(bd + ((part * NR * 128 + kb * 256) >> 4)),
-            "r"(idesc_s<T_::kSfbRows>(kb)), "r"(tm + T_::kSfa), "r"(tm + T_::kSfb + part * 4),
+            "r"(idesc_s<T_::kSfbRows>(kb)), "r"(tm + T_::kSfa + 4 * (k & 1)), "r"(tm + T_::kSfb + part * 4),
             "r"(part + kb)
             : "memory");
-    commit(bar(kSFull));
+    commit(bar(kSFull + (k & 1)));
   };
   // O^T (+)= V^T P^T
   auto issue_pv = [&](bool first) {
@@ -555,6 +563,63 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     commit(bar(kPvDone));
   };
 
+
+  int k = 0;  // pages done
+  for (Cursor cu = begin(); cu.left > 0; advance(cu)) {
+    sync_all();  // the tile before is written out
+    sync_all();  // rows and q are ready
+    if (cu.sp.np > 0) {
+      sync_all();  // q's scales are in tensor memory
+      int ahead = k - 1;  // S of the pages up to here has been issued
+#pragma unroll 1
+      for (int e = cu.e0; e < cu.e1; ++e, ++k) {
+        if (lane == 0) {
+          if (!*s_abort) {
+            fence_after();
+            if (e > cu.e0) {
+              issue_pv(e - 1 == cu.e0);
+              load_v();  // (page k - 1's V has been read)
+            }
+            if (ahead < k && wait(kKFull + k % KS, (k / KS) & 1)) issue_s(ahead = k);
+            wait(kSFull + (k & 1), (k >> 1) & 1);
+            load_k();  // (page k's K has been read)
+            if (e + 1 < cu.e1 && ahead == k && mbar_test(bar(kKFull + (k + 1) % KS), ((k + 1) / KS) & 1))
+              issue_s(ahead = k + 1);
+          }
+          s_more[(k + 1) % 3] = 0;
+        }
+        __syncwarp();
+        fence_before();
+        sync_all();
+        if (s_more[k % 3]) {
+          sync_all();
+          sync_all();
+          sync_all();
+        }
+      }
+      if (lane == 0 && !*s_abort) {
+        fence_after();
+        issue_pv(cu.e1 - 1 == cu.e0);
+        load_v();
+      }
+      __syncwarp();
+    }
+    sync_all();  // the sums are there
+    sync_all();
+  }
+  // After a time-out copies and MMAs may be under way: none is when the CTA ends.
+  if (*s_abort && lane == 0) {
+    for (int i = max(0, ki - KS); i < ki; ++i)
+      for (int j = 0; j < kWaits && !mbar_spin(bar(kKFull + i % KS), (i / KS) & 1); ++j) {}
+    for (int i = max(0, vi - VS); i < vi; ++i)
+      for (int j = 0; j < kWaits && !mbar_spin(bar(kVFull + i % VS), (i / VS) & 1); ++j) {}
+    const uint32_t b = smem_addr(s_scan);  // a commit follows all MMAs issued so far
+    mbar_init(b, 1);
+    fence_barrier_init();
+    commit(b);
+    for (int j = 0; j < kWaits && !mbar_spin(b, 0); ++j) {}
+  }
+  } else {
   // ---- the softmax group's rows c0 .. c0 + NC - 1 of a tile
   const int w = warp & 3, t = tid & 127, c0 = (warp >> 2) * NC;
   const uint32_t tl = tm + ((uint32_t)(32 * w) << 16);
@@ -574,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
   for (Cursor cu = begin(); cu.left > 0; advance(cu)) {
     const Span sp = cu.sp;
     const bool begins = cu.e0 == 0, ends = cu.e1 >= sp.np;
-    __syncthreads();  // the tile before is written out
+    sync_all();  // the tile before is written out
     // ---- the tile's rows
     if (t < NC) {
       const int row = cu.rt * NR + c0 + t, node = row / a.G;
@@ -607,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     // its largest magnitude
     if (sp.np > 0) {
 #pragma unroll 1
-      for (int n = tid >> 3; n < NR; n += kThreads / 8) {
+      for (int n = tid >> 3; n < NR; n += kWorkers / 8) {
         const int j = tid & 7, row = cu.rt * NR + n, node = row / a.G;
         uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
         if (node < sp.n) {
@@ -659,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
       }
       fence_async();
     }
-    __syncthreads();
+    sync_all();
     float l[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) l[c] = 0.f;
@@ -676,21 +741,58 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
         wait_st();
       }
       fence_before();
-      __syncthreads();
-      if (tid == 0) {
-        wait(kKFull + k % KS, (k / KS) & 1);
-        if (!*s_abort) {
-          fence_after();
-          issue_s(k);
-        }
-      }
+      sync_all();
 #pragma unroll 1
       for (int e = cu.e0; e < cu.e1; ++e, ++k) {
-        // ---- logits in log2 units relative to the rows' references
-        const int first = page_no(sp, e) * kPageTokens, live = s_info[k & 3];
+                const int first = page_no(sp, e) * kPageTokens, live = s_info[k & 3];
         const bool plain = live == kPageTokens && first + kPageTokens <= sp.base &&
                            (a.window == 0 || first > sp.base + 63 - a.window ||
                             first + kPageTokens <= a.sinks);
+        // ---- V.  Operand row (K index) m holds token 4 (m % 32) + m / 32, the order in which
+        // the tensor copy lays out K.  A warp's step: 8 operand rows (r8), lane >> 3 choosing
+        // which 32-dim block of each: 16 raw bytes a lane, four 16-byte stores without bank
+        // conflicts.
+        wait(kVFull + k % VS, (k / VS) & 1);
+        const uint8_t* raw = sm + L_::kVraw + (k % VS) * kPageBytes;
+        // NaN dim blocks of this lane's token
+        uint32_t vw = *reinterpret_cast<const uint32_t*>(raw + kScaleOffset + tok * kRowScaleBytes);
+        vw = ((vw & 0x7F7F7F7Fu) + 0x01010101u) & vw & 0x80808080u;
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+          const int m = (warp * 2 + it) * 8 + r8, tk = 4 * (m & 31) + (m >> 5);
+          const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tk * kRowDataBytes + blk * 16);
+          const uint32_t sc = raw[kScaleOffset + tk * kRowScaleBytes + blk];
+          // 2^(sc - 1), as two factors where it passes bf16's range
+          const uint32_t f1 = (tk < live && sc != 255u ? min(sc + 126u, 254u) : 0u) * 0x00800080u;
+          const bool big = __any_sync(0xFFFFFFFFu, sc > 128u);
+          const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+          uint32_t y[4][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t v = cw[j];
+            // codes i and i + 4 of the word as one pair
+            y[j][0] = ((v << 12) & 0x80008000u) | ((v << 6) & 0x01C001C0u);
+            y[j][1] = ((v << 8) & 0x80008000u) | ((v << 2) & 0x01C001C0u);
+            y[j][2] = ((v << 4) & 0x80008000u) | ((v >> 2) & 0x01C001C0u);
+            y[j][3] = (v & 0x80008000u) | ((v >> 6) & 0x01C001C0u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f1);
+          }
+          if (big) {
+            const uint32_t f2 = (sc > 128u ? sc - 1u : 127u) * 0x00800080u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f2);
+          }
+          if (it == 0 && k > 0) wait(kPvDone, (k - 1) & 1);  // the operands' buffers are free
+          uint8_t* const dst = sm + L_::kV + (blk >> 1) * kVHalf + (m >> 3) * 1024 + r8 * 128;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(dst + ((((blk & 1) * 4 + j) ^ r8) << 4)) =
+                make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
+        }
+        // ---- logits in log2 units relative to the rows' references
         // a row sees a draft by its mask, an earlier token from the window's first on; rows
         // without a node see what they like, their results are zeroed
         uint32_t vis = ~0u;
@@ -706,19 +808,23 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
             }
           }
         }
-        wait(kSFull, k & 1);
+        if (vw != 0u && tok < live) {  // the rows that see the token get its NaNs at the end
+#pragma unroll 1
+          for (int c = 0; c < NC; ++c)
+            if ((vis >> c) & 1u) atomicOr(s_nan + c, vw);
+        }
+        wait(kSFull + (k & 1), (k >> 1) & 1);
         fence_after();
-        float x[NC];
-        const uint32_t ts = tl + T_::kS + c0;
+        const uint32_t ts = tl + T_::kS + (k & 1) * C::kScols + c0;
         // S of W rows, hi and lo parts added where they are apart
         auto s_of = [&](int c, float* v) {
           ldw<W>(ts + c, v);
           if constexpr (C::kTwin) {
-            float y[W];
-            ldw<W>(ts + NR + c, y);
+            float z[W];
+            ldw<W>(ts + NR + c, z);
             wait_ld();
 #pragma unroll
-            for (int i = 0; i < W; ++i) v[i] += y[i];
+            for (int i = 0; i < W; ++i) v[i] += z[i];
           } else {
             wait_ld();
           }
@@ -730,8 +836,10 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < W; ++i) v[i] = (vb >> i) & 1u ? v[i] : -INFINITY;
         };
-        bool moved = false;  // new references were set on this page
-        for (;; moved = true) {
+        // the weights of the page: into the P operand, and their row sums' parts in x
+        float x[NC];
+        uint8_t* const pd = sm + L_::kP + (c0 >> 3) * kChunk + (4 * w + (lane >> 3)) * 128 + (lane & 7) * 16;
+        for (bool moved = false;; moved = true) {
           float top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < NC; c += W) {
@@ -753,11 +861,24 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
 #pragma unroll
               for (int i = 0; i < o; ++i) m[i] = fmaxf(m[i], m[i + o]);
             top = fmaxf(top, m[0]);
+#pragma unroll
+            for (int i = c; i < c + W; ++i) x[i] = ex2(x[i]);
+#pragma unroll
+            for (int i = c; i < c + W; i += 8)
+              *reinterpret_cast<uint4*>(pd + (i >> 3) * kChunk) =
+                  make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]),
+                             pack_bf16(x[i + 4], x[i + 5]), pack_bf16(x[i + 6], x[i + 7]));
           }
+          if (__any_sync(0xFFFFFFFFu, top > kLazy) && !moved && lane == 0) s_more[k % 3] = 1;
+          fence_async();
           fence_before();
-          if (moved || !__syncthreads_or(top > kLazy)) break;
-          // new references: the page's maximum of each row that has a larger one; what was
-          // summed so far is brought to them, and the page's logits are taken once more
+          sync_all();
+          if (moved || !s_more[k % 3]) break;
+          // New references: the page's maximum of each row that has a larger one; what was
+          // summed so far is brought to them, and the page's weights are taken once more.  (The
+          // page's product waits for the third barrier from here; that of the page before is
+          // done, its buffers were free above.)
+          fence_after();
 #pragma unroll 1
           for (int c = 0; c < NC; c += W) {
             float v[W];
@@ -768,8 +889,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
             const float mx = columns<W>(v, lane, [](float p, float q) { return fmaxf(p, q); });
             if (lane < W) s_warp[w * NC + c + lane] = mx;
           }
-          if (e > cu.e0) wait(kPvDone, (k - 1) & 1);
-          __syncthreads();
+          sync_all();
           if (t < NC) {
             const float v = fmaxf(fmaxf(s_warp[t], s_warp[NC + t]),
                                   fmaxf(s_warp[2 * NC + t], s_warp[3 * NC + t]));
@@ -777,11 +897,10 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
             s_fac[t] = old == kUnset ? 0.f : ex2(old - now);
             s_nref[t] = -now;
           }
-          __syncthreads();
+          sync_all();
 #pragma unroll
           for (int c = 0; c < NC; ++c) l[c] *= s_fac[c];
           if (e > cu.e0) {
-            fence_after();
 #pragma unroll 1
             for (int c = 0; c < NC; c += W) {
               float o[W];
@@ -794,87 +913,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
             wait_st();
           }
         }
-        // S is in registers everywhere (the vote's barrier): the next page's may replace it, if
-        // its K is there
-        bool ahead = false;
-        if (tid == 0 && !moved && e + 1 < cu.e1 && !*s_abort &&
-            mbar_test(bar(kKFull + (k + 1) % KS), ((k + 1) / KS) & 1)) {
-          fence_after();
-          issue_s(k + 1);
-          ahead = true;
-        }
-        // ---- weights
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          x[c] = ex2(x[c]);
-          l[c] += x[c];
-        }
-        if (k > 0) wait(kPvDone, (k - 1) & 1);  // the operands' buffers are free
-        uint8_t* const pd = sm + L_::kP + (c0 >> 3) * kChunk + (4 * w + (lane >> 3)) * 128 + (lane & 7) * 16;
-#pragma unroll
-        for (int c = 0; c < NC; c += 8)
-          *reinterpret_cast<uint4*>(pd + (c >> 3) * kChunk) =
-              make_uint4(pack_bf16(x[c], x[c + 1]), pack_bf16(x[c + 2], x[c + 3]),
-                         pack_bf16(x[c + 4], x[c + 5]), pack_bf16(x[c + 6], x[c + 7]));
-        // ---- V.  Operand row (K index) m holds token 4 (m % 32) + m / 32, the order in which
-        // the tensor copy lays out K.  A warp's step: 8 operand rows (r8), lane >> 3 choosing
-        // which 32-dim block of each: 16 raw bytes a lane, four 16-byte stores without bank
-        // conflicts.
-        wait(kVFull + k % VS, (k / VS) & 1);
-        const uint8_t* raw = sm + L_::kVraw + (k % VS) * kPageBytes;
-#pragma unroll
-        for (int it = 0; it < 2; ++it) {
-          const int m = (warp * 2 + it) * 8 + r8, tk = 4 * (m & 31) + (m >> 5);
-          const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tk * kRowDataBytes + blk * 16);
-          const uint32_t sc = raw[kScaleOffset + tk * kRowScaleBytes + blk];
-          // 2^(sc - 1), as two factors where it passes bf16's range
-          const uint32_t f1 = ((tk < live && sc != 255u ? min(sc + 126u, 254u) : 0u) << 7) * 0x10001u;
-          const bool big = __any_sync(0xFFFFFFFFu, sc > 128u);
-          const uint32_t f2 = ((sc > 128u ? sc - 1u : 127u) << 7) * 0x10001u;
-          uint8_t* const dst = sm + L_::kV + (blk >> 1) * kVHalf + (m >> 3) * 1024 + r8 * 128;
-          const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t v = cw[j];
-            // codes i and i + 4 of the word as one pair
-            uint32_t y[4];
-            y[0] = ((v << 12) & 0x80008000u) | ((v << 6) & 0x01C001C0u);
-            y[1] = ((v << 8) & 0x80008000u) | ((v << 2) & 0x01C001C0u);
-            y[2] = ((v << 4) & 0x80008000u) | ((v >> 2) & 0x01C001C0u);
-            y[3] = (v & 0x80008000u) | ((v >> 6) & 0x01C001C0u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = bf16_mul2(y[i], f1);
-            if (big) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) y[i] = bf16_mul2(y[i], f2);
-            }
-            *reinterpret_cast<uint4*>(dst + ((((blk & 1) * 4 + j) ^ r8) << 4)) =
-                make_uint4(y[0], y[1], y[2], y[3]);
-          }
-        }
-        // NaN dim blocks of this lane's token: the rows that see it get them at the end
-        uint32_t vw = *reinterpret_cast<const uint32_t*>(raw + kScaleOffset + tok * kRowScaleBytes);
-        vw = ((vw & 0x7F7F7F7Fu) + 0x01010101u) & vw & 0x80808080u;
-        if (vw != 0u && tok < live) {
-#pragma unroll 1
-          for (int c = 0; c < NC; ++c)
-            if ((vis >> c) & 1u) atomicOr(s_nan + c, vw);
-        }
-        fence_async();
-        fence_before();
-        __syncthreads();
-        if (tid == 0 && !*s_abort) {
-          fence_after();
-          issue_pv(e == cu.e0);
-          if (!ahead && e + 1 < cu.e1 && wait(kKFull + (k + 1) % KS, ((k + 1) / KS) & 1)) {
-            fence_after();
-            issue_s(k + 1);
-          }
-        }
-        if (tid == kLoader) {  // S of page k is done with its K, everyone with its V
-          load_k();
-          load_v();
-        }
+        for (int c = 0; c < NC; ++c) l[c] += x[c];
       }
 #pragma unroll
       for (int c = 0; c < NC; c += W) {
@@ -885,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     } else {
       for (int c = t; c < 4 * NC; c += 128) s_warp[c] = 0.f;
     }
-    __syncthreads();
+    sync_all();
     // ---- the tile's result: this lane's dim of every row
     const bool whole = begins && ends;
     float* const rec = a.rec + (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * (int64_t)(NR * 130);
@@ -904,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
         rec[NR * 129 + c0 + t] = sum;
       }
     }
-    __syncthreads();
+    sync_all();
     fence_after();
     // operand position -> dim: the codes of a word were paired i, i + 4
     const int dim = 32 * w + (lane & 24) + ((lane & 1) << 2) + ((lane & 7) >> 1);
@@ -932,21 +972,6 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     }
     fence_before();
   }
-  // After a time-out copies and MMAs may be under way: none is when the CTA ends.
-  if (*s_abort) {
-    if (tid == kLoader) {
-      for (int i = max(0, ki - KS); i < ki; ++i)
-        for (int j = 0; j < kWaits && !mbar_spin(bar(kKFull + i % KS), (i / KS) & 1); ++j) {}
-      for (int i = max(0, vi - VS); i < vi; ++i)
-        for (int j = 0; j < kWaits && !mbar_spin(bar(kVFull + i % VS), (i / VS) & 1); ++j) {}
-    }
-    if (tid == 0) {  // a commit follows all MMAs issued so far
-      const uint32_t b = smem_addr(s_scan);
-      mbar_init(b, 1);
-      fence_barrier_init();
-      commit(b);
-      for (int j = 0; j < kWaits && !mbar_spin(b, 0); ++j) {}
-    }
   }
   fence_before();
   __syncthreads();
