@@ -32,8 +32,8 @@
 //
 // A CTA goes through its pages in order, eight warps doing the same: a sixteenth of V's
 // dequantisation each half warp, then the softmax (two groups of four warps, each half of the
-// rows; one lane a token), one barrier a page.  A ninth warp issues all that is asynchronous:
-// P V of the page before, S of the page ahead (two accumulators), copies of the pages to come.
+// rows; one lane a token), one barrier a page.  Two more warps issue what is asynchronous: one
+// the products (P V of the page before, S of the page ahead, two accumulators), one the copies.
 // Two CTAs an SM fill each other's waits.  (Warps of fixed roles handing pages to each other by
 // barriers, 12 to 20 a CTA, took two to three times as long: each hand-over cost a few hundred
 // cycles.)
@@ -55,7 +55,7 @@ constexpr float kLazy = 12.f;      // log2 units a logit may lie above its row's
 constexpr float kUnset = -3e38f;   // the reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWorkers = 256;            // the eight warps that compute
-constexpr int kThreads = kWorkers + 32;  // and the one that issues
+constexpr int kThreads = kWorkers + 64;  // one that issues the products, one the copies
 constexpr int kKTile = 128 * 128;  // K operand tile
 // V operand: rows of 64 dims (128 bytes) a token, in 128-byte swizzle atoms of 8 tokens (the
 // 16-byte chunks of row r XOR-permuted by r % 8), 16 atoms, then the other 64 dims.
@@ -126,7 +126,7 @@ struct Lay {
   static constexpr int kInfo = kStart + 24;                  // [4] valid tokens of loaded pages
   static constexpr int kMore = kInfo + 16;                   // [3] a page asks for new references
   static constexpr int kMisc = kMore + 16;                   // abort, tmem address, scan space
-  static constexpr int kBytes = kMisc + 8 + 10 * 4 + 1024;    // + slack for the 1024-byte alignment
+  static constexpr int kBytes = kMisc + 8 + 12 * 4 + 1024;    // + slack for the 1024-byte alignment
   static_assert(kV % 1024 == 0 && kVraw % 16 == 0 && kRef % 16 == 0 && kMask % 8 == 0 &&
                 kOff % 8 == 0, "alignment");
   static_assert(C::CTAS * (kBytes + 1024) <= 228 * 1024, "shared memory");
@@ -312,7 +312,7 @@ __host__ __device__ __forceinline__ int64_t range_begin(int64_t g, int64_t U, in
 
 // Where a CTA's range begins.
 struct Start {
-  int64_t pages;
+  int pages;
   int s, h, rt, e;
 };
 constexpr int kMinPages = 2;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     int parts = 0;
     if (g < Gd) {
       const int64_t u0 = range_begin(g, U, Gd);
-      x.pages = range_begin(g + 1, U, Gd) - u0;
+      x.pages = (int)min(range_begin(g + 1, U, Gd) - u0, (int64_t)0x7FFFFFFF);
       int lo = 0, hi = a.B - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
 
   // A place in the list of tiles, and the pages [e0, e1) of the tile in this CTA's range.
   struct Cursor {
-    int64_t left;  // pages of the range from e0 on
+    int left;  // pages of the range from e0 on
     int s, h, rt, e0, e1, np;  // np: the tile's places in the list (1 for a tile without pages)
     Span sp;
   };
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     if (c.left <= 0) return;
     c.sp = span_of(s_len[c.s], s_cnt[c.s], a.window, a.sinks);
     c.np = max(1, c.sp.np);
-    c.e1 = (int)min((int64_t)c.np, c.e0 + c.left);
+    c.e1 = c.e0 + min(c.np - c.e0, c.left);
   };
   auto begin = [&]() {
     Cursor c{s_start->pages, s_start->s, s_start->h, s_start->rt, s_start->e, 0, 0, {}};
@@ -468,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
   };
   auto page_no = [](const Span& sp, int e) { return e < sp.ns ? e : sp.first + (e - sp.ns); };
 
-  if (tid >= kWorkers) {
-  // ================= the issuing warp (one lane; all keep step with the barriers)
+  if (warp == kWorkers / 32 + 1) {
+    // ================= the warp of the copies (one lane; all keep step with the barriers)
   // ---- loads, by one thread: page ki of the range is the next K to load, vi the next V.
   // The table entry of page ki is read a page ahead.  A page's offset and its number of valid
   // tokens (0: a bad page, not loaded) are left for V's load and the softmax.
@@ -525,12 +525,51 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     for (int i = 0; i < VS; ++i) load_v();
   }
 
-  // ---- MMAs, by one thread
+  int k = 0;
+  for (Cursor cu = begin(); cu.left > 0; advance(cu)) {
+    sync_all();
+    sync_all();
+    if (cu.sp.np > 0) {
+      sync_all();
+#pragma unroll 1
+      for (int e = cu.e0; e < cu.e1; ++e, ++k) {
+        if (lane == 0) {
+          if (e > cu.e0) load_v();  // (page k - 1's V has been read)
+          wait(kSFull + (k & 1), (k >> 1) & 1);
+          load_k();  // (page k's K has been read)
+          s_more[(k + 1) % 3] = 0;
+        }
+        __syncwarp();
+        sync_all();
+        if (s_more[k % 3]) {
+          sync_all();
+          sync_all();
+          sync_all();
+        }
+      }
+      if (lane == 0) load_v();
+      __syncwarp();
+    }
+    sync_all();
+    sync_all();
+  }
+  // after a time-out copies may be under way: none is when the CTA ends
+  if (*s_abort && lane == 0) {
+    for (int i = max(0, ki - KS); i < ki; ++i)
+      for (int j = 0; j < kWaits && !mbar_spin(bar(kKFull + i % KS), (i / KS) & 1); ++j) {}
+    for (int i = max(0, vi - VS); i < vi; ++i)
+      for (int j = 0; j < kWaits && !mbar_spin(bar(kVFull + i % VS), (i / VS) & 1); ++j) {}
+  }
+  } else if (warp == kWorkers / 32) {
+    // ================= the warp of the products (all lanes go the same way, one issues)
+  uint32_t leader;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(leader));
   // S^T = K q^T of page k (K landed: kKFull), fence_after() before
   auto issue_s = [&](int k) {
     const int st = k % KS;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(tm + T_::kSfa + 4 * (k & 1)),
-                 "l"(desc(sb + L_::kKsc + st * 512, 16, 128))
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+                 " @q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(tm + T_::kSfa + 4 * (k & 1)),
+                 "l"(desc(sb + L_::kKsc + st * 512, 16, 128)), "r"(leader)
                  : "memory");
     const uint64_t ad = desc(sb + L_::kK + st * kKTile, 16, 1024) | ((uint64_t)2 << 61);
     const uint64_t bd = desc(sb + L_::kQ, 128, 1024);
@@ -539,14 +578,14 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
 #pragma unroll
       for (uint32_t kb = 0; kb < 4; ++kb)
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, "
+            "{\n .reg .pred p, q;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 q, %7, 0;\n"
+            " @q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, "
             "%2, %3, [%4], [%5], p;\n}\n" ::"r"(tm + T_::kS + (k & 1) * C::kScols),
             "l"(ad + kb * (32 >> 4)), "l"(bd + ((part * NR * 128 + kb * 256) >> 4)),
             "r"(idesc_s<T_::kSfbRows>(kb)), "r"(tm + T_::kSfa + 4 * (k & 1)), "r"(tm + T_::kSfb + part * 4),
-            "r"(part + kb)
+            "r"(part + kb), "r"(leader)
             : "memory");
-    commit(bar(kSFull + (k & 1)));
+    if (leader) commit(bar(kSFull + (k & 1)));
   };
   // O^T (+)= V^T P^T
   auto issue_pv = [&](bool first) {
@@ -555,12 +594,12 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
 #pragma unroll
     for (uint32_t ks = 0; ks < 8; ++ks)
       asm volatile(
-          "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-          " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tm + T_::kO),
+          "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+          " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tm + T_::kO),
           "l"(ad + ks * (2048 >> 4)), "l"(bd + ks * (256 >> 4)), "r"(idesc_o<NR>()),
-          "r"((uint32_t)(ks > 0 || !first))
+          "r"((uint32_t)(ks > 0 || !first)), "r"(leader)
           : "memory");
-    commit(bar(kPvDone));
+    if (leader) commit(bar(kPvDone));
   };
 
 
@@ -573,22 +612,16 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
       int ahead = k - 1;  // S of the pages up to here has been issued
 #pragma unroll 1
       for (int e = cu.e0; e < cu.e1; ++e, ++k) {
-        if (lane == 0) {
-          if (!*s_abort) {
-            fence_after();
-            if (e > cu.e0) {
-              issue_pv(e - 1 == cu.e0);
-              load_v();  // (page k - 1's V has been read)
-            }
-            if (ahead < k && wait(kKFull + k % KS, (k / KS) & 1)) issue_s(ahead = k);
-            wait(kSFull + (k & 1), (k >> 1) & 1);
-            load_k();  // (page k's K has been read)
-            if (e + 1 < cu.e1 && ahead == k && mbar_test(bar(kKFull + (k + 1) % KS), ((k + 1) / KS) & 1))
-              issue_s(ahead = k + 1);
-          }
-          s_more[(k + 1) % 3] = 0;
+        const bool go = !__any_sync(0xFFFFFFFFu, *s_abort);
+        if (go) {
+          fence_after();
+          if (e > cu.e0) issue_pv(e - 1 == cu.e0);
+          if (ahead < k && __all_sync(0xFFFFFFFFu, wait(kKFull + k % KS, (k / KS) & 1)))
+            issue_s(ahead = k);
+          if (e + 1 < cu.e1 && ahead == k &&
+              __all_sync(0xFFFFFFFFu, mbar_test(bar(kKFull + (k + 1) % KS), ((k + 1) / KS) & 1)))
+            issue_s(ahead = k + 1);
         }
-        __syncwarp();
         fence_before();
         sync_all();
         if (s_more[k % 3]) {
@@ -597,23 +630,17 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
           sync_all();
         }
       }
-      if (lane == 0 && !*s_abort) {
+      if (!__any_sync(0xFFFFFFFFu, *s_abort)) {
         fence_after();
         issue_pv(cu.e1 - 1 == cu.e0);
-        load_v();
       }
-      __syncwarp();
     }
     sync_all();  // the sums are there
     sync_all();
   }
-  // After a time-out copies and MMAs may be under way: none is when the CTA ends.
-  if (*s_abort && lane == 0) {
-    for (int i = max(0, ki - KS); i < ki; ++i)
-      for (int j = 0; j < kWaits && !mbar_spin(bar(kKFull + i % KS), (i / KS) & 1); ++j) {}
-    for (int i = max(0, vi - VS); i < vi; ++i)
-      for (int j = 0; j < kWaits && !mbar_spin(bar(kVFull + i % VS), (i / VS) & 1); ++j) {}
-    const uint32_t b = smem_addr(s_scan);  // a commit follows all MMAs issued so far
+  // after a time-out MMAs may be under way: a commit follows all that were issued
+  if (*s_abort && leader) {
+    const uint32_t b = smem_addr(s_scan);
     mbar_init(b, 1);
     fence_barrier_init();
     commit(b);
@@ -836,40 +863,51 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < W; ++i) v[i] = (vb >> i) & 1u ? v[i] : -INFINITY;
         };
-        // the weights of the page: into the P operand, and their row sums' parts in x
-        float x[NC];
+        // The weights of the page, into the P operand and the row sums, W rows at a time.  Where
+        // a logit lies too far above its reference, those W rows' weights are not summed yet
+        // (owed): the page is taken again with new references.  What was summed is right in
+        // either case, it is brought to the new references with the rest.
+        uint32_t owed = ~0u;
         uint8_t* const pd = sm + L_::kP + (c0 >> 3) * kChunk + (4 * w + (lane >> 3)) * 128 + (lane & 7) * 16;
         for (bool moved = false;; moved = true) {
-          float top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < NC; c += W) {
-            s_of(c, x + c);
+            float x[W];
+            s_of(c, x);
 #pragma unroll
-            for (int i = c; i < c + W; i += 4) {
-              const float4 rf = *reinterpret_cast<const float4*>(s_nref + i);
+            for (int i = 0; i < W; i += 4) {
+              const float4 rf = *reinterpret_cast<const float4*>(s_nref + c + i);
               x[i] = fmaf(x[i], cs, rf.x);
               x[i + 1] = fmaf(x[i + 1], cs, rf.y);
               x[i + 2] = fmaf(x[i + 2], cs, rf.z);
               x[i + 3] = fmaf(x[i + 3], cs, rf.w);
             }
-            hide(c, x + c);
+            hide(c, x);
             float m[W / 2];
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) m[i] = fmaxf(x[c + i], x[c + W / 2 + i]);
+            for (int i = 0; i < W / 2; ++i) m[i] = fmaxf(x[i], x[W / 2 + i]);
 #pragma unroll
             for (int o = W / 4; o > 0; o >>= 1)
 #pragma unroll
               for (int i = 0; i < o; ++i) m[i] = fmaxf(m[i], m[i + o]);
-            top = fmaxf(top, m[0]);
+            const bool far = __any_sync(0xFFFFFFFFu, m[0] > kLazy);
 #pragma unroll
-            for (int i = c; i < c + W; ++i) x[i] = ex2(x[i]);
+            for (int i = 0; i < W; ++i) x[i] = ex2(x[i]);
+            if ((owed >> c) & 1u) {
+              if (far && !moved) {
+                if (lane == 0) s_more[k % 3] = 1;
+              } else {
 #pragma unroll
-            for (int i = c; i < c + W; i += 8)
-              *reinterpret_cast<uint4*>(pd + (i >> 3) * kChunk) =
+                for (int i = 0; i < W; ++i) l[c + i] += x[i];
+                owed &= ~(1u << c);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < W; i += 8)
+              *reinterpret_cast<uint4*>(pd + ((c + i) >> 3) * kChunk) =
                   make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]),
                              pack_bf16(x[i + 4], x[i + 5]), pack_bf16(x[i + 6], x[i + 7]));
           }
-          if (__any_sync(0xFFFFFFFFu, top > kLazy) && !moved && lane == 0) s_more[k % 3] = 1;
           fence_async();
           fence_before();
           sync_all();
@@ -913,8 +951,6 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
             wait_st();
           }
         }
-#pragma unroll
-        for (int c = 0; c < NC; ++c) l[c] += x[c];
       }
 #pragma unroll
       for (int c = 0; c < NC; c += W) {
