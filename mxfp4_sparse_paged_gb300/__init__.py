@@ -56,6 +56,8 @@ def library_path() -> str:
 
 def _load():
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -136,8 +138,11 @@ def _load():
 
 
 def _stream(stream):
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # the current stream, without making an object of it
+        try:
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except RuntimeError:  # no GPU: the arguments' own check says so
+            return None
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -561,20 +566,66 @@ def mx4_decode_steps(n_steps, h_inputs, n_new, d_staging, k_pages, v_pages, idx_
         _stream(stream), _stream(h2d_stream), _stream(d2h_stream)))
 
 
-def tree_paged_decode_workspace(B, N, H, Hkv) -> int:
-    return int(_load().tree_paged_decode_workspace(int(B), int(N), int(H), int(Hkv)))
+# The calls of a speculative step are short: their arguments are checked in one comparison
+# each, and only one that fails it is looked at again for the reason.  A host tensor that is
+# right otherwise becomes a _Host, which no C argument takes: types and shapes come first.
+
+class _Host:
+    def __init__(self, t):
+        self.t = t
+
+
+def _call(fn, *args):
+    try:
+        rc = fn(*args)
+    except ctypes.ArgumentError:
+        for x in args:
+            if isinstance(x, _Host):
+                _ptr(x.t)
+        raise
+    if rc != 0:
+        _check(rc)
+
+
+def _arg(t, dtype, shape, name):
+    """The address of a contiguous CUDA tensor of this type and shape (None sizes match)."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, dtype, name)
+    _dims(t, name, *shape)
+    return _Host(t)
+
+
+def _opt(t, dtype, shape, name):
+    return None if t is None else _arg(t, dtype, shape, name)
 
 
 def _kv_pools(k_pages, v_pages):
-    _pages(k_pages, "k_pages", 3)
-    _pages(v_pages, "v_pages", 3)
-    if k_pages.stride() != v_pages.stride() or k_pages.shape != v_pages.shape:
+    """(K address, V address, page stride, head stride, heads, pages)."""
+    ks = k_pages.shape
+    if not (k_pages.dtype is torch.uint8 and v_pages.dtype is torch.uint8 and len(ks) == 3 and
+            ks[2] == PAGE_BYTES and v_pages.shape == ks):
+        _pages(k_pages, "k_pages", 3)
+        _pages(v_pages, "v_pages", 3)
+        if v_pages.shape != ks:
+            raise ValueError("k_pages and v_pages must have the same shape and strides")
+    st = k_pages.stride()
+    if st[2] != 1 or v_pages.stride() != st:
+        _pages(k_pages, "k_pages", 3)
         raise ValueError("k_pages and v_pages must have the same shape and strides")
+    if not (k_pages.is_cuda and v_pages.is_cuda):
+        return _Host(k_pages if v_pages.is_cuda else v_pages), None, st[0], st[1], ks[1], ks[0]
+    return k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], ks[1], ks[0]
 
 
-def _int32(t, name, *sizes):
-    _need(t, torch.int32, name)
-    _dims(t, name, *sizes)
+def _ws(ws):
+    if ws is None:
+        return None, 0
+    return ws.data_ptr() if ws.is_cuda else _Host(ws), ws.numel() * ws.element_size()
+
+
+def tree_paged_decode_workspace(B, N, H, Hkv) -> int:
+    return int(_load().tree_paged_decode_workspace(int(B), int(N), int(H), int(Hkv)))
 
 
 def tree_paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, out, ws, tree_mask=None,
@@ -585,35 +636,28 @@ def tree_paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, out, ws
     sees node i (None: a chain).  window > 0: only the last `window` positions and the
     first `sinks` tokens.  N = 1 is the single-token decode step.  ws: uint8, at least
     tree_paged_decode_workspace(B, N, H, Hkv) bytes (None when that is 0)."""
-    _need(q, torch.bfloat16, "q")
-    _need(out, torch.bfloat16, "out")
-    _kv_pools(k_pages, v_pages)
+    i32, bf = torch.int32, torch.bfloat16
     _dims(q, "q", None, None, None, HEAD_DIM)
-    B, N, H = (int(x) for x in q.shape[:3])
-    _dims(out, "out", B, N, H, HEAD_DIM)
-    _int32(block_table, "block_table", B, None)
-    _int32(seq_lens, "seq_lens", B)
-    if n_nodes is not None:
-        _int32(n_nodes, "n_nodes", B)
-    if tree_mask is not None:
-        _need(tree_mask, torch.int64, "tree_mask")
-        _dims(tree_mask, "tree_mask", B, N)
-    if lse is not None:
-        _need(lse, torch.float32, "lse")
-        _dims(lse, "lse", B, N, H)
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(_load().tree_paged_decode(
-        _ptr(q), B, N, H, int(k_pages.shape[1]), _ptr(k_pages), _ptr(v_pages), k_pages.stride(0),
-        k_pages.stride(1), int(k_pages.shape[0]), _ptr(block_table), int(block_table.shape[1]),
-        _ptr(seq_lens), _ptr(n_nodes), _ptr(tree_mask), int(window), int(sinks), float(scale),
-        _ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
+    B, N, H, _ = shape = q.shape
+    _dims(block_table, "block_table", B, None)
+    W = block_table.shape[1]
+    args = (_arg(out, bf, shape, "out"), _opt(lse, torch.float32, (B, N, H), "lse"), *_ws(ws))
+    qp = _arg(q, bf, shape, "q")
+    tables = (_arg(block_table, i32, (B, W), "block_table"), W, _arg(seq_lens, i32, (B,), "seq_lens"),
+              _opt(n_nodes, i32, (B,), "n_nodes"), _opt(tree_mask, torch.int64, (B, N), "tree_mask"))
+    kp, vp, ps, hs, Hkv, P = _kv_pools(k_pages, v_pages)
+    _call(_load().tree_paged_decode, qp, B, N, H, Hkv, kp, vp, ps, hs, P, *tables, window, sinks,
+          scale, *args, _stream(stream))
 
 
-def _prob_rows(t, name, B, N, V):
-    _need(t, torch.float32, name, contiguous=False)
-    _dims(t, name, B, N, V)
-    if V > 1 and t.stride(2) != 1:
+def _prob_rows(t, name, shape):
+    if not (t.dtype is torch.float32 and t.shape == shape):
+        _need(t, torch.float32, name, contiguous=False)
+        _dims(t, name, *shape)
+    st = t.stride()
+    if shape[2] > 1 and st[2] != 1:
         raise ValueError(f"{name}: the vocabulary axis must be contiguous")
+    return t.data_ptr() if t.is_cuda else _Host(t), st[0], st[1]
 
 
 def verify_drafts(target, draft, tokens, parents, u_accept, u_sample, path, n_accepted, next_token,
@@ -623,45 +667,31 @@ def verify_drafts(target, draft, tokens, parents, u_accept, u_sample, path, n_ac
     [B], from the target's probabilities fp32 [B, N, V] after each node, the draft's (its
     children were drawn from it; None: drafts that were looked up), tokens and parents
     int32 [B, N] and the random numbers u_accept fp32 [B, N], u_sample fp32 [B]."""
+    i32, f32 = torch.int32, torch.float32
     _dims(target, "target", None, None, None)
-    B, N, V = (int(x) for x in target.shape)
-    _prob_rows(target, "target", B, N, V)
-    if draft is not None:
-        _prob_rows(draft, "draft", B, N, V)
-    _int32(tokens, "tokens", B, N)
-    _int32(parents, "parents", B, N)
-    _need(u_accept, torch.float32, "u_accept")
-    _dims(u_accept, "u_accept", B, N)
-    _need(u_sample, torch.float32, "u_sample")
-    _dims(u_sample, "u_sample", B)
-    _int32(path, "path", B, N)
-    _int32(n_accepted, "n_accepted", B)
-    _int32(next_token, "next_token", B)
-    if n_nodes is not None:
-        _int32(n_nodes, "n_nodes", B)
-    _check(_load().verify_drafts(
-        _ptr(target), target.stride(0), target.stride(1), _ptr(draft),
-        0 if draft is None else draft.stride(0), 0 if draft is None else draft.stride(1),
-        _ptr(tokens), _ptr(parents), _ptr(u_accept), _ptr(u_sample), _ptr(n_nodes), B, N, V,
-        _ptr(path), _ptr(n_accepted), _ptr(next_token), _stream(stream)))
+    B, N, V = shape = target.shape
+    args = (_arg(tokens, i32, (B, N), "tokens"), _arg(parents, i32, (B, N), "parents"),
+            _arg(u_accept, f32, (B, N), "u_accept"), _arg(u_sample, f32, (B,), "u_sample"),
+            _opt(n_nodes, i32, (B,), "n_nodes"), B, N, V, _arg(path, i32, (B, N), "path"),
+            _arg(n_accepted, i32, (B,), "n_accepted"), _arg(next_token, i32, (B,), "next_token"))
+    rows = (*_prob_rows(target, "target", shape),
+            *((None, 0, 0) if draft is None else _prob_rows(draft, "draft", shape)))
+    _call(_load().verify_drafts, *rows, *args, _stream(stream))
 
 
-def _pool_args(k_pages, v_pages, idx_pages):
-    """The pools as the row and page calls take them (index pages MXFP4, fp8 or None)."""
-    _kv_pools(k_pages, v_pages)
-    fp8 = False
-    if idx_pages is not None:
-        fp8 = idx_pages.shape[-1] == FP8_PAGE_BYTES
-        if fp8:
-            _fp8_pages(idx_pages, "idx_pages")
-        else:
-            _pages(idx_pages, "idx_pages", 2)
-        if idx_pages.shape[0] != k_pages.shape[0]:
-            raise ValueError(f"idx_pages has {int(idx_pages.shape[0])} pages, k_pages "
-                             f"{int(k_pages.shape[0])}")
-    return (_ptr(k_pages), _ptr(v_pages), k_pages.stride(0), k_pages.stride(1),
-            int(k_pages.shape[1]), _ptr(idx_pages),
-            0 if idx_pages is None else idx_pages.stride(0), int(fp8), int(k_pages.shape[0]))
+def _idx_pool(idx_pages, P):
+    """Index pages (MXFP4, fp8 or None) as the row and page calls take them."""
+    if idx_pages is None:
+        return None, 0, 0, P
+    fp8 = idx_pages.shape[-1] == FP8_PAGE_BYTES
+    if fp8:
+        _fp8_pages(idx_pages, "idx_pages")
+    else:
+        _pages(idx_pages, "idx_pages", 2)
+    if idx_pages.shape[0] != P:
+        raise ValueError(f"idx_pages has {int(idx_pages.shape[0])} pages, k_pages {P}")
+    return (idx_pages.data_ptr() if idx_pages.is_cuda else _Host(idx_pages), idx_pages.stride(0),
+            int(fp8), P)
 
 
 def mx4_accept_rows(path, n_accepted, seq_lens, block_table, k_pages, v_pages, idx_pages, new_lens,
@@ -669,24 +699,18 @@ def mx4_accept_rows(path, n_accepted, seq_lens, block_table, k_pages, v_pages, i
     """The cache after verify_drafts: the accepted nodes' rows (path int32 [B, N], ascending,
     its first n_accepted[s] entries) become the sequence's first draft rows in every pool
     (idx_pages MXFP4, fp8 or None); new_lens int32 [B] = seq_lens - n_nodes + n_accepted."""
-    _int32(path, "path", None, None)
-    B, N = int(path.shape[0]), int(path.shape[1])
-    _int32(n_accepted, "n_accepted", B)
-    _int32(seq_lens, "seq_lens", B)
-    _int32(block_table, "block_table", B, None)
-    _int32(new_lens, "new_lens", B)
-    if n_nodes is not None:
-        _int32(n_nodes, "n_nodes", B)
-    pools = _pool_args(k_pages, v_pages, idx_pages)
-    _check(_load().mx4_accept_rows(
-        _ptr(path), _ptr(n_accepted), _ptr(seq_lens), _ptr(n_nodes), B, N, _ptr(block_table),
-        int(block_table.shape[1]), *pools, _ptr(new_lens), _stream(stream)))
-
-
-def _free_state(ref_counts, free_list, free_count, P):
-    _int32(ref_counts, "ref_counts", P)
-    _int32(free_list, "free_list", P)
-    _int32(free_count, "free_count", 1)
+    i32 = torch.int32
+    _dims(path, "path", None, None)
+    B, N = path.shape
+    _dims(block_table, "block_table", B, None)
+    W = block_table.shape[1]
+    args = (_arg(path, i32, (B, N), "path"), _arg(n_accepted, i32, (B,), "n_accepted"),
+            _arg(seq_lens, i32, (B,), "seq_lens"), _opt(n_nodes, i32, (B,), "n_nodes"), B, N,
+            _arg(block_table, i32, (B, W), "block_table"), W)
+    new = _arg(new_lens, i32, (B,), "new_lens")
+    idx = _idx_pool(idx_pages, k_pages.shape[0])
+    kv = _kv_pools(k_pages, v_pages)
+    _call(_load().mx4_accept_rows, *args, *kv[:5], *idx, new, _stream(stream))
 
 
 def mx4_fork_pages(rows, block_table, seq_lens, ref_counts, free_list, free_count, k_pages, v_pages,
@@ -694,31 +718,30 @@ def mx4_fork_pages(rows, block_table, seq_lens, ref_counts, free_list, free_coun
     """Children of the table rows rows int32 [n]: child_tables int32 [n, W] shares the full
     pages (ref_counts int32 [P] grows) and gets a copy of a partly filled last page on a
     page off the stack free_list int32 [P], free_count int32 [1]; child_lens int32 [n]."""
-    _int32(rows, "rows", None)
-    n = int(rows.shape[0])
-    _int32(block_table, "block_table", None, None)
-    B, W = int(block_table.shape[0]), int(block_table.shape[1])
-    _int32(seq_lens, "seq_lens", B)
-    _int32(child_tables, "child_tables", n, W)
-    _int32(child_lens, "child_lens", n)
-    _free_state(ref_counts, free_list, free_count, int(k_pages.shape[0]))
-    pools = _pool_args(k_pages, v_pages, idx_pages)
-    _check(_load().mx4_fork_pages(
-        _ptr(rows), n, _ptr(block_table), B, W, _ptr(seq_lens), _ptr(ref_counts), _ptr(free_list),
-        _ptr(free_count), *pools, _ptr(child_tables), _ptr(child_lens), _stream(stream)))
+    i32 = torch.int32
+    _dims(rows, "rows", None)
+    _dims(block_table, "block_table", None, None)
+    n, (B, W), P = rows.shape[0], block_table.shape, k_pages.shape[0]
+    args = (_arg(rows, i32, (n,), "rows"), n, _arg(block_table, i32, (B, W), "block_table"), B, W,
+            _arg(seq_lens, i32, (B,), "seq_lens"), _arg(ref_counts, i32, (P,), "ref_counts"),
+            _arg(free_list, i32, (P,), "free_list"), _arg(free_count, i32, (1,), "free_count"))
+    child = (_arg(child_tables, i32, (n, W), "child_tables"), _arg(child_lens, i32, (n,), "child_lens"))
+    idx = _idx_pool(idx_pages, P)
+    kv = _kv_pools(k_pages, v_pages)
+    _call(_load().mx4_fork_pages, *args, *kv[:5], *idx, *child, _stream(stream))
 
 
 def mx4_free_pages(tables, lens, ref_counts, free_list, free_count, stream=None):
     """The rows of tables int32 [n, W] (lens int32 [n] tokens each) give their pages back:
     a reference less each, and pages without one go on the stack, ascending by id."""
-    _int32(tables, "tables", None, None)
-    n, W = int(tables.shape[0]), int(tables.shape[1])
-    _int32(lens, "lens", n)
-    _int32(ref_counts, "ref_counts", None)
-    P = int(ref_counts.shape[0])
-    _free_state(ref_counts, free_list, free_count, P)
-    _check(_load().mx4_free_pages(_ptr(tables), n, W, _ptr(lens), _ptr(ref_counts), P,
-                                  _ptr(free_list), _ptr(free_count), _stream(stream)))
+    i32 = torch.int32
+    _dims(tables, "tables", None, None)
+    _dims(ref_counts, "ref_counts", None)
+    (n, W), P = tables.shape, ref_counts.shape[0]
+    _call(_load().mx4_free_pages, _arg(tables, i32, (n, W), "tables"), n, W,
+          _arg(lens, i32, (n,), "lens"), _arg(ref_counts, i32, (P,), "ref_counts"), P,
+          _arg(free_list, i32, (P,), "free_list"), _arg(free_count, i32, (1,), "free_count"),
+          _stream(stream))
 
 
 def mx4_check_status(stream=None) -> int:

@@ -29,10 +29,14 @@ namespace mx4 {
 // a hundredth of its fp32 rate; the integer form costs some ten 32-bit operations a
 // value, below what the loads take).
 //
-// One cluster of CTAs per sequence, each CTA one contiguous part of the vocabulary.
-// What the walk looks up (parents, tokens, random numbers, p and q of each draft at its
-// parent) is loaded by all threads at once, so accepted drafts cost no dependent loads;
-// a rejection is one pass over the node's two rows and one exchange in the cluster.
+// One cluster of CTAs per sequence, each CTA one contiguous part of the vocabulary, each warp
+// one of that.  What the walk looks up (parents, tokens, random numbers, p and q of each draft
+// at its parent) is loaded by all threads at once, so accepted drafts cost no dependent loads.
+// At a node's first rejection its rows are read, once: a thread keeps E values of W (and of q)
+// in registers, and every further rejection of a sibling, the sums and the drawing of the
+// next token work on those.  (Reading both rows again for each took 206 us for 64 trees of 32
+// nodes over 131072 tokens, four fifths of it in recomputing W from p.)  E = 0, for
+// vocabularies above 8 x 16384: the rows are read again.
 // Every thread runs the walk itself on the same numbers, so it needs no broadcast.
 constexpr int kMaxNodes = 64;
 constexpr int kVerThreads = 512;
@@ -56,9 +60,13 @@ struct VerifyArgs {
   uint32_t* status;
 };
 
-// A probability in units of 2^-62 (truncated); a NaN or negative value counts as 0.
+// A probability in units of 2^-62 (truncated); a NaN or negative value counts as 0.  By the
+// bits: the 64-bit conversion instruction is as slow here as fp64 is.
 __device__ __forceinline__ uint64_t to_fixed(float x) {
-  return __float2ull_rz(fminf(fmaxf(x, 0.f), 1.9999f) * 0x1p62f);
+  const uint32_t b = __float_as_uint(fminf(fmaxf(x, 0.f), 1.9999f));
+  const uint32_t m = (b & 0x7FFFFFu) | 0x800000u;
+  const int e = (int)(b >> 23) - 88;  // the value is m 2^e
+  return e >= 0 ? (uint64_t)m << e : (uint64_t)(m >> min(-e, 31));
 }
 __device__ __forceinline__ bool prob_ok(float x) { return x >= 0.f && x <= 1.001f; }
 // a * b for a, b in units of 2^-62
@@ -118,7 +126,8 @@ __device__ __forceinline__ uint64_t warp_range_sum(const Residual& R, int v0, in
   return warp_sum(s);
 }
 
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a) {
+template <int E, bool kGiven>
+__global__ void __launch_bounds__(kVerThreads, kGiven || E == 0 || E == 8 ? 2 : 1) verify_kernel(const VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t s = blockIdx.x / C;
@@ -126,9 +135,10 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
   __shared__ int32_t s_par[kMaxNodes], s_tok[kMaxNodes], s_gone[kMaxNodes], s_path[kMaxNodes];
   __shared__ float s_u[kMaxNodes], s_p[kMaxNodes], s_q[kMaxNodes];
   __shared__ uint64_t s_T[kMaxNodes + 1];
-  __shared__ uint64_t s_warp[2][kVerWarps];          // this CTA's warp sums, by pass parity
-  __shared__ uint64_t s_part[2][kVerMaxCluster];     // the cluster's CTA sums, by pass parity
+  __shared__ uint64_t s_warp[3][kVerWarps];       // this CTA's warp sums, three passes' places
+  __shared__ uint64_t s_part[3][kVerMaxCluster];  // the cluster's CTA sums
   __shared__ uint64_t s_sub[kVerWarps];
+  __shared__ bool s_ok[kMaxNodes], s_now;  // a first child's test; the present one's
   pdl_launch_dependents();
   pdl_wait();
 
@@ -146,7 +156,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
     return;
   }
   const float* tgt = a.target + s * a.t_batch;
-  const float* drf = a.draft ? a.draft + s * a.d_batch : nullptr;
+  const float* drf = kGiven ? nullptr : a.draft + s * a.d_batch;
   for (int j = tid; j < n; j += kVerThreads) {
     int par = j == 0 ? -1 : a.parents[s * a.N + j];
     const int tok = a.tokens[s * a.N + j];
@@ -159,124 +169,232 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
     s_path[j] = -1;
     s_u[j] = j > 0 ? a.u_accept[s * a.N + j] : 0.f;
     s_p[j] = par >= 0 ? tgt[par * a.t_node + tok] : 0.f;
-    s_q[j] = par >= 0 ? (drf ? drf[par * a.d_node + tok] : 1.f) : 0.f;
+    s_q[j] = par >= 0 ? (kGiven ? 1.f : drf[par * a.d_node + tok]) : 0.f;
+    s_ok[j] = (double)s_u[j] * (double)s_q[j] < (double)s_p[j];
   }
+  if (tid == 0) s_T[0] = 1ull << 62;
+  if (tid < 3 * kVerMaxCluster) s_part[tid / kVerMaxCluster][tid % kVerMaxCluster] = 0;
   cluster.sync();  // every CTA of the cluster runs: its shared memory may be written
 
   // this CTA's part of the vocabulary, and this warp's part of that
   const int c0 = (int)((int64_t)a.V * rank / C), c1 = (int)((int64_t)a.V * (rank + 1) / C);
   auto warp_begin = [&](int w) { return c0 + (int)((int64_t)(c1 - c0) * w / kVerWarps); };
+  const int v0 = warp_begin(warp), v1 = warp_begin(warp + 1);
   int pass = 0;
   bool bad = false;
-  // one pass over the residual: T, with the warp and CTA sums left in parity `pass`
-  auto total = [&](const Residual& R) {
-    ++pass;
-    const uint64_t ws = warp_range_sum(R, warp_begin(warp), warp_begin(warp + 1), lane, bad);
-    if (lane == 0) s_warp[pass & 1][warp] = ws;
-    __syncthreads();
-    if (warp == 0) {
-      const uint64_t cs = warp_sum(lane < kVerWarps ? s_warp[pass & 1][lane] : 0);
-      if (lane < C) *cluster.map_shared_rank(&s_part[pass & 1][rank], lane) = cs;
+  Residual R{tgt, drf, 0, s_T, s_gone};
+
+  // E > 0: W of value v0 + 32 i + lane (given drafts: p, the rejected tokens zeroed) and q
+  constexpr int E1 = E > 0 ? E : 1;
+  uint64_t W[kGiven ? 1 : E1];
+  float f[E1];
+  bool loaded = false;
+  auto load = [&](bool with_q) {
+    const float* const pr = R.p + v0 + lane;
+    const int left = v1 - v0 - lane;  // values from this lane's first on
+    if constexpr (kGiven) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = 32 * i < left ? __ldg(pr + 32 * i) : 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) bad |= !prob_ok(f[i]);
+    } else {
+      const float* const qr = R.q + v0 + lane;
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = with_q && 32 * i < left ? __ldg(qr + 32 * i) : 0.f;
+      constexpr int kAt = E < 16 ? E1 : 16;  // rows of p in flight with them
+#pragma unroll
+      for (int b = 0; b < E; b += kAt) {
+        float pv[kAt];
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) pv[i] = 32 * (b + i) < left ? __ldg(pr + 32 * (b + i)) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) {
+          bad |= !prob_ok(pv[i]);
+          W[b + i] = to_fixed(pv[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) bad |= !prob_ok(f[i]);
     }
+    loaded = true;
+  };
+  // the sum of the residual, with the warp and CTA sums left in place `pass % 3`
+  auto total = [&]() {
+    ++pass;
+    uint64_t ws = 0;
+    if constexpr (E > 0) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) ws += kGiven ? to_fixed(f[i]) : W[kGiven ? 0 : i];
+      ws = warp_sum(ws);
+    } else {
+      ws = warp_range_sum(R, v0, v1, lane, bad);
+    }
+    // every warp adds its sum to this CTA's place in all the cluster's CTAs (integers: in any
+    // order); the place after the next is cleared a pass ahead, its readers are long through
+    if (lane == 0) s_warp[pass % 3][warp] = ws;
+    if (lane < C)
+      atomicAdd((unsigned long long*)cluster.map_shared_rank(&s_part[pass % 3][rank], lane),
+                (unsigned long long)ws);
+    if (tid < kVerMaxCluster) s_part[(pass + 1) % 3][tid] = 0;
     cluster.sync();
     uint64_t t = 0;
-    for (int i = 0; i < C; ++i) t += s_part[pass & 1][i];
+    for (int i = 0; i < C; ++i) t += s_part[pass % 3][i];
     return t;
   };
 
   int cur = 0, acc = 1;
   bool shut = false, summed = false;  // summed: the last pass is of the current residual
   uint64_t T = 1ull << 62;
-  Residual R{tgt, drf, 0, s_T, s_gone};
   if (tid == 0) s_path[0] = 0;
   for (int j = 1; j < n; ++j) {
     if (s_par[j] != cur || shut) continue;
     const float pv = s_p[j], qv = s_q[j];
-    bool ok;
-    if (R.k == 0) {
-      ok = (double)s_u[j] * (double)qv < (double)pv;
-    } else {
-      const double w = (double)R.of(s_tok[j], pv, qv);
-      ok = (double)s_u[j] * (double)T * (double)qv < w;
+    bool ok = s_ok[j];
+    if (R.k > 0) {
+      if (tid == 0) {
+        const double w = (double)R.of(s_tok[j], pv, qv);
+        s_now = (double)s_u[j] * (double)T * (double)qv < w;
+      }
+      __syncthreads();
+      ok = s_now;
     }
     if (ok) {
       cur = j;
-      R = Residual{tgt + (int64_t)j * a.t_node, drf ? drf + (int64_t)j * a.d_node : nullptr, 0,
+      R = Residual{tgt + (int64_t)j * a.t_node, kGiven ? nullptr : drf + (int64_t)j * a.d_node, 0,
                    s_T, s_gone};
       T = 1ull << 62;
-      summed = false;
+      summed = loaded = false;
       if (tid == 0) s_path[acc] = j;
       ++acc;
       continue;
     }
     // rejected: T (of k rejections) is known; the residual of k + 1
-    __syncthreads();  // the walk above has read s_T and s_gone
-    if (tid == 0) {
-      s_T[R.k] = T;
-      s_gone[R.k] = s_tok[j];
+    if constexpr (E > 0 && kGiven) {
+      // its sum is the row's (the only one that is summed) less what has been rejected
+      if (!loaded) load(false);
+      if (R.k == 0) T = total();
+      T -= R.of(s_tok[j], pv, 1.f);
+      const int at = s_tok[j] - v0 - lane;
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (at == 32 * i && s_tok[j] < v1) f[i] = 0.f;
+      summed = false;
+      __syncthreads();  // the walk above has read s_gone
+      if (tid == 0) s_gone[R.k] = s_tok[j];
+      ++R.k;
+      __syncthreads();
+    } else {
+      if constexpr (E > 0) {
+        if (!loaded) load(true);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const uint64_t qf = to_fixed(f[i]), t = R.k == 0 ? qf : mul_fixed(T, qf);
+          W[kGiven ? 0 : i] = W[kGiven ? 0 : i] > t ? W[kGiven ? 0 : i] - t : 0;
+        }
+      }
+      __syncthreads();  // the walk above has read s_T and s_gone
+      if (tid == 0) {
+        s_T[R.k] = T;
+        s_gone[R.k] = s_tok[j];
+      }
+      ++R.k;
+      __syncthreads();
+      T = total();
+      summed = true;
     }
-    ++R.k;
-    __syncthreads();
-    T = total(R);
-    summed = true;
     if (T == 0) {  // nothing left (p <= q everywhere): draw from p itself
       shut = true;
       R.k = 0;
-      summed = false;
+      summed = loaded = false;
     }
   }
-  if (!summed) T = total(R);
+  if (!summed) {
+    if (E > 0 && !loaded) load(false);
+    T = total();
+  }
 
   // the next token: the first v whose running sum exceeds u T
-  const float us = a.u_sample[s];
-  const uint64_t ui = __double2ull_rz((double)fminf(fmaxf(us, 0.f), 0x1.fffffep-1f) * 0x1p64);
-  uint64_t left = __umul64hi(ui, T);
+  // (u in units of 2^-64: its 24 bits, shifted)
+  const uint32_t ub = __float_as_uint(fminf(fmaxf(a.u_sample[s], 0.f), 0x1.fffffep-1f));
+  const uint64_t um = (ub & 0x7FFFFFu) | 0x800000u;
+  const int ue = (int)(ub >> 23) - 86;
+  const uint64_t ui = ub < 0x00800000u ? 0ull : ue >= 0 ? um << ue : ue > -64 ? um >> -ue : 0ull;
+  const uint64_t left = __umul64hi(ui, T);
   int at = -1;  // the CTA
   uint64_t before = 0;
   for (int i = 0; i < C; ++i) {
-    const uint64_t cs = s_part[pass & 1][i];
+    const uint64_t cs = s_part[pass % 3][i];
     if (at < 0 && before + cs > left) at = i;
     if (at < 0) before += cs;
   }
   if (T == 0) at = -1;  // a row of zeros: no token
+  // the first of 32 values b + lane (value x each) whose running sum exceeds `left`
+  auto pick = [&](int b, bool in, uint64_t x, int& found) {
+    uint64_t inc = in ? x : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, in && before + inc > left);
+    if (hit) found = b + __ffs(hit) - 1;
+    before += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    return hit != 0u;
+  };
   if (at == rank) {
     int w = 0;
     for (; w < kVerWarps - 1; ++w) {
-      const uint64_t x = s_warp[pass & 1][w];
+      const uint64_t x = s_warp[pass % 3][w];
       if (before + x > left) break;
       before += x;
     }
-    // the warp's part in sixteenths, then one warp's sixteenth 32 values at a time
-    const int w0 = warp_begin(w), w1 = warp_begin(w + 1);
-    auto sub = [&](int i) { return w0 + (int)((int64_t)(w1 - w0) * i / kVerWarps); };
-    const uint64_t x = warp_range_sum(R, sub(warp), sub(warp + 1), lane, bad);
-    if (lane == 0) s_sub[warp] = x;
-    __syncthreads();
-    int i = 0;
-    for (; i < kVerWarps - 1; ++i) {
-      if (before + s_sub[i] > left) break;
-      before += s_sub[i];
-    }
-    if (warp == 0) {
-      const bool two = R.q != nullptr && R.k > 0;
-      int found = sub(i + 1) - 1;
-      for (int b = sub(i); b < sub(i + 1); b += 32) {
-        const int v = b + lane;
-        const bool in = v < sub(i + 1);
-        uint64_t inc = in ? R.of(v, R.p[v], two ? R.q[v] : 0.f) : 0;
+    if constexpr (E > 0) {
+      if (warp == w) {
+        int found = v1 - 1;
+        bool done = false;
+        constexpr int kGroup = E < 8 ? E : 8;  // eight rows of 32 at a time, then one
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-          if (lane >= o) inc += y;
+        for (int b = 0; b < E; b += kGroup) {
+          uint64_t x = 0;
+#pragma unroll
+          for (int i = b; i < b + kGroup; ++i) x += kGiven ? to_fixed(f[i]) : W[kGiven ? 0 : i];
+          x = warp_sum(x);
+          if (done) continue;
+          if (before + x <= left) {
+            before += x;
+            continue;
+          }
+#pragma unroll
+          for (int i = b; i < b + kGroup; ++i)
+            if (!done)
+              done = pick(v0 + 32 * i, v0 + 32 * i + lane < v1,
+                          kGiven ? to_fixed(f[i]) : W[kGiven ? 0 : i], found);
+          done = true;
         }
-        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, in && before + inc > left);
-        if (hit) {
-          found = b + __ffs(hit) - 1;
-          break;
-        }
-        before += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        if (lane == 0) a.next_token[s] = found;
       }
-      if (lane == 0) a.next_token[s] = found;
+    } else {
+      // the warp's part in sixteenths, then one warp's sixteenth 32 values at a time
+      const int w0 = warp_begin(w), w1 = warp_begin(w + 1);
+      auto sub = [&](int i) { return w0 + (int)((int64_t)(w1 - w0) * i / kVerWarps); };
+      const uint64_t x = warp_range_sum(R, sub(warp), sub(warp + 1), lane, bad);
+      if (lane == 0) s_sub[warp] = x;
+      __syncthreads();
+      int i = 0;
+      for (; i < kVerWarps - 1; ++i) {
+        if (before + s_sub[i] > left) break;
+        before += s_sub[i];
+      }
+      if (warp == 0) {
+        const bool two = R.q != nullptr && R.k > 0;
+        int found = sub(i + 1) - 1;
+        for (int b = sub(i); b < sub(i + 1); b += 32) {
+          const int v = b + lane;
+          const bool in = v < sub(i + 1);
+          if (pick(b, in, in ? R.of(v, R.p[v], two ? R.q[v] : 0.f) : 0, found)) break;
+        }
+        if (lane == 0) a.next_token[s] = found;
+      }
     }
   }
   if (rank == 0) {
@@ -292,6 +410,12 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
   cluster.sync();  // no CTA leaves while another may still write to its shared memory
 }
 
+template <int E>
+cudaError_t launch_verify_e(const VerifyArgs& a, const cudaLaunchConfig_t& cfg) {
+  return a.draft ? cudaLaunchKernelEx(&cfg, verify_kernel<E, false>, a)
+                 : cudaLaunchKernelEx(&cfg, verify_kernel<E, true>, a);
+}
+
 cudaError_t launch_verify(const float* target, const float* draft, const int64_t* strides,
                           const int32_t* tokens, const int32_t* parents, const float* u_accept,
                           const float* u_sample, const int32_t* n_nodes, int64_t B, int N, int V,
@@ -299,9 +423,12 @@ cudaError_t launch_verify(const float* target, const float* draft, const int64_t
                           uint32_t* status, int num_sms, cudaStream_t stream) {
   VerifyArgs a{target, draft, strides[0], strides[1], strides[2], strides[3], tokens, parents,
                u_accept, u_sample, n_nodes, N, V, path, n_accepted, next_token, status};
-  // CTAs a sequence: about four a SM in all, each with 2048 values or more
-  int C = kVerMaxCluster;
-  while (C > 1 && (B * C > 4 * (int64_t)num_sms || V / C < 2048)) C /= 2;
+  // CTAs a sequence: few (an exchange costs the more), but enough that a thread keeps at most
+  // 32 values, and that a small batch takes about two CTAs an SM of 2048 values or more
+  int C = 1;
+  while (C < kVerMaxCluster &&
+         (V > (int64_t)C * kVerThreads * 32 || (B * C * 2 <= 2 * (int64_t)num_sms && V / C > 4096)))
+    C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * C));
   cfg.blockDim = dim3(kVerThreads);
@@ -314,7 +441,12 @@ cudaError_t launch_verify(const float* target, const float* draft, const int64_t
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, verify_kernel, a);
+  // the largest part of a warp, in rows of 32 values
+  const int part = ((V + C - 1) / C + kVerWarps - 1) / kVerWarps, rows = (part + 31) / 32;
+  if (rows > 32) return launch_verify_e<0>(a, cfg);
+  if (rows > 16) return launch_verify_e<32>(a, cfg);
+  if (rows > 8) return launch_verify_e<16>(a, cfg);
+  return launch_verify_e<8>(a, cfg);
 }
 
 // ---------------------------------------------------------------------------
@@ -550,14 +682,25 @@ fork_copy_kernel(const int32_t* __restrict__ rows, int64_t n, int64_t bt_width,
   bool fp8;
   const uint8_t* from = pools.part(r, sp, fp8);
   uint8_t* to = pools.part(r, dp, fp8);
+  // four 16-byte pieces a thread (all of an MXFP4 part) and its scale word, all loaded before
+  // the first is stored
   const int pieces = rem * (fp8 ? 8 : 4);
-  for (int e = tid; e < pieces; e += kCopyThreads)
-    reinterpret_cast<uint4*>(to)[e] = reinterpret_cast<const uint4*>(from)[e];
-  if (!fp8)
-    for (int e = tid; e < rem; e += kCopyThreads)
-      reinterpret_cast<uint32_t*>(to + kScaleOffset)[e] =
-          reinterpret_cast<const uint32_t*>(from + kScaleOffset)[e];
+  uint32_t sc = 0;
+  if (!fp8 && tid < rem) sc = reinterpret_cast<const uint32_t*>(from + kScaleOffset)[tid];
+  for (int b = 0; b < pieces; b += 4 * kCopyThreads) {
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (b + i * kCopyThreads + tid < pieces)
+        x[i] = reinterpret_cast<const uint4*>(from)[b + i * kCopyThreads + tid];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (b + i * kCopyThreads + tid < pieces)
+        reinterpret_cast<uint4*>(to)[b + i * kCopyThreads + tid] = x[i];
+  }
+  if (!fp8 && tid < rem) reinterpret_cast<uint32_t*>(to + kScaleOffset)[tid] = sc;
 }
+static_assert(kCopyThreads >= kPageTokens, "a thread a scale word");
 
 cudaError_t launch_fork(const int32_t* rows, int64_t n, const int32_t* table, int64_t B,
                         int64_t bt_width, const int32_t* seq_lens, int32_t* refs,
@@ -582,51 +725,78 @@ cudaError_t launch_fork(const int32_t* rows, int64_t n, const int32_t* table, in
 // ids: 4 bytes a page of the pool.
 constexpr int kFreeThreads = 256;
 constexpr int kFreed = -1;
+
+// One reference less for the page of entry j of row s.
+__device__ __forceinline__ void free_entry(const int32_t* __restrict__ table, int64_t s,
+                                           int64_t bt_width, int64_t j, int32_t* refs,
+                                           int64_t num_pages, uint32_t* status) {
+  const int32_t p = table[s * bt_width + j];
+  if (p < 0 || p >= num_pages) {
+    flag(status, MX4_STATUS_BAD_PAGE);
+    return;
+  }
+  int32_t c = *reinterpret_cast<volatile int32_t*>(refs + p);
+  for (;;) {  // ends: every failed exchange is another thread's success
+    if (c <= 0) {  // a page that nobody holds (or that this call has already freed)
+      flag(status, MX4_STATUS_BAD_REF);
+      return;
+    }
+    const int32_t seen = atomicCAS(refs + p, c, c == 1 ? kFreed : c - 1);
+    if (seen == c) return;
+    c = seen;
+  }
+}
+
+// The pages of row s, or -1 for a bad length.
+__device__ __forceinline__ int64_t free_pages_of(const int32_t* __restrict__ lens, int64_t s,
+                                                 int64_t bt_width) {
+  const int64_t L = lens[s];
+  return L < 0 || L > bt_width * kPageTokens ? -1 : (L + kPageTokens - 1) / kPageTokens;
+}
+
 __global__ void __launch_bounds__(kFreeThreads)
 free_refs_kernel(const int32_t* __restrict__ table, int64_t n, int64_t bt_width,
                  const int32_t* __restrict__ lens, int32_t* refs, int64_t num_pages,
                  uint32_t* status) {
   pdl_wait();
-  const int64_t s = blockIdx.x;
-  const int64_t L = lens[s];
-  if (L < 0 || L > bt_width * kPageTokens) {
-    if (threadIdx.x == 0) flag(status, MX4_STATUS_BAD_LEN);
-    return;
-  }
-  const int64_t pages = (L + kPageTokens - 1) / kPageTokens;
-  for (int64_t j = threadIdx.x; j < pages; j += kFreeThreads) {
-    const int32_t p = table[s * bt_width + j];
-    if (p < 0 || p >= num_pages) {
-      flag(status, MX4_STATUS_BAD_PAGE);
-      continue;
-    }
-    int32_t c = refs[p], seen;
-    for (;;) {
-      if (c <= 0) {  // a page that nobody holds (or that this call has already freed)
-        flag(status, MX4_STATUS_BAD_REF);
-        break;
-      }
-      seen = atomicCAS(refs + p, c, c == 1 ? kFreed : c - 1);
-      if (seen == c) break;
-      c = seen;
-    }
-  }
+  const int64_t s = blockIdx.x, pages = free_pages_of(lens, s, bt_width);
+  if (pages < 0 && threadIdx.x == 0) flag(status, MX4_STATUS_BAD_LEN);
+  for (int64_t j = threadIdx.x; j < pages; j += kFreeThreads)
+    free_entry(table, s, bt_width, j, refs, num_pages, status);
 }
 
+// kAll: the references too, of few rows, by the same CTA (a warp a row): one launch instead of
+// two.
+template <bool kAll>
 __global__ void __launch_bounds__(kForkThreads)
-free_push_kernel(int32_t* refs, int64_t num_pages, int32_t* __restrict__ free_list,
-                 int32_t* free_count, uint32_t* status) {
+free_push_kernel(const int32_t* __restrict__ table, int64_t n, int64_t bt_width,
+                 const int32_t* __restrict__ lens, int32_t* refs, int64_t num_pages,
+                 int32_t* __restrict__ free_list, int32_t* free_count, uint32_t* status) {
   __shared__ int s_warp[32];
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if constexpr (kAll) {
+    for (int64_t s = warp; s < n; s += kForkThreads / 32) {
+      const int64_t pages = free_pages_of(lens, s, bt_width);
+      if (pages < 0 && lane == 0) flag(status, MX4_STATUS_BAD_LEN);
+      for (int64_t j = lane; j < pages; j += 32)
+        free_entry(table, s, bt_width, j, refs, num_pages, status);
+    }
+    __threadfence_block();
+    __syncthreads();
+  }
   int64_t top = max(*free_count, 0);
   constexpr int E = 8;  // ids a thread and round
   for (int64_t b = 0; b < num_pages; b += (int64_t)kForkThreads * E) {
     const int64_t p0 = b + (int64_t)tid * E;
     uint32_t mine = 0;
+    int32_t c[E];
+    // (past the L1, where the references' atomics are)
+#pragma unroll
+    for (int e = 0; e < E; ++e) c[e] = p0 + e < num_pages ? __ldcg(refs + p0 + e) : 0;
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (p0 + e < num_pages && refs[p0 + e] == kFreed) mine |= 1u << e;
+      if (c[e] == kFreed) mine |= 1u << e;
     int inc = __popc(mine);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -657,14 +827,20 @@ free_push_kernel(int32_t* refs, int64_t num_pages, int32_t* __restrict__ free_li
   if (tid == 0) *free_count = (int32_t)min(top, num_pages);
 }
 
+// Up to this many table entries one CTA takes the references as well.
+constexpr int64_t kFreeSmall = 4096;
+
 cudaError_t launch_free(const int32_t* table, int64_t n, int64_t bt_width, const int32_t* lens,
                         int32_t* refs, int64_t num_pages, int32_t* free_list,
                         int32_t* free_count, uint32_t* status, cudaStream_t stream) {
+  if (n * bt_width <= kFreeSmall)
+    return launch_pdl(free_push_kernel<true>, dim3(1), dim3(kForkThreads), 0, stream, table, n,
+                      bt_width, lens, refs, num_pages, free_list, free_count, status);
   cudaError_t e = launch_pdl(free_refs_kernel, dim3((unsigned)n), dim3(kFreeThreads), 0, stream,
                              table, n, bt_width, lens, refs, num_pages, status);
   if (e != cudaSuccess) return e;
-  return launch_pdl(free_push_kernel, dim3(1), dim3(kForkThreads), 0, stream, refs, num_pages,
-                    free_list, free_count, status);
+  return launch_pdl(free_push_kernel<false>, dim3(1), dim3(kForkThreads), 0, stream, table, n,
+                    bt_width, lens, refs, num_pages, free_list, free_count, status);
 }
 
 }  // namespace mx4
