@@ -251,6 +251,26 @@ __device__ __forceinline__ void stw(uint32_t taddr, const float* x) {
   if constexpr (W == 8) st8(taddr, x); else st16(taddr, x);
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ void fma2(float& x0, float& x1, uint64_t m, float c0, float c1) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(pair(x0, x1)), "l"(m), "l"(pair(c0, c1)));
+  unpair(r, x0, x1);
+}
+__device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(pair(x0, x1)), "l"(pair(y0, y1)));
+  unpair(r, x0, x1);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -658,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
   int* const s_lo = reinterpret_cast<int*>(sm + L_::kLo) + c0;
   uint32_t* const s_mask = reinterpret_cast<uint32_t*>(sm + L_::kMask) + 2 * c0;  // [NC][2]
   const float cs = a.scale * kLog2e;
+  const uint64_t cs2 = pair(cs, cs);
   const int tok = 4 * lane + w;  // this lane's token of a page
   // dequantisation: see below
   const int r8 = lane & 7, blk = ((r8 >> 1) + (lane >> 3)) & 3;
@@ -779,11 +800,9 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
         // the tensor copy lays out K.  A warp's step: 8 operand rows (r8), lane >> 3 choosing
         // which 32-dim block of each: 16 raw bytes a lane, four 16-byte stores without bank
         // conflicts.
+        auto take_v = [&]() {
         wait(kVFull + k % VS, (k / VS) & 1);
         const uint8_t* raw = sm + L_::kVraw + (k % VS) * kPageBytes;
-        // NaN dim blocks of this lane's token
-        uint32_t vw = *reinterpret_cast<const uint32_t*>(raw + kScaleOffset + tok * kRowScaleBytes);
-        vw = ((vw & 0x7F7F7F7Fu) + 0x01010101u) & vw & 0x80808080u;
 #pragma unroll
         for (int it = 0; it < 2; ++it) {
           const int m = (warp * 2 + it) * 8 + r8, tk = 4 * (m & 31) + (m >> 5);
@@ -819,6 +838,9 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
             *reinterpret_cast<uint4*>(dst + ((((blk & 1) * 4 + j) ^ r8) << 4)) =
                 make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
         }
+        };
+        if constexpr (VS > 1) take_v();
+        else if (k > 0) wait(kPvDone, (k - 1) & 1);  // (P's buffer is free)
         // ---- logits in log2 units relative to the rows' references
         // a row sees a draft by its mask, an earlier token from the window's first on; rows
         // without a node see what they like, their results are zeroed
@@ -835,11 +857,6 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
             }
           }
         }
-        if (vw != 0u && tok < live) {  // the rows that see the token get its NaNs at the end
-#pragma unroll 1
-          for (int c = 0; c < NC; ++c)
-            if ((vis >> c) & 1u) atomicOr(s_nan + c, vw);
-        }
         wait(kSFull + (k & 1), (k >> 1) & 1);
         fence_after();
         const uint32_t ts = tl + T_::kS + (k & 1) * C::kScols + c0;
@@ -851,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
             ldw<W>(ts + NR + c, z);
             wait_ld();
 #pragma unroll
-            for (int i = 0; i < W; ++i) v[i] += z[i];
+            for (int i = 0; i < W; i += 2) add2(v[i], v[i + 1], z[i], z[i + 1]);
           } else {
             wait_ld();
           }
@@ -877,10 +894,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < W; i += 4) {
               const float4 rf = *reinterpret_cast<const float4*>(s_nref + c + i);
-              x[i] = fmaf(x[i], cs, rf.x);
-              x[i + 1] = fmaf(x[i + 1], cs, rf.y);
-              x[i + 2] = fmaf(x[i + 2], cs, rf.z);
-              x[i + 3] = fmaf(x[i + 3], cs, rf.w);
+              fma2(x[i], x[i + 1], cs2, rf.x, rf.y);
+              fma2(x[i + 2], x[i + 3], cs2, rf.z, rf.w);
             }
             hide(c, x);
             float m[W / 2];
@@ -898,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
                 if (lane == 0) s_more[k % 3] = 1;
               } else {
 #pragma unroll
-                for (int i = 0; i < W; ++i) l[c + i] += x[i];
+                for (int i = 0; i < W; i += 2) add2(l[c + i], l[c + i + 1], x[i], x[i + 1]);
                 owed &= ~(1u << c);
               }
             }
@@ -907,6 +922,17 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
               *reinterpret_cast<uint4*>(pd + ((c + i) >> 3) * kChunk) =
                   make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]),
                              pack_bf16(x[i + 4], x[i + 5]), pack_bf16(x[i + 6], x[i + 7]));
+          }
+          if (!moved) {
+            if constexpr (VS == 1) take_v();
+        // NaN dim blocks of this lane's token
+        uint32_t vw = *reinterpret_cast<const uint32_t*>(sm + L_::kVraw + (k % VS) * kPageBytes + kScaleOffset + tok * kRowScaleBytes);
+        vw = ((vw & 0x7F7F7F7Fu) + 0x01010101u) & vw & 0x80808080u;
+        if (vw != 0u && tok < live) {  // the rows that see the token get its NaNs at the end
+#pragma unroll 1
+          for (int c = 0; c < NC; ++c)
+            if ((vis >> c) & 1u) atomicOr(s_nan + c, vw);
+        }
           }
           fence_async();
           fence_before();
