@@ -512,13 +512,14 @@ int verify_drafts(const float *target, int64_t t_batch_stride, int64_t t_node_st
  *   path int32 [B, N], ascending over its first n_accepted[s] entries;
  *   n_accepted, seq_lens int32 [B]; n_nodes int32 [B] or NULL; block_table [B, bt_width]
  *   k_pages, v_pages as mx4_insert; idx_pages index-K pages, MXFP4 (idx_fp8 = 0) or
- *                fp8 (idx_fp8 = 1, 16384-byte pages), or NULL
+ *                fp8 (idx_fp8 = 1, 16384-byte pages), or NULL; with Hkv = 0 the index
+ *                pages alone (k_pages, v_pages not read): a cache with a second index pool
  *   new_lens     int32 [B] (output; not seq_lens itself)
  * A path that does not ascend within the nodes (MX4_STATUS_BAD_INDEX), a bad length or
  * count (MX4_STATUS_BAD_LEN) or a bad page (MX4_STATUS_BAD_PAGE) leaves the sequence's
  * rows alone, with new_lens[s] = seq_lens[s].  The drafted rows' pages belong to this
  * sequence alone (mx4_fork_pages copies the page that is being filled).
- * 1 <= N <= 64, 1 <= Hkv <= 8.
+ * 1 <= N <= 64, 0 <= Hkv <= 8.
  * ------------------------------------------------------------------------- */
 int mx4_accept_rows(const int32_t *path, const int32_t *n_accepted, const int32_t *seq_lens,
                     const int32_t *n_nodes, int64_t B, int N, const int32_t *block_table,

@@ -698,7 +698,8 @@ def mx4_accept_rows(path, n_accepted, seq_lens, block_table, k_pages, v_pages, i
                     n_nodes=None, stream=None):
     """The cache after verify_drafts: the accepted nodes' rows (path int32 [B, N], ascending,
     its first n_accepted[s] entries) become the sequence's first draft rows in every pool
-    (idx_pages MXFP4, fp8 or None); new_lens int32 [B] = seq_lens - n_nodes + n_accepted."""
+    (idx_pages MXFP4, fp8 or None; k_pages and v_pages None: the index pages alone);
+    new_lens int32 [B] = seq_lens - n_nodes + n_accepted."""
     i32 = torch.int32
     _dims(path, "path", None, None)
     B, N = path.shape
@@ -708,8 +709,11 @@ def mx4_accept_rows(path, n_accepted, seq_lens, block_table, k_pages, v_pages, i
             _arg(seq_lens, i32, (B,), "seq_lens"), _opt(n_nodes, i32, (B,), "n_nodes"), B, N,
             _arg(block_table, i32, (B, W), "block_table"), W)
     new = _arg(new_lens, i32, (B,), "new_lens")
-    idx = _idx_pool(idx_pages, k_pages.shape[0])
-    kv = _kv_pools(k_pages, v_pages)
+    if k_pages is None and v_pages is None and idx_pages is not None:
+        kv = None, None, 0, 0, 0, idx_pages.shape[0]
+    else:
+        kv = _kv_pools(k_pages, v_pages)
+    idx = _idx_pool(idx_pages, kv[5])
     _call(_load().mx4_accept_rows, *args, *kv[:5], *idx, new, _stream(stream))
 
 

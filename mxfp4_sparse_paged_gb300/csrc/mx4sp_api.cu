@@ -811,11 +811,12 @@ constexpr int kMaxTreeNodes = 64;  // a node's mask is one 64-bit word
 int check_pools(const char* name, const uint8_t* k_pages, const uint8_t* v_pages,
                 int64_t kv_page_stride, int64_t kv_head_stride, int Hkv, const uint8_t* idx_pages,
                 int64_t idx_page_stride, int idx_fp8, int64_t num_pages) {
-  if (!k_pages || !v_pages) return fail(MX4_ERR_INVALID, "%s: NULL pages", name);
+  if (Hkv > 0 ? !k_pages || !v_pages : !idx_pages)
+    return fail(MX4_ERR_INVALID, "%s: NULL pages", name);
   if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(idx_pages, 16) ||
       kv_page_stride % 16 || kv_head_stride % 16 || (idx_pages && idx_page_stride % 16))
     return fail(MX4_ERR_INVALID, "%s: pages must be 16-byte aligned with 16-byte strides", name);
-  if (num_pages < 1 || num_pages > 0x7FFFFFFF || kv_page_stride < mx4::kPageBytes ||
+  if (num_pages < 1 || num_pages > 0x7FFFFFFF || (Hkv > 0 && kv_page_stride < mx4::kPageBytes) ||
       (Hkv > 1 && kv_head_stride < mx4::kPageBytes) ||
       (idx_pages && idx_page_stride < (idx_fp8 ? MX4_FP8_PAGE_BYTES : mx4::kPageBytes)))
     return fail(MX4_ERR_INVALID, "%s: num_pages or a stride below a page", name);
@@ -927,8 +928,8 @@ extern "C" int mx4_accept_rows(const int32_t* path, const int32_t* n_accepted,
   static const char* kName = "mx4_accept_rows";
   if (N < 1 || N > kMaxTreeNodes)
     return fail(MX4_ERR_UNSUPPORTED, "%s: N = %d (supported 1..64)", kName, N);
-  if (Hkv < 1 || Hkv > 8)
-    return fail(MX4_ERR_UNSUPPORTED, "%s: Hkv = %d (supported 1..8)", kName, Hkv);
+  if (Hkv < 0 || Hkv > 8)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: Hkv = %d (supported 0..8)", kName, Hkv);
   if (B < 0 || B > 0x7FFFFFFF)
     return fail(MX4_ERR_UNSUPPORTED, "%s: B = %lld", kName, (long long)B);
   if (B == 0) return ok();
