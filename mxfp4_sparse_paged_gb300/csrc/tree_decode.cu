@@ -560,6 +560,10 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
           s_more[(k + 1) % 3] = 0;
         }
         __syncwarp();
+        if (e == cu.e0) {
+          sync_all();
+          sync_all();
+        }
         sync_all();
         if (s_more[k % 3]) {
           sync_all();
@@ -643,6 +647,10 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
             issue_s(ahead = k + 1);
         }
         fence_before();
+        if (e == cu.e0) {
+          sync_all();
+          sync_all();
+        }
         sync_all();
         if (s_more[k % 3]) {
           sync_all();
@@ -683,8 +691,29 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
   // dequantisation: see below
   const int r8 = lane & 7, blk = ((r8 >> 1) + (lane >> 3)) & 3;
 
+  // A tile's q: 16 elements a thread, K-chunk j of row n (the two threads of a 32-block share
+  // its largest magnitude), on their way while the tile before is written out.
+  constexpr int kQIt = (NR * 8 + kWorkers - 1) / kWorkers;
+  uint4 qx[kQIt][2];
+  auto fetch_q = [&](const Cursor& c) {
+#pragma unroll
+    for (int it = 0; it < kQIt; ++it) {
+      const int n = (tid >> 3) + it * (kWorkers / 8), row = c.rt * NR + n, node = row / a.G;
+      qx[it][0] = qx[it][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (n < NR && c.left > 0 && node < c.sp.n) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + (((int64_t)c.s * a.N + node) * a.H + c.h * a.G + row % a.G) * kHeadDim +
+            16 * (tid & 7));
+        qx[it][0] = src[0];
+        qx[it][1] = src[1];
+      }
+    }
+  };
+
   int k = 0;  // pages done
-  for (Cursor cu = begin(); cu.left > 0; advance(cu)) {
+  Cursor cu = begin();
+  fetch_q(cu);
+  while (cu.left > 0) {
     const Span sp = cu.sp;
     const bool begins = cu.e0 == 0, ends = cu.e1 >= sp.np;
     sync_all();  // the tile before is written out
@@ -716,19 +745,13 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
       s_nref[t] = -kUnset;
       s_nan[t] = 0;
     }
-    // ---- q: 16 elements a thread, K-chunk j of row n; the two threads of a 32-block share
-    // its largest magnitude
+    // ---- q
     if (sp.np > 0) {
-#pragma unroll 1
-      for (int n = tid >> 3; n < NR; n += kWorkers / 8) {
-        const int j = tid & 7, row = cu.rt * NR + n, node = row / a.G;
-        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
-        if (node < sp.n) {
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + (((int64_t)cu.s * a.N + node) * a.H + cu.h * a.G + row % a.G) * kHeadDim + 16 * j);
-          x0 = src[0];
-          x1 = src[1];
-        }
+#pragma unroll
+      for (int it = 0; it < kQIt; ++it) {
+        const int n = (tid >> 3) + it * (kWorkers / 8), j = tid & 7;
+        if (n >= NR) break;
+        const uint4 x0 = qx[it][0], x1 = qx[it][1];
         const uint32_t wd[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
         float amax = 0.f;
 #pragma unroll
@@ -801,43 +824,43 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
         // which 32-dim block of each: 16 raw bytes a lane, four 16-byte stores without bank
         // conflicts.
         auto take_v = [&]() {
-        wait(kVFull + k % VS, (k / VS) & 1);
-        const uint8_t* raw = sm + L_::kVraw + (k % VS) * kPageBytes;
+          wait(kVFull + k % VS, (k / VS) & 1);
+          const uint8_t* raw = sm + L_::kVraw + (k % VS) * kPageBytes;
 #pragma unroll
-        for (int it = 0; it < 2; ++it) {
-          const int m = (warp * 2 + it) * 8 + r8, tk = 4 * (m & 31) + (m >> 5);
-          const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tk * kRowDataBytes + blk * 16);
-          const uint32_t sc = raw[kScaleOffset + tk * kRowScaleBytes + blk];
-          // 2^(sc - 1), as two factors where it passes bf16's range
-          const uint32_t f1 = (tk < live && sc != 255u ? min(sc + 126u, 254u) : 0u) * 0x00800080u;
-          const bool big = __any_sync(0xFFFFFFFFu, sc > 128u);
-          const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
-          uint32_t y[4][4];
+          for (int it = 0; it < 2; ++it) {
+            const int m = (warp * 2 + it) * 8 + r8, tk = 4 * (m & 31) + (m >> 5);
+            const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tk * kRowDataBytes + blk * 16);
+            const uint32_t sc = raw[kScaleOffset + tk * kRowScaleBytes + blk];
+            const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+            uint32_t y[4][4];
+            // 2^(sc - 1), as two factors where it passes bf16's range
+            const uint32_t f1 = (tk < live && sc != 255u ? min(sc + 126u, 254u) : 0u) * 0x00800080u;
+            const bool big = __any_sync(0xFFFFFFFFu, sc > 128u);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t v = cw[j];
-            // codes i and i + 4 of the word as one pair
-            y[j][0] = ((v << 12) & 0x80008000u) | ((v << 6) & 0x01C001C0u);
-            y[j][1] = ((v << 8) & 0x80008000u) | ((v << 2) & 0x01C001C0u);
-            y[j][2] = ((v << 4) & 0x80008000u) | ((v >> 2) & 0x01C001C0u);
-            y[j][3] = (v & 0x80008000u) | ((v >> 6) & 0x01C001C0u);
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t v = cw[j];
+              // codes i and i + 4 of the word as one pair
+              y[j][0] = ((v << 12) & 0x80008000u) | ((v << 6) & 0x01C001C0u);
+              y[j][1] = ((v << 8) & 0x80008000u) | ((v << 2) & 0x01C001C0u);
+              y[j][2] = ((v << 4) & 0x80008000u) | ((v >> 2) & 0x01C001C0u);
+              y[j][3] = (v & 0x80008000u) | ((v >> 6) & 0x01C001C0u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f1);
-          }
-          if (big) {
-            const uint32_t f2 = (sc > 128u ? sc - 1u : 127u) * 0x00800080u;
+              for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f1);
+            }
+            if (big) {
+              const uint32_t f2 = (sc > 128u ? sc - 1u : 127u) * 0x00800080u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f2);
+            }
+            if (it == 0 && k > 0) wait(kPvDone, (k - 1) & 1);  // the buffers are free
+            uint8_t* const dst = sm + L_::kV + (blk >> 1) * kVHalf + (m >> 3) * 1024 + r8 * 128;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f2);
+              *reinterpret_cast<uint4*>(dst + ((((blk & 1) * 4 + j) ^ r8) << 4)) =
+                  make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
           }
-          if (it == 0 && k > 0) wait(kPvDone, (k - 1) & 1);  // the operands' buffers are free
-          uint8_t* const dst = sm + L_::kV + (blk >> 1) * kVHalf + (m >> 3) * 1024 + r8 * 128;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(dst + ((((blk & 1) * 4 + j) ^ r8) << 4)) =
-                make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
-        }
         };
         if constexpr (VS > 1) take_v();
         else if (k > 0) wait(kPvDone, (k - 1) & 1);  // (P's buffer is free)
@@ -883,10 +906,54 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
         // The weights of the page, into the P operand and the row sums, W rows at a time.  Where
         // a logit lies too far above its reference, those W rows' weights are not summed yet
         // (owed): the page is taken again with new references.  What was summed is right in
-        // either case, it is brought to the new references with the rest.
+        // either case, it is brought to the new references with the rest.  A tile's first page
+        // starts with them.
         uint32_t owed = ~0u;
         uint8_t* const pd = sm + L_::kP + (c0 >> 3) * kChunk + (4 * w + (lane >> 3)) * 128 + (lane & 7) * 16;
-        for (bool moved = false;; moved = true) {
+        bool renew = e == cu.e0;
+#pragma unroll 1
+        for (int round = 0;; ++round) {
+          if (renew) {
+            // The page's maximum of each row that has a larger one; what was summed so far is
+            // brought to them.  (The product of the page before is done, its buffers were free
+            // above; this page's waits for the round's last barrier.)
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < NC; c += W) {
+              float v[W];
+              s_of(c, v);
+#pragma unroll
+              for (int i = 0; i < W; ++i) v[i] *= cs;
+              hide(c, v);
+              const float mx = columns<W>(v, lane, [](float p, float q) { return fmaxf(p, q); });
+              if (lane < W) s_warp[w * NC + c + lane] = mx;
+            }
+            sync_all();
+            if (t < NC) {
+              const float v = fmaxf(fmaxf(s_warp[t], s_warp[NC + t]),
+                                    fmaxf(s_warp[2 * NC + t], s_warp[3 * NC + t]));
+              const float old = -s_nref[t], now = fmaxf(old, v);
+              s_fac[t] = old == kUnset ? 0.f : ex2(old - now);
+              s_nref[t] = -now;
+            }
+            sync_all();
+            if (e > cu.e0 || round > 0) {
+#pragma unroll
+              for (int c = 0; c < NC; ++c) l[c] *= s_fac[c];
+            }
+            if (e > cu.e0) {
+#pragma unroll 1
+              for (int c = 0; c < NC; c += W) {
+                float o[W];
+                ldw<W>(tl + T_::kO + c0 + c, o);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < W; ++i) o[i] *= s_fac[c + i];
+                stw<W>(tl + T_::kO + c0 + c, o);
+              }
+              wait_st();
+            }
+          }
 #pragma unroll
           for (int c = 0; c < NC; c += W) {
             float x[W];
@@ -909,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < W; ++i) x[i] = ex2(x[i]);
             if ((owed >> c) & 1u) {
-              if (far && !moved) {
+              if (far && round == 0) {
                 if (lane == 0) s_more[k % 3] = 1;
               } else {
 #pragma unroll
@@ -923,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
                   make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]),
                              pack_bf16(x[i + 4], x[i + 5]), pack_bf16(x[i + 6], x[i + 7]));
           }
-          if (!moved) {
+          if (round == 0) {
             if constexpr (VS == 1) take_v();
         // NaN dim blocks of this lane's token
         uint32_t vw = *reinterpret_cast<const uint32_t*>(sm + L_::kVraw + (k % VS) * kPageBytes + kScaleOffset + tok * kRowScaleBytes);
@@ -937,47 +1004,13 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
           fence_async();
           fence_before();
           sync_all();
-          if (moved || !s_more[k % 3]) break;
-          // New references: the page's maximum of each row that has a larger one; what was
-          // summed so far is brought to them, and the page's weights are taken once more.  (The
-          // page's product waits for the third barrier from here; that of the page before is
-          // done, its buffers were free above.)
-          fence_after();
-#pragma unroll 1
-          for (int c = 0; c < NC; c += W) {
-            float v[W];
-            s_of(c, v);
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[i] *= cs;
-            hide(c, v);
-            const float mx = columns<W>(v, lane, [](float p, float q) { return fmaxf(p, q); });
-            if (lane < W) s_warp[w * NC + c + lane] = mx;
-          }
-          sync_all();
-          if (t < NC) {
-            const float v = fmaxf(fmaxf(s_warp[t], s_warp[NC + t]),
-                                  fmaxf(s_warp[2 * NC + t], s_warp[3 * NC + t]));
-            const float old = -s_nref[t], now = fmaxf(old, v);
-            s_fac[t] = old == kUnset ? 0.f : ex2(old - now);
-            s_nref[t] = -now;
-          }
-          sync_all();
-#pragma unroll
-          for (int c = 0; c < NC; ++c) l[c] *= s_fac[c];
-          if (e > cu.e0) {
-#pragma unroll 1
-            for (int c = 0; c < NC; c += W) {
-              float o[W];
-              ldw<W>(tl + T_::kO + c0 + c, o);
-              wait_ld();
-#pragma unroll
-              for (int i = 0; i < W; ++i) o[i] *= s_fac[c + i];
-              stw<W>(tl + T_::kO + c0 + c, o);
-            }
-            wait_st();
-          }
+          if (round > 0 || !s_more[k % 3]) break;
+          renew = true;
         }
       }
+      Cursor nx = cu;
+      advance(nx);
+      fetch_q(nx);
 #pragma unroll
       for (int c = 0; c < NC; c += W) {
         const float v = columns<W>(l + c, lane, [](float p, float q) { return p + q; });
@@ -985,6 +1018,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
       }
       wait(kPvDone, (k - 1) & 1);
     } else {
+#pragma unroll 1
       for (int c = t; c < 4 * NC; c += 128) s_warp[c] = 0.f;
     }
     sync_all();
@@ -1011,6 +1045,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     // operand position -> dim: the codes of a word were paired i, i + 4
     const int dim = 32 * w + (lane & 24) + ((lane & 1) << 2) + ((lane & 7) >> 1);
     const uint32_t nb = 0x80u << (8 * w);
+    uint16_t* const out = a.out + (int64_t)cu.s * a.N * a.H * kHeadDim + dim;
+    float* const orec = rec + c0 * 128 + dim;
 #pragma unroll 1
     for (int c = 0; c < NC; c += W) {
       float o[W];
@@ -1019,20 +1055,35 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
         wait_ld();
       }
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const float f = s_fac[c + i];
-        const float v = sp.np == 0 || f == 0.f ? 0.f : (s_nan[c + i] & nb) ? NAN : o[i] * f;
+      for (int i = 0; i < W; i += 4) {
+        const float4 f4 = *reinterpret_cast<const float4*>(s_fac + c + i);
+        const uint4 n4 = *reinterpret_cast<const uint4*>(s_nan + c + i);
+        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+        const uint32_t nn[4] = {n4.x, n4.y, n4.z, n4.w};
+        float v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          v[u] = sp.np == 0 || f[u] == 0.f ? 0.f : (nn[u] & nb) ? NAN : o[i + u] * f[u];
         if (whole) {
-          const int row = s_node[c + i];
-          if (row >= 0)
-            a.out[((int64_t)cu.s * a.N * a.H + row) * kHeadDim + dim] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(v));
+          const int4 r4 = *reinterpret_cast<const int4*>(s_node + c + i);
+          const int row[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (row[u] >= 0)
+              out[row[u] * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(v[u]));
         } else {
-          rec[(c0 + c + i) * 128 + dim] = v;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) orec[(c + i + u) * 128] = v[u];
         }
       }
     }
     fence_before();
+    if (sp.np == 0) {
+      Cursor nx = cu;
+      advance(nx);
+      fetch_q(nx);
+    }
+    advance(cu);
   }
   }
   fence_before();

@@ -210,6 +210,20 @@ def test_logits_that_climb_and_fall(slope):
     a.check(out, lse)
 
 
+@pytest.mark.parametrize("N,H,kind", [(1, 16, "chain"), (6, 5, "tree"), (7, 16, "tree")])
+def test_value_scales_that_change_from_page_to_page(N, H, kind):
+    # blocks of some pages far above and far below the others, a page of zeros (scale byte 0)
+    a = Attn(18, [1300], N, H=H, kind=kind)
+    for pg, sc in ((0, 0), (2, 150), (3, 90), (6, 103), (7, 141), (9, 200)):
+        p = a.bt[0, pg]
+        a.vp[p, 0, 8192:].reshape(128, 4)[:, pg % 4] = sc
+        if pg == 0:
+            a.vp[p, 0, :8192] = 0
+    out, lse = a.run()
+    assert m.mx4_check_status() == 0
+    a.check(out, lse)
+
+
 def test_infinite_queries_are_nan():
     a = Attn(11, [200], 2)
     a.q[0, 1, 3, 5] = float("inf")
