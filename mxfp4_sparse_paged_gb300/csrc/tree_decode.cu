@@ -271,6 +271,13 @@ __device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
   unpair(r, x0, x1);
 }
 
+// The largest of three; a NaN loses.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -839,11 +846,14 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint32_t v = cw[j];
-              // codes i and i + 4 of the word as one pair
-              y[j][0] = ((v << 12) & 0x80008000u) | ((v << 6) & 0x01C001C0u);
-              y[j][1] = ((v << 8) & 0x80008000u) | ((v << 2) & 0x01C001C0u);
-              y[j][2] = ((v << 4) & 0x80008000u) | ((v >> 2) & 0x01C001C0u);
-              y[j][3] = (v & 0x80008000u) | ((v >> 6) & 0x01C001C0u);
+              // Codes i and i + 4 of the word as one pair: a code's four bits to places 15 .. 12
+              // and 9 .. 6 by one multiplication (on the FMA pipe, which has twice the logic
+              // pipe's rate), then its sign from the one and the other three from the other.
+              const uint32_t u = v >> 8;
+              y[j][0] = ((v & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+              y[j][1] = ((v & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
+              y[j][2] = ((u & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+              y[j][3] = ((u & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
 #pragma unroll
               for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f1);
             }
@@ -965,14 +975,14 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
               fma2(x[i + 2], x[i + 3], cs2, rf.z, rf.w);
             }
             hide(c, x);
-            float m[W / 2];
+            float m0 = x[0], m1 = x[1];
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) m[i] = fmaxf(x[i], x[W / 2 + i]);
-#pragma unroll
-            for (int o = W / 4; o > 0; o >>= 1)
-#pragma unroll
-              for (int i = 0; i < o; ++i) m[i] = fmaxf(m[i], m[i + o]);
-            const bool far = __any_sync(0xFFFFFFFFu, m[0] > kLazy);
+            for (int i = 2; i + 3 < W; i += 4) {
+              m0 = max3(m0, x[i], x[i + 1]);
+              m1 = max3(m1, x[i + 2], x[i + 3]);
+            }
+            m0 = max3(m0, m1, fmaxf(x[W - 2], x[W - 1]));
+            const bool far = __any_sync(0xFFFFFFFFu, m0 > kLazy);
 #pragma unroll
             for (int i = 0; i < W; ++i) x[i] = ex2(x[i]);
             if ((owed >> c) & 1u) {
