@@ -565,6 +565,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
           wait(kSFull + (k & 1), (k >> 1) & 1);
           load_k();  // (page k's K has been read)
           s_more[(k + 1) % 3] = 0;
+          // the workers find the next page's V landed after the barrier, without a wait
+          if (VS > 1 && e + 1 < cu.e1) wait(kVFull + (k + 1) % VS, ((k + 1) / VS) & 1);
         }
         __syncwarp();
         if (e == cu.e0) {
@@ -640,18 +642,19 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
     sync_all();  // rows and q are ready
     if (cu.sp.np > 0) {
       sync_all();  // q's scales are in tensor memory
-      int ahead = k - 1;  // S of the pages up to here has been issued
 #pragma unroll 1
       for (int e = cu.e0; e < cu.e1; ++e, ++k) {
         const bool go = !__any_sync(0xFFFFFFFFu, *s_abort);
         if (go) {
           fence_after();
           if (e > cu.e0) issue_pv(e - 1 == cu.e0);
-          if (ahead < k && __all_sync(0xFFFFFFFFu, wait(kKFull + k % KS, (k / KS) & 1)))
-            issue_s(ahead = k);
-          if (e + 1 < cu.e1 && ahead == k &&
-              __all_sync(0xFFFFFFFFu, mbar_test(bar(kKFull + (k + 1) % KS), ((k + 1) / KS) & 1)))
-            issue_s(ahead = k + 1);
+          if (e == cu.e0 && __all_sync(0xFFFFFFFFu, wait(kKFull + k % KS, (k / KS) & 1))) issue_s(k);
+          // the next page's S, which the workers find done after the barrier
+          if (e + 1 < cu.e1) {
+            if (__all_sync(0xFFFFFFFFu, wait(kKFull + (k + 1) % KS, ((k + 1) / KS) & 1)))
+              issue_s(k + 1);
+            wait(kSFull + ((k + 1) & 1), ((k + 1) >> 1) & 1);
+          }
         }
         fence_before();
         if (e == cu.e0) {
@@ -830,50 +833,57 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
         // the tensor copy lays out K.  A warp's step: 8 operand rows (r8), lane >> 3 choosing
         // which 32-dim block of each: 16 raw bytes a lane, four 16-byte stores without bank
         // conflicts.
-        auto take_v = [&]() {
-          wait(kVFull + k % VS, (k / VS) & 1);
+        auto convert_v = [&](int it, uint32_t (&y)[4][4]) {
           const uint8_t* raw = sm + L_::kVraw + (k % VS) * kPageBytes;
+          const int m = (warp * 2 + it) * 8 + r8, tk = 4 * (m & 31) + (m >> 5);
+          const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tk * kRowDataBytes + blk * 16);
+          const uint32_t sc = raw[kScaleOffset + tk * kRowScaleBytes + blk];
+          const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+          // 2^(sc - 1), as two factors where it passes bf16's range
+          const uint32_t f1 = (tk < live && sc != 255u ? min(sc + 126u, 254u) : 0u) * 0x00800080u;
+          const bool big = __any_sync(0xFFFFFFFFu, sc > 128u);
 #pragma unroll
-          for (int it = 0; it < 2; ++it) {
-            const int m = (warp * 2 + it) * 8 + r8, tk = 4 * (m & 31) + (m >> 5);
-            const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tk * kRowDataBytes + blk * 16);
-            const uint32_t sc = raw[kScaleOffset + tk * kRowScaleBytes + blk];
-            const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
-            uint32_t y[4][4];
-            // 2^(sc - 1), as two factors where it passes bf16's range
-            const uint32_t f1 = (tk < live && sc != 255u ? min(sc + 126u, 254u) : 0u) * 0x00800080u;
-            const bool big = __any_sync(0xFFFFFFFFu, sc > 128u);
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t v = cw[j];
+            // Codes i and i + 4 of the word as one pair: a code's four bits to places 15 .. 12
+            // and 9 .. 6 by one multiplication (on the FMA pipe, which has twice the logic
+            // pipe's rate), then its sign from the one and the other three from the other.
+            const uint32_t u = v >> 8;
+            y[j][0] = ((v & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+            y[j][1] = ((v & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
+            y[j][2] = ((u & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+            y[j][3] = ((u & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t v = cw[j];
-              // Codes i and i + 4 of the word as one pair: a code's four bits to places 15 .. 12
-              // and 9 .. 6 by one multiplication (on the FMA pipe, which has twice the logic
-              // pipe's rate), then its sign from the one and the other three from the other.
-              const uint32_t u = v >> 8;
-              y[j][0] = ((v & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
-              y[j][1] = ((v & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
-              y[j][2] = ((u & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
-              y[j][3] = ((u & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f1);
-            }
-            if (big) {
-              const uint32_t f2 = (sc > 128u ? sc - 1u : 127u) * 0x00800080u;
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f2);
-            }
-            if (it == 0 && k > 0) wait(kPvDone, (k - 1) & 1);  // the buffers are free
-            uint8_t* const dst = sm + L_::kV + (blk >> 1) * kVHalf + (m >> 3) * 1024 + r8 * 128;
+            for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f1);
+          }
+          if (big) {
+            const uint32_t f2 = (sc > 128u ? sc - 1u : 127u) * 0x00800080u;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(dst + ((((blk & 1) * 4 + j) ^ r8) << 4)) =
-                  make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f2);
           }
         };
-        if constexpr (VS > 1) take_v();
-        else if (k > 0) wait(kPvDone, (k - 1) & 1);  // (P's buffer is free)
+        auto store_v = [&](int it, const uint32_t (&y)[4][4]) {
+          const int m = (warp * 2 + it) * 8 + r8;
+          uint8_t* const dst = sm + L_::kV + (blk >> 1) * kVHalf + (m >> 3) * 1024 + r8 * 128;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(dst + ((((blk & 1) * 4 + j) ^ r8) << 4)) =
+                make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
+        };
+        // The operands' buffers are free once the product of the page before is done.  With two
+        // stages of V its first half is converted before that, else (V lands last) the weights
+        // are computed before.
+        uint32_t yv[4][4];
+        if (VS > 1 && e == cu.e0) wait(kVFull + k % VS, (k / VS) & 1);
+        if constexpr (VS > 1) {
+          convert_v(0, yv);
+          if (k > 0) wait(kPvDone, (k - 1) & 1);
+          store_v(0, yv);
+          convert_v(1, yv);
+          store_v(1, yv);
+        }
         // ---- logits in log2 units relative to the rows' references
         // a row sees a draft by its mask, an earlier token from the window's first on; rows
         // without a node see what they like, their results are zeroed
@@ -890,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
             }
           }
         }
-        wait(kSFull + (k & 1), (k >> 1) & 1);
+        if (e == cu.e0) wait(kSFull + (k & 1), (k >> 1) & 1);
         fence_after();
         const uint32_t ts = tl + T_::kS + (k & 1) * C::kScols + c0;
         // S of W rows, hi and lo parts added where they are apart
@@ -920,6 +930,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
         // starts with them.
         uint32_t owed = ~0u;
         uint8_t* const pd = sm + L_::kP + (c0 >> 3) * kChunk + (4 * w + (lane >> 3)) * 128 + (lane & 7) * 16;
+        uint32_t pk[NC / 2];
         bool renew = e == cu.e0;
 #pragma unroll 1
         for (int round = 0;; ++round) {
@@ -995,13 +1006,21 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
               }
             }
 #pragma unroll
-            for (int i = 0; i < W; i += 8)
-              *reinterpret_cast<uint4*>(pd + ((c + i) >> 3) * kChunk) =
-                  make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]),
-                             pack_bf16(x[i + 4], x[i + 5]), pack_bf16(x[i + 6], x[i + 7]));
+            for (int i = 0; i < W; i += 2) pk[(c + i) / 2] = pack_bf16(x[i], x[i + 1]);
           }
+          if (VS == 1 && round == 0 && k > 0) wait(kPvDone, (k - 1) & 1);
+#pragma unroll
+          for (int c = 0; c < NC; c += 8)
+            *reinterpret_cast<uint4*>(pd + (c >> 3) * kChunk) =
+                make_uint4(pk[c / 2], pk[c / 2 + 1], pk[c / 2 + 2], pk[c / 2 + 3]);
           if (round == 0) {
-            if constexpr (VS == 1) take_v();
+            if constexpr (VS == 1) {
+              wait(kVFull + k % VS, (k / VS) & 1);
+              convert_v(0, yv);
+              store_v(0, yv);
+              convert_v(1, yv);
+              store_v(1, yv);
+            }
         // NaN dim blocks of this lane's token
         uint32_t vw = *reinterpret_cast<const uint32_t*>(sm + L_::kVraw + (k % VS) * kPageBytes + kScaleOffset + tok * kRowScaleBytes);
         vw = ((vw & 0x7F7F7F7Fu) + 0x01010101u) & vw & 0x80808080u;
