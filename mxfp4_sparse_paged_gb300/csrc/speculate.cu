@@ -23,25 +23,28 @@ namespace mx4 {
 // (W / T is the residual distribution; kept unnormalised so nothing is divided), and
 // where no child stands the next token is drawn from W by its running sum.
 //
-// Sums are exact: probabilities are 64-bit integers in units of 2^-62 (fp32 values of
-// at least 2^-38 without any rounding), so no order of summation and no cluster size
-// changes a decision, and the only fp64 left is a few scalars (this GPU's fp64 rate is
-// a hundredth of its fp32 rate; the integer form costs some ten 32-bit operations a
-// value, below what the loads take).
+// As max(max(p - a, 0) - b, 0) = max(p - a - b, 0) for b >= 0, after k rejections
+//   W_k = max(p - S_k q, 0),   S_k = T_0 + ... + T_{k-1}:
+// p, q and one number give every residual, none is kept.
+//
+// Sums are exact: W is a 64-bit integer in units of 2^-62 (fp32 probabilities of at least
+// 2^-38 without any rounding; S to 32 significant bits, 2^-8 of the step of the fp32 q that it
+// scales), so no order of summation and no cluster size changes a decision.  There is no fp64
+// (this GPU's rate is a hundredth of its fp32 rate): a residual costs some twenty 32-bit
+// operations.
 //
 // One cluster of CTAs per sequence, each CTA one contiguous part of the vocabulary, each warp
 // one of that.  What the walk looks up (parents, tokens, random numbers, p and q of each draft
 // at its parent) is loaded by all threads at once, so accepted drafts cost no dependent loads.
-// At a node's first rejection its rows are read, once: a thread keeps E values of W (and of q)
-// in registers, and every further rejection of a sibling, the sums and the drawing of the
-// next token work on those.  (Reading both rows again for each took 206 us for 64 trees of 32
-// nodes over 131072 tokens, four fifths of it in recomputing W from p.)  E = 0, for
-// vocabularies above 8 x 16384: the rows are read again.
+// At a node's first rejection its rows are read, once: a thread keeps E values of p in
+// registers and of q in shared memory (a row of 131072 values by eight CTAs, two an SM), and
+// every further rejection of a sibling, the sums and the drawing of the next token work on
+// those.  E = 0, for vocabularies above 8 x 16384: the rows are read again.
 // Every thread runs the walk itself on the same numbers, so it needs no broadcast.
 constexpr int kMaxNodes = 64;
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
-constexpr int kVerUnroll = 8;  // loads in flight per thread and row
+constexpr int kVerUnroll = 8;  // loads in flight per thread and row (E = 0)
 constexpr int kVerMaxCluster = 8;
 
 struct VerifyArgs {
@@ -60,18 +63,30 @@ struct VerifyArgs {
   uint32_t* status;
 };
 
-// A probability in units of 2^-62 (truncated); a NaN or negative value counts as 0.  By the
-// bits: the 64-bit conversion instruction is as slow here as fp64 is.
-__device__ __forceinline__ uint64_t to_fixed(float x) {
-  const uint32_t b = __float_as_uint(fminf(fmaxf(x, 0.f), 1.9999f));
-  const uint32_t m = (b & 0x7FFFFFu) | 0x800000u;
-  const int e = (int)(b >> 23) - 88;  // the value is m 2^e
-  return e >= 0 ? (uint64_t)m << e : (uint64_t)(m >> min(-e, 31));
-}
 __device__ __forceinline__ bool prob_ok(float x) { return x >= 0.f && x <= 1.001f; }
-// a * b for a, b in units of 2^-62
-__device__ __forceinline__ uint64_t mul_fixed(uint64_t a, uint64_t b) {
-  return __umul64hi(a << 1, b << 1);
+// NaN and negative values count as 0 (and what rounding put above 1 as 1)
+__device__ __forceinline__ float prob(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+// x >> n, 0 for n of 64 and more
+__device__ __forceinline__ uint64_t shift_down(uint64_t x, int n) {
+  uint64_t y;
+  asm("shr.u64 %0, %1, %2;\n" : "=l"(y) : "l"(x), "r"(n));
+  return y;
+}
+// A probability in units of 2^-62, truncated.  By the bits: the 64-bit conversion instruction
+// is as slow here as fp64 is.
+__device__ __forceinline__ uint64_t to_fixed(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return shift_down((uint64_t)(b << 8 | 0x80000000u) << 32, 128 - (int)(b >> 23));
+}
+// u in [0, 1) in units of 2^-64
+__device__ __forceinline__ uint64_t uniform_fixed(float u) {
+  const uint32_t b = __float_as_uint(fminf(fmaxf(u, 0.f), 0x1.fffffep-1f));
+  return shift_down((uint64_t)(b << 8 | 0x80000000u) << 32, 126 - (int)(b >> 23));
+}
+// u q < p, exactly: the product's rounding error decides where its rounded value is p
+__device__ __forceinline__ bool stands(float u, float q, float p) {
+  const float h = u * q;
+  return h < p || (h == p && fmaf(u, q, -h) < 0.f);
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -80,74 +95,54 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
   return x;
 }
 
-// What is left of the target's distribution at the current node.
-struct Residual {
-  const float* p;       // the target's row
-  const float* q;       // the draft's row (NULL: one-hot drafts)
-  int k;                // rejections so far
-  const uint64_t* T;    // T_0 .. T_{k-1}
-  const int32_t* gone;  // the rejected tokens (one-hot drafts)
-  __device__ __forceinline__ uint64_t of(int v, float pv, float qv) const {
-    uint64_t w = to_fixed(pv);
-    if (k == 0) return w;
-    if (q) {
-      const uint64_t qf = to_fixed(qv);
-      for (int r = 0; r < k; ++r) {
-        const uint64_t t = r == 0 ? qf : mul_fixed(T[r], qf);
-        w = w > t ? w - t : 0;
-      }
-    } else {
-      for (int r = 0; r < k; ++r)
-        if (gone[r] == v) w = 0;
-    }
-    return w;
+// S_k, as m 2^(x - 31) with 2^31 <= m < 2^32; at 0 there is none
+struct Factor {
+  uint64_t sum = 0;  // in units of 2^-56 (S <= 64)
+  uint32_t m = 0;
+  int x = 0;
+  __device__ __forceinline__ void add(uint64_t T) {
+    sum += T >> 6;
+    const int lz = __clzll((long long)sum);
+    m = (uint32_t)((sum << lz) >> 32);
+    x = 7 - lz;
+  }
+  // max(p - S q, 0); S q >= 1 >= p where the shift would be to the left
+  __device__ __forceinline__ uint64_t left(float p, float q) const {
+    const uint64_t w = to_fixed(p);
+    const uint32_t b = __float_as_uint(q);
+    const uint64_t t = shift_down((uint64_t)(b << 8 | 0x80000000u) * m, max(127 - x - (int)(b >> 23), 0));
+    return w > t ? w - t : 0;
   }
 };
 
-// Sum of the residual over v0 <= v < v1 by one warp (all lanes get it).
-__device__ __forceinline__ uint64_t warp_range_sum(const Residual& R, int v0, int v1, int lane,
-                                                   bool& bad) {
-  uint64_t s = 0;
-  const bool two = R.q != nullptr && R.k > 0;
-  for (int b = v0 + lane; b < v1; b += 32 * kVerUnroll) {
-    float pv[kVerUnroll], qv[kVerUnroll];
-#pragma unroll
-    for (int i = 0; i < kVerUnroll; ++i) {
-      const int v = b + 32 * i;
-      pv[i] = v < v1 ? R.p[v] : 0.f;
-      qv[i] = two && v < v1 ? R.q[v] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kVerUnroll; ++i) {
-      bad |= !prob_ok(pv[i]) || !prob_ok(qv[i]);
-      s += R.of(b + 32 * i, pv[i], qv[i]);
-    }
-  }
-  return warp_sum(s);
-}
-
 template <int E, bool kGiven>
-__global__ void __launch_bounds__(kVerThreads, kGiven || E == 0 || E == 8 ? 2 : 1) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t s = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  __shared__ int32_t s_par[kMaxNodes], s_tok[kMaxNodes], s_gone[kMaxNodes], s_path[kMaxNodes];
+  extern __shared__ float s_row[];  // E > 0: q, value i of thread t at 512 i + t
+  __shared__ int32_t s_par[kMaxNodes], s_tok[kMaxNodes], s_path[kMaxNodes];
   __shared__ float s_u[kMaxNodes], s_p[kMaxNodes], s_q[kMaxNodes];
-  __shared__ uint64_t s_T[kMaxNodes + 1];
-  __shared__ uint64_t s_warp[3][kVerWarps];       // this CTA's warp sums, three passes' places
-  __shared__ uint64_t s_part[3][kVerMaxCluster];  // the cluster's CTA sums
+  __shared__ uint64_t s_warp[2][kVerWarps];       // this CTA's warp sums, of two passes
+  __shared__ uint64_t s_part[2][kVerMaxCluster];  // the cluster's CTA sums
   __shared__ uint64_t s_sub[kVerWarps];
-  __shared__ bool s_ok[kMaxNodes], s_now;  // a first child's test; the present one's
   pdl_launch_dependents();
   pdl_wait();
 
-  const int n = a.n_nodes ? min(max(a.n_nodes[s], 0), a.N) : a.N;
-  if (a.n_nodes && rank == 0 && tid == 0 && a.n_nodes[s] != n)
-    flag(a.status, MX4_STATUS_BAD_LEN);
+  int par = -1, tok = 0;
+  float u = 0.f;
+  if (tid > 0 && tid < a.N) {
+    par = a.parents[s * a.N + tid];
+    tok = a.tokens[s * a.N + tid];
+    u = a.u_accept[s * a.N + tid];
+  }
+  const float u_next = a.u_sample[s];
+  const int n0 = a.n_nodes ? a.n_nodes[s] : a.N, n = min(max(n0, 0), a.N);
+  if (n0 != n && rank == 0 && tid == 0) flag(a.status, MX4_STATUS_BAD_LEN);
   if (n < 1) {  // an idle sequence (uniform over the cluster)
     if (rank == 0) {
-      for (int j = tid; j < a.N; j += kVerThreads) a.path[s * a.N + j] = -1;
+      if (tid < a.N) a.path[s * a.N + tid] = -1;
       if (tid == 0) {
         a.n_accepted[s] = 0;
         a.next_token[s] = -1;
@@ -155,157 +150,196 @@ __global__ void __launch_bounds__(kVerThreads, kGiven || E == 0 || E == 8 ? 2 : 
     }
     return;
   }
-  const float* tgt = a.target + s * a.t_batch;
-  const float* drf = kGiven ? nullptr : a.draft + s * a.d_batch;
-  for (int j = tid; j < n; j += kVerThreads) {
-    int par = j == 0 ? -1 : a.parents[s * a.N + j];
-    const int tok = a.tokens[s * a.N + j];
-    if (j > 0 && par != -1 && (par < 0 || par >= j || tok < 0 || tok >= a.V)) {
+  const float* const tgt = a.target + s * a.t_batch;
+  const float* const drf = kGiven ? nullptr : a.draft + s * a.d_batch;
+  // The cluster's other CTAs run once they have arrived here: their shared memory may be
+  // written after the wait that goes with it, in front of the first sum.
+  cluster.barrier_arrive();
+  if (tid < kMaxNodes) {
+    if (tid >= n) {
+      par = -1;
+    } else if (par != -1 && (par < 0 || par >= tid || tok < 0 || tok >= a.V)) {
       flag(a.status, MX4_STATUS_BAD_INDEX);
       par = -1;  // never tested
     }
-    s_par[j] = par;
-    s_tok[j] = tok;
-    s_path[j] = -1;
-    s_u[j] = j > 0 ? a.u_accept[s * a.N + j] : 0.f;
-    s_p[j] = par >= 0 ? tgt[par * a.t_node + tok] : 0.f;
-    s_q[j] = par >= 0 ? (kGiven ? 1.f : drf[par * a.d_node + tok]) : 0.f;
-    s_ok[j] = (double)s_u[j] * (double)s_q[j] < (double)s_p[j];
+    s_par[tid] = par;
+    s_tok[tid] = tok;
+    s_path[tid] = tid == 0 ? 0 : -1;
+    s_u[tid] = u;
+    s_p[tid] = par >= 0 ? prob(tgt[par * a.t_node + tok]) : 0.f;
+    s_q[tid] = par >= 0 ? (kGiven ? 1.f : prob(drf[par * a.d_node + tok])) : 0.f;
   }
-  if (tid == 0) s_T[0] = 1ull << 62;
-  if (tid < 3 * kVerMaxCluster) s_part[tid / kVerMaxCluster][tid % kVerMaxCluster] = 0;
-  cluster.sync();  // every CTA of the cluster runs: its shared memory may be written
+  __syncthreads();
 
   // this CTA's part of the vocabulary, and this warp's part of that
   const int c0 = (int)((int64_t)a.V * rank / C), c1 = (int)((int64_t)a.V * (rank + 1) / C);
   auto warp_begin = [&](int w) { return c0 + (int)((int64_t)(c1 - c0) * w / kVerWarps); };
   const int v0 = warp_begin(warp), v1 = warp_begin(warp + 1);
-  int pass = 0;
   bool bad = false;
-  Residual R{tgt, drf, 0, s_T, s_gone};
 
-  // E > 0: W of value v0 + 32 i + lane (given drafts: p, the rejected tokens zeroed) and q
-  constexpr int E1 = E > 0 ? E : 1;
-  uint64_t W[kGiven ? 1 : E1];
-  float f[E1];
+  int cur = 0, k = 0;  // the node; its children rejected so far
+  Factor S;
+  uint64_t gone = 0;   // (given drafts) those, by node
+  const float* p_row = tgt;
+  const float* q_row = drf;
+  // E > 0: values v0 + 32 i + lane of p (of given drafts, the rejected tokens zeroed)
+  float f[E > 0 ? E : 1];
   bool loaded = false;
   auto load = [&](bool with_q) {
-    const float* const pr = R.p + v0 + lane;
     const int left = v1 - v0 - lane;  // values from this lane's first on
-    if constexpr (kGiven) {
+    if constexpr (!kGiven) {
+      if (with_q) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = 32 * i < left ? __ldg(pr + 32 * i) : 0.f;
+        for (int i = 0; i < E; ++i)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(
+                           smem_addr(s_row + kVerThreads * i + tid)),
+                       "l"(32 * i < left ? q_row + v0 + lane + 32 * i : q_row),
+                       "r"(32 * i < left ? 4 : 0)
+                       : "memory");
+      }
+    }
 #pragma unroll
-      for (int i = 0; i < E; ++i) bad |= !prob_ok(f[i]);
-    } else {
-      const float* const qr = R.q + v0 + lane;
+    for (int i = 0; i < E; ++i) f[i] = 32 * i < left ? __ldg(p_row + v0 + lane + 32 * i) : 0.f;
 #pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = with_q && 32 * i < left ? __ldg(qr + 32 * i) : 0.f;
-      constexpr int kAt = E < 16 ? E1 : 16;  // rows of p in flight with them
-#pragma unroll
-      for (int b = 0; b < E; b += kAt) {
-        float pv[kAt];
-#pragma unroll
-        for (int i = 0; i < kAt; ++i) pv[i] = 32 * (b + i) < left ? __ldg(pr + 32 * (b + i)) : 0.f;
-#pragma unroll
-        for (int i = 0; i < kAt; ++i) {
-          bad |= !prob_ok(pv[i]);
-          W[b + i] = to_fixed(pv[i]);
+    for (int i = 0; i < E; ++i) {
+      bad |= !prob_ok(f[i]);
+      f[i] = prob(f[i]);
+    }
+    if constexpr (!kGiven) {
+      if (with_q) {
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+#pragma unroll 8
+        for (int i = 0; i < E; ++i) {  // (a thread's own values: no barrier)
+          const float q = s_row[kVerThreads * i + tid];
+          bad |= !prob_ok(q);
+          s_row[kVerThreads * i + tid] = prob(q);
         }
       }
-#pragma unroll
-      for (int i = 0; i < E; ++i) bad |= !prob_ok(f[i]);
     }
     loaded = true;
   };
-  // the sum of the residual, with the warp and CTA sums left in place `pass % 3`
+  // what is left of value i (in registers), of token v (in memory)
+  auto at_reg = [&](int i) -> uint64_t {
+    if (kGiven || k == 0) return to_fixed(f[i]);
+    return S.left(f[i], s_row[kVerThreads * i + tid]);
+  };
+  auto at_mem = [&](int v, float pv, float qv) -> uint64_t {
+    bad |= !prob_ok(pv) || !prob_ok(qv);
+    if (!kGiven) return k == 0 ? to_fixed(prob(pv)) : S.left(prob(pv), prob(qv));
+    for (uint64_t g = gone; g; g &= g - 1)
+      if (s_tok[__ffsll((long long)g) - 1] == v) return 0;
+    return to_fixed(prob(pv));
+  };
+  // its sum over b0 <= v < b1 by one warp (all lanes get it)
+  auto range_sum = [&](int b0, int b1) {
+    uint64_t sum = 0;
+    const bool two = !kGiven && k > 0;
+    for (int b = b0 + lane; b < b1; b += 32 * kVerUnroll) {
+      float pv[kVerUnroll], qv[kVerUnroll];
+#pragma unroll
+      for (int i = 0; i < kVerUnroll; ++i) {
+        const int v = b + 32 * i;
+        pv[i] = v < b1 ? p_row[v] : 0.f;
+        qv[i] = two && v < b1 ? q_row[v] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kVerUnroll; ++i) sum += at_mem(b + 32 * i, pv[i], qv[i]);
+    }
+    return warp_sum(sum);
+  };
+  // the sum of the residual, with the warp and CTA sums left in place `pass & 1`
+  int pass = 0;
   auto total = [&]() {
-    ++pass;
     uint64_t ws = 0;
     if constexpr (E > 0) {
+      if (kGiven || k == 0) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) ws += kGiven ? to_fixed(f[i]) : W[kGiven ? 0 : i];
+        for (int i = 0; i < E; ++i) ws += to_fixed(f[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) ws += S.left(f[i], s_row[kVerThreads * i + tid]);
+      }
       ws = warp_sum(ws);
     } else {
-      ws = warp_range_sum(R, v0, v1, lane, bad);
+      ws = range_sum(v0, v1);
     }
-    // every warp adds its sum to this CTA's place in all the cluster's CTAs (integers: in any
-    // order); the place after the next is cleared a pass ahead, its readers are long through
-    if (lane == 0) s_warp[pass % 3][warp] = ws;
-    if (lane < C)
-      atomicAdd((unsigned long long*)cluster.map_shared_rank(&s_part[pass % 3][rank], lane),
-                (unsigned long long)ws);
-    if (tid < kVerMaxCluster) s_part[(pass + 1) % 3][tid] = 0;
+    if (pass == 0) cluster.barrier_wait();
+    ++pass;
+    // (the places two passes back have been read by all before the barrier of the last pass)
+    if (lane == 0) s_warp[pass & 1][warp] = ws;
+    __syncthreads();
+    if (warp == 0) {
+      const uint64_t cs = warp_sum(lane < kVerWarps ? s_warp[pass & 1][lane] : 0);
+      if (lane < C) *cluster.map_shared_rank(&s_part[pass & 1][rank], lane) = cs;
+    }
     cluster.sync();
     uint64_t t = 0;
-    for (int i = 0; i < C; ++i) t += s_part[pass % 3][i];
+    for (int i = 0; i < C; ++i) t += s_part[pass & 1][i];
     return t;
   };
 
-  int cur = 0, acc = 1;
-  bool shut = false, summed = false;  // summed: the last pass is of the current residual
+  // children of cur, by node (they come after it)
+  auto children = [&]() {
+    return (uint64_t)__ballot_sync(0xFFFFFFFFu, s_par[lane] == cur) |
+           (uint64_t)__ballot_sync(0xFFFFFFFFu, s_par[32 + lane] == cur) << 32;
+  };
+  int acc = 1;
+  bool summed = false;  // the last pass is of the present residual
   uint64_t T = 1ull << 62;
-  if (tid == 0) s_path[0] = 0;
-  for (int j = 1; j < n; ++j) {
-    if (s_par[j] != cur || shut) continue;
+  for (uint64_t kids = children(); kids;) {
+    const int j = __ffsll((long long)kids) - 1;
+    kids &= kids - 1;
     const float pv = s_p[j], qv = s_q[j];
-    bool ok = s_ok[j];
-    if (R.k > 0) {
-      if (tid == 0) {
-        const double w = (double)R.of(s_tok[j], pv, qv);
-        s_now = (double)s_u[j] * (double)T * (double)qv < w;
-      }
-      __syncthreads();
-      ok = s_now;
+    uint64_t w = 0;  // what is left of its token
+    bool ok;
+    if constexpr (kGiven) {
+      w = at_mem(s_tok[j], pv, 0.f);
+      ok = k == 0 ? s_u[j] < pv : __umul64hi(uniform_fixed(s_u[j]), T) < w;
+    } else {
+      // floor(u T q) < W, both integers, T q rounded down to one
+      ok = k == 0 ? stands(s_u[j], qv, pv)
+                  : __umul64hi(uniform_fixed(s_u[j]), __umul64hi(T << 1, to_fixed(qv) << 1)) <
+                        S.left(pv, qv);
     }
     if (ok) {
       cur = j;
-      R = Residual{tgt + (int64_t)j * a.t_node, kGiven ? nullptr : drf + (int64_t)j * a.d_node, 0,
-                   s_T, s_gone};
+      p_row = tgt + (int64_t)j * a.t_node;
+      if constexpr (!kGiven) q_row = drf + (int64_t)j * a.d_node;
+      S = Factor{};
       T = 1ull << 62;
+      k = 0;
+      gone = 0;
       summed = loaded = false;
       if (tid == 0) s_path[acc] = j;
       ++acc;
+      kids = children();
       continue;
     }
-    // rejected: T (of k rejections) is known; the residual of k + 1
-    if constexpr (E > 0 && kGiven) {
+    if (E > 0 && !loaded) load(true);
+    if constexpr (kGiven) {
       // its sum is the row's (the only one that is summed) less what has been rejected
-      if (!loaded) load(false);
-      if (R.k == 0) T = total();
-      T -= R.of(s_tok[j], pv, 1.f);
-      const int at = s_tok[j] - v0 - lane;
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (at == 32 * i && s_tok[j] < v1) f[i] = 0.f;
-      summed = false;
-      __syncthreads();  // the walk above has read s_gone
-      if (tid == 0) s_gone[R.k] = s_tok[j];
-      ++R.k;
-      __syncthreads();
-    } else {
+      if (k == 0) T = total();
+      T -= w;
       if constexpr (E > 0) {
-        if (!loaded) load(true);
+        const int at = s_tok[j] - v0 - lane;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const uint64_t qf = to_fixed(f[i]), t = R.k == 0 ? qf : mul_fixed(T, qf);
-          W[kGiven ? 0 : i] = W[kGiven ? 0 : i] > t ? W[kGiven ? 0 : i] - t : 0;
-        }
+        for (int i = 0; i < E; ++i)
+          if (at == 32 * i && s_tok[j] < v1) f[i] = 0.f;
       }
-      __syncthreads();  // the walk above has read s_T and s_gone
-      if (tid == 0) {
-        s_T[R.k] = T;
-        s_gone[R.k] = s_tok[j];
-      }
-      ++R.k;
-      __syncthreads();
+      gone |= 1ull << j;
+      summed = false;
+      ++k;
+    } else {
+      S.add(T);
+      ++k;
       T = total();
       summed = true;
     }
     if (T == 0) {  // nothing left (p <= q everywhere): draw from p itself
-      shut = true;
-      R.k = 0;
+      k = 0;
+      gone = 0;
       summed = loaded = false;
+      break;
     }
   }
   if (!summed) {
@@ -314,16 +348,11 @@ __global__ void __launch_bounds__(kVerThreads, kGiven || E == 0 || E == 8 ? 2 : 
   }
 
   // the next token: the first v whose running sum exceeds u T
-  // (u in units of 2^-64: its 24 bits, shifted)
-  const uint32_t ub = __float_as_uint(fminf(fmaxf(a.u_sample[s], 0.f), 0x1.fffffep-1f));
-  const uint64_t um = (ub & 0x7FFFFFu) | 0x800000u;
-  const int ue = (int)(ub >> 23) - 86;
-  const uint64_t ui = ub < 0x00800000u ? 0ull : ue >= 0 ? um << ue : ue > -64 ? um >> -ue : 0ull;
-  const uint64_t left = __umul64hi(ui, T);
+  const uint64_t left = __umul64hi(uniform_fixed(u_next), T);
   int at = -1;  // the CTA
   uint64_t before = 0;
   for (int i = 0; i < C; ++i) {
-    const uint64_t cs = s_part[pass % 3][i];
+    const uint64_t cs = s_part[pass & 1][i];
     if (at < 0 && before + cs > left) at = i;
     if (at < 0) before += cs;
   }
@@ -344,7 +373,7 @@ __global__ void __launch_bounds__(kVerThreads, kGiven || E == 0 || E == 8 ? 2 : 
   if (at == rank) {
     int w = 0;
     for (; w < kVerWarps - 1; ++w) {
-      const uint64_t x = s_warp[pass % 3][w];
+      const uint64_t x = s_warp[pass & 1][w];
       if (before + x > left) break;
       before += x;
     }
@@ -352,12 +381,11 @@ __global__ void __launch_bounds__(kVerThreads, kGiven || E == 0 || E == 8 ? 2 : 
       if (warp == w) {
         int found = v1 - 1;
         bool done = false;
-        constexpr int kGroup = E < 8 ? E : 8;  // eight rows of 32 at a time, then one
 #pragma unroll
-        for (int b = 0; b < E; b += kGroup) {
+        for (int b = 0; b < E; b += 8) {  // eight rows of 32 at a time, then one
           uint64_t x = 0;
 #pragma unroll
-          for (int i = b; i < b + kGroup; ++i) x += kGiven ? to_fixed(f[i]) : W[kGiven ? 0 : i];
+          for (int i = b; i < b + 8; ++i) x += at_reg(i);
           x = warp_sum(x);
           if (done) continue;
           if (before + x <= left) {
@@ -365,10 +393,8 @@ __global__ void __launch_bounds__(kVerThreads, kGiven || E == 0 || E == 8 ? 2 : 
             continue;
           }
 #pragma unroll
-          for (int i = b; i < b + kGroup; ++i)
-            if (!done)
-              done = pick(v0 + 32 * i, v0 + 32 * i + lane < v1,
-                          kGiven ? to_fixed(f[i]) : W[kGiven ? 0 : i], found);
+          for (int i = b; i < b + 8; ++i)
+            if (!done) done = pick(v0 + 32 * i, v0 + 32 * i + lane < v1, at_reg(i), found);
           done = true;
         }
         if (lane == 0) a.next_token[s] = found;
@@ -377,7 +403,7 @@ __global__ void __launch_bounds__(kVerThreads, kGiven || E == 0 || E == 8 ? 2 : 
       // the warp's part in sixteenths, then one warp's sixteenth 32 values at a time
       const int w0 = warp_begin(w), w1 = warp_begin(w + 1);
       auto sub = [&](int i) { return w0 + (int)((int64_t)(w1 - w0) * i / kVerWarps); };
-      const uint64_t x = warp_range_sum(R, sub(warp), sub(warp + 1), lane, bad);
+      const uint64_t x = range_sum(sub(warp), sub(warp + 1));
       if (lane == 0) s_sub[warp] = x;
       __syncthreads();
       int i = 0;
@@ -386,12 +412,12 @@ __global__ void __launch_bounds__(kVerThreads, kGiven || E == 0 || E == 8 ? 2 : 
         before += s_sub[i];
       }
       if (warp == 0) {
-        const bool two = R.q != nullptr && R.k > 0;
+        const bool two = !kGiven && k > 0;
         int found = sub(i + 1) - 1;
         for (int b = sub(i); b < sub(i + 1); b += 32) {
           const int v = b + lane;
           const bool in = v < sub(i + 1);
-          if (pick(b, in, in ? R.of(v, R.p[v], two ? R.q[v] : 0.f) : 0, found)) break;
+          if (pick(b, in, in ? at_mem(v, p_row[v], two ? q_row[v] : 0.f) : 0, found)) break;
         }
         if (lane == 0) a.next_token[s] = found;
       }
@@ -404,14 +430,22 @@ __global__ void __launch_bounds__(kVerThreads, kGiven || E == 0 || E == 8 ? 2 : 
     }
     if (tid == 0) a.n_accepted[s] = acc;
     __syncthreads();
-    for (int j = tid; j < a.N; j += kVerThreads) a.path[s * a.N + j] = j < n ? s_path[j] : -1;
+    if (tid < a.N) a.path[s * a.N + tid] = s_path[tid];
   }
   if (bad) flag(a.status, MX4_STATUS_BAD_VALUE);
-  cluster.sync();  // no CTA leaves while another may still write to its shared memory
 }
 
 template <int E>
-cudaError_t launch_verify_e(const VerifyArgs& a, const cudaLaunchConfig_t& cfg) {
+cudaError_t launch_verify_e(const VerifyArgs& a, cudaLaunchConfig_t& cfg) {
+  if (a.draft) {
+    cfg.dynamicSmemBytes = E * kVerThreads * sizeof(float);
+    if (cfg.dynamicSmemBytes > 40 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(verify_kernel<E, false>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)cfg.dynamicSmemBytes);
+      if (e != cudaSuccess) return e;
+    }
+  }
   return a.draft ? cudaLaunchKernelEx(&cfg, verify_kernel<E, false>, a)
                  : cudaLaunchKernelEx(&cfg, verify_kernel<E, true>, a);
 }
