@@ -27,11 +27,10 @@ namespace mx4 {
 //   W_k = max(p - S_k q, 0),   S_k = T_0 + ... + T_{k-1}:
 // p, q and one number give every residual, none is kept.
 //
-// Sums are exact: W is a 64-bit integer in units of 2^-62 (fp32 probabilities of at least
-// 2^-38 without any rounding; S to 32 significant bits, 2^-8 of the step of the fp32 q that it
-// scales), so no order of summation and no cluster size changes a decision.  There is no fp64
-// (this GPU's rate is a hundredth of its fp32 rate): a residual costs some twenty 32-bit
-// operations.
+// W is rounded as p is, to fp32 (S has 48 bits, so no more is lost where p and S q cancel), and
+// summed exactly: as a 64-bit integer in units of 2^-62, so that no order of summation and no
+// cluster size changes a decision.  There is no fp64 (this GPU's rate is a hundredth of its
+// fp32 rate): a residual costs some dozen 32-bit operations.
 //
 // One cluster of CTAs per sequence, each CTA one contiguous part of the vocabulary, each warp
 // one of that.  What the walk looks up (parents, tokens, random numbers, p and q of each draft
@@ -95,23 +94,20 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
   return x;
 }
 
-// S_k, as m 2^(x - 31) with 2^31 <= m < 2^32; at 0 there is none
+// S_k as the sum of two fp32 numbers (48 bits), and a residual by it
 struct Factor {
   uint64_t sum = 0;  // in units of 2^-56 (S <= 64)
-  uint32_t m = 0;
-  int x = 0;
+  float hi = 0.f, lo = 0.f;
   __device__ __forceinline__ void add(uint64_t T) {
     sum += T >> 6;
     const int lz = __clzll((long long)sum);
-    m = (uint32_t)((sum << lz) >> 32);
-    x = 7 - lz;
+    const uint64_t m = sum << lz;  // S = m 2^(-56 - lz)
+    const float e = __uint_as_float((uint32_t)(127 - 16 - lz) << 23);
+    hi = (float)(uint32_t)(m >> 40) * e;
+    lo = (float)((uint32_t)(m >> 16) & 0xFFFFFFu) * 0x1p-24f * e;
   }
-  // max(p - S q, 0); S q >= 1 >= p where the shift would be to the left
   __device__ __forceinline__ uint64_t left(float p, float q) const {
-    const uint64_t w = to_fixed(p);
-    const uint32_t b = __float_as_uint(q);
-    const uint64_t t = shift_down((uint64_t)(b << 8 | 0x80000000u) * m, max(127 - x - (int)(b >> 23), 0));
-    return w > t ? w - t : 0;
+    return to_fixed(fmaxf(fmaf(-lo, q, fmaf(-hi, q, p)), 0.f));
   }
 };
 
