@@ -168,8 +168,11 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   __syncthreads();
 
   // this CTA's part of the vocabulary, and this warp's part of that
-  const int c0 = (int)((int64_t)a.V * rank / C), c1 = (int)((int64_t)a.V * (rank + 1) / C);
-  auto warp_begin = [&](int w) { return c0 + (int)((int64_t)(c1 - c0) * w / kVerWarps); };
+  // (V <= 2^24; C is a power of two)
+  const int log2c = 31 - __clz(C);
+  auto cta_begin = [&](int r) { return a.V * r >> log2c; };
+  const int c0 = cta_begin(rank), c1 = cta_begin(rank + 1);
+  auto warp_begin = [&](int w) { return c0 + (c1 - c0) * w / kVerWarps; };
   const int v0 = warp_begin(warp), v1 = warp_begin(warp + 1);
   bool bad = false;
 
@@ -270,7 +273,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     }
     cluster.sync();
     uint64_t t = 0;
-    for (int i = 0; i < C; ++i) t += s_part[pass & 1][i];
+#pragma unroll
+    for (int i = 0; i < kVerMaxCluster; ++i) t += i < C ? s_part[pass & 1][i] : 0;
     return t;
   };
 
@@ -313,17 +317,18 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     }
     if (E > 0 && !loaded) load(true);
     if constexpr (kGiven) {
-      // its sum is the row's (the only one that is summed) less what has been rejected
+      // the row is summed once; what has been rejected is taken off that sum, and in the end
+      // off the CTA's and the warp's that hold it
       if (k == 0) T = total();
       T -= w;
+      summed = true;
       if constexpr (E > 0) {
         const int at = s_tok[j] - v0 - lane;
 #pragma unroll
         for (int i = 0; i < E; ++i)
           if (at == 32 * i && s_tok[j] < v1) f[i] = 0.f;
       }
-      gone |= 1ull << j;
-      summed = false;
+      if (w != 0) gone |= 1ull << j;  // (a token once)
       ++k;
     } else {
       S.add(T);
@@ -343,57 +348,68 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     T = total();
   }
 
+  // of a sum over b0 <= v < b1, less what has been rejected there
+  auto kept = [&](uint64_t sum, int b0, int b1) -> uint64_t {
+    if (kGiven)
+      for (uint64_t g = gone; g; g &= g - 1) {
+        const int j = __ffsll((long long)g) - 1;
+        if (s_tok[j] >= b0 && s_tok[j] < b1) sum -= to_fixed(s_p[j]);
+      }
+    return sum;
+  };
   // the next token: the first v whose running sum exceeds u T
   const uint64_t left = __umul64hi(uniform_fixed(u_next), T);
-  int at = -1;  // the CTA
+  // the first lane whose running sum of x exceeds `left` (-1: none); `before` goes on to it
   uint64_t before = 0;
-  for (int i = 0; i < C; ++i) {
-    const uint64_t cs = s_part[pass & 1][i];
-    if (at < 0 && before + cs > left) at = i;
-    if (at < 0) before += cs;
-  }
-  if (T == 0) at = -1;  // a row of zeros: no token
-  // the first of 32 values b + lane (value x each) whose running sum exceeds `left`
-  auto pick = [&](int b, bool in, uint64_t x, int& found) {
-    uint64_t inc = in ? x : 0;
+  auto scan = [&](uint64_t x) {
+    uint64_t inc = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
       if (lane >= o) inc += y;
     }
-    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, in && before + inc > left);
-    if (hit) found = b + __ffs(hit) - 1;
-    before += __shfl_sync(0xFFFFFFFFu, inc, 31);
-    return hit != 0u;
+    const int l = __ffs(__ballot_sync(0xFFFFFFFFu, before + inc > left)) - 1;
+    before += __shfl_sync(0xFFFFFFFFu, l < 0 ? inc : inc - x, l < 0 ? 31 : l);
+    return l;
   };
+  int at = scan(lane < C ? kept(s_part[pass & 1][lane & (kVerMaxCluster - 1)], cta_begin(lane),
+                                cta_begin(lane + 1)) : 0);  // the CTA
+  if (T == 0) at = -1;  // a row of zeros: no token
   if (at == rank) {
-    int w = 0;
-    for (; w < kVerWarps - 1; ++w) {
-      const uint64_t x = s_warp[pass & 1][w];
-      if (before + x > left) break;
-      before += x;
-    }
+    // (one is always found, but for rows whose sum leaves 64 bits)
+    const int w = scan(lane < kVerWarps ? kept(s_warp[pass & 1][lane & (kVerWarps - 1)],
+                                               warp_begin(lane), warp_begin(lane + 1)) : 0) &
+                  (kVerWarps - 1);
     if constexpr (E > 0) {
       if (warp == w) {
-        int found = v1 - 1;
-        bool done = false;
+        // the sums of the rows of 32 values, lane i that of row i: four rows at a time, of
+        // which a lane keeps half in each of two steps
+        uint64_t mine = 0;
 #pragma unroll
-        for (int b = 0; b < E; b += 8) {  // eight rows of 32 at a time, then one
-          uint64_t x = 0;
+        for (int b = 0; b < E; b += 4) {
+          uint64_t x[4];
 #pragma unroll
-          for (int i = b; i < b + 8; ++i) x += at_reg(i);
-          x = warp_sum(x);
-          if (done) continue;
-          if (before + x <= left) {
-            before += x;
-            continue;
+          for (int i = 0; i < 4; ++i) x[i] = at_reg(b + i);
+#pragma unroll
+          for (int o = 2; o > 0; o >>= 1) {
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int i = 0; i < o; ++i) {
+              const uint64_t send = up ? x[i] : x[i + o], keep = up ? x[i + o] : x[i];
+              x[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+            }
           }
 #pragma unroll
-          for (int i = b; i < b + 8; ++i)
-            if (!done) done = pick(v0 + 32 * i, v0 + 32 * i + lane < v1, at_reg(i), found);
-          done = true;
+          for (int o = 4; o < 32; o <<= 1) x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], o);
+          if (lane >> 2 == b >> 2) mine = x[0];
         }
-        if (lane == 0) a.next_token[s] = found;
+        const int row = scan(mine);
+        uint64_t x = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (i == row) x = at_reg(i);
+        const int l = scan(x);
+        if (lane == 0) a.next_token[s] = row < 0 || l < 0 ? v1 - 1 : min(v0 + 32 * row + l, v1 - 1);
       }
     } else {
       // the warp's part in sixteenths, then one warp's sixteenth 32 values at a time
@@ -412,8 +428,11 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
         int found = sub(i + 1) - 1;
         for (int b = sub(i); b < sub(i + 1); b += 32) {
           const int v = b + lane;
-          const bool in = v < sub(i + 1);
-          if (pick(b, in, in ? at_mem(v, p_row[v], two ? q_row[v] : 0.f) : 0, found)) break;
+          const int l = scan(v < sub(i + 1) ? at_mem(v, p_row[v], two ? q_row[v] : 0.f) : 0);
+          if (l >= 0) {
+            found = b + l;
+            break;
+          }
         }
         if (lane == 0) a.next_token[s] = found;
       }
