@@ -38,7 +38,9 @@ namespace mx4 {
 // At a node's first rejection its rows are read, once: a thread keeps E values of p in
 // registers and of q in shared memory (a row of 131072 values by eight CTAs, two an SM), and
 // every further rejection of a sibling, the sums and the drawing of the next token work on
-// those.  E = 0, for vocabularies above 8 x 16384: the rows are read again.
+// those.  E = 0, for vocabularies above 8 x 16384: the rows are read again.  So are those of
+// given drafts, whose rejections take one token off the sum: a row is read once, and then the
+// 256th of it that the next token is in.
 // Every thread runs the walk itself on the same numbers, so it needs no broadcast.
 constexpr int kMaxNodes = 64;
 constexpr int kVerThreads = 512;
@@ -181,21 +183,19 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   uint64_t gone = 0;   // (given drafts) those, by node
   const float* p_row = tgt;
   const float* q_row = drf;
-  // E > 0: values v0 + 32 i + lane of p (of given drafts, the rejected tokens zeroed)
+  // E > 0: values v0 + 32 i + lane of p
   float f[E > 0 ? E : 1];
   bool loaded = false;
   auto load = [&](bool with_q) {
     const int left = v1 - v0 - lane;  // values from this lane's first on
-    if constexpr (!kGiven) {
-      if (with_q) {
+    if (with_q) {
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(
-                           smem_addr(s_row + kVerThreads * i + tid)),
-                       "l"(32 * i < left ? q_row + v0 + lane + 32 * i : q_row),
-                       "r"(32 * i < left ? 4 : 0)
-                       : "memory");
-      }
+      for (int i = 0; i < E; ++i)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(
+                         smem_addr(s_row + kVerThreads * i + tid)),
+                     "l"(32 * i < left ? q_row + v0 + lane + 32 * i : q_row),
+                     "r"(32 * i < left ? 4 : 0)
+                     : "memory");
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) f[i] = 32 * i < left ? __ldg(p_row + v0 + lane + 32 * i) : 0.f;
@@ -204,22 +204,20 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
       bad |= !prob_ok(f[i]);
       f[i] = prob(f[i]);
     }
-    if constexpr (!kGiven) {
-      if (with_q) {
-        asm volatile("cp.async.wait_all;\n" ::: "memory");
+    if (with_q) {
+      asm volatile("cp.async.wait_all;\n" ::: "memory");
 #pragma unroll 8
-        for (int i = 0; i < E; ++i) {  // (a thread's own values: no barrier)
-          const float q = s_row[kVerThreads * i + tid];
-          bad |= !prob_ok(q);
-          s_row[kVerThreads * i + tid] = prob(q);
-        }
+      for (int i = 0; i < E; ++i) {  // (a thread's own values: no barrier)
+        const float q = s_row[kVerThreads * i + tid];
+        bad |= !prob_ok(q);
+        s_row[kVerThreads * i + tid] = prob(q);
       }
     }
     loaded = true;
   };
   // what is left of value i (in registers), of token v (in memory)
   auto at_reg = [&](int i) -> uint64_t {
-    if (kGiven || k == 0) return to_fixed(f[i]);
+    if (k == 0) return to_fixed(f[i]);
     return S.left(f[i], s_row[kVerThreads * i + tid]);
   };
   auto at_mem = [&](int v, float pv, float qv) -> uint64_t {
@@ -251,7 +249,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   auto total = [&]() {
     uint64_t ws = 0;
     if constexpr (E > 0) {
-      if (kGiven || k == 0) {
+      if (k == 0) {
 #pragma unroll
         for (int i = 0; i < E; ++i) ws += to_fixed(f[i]);
       } else {
@@ -322,12 +320,6 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
       if (k == 0) T = total();
       T -= w;
       summed = true;
-      if constexpr (E > 0) {
-        const int at = s_tok[j] - v0 - lane;
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (at == 32 * i && s_tok[j] < v1) f[i] = 0.f;
-      }
       if (w != 0) gone |= 1ull << j;  // (a token once)
       ++k;
     } else {
@@ -414,24 +406,27 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     } else {
       // the warp's part in sixteenths, then one warp's sixteenth 32 values at a time
       const int w0 = warp_begin(w), w1 = warp_begin(w + 1);
-      auto sub = [&](int i) { return w0 + (int)((int64_t)(w1 - w0) * i / kVerWarps); };
+      auto sub = [&](int i) { return w0 + (w1 - w0) * i / kVerWarps; };
       const uint64_t x = range_sum(sub(warp), sub(warp + 1));
       if (lane == 0) s_sub[warp] = x;
       __syncthreads();
-      int i = 0;
-      for (; i < kVerWarps - 1; ++i) {
-        if (before + s_sub[i] > left) break;
-        before += s_sub[i];
-      }
       if (warp == 0) {
+        const int i = scan(lane < kVerWarps ? s_sub[lane & (kVerWarps - 1)] : 0) & (kVerWarps - 1);
         const bool two = !kGiven && k > 0;
-        int found = sub(i + 1) - 1;
-        for (int b = sub(i); b < sub(i + 1); b += 32) {
-          const int v = b + lane;
-          const int l = scan(v < sub(i + 1) ? at_mem(v, p_row[v], two ? q_row[v] : 0.f) : 0);
-          if (l >= 0) {
-            found = b + l;
-            break;
+        int found = sub(i + 1) - 1, l = -1;
+        for (int b = sub(i); b < sub(i + 1) && l < 0; b += 32 * kVerUnroll) {
+          float pv[kVerUnroll], qv[kVerUnroll];
+#pragma unroll
+          for (int r = 0; r < kVerUnroll; ++r) {
+            const int v = b + 32 * r + lane;
+            pv[r] = v < sub(i + 1) ? p_row[v] : 0.f;
+            qv[r] = two && v < sub(i + 1) ? q_row[v] : 0.f;
+          }
+#pragma unroll
+          for (int r = 0; r < kVerUnroll; ++r) {
+            if (l >= 0) continue;
+            l = scan(at_mem(b + 32 * r + lane, pv[r], qv[r]));
+            if (l >= 0) found = min(b + 32 * r + l, found);
           }
         }
         if (lane == 0) a.next_token[s] = found;
@@ -452,17 +447,14 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
 
 template <int E>
 cudaError_t launch_verify_e(const VerifyArgs& a, cudaLaunchConfig_t& cfg) {
-  if (a.draft) {
-    cfg.dynamicSmemBytes = E * kVerThreads * sizeof(float);
-    if (cfg.dynamicSmemBytes > 40 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(verify_kernel<E, false>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)cfg.dynamicSmemBytes);
-      if (e != cudaSuccess) return e;
-    }
+  cfg.dynamicSmemBytes = E * kVerThreads * sizeof(float);
+  if (cfg.dynamicSmemBytes > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(verify_kernel<E, false>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
   }
-  return a.draft ? cudaLaunchKernelEx(&cfg, verify_kernel<E, false>, a)
-                 : cudaLaunchKernelEx(&cfg, verify_kernel<E, true>, a);
+  return cudaLaunchKernelEx(&cfg, verify_kernel<E, false>, a);
 }
 
 cudaError_t launch_verify(const float* target, const float* draft, const int64_t* strides,
@@ -473,10 +465,11 @@ cudaError_t launch_verify(const float* target, const float* draft, const int64_t
   VerifyArgs a{target, draft, strides[0], strides[1], strides[2], strides[3], tokens, parents,
                u_accept, u_sample, n_nodes, N, V, path, n_accepted, next_token, status};
   // CTAs a sequence: few (an exchange costs the more), but enough that a thread keeps at most
-  // 32 values, and that a small batch takes about two CTAs an SM of 2048 values or more
+  // 32 values (of rows that are kept), and that a small batch takes about two CTAs an SM of 2048
+  // values or more
   int C = 1;
-  while (C < kVerMaxCluster &&
-         (V > (int64_t)C * kVerThreads * 32 || (B * C * 2 <= 2 * (int64_t)num_sms && V / C > 4096)))
+  while (C < kVerMaxCluster && ((draft && V > (int64_t)C * kVerThreads * 32) ||
+                                (B * C * 2 <= 2 * (int64_t)num_sms && V / C > 4096)))
     C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * C));
@@ -492,6 +485,7 @@ cudaError_t launch_verify(const float* target, const float* draft, const int64_t
   cfg.numAttrs = 2;
   // the largest part of a warp, in rows of 32 values
   const int part = ((V + C - 1) / C + kVerWarps - 1) / kVerWarps, rows = (part + 31) / 32;
+  if (!draft) return cudaLaunchKernelEx(&cfg, verify_kernel<0, true>, a);
   if (rows > 32) return launch_verify_e<0>(a, cfg);
   if (rows > 16) return launch_verify_e<32>(a, cfg);
   if (rows > 8) return launch_verify_e<16>(a, cfg);
