@@ -30,13 +30,16 @@
 // CTA.  A tile cut by a range's end leaves a partial record (O, reference, sum) in the
 // workspace, and a second kernel joins the records of each cut tile.
 //
-// A CTA goes through its pages in order, eight warps doing the same: a sixteenth of V's
-// dequantisation each half warp, then the softmax (two groups of four warps, each half of the
-// rows; one lane a token), one barrier a page.  Two more warps issue what is asynchronous: one
-// the products (P V of the page before, S of the page ahead, two accumulators), one the copies.
-// Two CTAs an SM fill each other's waits.  (Warps of fixed roles handing pages to each other by
-// barriers, 12 to 20 a CTA, took two to three times as long: each hand-over cost a few hundred
-// cycles.)
+// A CTA goes through its pages in order, all its warps doing the same: their part of V's
+// dequantisation, then the softmax (groups of four warps, each some of the rows; one lane a
+// token), one barrier a page.  Two more warps issue what is asynchronous: one the products (P V
+// of the page before, S of the page ahead, two accumulators), one the copies.  Up to 64 rows a
+// tile there are two groups a CTA and two CTAs an SM, which fill each other's waits.  More rows
+// share a page's fixed costs (V's dequantisation, the barrier, the products' latency) in tiles of
+// 128 by four groups and one CTA an SM: 16 trees of 64 nodes and 16 heads over 4096 to 65536
+// tokens took 564 us in tiles of 64, 460 in tiles of 128.  (Warps of fixed roles handing pages to
+// each other by barriers, 12 to 20 a CTA, took two to three times as long: each hand-over cost a
+// few hundred cycles.)
 // All waits are bounded; after one that runs out the CTA goes through its loop without waiting
 // or issuing, and the status word says so.
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
@@ -54,8 +57,6 @@ constexpr int kMaxSeq = 256;       // sequences per launch
 constexpr float kLazy = 12.f;      // log2 units a logit may lie above its row's reference
 constexpr float kUnset = -3e38f;   // the reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWorkers = 256;            // the eight warps that compute
-constexpr int kThreads = kWorkers + 64;  // one that issues the products, one the copies
 constexpr int kKTile = 128 * 128;  // K operand tile
 // V operand: rows of 64 dims (128 bytes) a token, in 128-byte swizzle atoms of 8 tokens (the
 // 16-byte chunks of row r XOR-permuted by r % 8), 16 atoms, then the other 64 dims.
@@ -65,11 +66,15 @@ constexpr int kVHalf = kVTile / 2;
 // 8 rows kChunk bytes on.
 constexpr int kChunk = 128 * 16;
 
-// A configuration: NR rows a tile, KS and VS stages of K and V pages, CTAs an SM.
-template <int NR_, int KS_, int VS_, int CTAS_>
+// A configuration: NR rows a tile, softmax groups of four warps each, KS and VS stages of K and
+// V pages, CTAs an SM.
+template <int NR_, int GROUPS_, int KS_, int VS_, int CTAS_>
 struct Cfg {
   static constexpr int NR = NR_, KS = KS_, VS = VS_, CTAS = CTAS_;
-  static constexpr int NC = NR / 2;  // rows of a softmax group
+  static constexpr int NC = NR / GROUPS_;  // rows of a softmax group
+  static constexpr int kWorkers = 128 * GROUPS_;   // the threads that compute
+  static constexpr int kThreads = kWorkers + 64;   // a warp more for the products, one for the copies
+  static constexpr int kVSteps = 16 / (kWorkers / 32);  // V's dequantisation, 8 tokens a warp each
   // hi and lo of q as one operand of 2 NR rows (K read once, their products added by the
   // softmax) while that is cheap there
   static constexpr bool kTwin = NR <= 32;
@@ -126,7 +131,7 @@ struct Lay {
   static constexpr int kInfo = kStart + 24;                  // [4] valid tokens of loaded pages
   static constexpr int kMore = kInfo + 16;                   // [3] a page asks for new references
   static constexpr int kMisc = kMore + 16;                   // abort, tmem address, scan space
-  static constexpr int kBytes = kMisc + 8 + 12 * 4 + 1024;    // + slack for the 1024-byte alignment
+  static constexpr int kBytes = kMisc + 8 + 20 * 4 + 1024;    // + slack for the 1024-byte alignment
   static_assert(kV % 1024 == 0 && kVraw % 16 == 0 && kRef % 16 == 0 && kMask % 8 == 0 &&
                 kOff % 8 == 0, "alignment");
   static_assert(C::CTAS * (kBytes + 1024) <= 228 * 1024, "shared memory");
@@ -345,10 +350,11 @@ struct Start {
 constexpr int kMinPages = 2;
 
 template <class C>
-__global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid_constant__ Args a) {
   using L_ = Lay<C>;
   using T_ = Tm<C>;
   constexpr int NR = C::NR, NC = C::NC, KS = C::KS, VS = C::VS, W = NC < 16 ? NC : 16;
+  constexpr int kWorkers = C::kWorkers, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   // (by an offset, not by rounding the pointer: it stays a pointer to shared memory)
   uint8_t* const sm = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
@@ -825,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
       sync_all();
 #pragma unroll 1
       for (int e = cu.e0; e < cu.e1; ++e, ++k) {
-                const int first = page_no(sp, e) * kPageTokens, live = s_info[k & 3];
+        const int first = page_no(sp, e) * kPageTokens, live = s_info[k & 3];
         const bool plain = live == kPageTokens && first + kPageTokens <= sp.base &&
                            (a.window == 0 || first > sp.base + 63 - a.window ||
                             first + kPageTokens <= a.sinks);
@@ -835,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
         // conflicts.
         auto convert_v = [&](int it, uint32_t (&y)[4][4]) {
           const uint8_t* raw = sm + L_::kVraw + (k % VS) * kPageBytes;
-          const int m = (warp * 2 + it) * 8 + r8, tk = 4 * (m & 31) + (m >> 5);
+          const int m = (warp * C::kVSteps + it) * 8 + r8, tk = 4 * (m & 31) + (m >> 5);
           const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tk * kRowDataBytes + blk * 16);
           const uint32_t sc = raw[kScaleOffset + tk * kRowScaleBytes + blk];
           const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
@@ -865,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
           }
         };
         auto store_v = [&](int it, const uint32_t (&y)[4][4]) {
-          const int m = (warp * 2 + it) * 8 + r8;
+          const int m = (warp * C::kVSteps + it) * 8 + r8;
           uint8_t* const dst = sm + L_::kV + (blk >> 1) * kVHalf + (m >> 3) * 1024 + r8 * 128;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -881,8 +887,10 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
           convert_v(0, yv);
           if (k > 0) wait(kPvDone, (k - 1) & 1);
           store_v(0, yv);
-          convert_v(1, yv);
-          store_v(1, yv);
+          if constexpr (C::kVSteps > 1) {
+            convert_v(1, yv);
+            store_v(1, yv);
+          }
         }
         // ---- logits in log2 units relative to the rows' references
         // a row sees a draft by its mask, an earlier token from the window's first on; rows
@@ -1016,19 +1024,21 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) tree_kernel(const __grid_co
           if (round == 0) {
             if constexpr (VS == 1) {
               wait(kVFull + k % VS, (k / VS) & 1);
-              convert_v(0, yv);
-              store_v(0, yv);
-              convert_v(1, yv);
-              store_v(1, yv);
+#pragma unroll
+              for (int it = 0; it < C::kVSteps; ++it) {
+                convert_v(it, yv);
+                store_v(it, yv);
+              }
             }
-        // NaN dim blocks of this lane's token
-        uint32_t vw = *reinterpret_cast<const uint32_t*>(sm + L_::kVraw + (k % VS) * kPageBytes + kScaleOffset + tok * kRowScaleBytes);
-        vw = ((vw & 0x7F7F7F7Fu) + 0x01010101u) & vw & 0x80808080u;
-        if (vw != 0u && tok < live) {  // the rows that see the token get its NaNs at the end
-#pragma unroll 1
-          for (int c = 0; c < NC; ++c)
-            if ((vis >> c) & 1u) atomicOr(s_nan + c, vw);
-        }
+            // NaN dim blocks of this lane's token
+            uint32_t vw = *reinterpret_cast<const uint32_t*>(
+                sm + L_::kVraw + (k % VS) * kPageBytes + kScaleOffset + tok * kRowScaleBytes);
+            vw = ((vw & 0x7F7F7F7Fu) + 0x01010101u) & vw & 0x80808080u;
+            if (vw != 0u && tok < live) {  // the rows that see the token get its NaNs at the end
+    #pragma unroll 1
+              for (int c = 0; c < NC; ++c)
+                if ((vis >> c) & 1u) atomicOr(s_nan + c, vw);
+            }
           }
           fence_async();
           fence_before();
@@ -1219,7 +1229,7 @@ cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
     a.seq_lens += b0;
     if (a.n_nodes) a.n_nodes += b0;
     if (a.mask) a.mask += b0 * a.N;
-    e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, a);
+    e = launch_pdl(kern, dim3(grid), dim3(C::kThreads), smem, stream, a);
     if (e != cudaSuccess) return e;
     e = launch_pdl(tree_merge_kernel<C::NR>, dim3(grid, C::NR / 4), dim3(128), 0, stream, a);
     if (e != cudaSuccess) return e;
@@ -1228,16 +1238,19 @@ cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
 }
 
 // Rows a tile: the smallest that holds all of a sequence's rows of one KV head, else the
-// largest.
-//               NR KS VS CTAs
-using C16 = Cfg<16, 2, 2, 2>;
-using C32 = Cfg<32, 2, 2, 2>;
-using C64 = Cfg<64, 2, 1, 2>;
+// largest.  (Three stages of K at 128 rows: 450 us for 466 with two.)
+//               NR groups KS VS CTAs
+using C16 = Cfg<16, 2, 2, 2, 2>;
+using C32 = Cfg<32, 2, 2, 2, 2>;
+using C64 = Cfg<64, 2, 2, 1, 2>;
+using C128 = Cfg<128, 4, 3, 2, 1>;
 inline int rows_of(int N, int H, int Hkv) {
   const int rows = N * (H / Hkv);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
-inline int ctas_of(int nr) { return nr == 16 ? C16::CTAS : nr == 32 ? C32::CTAS : C64::CTAS; }
+inline int ctas_of(int nr) {
+  return nr == 16 ? C16::CTAS : nr == 32 ? C32::CTAS : nr == 64 ? C64::CTAS : C128::CTAS;
+}
 
 }  // namespace tree
 
@@ -1284,7 +1297,8 @@ cudaError_t launch_tree_decode(const uint16_t* q, int64_t B, int N, int H, int H
   switch (tree::rows_of(N, H, Hkv)) {
     case 16: return tree::launch<tree::C16>(a, B, num_sms, stream);
     case 32: return tree::launch<tree::C32>(a, B, num_sms, stream);
-    default: return tree::launch<tree::C64>(a, B, num_sms, stream);
+    case 64: return tree::launch<tree::C64>(a, B, num_sms, stream);
+    default: return tree::launch<tree::C128>(a, B, num_sms, stream);
   }
 }
 

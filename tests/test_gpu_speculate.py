@@ -210,6 +210,25 @@ def test_logits_that_climb_and_fall(slope):
     a.check(out, lse)
 
 
+@pytest.mark.parametrize("N", [1, 3, 8, 13])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rows_of_every_tile_size_with_references_that_move(N, sign):
+    # 16, 48, 128 and 208 rows of a head: half of the heads' logits climb from page to page,
+    # half fall
+    a = Attn(19, [900 + N], N, kind="tree")
+    q = np.zeros((1, N, 16, 128), np.float32)
+    q[..., 0] = sign * np.linspace(0.5, 1.0, 16) * np.where(np.arange(16) % 2, 1, -1)
+    a.q = bf16(q)
+    a.scale = 10.0
+    for pg in range(8):
+        d = a.kp[a.bt[0, pg], 0, :8192].reshape(128, 64)
+        d[:, 0] = (d[:, 0] & 0xF0) | pg
+        a.kp[a.bt[0, pg], 0, 8192:].reshape(128, 4)[:, 0] = 127
+    out, lse = a.run()
+    assert m.mx4_check_status() == 0
+    a.check(out, lse)
+
+
 @pytest.mark.parametrize("N,H,kind", [(1, 16, "chain"), (6, 5, "tree"), (7, 16, "tree")])
 def test_value_scales_that_change_from_page_to_page(N, H, kind):
     # blocks of some pages far above and far below the others, a page of zeros (scale byte 0)
