@@ -101,6 +101,11 @@ struct Args {
   int32_t* meta;  // [grid][4]
   uint32_t* status;
   int B, N, H, Hkv, G, tiles;
+  uint32_t g_inv;  // ceil(2^32 / G)
+  // row / G, exact for the rows of a sequence (at most 64 x 128, G at most 128)
+  __device__ __forceinline__ int node_of(int row) const {
+    return G == 1 ? row : (int)__umulhi((uint32_t)row, g_inv);
+  }
 };
 
 // Shared-memory layout, in bytes.
@@ -132,7 +137,7 @@ struct Lay {
   static constexpr int kMore = kInfo + 16;                   // [3] a page asks for new references
   static constexpr int kMisc = kMore + 16;                   // abort, tmem address, scan space
   static constexpr int kBytes = kMisc + 8 + 20 * 4 + 1024;    // + slack for the 1024-byte alignment
-  static_assert(kV % 1024 == 0 && kVraw % 16 == 0 && kRef % 16 == 0 && kMask % 8 == 0 &&
+  static_assert(kV % 1024 == 0 && kVraw % 16 == 0 && kRef % 16 == 0 && kMask % 16 == 0 &&
                 kOff % 8 == 0, "alignment");
   static_assert(C::CTAS * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
@@ -700,7 +705,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
   uint32_t* const s_nan = reinterpret_cast<uint32_t*>(sm + L_::kNan) + c0;
   int* const s_node = reinterpret_cast<int*>(sm + L_::kNode) + c0;
   int* const s_lo = reinterpret_cast<int*>(sm + L_::kLo) + c0;
-  uint32_t* const s_mask = reinterpret_cast<uint32_t*>(sm + L_::kMask) + 2 * c0;  // [NC][2]
+  uint32_t* const s_mask = reinterpret_cast<uint32_t*>(sm + L_::kMask) + 2 * c0;  // [2][NC]
   const float cs = a.scale * kLog2e;
   const uint64_t cs2 = pair(cs, cs);
   const int tok = 4 * lane + w;  // this lane's token of a page
@@ -714,11 +719,11 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
   auto fetch_q = [&](const Cursor& c) {
 #pragma unroll
     for (int it = 0; it < kQIt; ++it) {
-      const int n = (tid >> 3) + it * (kWorkers / 8), row = c.rt * NR + n, node = row / a.G;
+      const int n = (tid >> 3) + it * (kWorkers / 8), row = c.rt * NR + n, node = a.node_of(row);
       qx[it][0] = qx[it][1] = make_uint4(0u, 0u, 0u, 0u);
       if (n < NR && c.left > 0 && node < c.sp.n) {
         const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + (((int64_t)c.s * a.N + node) * a.H + c.h * a.G + row % a.G) * kHeadDim +
+            a.q + (((int64_t)c.s * a.N + node) * a.H + c.h * a.G + (row - node * a.G)) * kHeadDim +
             16 * (tid & 7));
         qx[it][0] = src[0];
         qx[it][1] = src[1];
@@ -735,8 +740,8 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
     sync_all();  // the tile before is written out
     // ---- the tile's rows
     if (t < NC) {
-      const int row = cu.rt * NR + c0 + t, node = row / a.G;
-      s_node[t] = node < a.N ? node * a.H + cu.h * a.G + row % a.G : -1;
+      const int row = cu.rt * NR + c0 + t, node = a.node_of(row);
+      s_node[t] = node < a.N ? node * a.H + cu.h * a.G + (row - node * a.G) : -1;
       uint64_t mk = 0;
       int lo = 0;
       if (node < sp.n) {
@@ -755,8 +760,8 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
           }
         }
       }
-      s_mask[2 * t] = (uint32_t)mk;
-      s_mask[2 * t + 1] = (uint32_t)(mk >> 32);
+      s_mask[t] = (uint32_t)mk;
+      s_mask[NC + t] = (uint32_t)(mk >> 32);
       s_lo[t] = lo;
       s_nref[t] = -kUnset;
       s_nan[t] = 0;
@@ -833,7 +838,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
       for (int e = cu.e0; e < cu.e1; ++e, ++k) {
         const int first = page_no(sp, e) * kPageTokens, live = s_info[k & 3];
         const bool plain = live == kPageTokens && first + kPageTokens <= sp.base &&
-                           (a.window == 0 || first > sp.base + 63 - a.window ||
+                           (a.window == 0 || first >= sp.base + sp.n - a.window ||
                             first + kPageTokens <= a.sinks);
         // ---- V.  Operand row (K index) m holds token 4 (m % 32) + m / 32, the order in which
         // the tensor copy lays out K.  A warp's step: 8 operand rows (r8), lane >> 3 choosing
@@ -899,13 +904,24 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
         if (!plain) {
           vis = 0u;
           const int i_g = first + tok, nd = i_g - sp.base;
-          if (tok < live) {
-#pragma unroll 1
-            for (int c = 0; c < NC; ++c) {
-              const bool see = nd >= 0 ? ((s_mask[2 * c + ((nd >> 5) & 1)] >> (nd & 31)) & 1u) != 0u
-                                       : i_g >= s_lo[c] || i_g < a.sinks;
-              vis |= (uint32_t)see << c;
+          if (tok < live && nd >= 0) {
+            const uint32_t* const mw = s_mask + ((nd >> 5) & 1) * NC;
+#pragma unroll
+            for (int c = 0; c < NC; c += 4) {
+              const uint4 m4 = *reinterpret_cast<const uint4*>(mw + c);
+              const uint32_t mm[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) vis |= ((mm[i] >> (nd & 31)) & 1u) << (c + i);
             }
+          } else if (tok < live) {
+#pragma unroll
+            for (int c = 0; c < NC; c += 4) {
+              const int4 l4 = *reinterpret_cast<const int4*>(s_lo + c);
+              const int lo[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) vis |= (uint32_t)(i_g >= lo[i]) << (c + i);
+            }
+            if (i_g < a.sinks) vis = ~0u;
           }
         }
         if (e == cu.e0) wait(kSFull + (k & 1), (k >> 1) & 1);
@@ -1066,7 +1082,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
     float* const rec = a.rec + (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * (int64_t)(NR * 130);
     if (t < NC) {
       float sum = (s_warp[t] + s_warp[NC + t]) + (s_warp[2 * NC + t] + s_warp[3 * NC + t]);
-      if ((cu.rt * NR + c0 + t) / a.G >= sp.n) sum = 0.f;
+      if (a.node_of(cu.rt * NR + c0 + t) >= sp.n) sum = 0.f;
       const float rf = -s_nref[t];
       if (whole) {
         s_fac[t] = sum == 0.f ? 0.f : 1.f / sum;
@@ -1145,7 +1161,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
   const int s = a.meta[4 * g + 1], ht = a.meta[4 * g + 2];
   const int h = ht / a.tiles, rt = ht % a.tiles, lane = threadIdx.x & 31;
   const int c = blockIdx.y * 4 + (threadIdx.x >> 5);
-  const int row = rt * NR + c, node = row / a.G;
+  const int row = rt * NR + c, node = a.node_of(row);
   if (node >= a.N) return;
   // the first record is the last of range g - 1, the others the first of theirs
   auto rec = [&](int p) {
@@ -1169,7 +1185,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
     acc.z = fmaf(v.z, f, acc.z);
     acc.w = fmaf(v.w, f, acc.w);
   }
-  const int64_t o = ((int64_t)s * a.N + node) * a.H + h * a.G + row % a.G;
+  const int64_t o = ((int64_t)s * a.N + node) * a.H + h * a.G + (row - node * a.G);
   const float f = sum == 0.f ? 0.f : 1.f / sum;
   uint2 y;
   y.x = pack_bf16(f == 0.f ? 0.f : acc.x * f, f == 0.f ? 0.f : acc.y * f);
@@ -1291,6 +1307,7 @@ cudaError_t launch_tree_decode(const uint16_t* q, int64_t B, int N, int H, int H
   a.H = H;
   a.Hkv = Hkv;
   a.G = H / Hkv;
+  a.g_inv = (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
   a.tiles = 0;
   if (cudaError_t e = tree::encode_pool(k_pages, page_stride, head_stride, num_pages, Hkv, &a.tmap))
     return e;
