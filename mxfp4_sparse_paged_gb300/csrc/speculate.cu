@@ -27,10 +27,12 @@ namespace mx4 {
 //   W_k = max(p - S_k q, 0),   S_k = T_0 + ... + T_{k-1}:
 // p, q and one number give every residual, none is kept.
 //
-// W is rounded as p is, to fp32 (S has 48 bits, so no more is lost where p and S q cancel), and
-// summed exactly: as a 64-bit integer in units of 2^-62, so that no order of summation and no
-// cluster size changes a decision.  There is no fp64 (this GPU's rate is a hundredth of its
-// fp32 rate): a residual costs some dozen 32-bit operations.
+// W is a 64-bit integer in units of 2^-61 (fp32 probabilities of at least 2^-37 without any
+// rounding), and so are its sums: no order of summation and no cluster size changes a decision.
+// There is no fp64 (this GPU's rate is a hundredth of its fp32 rate): a residual costs some
+// twenty 32-bit operations.  (As fp32 numbers, by two fused multiply-adds, they would cost a
+// dozen, and 64 trees of 32 nodes over 131072 tokens 58 us for 73; but the running sums would be
+// off by 2^-30 of the total, enough to draw another token once in some ten thousand draws.)
 //
 // One cluster of CTAs per sequence, each CTA one contiguous part of the vocabulary, each warp
 // one of that.  What the walk looks up (parents, tokens, random numbers, p and q of each draft
@@ -73,11 +75,11 @@ __device__ __forceinline__ uint64_t shift_down(uint64_t x, int n) {
   asm("shr.u64 %0, %1, %2;\n" : "=l"(y) : "l"(x), "r"(n));
   return y;
 }
-// A probability in units of 2^-62, truncated.  By the bits: the 64-bit conversion instruction
+// A probability in units of 2^-61, truncated.  By the bits: the 64-bit conversion instruction
 // is as slow here as fp64 is.
 __device__ __forceinline__ uint64_t to_fixed(float x) {
   const uint32_t b = __float_as_uint(x);
-  return shift_down((uint64_t)(b << 8 | 0x80000000u) << 32, 128 - (int)(b >> 23));
+  return shift_down((uint64_t)(b << 8 | 0x80000000u) << 32, 129 - (int)(b >> 23));
 }
 // u in [0, 1) in units of 2^-64
 __device__ __forceinline__ uint64_t uniform_fixed(float u) {
@@ -96,20 +98,23 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
   return x;
 }
 
-// S_k as the sum of two fp32 numbers (48 bits), and a residual by it
+// S_k, as m 2^(x - 63) with 2^63 <= m < 2^64, and p - S q (W where it is positive)
 struct Factor {
   uint64_t sum = 0;  // in units of 2^-56 (S <= 64)
-  float hi = 0.f, lo = 0.f;
+  uint32_t hi = 0, lo = 0;  // m
+  int x = 0;
   __device__ __forceinline__ void add(uint64_t T) {
-    sum += T >> 6;
+    sum += T >> 5;
     const int lz = __clzll((long long)sum);
-    const uint64_t m = sum << lz;  // S = m 2^(-56 - lz)
-    const float e = __uint_as_float((uint32_t)(127 - 16 - lz) << 23);
-    hi = (float)(uint32_t)(m >> 40) * e;
-    lo = (float)((uint32_t)(m >> 16) & 0xFFFFFFu) * 0x1p-24f * e;
+    hi = (uint32_t)(sum << lz >> 32);
+    lo = (uint32_t)(sum << lz);
+    x = 7 - lz;
   }
-  __device__ __forceinline__ uint64_t left(float p, float q) const {
-    return to_fixed(fmaxf(fmaf(-lo, q, fmaf(-hi, q, p)), 0.f));
+  __device__ __forceinline__ int64_t left(float p, float q) const {
+    const uint32_t b = __float_as_uint(q), m = b << 8 | 0x80000000u;
+    // (a shift below 1 would be for an S q >= 1 >= p; so is what 1 gives)
+    return (int64_t)(to_fixed(p) - shift_down((uint64_t)m * hi + __umulhi(m, lo),
+                                              max(128 - x - (int)(b >> 23), 1)));
   }
 };
 
@@ -218,11 +223,11 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   // what is left of value i (in registers), of token v (in memory)
   auto at_reg = [&](int i) -> uint64_t {
     if (k == 0) return to_fixed(f[i]);
-    return S.left(f[i], s_row[kVerThreads * i + tid]);
+    return max(S.left(f[i], s_row[kVerThreads * i + tid]), (int64_t)0);
   };
   auto at_mem = [&](int v, float pv, float qv) -> uint64_t {
     bad |= !prob_ok(pv) || !prob_ok(qv);
-    if (!kGiven) return k == 0 ? to_fixed(prob(pv)) : S.left(prob(pv), prob(qv));
+    if (!kGiven) return k == 0 ? to_fixed(prob(pv)) : max(S.left(prob(pv), prob(qv)), (int64_t)0);
     for (uint64_t g = gone; g; g &= g - 1)
       if (s_tok[__ffsll((long long)g) - 1] == v) return 0;
     return to_fixed(prob(pv));
@@ -254,7 +259,10 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
         for (int i = 0; i < E; ++i) ws += to_fixed(f[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) ws += S.left(f[i], s_row[kVerThreads * i + tid]);
+        for (int i = 0; i < E; ++i) {
+          const int64_t w = S.left(f[i], s_row[kVerThreads * i + tid]);
+          if (w > 0) ws += w;
+        }
       }
       ws = warp_sum(ws);
     } else {
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   };
   int acc = 1;
   bool summed = false;  // the last pass is of the present residual
-  uint64_t T = 1ull << 62;
+  uint64_t T = 1ull << 61;
   for (uint64_t kids = children(); kids;) {
     const int j = __ffsll((long long)kids) - 1;
     kids &= kids - 1;
@@ -296,15 +304,15 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     } else {
       // floor(u T q) < W, both integers, T q rounded down to one
       ok = k == 0 ? stands(s_u[j], qv, pv)
-                  : __umul64hi(uniform_fixed(s_u[j]), __umul64hi(T << 1, to_fixed(qv) << 1)) <
-                        S.left(pv, qv);
+                  : (int64_t)__umul64hi(uniform_fixed(s_u[j]),
+                                        __umul64hi(T << 2, to_fixed(qv) << 1)) < S.left(pv, qv);
     }
     if (ok) {
       cur = j;
       p_row = tgt + (int64_t)j * a.t_node;
       if constexpr (!kGiven) q_row = drf + (int64_t)j * a.d_node;
       S = Factor{};
-      T = 1ull << 62;
+      T = 1ull << 61;
       k = 0;
       gone = 0;
       summed = loaded = false;
