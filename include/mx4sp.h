@@ -449,7 +449,8 @@ int mx4_decode_steps(int64_t n_steps, const void *h_inputs, size_t h_inputs_stri
  *   k_pages, v_pages  uint8 [num_pages, Hkv, 8704] at the given strides (the same for
  *                both); 32-byte aligned, strides multiples of 32 (they are read by
  *                tensor copies of the pool)
- *   block_table  int32 [B, bt_width]; seq_lens int32 [B]; n_nodes int32 [B] or NULL
+ *   block_table  int32 [B, bt_width], bt_width < 2^23; seq_lens int32 [B]; n_nodes int32
+ *                [B] or NULL
  *   tree_mask    uint64 [B, N] or NULL
  *   window, sinks  >= 0 (sinks counts only with a window)
  *   out          bf16 [B, N, H, 128]; lse fp32 [B, N, H] or NULL (outputs; out 16-byte

@@ -37,9 +37,11 @@ __device__ __forceinline__ float e2m1_to_float(uint32_t c) {
 }
 
 // Programmatic dependent launch.  Every kernel of the library is launched with
-// launch_pdl and signals its dependents as soon as it starts, so the next kernel
-// in the stream can be scheduled while this one drains.  A kernel may run code
-// before pdl_wait() only if it reads inputs no kernel of the library writes
+// launch_pdl and signals its dependents as soon as it starts (attention over drafts: once it
+// has its tensor memory), so the next kernel in the stream can be scheduled while this one
+// drains; but for the kernels that write lengths or block tables, which do not signal: their
+// dependents start when they have completed.  A kernel may run code
+// before pdl_wait() only if it reads inputs that no signalling kernel writes
 // (sequence lengths, block tables) and writes nothing but shared memory;
 // pdl_wait() returns once the previous kernel in the stream has completed and
 // its writes are visible (at once when there is none).

@@ -20,6 +20,11 @@
 // exponent and first mantissa bit read as the code's value times 2^-126 (e = 0 being
 // bf16's subnormals), and one multiplication by 2^(s - 1) gives the value.
 //
+// P in bf16, like the results: half a step, 2^-9, of each weight (its fp32 value goes into the row's
+// sum), which takes the 2-norm error of the results from 1.7e-3, bf16's own, to 2.3e-3, and to
+// 3.2e-3 where single tokens hold most of a row.  P as the sum of two bf16 numbers leaves 1.7e-3,
+// but costs 256 ragged single tokens 178 us for 161, and trees of 64 nodes 746 for 447.
+//
 // Softmax.  bf16 and fp32 hold the weights to the same relative precision at any size, so
 // the reference of a row need not be its running maximum: it is the maximum of the page
 // that set it, and stays until a logit lies 2^kLazy above it.  Only then (and on the first
