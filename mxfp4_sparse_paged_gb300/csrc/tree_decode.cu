@@ -348,9 +348,16 @@ __device__ __forceinline__ Span span_of(int L, int n, int window, int sinks) {
   return sp;
 }
 
-__host__ __device__ __forceinline__ int64_t range_begin(int64_t g, int64_t U, int64_t G) {
-  return U * g / G;
-}
+// floor(U g / G) for g <= G, by one long division
+struct Cuts {
+  int64_t q;
+  uint32_t r, G;
+  __device__ __forceinline__ Cuts(int64_t U, uint32_t G_) : G(G_) {
+    q = U < (1ll << 32) ? (uint32_t)U / G_ : U / G_;
+    r = (uint32_t)(U - q * G_);
+  }
+  __device__ __forceinline__ int64_t operator()(uint32_t g) const { return q * g + r * g / G; }
+};
 
 // Where a CTA's range begins.
 struct Start {
@@ -429,21 +436,22 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
   // ---- this CTA's range of pages, by one thread (all the divisions are here, once)
   if (tid == 0) {
     const int HT = a.Hkv * a.tiles;
-    const int64_t U = (int64_t)s_pref[a.B - 1] * HT, g = blockIdx.x;
+    const int64_t U = (int64_t)s_pref[a.B - 1] * HT;
     // few pages a CTA are not worth the records: at least kMinPages each
-    const int64_t Gd = max((int64_t)1, min((int64_t)gridDim.x, U / kMinPages));
+    const uint32_t g = blockIdx.x, Gd = (uint32_t)max((int64_t)1, min((int64_t)gridDim.x, U / kMinPages));
+    const Cuts cuts(U, Gd);
     Start x{};
     int parts = 0;
     if (g < Gd) {
-      const int64_t u0 = range_begin(g, U, Gd);
-      x.pages = (int)min(range_begin(g + 1, U, Gd) - u0, (int64_t)0x7FFFFFFF);
+      const int64_t u0 = cuts(g);
+      x.pages = (int)min(cuts(g + 1) - u0, (int64_t)0x7FFFFFFF);
       int lo = 0, hi = a.B - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if ((int64_t)s_pref[mid] * HT > u0) hi = mid; else lo = mid + 1;
       }
       const int64_t p0 = lo > 0 ? s_pref[lo - 1] : 0, np = s_pref[lo] - p0, r = u0 - p0 * HT;
-      const int ht = (int)(r / np);
+      const int ht = r < (1ll << 32) ? (int)((uint32_t)r / (uint32_t)np) : (int)(r / np);
       x.s = lo;
       x.h = ht / a.tiles;
       x.rt = ht % a.tiles;
@@ -451,9 +459,9 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
       // a tile that began in the range before this one, and there alone: this CTA's place in
       // the list says how many records join
       const int64_t start = u0 - x.e, end = start + np;
-      if (x.e > 0 && range_begin(g - 1, U, Gd) <= start) {
+      if (x.e > 0 && cuts(g - 1) <= start) {
         parts = 2;
-        while (g + parts - 1 < Gd && range_begin(g + parts - 1, U, Gd) < end) ++parts;
+        while (g + parts - 1 < Gd && cuts(g + parts - 1) < end) ++parts;
         a.meta[4 * g + 1] = x.s;
         a.meta[4 * g + 2] = ht;
       }
@@ -758,8 +766,9 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
         if (a.window > 0) {
           const int d = max(1, __popcll(mk)) - 1;
           lo = max(0, sp.base + d + 1 - a.window);
+          // (nodes' depths differ by less than n: none leaves a window that is not shorter)
 #pragma unroll 1
-          for (int i = 0; i < sp.n; ++i) {
+          for (int i = 0; i < (a.window < sp.n ? sp.n : 0); ++i) {
             const int di = max(1, __popcll(mask_of(i))) - 1;
             if (!(di > d - a.window || sp.base + di < a.sinks)) mk &= ~(1ull << i);
           }
