@@ -396,6 +396,8 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
     s_more[0] = s_more[1] = s_more[2] = 0;
     fence_barrier_init();
   }
+  if (tid == kThreads - 32)
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&a.tmap)) : "memory");
   // The kernel in front may hold tensor memory that this one would wait for: its end first.
   pdl_wait();
   if (warp == 1) {
