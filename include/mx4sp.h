@@ -485,7 +485,8 @@ size_t tree_paged_decode_workspace(int64_t B, int N, int H, int Hkv);
  *            further child of cur is tested.
  * Then next_token[s] is the lowest v with W(0) + .. + W(v) > u_sample[s] * sum W.
  * path[s] lists the nodes that stand (0 first), -1 padded, and n_accepted[s] counts
- * them.  Sums are exact in units of 2^-61.
+ * them.  W is rounded to 2^-46 of target's probability and to a multiple of 2^-61; sums
+ * are exact.
  *
  *   target       fp32, row of node j at target + s*t_batch_stride + j*t_node_stride
  *                (elements), V values each; draft likewise, or NULL

@@ -27,12 +27,13 @@ namespace mx4 {
 //   W_k = max(p - S_k q, 0),   S_k = T_0 + ... + T_{k-1}:
 // p, q and one number give every residual, none is kept.
 //
-// W is a 64-bit integer in units of 2^-61 (fp32 probabilities of at least 2^-37 without any
-// rounding), and so are its sums: no order of summation and no cluster size changes a decision.
-// There is no fp64 (this GPU's rate is a hundredth of its fp32 rate): a residual costs some
-// twenty 32-bit operations.  (As fp32 numbers, by two fused multiply-adds, they would cost a
-// dozen, and 64 trees of 32 nodes over 131072 tokens 58 us for 73; but the running sums would be
-// off by 2^-30 of the total, enough to draw another token once in some ten thousand draws.)
+// W is rounded to 2^-46 of p and then to a multiple of 2^-61, and summed exactly, as integers:
+// no order of summation and no cluster size changes a decision.  fp64 and 64-bit shifts and
+// conversions run at a small part of fp32's rate here, so the integers are made by fp32
+// additions, two values an instruction: adding 3 to a value in [0, 1] leaves its multiple of
+// 2^-22 in the sum's low bits, what is left over goes on to smaller constants, and the bits of
+// each step are added up as 32-bit integers.  (64-bit integer arithmetic: 73 us for 64 trees
+// of 32 nodes over 131072 tokens.)
 //
 // One cluster of CTAs per sequence, each CTA one contiguous part of the vocabulary, each warp
 // one of that.  What the walk looks up (parents, tokens, random numbers, p and q of each draft
@@ -44,8 +45,8 @@ namespace mx4 {
 // given drafts, whose rejections take one token off the sum: a row is read once, and then the
 // 256th of it that the next token is in.
 // Every thread runs the walk itself on the same numbers, so it needs no broadcast.
-// 64 trees of 32 nodes over 131072 tokens take 73 us (rejections follow one another, 2.5 us
-// each for a cluster, in two waves of clusters), 256 given chains of 8 over 50001 tokens 32 us
+// 64 trees of 32 nodes over 131072 tokens take 65 us (rejections follow one another, about 2 us
+// each for a cluster, in two waves of clusters), 256 given chains of 8 over 50001 tokens 28 us
 // (with rows kept by clusters of four 45 us), one chain of 4 over 32000 tokens 11 us.
 constexpr int kMaxNodes = 64;
 constexpr int kVerThreads = 512;
@@ -72,17 +73,121 @@ struct VerifyArgs {
 __device__ __forceinline__ bool prob_ok(float x) { return x >= 0.f && x <= 1.001f; }
 // NaN and negative values count as 0 (and what rounding put above 1 as 1)
 __device__ __forceinline__ float prob(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+// W values made probabilities; is one no probability?  One comparison each where all lie in
+// [0, 1], by their bits.
+template <int W>
+__device__ __forceinline__ bool clean(float* x) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) most = max(most, __float_as_uint(x[i]));
+  bool bad = false;
+  if (most > 0x3F800000u) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      bad |= !prob_ok(x[i]);
+      x[i] = prob(x[i]);
+    }
+  }
+  return bad;
+}
+
+// Two fp32 numbers in one register pair.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 two(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 two(float a) { return two(a, a); }
+__device__ __forceinline__ float first(F2 x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float second(F2 x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint32_t bits(F2 x) { return (uint32_t)x + (uint32_t)(x >> 32); }
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, two(-1.f), a); }
+
+// S_k as the sum of two fp32 numbers (48 bits)
+struct Factor {
+  uint64_t sum = 0;  // in units of 2^-56 (S <= 64)
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(uint64_t T) {
+    sum += T >> 5;
+    const int lz = __clzll((long long)sum);
+    const uint64_t m = sum << lz;  // S = m 2^(-56 - lz)
+    const float e = __uint_as_float((uint32_t)(127 - 16 - lz) << 23);
+    hi = (float)(uint32_t)(m >> 40) * e;
+    lo = (float)((uint32_t)(m >> 16) & 0xFFFFFFu) * 0x1p-24f * e;
+  }
+};
+
+// A sum of n values in units of 2^-61 (at most 64 pairs: the 32-bit sums of the steps' bits).
+struct Fixed {
+  static constexpr float k1 = 3.f, k2 = 0x1.8p-22f, kc = 0x1.8p-21f, k3 = 0x1.8p-38f;
+  uint32_t h = 0, l = 0, lc = 0, z = 0;
+  int pairs = 0, corrections = 0;
+  // d, each in [0, 1]: multiples of 2^-22, 2^-45 and 2^-61
+  __device__ __forceinline__ void put(F2 d) {
+    const F2 x = add(d, two(k1)), r = sub(d, add(x, two(-k1)));
+    const F2 y = add(r, two(k2)), r2 = sub(r, add(y, two(-k2)));
+    h += bits(x);
+    l += bits(y);
+    z += bits(add(r2, two(k3)));
+    ++pairs;
+  }
+  // c, at most 2^-22 in magnitude: multiples of 2^-44 and 2^-61
+  __device__ __forceinline__ void put_small(F2 c) {
+    const F2 y = add(c, two(kc)), r = sub(c, add(y, two(-kc)));
+    lc += bits(y);
+    z += bits(add(r, two(k3)));
+    ++corrections;
+  }
+  // max(p - S q, 0): d + c with d = p - hi q rounded, c its error (exact where d >= 0, the
+  // difference of a larger and a smaller number), the product's and lo q
+  __device__ __forceinline__ void put(F2 p, F2 q, const Factor& S) {
+    const F2 np = mul(two(-S.hi), q), d = add(p, np);
+    const F2 c = sub(fma(two(-S.lo), q, add(sub(p, d), np)), fma(two(S.hi), q, np));
+    const F2 w = add(d, c);
+    const bool a = first(w) > 0.f, b = second(w) > 0.f;
+    put(two(a ? first(d) : 0.f, b ? second(d) : 0.f));
+    put_small(two(a ? first(c) : 0.f, b ? second(c) : 0.f));
+  }
+  __device__ __forceinline__ uint64_t total() const {
+    const int n = 2 * pairs, m = 2 * corrections;
+    return (uint64_t)(((int64_t)(int)(h - n * 0x40400000u) << 39) +
+                      ((int64_t)(int)(l - n * 0x34C00000u) << 16) +
+                      ((int64_t)(int)(lc - m * 0x35400000u) << 17) +
+                      (int64_t)(int)(z - (n + m) * 0x2CC00000u));
+  }
+};
+__device__ __forceinline__ uint64_t to_fixed(float p) {
+  Fixed x;
+  x.put(two(p, 0.f));
+  return x.total();
+}
+__device__ __forceinline__ uint64_t left_of(float p, float q, const Factor& S) {
+  Fixed x;
+  x.put(two(p, 0.f), two(q, 0.f), S);
+  return x.total();
+}
+
 // x >> n, 0 for n of 64 and more
 __device__ __forceinline__ uint64_t shift_down(uint64_t x, int n) {
   uint64_t y;
   asm("shr.u64 %0, %1, %2;\n" : "=l"(y) : "l"(x), "r"(n));
   return y;
-}
-// A probability in units of 2^-61, truncated.  By the bits: the 64-bit conversion instruction
-// is as slow here as fp64 is.
-__device__ __forceinline__ uint64_t to_fixed(float x) {
-  const uint32_t b = __float_as_uint(x);
-  return shift_down((uint64_t)(b << 8 | 0x80000000u) << 32, 129 - (int)(b >> 23));
 }
 // u in [0, 1) in units of 2^-64
 __device__ __forceinline__ uint64_t uniform_fixed(float u) {
@@ -100,26 +205,6 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
   return x;
 }
-
-// S_k, as m 2^(x - 63) with 2^63 <= m < 2^64, and p - S q (W where it is positive)
-struct Factor {
-  uint64_t sum = 0;  // in units of 2^-56 (S <= 64)
-  uint32_t hi = 0, lo = 0;  // m
-  int x = 0;
-  __device__ __forceinline__ void add(uint64_t T) {
-    sum += T >> 5;
-    const int lz = __clzll((long long)sum);
-    hi = (uint32_t)(sum << lz >> 32);
-    lo = (uint32_t)(sum << lz);
-    x = 7 - lz;
-  }
-  __device__ __forceinline__ int64_t left(float p, float q) const {
-    const uint32_t b = __float_as_uint(q), m = b << 8 | 0x80000000u;
-    // (a shift below 1 would be for an S q >= 1 >= p; so is what 1 gives)
-    return (int64_t)(to_fixed(p) - shift_down((uint64_t)m * hi + __umulhi(m, lo),
-                                              max(128 - x - (int)(b >> 23), 1)));
-  }
-};
 
 template <int E, bool kGiven>
 __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs a) {
@@ -207,11 +292,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) f[i] = 32 * i < left ? __ldg(p_row + v0 + lane + 32 * i) : 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      bad |= !prob_ok(f[i]);
-      f[i] = prob(f[i]);
-    }
+    bad |= clean<E>(f);
     if (with_q) {
       asm volatile("cp.async.wait_all;\n" ::: "memory");
 #pragma unroll 8
@@ -223,32 +304,43 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     }
     loaded = true;
   };
-  // what is left of value i (in registers), of token v (in memory)
-  auto at_reg = [&](int i) -> uint64_t {
-    if (k == 0) return to_fixed(f[i]);
-    return max(S.left(f[i], s_row[kVerThreads * i + tid]), (int64_t)0);
-  };
+  // what is left of token v
   auto at_mem = [&](int v, float pv, float qv) -> uint64_t {
-    bad |= !prob_ok(pv) || !prob_ok(qv);
-    if (!kGiven) return k == 0 ? to_fixed(prob(pv)) : max(S.left(prob(pv), prob(qv)), (int64_t)0);
+    if (!kGiven) return k == 0 ? to_fixed(pv) : left_of(pv, qv, S);
     for (uint64_t g = gone; g; g &= g - 1)
       if (s_tok[__ffsll((long long)g) - 1] == v) return 0;
-    return to_fixed(prob(pv));
+    return to_fixed(pv);
   };
   // its sum over b0 <= v < b1 by one warp (all lanes get it)
   auto range_sum = [&](int b0, int b1) {
     uint64_t sum = 0;
-    const bool two = !kGiven && k > 0;
+    const bool two_rows = !kGiven && k > 0;
     for (int b = b0 + lane; b < b1; b += 32 * kVerUnroll) {
       float pv[kVerUnroll], qv[kVerUnroll];
 #pragma unroll
       for (int i = 0; i < kVerUnroll; ++i) {
         const int v = b + 32 * i;
         pv[i] = v < b1 ? p_row[v] : 0.f;
-        qv[i] = two && v < b1 ? q_row[v] : 0.f;
+        qv[i] = two_rows && v < b1 ? q_row[v] : 0.f;
       }
+      bad |= clean<kVerUnroll>(pv);
+      if (two_rows) bad |= clean<kVerUnroll>(qv);
+      if (kGiven)
+        for (uint64_t g = gone; g; g &= g - 1) {
+          const int at = s_tok[__ffsll((long long)g) - 1] - b;
 #pragma unroll
-      for (int i = 0; i < kVerUnroll; ++i) sum += at_mem(b + 32 * i, pv[i], qv[i]);
+          for (int i = 0; i < kVerUnroll; ++i)
+            if (at == 32 * i) pv[i] = 0.f;
+        }
+      Fixed x;
+#pragma unroll
+      for (int i = 0; i < kVerUnroll; i += 2) {
+        if (two_rows)
+          x.put(two(pv[i], pv[i + 1]), two(qv[i], qv[i + 1]), S);
+        else
+          x.put(two(pv[i], pv[i + 1]));
+      }
+      sum += x.total();
     }
     return warp_sum(sum);
   };
@@ -257,16 +349,17 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   auto total = [&]() {
     uint64_t ws = 0;
     if constexpr (E > 0) {
+      Fixed x;
       if (k == 0) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) ws += to_fixed(f[i]);
+        for (int i = 0; i < E; i += 2) x.put(two(f[i], f[i + 1]));
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const int64_t w = S.left(f[i], s_row[kVerThreads * i + tid]);
-          if (w > 0) ws += w;
-        }
+        for (int i = 0; i < E; i += 2)
+          x.put(two(f[i], f[i + 1]),
+                two(s_row[kVerThreads * i + tid], s_row[kVerThreads * (i + 1) + tid]), S);
       }
+      ws = x.total();
       ws = warp_sum(ws);
     } else {
       ws = range_sum(v0, v1);
@@ -307,8 +400,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     } else {
       // floor(u T q) < W, both integers, T q rounded down to one
       ok = k == 0 ? stands(s_u[j], qv, pv)
-                  : (int64_t)__umul64hi(uniform_fixed(s_u[j]),
-                                        __umul64hi(T << 2, to_fixed(qv) << 1)) < S.left(pv, qv);
+                  : __umul64hi(uniform_fixed(s_u[j]), __umul64hi(T << 2, to_fixed(qv) << 1)) <
+                        left_of(pv, qv, S);
     }
     if (ok) {
       cur = j;
@@ -383,65 +476,39 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     const int w = scan(lane < kVerWarps ? kept(s_warp[pass & 1][lane & (kVerWarps - 1)],
                                                warp_begin(lane), warp_begin(lane + 1)) : 0) &
                   (kVerWarps - 1);
-    if constexpr (E > 0) {
-      if (warp == w) {
-        // the sums of the rows of 32 values, lane i that of row i: four rows at a time, of
-        // which a lane keeps half in each of two steps
-        uint64_t mine = 0;
+    // the warp's part in sixteenths, then one warp's sixteenth 32 values at a time (from the L2
+    // cache: every thread's own values, by code for each of them, would be 90 KB of it)
+    const int w0 = warp_begin(w), w1 = warp_begin(w + 1);
+    auto part = [&](int i) { return w0 + (w1 - w0) * i / kVerWarps; };
+    const uint64_t sum = range_sum(part(warp), part(warp + 1));
+    if (lane == 0) s_sub[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      const int i = scan(lane < kVerWarps ? s_sub[lane & (kVerWarps - 1)] : 0) & (kVerWarps - 1);
+      const int end = part(i + 1);
+      const bool two_rows = !kGiven && k > 0;
+      int found = end - 1, l = -1;
+#pragma unroll 1
+      for (int b = part(i); b < end && l < 0; b += 32 * kVerUnroll) {
+        float pv[kVerUnroll], qv[kVerUnroll];
 #pragma unroll
-        for (int b = 0; b < E; b += 4) {
-          uint64_t x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = at_reg(b + i);
-#pragma unroll
-          for (int o = 2; o > 0; o >>= 1) {
-            const bool up = (lane & o) != 0;
-#pragma unroll
-            for (int i = 0; i < o; ++i) {
-              const uint64_t send = up ? x[i] : x[i + o], keep = up ? x[i + o] : x[i];
-              x[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
-            }
-          }
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], o);
-          if (lane >> 2 == b >> 2) mine = x[0];
+        for (int r = 0; r < kVerUnroll; ++r) {
+          const int v = b + 32 * r + lane;
+          pv[r] = v < end ? p_row[v] : 0.f;
+          qv[r] = two_rows && v < end ? q_row[v] : 0.f;
         }
-        const int row = scan(mine);
-        uint64_t x = 0;
+#pragma unroll 1
+        for (int r = 0; r < kVerUnroll && l < 0; ++r) {
+          l = scan(at_mem(b + 32 * r + lane, prob(pv[0]), prob(qv[0])));
+          if (l >= 0) found = min(b + 32 * r + l, found);
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (i == row) x = at_reg(i);
-        const int l = scan(x);
-        if (lane == 0) a.next_token[s] = row < 0 || l < 0 ? v1 - 1 : min(v0 + 32 * row + l, v1 - 1);
-      }
-    } else {
-      // the warp's part in sixteenths, then one warp's sixteenth 32 values at a time
-      const int w0 = warp_begin(w), w1 = warp_begin(w + 1);
-      auto sub = [&](int i) { return w0 + (w1 - w0) * i / kVerWarps; };
-      const uint64_t x = range_sum(sub(warp), sub(warp + 1));
-      if (lane == 0) s_sub[warp] = x;
-      __syncthreads();
-      if (warp == 0) {
-        const int i = scan(lane < kVerWarps ? s_sub[lane & (kVerWarps - 1)] : 0) & (kVerWarps - 1);
-        const bool two = !kGiven && k > 0;
-        int found = sub(i + 1) - 1, l = -1;
-        for (int b = sub(i); b < sub(i + 1) && l < 0; b += 32 * kVerUnroll) {
-          float pv[kVerUnroll], qv[kVerUnroll];
-#pragma unroll
-          for (int r = 0; r < kVerUnroll; ++r) {
-            const int v = b + 32 * r + lane;
-            pv[r] = v < sub(i + 1) ? p_row[v] : 0.f;
-            qv[r] = two && v < sub(i + 1) ? q_row[v] : 0.f;
-          }
-#pragma unroll
-          for (int r = 0; r < kVerUnroll; ++r) {
-            if (l >= 0) continue;
-            l = scan(at_mem(b + 32 * r + lane, pv[r], qv[r]));
-            if (l >= 0) found = min(b + 32 * r + l, found);
+          for (int j = 0; j + 1 < kVerUnroll; ++j) {
+            pv[j] = pv[j + 1];
+            qv[j] = qv[j + 1];
           }
         }
-        if (lane == 0) a.next_token[s] = found;
       }
+      if (lane == 0) a.next_token[s] = found;
     }
   }
   if (rank == 0) {
