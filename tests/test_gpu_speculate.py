@@ -386,6 +386,33 @@ def test_verify_drafts(B, N, V, chain, given):
     same(run_verify(*a), R.verify(*a, np.full(B, N)))
 
 
+def test_verify_rows_that_are_not_kept():
+    # a vocabulary beyond what a cluster's registers hold, siblings of one node tested in turn
+    a = verify_inputs(21, 3, 6, 140001, noise=2.0)
+    a[3][:] = [-1, 0, 0, 0, 1, 1]
+    a[5][1:] = 0
+    same(run_verify(*a), R.verify(*a, np.full(3, 6)))
+    assert m.mx4_check_status() == 0
+
+
+@pytest.mark.parametrize("V,noise", [(40, 3.0), (700, 1e-3), (9000, 1.0), (30000, 1e-4)])
+def test_verify_many_siblings(V, noise):
+    # up to 63 rejections at one node, drafts far from the target and next to it
+    N = 64
+    a = verify_inputs(22, 5, N, V, noise=noise)
+    a[3][:] = 0
+    a[3][:, 0] = -1
+    a[4][:4] = np.maximum(a[4][:4], 0.97)
+    rng = np.random.default_rng(V)
+    for s in range(5):
+        c = np.cumsum(a[1][s, 0].astype(np.float64))
+        a[2][s, 1:] = np.minimum(V - 1, np.searchsorted(c, rng.random(N - 1) * c[-1]))
+    same(run_verify(*a), R.verify(*a, np.full(5, N)))
+    b = (a[0], None) + a[2:]
+    same(run_verify(*b), R.verify(*b, np.full(5, N)))
+    assert m.mx4_check_status() == 0
+
+
 def test_verify_borders():
     # u of 0 and next to 1, one-hot targets, drafts equal to the target, zero probabilities
     V, N = 300, 5
