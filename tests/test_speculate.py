@@ -96,6 +96,12 @@ def test_accept_rows_refusals(lib, kw, code, word):
     assert _accept(lib, B=0, path=None) == 0
 
 
+def test_accept_rows_without_heads_needs_index_pages(lib):
+    assert _accept(lib, Hkv=0, k=None, v=None, idx=None) == -1
+    assert "NULL" in m.mx4_last_error()
+    assert _accept(lib, Hkv=-1) == -2
+
+
 def _fork(lib, **kw):
     a = dict(rows=ONE, n=2, bt=ctypes.c_void_p(1 << 20), B=2, W=3, sl=ctypes.c_void_p(2 << 20), refs=ONE,
              fl=ONE, fc=ONE, k=ONE, v=ONE, ps=8704, hs=8704, Hkv=1, idx=None, ips=0, fp8=0, P=4,
