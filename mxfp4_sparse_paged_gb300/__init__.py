@@ -596,6 +596,14 @@ def _arg(t, dtype, shape, name):
     return _Host(t)
 
 
+def _sizes(t, name, dims):
+    """The sizes of a tensor of this many dims."""
+    s = t.shape
+    if len(s) != dims:
+        _dims(t, name, *(None,) * dims)
+    return s
+
+
 def _opt(t, dtype, shape, name):
     return None if t is None else _arg(t, dtype, shape, name)
 
@@ -637,10 +645,10 @@ def tree_paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, out, ws
     first `sinks` tokens.  N = 1 is the single-token decode step.  ws: uint8, at least
     tree_paged_decode_workspace(B, N, H, Hkv) bytes (None when that is 0)."""
     i32, bf = torch.int32, torch.bfloat16
-    _dims(q, "q", None, None, None, HEAD_DIM)
-    B, N, H, _ = shape = q.shape
-    _dims(block_table, "block_table", B, None)
-    W = block_table.shape[1]
+    B, N, H, D = shape = _sizes(q, "q", 4)
+    if D != HEAD_DIM:
+        _dims(q, "q", None, None, None, HEAD_DIM)
+    W = _sizes(block_table, "block_table", 2)[1]
     args = (_arg(out, bf, shape, "out"), _opt(lse, torch.float32, (B, N, H), "lse"), *_ws(ws))
     qp = _arg(q, bf, shape, "q")
     tables = (_arg(block_table, i32, (B, W), "block_table"), W, _arg(seq_lens, i32, (B,), "seq_lens"),
@@ -668,8 +676,7 @@ def verify_drafts(target, draft, tokens, parents, u_accept, u_sample, path, n_ac
     children were drawn from it; None: drafts that were looked up), tokens and parents
     int32 [B, N] and the random numbers u_accept fp32 [B, N], u_sample fp32 [B]."""
     i32, f32 = torch.int32, torch.float32
-    _dims(target, "target", None, None, None)
-    B, N, V = shape = target.shape
+    B, N, V = shape = _sizes(target, "target", 3)
     args = (_arg(tokens, i32, (B, N), "tokens"), _arg(parents, i32, (B, N), "parents"),
             _arg(u_accept, f32, (B, N), "u_accept"), _arg(u_sample, f32, (B,), "u_sample"),
             _opt(n_nodes, i32, (B,), "n_nodes"), B, N, V, _arg(path, i32, (B, N), "path"),
@@ -683,15 +690,17 @@ def _idx_pool(idx_pages, P):
     """Index pages (MXFP4, fp8 or None) as the row and page calls take them."""
     if idx_pages is None:
         return None, 0, 0, P
-    fp8 = idx_pages.shape[-1] == FP8_PAGE_BYTES
-    if fp8:
-        _fp8_pages(idx_pages, "idx_pages")
-    else:
-        _pages(idx_pages, "idx_pages", 2)
-    if idx_pages.shape[0] != P:
-        raise ValueError(f"idx_pages has {int(idx_pages.shape[0])} pages, k_pages {P}")
-    return (idx_pages.data_ptr() if idx_pages.is_cuda else _Host(idx_pages), idx_pages.stride(0),
-            int(fp8), P)
+    s, st = idx_pages.shape, idx_pages.stride()
+    fp8 = s[-1] == FP8_PAGE_BYTES
+    if not (idx_pages.dtype is torch.uint8 and len(s) == 2 and (fp8 or s[1] == PAGE_BYTES) and
+            st[1] == 1):
+        if fp8:
+            _fp8_pages(idx_pages, "idx_pages")
+        else:
+            _pages(idx_pages, "idx_pages", 2)
+    if s[0] != P:
+        raise ValueError(f"idx_pages has {int(s[0])} pages, k_pages {P}")
+    return idx_pages.data_ptr() if idx_pages.is_cuda else _Host(idx_pages), st[0], int(fp8), P
 
 
 def mx4_accept_rows(path, n_accepted, seq_lens, block_table, k_pages, v_pages, idx_pages, new_lens,
@@ -701,10 +710,8 @@ def mx4_accept_rows(path, n_accepted, seq_lens, block_table, k_pages, v_pages, i
     (idx_pages MXFP4, fp8 or None; k_pages and v_pages None: the index pages alone);
     new_lens int32 [B] = seq_lens - n_nodes + n_accepted."""
     i32 = torch.int32
-    _dims(path, "path", None, None)
-    B, N = path.shape
-    _dims(block_table, "block_table", B, None)
-    W = block_table.shape[1]
+    B, N = _sizes(path, "path", 2)
+    W = _sizes(block_table, "block_table", 2)[1]
     args = (_arg(path, i32, (B, N), "path"), _arg(n_accepted, i32, (B,), "n_accepted"),
             _arg(seq_lens, i32, (B,), "seq_lens"), _opt(n_nodes, i32, (B,), "n_nodes"), B, N,
             _arg(block_table, i32, (B, W), "block_table"), W)
@@ -723,9 +730,8 @@ def mx4_fork_pages(rows, block_table, seq_lens, ref_counts, free_list, free_coun
     pages (ref_counts int32 [P] grows) and gets a copy of a partly filled last page on a
     page off the stack free_list int32 [P], free_count int32 [1]; child_lens int32 [n]."""
     i32 = torch.int32
-    _dims(rows, "rows", None)
-    _dims(block_table, "block_table", None, None)
-    n, (B, W), P = rows.shape[0], block_table.shape, k_pages.shape[0]
+    n, (B, W) = _sizes(rows, "rows", 1)[0], _sizes(block_table, "block_table", 2)
+    P = k_pages.shape[0]
     args = (_arg(rows, i32, (n,), "rows"), n, _arg(block_table, i32, (B, W), "block_table"), B, W,
             _arg(seq_lens, i32, (B,), "seq_lens"), _arg(ref_counts, i32, (P,), "ref_counts"),
             _arg(free_list, i32, (P,), "free_list"), _arg(free_count, i32, (1,), "free_count"))
@@ -739,9 +745,7 @@ def mx4_free_pages(tables, lens, ref_counts, free_list, free_count, stream=None)
     """The rows of tables int32 [n, W] (lens int32 [n] tokens each) give their pages back:
     a reference less each, and pages without one go on the stack, ascending by id."""
     i32 = torch.int32
-    _dims(tables, "tables", None, None)
-    _dims(ref_counts, "ref_counts", None)
-    (n, W), P = tables.shape, ref_counts.shape[0]
+    (n, W), P = _sizes(tables, "tables", 2), _sizes(ref_counts, "ref_counts", 1)[0]
     _call(_load().mx4_free_pages, _arg(tables, i32, (n, W), "tables"), n, W,
           _arg(lens, i32, (n,), "lens"), _arg(ref_counts, i32, (P,), "ref_counts"), P,
           _arg(free_list, i32, (P,), "free_list"), _arg(free_count, i32, (1,), "free_count"),
