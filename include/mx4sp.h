@@ -458,8 +458,9 @@ int mx4_decode_steps(int64_t n_steps, const void *h_inputs, size_t h_inputs_stri
  *   ws           tree_paged_decode_workspace(B, N, H, Hkv) bytes, 16-byte aligned; the
  *                size depends on the current device's SM count
  * Logits, softmax statistics and sums are fp32; the weights are rounded to bf16 for the
- * product with V, as is the output.  1 <= N <= 64, 1 <= Hkv <= 8, H a multiple of Hkv,
- * H <= 128, B <= 65535.  A bad length (seq_len < n_nodes, or beyond the block table) gives
+ * product with V, as is the output.  The sums before their division overflow for no result
+ * below 2^118 / (tokens seen); past that one may come out infinite.  1 <= N <= 64,
+ * 1 <= Hkv <= 8, H a multiple of Hkv, H <= 128, B <= 65535.  A bad length (seq_len < n_nodes, or beyond the block table) gives
  * zeros and sets MX4_STATUS_BAD_LEN; tokens on a bad page are not seen
  * (MX4_STATUS_BAD_PAGE).
  * ------------------------------------------------------------------------- */

@@ -8,17 +8,20 @@
 //   S^T[token, row] = K q^T      tcgen05.mma kind::mxf8f6f4.block_scale, A = the page's e2m1
 //                                rows and e8m0 scales as they are stored, no dequantisation;
 //   P^T = 2^(scale log2e S - ref) rounded to bf16;
-//   O^T[dim, row] += V^T P^T     tcgen05.mma kind::f16 on bf16.
+//   O^T[dim, row] += V^T P^T     tcgen05.mma kind::f16 on bf16 (V / 4, see below).
 //
 // q as a sum of two E4M3 numbers.  The block-scaled product wants q in an MX format.  A bf16
 // has 8 significant bits: hi = E4M3(q 2^-E) takes the first 4 (E puts the 32-block's largest
 // element in [2^7, 2^8)), lo = E4M3((q 2^-E - hi) 2^5) the rest exactly, down to 2^-14 of the
 // largest element and to 2^-22 of it in absolute terms.  Two MMAs into one accumulator.
 //
-// V.  Its scales run along the contraction's other axis, so V is dequantised into a bf16
-// operand in shared memory, exactly: an e2m1 code's bits moved to a bf16's sign, low
+// V.  Its scales run along the contraction's other axis, so a quarter of V is dequantised into a
+// bf16 operand in shared memory, exactly: an e2m1 code's bits moved to a bf16's sign, low
 // exponent and first mantissa bit read as the code's value times 2^-126 (e = 0 being
-// bf16's subnormals), and one multiplication by 2^(s - 1) gives the value.
+// bf16's subnormals), and one multiplication by 2^(s - 3) gives a quarter of the value; the
+// results are multiplied by 4.  The largest value, 6 x 2^127, is past bf16's range: as an
+// infinity it would be NaN times the weight 0 of a row that does not see it.  Its quarter is
+// not, and the smallest quarter, 2^-130, is a bf16 as well.
 //
 // P in bf16, like the results: half a step, 2^-9, of each weight (its fp32 value goes into the row's
 // sum), which takes the 2-norm error of the results from 1.7e-3, bf16's own, to 2.3e-3, and to
@@ -125,7 +128,7 @@ struct Lay {
   static constexpr int kVraw = kKsc + C::KS * 512;           // [VS] V pages as stored
   static constexpr int kSf = kVraw + C::VS * kPageBytes;     // q scale words: hi, lo
   static constexpr int kRef = kSf + 2 * NR * 4;              // [NR] minus the references
-  static constexpr int kFac = kRef + NR * 4;                 // [NR] rescaling factors, then 1 / sum
+  static constexpr int kFac = kRef + NR * 4;                 // [NR] rescaling factors, then 4 / sum
   static constexpr int kWarp = kFac + NR * 4;                // [4][NR] per-warp maxima and sums
   static constexpr int kNan = kWarp + 4 * NR * 4;            // [NR] dim blocks with a visible NaN
   static constexpr int kNode = kNan + NR * 4;                // [NR] output row, -1 none
@@ -866,9 +869,9 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
           const uint4 c4 = *reinterpret_cast<const uint4*>(raw + tk * kRowDataBytes + blk * 16);
           const uint32_t sc = raw[kScaleOffset + tk * kRowScaleBytes + blk];
           const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
-          // 2^(sc - 1), as two factors where it passes bf16's range
-          const uint32_t f1 = (tk < live && sc != 255u ? min(sc + 126u, 254u) : 0u) * 0x00800080u;
-          const bool big = __any_sync(0xFFFFFFFFu, sc > 128u);
+          // 2^(sc - 3), as two factors where it passes bf16's range
+          const uint32_t f1 = (tk < live && sc != 255u ? min(sc + 124u, 254u) : 0u) * 0x00800080u;
+          const bool big = __any_sync(0xFFFFFFFFu, sc > 130u);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t v = cw[j];
@@ -884,7 +887,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
             for (int i = 0; i < 4; ++i) y[j][i] = bf16_mul2(y[j][i], f1);
           }
           if (big) {
-            const uint32_t f2 = (sc > 128u ? sc - 1u : 127u) * 0x00800080u;
+            const uint32_t f2 = (sc > 130u ? sc - 3u : 127u) * 0x00800080u;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -1101,7 +1104,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
       if (a.node_of(cu.rt * NR + c0 + t) >= sp.n) sum = 0.f;
       const float rf = -s_nref[t];
       if (whole) {
-        s_fac[t] = sum == 0.f ? 0.f : 1.f / sum;
+        s_fac[t] = sum == 0.f ? 0.f : 4.f / sum;
         if (a.lse && s_node[t] >= 0)
           a.lse[(int64_t)cu.s * a.N * a.H + s_node[t]] =
               sum == 0.f ? -INFINITY : (log2f(sum) + (rf == kUnset ? 0.f : rf)) * 0.6931471805599453f;
@@ -1166,7 +1169,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
 }
 
 // Joins the records of a cut tile: block x = the range after its first cut, a warp a row,
-// a lane four dims: out = sum_r O_r 2^(m_r - M) / sum_r l_r 2^(m_r - M).
+// a lane four dims: out = 4 sum_r O_r 2^(m_r - M) / sum_r l_r 2^(m_r - M).
 template <int NR>
 __global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
   pdl_launch_dependents();
@@ -1202,7 +1205,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
     acc.w = fmaf(v.w, f, acc.w);
   }
   const int64_t o = ((int64_t)s * a.N + node) * a.H + h * a.G + (row - node * a.G);
-  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  const float f = sum == 0.f ? 0.f : 4.f / sum;
   uint2 y;
   y.x = pack_bf16(f == 0.f ? 0.f : acc.x * f, f == 0.f ? 0.f : acc.y * f);
   y.y = pack_bf16(f == 0.f ? 0.f : acc.z * f, f == 0.f ? 0.f : acc.w * f);

@@ -1,0 +1,77 @@
+"""GPU parity of the speculative step's calls at the ends of their ranges: the largest value
+scales (64-bit references of
+_spec_ref; tolerances derived there and below)."""
+import numpy as np
+import pytest
+import torch
+
+import _spec_ref as R
+import mxfp4_sparse_paged_gb300 as m
+from test_gpu_speculate import Attn, bf16
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+BF16_MAX = float(torch.finfo(torch.bfloat16).max)
+
+
+def value_block(a, token, block, scale, codes):
+    """The 32-dim block of the value of cached token `token` of sequence 0, head 0: a scale byte
+    and one code for the even dims, one for the odd."""
+    p, r = a.bt[0, token // 128], token % 128
+    a.vp[p, 0, 64 * r + 16 * block:64 * r + 16 * block + 16] = codes[0] | codes[1] << 4
+    a.vp[p, 0, 8192 + 4 * r + block] = scale
+
+
+# ------------------------------------------------------------------ tree_paged_decode
+
+@pytest.mark.parametrize("heads", [4, 16, 32])  # 16, 64 and 128 rows a tile
+@pytest.mark.parametrize("scale,codes", [(253, (6, 7)), (253, (14, 7)), (254, (2, 4)), (254, (7, 15))])
+def test_values_beyond_bf16_in_places_not_seen(heads, scale, codes):
+    # codes whose value passes bf16's largest, in a sibling and in a token that the window leaves
+    # out: the other nodes' results are those without them; the node that sees its own has a
+    # result that bf16 holds, as its weight is small
+    a = Attn(31, [300], 4, H=heads, kind="tree", window=150, sinks=2)
+    a.mask[0] = [1, 3, 5, 9]  # a root and three children
+    value_block(a, 296 + 2, 1, scale, codes)
+    for block in range(4):
+        value_block(a, 60, block, scale, codes)  # outside every window (296 - 150 > 60)
+    want = a.want()
+    assert np.abs(want[0][0, [0, 1, 3]]).max() < 100 and np.abs(want[0]).max() < 0.9 * BF16_MAX
+    out, lse = a.run()
+    assert m.mx4_check_status() == 0
+    a.check(out, lse, want)
+
+
+def test_values_beyond_bf16_with_a_weight_of_zero():
+    # seen, but 2^-200 of the row: no part in the result
+    a = Attn(32, [200], 1)
+    q = np.zeros((1, 1, 16, 128), np.float32)
+    q[..., 0] = np.linspace(1.0, 2.0, 16)
+    a.q, a.scale = bf16(q), 140.0
+    d = a.kp[a.bt[0, 0], 0, :8192].reshape(128, 64)
+    a.kp[a.bt[0, 0], 0, 8192:].reshape(128, 4)[:, 0] = 127
+    a.kp[a.bt[0, 1], 0, 8192:].reshape(128, 4)[:72, 0] = 127
+    d[:, 0] = d[:, 0] & 0xF0 | 1
+    e = a.kp[a.bt[0, 1], 0, :8192].reshape(128, 64)
+    e[:72, 0] = e[:72, 0] & 0xF0 | 1
+    d[7, 0] = d[7, 0] & 0xF0 | 9  # -0.5: 140 below the others and more
+    value_block(a, 7, 2, 254, (7, 6))
+    seen = R.rows_of(a.kp, a.bt[0], 0, 200)[:, 0]
+    assert (seen == np.where(np.arange(200) == 7, -0.5, 0.5)).all()
+    out, lse = a.run()
+    assert m.mx4_check_status() == 0
+    a.check(out, lse)
+
+
+def test_the_largest_values_that_bf16_holds():
+    # one token: the result is its value, 3 x 2^126 and 1.5 x 2^127 exactly, and infinite past that
+    a = Attn(33, [1], 1)
+    for block, (scale, codes) in enumerate([(253, (5, 12)), (254, (3, 2)), (254, (1, 9)), (254, (7, 15))]):
+        value_block(a, 0, block, scale, codes)
+    out, _ = a.run()
+    assert m.mx4_check_status() == 0
+    o = out.float().cpu().numpy()[0, 0].astype(np.float64)
+    want = R.rows_of(a.vp, a.bt[0], 0, 1)[0]
+    assert np.array_equal(o[:, :96], np.broadcast_to(want[:96], (16, 96)))
+    assert np.array_equal(o[:, 96:], np.broadcast_to(np.where(want[96:] > 0, np.inf, -np.inf), (16, 32)))
