@@ -7,7 +7,7 @@
 // token's 16 heads take an N of 16 and not an eighth of an M of 128:
 //   S^T[token, row] = K q^T      tcgen05.mma kind::mxf8f6f4.block_scale, A = the page's e2m1
 //                                rows and e8m0 scales as they are stored, no dequantisation;
-//   P^T = 2^(scale log2e S - ref) rounded to bf16;
+//   P^T = 2^(scale log2e (S - ref)) rounded to bf16;
 //   O^T[dim, row] += V^T P^T     tcgen05.mma kind::f16 on bf16 (V / 4, see below).
 //
 // q as a sum of two E4M3 numbers.  The block-scaled product wants q in an MX format.  A bf16
@@ -33,6 +33,11 @@
 // that set it, and stays until a logit lies 2^kLazy above it.  Only then (and on the first
 // page) is there a reduction over the tokens, which lie across lanes; a page otherwise
 // costs one vote.  Row sums stay in the lanes until the end of the tile.
+// The reference is a score, taken off before the multiplication by scale log2e (a negative
+// scale's sign goes into q): the difference of two near scores is exact, and the largest
+// weight 1, however large the logits are.  (A fused multiply-add against the rounded product
+// as reference is no faster, and off by 2^7 log2 units, a sum of 0 or infinity, at logits of
+// 2^31.)
 //
 // Work.  The pages of all tiles, in order, are cut into equal contiguous ranges, one per
 // CTA.  A tile cut by a range's end leaves a partial record (O, reference, sum) in the
@@ -54,6 +59,8 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
+#include <cmath>
 
 #include "score_pipeline.cuh"
 
@@ -63,7 +70,7 @@ namespace tree {
 
 constexpr int kMaxSeq = 256;       // sequences per launch
 constexpr float kLazy = 12.f;      // log2 units a logit may lie above its row's reference
-constexpr float kUnset = -3e38f;   // the reference of a row that has seen nothing
+constexpr float kUnset = -FLT_MAX;  // the reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKTile = 128 * 128;  // K operand tile
 // V operand: rows of 64 dims (128 bytes) a token, in 128-byte swizzle atoms of 8 tokens (the
@@ -102,7 +109,8 @@ struct Args {
   const int32_t* n_nodes;
   const uint64_t* mask;
   int window, sinks;  // (clamped below 2^30: no cached token lies further)
-  float scale;
+  float cs;     // |scale| log2e (scale 0: 1), finite
+  float qsign;  // the scale's sign; 0 for a scale of 0
   uint16_t* out;
   float* lse;
   float* rec;   // [grid][2][NR * 130] partial records
@@ -278,9 +286,11 @@ __device__ __forceinline__ uint64_t pair(float lo, float hi) {
 __device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v));
 }
-__device__ __forceinline__ void fma2(float& x0, float& x1, uint64_t m, float c0, float c1) {
+// x = (x + y) m
+__device__ __forceinline__ void addmul2(float& x0, float& x1, float y0, float y1, uint64_t m) {
   uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(pair(x0, x1)), "l"(m), "l"(pair(c0, c1)));
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(pair(x0, x1)), "l"(pair(y0, y1)));
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(r), "l"(m));
   unpair(r, x0, x1);
 }
 __device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
@@ -724,8 +734,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
   int* const s_node = reinterpret_cast<int*>(sm + L_::kNode) + c0;
   int* const s_lo = reinterpret_cast<int*>(sm + L_::kLo) + c0;
   uint32_t* const s_mask = reinterpret_cast<uint32_t*>(sm + L_::kMask) + 2 * c0;  // [2][NC]
-  const float cs = a.scale * kLog2e;
-  const uint64_t cs2 = pair(cs, cs);
+  const uint64_t cs2 = pair(a.cs, a.cs);
   const int tok = 4 * lane + w;  // this lane's token of a page
   // dequantisation: see below
   const int r8 = lane & 7, blk = ((r8 >> 1) + (lane >> 3)) & 3;
@@ -801,7 +810,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
         const int ef = min(254, (int)(__float_as_uint(amax) >> 23));
         const int E = amax == 0.f ? 0 : max(-122, ef - 127 - 7);
-        const float inv = __uint_as_float((uint32_t)(127 - E) << 23);
+        const float inv = __uint_as_float((uint32_t)(127 - E) << 23) * a.qsign;
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -916,7 +925,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
             store_v(1, yv);
           }
         }
-        // ---- logits in log2 units relative to the rows' references
+        // ---- scores, their differences from the rows' references in log2 units
         // a row sees a draft by its mask, an earlier token from the window's first on; rows
         // without a node see what they like, their results are zeroed
         uint32_t vis = ~0u;
@@ -986,8 +995,6 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
             for (int c = 0; c < NC; c += W) {
               float v[W];
               s_of(c, v);
-#pragma unroll
-              for (int i = 0; i < W; ++i) v[i] *= cs;
               hide(c, v);
               const float mx = columns<W>(v, lane, [](float p, float q) { return fmaxf(p, q); });
               if (lane < W) s_warp[w * NC + c + lane] = mx;
@@ -997,7 +1004,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
               const float v = fmaxf(fmaxf(s_warp[t], s_warp[NC + t]),
                                     fmaxf(s_warp[2 * NC + t], s_warp[3 * NC + t]));
               const float old = -s_nref[t], now = fmaxf(old, v);
-              s_fac[t] = old == kUnset ? 0.f : ex2(old - now);
+              s_fac[t] = ex2((old - now) * a.cs);
               s_nref[t] = -now;
             }
             sync_all();
@@ -1025,8 +1032,8 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < W; i += 4) {
               const float4 rf = *reinterpret_cast<const float4*>(s_nref + c + i);
-              fma2(x[i], x[i + 1], cs2, rf.x, rf.y);
-              fma2(x[i + 2], x[i + 3], cs2, rf.z, rf.w);
+              addmul2(x[i], x[i + 1], rf.x, rf.y, cs2);
+              addmul2(x[i + 2], x[i + 3], rf.z, rf.w, cs2);
             }
             hide(c, x);
             float m0 = x[0], m1 = x[1];
@@ -1107,7 +1114,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
         s_fac[t] = sum == 0.f ? 0.f : 4.f / sum;
         if (a.lse && s_node[t] >= 0)
           a.lse[(int64_t)cu.s * a.N * a.H + s_node[t]] =
-              sum == 0.f ? -INFINITY : (log2f(sum) + (rf == kUnset ? 0.f : rf)) * 0.6931471805599453f;
+              sum == 0.f ? -INFINITY : (log2f(sum) + rf * a.cs) * 0.6931471805599453f;
       } else {
         s_fac[t] = sum == 0.f ? 0.f : 1.f;
         rec[NR * 128 + c0 + t] = rf;
@@ -1169,7 +1176,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS) tree_kernel(const __grid
 }
 
 // Joins the records of a cut tile: block x = the range after its first cut, a warp a row,
-// a lane four dims: out = 4 sum_r O_r 2^(m_r - M) / sum_r l_r 2^(m_r - M).
+// a lane four dims: out = 4 sum_r O_r f_r / sum_r l_r f_r with f_r = 2^(cs (m_r - M)).
 template <int NR>
 __global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
   pdl_launch_dependents();
@@ -1197,7 +1204,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
     const float* r = rec(p);
     const float m = r[NR * 128 + c], l = r[NR * 129 + c];
     const float4 v = reinterpret_cast<const float4*>(r + c * 128)[lane];
-    const float f = m == kUnset ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);
+    const float f = ex2((m - M) * a.cs);
     sum = fmaf(l, f, sum);
     acc.x = fmaf(v.x, f, acc.x);
     acc.y = fmaf(v.y, f, acc.y);
@@ -1211,8 +1218,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
   y.y = pack_bf16(f == 0.f ? 0.f : acc.z * f, f == 0.f ? 0.f : acc.w * f);
   reinterpret_cast<uint2*>(a.out + o * kHeadDim)[lane] = y;
   if (a.lse && lane == 0)
-    a.lse[o] = sum == 0.f ? -INFINITY
-                          : (log2f(sum) + (M == kUnset ? 0.f : M)) * 0.6931471805599453f;
+    a.lse[o] = sum == 0.f ? -INFINITY : (log2f(sum) + M * a.cs) * 0.6931471805599453f;
 }
 
 // The K pool as a 5-d tensor: 128 4-bit elements, rows 4r + c of a page as r (32) and c
@@ -1315,7 +1321,8 @@ cudaError_t launch_tree_decode(const uint16_t* q, int64_t B, int N, int H, int H
   a.mask = mask;
   a.window = (int)std::min<int64_t>(window, 1 << 30);
   a.sinks = (int)std::min<int64_t>(sinks, 1 << 30);
-  a.scale = scale;
+  a.cs = scale == 0.f ? 1.f : std::min(std::fabs(scale) * tree::kLog2e, FLT_MAX);
+  a.qsign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
   a.out = out;
   a.lse = lse;
   a.rec = static_cast<float*>(ws);

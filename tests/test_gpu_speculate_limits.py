@@ -1,6 +1,6 @@
 """GPU parity of the speculative step's calls at the ends of their ranges: the largest value
-scales (64-bit references of
-_spec_ref; tolerances derived there and below)."""
+scales, logits far beyond fp32's integers (64-bit references of _spec_ref; tolerances derived
+there and below)."""
 import numpy as np
 import pytest
 import torch
@@ -75,3 +75,43 @@ def test_the_largest_values_that_bf16_holds():
     want = R.rows_of(a.vp, a.bt[0], 0, 1)[0]
     assert np.array_equal(o[:, :96], np.broadcast_to(want[:96], (16, 96)))
     assert np.array_equal(o[:, 96:], np.broadcast_to(np.where(want[96:] > 0, np.inf, -np.inf), (16, 32)))
+
+
+@pytest.mark.parametrize("N", [1, 2, 4, 13])  # 16, 32, 64 and 128 rows a tile
+@pytest.mark.parametrize("power", [24, 30, 33, 36, 60])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_logits_far_beyond_the_integers_of_fp32(N, power, sign):
+    # one dim of q and of K: the logits are exact products, 2^power times a few, and lie so far
+    # apart that the largest alone have a weight.  Six pages, larger keys in the later ones.
+    a = Attn(34, [700], N, kind="tree")
+    q = np.zeros((1, N, 16, 128), np.float32)
+    q[..., 0] = (1 + np.arange(16) / 16) * np.where(np.arange(16) % 3 == 1, -1, 1)
+    a.q = bf16(q)
+    a.scale = sign * 2.0 ** power
+    codes = np.zeros((6, 128), np.int64)
+    for pg in range(6):
+        codes[pg] = a.rng.integers(0, 4 + min(pg, 2), 128) | 8 * a.rng.integers(0, 2, 128)
+        p = a.bt[0, pg]
+        d = a.kp[p, 0, :8192].reshape(128, 64)
+        d[:, 0] = d[:, 0] & 0xF0 | codes[pg]
+        a.kp[p, 0, 8192:].reshape(128, 4)[:, 0] = 127
+    out, lse = a.run()
+    assert m.mx4_check_status() == 0
+    o, l, _, _ = a.want()
+    got, gl = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    # the weights are 0 or 1, exactly; the mean rounds in fp32 and to bf16 (half a step), the
+    # logsumexp by five fp32 operations
+    v = R.rows_of(a.vp, a.bt[0], 0, 700)
+    tol = 2.0 ** -8 * np.abs(o) + 2.0 ** -16 * np.abs(v).max()
+    assert np.all(np.abs(got - o) <= tol), float(np.nanmax(np.abs(got - o)))
+    assert np.all(np.abs(gl - l) <= 2.0 ** -21 * np.abs(l))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-30, -1e-30])
+def test_scales_next_to_zero(scale):
+    # every visible token has nearly the same weight, whatever the queries
+    a = Attn(35, [300, 140], 3, kind="tree", scale=scale)
+    a.q[0, 1] *= 2.0 ** 40
+    out, lse = a.run()
+    assert m.mx4_check_status() == 0
+    a.check(out, lse)
