@@ -487,7 +487,8 @@ size_t tree_paged_decode_workspace(int64_t B, int N, int H, int Hkv);
  * Then next_token[s] is the lowest v with W(0) + .. + W(v) > u_sample[s] * sum W.
  * path[s] lists the nodes that stand (0 first), -1 padded, and n_accepted[s] counts
  * them.  W is rounded to 2^-46 of target's probability and to a multiple of 2^-61; sums
- * are exact.
+ * are exact.  They have to stay below 2: where a sum of W that is needed does not, no
+ * further draft is tested, next_token is -1 and MX4_STATUS_BAD_VALUE is set.
  *
  *   target       fp32, row of node j at target + s*t_batch_stride + j*t_node_stride
  *                (elements), V values each; draft likewise, or NULL

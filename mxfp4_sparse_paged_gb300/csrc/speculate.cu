@@ -33,7 +33,9 @@ namespace mx4 {
 // additions, two values an instruction: adding 3 to a value in [0, 1] leaves its multiple of
 // 2^-22 in the sum's low bits, what is left over goes on to smaller constants, and the bits of
 // each step are added up as 32-bit integers.  (64-bit integer arithmetic: 73 us for 64 trees
-// of 32 nodes over 131072 tokens.)
+// of 32 nodes over 131072 tokens.)  Sums stop at kFull, just below 2: the test's products and
+// the sums themselves have no room for more, and no row of probabilities comes near it.  As
+// every partial sum stops there, a row's sum does whatever the order, and is refused.
 //
 // One cluster of CTAs per sequence, each CTA one contiguous part of the vocabulary, each warp
 // one of that.  What the walk looks up (parents, tokens, random numbers, p and q of each draft
@@ -119,9 +121,11 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
 }
 __device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, two(-1.f), a); }
 
+constexpr int64_t kFull = (1ll << 62) - 1;
+
 // S_k as the sum of two fp32 numbers (48 bits)
 struct Factor {
-  uint64_t sum = 0;  // in units of 2^-56 (S <= 64)
+  uint64_t sum = 0;  // in units of 2^-56 (S <= 128)
   float hi = 0.f, lo = 0.f;
   __device__ __forceinline__ void add(uint64_t T) {
     sum += T >> 5;
@@ -164,23 +168,26 @@ struct Fixed {
     put(two(a ? first(d) : 0.f, b ? second(d) : 0.f));
     put_small(two(a ? first(c) : 0.f, b ? second(c) : 0.f));
   }
-  __device__ __forceinline__ uint64_t total() const {
+  // (at most kFull; the steps of 2^-22 alone say where 64 bits would not hold the sum)
+  __device__ __forceinline__ int64_t total() const {
     const int n = 2 * pairs, m = 2 * corrections;
-    return (uint64_t)(((int64_t)(int)(h - n * 0x40400000u) << 39) +
+    const int coarse = (int)(h - n * 0x40400000u);
+    const int64_t t = ((int64_t)min(coarse, 3 << 22) << 39) +
                       ((int64_t)(int)(l - n * 0x34C00000u) << 16) +
                       ((int64_t)(int)(lc - m * 0x35400000u) << 17) +
-                      (int64_t)(int)(z - (n + m) * 0x2CC00000u));
+                      (int64_t)(int)(z - (n + m) * 0x2CC00000u);
+    return min(t, kFull);
   }
 };
 __device__ __forceinline__ uint64_t to_fixed(float p) {
   Fixed x;
   x.put(two(p, 0.f));
-  return x.total();
+  return (uint64_t)x.total();
 }
 __device__ __forceinline__ uint64_t left_of(float p, float q, const Factor& S) {
   Fixed x;
   x.put(two(p, 0.f), two(q, 0.f), S);
-  return x.total();
+  return (uint64_t)x.total();
 }
 
 // x >> n, 0 for n of 64 and more
@@ -200,9 +207,9 @@ __device__ __forceinline__ bool stands(float u, float q, float p) {
   return h < p || (h == p && fmaf(u, q, -h) < 0.f);
 }
 
-__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  for (int o = 16; o > 0; o >>= 1) x = min(x + __shfl_xor_sync(0xFFFFFFFFu, x, o), kFull);
   return x;
 }
 
@@ -215,9 +222,9 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   extern __shared__ float s_row[];  // E > 0: q, value i of thread t at 512 i + t
   __shared__ int32_t s_par[kMaxNodes], s_tok[kMaxNodes], s_path[kMaxNodes];
   __shared__ float s_u[kMaxNodes], s_p[kMaxNodes], s_q[kMaxNodes];
-  __shared__ uint64_t s_warp[2][kVerWarps];       // this CTA's warp sums, of two passes
-  __shared__ uint64_t s_part[2][kVerMaxCluster];  // the cluster's CTA sums
-  __shared__ uint64_t s_sub[kVerWarps];
+  __shared__ int64_t s_warp[2][kVerWarps];       // this CTA's warp sums, of two passes
+  __shared__ int64_t s_part[2][kVerMaxCluster];  // the cluster's CTA sums
+  __shared__ int64_t s_sub[kVerWarps];
   pdl_launch_dependents();
   pdl_wait();
 
@@ -313,7 +320,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   };
   // its sum over b0 <= v < b1 by one warp (all lanes get it)
   auto range_sum = [&](int b0, int b1) {
-    uint64_t sum = 0;
+    int64_t sum = 0;
     const bool two_rows = !kGiven && k > 0;
     for (int b = b0 + lane; b < b1; b += 32 * kVerUnroll) {
       float pv[kVerUnroll], qv[kVerUnroll];
@@ -340,14 +347,14 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
         else
           x.put(two(pv[i], pv[i + 1]));
       }
-      sum += x.total();
+      sum = min(sum + x.total(), kFull);
     }
     return warp_sum(sum);
   };
   // the sum of the residual, with the warp and CTA sums left in place `pass & 1`
   int pass = 0;
-  auto total = [&]() {
-    uint64_t ws = 0;
+  auto total = [&]() -> uint64_t {
+    int64_t ws = 0;
     if constexpr (E > 0) {
       Fixed x;
       if (k == 0) {
@@ -370,14 +377,14 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     if (lane == 0) s_warp[pass & 1][warp] = ws;
     __syncthreads();
     if (warp == 0) {
-      const uint64_t cs = warp_sum(lane < kVerWarps ? s_warp[pass & 1][lane] : 0);
+      const int64_t cs = warp_sum(lane < kVerWarps ? s_warp[pass & 1][lane] : 0);
       if (lane < C) *cluster.map_shared_rank(&s_part[pass & 1][rank], lane) = cs;
     }
     cluster.sync();
-    uint64_t t = 0;
+    int64_t t = 0;
 #pragma unroll
-    for (int i = 0; i < kVerMaxCluster; ++i) t += i < C ? s_part[pass & 1][i] : 0;
-    return t;
+    for (int i = 0; i < kVerMaxCluster; ++i) t = min(t + (i < C ? s_part[pass & 1][i] : 0), kFull);
+    return (uint64_t)max(t, (int64_t)0);
   };
 
   // children of cur, by node (they come after it)
@@ -422,7 +429,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
       // the row is summed once; what has been rejected is taken off that sum, and in the end
       // off the CTA's and the warp's that hold it
       if (k == 0) T = total();
-      T -= w;
+      if (T < kFull) T -= w;
       summed = true;
       if (w != 0) gone |= 1ull << j;  // (a token once)
       ++k;
@@ -432,6 +439,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
       T = total();
       summed = true;
     }
+    if (T >= kFull) break;  // no probabilities
     if (T == 0) {  // nothing left (p <= q everywhere): draw from p itself
       k = 0;
       gone = 0;
@@ -470,9 +478,9 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   };
   int at = scan(lane < C ? kept(s_part[pass & 1][lane & (kVerMaxCluster - 1)], cta_begin(lane),
                                 cta_begin(lane + 1)) : 0);  // the CTA
-  if (T == 0) at = -1;  // a row of zeros: no token
+  if (T == 0 || T >= kFull) at = -1;  // a row of zeros, or of 2 or more: no token
   if (at == rank) {
-    // (one is always found, but for rows whose sum leaves 64 bits)
+    // (one is always found)
     const int w = scan(lane < kVerWarps ? kept(s_warp[pass & 1][lane & (kVerWarps - 1)],
                                                warp_begin(lane), warp_begin(lane + 1)) : 0) &
                   (kVerWarps - 1);

@@ -1,13 +1,13 @@
 """GPU parity of the speculative step's calls at the ends of their ranges: the largest value
-scales, logits far beyond fp32's integers (64-bit references of _spec_ref; tolerances derived
-there and below)."""
+scales, logits far beyond fp32's integers, rows that sum to more than 1 (64-bit references of
+_spec_ref; tolerances derived there and below)."""
 import numpy as np
 import pytest
 import torch
 
 import _spec_ref as R
 import mxfp4_sparse_paged_gb300 as m
-from test_gpu_speculate import Attn, bf16
+from test_gpu_speculate import Attn, bf16, run_verify, same, verify_inputs
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -115,3 +115,66 @@ def test_scales_next_to_zero(scale):
     out, lse = a.run()
     assert m.mx4_check_status() == 0
     a.check(out, lse)
+
+
+# ------------------------------------------------------------------ verify_drafts
+
+def flat_rows(a, rows, total):
+    """Rows (s, j) of the target become flat with this sum."""
+    V = a[0].shape[2]
+    for s, j in rows:
+        a[0][s, j] = np.float32(total / V)
+
+
+@pytest.mark.parametrize("V", [40, 1000, 5000, 20001, 131072, 140001])
+@pytest.mark.parametrize("given", [False, True])
+def test_verify_rows_that_sum_to_two_and_more(V, given):
+    # no probabilities: rows of 1.5 are worked with as they are, those of 3, 10 and (where that
+    # many probabilities are) 40 are refused where their sum is needed: no next token
+    B, N = 6, 3
+    a = verify_inputs(V, B, N, V, chain=True)
+    if given:
+        a = (a[0], None) + a[2:]
+    a[3][:] = [-1, 0, 0]
+    a[4][1:5] = 0.999  # both drafts, the only token of the draft's row, are rejected at the root
+    a[2][1:5, 1:] = 7
+    if not given:
+        a[1][1:5, 0] = np.arange(V) == 7
+    for s, total in ((1, 1.5), (2, 3.0), (3, 10.0), (4, min(V / 2, 40.0))):
+        flat_rows(a, [(s, 0)], total)
+    want = R.verify(*a, np.full(B, N))
+    got = run_verify(*a)
+    with pytest.raises(m.Mx4Error) as ei:
+        m.mx4_check_status()
+    assert ei.value.bits == 0x10
+    for g, w in zip(got, want):
+        assert np.array_equal(g[[0, 1, 5]], w[[0, 1, 5]])
+    assert (got[2][2:5] == -1).all() and (got[1][2:5] == 1).all()
+    assert (got[0][2:5] == [0, -1, -1]).all()
+
+
+def test_verify_rows_past_two_in_one_thread():
+    # all of a large sum in the values of one thread, of one warp and of one CTA
+    B, N, V = 4, 1, 70001
+    a = verify_inputs(5, B, N, V)
+    a[0][:3] = 0
+    a[0][0, 0, 32 * np.arange(30)] = 0.9
+    a[0][1, 0, :1000] = 0.5
+    a[0][2, 0, 100:30000] = 0.5
+    want = R.verify(*a, np.full(B, N))
+    got = run_verify(*a)
+    with pytest.raises(m.Mx4Error) as ei:
+        m.mx4_check_status()
+    assert ei.value.bits == 0x10
+    assert (got[2][:3] == -1).all() and got[2][3] == want[2][3]
+
+
+def test_verify_sums_just_below_two_are_exact():
+    # two tokens of 1 and the number before it: drawn right up to the border between them
+    V = 256
+    a = verify_inputs(6, 5, 1, V)
+    a[0][:] = 0
+    a[0][:, 0, 3], a[0][:, 0, 200] = 1.0, np.float32(1) - np.float32(2.0 ** -24)
+    a[5][:] = np.array([0.0, 0.499, 0.5, 0.50001, 1 - 2.0 ** -24], np.float32)
+    same(run_verify(*a), R.verify(*a, np.full(5, 1)))
+    assert m.mx4_check_status() == 0
