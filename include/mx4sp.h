@@ -497,9 +497,11 @@ size_t tree_paged_decode_workspace(int64_t B, int N, int H, int Hkv);
  *   path int32 [B, N], n_accepted int32 [B], next_token int32 [B]  (outputs)
  * 1 <= N <= 64, 1 <= V <= 2^24, B <= 65535.  A parent of -1 takes a node out; one that
  * is not before its node, or a token outside [0, V), does too and sets
- * MX4_STATUS_BAD_INDEX.  Probabilities that are NaN or negative count as 0 and ones
- * above 1 set, like them, MX4_STATUS_BAD_VALUE; a row of zeros gives next_token -1.  An idle
- * sequence (n_nodes 0) gets n_accepted 0 and next_token -1.
+ * MX4_STATUS_BAD_INDEX.  Probabilities that are NaN or negative count as 0, ones above 1
+ * as 1; where a tested draft or a summed row has one, or one above 1.001 (what is below is
+ * rounding), MX4_STATUS_BAD_VALUE is set.  A row of zeros gives next_token -1 and sets it
+ * too.  An idle sequence (n_nodes 0) gets n_accepted 0 and next_token -1; n_nodes outside
+ * [0, N] is taken as the nearer end and sets MX4_STATUS_BAD_LEN.
  * ------------------------------------------------------------------------- */
 int verify_drafts(const float *target, int64_t t_batch_stride, int64_t t_node_stride,
                   const float *draft, int64_t d_batch_stride, int64_t d_node_stride,

@@ -72,6 +72,7 @@ struct VerifyArgs {
   uint32_t* status;
 };
 
+// (a probability that rounding took above 1 is one)
 __device__ __forceinline__ bool prob_ok(float x) { return x >= 0.f && x <= 1.001f; }
 // NaN and negative values count as 0 (and what rounding put above 1 as 1)
 __device__ __forceinline__ float prob(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   extern __shared__ float s_row[];  // E > 0: q, value i of thread t at 512 i + t
   __shared__ int32_t s_par[kMaxNodes], s_tok[kMaxNodes], s_path[kMaxNodes];
   __shared__ float s_u[kMaxNodes], s_p[kMaxNodes], s_q[kMaxNodes];
+  __shared__ bool s_bad[kMaxNodes];  // p or q of the draft is no probability
   __shared__ int64_t s_warp[2][kVerWarps];       // this CTA's warp sums, of two passes
   __shared__ int64_t s_part[2][kVerMaxCluster];  // the cluster's CTA sums
   __shared__ int64_t s_sub[kVerWarps];
@@ -264,8 +266,11 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     s_tok[tid] = tok;
     s_path[tid] = tid == 0 ? 0 : -1;
     s_u[tid] = u;
-    s_p[tid] = par >= 0 ? prob(tgt[par * a.t_node + tok]) : 0.f;
-    s_q[tid] = par >= 0 ? (kGiven ? 1.f : prob(drf[par * a.d_node + tok])) : 0.f;
+    const float p = par >= 0 ? tgt[par * a.t_node + tok] : 0.f;
+    const float q = kGiven ? 1.f : par >= 0 ? drf[par * a.d_node + tok] : 0.f;
+    s_p[tid] = prob(p);
+    s_q[tid] = prob(q);
+    s_bad[tid] = !prob_ok(p) || !prob_ok(q);
   }
   __syncthreads();
 
@@ -399,6 +404,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     const int j = __ffsll((long long)kids) - 1;
     kids &= kids - 1;
     const float pv = s_p[j], qv = s_q[j];
+    bad |= s_bad[j];
     uint64_t w = 0;  // what is left of its token
     bool ok;
     if constexpr (kGiven) {

@@ -1,5 +1,5 @@
 """GPU parity of the speculative step's calls at the ends of their ranges: the largest value
-scales, logits far beyond fp32's integers, rows that sum to more than 1 (64-bit references of
+scales, logits far beyond fp32's integers, probabilities that are none (64-bit references of
 _spec_ref; tolerances derived there and below)."""
 import numpy as np
 import pytest
@@ -178,3 +178,29 @@ def test_verify_sums_just_below_two_are_exact():
     a[5][:] = np.array([0.0, 0.499, 0.5, 0.50001, 1 - 2.0 ** -24], np.float32)
     same(run_verify(*a), R.verify(*a, np.full(5, 1)))
     assert m.mx4_check_status() == 0
+
+
+@pytest.mark.parametrize("which,value", [("target", np.nan), ("target", -0.5), ("target", 1.5),
+                                         ("draft", np.nan), ("draft", -0.5), ("draft", 1.5)])
+def test_verify_flags_what_it_looks_up(which, value):
+    # the probability of a tested draft, in a row that is not summed as the draft stands; the same
+    # of a draft that is never tested is not looked at
+    B, N, V = 2, 4, 50
+    a = verify_inputs(7, B, N, V, chain=True)
+    a[3][:] = [-1, 0, 1, 1]
+    a[4][:] = 0  # every tested draft with a probability stands
+    row = a[0] if which == "target" else a[1]
+    a[0][0, 0, a[2][0, 1]] = 0.5
+    clean = [np.copy(x) for x in a]
+    row[0, 1, a[2][0, 3]] = value  # node 2 stands first: 3 is not tested
+    a[2][0, 2] = (a[2][0, 3] + 1) % V
+    clean[2][0, 2] = a[2][0, 2]
+    a[0][0, 1, a[2][0, 2]] = clean[0][0, 1, a[2][0, 2]] = 0.5
+    same(run_verify(*a), R.verify(*clean, np.full(B, N)))
+    assert m.mx4_check_status() == 0
+    row[0, 0, a[2][0, 1]] = value
+    got = run_verify(*a)
+    with pytest.raises(m.Mx4Error) as ei:
+        m.mx4_check_status()
+    assert ei.value.bits == 0x10
+    assert got[1][0] == (1 if which == "target" and not value > 0 else 3)
