@@ -522,8 +522,8 @@ int verify_drafts(const float *target, int64_t t_batch_stride, int64_t t_node_st
  *                pages alone (k_pages, v_pages not read): a cache with a second index pool
  *   new_lens     int32 [B] (output; not seq_lens itself)
  * A path that does not ascend within the nodes (MX4_STATUS_BAD_INDEX), a bad length or
- * count (MX4_STATUS_BAD_LEN) or a bad page (MX4_STATUS_BAD_PAGE) leaves the sequence's
- * rows alone, with new_lens[s] = seq_lens[s].  The drafted rows' pages belong to this
+ * count (MX4_STATUS_BAD_LEN) or a bad page of an accepted row, moved or not
+ * (MX4_STATUS_BAD_PAGE), leaves the sequence's rows alone, with new_lens[s] = seq_lens[s].  The drafted rows' pages belong to this
  * sequence alone (mx4_fork_pages copies the page that is being filled).
  * 1 <= N <= 64, 0 <= Hkv <= 8.
  * ------------------------------------------------------------------------- */

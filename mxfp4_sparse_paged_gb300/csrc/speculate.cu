@@ -635,14 +635,14 @@ accept_kernel(const int32_t* __restrict__ path, const int32_t* __restrict__ n_ac
       const int32_t prev = tid > 0 ? path[s * N + tid - 1] : -1;
       if (p <= prev || p >= n) {
         ok = false;
-      } else if (p > tid) {
+      } else {  // (a row that stays has to be on a page as well)
         const int64_t i = base + p, o = base + tid;
         const int32_t sp = table[s * bt_width + i / kPageTokens];
         const int32_t dp = table[s * bt_width + o / kPageTokens];
         if (sp < 0 || sp >= pools.num_pages || dp < 0 || dp >= pools.num_pages) {
           bad_page = 1;
           ok = false;
-        } else {
+        } else if (p > tid) {
           src = (int64_t)sp * kPageTokens + i % kPageTokens;
           dst = (int64_t)dp * kPageTokens + o % kPageTokens;
         }

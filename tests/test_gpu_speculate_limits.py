@@ -7,7 +7,7 @@ import torch
 
 import _spec_ref as R
 import mxfp4_sparse_paged_gb300 as m
-from test_gpu_speculate import Attn, bf16, run_verify, same, verify_inputs
+from test_gpu_speculate import DEV, Attn, bf16, dev, pools_of, run_verify, same, verify_inputs
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -204,3 +204,27 @@ def test_verify_flags_what_it_looks_up(which, value):
         m.mx4_check_status()
     assert ei.value.bits == 0x10
     assert got[1][0] == (1 if which == "target" and not value > 0 else 3)
+
+
+# ------------------------------------------------------------------ mx4_accept_rows
+
+@pytest.mark.parametrize("path", [[0, 1, 2, -1], [0, 1, 3, -1]])
+@pytest.mark.parametrize("page", [-1, 1 << 20])
+def test_accepted_rows_have_to_be_on_a_page(path, page):
+    # the drafts' second page is none: its rows were never cached, so a path over them is
+    # refused, whether its rows move or stay; a path that ends before them stands
+    rng = np.random.default_rng(1)
+    lens = np.array([130, 130], np.int32)  # four nodes each, two on the second page
+    bt, P = R.block_table(rng, lens)
+    bt[:, 1] = page
+    pools = pools_of(rng, P, 1, False)
+    paths = np.array([path, [0, 1, -1, -1]], np.int32)
+    d = [dev(p) for p in pools]
+    new = torch.zeros(2, dtype=torch.int32, device=DEV)
+    m.mx4_accept_rows(dev(paths), dev(np.array([3, 2], np.int32)), dev(lens), dev(bt), *d, new)
+    with pytest.raises(m.Mx4Error) as ei:
+        m.mx4_check_status()
+    assert ei.value.bits == 0x2
+    assert new.cpu().tolist() == [130, 128]
+    for x, w in zip(d, pools):
+        assert np.array_equal(x.cpu().numpy(), w)
