@@ -59,13 +59,16 @@ class SpeculativeStep:
         self.ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
 
     def slots(self) -> torch.Tensor:
-        """int64 [B * N] page-128 slots of this step's nodes, -1 past a sequence's n_nodes."""
+        """int64 [B * N] page-128 slots of this step's nodes, -1 past a sequence's n_nodes.  A node
+        past the table, or where that has no page, gets a slot past the pool, which the insert
+        reports (bad-slot)."""
+        W = self.block_table.shape[1]
         pos = self.seq_lens[:, None].long() + self.node
         live = self.node < self.n_nodes[:, None]
-        col = torch.where(live, pos // PAGE_TOKENS, torch.zeros_like(pos))
-        page = self.block_table.gather(1, col).long()
-        return torch.where(live, page * PAGE_TOKENS + pos % PAGE_TOKENS,
-                           torch.full_like(pos, -1)).flatten()
+        page = self.block_table.gather(1, (pos // PAGE_TOKENS).clamp(0, W - 1)).long()
+        there = (pos >= 0) & (pos < W * PAGE_TOKENS) & (page >= 0)
+        page = torch.where(there, page, self.caches.num_pages)
+        return torch.where(live, page * PAGE_TOKENS + pos % PAGE_TOKENS, -1).flatten()
 
     def attend(self, q, k, v, idx_k, parents=None, n_nodes=None):
         """Insert the nodes' rows (fp32 k, v [B, N, Hkv, 128], idx_k [B, N, 128]) and attend:
