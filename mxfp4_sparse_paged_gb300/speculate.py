@@ -23,14 +23,16 @@ from . import (HEAD_DIM, PAGE_TOKENS, mx4_accept_rows, mx4_fork_pages, mx4_free_
 
 def tree_masks(parents: torch.Tensor) -> torch.Tensor:
     """int64 [B, N] masks of int32 [B, N] parents (before their nodes; -1: none): bit i of
-    word (s, j) set where i is j or an ancestor of j."""
+    word (s, j) set where i is j or an ancestor of j.  A parent that is not before its node is
+    none (verify_drafts reports it); parents[:, 0] is not read."""
     B, N = parents.shape
     masks = torch.zeros((B, N), dtype=torch.int64, device=parents.device)
-    for j in range(N):
+    masks[:, 0] = 1
+    for j in range(1, N):
         p = parents[:, j].long()
-        up = masks.gather(1, p.clamp_min(0)[:, None])[:, 0]
+        up = masks.gather(1, p.clamp(0, j - 1)[:, None])[:, 0]
         bit = (1 << j) if j < 63 else -(1 << 63)
-        masks[:, j] = torch.where(p >= 0, up, torch.zeros_like(up)) | bit
+        masks[:, j] = torch.where((p >= 0) & (p < j), up, 0) | bit
     return masks
 
 

@@ -8,7 +8,7 @@ import torch
 
 import _spec_ref as R
 from mxfp4_sparse_paged_gb300 import build as B_
-from mxfp4_sparse_paged_gb300.speculate import SpeculativeStep
+from mxfp4_sparse_paged_gb300.speculate import SpeculativeStep, tree_masks
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -44,3 +44,13 @@ def test_slots_past_a_table_and_without_a_page_are_flagged_by_the_insert():
     assert all(map(bad, got[4]))
     s.n_nodes.zero_()
     assert s.slots().tolist() == [-1] * 20
+
+
+def test_tree_masks_of_parents_that_are_none():
+    # parents past the nodes, after their node, below -1: roots of their own, as verify_drafts
+    # takes their nodes out (and reports them); the root's own entry is not read
+    parents = np.array([[-1, 0, 64, 2, -7], [9, 0, 2, 3, 1], [1 << 30, 5, 1, -(1 << 31), 4]], np.int32)
+    plain = np.array([[-1, 0, -1, 2, -1], [-1, 0, -1, -1, 1], [-1, -1, 1, -1, -1]], np.int32)
+    want = np.stack([R.masks_of(p) for p in plain]).view(np.int64)
+    got = tree_masks(torch.from_numpy(parents))
+    assert np.array_equal(got.numpy(), want)
