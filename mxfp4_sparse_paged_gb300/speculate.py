@@ -75,13 +75,17 @@ class SpeculativeStep:
     def attend(self, q, k, v, idx_k, parents=None, n_nodes=None):
         """Insert the nodes' rows (fp32 k, v [B, N, Hkv, 128], idx_k [B, N, 128]) and attend:
         q bf16 [B, N, H, 128]; parents int32 [B, N] (None: chains); n_nodes int32 [B] (None:
-        N each).  Returns out, bf16 [B, N, H, 128]."""
+        N each).  Returns out, bf16 [B, N, H, 128].  A sequence with a node that has no page
+        (reported: bad-slot) sits the step out: its n_nodes become 0, its length stays."""
         if n_nodes is not None:
             self.n_nodes.copy_(n_nodes)
         else:
             self.n_nodes.fill_(self.N)
+        slots = self.slots()
+        lost = slots.view(-1, self.N).amax(1) >= self.caches.num_pages * PAGE_TOKENS
+        self.n_nodes.masked_fill_(lost, 0)
         torch.add(self.seq_lens, self.n_nodes, out=self.with_nodes)
-        self.caches.insert_rows(k.flatten(0, 1), v.flatten(0, 1), idx_k.flatten(0, 1), self.slots())
+        self.caches.insert_rows(k.flatten(0, 1), v.flatten(0, 1), idx_k.flatten(0, 1), slots)
         tree_paged_decode(q, self.caches.k_pages, self.caches.v_pages, self.block_table,
                           self.with_nodes, self.scale, self.out, self.ws,
                           tree_mask=None if parents is None else tree_masks(parents),

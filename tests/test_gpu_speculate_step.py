@@ -181,3 +181,26 @@ def test_page_book_forks_and_frees_as_beams_do():
     book.free(table, torch.tensor([t * 128 for t in (table >= 0).sum(1).tolist()], dtype=torch.int32, device=DEV))
     assert m.mx4_check_status() == 0
     assert int(book.free_count) == caches.num_pages and not book.ref_counts.any()
+
+
+def test_a_step_past_the_table_is_reported_and_leaves_the_lengths():
+    # the first sequence's table ends one token on, the second's next page is none, the third has
+    # room: the first two sit the step out, with a bad-slot bit and no other
+    V, N, lens = 16, 3, [511, 128, 60]
+    model = Model(V, 9)
+    caches, table, _ = prompts(model, lens, V, 10, 3)
+    table = table[:, :4].contiguous()
+    table[1, 1:] = -1
+    step = SpeculativeStep(caches, table, torch.tensor(lens, dtype=torch.int32, device=DEV), N)
+    tk = torch.ones((3, N), dtype=torch.int32, device=DEV)
+    pt = torch.tensor([[-1, 0, 1]] * 3, dtype=torch.int32, device=DEV)
+    q, k, v, ik = model.rows(tk)
+    out = step.attend(q, k, v, ik, pt)
+    target = torch.full((3, N, V), 1.0 / V, device=DEV)
+    path, acc, nxt = step.verify(target, None, tk, pt, torch.zeros((3, N), device=DEV),
+                                 torch.zeros((3,), device=DEV))
+    with pytest.raises(m.Mx4Error) as ei:
+        m.mx4_check_status()
+    assert ei.value.bits == 0x1
+    assert step.seq_lens.tolist() == [511, 128, 63] and acc.tolist() == [0, 0, 3]
+    assert nxt.tolist() == [-1, -1, 0] and not out[:2].any() and out[2].any()

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import _spec_ref as R
-from mxfp4_sparse_paged_gb300 import build as B_
+from mxfp4_sparse_paged_gb300 import build as B_, speculate
 from mxfp4_sparse_paged_gb300.speculate import SpeculativeStep, tree_masks
 
 
@@ -17,7 +17,8 @@ def lib():
 
 
 def step_of(table, seq_lens, nodes, P):
-    caches = types.SimpleNamespace(num_pages=P, k_pages=torch.zeros((P, 1, 8704), dtype=torch.uint8))
+    pool = torch.zeros((P, 1, 8704), dtype=torch.uint8)
+    caches = types.SimpleNamespace(num_pages=P, k_pages=pool, v_pages=pool)
     return SpeculativeStep(caches, torch.tensor(table, dtype=torch.int32),
                            torch.tensor(seq_lens, dtype=torch.int32), nodes)
 
@@ -54,3 +55,19 @@ def test_tree_masks_of_parents_that_are_none():
     want = np.stack([R.masks_of(p) for p in plain]).view(np.int64)
     got = tree_masks(torch.from_numpy(parents))
     assert np.array_equal(got.numpy(), want)
+
+
+def test_a_sequence_with_a_node_without_a_page_sits_the_step_out(monkeypatch):
+    # the insert gets its slots (and reports them), every other call sees no nodes of it: its
+    # length stays, where a refused path would count the nodes as cached
+    s = step_of([[3, 5], [7, -1], [1, 2]], [254, 127, 200], 4, 8)
+    seen = {}
+    s.caches.insert_rows = lambda k, v, i, slots: seen.update(slots=slots)
+    monkeypatch.setattr(speculate, "tree_paged_decode", lambda *a, **kw: seen.update(
+        lens=a[4].tolist(), n_nodes=kw["n_nodes"].tolist()))
+    k = torch.zeros((3, 4, 1, 128))
+    s.attend(None, k, k, k[:, :, 0], n_nodes=torch.tensor([4, 2, 3], dtype=torch.int32))
+    assert seen["n_nodes"] == [0, 0, 3] and seen["lens"] == [254, 127, 203]
+    assert [int(x) for x in (seen["slots"].view(3, 4) >= 8 * 128).sum(1)] == [2, 1, 0]
+    s.attend(None, k, k, k[:, :, 0], n_nodes=torch.tensor([2, 1, 4], dtype=torch.int32))
+    assert seen["n_nodes"] == [2, 1, 4] and seen["lens"] == [256, 128, 204]
