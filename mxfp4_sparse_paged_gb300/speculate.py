@@ -135,5 +135,9 @@ class PageBook:
         return tables, lens
 
     def free(self, tables, seq_lens):
-        """The pages of ended sequences' table rows go back."""
-        mx4_free_pages(tables, seq_lens, self.ref_counts, self.free_list, self.free_count)
+        """The pages of ended sequences' table rows go back, those ahead of seq_lens too."""
+        col = torch.arange(1, tables.shape[1] + 1, dtype=torch.int32, device=tables.device)
+        held = torch.where(tables >= 0, col, 0).amax(1) * PAGE_TOKENS
+        # (a negative length stays, for the call to report)
+        lens = torch.where(seq_lens < 0, seq_lens, torch.maximum(seq_lens, held))
+        mx4_free_pages(tables, lens, self.ref_counts, self.free_list, self.free_count)

@@ -8,7 +8,7 @@ import torch
 
 import _spec_ref as R
 from mxfp4_sparse_paged_gb300 import build as B_, speculate
-from mxfp4_sparse_paged_gb300.speculate import SpeculativeStep, tree_masks
+from mxfp4_sparse_paged_gb300.speculate import PageBook, SpeculativeStep, tree_masks
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -71,3 +71,40 @@ def test_a_sequence_with_a_node_without_a_page_sits_the_step_out(monkeypatch):
     assert [int(x) for x in (seen["slots"].view(3, 4) >= 8 * 128).sum(1)] == [2, 1, 0]
     s.attend(None, k, k, k[:, :, 0], n_nodes=torch.tensor([2, 1, 4], dtype=torch.int32))
     assert seen["n_nodes"] == [2, 1, 4] and seen["lens"] == [256, 128, 204]
+
+
+# ------------------------------------------------------------------ PageBook
+
+@pytest.fixture
+def host_pages(monkeypatch):
+    """mx4_fork_pages and mx4_free_pages by the plain implementations, on host tensors."""
+    def fork(rows, bt, lens, refs, fl, fc, k, v, idx, child, child_lens):
+        c, cl, r, n, _ = R.fork(rows.numpy(), bt.numpy(), lens.numpy(), refs.numpy(), fl.numpy(),
+                                int(fc), [])
+        for dst, src in ((child, c), (child_lens, cl), (refs, r)):
+            dst.copy_(torch.from_numpy(src))
+        fc.fill_(n)
+
+    def free(tables, lens, refs, fl, fc):
+        assert all((t[:(L + 127) // 128] >= 0).all() for t, L in zip(tables, lens.tolist()))
+        r, f, n = R.free(tables.numpy(), lens.numpy(), refs.numpy(), fl.numpy(), int(fc))
+        refs.copy_(torch.from_numpy(r))
+        fl.copy_(torch.from_numpy(f))
+        fc.fill_(n)
+
+    monkeypatch.setattr(speculate, "mx4_fork_pages", fork)
+    monkeypatch.setattr(speculate, "mx4_free_pages", free)
+    return types.SimpleNamespace(fp8_idx_pages=None, k_pages=None, v_pages=None, idx_pages=None)
+
+
+def test_ended_sequences_give_all_their_pages_back(host_pages):
+    # pages ahead of a sequence's length, for its next drafts, were counted with the others
+    table = torch.tensor([[3, 5, 9], [7, 1, -1], [2, -1, -1]], dtype=torch.int32)
+    lens = torch.tensor([130, 128, 5], dtype=torch.int32)
+    book = PageBook(12, table)
+    assert int(book.free_count) == 6
+    children, cl = book.fork(torch.tensor([0, 1, 1], dtype=torch.int32), table, lens, host_pages)
+    assert int(book.free_count) == 5 and cl.tolist() == [130, 128, 128]
+    book.free(children, cl)
+    book.free(table, lens)
+    assert int(book.free_count) == 12 and not book.ref_counts.any()
