@@ -8,8 +8,8 @@ are inserted at the end of each sequence (mx4_insert through the shared page-128
 decides which nodes stand and mx4_accept_rows moves their rows together.  All on the current
 stream, nothing is read back: sequence lengths stay on the device.
 
-`PageBook` holds the references and the free stack of a pool: sequences branch (mx4_fork_pages)
-and end (mx4_free_pages).
+`PageBook` holds the references and the free stack of a pool: sequences branch (mx4_fork_pages),
+grow and end (mx4_free_pages).
 """
 from __future__ import annotations
 
@@ -133,6 +133,23 @@ class PageBook:
                        self.free_count, caches.k_pages, caches.v_pages, caches.idx_pages, tables,
                        lens)
         return tables, lens
+
+    def grow(self, tables, seq_lens, tokens):
+        """Rows of `tables` that end before seq_lens + tokens get pages off the stack, row after
+        row from the top.  Where the table or the stack ends an entry stays -1: a step whose
+        nodes come there reports it."""
+        W, P = tables.shape[1], self.free_list.shape[0]
+        need = (seq_lens.long() + tokens + PAGE_TOKENS - 1) // PAGE_TOKENS
+        want = (torch.arange(W, device=tables.device) < need[:, None]) & (tables < 0)
+        want &= seq_lens[:, None] >= 0
+        have = self.free_count.long().clamp(0, P)
+        at = have - want.flatten().cumsum(0)  # place in the stack, below 0 past its end
+        take = want.flatten() & (at >= 0)
+        page = self.free_list.gather(0, at.clamp(0, P - 1)).long()
+        ok = take & (page >= 0) & (page < P)
+        tables.copy_(torch.where(ok.view_as(want), page.view_as(want), tables))
+        self.ref_counts.index_add_(0, page.clamp(0, P - 1), ok.to(torch.int32))
+        self.free_count.copy_(have - take.sum())
 
     def free(self, tables, seq_lens):
         """The pages of ended sequences' table rows go back, those ahead of seq_lens too."""

@@ -204,3 +204,47 @@ def test_a_step_past_the_table_is_reported_and_leaves_the_lengths():
     assert ei.value.bits == 0x1
     assert step.seq_lens.tolist() == [511, 128, 63] and acc.tolist() == [0, 0, 3]
     assert nxt.tolist() == [-1, -1, 0] and not out[:2].any() and out[2].any()
+
+
+def test_children_grow_over_page_borders_and_give_all_pages_back():
+    # children of a partly filled page, of a full one and of one about to be full take pages as
+    # they go, four steps of five nodes, each attending to its own rows; freed with their lengths
+    V, N, lens = 16, 5, [126, 256, 250]
+    model = Model(V, 11)
+    caches, table, _ = prompts(model, lens, V, 12, 20)
+    for s, L in enumerate(lens):  # no page ahead of the lengths
+        table[s, (L + 127) // 128:] = -1
+    book = PageBook(caches.num_pages, table)
+    parents_lens = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    rows = torch.tensor([0, 1, 2, 0, 1], dtype=torch.int32, device=DEV)
+    tables, cl = book.fork(rows, table, parents_lens, caches)
+    step = SpeculativeStep(caches, tables, cl, N)
+    rng = np.random.default_rng(3)
+    cur = np.array(lens, np.int32)[rows.cpu().numpy()]
+    for it in range(4):
+        book.grow(tables, step.seq_lens, N)
+        bt = tables.cpu().numpy()
+        tk = torch.from_numpy(rng.integers(0, V, (5, N)).astype(np.int32)).to(DEV)
+        q, k, v, ik = model.rows(tk)
+        out = step.attend(q, k, v, ik)
+        kp, vp = caches.k_pages.cpu().numpy(), caches.v_pages.cpu().numpy()
+        chain = np.stack([R.masks_of(list(range(-1, N - 1)))] * 5)
+        want = R.attend(q.float().cpu().numpy(), kp, vp, bt, cur + N, np.full(5, N), chain, 0, 0,
+                        step.scale)
+        assert np.all(np.abs(out.float().cpu().numpy() - want[0]) <= want[2])
+        pt = torch.tensor([list(range(-1, N - 1))] * 5, dtype=torch.int32, device=DEV)
+        target = torch.full((5, N, V), 1.0 / V, device=DEV)
+        u = torch.zeros((5, N), device=DEV)  # all stand but, in one step, the first child's third
+        if it == 1:
+            u[0, 3] = 0.5
+        step.verify(target, None, tk, pt, u, torch.rand((5,), device=DEV))
+        assert m.mx4_check_status() == 0
+        cur = cur + N
+        if it == 1:
+            cur[0] -= 2
+        assert np.array_equal(step.seq_lens.cpu().numpy(), cur)
+    assert all(len(set(bt[s][bt[s] >= 0])) == (cur[s] + 127) // 128 for s in range(5))
+    book.free(tables, step.seq_lens)
+    book.free(table, parents_lens)
+    assert m.mx4_check_status() == 0
+    assert int(book.free_count) == caches.num_pages and not book.ref_counts.any()

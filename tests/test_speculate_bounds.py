@@ -108,3 +108,38 @@ def test_ended_sequences_give_all_their_pages_back(host_pages):
     book.free(children, cl)
     book.free(table, lens)
     assert int(book.free_count) == 12 and not book.ref_counts.any()
+
+
+def test_sequences_grow_by_pages_off_the_stack(host_pages):
+    # a child of a full page has no page for its next token: it takes one, in row order from the
+    # top, and all pages come back in the end
+    table = torch.tensor([[3, 5, -1], [7, -1, -1]], dtype=torch.int32)
+    lens = torch.tensor([250, 128], dtype=torch.int32)
+    book = PageBook(10, table)
+    assert book.free_list.tolist() == [0, 1, 2, 4, 6, 8, 9, -1, -1, -1]
+    children, cl = book.fork(torch.tensor([1, 0, 1], dtype=torch.int32), table, lens, host_pages)
+    assert children.tolist() == [[7, -1, -1], [3, 9, -1], [7, -1, -1]]
+    book.grow(children, cl, 6)
+    assert children.tolist() == [[7, 8, -1], [3, 9, -1], [7, 6, -1]] and int(book.free_count) == 4
+    book.grow(children, cl, 7)  # 250 + 7: one more for the second row alone
+    assert children.tolist() == [[7, 8, -1], [3, 9, 4], [7, 6, -1]] and int(book.free_count) == 3
+    assert [int(book.ref_counts[p]) for p in (7, 8, 3, 9, 4, 6, 0)] == [3, 1, 2, 1, 1, 1, 0]
+    # as many as the table and the stack have: rows in order, no page twice
+    book.grow(table, torch.tensor([250, 384], dtype=torch.int32), 1 << 20)
+    assert table.tolist() == [[3, 5, 2], [7, 1, 0]] and int(book.free_count) == 0
+    book.grow(children, cl, 200)
+    assert children.tolist() == [[7, 8, -1], [3, 9, 4], [7, 6, -1]] and int(book.free_count) == 0
+    book.free(children, cl)
+    book.free(table, lens)
+    assert int(book.free_count) == 10 and not book.ref_counts.any()
+
+
+def test_growing_takes_no_page_from_a_bad_stack_or_for_a_bad_length():
+    table = torch.tensor([[3, -1], [0, -1], [1, -1]], dtype=torch.int32)
+    book = PageBook(6, table)
+    book.free_list[book.free_count - 1] = 77
+    book.grow(table, torch.tensor([128, -300, 128], dtype=torch.int32), 1)
+    assert table.tolist() == [[3, -1], [0, -1], [1, 4]] and int(book.free_count) == 1
+    book.free_count.fill_(-3)
+    book.grow(table, torch.tensor([128, 128, 128], dtype=torch.int32), 1)
+    assert table.tolist() == [[3, -1], [0, -1], [1, 4]]
