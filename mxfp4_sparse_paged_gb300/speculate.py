@@ -116,6 +116,8 @@ class PageBook:
         dev = tables.device
         self.ref_counts = torch.zeros((num_pages,), dtype=torch.int32, device=dev)
         used = tables[tables >= 0].long()
+        if used.numel() and int(used.max()) >= num_pages:
+            raise ValueError(f"tables hold page {int(used.max())} of a pool of {num_pages}")
         self.ref_counts.index_add_(0, used, torch.ones_like(used, dtype=torch.int32))
         free = (self.ref_counts == 0).nonzero()[:, 0].to(torch.int32)
         self.free_list = torch.full((num_pages,), -1, dtype=torch.int32, device=dev)

@@ -143,3 +143,8 @@ def test_growing_takes_no_page_from_a_bad_stack_or_for_a_bad_length():
     book.free_count.fill_(-3)
     book.grow(table, torch.tensor([128, 128, 128], dtype=torch.int32), 1)
     assert table.tolist() == [[3, -1], [0, -1], [1, 4]]
+
+
+def test_page_ids_outside_the_pool_are_refused():
+    with pytest.raises(ValueError, match="page 6 of a pool of 6"):
+        PageBook(6, torch.tensor([[3, 5], [6, -1]], dtype=torch.int32))
