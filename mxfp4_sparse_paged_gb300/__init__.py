@@ -140,8 +140,11 @@ def _load():
 def _stream(stream):
     if stream is None:  # the current stream, without making an object of it
         try:
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        except RuntimeError:  # no GPU: the arguments' own check says so
+            try:
+                return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            except AttributeError:  # not in this torch
+                return torch.cuda.current_stream().cuda_stream
+        except (RuntimeError, AssertionError):  # no GPU: the arguments' own check says so
             return None
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
