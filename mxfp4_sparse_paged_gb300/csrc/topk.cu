@@ -312,8 +312,11 @@ topk_threshold_kernel(const float* __restrict__ scores, int64_t ld,
   pdl_launch_dependents();
   const int64_t t = blockIdx.x;
   const int64_t n = row_len(seq_lens, t, Q);
-  if (!use_filter(n, ld, k)) return;
+  const bool filtered = use_filter(n, ld, k);
+  // One CTA waits whatever its row: the kernels behind take this one's end for the scorer's.
+  if (!filtered && t > 0) return;
   pdl_wait();
+  if (!filtered) return;
   uint32_t smp[kSamplePer];
   load_sample(scores + t * ld, n, smp);
   uint32_t thr, unused;
