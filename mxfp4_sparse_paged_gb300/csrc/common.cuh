@@ -39,12 +39,16 @@ __device__ __forceinline__ float e2m1_to_float(uint32_t c) {
 // Programmatic dependent launch.  Every kernel of the library is launched with
 // launch_pdl and signals its dependents as soon as it starts (attention over drafts: once it
 // has its tensor memory), so the next kernel in the stream can be scheduled while this one
-// drains; but for the kernels that write lengths or block tables, which do not signal: their
-// dependents start when they have completed.  A kernel may run code
-// before pdl_wait() only if it reads inputs that no signalling kernel writes
-// (sequence lengths, block tables) and writes nothing but shared memory;
-// pdl_wait() returns once the previous kernel in the stream has completed and
-// its writes are visible (at once when there is none).
+// drains.  pdl_wait() returns once the previous kernel in the stream has completed and its
+// writes are visible (at once when there is none), and nothing else says so: a kernel that
+// did not signal has only ended when its dependents start.  So
+//   - the first kernel of a call reads what a caller or another call may have written
+//     (lengths and block tables among it) after pdl_wait();
+//   - one further on in a call may read such inputs before pdl_wait() where the first signals
+//     after its own pdl_wait() (the scorer, the selection's filter): those writes are done then;
+//   - in every kernel one CTA at least waits: the kernel behind takes its end for the end of
+//     all in front.
+// Kernels that write lengths or tables (accept, fork) signal late, by ending.
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }

@@ -24,7 +24,7 @@ cudaError_t launch_index_score_mxq(const uint16_t*, int, const uint8_t*, int64_t
                                    const int32_t*, int, int64_t, const int32_t*, float*, int64_t,
                                    uint32_t*, int, cudaStream_t);
 cudaError_t launch_topk(const float*, int64_t, const int32_t*, int64_t, int, int, int32_t*,
-                        void*, uint32_t*, int, cudaStream_t);
+                        void*, bool, uint32_t*, int, cudaStream_t);
 size_t topk_workspace_bytes(int64_t, int, int64_t);
 cudaError_t launch_norm_rope_insert(const float*, const float*, const float*, const float*,
                                     const float*, int64_t, int, int, const int64_t*, const float*,
@@ -335,7 +335,7 @@ int index_topk(const uint16_t* iq, int64_t T, int q_per_seq, const uint8_t* idx_
                                           ld_scores, d->status, d->num_sms, s);
   if (e == cudaSuccess)
     e = mx4::launch_topk(scores, ld_scores, seq_lens, T, q_per_seq, k, topk_idx,
-                         need > 0 ? ws : nullptr, d->status, d->num_sms, s);
+                         need > 0 ? ws : nullptr, false, d->status, d->num_sms, s);
   return cuda_result(e, kName);
 }
 
@@ -418,7 +418,7 @@ int topk_select(const float* scores, int64_t ld_scores, const int32_t* seq_lens,
   DeviceInfo* d;
   if (int rc = device_info(&d)) return rc;
   return cuda_result(mx4::launch_topk(scores, ld_scores, seq_lens, T, q_per_seq, k, topk_idx,
-                                      need > 0 ? ws : nullptr, d->status, d->num_sms,
+                                      need > 0 ? ws : nullptr, true, d->status, d->num_sms,
                                       static_cast<cudaStream_t>(stream)),
                      "topk_select");
 }

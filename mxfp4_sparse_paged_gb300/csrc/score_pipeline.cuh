@@ -145,6 +145,7 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
   int* pref = reinterpret_cast<int*>(smem_raw + Lay::kPrefOff);
   const int B = a.B;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();  // the kernel in front may have written lengths, tables or pages
   pdl_launch_dependents();
 
   // ---- pages per sequence and their prefix sum (contiguous segment per thread)
@@ -185,7 +186,6 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
     fence_barrier_init();
   }
   __syncthreads();
-  pdl_wait();  // pages (written by the insert) and scores are touched from here on
 
   const int total = B > 0 ? pref[B - 1] : 0;
   const int G = gridDim.x;

@@ -1,10 +1,6 @@
 // The steps around tree_paged_decode in a speculative decode step: which drafted
 // tokens stand (verify_drafts), the cache rows of the ones that do (accept_rows),
 // and sequences that branch and end (fork_pages, free_pages).
-//
-// Kernels that write lengths or block tables (accept, fork) do not signal their
-// dependents early: the library's other kernels read lengths and tables before they
-// wait for the kernel in front of them, so that kernel must have completed.
 #include <cooperative_groups.h>
 
 #include <algorithm>
