@@ -656,3 +656,21 @@ def test_lengths_written_by_a_call_are_read_by_the_next():
         assert torch.equal(out, first)
     assert m.mx4_check_status() == 0
     a.check(out, lse)
+
+
+@pytest.mark.parametrize("N,H,kind", [(1, 16, "chain"), (5, 7, "tree")])
+def test_more_sequences_than_a_launch_holds(N, H, kind):
+    # 300: a launch of 256 and one of 44 over the same workspace, masks, counts and lse with it;
+    # two long ones at the launches' border and one idle
+    rng = np.random.default_rng(N)
+    lens = [int(x) for x in rng.integers(N, 200, 300)]
+    lens[255], lens[256], lens[299] = 3000, 5000, 700
+    counts = rng.integers(1, N + 1, 300)
+    counts[7] = counts[290] = 0
+    a = Attn(40 + N, lens, N, H=H, kind=kind, counts=counts, window=150 if kind == "tree" else 0, sinks=2)
+    want = a.want()
+    out, lse = a.run()
+    assert m.mx4_check_status() == 0
+    a.check(out, lse, want)
+    again, _ = a.run(lse=False)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
