@@ -26,7 +26,7 @@
 // P in bf16, like the results: half a step, 2^-9, of each weight (its fp32 value goes into the row's
 // sum), which takes the 2-norm error of the results from 1.7e-3, bf16's own, to 2.3e-3, and to
 // 3.2e-3 where single tokens hold most of a row.  P as the sum of two bf16 numbers leaves 1.7e-3,
-// but costs 256 ragged single tokens 178 us for 161, and trees of 64 nodes 746 for 447.
+// but costs 256 ragged single tokens 11 % more time, and trees of 64 nodes 67 %.
 //
 // Softmax.  bf16 and fp32 hold the weights to the same relative precision at any size, so
 // the reference of a row need not be its running maximum: it is the maximum of the page
@@ -50,7 +50,7 @@
 // tile there are two groups a CTA and two CTAs an SM, which fill each other's waits.  More rows
 // share a page's fixed costs (V's dequantisation, the barrier, the products' latency) in tiles of
 // 128 by four groups and one CTA an SM: 16 trees of 64 nodes and 16 heads over 4096 to 65536
-// tokens took 564 us in tiles of 64, 460 in tiles of 128.  (Warps of fixed roles handing pages to
+// tokens take 563 us in tiles of 64, 442 in tiles of 128.  (Warps of fixed roles handing pages to
 // each other by barriers, 12 to 20 a CTA, took two to three times as long: each hand-over cost a
 // few hundred cycles.)
 // All waits are bounded; after one that runs out the CTA goes through its loop without waiting
@@ -1279,7 +1279,7 @@ cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
 }
 
 // Rows a tile: the smallest that holds all of a sequence's rows of one KV head, else the
-// largest.  (Three stages of K at 128 rows: 450 us for 466 with two.)
+// largest.  (Three stages of K at 128 rows: 442 us for 456 with two.)
 //               NR groups KS VS CTAs
 using C16 = Cfg<16, 2, 2, 2, 2>;
 using C32 = Cfg<32, 2, 2, 2, 2>;

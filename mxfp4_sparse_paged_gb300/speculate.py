@@ -26,14 +26,15 @@ def tree_masks(parents: torch.Tensor) -> torch.Tensor:
     word (s, j) set where i is j or an ancestor of j.  A parent that is not before its node is
     none (verify_drafts reports it); parents[:, 0] is not read."""
     B, N = parents.shape
-    masks = torch.zeros((B, N), dtype=torch.int64, device=parents.device)
-    masks[:, 0] = 1
-    for j in range(1, N):
-        p = parents[:, j].long()
-        up = masks.gather(1, p.clamp(0, j - 1)[:, None])[:, 0]
-        bit = (1 << j) if j < 63 else -(1 << 63)
-        masks[:, j] = torch.where((p >= 0) & (p < j), up, 0) | bit
-    return masks
+    node = torch.arange(N + 1, device=parents.device)
+    # column N: no node.  Each pass doubles the ancestors in a mask and how far `up` leads.
+    up = torch.full((B, N + 1), N, dtype=torch.int64, device=parents.device)
+    up[:, 1:N] = torch.where((parents >= 0) & (parents < node[:N]), parents, N)[:, 1:]
+    masks = torch.where(node < N, torch.ones_like(node) << node.clamp_max(N - 1), 0).expand(B, -1)
+    for _ in range((N - 1).bit_length()):
+        masks = masks | masks.gather(1, up)
+        up = up.gather(1, up)
+    return masks[:, :N].contiguous()
 
 
 class SpeculativeStep:
