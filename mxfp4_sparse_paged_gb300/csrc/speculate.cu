@@ -44,8 +44,10 @@ namespace mx4 {
 // 256th of it that the next token is in.
 // Every thread runs the walk itself on the same numbers, so it needs no broadcast.
 // 64 trees of 32 nodes over 131072 tokens take 65 us (rejections follow one another, about 2 us
-// each for a cluster, in two waves of clusters), 256 given chains of 8 over 50001 tokens 28 us
-// (with rows kept by clusters of four 45 us), one chain of 4 over 32000 tokens 11 us.
+// each for a cluster, in two waves of clusters; 77 us over 131073, 104 over 262144 by E = 0), 256
+// given chains of 8 over 50001 tokens 30 us (with rows kept by clusters of four half as much
+// again), one chain of 4 over 32000 tokens 13 us.  (Rows from memory, an event pair around a graph;
+// among other passes on fresh inputs 65, 20 and 9.5 us.)
 constexpr int kMaxNodes = 64;
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
@@ -165,26 +167,27 @@ struct Fixed {
     put(two(a ? first(d) : 0.f, b ? second(d) : 0.f));
     put_small(two(a ? first(c) : 0.f, b ? second(c) : 0.f));
   }
-  // (at most kFull; the steps of 2^-22 alone say where 64 bits would not hold the sum)
-  __device__ __forceinline__ int64_t total() const {
+  // (where it is below 4)
+  __device__ __forceinline__ int64_t value() const {
     const int n = 2 * pairs, m = 2 * corrections;
-    const int coarse = (int)(h - n * 0x40400000u);
-    const int64_t t = ((int64_t)min(coarse, 3 << 22) << 39) +
-                      ((int64_t)(int)(l - n * 0x34C00000u) << 16) +
-                      ((int64_t)(int)(lc - m * 0x35400000u) << 17) +
-                      (int64_t)(int)(z - (n + m) * 0x2CC00000u);
-    return min(t, kFull);
+    return (int64_t)((uint64_t)coarse() << 39) + ((int64_t)(int)(l - n * 0x34C00000u) << 16) +
+           ((int64_t)(int)(lc - m * 0x35400000u) << 17) + (int64_t)(int)(z - (n + m) * 0x2CC00000u);
+  }
+  // the multiples of 2^-22 alone: they say where 64 bits would not hold the sum
+  __device__ __forceinline__ int coarse() const { return (int)(h - 2 * pairs * 0x40400000u); }
+  __device__ __forceinline__ int64_t total() const {
+    return coarse() >= 3 << 22 ? kFull : min(value(), kFull);
   }
 };
 __device__ __forceinline__ uint64_t to_fixed(float p) {
   Fixed x;
   x.put(two(p, 0.f));
-  return (uint64_t)x.total();
+  return (uint64_t)x.value();
 }
 __device__ __forceinline__ uint64_t left_of(float p, float q, const Factor& S) {
   Fixed x;
   x.put(two(p, 0.f), two(q, 0.f), S);
-  return (uint64_t)x.total();
+  return (uint64_t)x.value();
 }
 
 // x >> n, 0 for n of 64 and more
@@ -204,10 +207,17 @@ __device__ __forceinline__ bool stands(float u, float q, float p) {
   return h < p || (h == p && fmaf(u, q, -h) < 0.f);
 }
 
+// A sum of numbers of at most kFull, stopped there.  Their top bits, added up alone, say whether
+// the 64-bit sum may have wrapped (they alone decide from 3 on).
+__device__ __forceinline__ int top(int64_t x) { return (int)(x >> 41); }
+__device__ __forceinline__ int64_t stopped(int64_t sum, int tops) {
+  return tops >= 3 << 20 ? kFull : min(sum, kFull);
+}
 __device__ __forceinline__ int64_t warp_sum(int64_t x) {
+  const int tops = __reduce_add_sync(0xFFFFFFFFu, top(x));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = min(x + __shfl_xor_sync(0xFFFFFFFFu, x, o), kFull);
-  return x;
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  return stopped(x, tops);
 }
 
 template <int E, bool kGiven>
@@ -323,6 +333,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   auto range_sum = [&](int b0, int b1) {
     int64_t sum = 0;
     const bool two_rows = !kGiven && k > 0;
+    Fixed x;
     for (int b = b0 + lane; b < b1; b += 32 * kVerUnroll) {
       float pv[kVerUnroll], qv[kVerUnroll];
 #pragma unroll
@@ -340,7 +351,6 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
           for (int i = 0; i < kVerUnroll; ++i)
             if (at == 32 * i) pv[i] = 0.f;
         }
-      Fixed x;
 #pragma unroll
       for (int i = 0; i < kVerUnroll; i += 2) {
         if (two_rows)
@@ -348,9 +358,12 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
         else
           x.put(two(pv[i], pv[i + 1]));
       }
-      sum = min(sum + x.total(), kFull);
+      if (x.pairs >= 64) {
+        sum = min(sum + x.total(), kFull);
+        x = Fixed{};
+      }
     }
-    return warp_sum(sum);
+    return warp_sum(min(sum + x.total(), kFull));
   };
   // the sum of the residual, with the warp and CTA sums left in place `pass & 1`
   int pass = 0;
@@ -383,9 +396,14 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     }
     cluster.sync();
     int64_t t = 0;
+    int tops = 0;
 #pragma unroll
-    for (int i = 0; i < kVerMaxCluster; ++i) t = min(t + (i < C ? s_part[pass & 1][i] : 0), kFull);
-    return (uint64_t)max(t, (int64_t)0);
+    for (int i = 0; i < kVerMaxCluster; ++i) {
+      const int64_t x = i < C ? s_part[pass & 1][i] : 0;
+      t += x;
+      tops += top(x);
+    }
+    return (uint64_t)max(stopped(t, tops), (int64_t)0);
   };
 
   // children of cur, by node (they come after it)
