@@ -460,9 +460,9 @@ int mx4_decode_steps(int64_t n_steps, const void *h_inputs, size_t h_inputs_stri
  * Logits, softmax statistics and sums are fp32; the weights are rounded to bf16 for the
  * product with V, as is the output.  The sums before their division overflow for no result
  * below 2^118 / (tokens seen); past that one may come out infinite.  1 <= N <= 64,
- * 1 <= Hkv <= 8, H a multiple of Hkv, H <= 128, B <= 65535.  A bad length (seq_len < n_nodes, or beyond the block table) gives
- * zeros and sets MX4_STATUS_BAD_LEN; tokens on a bad page are not seen
- * (MX4_STATUS_BAD_PAGE).
+ * 1 <= Hkv <= 8, H a multiple of Hkv, H <= 128, B <= 65535.  A bad length (seq_len <
+ * n_nodes, or beyond the block table) gives zeros and sets MX4_STATUS_BAD_LEN; tokens on a
+ * bad page are not seen (MX4_STATUS_BAD_PAGE).
  * ------------------------------------------------------------------------- */
 int tree_paged_decode(const uint16_t *q, int64_t B, int N, int H, int Hkv,
                       const uint8_t *k_pages, const uint8_t *v_pages, int64_t kv_page_stride,
@@ -523,8 +523,9 @@ int verify_drafts(const float *target, int64_t t_batch_stride, int64_t t_node_st
  *   new_lens     int32 [B] (output; not seq_lens itself)
  * A path that does not ascend within the nodes (MX4_STATUS_BAD_INDEX), a bad length or
  * count (MX4_STATUS_BAD_LEN) or a bad page of an accepted row, moved or not
- * (MX4_STATUS_BAD_PAGE), leaves the sequence's rows alone, with new_lens[s] = seq_lens[s].  The drafted rows' pages belong to this
- * sequence alone (mx4_fork_pages copies the page that is being filled).
+ * (MX4_STATUS_BAD_PAGE), leaves the sequence's rows alone, with new_lens[s] = seq_lens[s].
+ * The drafted rows' pages belong to this sequence alone (mx4_fork_pages copies the page
+ * that is being filled).
  * 1 <= N <= 64, 0 <= Hkv <= 8.
  * ------------------------------------------------------------------------- */
 int mx4_accept_rows(const int32_t *path, const int32_t *n_accepted, const int32_t *seq_lens,

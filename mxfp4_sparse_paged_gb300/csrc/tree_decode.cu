@@ -50,7 +50,7 @@
 // tile there are two groups a CTA and two CTAs an SM, which fill each other's waits.  More rows
 // share a page's fixed costs (V's dequantisation, the barrier, the products' latency) in tiles of
 // 128 by four groups and one CTA an SM: 16 trees of 64 nodes and 16 heads over 4096 to 65536
-// tokens take 563 us in tiles of 64, 442 in tiles of 128.  (Warps of fixed roles handing pages to
+// tokens take 563 us in tiles of 64, 443 in tiles of 128.  (Warps of fixed roles handing pages to
 // each other by barriers, 12 to 20 a CTA, took two to three times as long: each hand-over cost a
 // few hundred cycles.)
 // All waits are bounded; after one that runs out the CTA goes through its loop without waiting
@@ -1279,7 +1279,7 @@ cudaError_t launch(Args a, int64_t B, int num_sms, cudaStream_t stream) {
 }
 
 // Rows a tile: the smallest that holds all of a sequence's rows of one KV head, else the
-// largest.  (Three stages of K at 128 rows: 442 us for 456 with two.)
+// largest.  (Three stages of K at 128 rows: 443 us for 456 with two.)
 //               NR groups KS VS CTAs
 using C16 = Cfg<16, 2, 2, 2, 2>;
 using C32 = Cfg<32, 2, 2, 2, 2>;
