@@ -60,7 +60,7 @@ typedef enum {
 #define MX4_STATUS_BAD_PAGE 0x2u   /* block-table entry outside [0, num_pages) */
 #define MX4_STATUS_BAD_LEN 0x4u    /* seq_len < q, or beyond the block table / ld */
 #define MX4_STATUS_BAD_INDEX 0x8u  /* top-k index outside [0, position] */
-#define MX4_STATUS_BAD_VALUE 0x10u /* non-finite fp32 input to mx4_insert */
+#define MX4_STATUS_BAD_VALUE 0x10u /* non-finite input to an insert or append */
 #define MX4_STATUS_TIMEOUT 0x20u   /* a kernel gave up a bounded wait (should not happen) */
 #define MX4_STATUS_NO_PAGES 0x40u  /* mx4_fork_pages: the free list ran out */
 #define MX4_STATUS_BAD_REF 0x80u   /* mx4_free_pages: a page that nobody holds */
@@ -566,6 +566,122 @@ int mx4_fork_pages(const int32_t *rows, int64_t n, const int32_t *block_table, i
 int mx4_free_pages(const int32_t *tables, int64_t n, int64_t bt_width, const int32_t *lens,
                    int32_t *ref_counts, int64_t num_pages, int32_t *free_list,
                    int32_t *free_count, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit K/V cache ("vllm.models.minimax_m3.amd.mono.dispatch", _config_refusal: the fp8
+ * K/V cache of the other revision).  A page holds 128 token rows of one head as 128 OCP E4M3
+ * bytes each: k_pages, v_pages uint8 [num_pages, Hkv, 16384] with one page stride and one head
+ * stride for both.  Every 32 tokens of a page and head (a block of tokens) share the scale
+ * 2^(byte - 127): k_scales, v_scales uint8 [num_pages, Hkv, 4], contiguous.  A value is its
+ * E4M3 number times its block's scale; a scale byte of 255 is NaN.  Page p of sequence s's
+ * token i is block_table[s*bt_width + i/128], as in the MXFP4 cache.
+ *
+ * fp8_rope_append -- new tokens' q and K heads turned by their positions; q out as bf16, K and
+ * V appended to the cache.  cu_new int32 [B+1] ascending: the new tokens of sequence s are the
+ * rows t = cu_new[s] .. cu_new[s+1] - 1 of q, k and v, at the sequence's last positions: row t
+ * at seq_lens[s] - cu_new[s+1] + t (seq_lens counts them).  Rows behind the last sequence's (and
+ * before cu_new[0]) are left alone, their q_out rows as they were.
+ *   Turn: of a head's first rot dims, pair i (i < rot/2) is dims (i, i + rot/2), or (2i, 2i+1) if
+ *     interleaved, and becomes factor * (x_a c - x_b s, x_b c + x_a s), c and s the cosine and sine
+ *     of position * phases[i] / 2^64 turns (phases[i]: the angle a position in turns, as an unsigned
+ *     64-bit binary fraction).  The product is taken modulo one turn, exact for positions of any
+ *     size.  positions int64 [T] are the positions to turn by, NULL: those in the cache.  fp32.
+ *   Store: of each block of tokens and head, E is the smallest exponent >= -127 with
+ *     amax <= 448 * 2^E over the call's new rows, and no smaller than the block's stored E if the
+ *     block has rows before them (255 counts as -127 there).  New rows are the nearest E4M3
+ *     numbers (ties to even) to x / 2^E; rows stored before, where E grew, the nearest to theirs
+ *     divided by the growth.  Scale bytes are E + 127.  Non-finite elements (after the turn) are
+ *     stored as NaN, do not count for amax and set MX4_STATUS_BAD_VALUE.
+ *
+ *   q, k, v     fp32 (fp32 != 0) or bf16, [T, H, 128], [T, Hkv, 128] with q_stride, k_stride,
+ *               v_stride elements a token (heads contiguous); row starts aligned to 4 elements.
+ *               q may be NULL with q_out (K and V alone)
+ *   q_out       bf16 [T, H, 128], contiguous, 8-byte aligned
+ *   rot         0 (no turn; phases may be NULL) .. 128, a multiple of 8
+ * A sequence with more new tokens than seq_len, seq_len > bt_width*128 or cu_new[s+1] > T is
+ * skipped (MX4_STATUS_BAD_LEN), a block whose page id is outside the pool too
+ * (MX4_STATUS_BAD_PAGE).  Two sequences must not append to the same block of a shared page.
+ * H <= 128, Hkv <= 8, T <= 2^24, B <= 2^24.
+ * ------------------------------------------------------------------------- */
+int fp8_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                    const void *v, int64_t v_stride, int fp32, int64_t T, int H, int Hkv,
+                    const int32_t *cu_new, int64_t B, const int64_t *positions,
+                    const int64_t *phases, int rot, int interleaved, float factor,
+                    const int32_t *block_table, int64_t bt_width, const int32_t *seq_lens,
+                    uint8_t *k_pages, uint8_t *v_pages, int64_t kv_page_stride,
+                    int64_t kv_head_stride, int64_t num_pages, uint8_t *k_scales,
+                    uint8_t *v_scales, uint16_t *q_out, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * fp8_paged_decode, fp8_block_decode -- attention of the decode tokens over the 8-bit cache.
+ * For decode token t = s*q + j at position p = seq_lens[s] - q + j and query head h (KV head
+ * h / (H / Hkv)):
+ *     l_i = scale * q[t][h] . K[s, i],  out[t][h] = sum_i softmax(l)_i V[s, i],
+ *     lse[t][h] = ln sum_i exp(l_i)
+ * over all cached tokens i <= p, or (fp8_block_decode) those of the 128-token blocks that
+ * block_idx[t*kb ..] lists: block b is tokens 128 b .. 128 b + 127.  Entries may come in any
+ * order, a block listed twice counts twice, negative entries are skipped (the padding of
+ * block_topk).  Tokens past p hold whatever they hold: they reach no result.  Logits, the sum and
+ * the accumulator are fp32, weights 11 bits of f16 (relative to the largest of a row down to
+ * 2^-22, absolute below).  A token that sees nothing (p < 0: a sequence shorter than q, down to
+ * empty; no block) gets zeros and an lse of -inf.
+ *
+ *   q         bf16 [T, H, 128], contiguous, T = B * q_per_seq, 16-byte aligned
+ *   out       bf16 [T, H, 128], 16-byte aligned; lse fp32 [T, H] or NULL
+ *   block_idx int32 [T, kb]
+ *   ws        workspace of *_workspace(T, ...) bytes, 16-byte aligned; the size depends on the
+ *             current device's SM count and may be shared by calls that follow one another on a
+ *             stream
+ * H <= 128 a multiple of Hkv <= 8, 1 <= q_per_seq <= 8, B <= 65535, bt_width <= 2^20,
+ * 1 <= kb <= 4096; scale finite.  A negative seq_len or one past bt_width*128 counts as empty
+ * (MX4_STATUS_BAD_LEN), a block past the token's own is skipped (MX4_STATUS_BAD_INDEX), so are
+ * the tokens of a page id outside the pool (MX4_STATUS_BAD_PAGE).
+ * ------------------------------------------------------------------------- */
+int fp8_paged_decode(const uint16_t *q, int64_t T, int q_per_seq, int H, int Hkv,
+                     const uint8_t *k_pages, const uint8_t *v_pages, int64_t kv_page_stride,
+                     int64_t kv_head_stride, int64_t num_pages, const uint8_t *k_scales,
+                     const uint8_t *v_scales, const int32_t *block_table, int64_t B,
+                     int64_t bt_width, const int32_t *seq_lens, float scale, uint16_t *out,
+                     float *lse, void *ws, size_t ws_bytes, void *stream);
+size_t fp8_paged_decode_workspace(int64_t T, int q_per_seq, int H, int Hkv);
+int fp8_block_decode(const uint16_t *q, int64_t T, int q_per_seq, int H, int Hkv,
+                     const uint8_t *k_pages, const uint8_t *v_pages, int64_t kv_page_stride,
+                     int64_t kv_head_stride, int64_t num_pages, const uint8_t *k_scales,
+                     const uint8_t *v_scales, const int32_t *block_table, int64_t B,
+                     int64_t bt_width, const int32_t *seq_lens, const int32_t *block_idx, int kb,
+                     float scale, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
+                     void *stream);
+size_t fp8_block_decode_workspace(int64_t T, int kb, int H, int Hkv);
+
+/* ---------------------------------------------------------------------------
+ * index_block_score, index_block_score_fp8 -- a cheap score of every 128-token block for each
+ * decode token: the largest index score (index_score, index_score_fp8) of the block's tokens,
+ *     scores[t*ld_scores + b] = max over i of block b, i <= p of the index score of token i,
+ * -inf where the token sees none of the block; entries at b >= ceil(seq_len / 128) are not
+ * written.  A NaN score makes its block's NaN.
+ *   scores  fp32 [T, ld_scores]
+ * The rest, limits and status bits as index_score and index_score_fp8, but that a seq_len of
+ * 0 .. q-1 is allowed (tokens before position 0 see nothing), ld_scores counts blocks, and the
+ * scores of a page id outside the pool are -inf (MX4_STATUS_BAD_PAGE).
+ *
+ * block_topk -- of decode token t's n = p/128 + 1 blocks (p < 0: none) the min(k, n) best:
+ * the first `first` and the last `last` (the token's own and those before it) always, then the
+ * largest scores, ties to the lower index (NaN above all, -0.0 equal to +0.0); written in
+ * ascending order to block_idx[t*k ..], -1 padded.
+ *   scores fp32 [B * q_per_seq, ld_scores]; block_idx int32 [B * q_per_seq, k]
+ * 1 <= k <= 4096, first + last <= k, 1 <= ld_scores <= 65536, B <= 65535.  A negative seq_len or
+ * one with n > ld_scores writes a row of -1 (MX4_STATUS_BAD_LEN).
+ * ------------------------------------------------------------------------- */
+int index_block_score(const uint16_t *iq, int64_t T, int q_per_seq, const uint8_t *idx_pages,
+                      int64_t idx_page_stride, int64_t num_pages, const int32_t *block_table,
+                      int64_t B, int64_t bt_width, const int32_t *seq_lens, float *scores,
+                      int64_t ld_scores, void *stream);
+int index_block_score_fp8(const uint16_t *iq, int64_t T, int q_per_seq, const uint8_t *pages,
+                          int64_t page_stride, int64_t num_pages, const int32_t *block_table,
+                          int64_t B, int64_t bt_width, const int32_t *seq_lens, float scale,
+                          float *scores, int64_t ld_scores, void *stream);
+int block_topk(const float *scores, int64_t ld_scores, const int32_t *seq_lens, int64_t B,
+               int q_per_seq, int k, int first, int last, int32_t *block_idx, void *stream);
 
 /* ---------------------------------------------------------------------------
  * mx4_check_status -- synchronise `stream`, return MX4_OK if no kernel of this

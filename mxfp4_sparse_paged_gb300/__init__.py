@@ -18,12 +18,17 @@ import threading
 
 import torch
 
+from .rotary import rope_frequencies, rope_phases
+
 __all__ = ["mx4_insert", "mx4_norm_rope_insert", "fp8_index_insert", "index_score_fp8", "index_score", "index_score_mxq",
            "index_topk", "index_topk_workspace", "topk_select", "sparse_paged_decode",
            "topk_select_workspace", "sparse_paged_decode_workspace", "mx4_check_status",
            "sparse_paged_decode_noalloc", "NOALLOC_SCRATCH_BYTES", "mx4_decode_step", "mx4_decode_steps",
            "mx4_decode_step_input_layout", "tree_paged_decode", "tree_paged_decode_workspace",
            "verify_drafts", "mx4_accept_rows", "mx4_fork_pages", "mx4_free_pages",
+           "fp8_rope_append", "rope_frequencies", "rope_phases", "index_block_score",
+           "index_block_score_fp8", "block_topk", "fp8_paged_decode", "fp8_paged_decode_workspace",
+           "fp8_block_decode", "fp8_block_decode_workspace",
            "mx4_last_error", "mx4_page_bytes", "library_path", "Mx4Error", "PAGE_BYTES",
            "PAGE_TOKENS", "HEAD_DIM"]
 
@@ -131,6 +136,26 @@ def _load():
                                        i64, i32, i64, P, P, P]
         lib.mx4_free_pages.restype = i32
         lib.mx4_free_pages.argtypes = [P, i64, i64, P, P, i64, P, P, P]
+        lib.fp8_rope_append.restype = i32
+        lib.fp8_rope_append.argtypes = [P, i64, P, i64, P, i64, i32, i64, i32, i32, P, i64, P, P,
+                                        i32, i32, ctypes.c_float, P, i64, P, P, P, i64, i64, i64,
+                                        P, P, P, P]
+        lib.index_block_score.restype = i32
+        lib.index_block_score.argtypes = lib.index_score.argtypes
+        lib.index_block_score_fp8.restype = i32
+        lib.index_block_score_fp8.argtypes = lib.index_score_fp8.argtypes
+        lib.block_topk.restype = i32
+        lib.block_topk.argtypes = [P, i64, P, i64, i32, i32, i32, i32, P, P]
+        lib.fp8_paged_decode.restype = i32
+        lib.fp8_paged_decode.argtypes = [P, i64, i32, i32, i32, P, P, i64, i64, i64, P, P, P, i64,
+                                         i64, P, ctypes.c_float, P, P, P, sz, P]
+        lib.fp8_paged_decode_workspace.restype = sz
+        lib.fp8_paged_decode_workspace.argtypes = [i64, i32, i32, i32]
+        lib.fp8_block_decode.restype = i32
+        lib.fp8_block_decode.argtypes = [P, i64, i32, i32, i32, P, P, i64, i64, i64, P, P, P, i64,
+                                         i64, P, P, i32, ctypes.c_float, P, P, P, sz, P]
+        lib.fp8_block_decode_workspace.restype = sz
+        lib.fp8_block_decode_workspace.argtypes = [i64, i32, i32, i32]
         lib.mx4_check_status.restype = i32
         lib.mx4_check_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
         _lib = lib
@@ -753,6 +778,174 @@ def mx4_free_pages(tables, lens, ref_counts, free_list, free_count, stream=None)
           _arg(lens, i32, (n,), "lens"), _arg(ref_counts, i32, (P,), "ref_counts"), P,
           _arg(free_list, i32, (P,), "free_list"), _arg(free_count, i32, (1,), "free_count"),
           _stream(stream))
+
+
+# ---- the 8-bit K/V cache
+
+def _one_device(*tensors):
+    """All of a call's CUDA tensors live on the current device (where the call runs)."""
+    seen = {t.get_device() for t in tensors if t is not None}
+    seen.discard(-1)  # a host tensor: refused with the call
+    if not seen:
+        return
+    here = torch.cuda.current_device()
+    if seen != {here}:
+        raise ValueError(f"the call runs on device {here}, its tensors are on {sorted(seen)}")
+
+
+def _fp8_kv_pools(k_pages, v_pages, k_scales, v_scales):
+    """(K address, V address, page stride, head stride, pages), (scale addresses), KV heads."""
+    s, st = k_pages.shape, k_pages.stride()
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if not (t.dtype is torch.uint8 and len(t.shape) == 3 and t.shape[2] == FP8_PAGE_BYTES and
+                t.stride(2) == 1):
+            _need(t, torch.uint8, name, contiguous=False)
+            raise ValueError(f"{name}: uint8 pages need shape [P, Hkv, {FP8_PAGE_BYTES}] with a "
+                             f"contiguous byte axis, got {tuple(t.shape)} strides {t.stride()}")
+    if v_pages.shape != s or v_pages.stride() != st:
+        raise ValueError("k_pages and v_pages must have the same shape and strides")
+    scales = (_arg(k_scales, torch.uint8, (s[0], s[1], 4), "k_scales"),
+              _arg(v_scales, torch.uint8, (s[0], s[1], 4), "v_scales"))
+    kp = k_pages.data_ptr() if k_pages.is_cuda else _Host(k_pages)
+    vp = v_pages.data_ptr() if v_pages.is_cuda else _Host(v_pages)
+    return (kp, vp, st[0], st[1], s[0]), scales, s[1]
+
+
+def _head_rows(t, name, dtype, shape):
+    """(address, token stride) of [T, heads, 128] rows with contiguous heads."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        _dims(t, name, *shape)
+    st = t.stride()
+    if st[2] != 1 or (shape[1] > 1 and st[1] != HEAD_DIM):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {st}")
+    # (the stride of a single token says nothing)
+    return t.data_ptr() if t.is_cuda else _Host(t), st[0] if shape[0] > 1 else shape[1] * HEAD_DIM
+
+
+def fp8_rope_append(q, k, v, cu_new, block_table, seq_lens, k_pages, v_pages, k_scales, v_scales,
+                    q_out, phases=None, positions=None, interleaved=False, factor=1.0, stream=None):
+    """New tokens' q [T, H, 128] and k [T, Hkv, 128] turned by their positions (phases int64
+    [rot / 2] of rope_phases, None: not at all; positions int64 [T], None: those in the cache),
+    q to q_out bf16 [T, H, 128], K and v [T, Hkv, 128] to the 8-bit pages uint8 [P, Hkv, 16384]
+    with their scales uint8 [P, Hkv, 4].  q, k, v fp32 or bf16, heads contiguous, any token
+    stride.  cu_new int32 [B + 1]: sequence s's rows, the last of its seq_lens int32 [B] tokens.
+    q and q_out None: K and V alone."""
+    i32, i64 = torch.int32, torch.int64
+    T, Hkv, D = _sizes(k, "k", 3)
+    if D != HEAD_DIM:
+        _dims(k, "k", None, None, HEAD_DIM)
+    dtype = k.dtype
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise TypeError(f"k: expected torch.float32 or torch.bfloat16, got {dtype}")
+    B, W = _sizes(seq_lens, "seq_lens", 1)[0], _sizes(block_table, "block_table", 2)[1]
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    H, qp, qo = 0, (None, 0), None
+    if q is not None:
+        H = _sizes(q, "q", 3)[1]
+        qp = _head_rows(q, "q", dtype, (T, H, HEAD_DIM))
+        qo = _arg(q_out, torch.bfloat16, (T, H, HEAD_DIM), "q_out")
+    kr, vr = _head_rows(k, "k", dtype, (T, Hkv, HEAD_DIM)), _head_rows(v, "v", dtype, (T, Hkv, HEAD_DIM))
+    pools, scales, heads = _fp8_kv_pools(k_pages, v_pages, k_scales, v_scales)
+    if heads != Hkv:
+        raise ValueError(f"k_pages has {int(heads)} KV heads, k has {Hkv}")
+    rot = 0 if phases is None else 2 * _sizes(phases, "phases", 1)[0]
+    cu, pos = _arg(cu_new, i32, (B + 1,), "cu_new"), _opt(positions, i64, (T,), "positions")
+    ph = _arg(phases, i64, (rot // 2,), "phases") if rot else None
+    tables = _arg(block_table, i32, (B, W), "block_table"), W, _arg(seq_lens, i32, (B,), "seq_lens")
+    _one_device(q, k, v, cu_new, block_table, seq_lens, k_pages, v_pages, k_scales, v_scales, q_out,
+                phases, positions)
+    _call(_load().fp8_rope_append, *qp, *kr, *vr, dtype is torch.float32, T, H, Hkv, cu, B, pos, ph,
+          rot, bool(interleaved), factor, *tables, *pools, *scales, qo, _stream(stream))
+
+
+def index_block_score(iq, q_per_seq, idx_pages, block_table, seq_lens, scores, stream=None):
+    """scores[t, b] = the largest index_score of the tokens of block b (128 tokens, one page) that
+    decode token t sees, fp32 [T, ld], ld at least the most blocks of a sequence."""
+    _one_device(iq, idx_pages, block_table, seq_lens, scores)
+    _score_call("index_block_score", iq, q_per_seq, idx_pages, block_table, seq_lens, scores, stream)
+
+
+def index_block_score_fp8(iq, q_per_seq, pages, block_table, seq_lens, scale, scores, stream=None):
+    """index_block_score over the fp8 index cache."""
+    _one_device(iq, pages, block_table, seq_lens, scores)
+    _need(iq, torch.bfloat16, "iq")
+    _need(block_table, torch.int32, "block_table")
+    _need(seq_lens, torch.int32, "seq_lens")
+    _need(scores, torch.float32, "scores")
+    _fp8_pages(pages, "pages")
+    _dims(seq_lens, "seq_lens", None)
+    B = int(seq_lens.shape[0])
+    _dims(iq, "iq", B * int(q_per_seq), HEAD_DIM)
+    _dims(block_table, "block_table", None, None)
+    _rows_at_least(block_table, B, "block_table")
+    _dims(scores, "scores", None, None)
+    _rows_at_least(scores, B * int(q_per_seq), "scores")
+    _check(_load().index_block_score_fp8(_ptr(iq), int(iq.shape[0]), int(q_per_seq), _ptr(pages),
+                                         pages.stride(0), int(pages.shape[0]), _ptr(block_table), B,
+                                         int(block_table.shape[1]), _ptr(seq_lens), float(scale),
+                                         _ptr(scores), scores.stride(0), _stream(stream)))
+
+
+def block_topk(scores, seq_lens, q_per_seq, block_idx, first=0, last=0, stream=None):
+    """block_idx int32 [T, k]: for each decode token the first `first` and last `last` of its
+    blocks and those with the largest scores (fp32 [T, ld]), ties to the lower index, ascending,
+    -1 padded."""
+    B = _sizes(seq_lens, "seq_lens", 1)[0]
+    T = B * int(q_per_seq)
+    ld, k = _sizes(scores, "scores", 2)[1], _sizes(block_idx, "block_idx", 2)[1]
+    args = (_arg(scores, torch.float32, (T, ld), "scores"), ld, _arg(seq_lens, torch.int32, (B,), "seq_lens"),
+            B, q_per_seq, k, first, last, _arg(block_idx, torch.int32, (T, k), "block_idx"))
+    _one_device(scores, seq_lens, block_idx)
+    _call(_load().block_topk, *args, _stream(stream))
+
+
+def fp8_paged_decode_workspace(T, q_per_seq, H, Hkv) -> int:
+    return int(_load().fp8_paged_decode_workspace(int(T), int(q_per_seq), int(H), int(Hkv)))
+
+
+def fp8_block_decode_workspace(T, k, H, Hkv) -> int:
+    return int(_load().fp8_block_decode_workspace(int(T), int(k), int(H), int(Hkv)))
+
+
+def _fp8_decode_args(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, out,
+                     lse, block_idx=None):
+    i32, bf = torch.int32, torch.bfloat16
+    T, H, D = shape = _sizes(q, "q", 3)
+    if D != HEAD_DIM:
+        _dims(q, "q", None, None, HEAD_DIM)
+    B, W = _sizes(seq_lens, "seq_lens", 1)[0], _sizes(block_table, "block_table", 2)[1]
+    if T != B * q_per_seq:
+        raise ValueError(f"q has {T} tokens, seq_lens gives {B} x {int(q_per_seq)}")
+    qp, op = _arg(q, bf, shape, "q"), _arg(out, bf, shape, "out")
+    lp = _opt(lse, torch.float32, (T, H), "lse")
+    pools, scales, heads = _fp8_kv_pools(k_pages, v_pages, k_scales, v_scales)
+    tables = (_arg(block_table, i32, (B, W), "block_table"), B, W, _arg(seq_lens, i32, (B,), "seq_lens"))
+    _one_device(q, out, lse, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, block_idx)
+    return (qp, T, q_per_seq, H, heads, *pools, *scales, *tables), (op, lp)
+
+
+def fp8_paged_decode(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens,
+                     scale, out, ws, lse=None, stream=None):
+    """Attention of q bf16 [T, H, 128] (q_per_seq decode tokens a sequence, causal) over all cached
+    tokens of the 8-bit pages uint8 [P, Hkv, 16384], scales uint8 [P, Hkv, 4]: out bf16 like q,
+    lse fp32 [T, H] or None.  ws: uint8, fp8_paged_decode_workspace(T, q_per_seq, H, Hkv) bytes."""
+    args, outs = _fp8_decode_args(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table,
+                                  seq_lens, out, lse)
+    _call(_load().fp8_paged_decode, *args, scale, *outs, *_ws(ws), _stream(stream))
+
+
+def fp8_block_decode(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens,
+                     block_idx, scale, out, ws, lse=None, stream=None):
+    """fp8_paged_decode over the 128-token blocks that each token lists, block_idx int32 [T, k]
+    (negative entries are skipped).  ws: fp8_block_decode_workspace(T, k, H, Hkv) bytes."""
+    args, outs = _fp8_decode_args(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table,
+                                  seq_lens, out, lse, block_idx)
+    k = _sizes(block_idx, "block_idx", 2)[1]
+    idx = _arg(block_idx, torch.int32, (q.shape[0], k), "block_idx")
+    _call(_load().fp8_block_decode, *args, idx, k, scale, *outs, *_ws(ws), _stream(stream))
 
 
 def mx4_check_status(stream=None) -> int:

@@ -209,4 +209,16 @@ cudaError_t launch_index_score_fp8(const uint16_t* iq, int q, const uint8_t* pag
   }
 }
 
+// index_block_score_fp8: the largest score of each page (block mode of the pipeline).
+cudaError_t launch_index_block_score_fp8(const uint16_t* iq, int q, const uint8_t* pages,
+                                         int64_t page_stride, int64_t num_pages,
+                                         const int32_t* block_table, int B, int64_t bt_width,
+                                         const int32_t* seq_lens, float scale, float* scores,
+                                         int64_t ld, uint32_t* status, int num_sms,
+                                         cudaStream_t stream) {
+  const ScoreArgs a{iq, pages, page_stride, num_pages, block_table, B, bt_width, seq_lens,
+                    scores, ld, status, scale};
+  return launch_score_q<Fp8Fmt, true>(q, a, num_sms, stream);
+}
+
 }  // namespace mx4

@@ -58,6 +58,24 @@ cudaError_t launch_fork(const int32_t*, int64_t, const int32_t*, int64_t, int64_
                         cudaStream_t);
 cudaError_t launch_free(const int32_t*, int64_t, int64_t, const int32_t*, int32_t*, int64_t,
                         int32_t*, int32_t*, uint32_t*, cudaStream_t);
+cudaError_t launch_index_block_score(const uint16_t*, int, const uint8_t*, int64_t, int64_t,
+                                     const int32_t*, int, int64_t, const int32_t*, float*, int64_t,
+                                     uint32_t*, int, cudaStream_t);
+cudaError_t launch_index_block_score_fp8(const uint16_t*, int, const uint8_t*, int64_t, int64_t,
+                                         const int32_t*, int, int64_t, const int32_t*, float,
+                                         float*, int64_t, uint32_t*, int, cudaStream_t);
+cudaError_t launch_block_topk(const float*, int64_t, const int32_t*, int64_t, int, int, int, int,
+                              int32_t*, uint32_t*, cudaStream_t);
+cudaError_t launch_fp8_append(const void*, const void*, const void*, int, const int64_t*, int64_t,
+                              int, int, const int32_t*, int64_t, const int64_t*, const int64_t*,
+                              int, int, float, const int32_t*, int64_t, const int32_t*, uint8_t*,
+                              uint8_t*, int64_t, int64_t, int64_t, uint8_t*, uint8_t*, uint16_t*,
+                              uint32_t*, cudaStream_t);
+cudaError_t launch_fp8_decode(const uint16_t*, int64_t, int, int, int, const uint8_t*,
+                              const uint8_t*, const uint8_t*, const uint8_t*, int64_t, int64_t,
+                              int64_t, const int32_t*, int64_t, const int32_t*, const int32_t*,
+                              int, float, uint16_t*, float*, void*, uint32_t*, int, cudaStream_t);
+size_t fp8_decode_workspace_bytes(int, int);
 }  // namespace mx4
 
 // Device status word: kernels OR MX4_STATUS_* bits into it when they skip bad
@@ -189,6 +207,38 @@ int score_entry(const char* name, ScoreLaunch launch, const uint16_t* iq, int64_
   if (int rc = device_info(&d)) return rc;
   return cuda_result(launch(iq, q_per_seq, idx_pages, idx_page_stride, num_pages, block_table,
                             (int)B, bt_width, seq_lens, scores, ld_scores, d->status, d->num_sms,
+                            static_cast<cudaStream_t>(stream)),
+                     name);
+}
+
+// index_score_fp8 and index_block_score_fp8: the checks they share and the launch.
+using Fp8ScoreLaunch = cudaError_t (*)(const uint16_t*, int, const uint8_t*, int64_t, int64_t,
+                                       const int32_t*, int, int64_t, const int32_t*, float, float*,
+                                       int64_t, uint32_t*, int, cudaStream_t);
+int fp8_score_entry(const char* name, Fp8ScoreLaunch launch, const uint16_t* iq, int64_t T,
+                    int q_per_seq, const uint8_t* pages, int64_t page_stride, int64_t num_pages,
+                    const int32_t* block_table, int64_t B, int64_t bt_width,
+                    const int32_t* seq_lens, float scale, float* scores, int64_t ld_scores,
+                    void* stream) {
+  if (q_per_seq < 1 || q_per_seq > 8)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: q_per_seq = %d (supported 1..8)", name, q_per_seq);
+  if (B < 0 || B > 65535)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: B = %lld", name, (long long)B);
+  if (T != B * q_per_seq)
+    return fail(MX4_ERR_INVALID, "%s: T = %lld != B * q_per_seq", name, (long long)T);
+  if (!(scale > 0.f) || !(scale < INFINITY))
+    return fail(MX4_ERR_INVALID, "%s: scale must be finite and > 0", name);
+  if (B == 0) return ok();
+  if (!iq || !pages || !block_table || !seq_lens || !scores)
+    return fail(MX4_ERR_INVALID, "%s: NULL pointer", name);
+  if (!aligned(iq, 16) || !aligned(pages, 16) || page_stride % 16 || !aligned(scores, 4))
+    return fail(MX4_ERR_INVALID, "%s: misaligned iq, pages or page stride", name);
+  if (num_pages < 1 || page_stride < MX4_FP8_PAGE_BYTES || bt_width < 1 || ld_scores < 1)
+    return fail(MX4_ERR_INVALID, "%s: num_pages, page stride, bt_width or ld invalid", name);
+  DeviceInfo* d;
+  if (int rc = device_info(&d)) return rc;
+  return cuda_result(launch(iq, q_per_seq, pages, page_stride, num_pages, block_table, (int)B,
+                            bt_width, seq_lens, scale, scores, ld_scores, d->status, d->num_sms,
                             static_cast<cudaStream_t>(stream)),
                      name);
 }
@@ -365,30 +415,9 @@ int index_score_fp8(const uint16_t* iq, int64_t T, int q_per_seq, const uint8_t*
                     int64_t page_stride, int64_t num_pages, const int32_t* block_table,
                     int64_t B, int64_t bt_width, const int32_t* seq_lens, float scale,
                     float* scores, int64_t ld_scores, void* stream) {
-  if (q_per_seq < 1 || q_per_seq > 8)
-    return fail(MX4_ERR_UNSUPPORTED, "index_score_fp8: q_per_seq = %d (supported 1..8)",
-                q_per_seq);
-  if (B < 0 || B > 65535)
-    return fail(MX4_ERR_UNSUPPORTED, "index_score_fp8: B = %lld", (long long)B);
-  if (T != B * q_per_seq)
-    return fail(MX4_ERR_INVALID, "index_score_fp8: T = %lld != B * q_per_seq", (long long)T);
-  if (!(scale > 0.f) || !(scale < INFINITY))
-    return fail(MX4_ERR_INVALID, "index_score_fp8: scale must be finite and > 0");
-  if (B == 0) return ok();
-  if (!iq || !pages || !block_table || !seq_lens || !scores)
-    return fail(MX4_ERR_INVALID, "index_score_fp8: NULL pointer");
-  if (!aligned(iq, 16) || !aligned(pages, 16) || page_stride % 16 || !aligned(scores, 4))
-    return fail(MX4_ERR_INVALID, "index_score_fp8: misaligned iq, pages or page stride");
-  if (num_pages < 1 || page_stride < MX4_FP8_PAGE_BYTES || bt_width < 1 || ld_scores < 1)
-    return fail(MX4_ERR_INVALID,
-                "index_score_fp8: num_pages, page stride, bt_width or ld invalid");
-  DeviceInfo* d;
-  if (int rc = device_info(&d)) return rc;
-  return cuda_result(mx4::launch_index_score_fp8(iq, q_per_seq, pages, page_stride, num_pages,
-                                                 block_table, (int)B, bt_width, seq_lens, scale,
-                                                 scores, ld_scores, d->status, d->num_sms,
-                                                 static_cast<cudaStream_t>(stream)),
-                     "index_score_fp8");
+  return fp8_score_entry("index_score_fp8", mx4::launch_index_score_fp8, iq, T, q_per_seq, pages,
+                         page_stride, num_pages, block_table, B, bt_width, seq_lens, scale, scores,
+                         ld_scores, stream);
 }
 
 size_t topk_select_workspace(int64_t T, int k, int64_t ld_scores) {
@@ -998,5 +1027,211 @@ extern "C" int mx4_free_pages(const int32_t* tables, int64_t n, int64_t bt_width
   if (int rc = device_info(&d)) return rc;
   return cuda_result(mx4::launch_free(tables, n, bt_width, lens, ref_counts, num_pages, free_list,
                                       free_count, d->status, static_cast<cudaStream_t>(stream)),
+                     kName);
+}
+
+// ---------------------------------------------------------------------------
+// The 8-bit K/V cache: fp8_rope_append, fp8_paged_decode, fp8_block_decode, and the choice of
+// blocks: index_block_score, index_block_score_fp8, block_topk.
+
+namespace {
+
+bool finite(float x) { return x == x && x != INFINITY && x != -INFINITY; }
+
+int check_fp8_pools(const char* name, const uint8_t* k_pages, const uint8_t* v_pages,
+                    int64_t page_stride, int64_t head_stride, int Hkv, int64_t num_pages,
+                    const uint8_t* k_scales, const uint8_t* v_scales) {
+  if (!k_pages || !v_pages || !k_scales || !v_scales)
+    return fail(MX4_ERR_INVALID, "%s: NULL pages or scales", name);
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || page_stride % 16 ||
+      (Hkv > 1 && head_stride % 16))
+    return fail(MX4_ERR_INVALID, "%s: pages must be 16-byte aligned with 16-byte strides", name);
+  if (num_pages < 1 || num_pages > 0x7FFFFFFF || page_stride < MX4_FP8_PAGE_BYTES ||
+      page_stride >= (int64_t)1 << 40 ||
+      (Hkv > 1 && (head_stride < MX4_FP8_PAGE_BYTES || head_stride >= (int64_t)1 << 40)))
+    return fail(MX4_ERR_INVALID, "%s: num_pages or a stride out of range", name);
+  return MX4_OK;
+}
+
+int check_fp8_sizes(const char* name, int q_per_seq, int H, int Hkv, int64_t B) {
+  if (q_per_seq < 1 || q_per_seq > 8)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: q_per_seq = %d (supported 1..8)", name, q_per_seq);
+  if (Hkv < 1 || Hkv > 8 || H < 1 || H > 128 || H % Hkv)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: H = %d, Hkv = %d (H <= 128 a multiple of Hkv <= 8)", name,
+                H, Hkv);
+  if (B < 0 || B > 65535) return fail(MX4_ERR_UNSUPPORTED, "%s: B = %lld", name, (long long)B);
+  return MX4_OK;
+}
+
+// fp8_paged_decode (block_idx null, kb 0) and fp8_block_decode after their own checks.
+int fp8_decode_entry(const char* name, const uint16_t* q, int64_t T, int q_per_seq, int H, int Hkv,
+                     const uint8_t* k_pages, const uint8_t* v_pages, int64_t page_stride,
+                     int64_t head_stride, int64_t num_pages, const uint8_t* k_scales,
+                     const uint8_t* v_scales, const int32_t* block_table, int64_t B,
+                     int64_t bt_width, const int32_t* seq_lens, const int32_t* block_idx, int kb,
+                     float scale, uint16_t* out, float* lse, size_t need, void* ws, size_t ws_bytes,
+                     void* stream) {
+  if (T != B * q_per_seq)
+    return fail(MX4_ERR_INVALID, "%s: T = %lld != B * q_per_seq", name, (long long)T);
+  if (!finite(scale)) return fail(MX4_ERR_INVALID, "%s: scale is not finite", name);
+  if (ws_bytes < need)
+    return fail(MX4_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", name, ws_bytes, need);
+  if (B == 0) return ok();
+  if (!q || !block_table || !seq_lens || !out)
+    return fail(MX4_ERR_INVALID, "%s: NULL pointer", name);
+  if (int rc = check_fp8_pools(name, k_pages, v_pages, page_stride, head_stride, Hkv, num_pages,
+                               k_scales, v_scales))
+    return rc;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(seq_lens, 4) ||
+      !aligned(block_table, 4) || !aligned(block_idx, 4))
+    return fail(MX4_ERR_INVALID, "%s: misaligned buffer", name);
+  if (!ws || !aligned(ws, 16))
+    return fail(MX4_ERR_INVALID, "%s: workspace NULL or not 16-byte aligned", name);
+  if (bt_width < 1 || bt_width > (1 << 20))
+    return fail(MX4_ERR_UNSUPPORTED, "%s: bt_width = %lld (1..2^20)", name, (long long)bt_width);
+  DeviceInfo* d;
+  if (int rc = device_info(&d)) return rc;
+  return cuda_result(
+      mx4::launch_fp8_decode(q, B, q_per_seq, H, Hkv, k_pages, v_pages, k_scales, v_scales,
+                             page_stride, head_stride, num_pages, block_table, bt_width, seq_lens,
+                             block_idx, kb, scale, out, lse, ws, d->status, d->num_sms,
+                             static_cast<cudaStream_t>(stream)),
+      name);
+}
+
+}  // namespace
+
+extern "C" size_t fp8_paged_decode_workspace(int64_t T, int q_per_seq, int H, int Hkv) {
+  if (T < 1 || q_per_seq < 1 || q_per_seq > 8 || Hkv < 1 || H < Hkv || H % Hkv) return 0;
+  return mx4::fp8_decode_workspace_bytes(q_per_seq * (H / Hkv), current_sms());
+}
+
+extern "C" size_t fp8_block_decode_workspace(int64_t T, int kb, int H, int Hkv) {
+  if (T < 1 || kb < 1 || Hkv < 1 || H < Hkv || H % Hkv) return 0;
+  return mx4::fp8_decode_workspace_bytes(H / Hkv, current_sms());
+}
+
+extern "C" int fp8_paged_decode(const uint16_t* q, int64_t T, int q_per_seq, int H, int Hkv,
+                                const uint8_t* k_pages, const uint8_t* v_pages,
+                                int64_t kv_page_stride, int64_t kv_head_stride, int64_t num_pages,
+                                const uint8_t* k_scales, const uint8_t* v_scales,
+                                const int32_t* block_table, int64_t B, int64_t bt_width,
+                                const int32_t* seq_lens, float scale, uint16_t* out, float* lse,
+                                void* ws, size_t ws_bytes, void* stream) {
+  static const char* kName = "fp8_paged_decode";
+  if (int rc = check_fp8_sizes(kName, q_per_seq, H, Hkv, B)) return rc;
+  return fp8_decode_entry(kName, q, T, q_per_seq, H, Hkv, k_pages, v_pages, kv_page_stride,
+                          kv_head_stride, num_pages, k_scales, v_scales, block_table, B, bt_width,
+                          seq_lens, nullptr, 0, scale, out, lse,
+                          fp8_paged_decode_workspace(T, q_per_seq, H, Hkv), ws, ws_bytes, stream);
+}
+
+extern "C" int fp8_block_decode(const uint16_t* q, int64_t T, int q_per_seq, int H, int Hkv,
+                                const uint8_t* k_pages, const uint8_t* v_pages,
+                                int64_t kv_page_stride, int64_t kv_head_stride, int64_t num_pages,
+                                const uint8_t* k_scales, const uint8_t* v_scales,
+                                const int32_t* block_table, int64_t B, int64_t bt_width,
+                                const int32_t* seq_lens, const int32_t* block_idx, int kb,
+                                float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                                void* stream) {
+  static const char* kName = "fp8_block_decode";
+  if (int rc = check_fp8_sizes(kName, q_per_seq, H, Hkv, B)) return rc;
+  if (kb < 1 || kb > 4096)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: kb = %d (supported 1..4096)", kName, kb);
+  if (B > 0 && !block_idx) return fail(MX4_ERR_INVALID, "%s: NULL pointer", kName);
+  return fp8_decode_entry(kName, q, T, q_per_seq, H, Hkv, k_pages, v_pages, kv_page_stride,
+                          kv_head_stride, num_pages, k_scales, v_scales, block_table, B, bt_width,
+                          seq_lens, block_idx, kb, scale, out, lse,
+                          fp8_block_decode_workspace(T, kb, H, Hkv), ws, ws_bytes, stream);
+}
+
+extern "C" int fp8_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, int fp32, int64_t T, int H, int Hkv,
+                               const int32_t* cu_new, int64_t B, const int64_t* positions,
+                               const int64_t* phases, int rot, int interleaved, float factor,
+                               const int32_t* block_table, int64_t bt_width,
+                               const int32_t* seq_lens, uint8_t* k_pages, uint8_t* v_pages,
+                               int64_t kv_page_stride, int64_t kv_head_stride, int64_t num_pages,
+                               uint8_t* k_scales, uint8_t* v_scales, uint16_t* q_out,
+                               void* stream) {
+  static const char* kName = "fp8_rope_append";
+  if (Hkv < 1 || Hkv > 8 || (q && (H < 1 || H > 128)))
+    return fail(MX4_ERR_UNSUPPORTED, "%s: H = %d, Hkv = %d (1..128, 1..8)", kName, H, Hkv);
+  if (T < 0 || T > (1 << 24) || B < 0 || B > (1 << 24))
+    return fail(MX4_ERR_UNSUPPORTED, "%s: T = %lld, B = %lld (at most 2^24)", kName, (long long)T,
+                (long long)B);
+  if (rot < 0 || rot > 128 || rot % 8)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: rot = %d (a multiple of 8 up to 128)", kName, rot);
+  if (!finite(factor)) return fail(MX4_ERR_INVALID, "%s: factor is not finite", kName);
+  if (T == 0 || B == 0) return ok();
+  if (!k || !v || !cu_new || !block_table || !seq_lens || (rot > 0 && !phases))
+    return fail(MX4_ERR_INVALID, "%s: NULL pointer", kName);
+  if (!q != !q_out) return fail(MX4_ERR_INVALID, "%s: q and q_out go together", kName);
+  const size_t e = fp32 ? 4 : 2;
+  if (!aligned(q, 4 * e) || !aligned(k, 4 * e) || !aligned(v, 4 * e) || (q && q_stride % 4) ||
+      k_stride % 4 || v_stride % 4 || !aligned(q_out, 8) || !aligned(phases, 8) ||
+      !aligned(positions, 8))
+    return fail(MX4_ERR_INVALID, "%s: misaligned array or a token stride not of 4 elements", kName);
+  if (T > 1 && ((q && q_stride < (int64_t)H * 128) || k_stride < (int64_t)Hkv * 128 ||
+                v_stride < (int64_t)Hkv * 128))
+    return fail(MX4_ERR_INVALID, "%s: a token stride below its heads", kName);
+  if (int rc = check_fp8_pools(kName, k_pages, v_pages, kv_page_stride, kv_head_stride, Hkv,
+                               num_pages, k_scales, v_scales))
+    return rc;
+  if (bt_width < 1) return fail(MX4_ERR_INVALID, "%s: bt_width < 1", kName);
+  const int64_t strides[3] = {q_stride, k_stride, v_stride};
+  DeviceInfo* d;
+  if (int rc = device_info(&d)) return rc;
+  return cuda_result(
+      mx4::launch_fp8_append(q, k, v, fp32 ? 1 : 0, strides, T, H, Hkv, cu_new, B, positions,
+                             phases, rot, interleaved ? 1 : 0, factor, block_table, bt_width,
+                             seq_lens, k_pages, v_pages, kv_page_stride, kv_head_stride, num_pages,
+                             k_scales, v_scales, q_out, d->status,
+                             static_cast<cudaStream_t>(stream)),
+      kName);
+}
+
+extern "C" int index_block_score(const uint16_t* iq, int64_t T, int q_per_seq,
+                                 const uint8_t* idx_pages, int64_t idx_page_stride,
+                                 int64_t num_pages, const int32_t* block_table, int64_t B,
+                                 int64_t bt_width, const int32_t* seq_lens, float* scores,
+                                 int64_t ld_scores, void* stream) {
+  return score_entry("index_block_score", mx4::launch_index_block_score, iq, T, q_per_seq,
+                     idx_pages, idx_page_stride, num_pages, block_table, B, bt_width, seq_lens,
+                     scores, ld_scores, stream);
+}
+
+extern "C" int index_block_score_fp8(const uint16_t* iq, int64_t T, int q_per_seq,
+                                     const uint8_t* pages, int64_t page_stride, int64_t num_pages,
+                                     const int32_t* block_table, int64_t B, int64_t bt_width,
+                                     const int32_t* seq_lens, float scale, float* scores,
+                                     int64_t ld_scores, void* stream) {
+  return fp8_score_entry("index_block_score_fp8", mx4::launch_index_block_score_fp8, iq, T,
+                         q_per_seq, pages, page_stride, num_pages, block_table, B, bt_width,
+                         seq_lens, scale, scores, ld_scores, stream);
+}
+
+extern "C" int block_topk(const float* scores, int64_t ld_scores, const int32_t* seq_lens,
+                          int64_t B, int q_per_seq, int k, int first, int last,
+                          int32_t* block_idx, void* stream) {
+  static const char* kName = "block_topk";
+  if (q_per_seq < 1 || q_per_seq > 8)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: q_per_seq = %d (supported 1..8)", kName, q_per_seq);
+  if (k < 1 || k > 4096) return fail(MX4_ERR_UNSUPPORTED, "%s: k = %d (supported 1..4096)", kName, k);
+  if (first < 0 || last < 0 || first > k || last > k || first + last > k)
+    return fail(MX4_ERR_INVALID, "%s: first = %d, last = %d of k = %d", kName, first, last, k);
+  if (B < 0 || B > 65535) return fail(MX4_ERR_UNSUPPORTED, "%s: B = %lld", kName, (long long)B);
+  if (ld_scores < 1 || ld_scores > 65536)
+    return fail(MX4_ERR_UNSUPPORTED, "%s: ld_scores = %lld (1..65536)", kName,
+                (long long)ld_scores);
+  if (B == 0) return ok();
+  if (!scores || !seq_lens || !block_idx) return fail(MX4_ERR_INVALID, "%s: NULL pointer", kName);
+  if (!aligned(scores, 4) || !aligned(seq_lens, 4) || !aligned(block_idx, 4))
+    return fail(MX4_ERR_INVALID, "%s: misaligned buffer", kName);
+  DeviceInfo* d;
+  if (int rc = device_info(&d)) return rc;
+  return cuda_result(mx4::launch_block_topk(scores, ld_scores, seq_lens, B * q_per_seq, q_per_seq,
+                                            k, first, last, block_idx, d->status,
+                                            static_cast<cudaStream_t>(stream)),
                      kName);
 }

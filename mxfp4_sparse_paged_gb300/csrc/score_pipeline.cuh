@@ -18,6 +18,10 @@
 // mbarrier.  Every wait is bounded: on time-out the kernel sets
 // MX4_STATUS_TIMEOUT, stops, and drains the copies in flight before exiting.
 //
+// In block mode (Blocks) the scores stay in the kernel: a page's largest score for each query goes
+// out, scores[t][page], by an order-preserving integer maximum over lanes (one instruction), then
+// over the warps of the page in shared memory; the warp that comes last writes.
+//
 // A format whose tile math takes a whole page at once (kWholePage: the
 // block-scaled tensor-core scorer) gets a region of kExtraBytes of shared memory
 // for its operand tiles and runs its own producer and consumer loops over the
@@ -43,6 +47,11 @@ __device__ __forceinline__ uint32_t score_key(float f) {
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+constexpr uint32_t kNanKey = 0xFFC00000u;  // above +inf: a NaN score makes a block's score NaN
+
 struct ScoreArgs {
   const uint16_t* iq;          // bf16 [B * Q, 128]
   const uint8_t* pages;        // page p at pages + p * page_stride
@@ -61,7 +70,7 @@ struct ScoreArgs {
 
 // Shared-memory layout of the kernel, in bytes: format region | stages |
 // barriers | stage info | warp sums, flags | per-sequence page prefix [B].
-template <class F, int Q>
+template <class F, int Q, bool Blocks = false>
 struct ScoreLayout {
   static constexpr int kStageBytes =
       (F::kStageDataBytes + Q * kHeadDim * 2 + F::kStageAlign - 1) / F::kStageAlign * F::kStageAlign;
@@ -73,7 +82,8 @@ struct ScoreLayout {
   static constexpr int kInfoOff = kBarOff + 2 * F::kStages * 8;
   static constexpr int kWarpSumOff = kInfoOff + 4 * F::kStages * 4;
   static constexpr int kFlagOff = kWarpSumOff + 32 * 4;  // abort, issued
-  static constexpr int kPrefOff = (kFlagOff + 8 + 15) / 16 * 16;
+  static constexpr int kKeyOff = (kFlagOff + 8 + 15) / 16 * 16;  // block mode: [S] keys of Q, count
+  static constexpr int kPrefOff = kKeyOff + (Blocks ? (F::kStages * (Q + 1) * 4 + 15) / 16 * 16 : 0);
   // (plus the slack that aligns the dynamic shared memory to a stage alignment above 128)
   static size_t bytes(int B) {
     return (size_t)kPrefOff + (size_t)B * 4 + (F::kStageAlign > 128 ? F::kStageAlign : 0);
@@ -122,10 +132,10 @@ __device__ __forceinline__ PageRef resolve_page(const ScoreArgs& a, const int* p
   return r;
 }
 
-template <class F, int Q>
+template <class F, int Q, bool Blocks = false>
 __global__ void __launch_bounds__((F::kConsumers + 1) * 32, F::ctas_per_sm(Q))
 score_kernel(const __grid_constant__ ScoreArgs a) {
-  using Lay = ScoreLayout<F, Q>;
+  using Lay = ScoreLayout<F, Q, Blocks>;
   constexpr int S = F::kStages, NC = F::kConsumers, NTHR = (NC + 1) * 32;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   uint8_t* const smem_raw =
@@ -149,13 +159,17 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
   pdl_launch_dependents();
 
   // ---- pages per sequence and their prefix sum (contiguous segment per thread)
+  auto fits = [&](int64_t L) {  // (block mode: a sequence shorter than its queries has empty ones)
+    return L >= (Blocks ? 0 : Q) && L <= a.bt_width * kPageTokens &&
+           (Blocks ? (L + kPageTokens - 1) / kPageTokens : L) <= a.ld;
+  };
   {
     const int per = (B + NTHR - 1) / NTHR;
     const int s0 = min(B, tid * per), s1 = min(B, s0 + per);
     int sum = 0;
     for (int sq = s0; sq < s1; ++sq) {
       const int64_t L = a.seq_lens[sq];
-      const bool ok = L >= Q && L <= a.bt_width * kPageTokens && L <= a.ld;
+      const bool ok = fits(L);
       if (!ok && blockIdx.x == 0) flag(a.status, MX4_STATUS_BAD_LEN);
       sum += ok ? (int)((L + kPageTokens - 1) / kPageTokens) : 0;
     }
@@ -171,7 +185,7 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
     for (int sq = s0; sq < s1; ++sq) {
       const int64_t L = a.seq_lens[sq];
-      const bool ok = L >= Q && L <= a.bt_width * kPageTokens && L <= a.ld;
+      const bool ok = fits(L);
       before += ok ? (int)((L + kPageTokens - 1) / kPageTokens) : 0;
       pref[sq] = before;
     }
@@ -185,6 +199,9 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
     *issued = 0;
     fence_barrier_init();
   }
+  uint32_t* const keys = reinterpret_cast<uint32_t*>(smem_raw + Lay::kKeyOff);
+  if constexpr (Blocks)
+    for (int i = tid; i < S * (Q + 1); i += NTHR) keys[i] = 0u;
   __syncthreads();
 
   const int total = B > 0 ? pref[B - 1] : 0;
@@ -281,8 +298,16 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
         float* const base = a.scores + (int64_t)seq * Q * a.ld + (int64_t)pg * kPageTokens;
         const int nrows = min(kPageTokens, L - pg * kPageTokens);
         const int last0 = L - Q - pg * kPageTokens;  // query 0's last finite row
+        uint32_t best[Q];
+#pragma unroll
+        for (int qq = 0; qq < Q; ++qq) best[qq] = 0u;
         auto emit = [&](int qq, int r, float v) {
-          if constexpr (Q >= 3) {
+          if constexpr (Blocks) {
+            const uint32_t key = v != v ? kNanKey : score_key(v);
+#pragma unroll
+            for (int q2 = 0; q2 < Q; ++q2)  // (no lane-dependent index)
+              if (q2 == qq && r <= last0 + q2) best[q2] = max(best[q2], key);
+          } else if constexpr (Q >= 3) {
             if (r < nrows) base[qq * a.ld + r] = (r <= last0 + qq) ? v : -INFINITY;
           } else {
             const int64_t i_g = (int64_t)pg * kPageTokens + r;
@@ -294,6 +319,30 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
 #pragma unroll
         for (int tt = 0; tt < kPageTokens / 16 / NC; ++tt)
           tile.run(page, (warp + NC * tt) * 16, lane, emit);
+        if constexpr (Blocks) {
+          uint32_t* const k = keys + st * (Q + 1);
+          uint32_t mine = 0u;
+#pragma unroll
+          for (int qq = 0; qq < Q; ++qq) {
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best[qq]);
+            if (lane == qq) mine = top;
+          }
+          if (lane < Q) atomicMax(&k[lane], mine);
+          __threadfence_block();
+          __syncwarp();
+          uint32_t before = 0u;
+          if (lane == 0) before = atomicAdd(&k[Q], 1u);
+          if (__shfl_sync(0xFFFFFFFFu, before, 0) == NC - 1) {  // the page's last warp
+            __threadfence_block();
+            if (lane < Q) {
+              const uint32_t top = atomicExch(&k[lane], 0u);  // 0: the query sees nothing here
+              a.scores[((int64_t)seq * Q + lane) * a.ld + pg] = top ? key_score(top) : -INFINITY;
+            }
+            if (lane == 0) k[Q] = 0u;
+          }
+        }
+      } else if (Blocks && warp == 0 && lane < Q) {  // no page: no score
+        a.scores[((int64_t)seq * Q + lane) * a.ld + pg] = -INFINITY;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&empty[st]));
@@ -332,10 +381,10 @@ inline cudaError_t resident_ctas(const void* kern, int threads, size_t smem, int
 }
 
 // Launch over batches of at most kScoreMaxBatch sequences (the prefix array).
-template <class F, int Q>
+template <class F, int Q, bool Blocks = false>
 cudaError_t launch_score(ScoreArgs a, int num_sms, cudaStream_t stream) {
-  using Lay = ScoreLayout<F, Q>;
-  auto kern = score_kernel<F, Q>;
+  using Lay = ScoreLayout<F, Q, Blocks>;
+  auto kern = score_kernel<F, Q, Blocks>;
   const int B = a.B;
   const size_t smem = Lay::bytes(min(B, kScoreMaxBatch));
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -366,6 +415,21 @@ cudaError_t launch_score(ScoreArgs a, int num_sms, cudaStream_t stream) {
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
+}
+
+template <class F, bool Blocks>
+cudaError_t launch_score_q(int q, const ScoreArgs& a, int num_sms, cudaStream_t stream) {
+  switch (q) {
+    case 1: return launch_score<F, 1, Blocks>(a, num_sms, stream);
+    case 2: return launch_score<F, 2, Blocks>(a, num_sms, stream);
+    case 3: return launch_score<F, 3, Blocks>(a, num_sms, stream);
+    case 4: return launch_score<F, 4, Blocks>(a, num_sms, stream);
+    case 5: return launch_score<F, 5, Blocks>(a, num_sms, stream);
+    case 6: return launch_score<F, 6, Blocks>(a, num_sms, stream);
+    case 7: return launch_score<F, 7, Blocks>(a, num_sms, stream);
+    case 8: return launch_score<F, 8, Blocks>(a, num_sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace mx4

@@ -1,0 +1,105 @@
+"""A decode step over the 8-bit K/V cache: append, choice of blocks, attention.
+
+`Fp8Caches` holds the pools: E4M3 K and V pages with a scale for every 32 tokens and head, and the
+fp8 index pages that share their page ids ("vllm.models.minimax_m3.amd.mono.dispatch",
+_config_refusal: fp8 K/V and index caches; _slots_shared).  `Fp8Step` holds the buffers of steps in
+which every sequence brings q tokens: their K heads turn by their positions and are appended with V
+(fp8_rope_append) and the index keys (fp8_index_insert); index scores choose blocks of 128 tokens
+for each of them (index_block_score_fp8, block_topk), and attention reads those (fp8_block_decode),
+or everything (fp8_paged_decode).  All on the current stream; lengths stay on the device, so a step
+can be captured into a CUDA graph.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import (FP8_PAGE_BYTES, HEAD_DIM, PAGE_TOKENS, block_topk, fp8_block_decode,
+               fp8_block_decode_workspace, fp8_index_insert, fp8_paged_decode,
+               fp8_paged_decode_workspace, fp8_rope_append, index_block_score_fp8)
+
+
+class Fp8Caches:
+    """Resident pools, poisoned (0xFF: NaN) until written."""
+
+    def __init__(self, num_pages: int, kv_heads: int = 1, index_scale: float = 1.0, device="cuda"):
+        self.num_pages, self.index_scale = num_pages, index_scale
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.k_pages = torch.full((num_pages, kv_heads, FP8_PAGE_BYTES), 0xFF, **u8)
+        self.v_pages = torch.full_like(self.k_pages, 0xFF)
+        self.k_scales = torch.full((num_pages, kv_heads, 4), 0xFF, **u8)
+        self.v_scales = torch.full_like(self.k_scales, 0xFF)
+        self.idx_pages = torch.full((num_pages, FP8_PAGE_BYTES), 0xFF, **u8)
+
+    def kv(self):
+        return self.k_pages, self.v_pages, self.k_scales, self.v_scales
+
+
+class Fp8Step:
+    """Buffers and calls of decode steps of `block_table`'s sequences, q_per_seq tokens each.
+
+    seq_lens (int32 [B], device): tokens cached so far.  blocks: how many blocks a token reads, the
+    first `first` and last `last` in any case (0: all tokens).  phases (int64, rope_phases): how the
+    heads turn, None: not at all."""
+
+    def __init__(self, caches: Fp8Caches, block_table, seq_lens, q_per_seq: int = 1, heads: int = 16,
+                 blocks: int = 16, first: int = 1, last: int = 2, phases=None, interleaved=False,
+                 factor: float = 1.0, scale: float = 1.0 / math.sqrt(HEAD_DIM)):
+        dev, (B, W) = block_table.device, block_table.shape
+        self.caches, self.block_table, self.q, self.scale = caches, block_table, q_per_seq, scale
+        self.blocks, self.first, self.last = blocks, first, last
+        self.phases, self.interleaved, self.factor = phases, interleaved, factor
+        self.seq_lens = seq_lens.clone()
+        T, Hkv = B * q_per_seq, caches.k_pages.shape[1]
+        self.cu_step = torch.arange(0, T + 1, q_per_seq, dtype=torch.int32, device=dev)
+        self.q_out = torch.empty((T, heads, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty_like(self.q_out)
+        self.lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
+        need = fp8_paged_decode_workspace(T, q_per_seq, heads, Hkv)
+        if blocks:
+            self.scores = torch.empty((T, W), dtype=torch.float32, device=dev)
+            self.block_idx = torch.empty((T, blocks), dtype=torch.int32, device=dev)
+            need = fp8_block_decode_workspace(T, blocks, heads, Hkv)
+        self.ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+
+    def slots(self, cu_new, T: int) -> torch.Tensor:
+        """int64 [T] page-128 slots of the rows that cu_new gives the sequences' last positions, -1
+        for rows of none.  A row past the table, or where that has no page, gets a slot past the
+        pool, which the insert reports (bad-slot)."""
+        (B, W), dev = self.block_table.shape, self.block_table.device
+        t = torch.arange(T, device=dev, dtype=cu_new.dtype)
+        s = torch.searchsorted(cu_new, t, right=True).sub_(1)
+        live = (s >= 0) & (s < B)
+        s = s.clamp_(0, B - 1)
+        pos = self.seq_lens[s].long() - cu_new[s + 1] + t
+        page = self.block_table[s, (pos // PAGE_TOKENS).clamp(0, W - 1)].long()
+        there = (pos >= 0) & (pos < W * PAGE_TOKENS) & (page >= 0)
+        page = torch.where(there, page, self.caches.num_pages)
+        return torch.where(live, page * PAGE_TOKENS + pos % PAGE_TOKENS, -1)
+
+    def append(self, k, v, idx_k, cu_new, new, q=None, q_out=None, positions=None):
+        """`new` (int32 [B]) more tokens a sequence, the rows of k, v [T, Hkv, 128] and idx_k fp32
+        [T, 128] that cu_new (int32 [B + 1]) gives it; q [T, H, 128] turned into q_out."""
+        c = self.caches
+        self.seq_lens.add_(new)
+        fp8_rope_append(q, k, v, cu_new, self.block_table, self.seq_lens, *c.kv(), q_out,
+                        phases=self.phases, positions=positions, interleaved=self.interleaved,
+                        factor=self.factor)
+        fp8_index_insert(idx_k, self.slots(cu_new, k.shape[0]), c.index_scale, c.idx_pages)
+
+    def run(self, q, k, v, iq, idx_k, positions=None):
+        """One step: q [T, H, 128], k, v [T, Hkv, 128] (fp32 or bf16, before the turn), iq bf16 and
+        idx_k fp32 [T, 128].  Returns out, bf16 [T, H, 128]."""
+        c, cached = self.caches, (self.block_table, self.seq_lens)
+        self.append(k, v, idx_k, self.cu_step, self.q, q, self.q_out, positions)
+        if not self.blocks:
+            fp8_paged_decode(self.q_out, self.q, *c.kv(), *cached, self.scale, self.out, self.ws,
+                             lse=self.lse)
+            return self.out
+        index_block_score_fp8(iq, self.q, c.idx_pages, *cached, c.index_scale, self.scores)
+        block_topk(self.scores, self.seq_lens, self.q, self.block_idx, first=self.first,
+                   last=self.last)
+        fp8_block_decode(self.q_out, self.q, *c.kv(), *cached, self.block_idx, self.scale, self.out,
+                         self.ws, lse=self.lse)
+        return self.out
