@@ -22,13 +22,15 @@
 //   p = 2^(S f - m + 8), f = scale log2(e) 2^Ek.  m moves only where a row's largest logit lies
 //     2^7 above it, so a unit costs one vote and no reduction.  z sums p in fp32; P is f16 (11
 //     bits: 2^-12 of a weight; weights down to 2^-22 of the largest keep all of them).
-//   O += 2^Ev (P V): the accumulator fragment of S is the operand of the second product; a pair of
-//     tokens' bytes is put side by side by byte permutes and widened to f16x2, exact.  The product
-//     of 32 tokens is scaled in fp32, so scales of any two blocks may be any powers apart.
+//   O += P V: the accumulator fragment of S is the operand of the second product; a pair of tokens'
+//     bytes is put side by side by byte permutes and widened to f16x2, exact.  O is kept in units of
+//     2^Er, the largest 2^Ev met: 2^(Ev - Er) goes into the exponent of p (and out of z).  Units with
+//     Ev more than 6 below Er take the second form below, which scales their product in fp32, so
+//     scales of any two blocks may be any powers apart.
 // The tensor memory path (tcgen05) has no use here at 16 rows: it computes 128-row tiles from shared
 // memory, and would put scores and weights through tensor and shared memory on the way.
 //
-// Units where some row does not see all 32 tokens (a sequence's end) take a second form of the step:
+// Units where some row does not see all 32 tokens (a sequence's end) take the second form of the step:
 // scores are masked, values that no row sees are zeroed (rows past the length may hold anything), and
 // NaN codes that only some rows see reach those rows alone, by counting them in one more product.
 //
@@ -47,20 +49,46 @@ namespace mx4 {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 24;                      // of all groups of a CTA
+// Warps of a CTA by the warps of a group.  One: HBM is the limit, and stages of the ring count for
+// more than warps (256 ragged contexts: 163 us; 12 warps of two stages each 180).  Two and four:
+// three warps a scheduler hide the chain of a unit's products, exponentials and conversions; their
+// 168 registers leave no room for q, which they read from shared memory.
+constexpr int warps_of(int M) { return M == 1 || M == 8 ? 8 : 12; }
+constexpr bool q_shared(int M) { return M == 2 || M == 4; }
+constexpr int stages_of(int M) { return q_shared(M) ? 18 : 24; }  // of all groups of a CTA
+constexpr int kMaxWarps = 12;
 constexpr int kStepBytes = 2 * kSub * kFp8Row;   // K rows, V rows of a unit
 constexpr int kMaxOwners = 2048;                 // sequences of a launch (their prefix sums)
-constexpr int kRecRow = kHeadDim + 4;            // floats of a row in shared memory: O, m, z
+constexpr int kRecRow = kHeadDim + 4;            // floats of a row in shared memory: O, m, z, Er
+constexpr int kFold = 6;                         // V scales this far below Er go into the weights
+constexpr int kNoScale = -1000;                  // Er before the first unit
 constexpr float kUp = 8.f;                       // weights are 2^kUp at the reference
 constexpr int64_t kMinUnits = 8;                 // of a CTA: one for each group of one warp
 
-constexpr int kBarOff = kStages * kStepBytes;
-constexpr int kSumOff = kBarOff + 2 * kStages * 8;
-constexpr int kSegOff = kSumOff + kWarps * 8;    // [group]: last tile, the end of its units, first tile
-constexpr int kPrefOff = kSegOff + kWarps * 24;
-constexpr int kSmemBytes = kPrefOff + kMaxOwners * 8 + 1024;  // 1024: the stages' alignment
+// Shared memory, in bytes: stages | q fragments | barriers | sums | seg | jobs | units | prefix sums.
+template <int M>
+struct Layout {
+  static constexpr int kQOff = stages_of(M) * kStepBytes;  // [warp][8][32 lanes] of 16 bytes
+  static constexpr int kBarOff = kQOff + (q_shared(M) ? warps_of(M) * 4096 : 0);
+  static constexpr int kSumOff = kBarOff + 2 * stages_of(M) * 8;
+  static constexpr int kSegOff = kSumOff + kMaxWarps * 8;   // [group]: last tile, first tile if it began before
+  static constexpr int kJobOff = kSegOff + kMaxWarps * 8;   // tiles whose pieces are joined
+  static constexpr int kUnitOff = kJobOff + (kMaxWarps + 2) * 16;  // [warp][64]: units looked up ahead
+  static constexpr int kPrefOff = kUnitOff + kMaxWarps * 64 * 16;
+  static constexpr int kBytes = kPrefOff + kMaxOwners * 8 + 1024;  // 1024: the stages' alignment
+  static_assert(kUnitOff % 16 == 0 && kJobOff % 16 == 0 && kBytes <= 232448, "shared memory");
+};
+
+// Division of numbers below 2^31 by d >= 1: (mulhi(x, mul) + x) >> shift.
+struct Div {
+  uint32_t mul, shift, d;
+  explicit Div(uint32_t v = 1) : d(v) {
+    shift = 0;
+    while ((1ull << shift) < v) ++shift;
+    mul = (uint32_t)((((1ull << shift) - v) << 32) / v + 1);
+  }
+  __device__ __forceinline__ int operator()(uint32_t x) const { return (int)((__umulhi(x, mul) + x) >> shift); }
+};
 
 struct DecodeArgs {
   CUtensorMap kmap, vmap;
@@ -75,12 +103,13 @@ struct DecodeArgs {
   int64_t num_pages;
   int B, Q, H, Hkv, G;
   int R, RT;                // rows of an owner and KV head, tiles they take
+  Div by_hr, by_rt, by_g, by_q, by_n;  // tiles of an owner, tiles of a head, G, Q, units of a list
   float scale;
   uint16_t* out;
   float* lse;
-  float* rec;               // pieces: [CTA][0: of a tile begun before, 1: begun here][16 M][128], m z
-  float* scratch;           // [CTA][8 warps][16][128], m z: tiles that a group ended but did not begin
-  int64_t* meta;            // [CTA][3]: the tile that begins here and ends in a later CTA (-1: none), that CTA
+  float* rec;               // pieces: [CTA][0: of a tile begun before, 1: begun here][16 M][128], m z Er
+  float* scratch;           // [CTA][warps][16][128], m z Er: tiles that a group ended but did not begin
+  int32_t* meta;            // [CTA][2]: the tile that begins here and ends in a later CTA (-1: none), that CTA
   uint32_t* status;
 };
 
@@ -133,6 +162,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {  // i known at compile time
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
 __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, int row, int head,
                                             int page, uint32_t bar) {
   asm volatile(
@@ -144,10 +177,13 @@ __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map
 
 // A warp's part of a tile: 16 rows, lane (g, c) = (lane / 4, lane % 4) holds rows g and g + 8,
 // dims 32 c .. 32 c + 31 of O (o[j]: dims 32 c + j and 32 c + 16 + j of row g, then of row g + 8).
+template <bool QS>
 struct Rows {
-  uint32_t qa[8][4];
+  uint32_t qa[QS ? 1 : 8][4];
+  uint32_t qs;                    // QS: where the lane's fragments are, 512 bytes apart
   float o[16][4];
-  float m[2], nb[2], z[2], f[2];  // reference, 8 - reference, sum, logit factor without 2^Ek
+  float m[2], nb[2], z[2], f[2];  // reference, kUp - reference, sum, logit factor without 2^Ek
+  int er;                         // O is in units of 2^er
   int lim[2];                     // last visible token of rows g, g + 8
   int min_lim, max_lim;           // over the warp's rows
 
@@ -160,64 +196,81 @@ struct Rows {
       nb[h] = 0.f;
       z[h] = 0.f;
     }
+    er = kNoScale;
   }
 
   // q rows -> f16 fragments, scaled so that a row's largest element lies in [2^14, 2^15) (exact, but
-  // for elements 2^-29 of it; rows whose largest is below 2^-86 lose bits).
-  __device__ __forceinline__ void load_q(const uint16_t* p, bool real, int h, float scale, int lane) {
-    const int c = lane & 3;
-    uint4 v[4];
+  // for elements 2^-29 of it; rows whose largest is below 2^-86 lose bits).  v: the lane's 32 dims.
+  __device__ __forceinline__ void set_q(const uint4 (&v)[2][4], float scale) {
+    float up[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = real ? *reinterpret_cast<const uint4*>(p + 32 * c + 8 * i) : make_uint4(0, 0, 0, 0);
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
-    uint32_t am = 0;
+    for (int h = 0; h < 2; ++h) {
+      uint32_t am = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      am = max(am, max((w[i] << 17) >> 1, w[i] & 0x7FFF0000u));
-    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-    const int sigma = am == 0u ? 0 : min(100, max(-113, 14 - ((int)(am >> 23) - 127)));
-    const float up = __uint_as_float((uint32_t)(127 + sigma) << 23) * (scale < 0.f ? -1.f : 1.f);
-    f[h] = fabsf(scale) * 1.44269504f * __uint_as_float((uint32_t)(127 - sigma) << 23);
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t w = word(v[h][i >> 2], i & 3);
+        am = max(am, max((w << 17) >> 1, w & 0x7FFF0000u));
+      }
+      am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+      am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+      const int sigma = am == 0u ? 0 : min(100, max(-113, 14 - ((int)(am >> 23) - 127)));
+      up[h] = __uint_as_float((uint32_t)(127 + sigma) << 23) * (scale < 0.f ? -1.f : 1.f);
+      f[h] = fabsf(scale) * 1.44269504f * __uint_as_float((uint32_t)(127 - sigma) << 23);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      qa[j][h] = half2_bits(bf16_bits_to_float(w[2 * j] & 0xFFFFu) * up,
-                            bf16_bits_to_float(w[2 * j] >> 16) * up);
-      qa[j][h + 2] = half2_bits(bf16_bits_to_float(w[2 * j + 1] & 0xFFFFu) * up,
-                                bf16_bits_to_float(w[2 * j + 1] >> 16) * up);
+      uint32_t a[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = word(v[i & 1][j >> 1], (2 * j + (i >> 1)) & 3);
+        a[i] = half2_bits(bf16_bits_to_float(w & 0xFFFFu) * up[i & 1], bf16_bits_to_float(w >> 16) * up[i & 1]);
+      }
+      if (QS)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + j * 512), "r"(a[0]), "r"(a[1]),
+                     "r"(a[2]), "r"(a[3])
+                     : "memory");
+      else
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qa[QS ? 0 : j][i] = a[i];
     }
   }
 
-  // One unit: 32 tokens from position tb on, K rows at ka and V rows at va (shared memory), Ek and
-  // Ev as powers of two.  Tail: some row does not see all of them.
-  template <bool Tail>
-  __device__ __forceinline__ void step(uint32_t ka, uint32_t va, float ek, float ev, int tb, int lane) {
+  // One unit: 32 tokens from position tb on, K rows at ka and V rows at va (shared memory), scale
+  // bytes kb and vb.  General: some row does not see all of them, or Ev is far below er, or NaN.
+  template <bool General>
+  __device__ __forceinline__ void step(uint32_t ka, uint32_t va, int kb, int vb, int tb, int lane) {
     const int g = lane >> 2, c = lane & 3;
     float s[4][4];
-    {
-      uint4 x[4][2];
-      const uint32_t at = ka + g * kFp8Row;
+    constexpr int kN = QS ? 4 : 2;  // groups of eight tokens at a time
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        x[n][0] = lds128(at + n * 8 * kFp8Row + (((2 * c) ^ g) << 4));
-        x[n][1] = lds128(at + n * 8 * kFp8Row + (((2 * c + 1) ^ g) << 4));
+    for (int n = 0; n < 4; n += kN) {
+      uint4 x[kN][2];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t at = ka + (8 * (n + i) + g) * kFp8Row;
+        x[i][0] = lds128(at + (((2 * c) ^ g) << 4));
+        x[i][1] = lds128(at + (((2 * c + 1) ^ g) << 4));
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      for (int j = 0; j < 8; ++j) {
+        uint32_t q[4];
+        if (QS) {
+          const uint4 v = lds128(qs + j * 512);
+          q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
+        } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint4 y = x[n][j >> 2];
-          const uint32_t w = (j & 3) == 0 ? y.x : (j & 3) == 1 ? y.y : (j & 3) == 2 ? y.z : y.w;
-          uint32_t b0, b1;
-          e4m3x4_f16x2(w, b0, b1);
-          mma(s[n], qa[j], b0, b1);
+          for (int i = 0; i < 4; ++i) q[i] = qa[QS ? 0 : j][i];
         }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          uint32_t b0, b1;
+          e4m3x4_f16x2(word(x[i][j >> 2], j & 3), b0, b1);
+          if (j == 0) mma0(s[n + i], q, b0, b1); else mma(s[n + i], q, b0, b1);
+        }
+      }
     }
     const int rel0 = lim[0] - tb, rel1 = lim[1] - tb;  // last visible token of the unit
-    if (Tail) {
+    if (General) {
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -227,12 +280,13 @@ struct Rows {
         }
     }
     // factors stay finite (a score of 0 is a logit of 0 whatever the scales) or NaN
+    const float ek = e8m0_to_float(kb);
     float f0 = f[0] * ek, f1 = f[1] * ek;
     f0 = f0 > FLT_MAX ? FLT_MAX : f0;
     f1 = f1 > FLT_MAX ? FLT_MAX : f1;
-    float mx0 = s[0][0], mx1 = s[0][2];
+    float mx0 = fmaxf(s[0][0], s[0][1]), mx1 = fmaxf(s[0][2], s[0][3]);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 1; n < 4; ++n) {
       mx0 = fmaxf(mx0, fmaxf(s[n][0], s[n][1]));
       mx1 = fmaxf(mx1, fmaxf(s[n][2], s[n][3]));
     }
@@ -257,16 +311,26 @@ struct Rows {
         }
       }
     }
+    if (vb - 127 > er && vb != 255) {  // O to the new unit (nothing is in it before the first)
+      const float down = er == kNoScale ? 0.f : ex2((float)(er - vb + 127));
+      er = vb - 127;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] *= down;
+    }
+    const float fold = General ? 0.f : (float)(vb - 127 - er);
     uint32_t pa[2][4];
     {
+      const float n0 = nb[0] + fold, n1 = nb[1] + fold;
       float p[4][4], z0 = 0.f, z1 = 0.f;
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          p[n][e] = ex2(fmaf(s[n][e], f0, nb[0]));
-          p[n][2 + e] = ex2(fmaf(s[n][2 + e], f1, nb[1]));
-          if (Tail) {  // -inf times a factor of 0 or NaN is not -inf
+          p[n][e] = ex2(fmaf(s[n][e], f0, n0));
+          p[n][2 + e] = ex2(fmaf(s[n][2 + e], f1, n1));
+          if (General) {  // -inf times a factor of 0 or NaN is not -inf
             if (8 * n + 2 * c + e > rel0) p[n][e] = 0.f;
             if (8 * n + 2 * c + e > rel1) p[n][2 + e] = 0.f;
           }
@@ -274,8 +338,9 @@ struct Rows {
         z0 += p[n][0] + p[n][1];
         z1 += p[n][2] + p[n][3];
       }
-      z[0] += z0;
-      z[1] += z1;
+      const float back = General ? 1.f : __int_as_float((127 - (vb - 127 - er)) << 23);
+      z[0] = fmaf(z0, back, z[0]);
+      z[1] = fmaf(z1, back, z[1]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         pa[k][0] = half2_bits(p[2 * k][0], p[2 * k][1]);
@@ -284,84 +349,75 @@ struct Rows {
         pa[k][3] = half2_bits(p[2 * k + 1][2], p[2 * k + 1][3]);
       }
     }
-    uint4 y[2][4];  // tokens 16 k + 2 c + {0, 1, 8, 9}, dims 16 g .. 16 g + 15
+    // a scale of NaN reaches only rows that see its tokens
+    float ev0 = 0.f, ev1 = 0.f;
+    if (General) {
+      const float ev = vb == 255 ? e8m0_to_float(255) : ex2((float)(vb - 127 - er));
+      ev0 = rel0 < 0 ? 0.f : ev;
+      ev1 = rel1 < 0 ? 0.f : ev;
+    }
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
+      uint4 y[4];  // tokens 16 k + 2 c + {0, 1, 8, 9}, dims 16 g .. 16 g + 15
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 16 * k + 2 * c + (i & 1) + 8 * (i >> 1);
-        y[k][i] = lds128(va + r * kFp8Row + ((g ^ (2 * c + (i & 1))) << 4));
-        if (Tail && tb + r > max_lim) y[k][i] = make_uint4(0, 0, 0, 0);
+        y[i] = lds128(va + r * kFp8Row + ((g ^ (2 * c + (i & 1))) << 4));
+        if (General && tb + r > max_lim) y[i] = make_uint4(0, 0, 0, 0);
       }
-    uint32_t seen[2][4];
-    float ev0 = ev, ev1 = ev;
-    if (Tail) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
+      uint32_t seen[4];
+      if (General) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 16 * k + 2 * c + 8 * (i >> 1), rel = (i & 1) ? rel1 : rel0;
-          seen[k][i] = (r <= rel ? 0x3C00u : 0u) | (r + 1 <= rel ? 0x3C000000u : 0u);
+          seen[i] = (r <= rel ? 0x3C00u : 0u) | (r + 1 <= rel ? 0x3C000000u : 0u);
         }
-      if (rel0 < 0) ev0 = 0.f;  // a scale of NaN reaches only rows that see its tokens
-      if (rel1 < 0) ev1 = 0.f;
-    }
+      }
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      uint32_t b[2][4][2];  // [k][dim of the word][token pair]
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int w = 0; w < 4; ++w) {
+        uint32_t b[4][2];  // [dim of the word][token pair]
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint4 ya = y[k][2 * h], yb = y[k][2 * h + 1];
-          const uint32_t wa = w == 0 ? ya.x : w == 1 ? ya.y : w == 2 ? ya.z : ya.w;
-          const uint32_t wb = w == 0 ? yb.x : w == 1 ? yb.y : w == 2 ? yb.z : yb.w;
-          e4m3x4_f16x2(__byte_perm(wa, wb, 0x5140), b[k][0][h], b[k][1][h]);
-          e4m3x4_f16x2(__byte_perm(wa, wb, 0x7362), b[k][2][h], b[k][3][h]);
+          const uint32_t wa = word(y[2 * h], w), wb = word(y[2 * h + 1], w);
+          e4m3x4_f16x2(__byte_perm(wa, wb, 0x5140), b[0][h], b[1][h]);
+          e4m3x4_f16x2(__byte_perm(wa, wb, 0x7362), b[2][h], b[3][h]);
         }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float t[4];
-        if (Tail) {
-          float nan[4];
-          uint32_t ind[2][2];
+        for (int i = 0; i < 4; ++i) {
+          float(&d)[4] = o[4 * w + i];
+          if (!General) {
+            mma(d, pa[k], b[i][0], b[i][1]);
+            continue;
+          }
+          float t[4], nan[4];
+          uint32_t ind[2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int h = 0; h < 2; ++h) {
+            const __half2 v = *reinterpret_cast<const __half2*>(&b[i][h]);
+            const __half2 n = __hisnan2(v);
+            ind[h] = *reinterpret_cast<const uint32_t*>(&n);
+            b[i][h] &= ~(((ind[h] >> 10) & 0x00010001u) * 0xFFFFu);
+          }
+          mma0(nan, seen, ind[0], ind[1]);
+          mma0(t, pa[k], b[i][0], b[i][1]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const __half2 v = *reinterpret_cast<const __half2*>(&b[k][i][h]);
-              const __half2 n = __hisnan2(v);
-              ind[k][h] = *reinterpret_cast<const uint32_t*>(&n);
-              b[k][i][h] &= ~(((ind[k][h] >> 10) & 0x00010001u) * 0xFFFFu);
-            }
-          mma0(nan, seen[0], ind[0][0], ind[0][1]);
-          mma(nan, seen[1], ind[1][0], ind[1][1]);
-          mma0(t, pa[0], b[0][i][0], b[0][i][1]);
-          mma(t, pa[1], b[1][i][0], b[1][i][1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 4; ++e) {
             if (nan[e] > 0.f) t[e] = __uint_as_float(0x7FC00000u);
-        } else {
-          mma0(t, pa[0], b[0][i][0], b[0][i][1]);
-          mma(t, pa[1], b[1][i][0], b[1][i][1]);
+            d[e] = fmaf(e < 2 ? ev0 : ev1, t[e], d[e]);
+          }
         }
-        float(&d)[4] = o[4 * w + i];
-        d[0] = fmaf(ev0, t[0], d[0]);
-        d[1] = fmaf(ev0, t[1], d[1]);
-        d[2] = fmaf(ev1, t[2], d[2]);
-        d[3] = fmaf(ev1, t[3], d[3]);
       }
     }
   }
 
-  // z over the lanes of a row; O, m and z of row g + 8 h at p (128 floats), mz.
-  __device__ __forceinline__ void sum_z() {
+  __device__ __forceinline__ void sum_z() {  // over the lanes of a row
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       z[h] += __shfl_xor_sync(0xFFFFFFFFu, z[h], 1);
       z[h] += __shfl_xor_sync(0xFFFFFFFFu, z[h], 2);
     }
   }
+  // row g + 8 h: O at p, its reference, sum and unit at mz
   __device__ __forceinline__ void put(int h, float* p, float* mz, int lane) const {
     const int c = lane & 3;
 #pragma unroll
@@ -371,14 +427,14 @@ struct Rows {
         *reinterpret_cast<float4*>(p + 32 * c + 16 * e + 4 * i) =
             make_float4(o[4 * i][2 * h + e], o[4 * i + 1][2 * h + e], o[4 * i + 2][2 * h + e],
                         o[4 * i + 3][2 * h + e]);
-    if (c == 0) {
-      mz[0] = m[h];
-      mz[1] = z[h];
-    }
+    if (c == 0) *reinterpret_cast<float4*>(mz) = make_float4(m[h], z[h], (float)er, 0.f);
   }
 };
 
-// A finished row's value and lse from O (units 2^(m - kUp)), m and z.
+// A finished row from O (units 2^(m - kUp + er)), m and z: what O is multiplied by, and the lse.
+__device__ __forceinline__ float row_factor(float z, float er) {
+  return z == 0.f ? 0.f : (er < -127.f ? 0.f : e8m0_to_float((uint32_t)((int)er + 127))) / z;
+}
 __device__ __forceinline__ float row_lse(float m, float z) {
   return z == 0.f ? -INFINITY : (m - kUp + log2f(z)) * 0.69314718f;
 }
@@ -386,12 +442,11 @@ __device__ __forceinline__ float row_lse(float m, float z) {
 struct Tile {
   int owner, head, rt;
 };
-__device__ __forceinline__ Tile tile_of(const DecodeArgs& a, int64_t tile) {
-  const int per = a.Hkv * a.RT;
+__device__ __forceinline__ Tile tile_of(const DecodeArgs& a, int tile) {
   Tile t;
-  t.owner = (int)(tile / per);
-  const int r = (int)(tile - (int64_t)t.owner * per);
-  t.head = r / a.RT;
+  t.owner = a.by_hr(tile);
+  const int r = tile - t.owner * (int)a.by_hr.d;
+  t.head = a.by_rt(r);
   t.rt = r - t.head * a.RT;
   return t;
 }
@@ -399,50 +454,61 @@ __device__ __forceinline__ Tile tile_of(const DecodeArgs& a, int64_t tile) {
 // Row r of a tile's owner: the decode token and query head it is.
 template <bool Lists>
 __device__ __forceinline__ int64_t row_of(const DecodeArgs& a, const Tile& t, int r) {
-  const int j = Lists ? 0 : r / a.G;
+  const int j = Lists ? 0 : a.by_g(r);
   const int64_t tok = Lists ? t.owner : (int64_t)t.owner * a.Q + j;
   return tok * a.H + t.head * a.G + (r - j * a.G);
 }
 
-// A piece of a row onto a sum with the reference ref.
-__device__ __forceinline__ void add_piece(float4& acc, float& z, float4 v, float pm, float pz, float ref) {
-  // (a piece without a reference holds nothing, or NaN)
-  const float f = pm == -INFINITY ? (pz == 0.f ? 0.f : 1.f) : ex2(pm - ref);
-  z = fmaf(f, pz, z);
-  acc.x = fmaf(f, v.x, acc.x);
-  acc.y = fmaf(f, v.y, acc.y);
-  acc.z = fmaf(f, v.z, acc.z);
-  acc.w = fmaf(f, v.w, acc.w);
-}
+// A row's sum of pieces, mz = (m, z, er, -) of each.
+struct Joined {
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float z = 0.f, m = -INFINITY, er = kNoScale;
+  __device__ __forceinline__ void see(float4 mz) {  // all pieces, before the first is added
+    m = fmaxf(m, mz.x);
+    er = fmaxf(er, mz.z);
+  }
+  __device__ __forceinline__ void add(float4 v, float4 mz) {
+    // (a piece without a reference holds nothing, or NaN)
+    const float f = mz.x == -INFINITY ? (mz.y == 0.f ? 0.f : 1.f) : ex2(mz.x - m);
+    const float fo = f * ex2(mz.z - er);
+    z = fmaf(f, mz.y, z);
+    acc.x = fmaf(fo, v.x, acc.x);
+    acc.y = fmaf(fo, v.y, acc.y);
+    acc.z = fmaf(fo, v.z, acc.z);
+    acc.w = fmaf(fo, v.w, acc.w);
+  }
+};
 template <bool Lists>
-__device__ __forceinline__ void put_row(const DecodeArgs& a, const Tile& t, int row, float4 acc, float m,
-                                        float z, int lane) {
-  const float inv = z == 0.f ? 0.f : 1.f / z;
+__device__ __forceinline__ void put_row(const DecodeArgs& a, const Tile& t, int row, const Joined& j, int lane) {
+  const float f = row_factor(j.z, j.er);
   const int64_t at = row_of<Lists>(a, t, row);
   *reinterpret_cast<uint2*>(a.out + at * kHeadDim + 4 * lane) =
-      make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
-  if (a.lse && lane == 0) a.lse[at] = row_lse(m, z);
+      make_uint2(bf16x2_bits(j.acc.x * f, j.acc.y * f), bf16x2_bits(j.acc.z * f, j.acc.w * f));
+  if (a.lse && lane == 0) a.lse[at] = row_lse(j.m, j.z);
 }
 
 // ---------------------------------------------------------------------------
 
 template <int M, bool Lists>
-__global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(warps_of(M) * 32, 1) fp8_decode_kernel(const __grid_constant__ DecodeArgs a) {
+  using Lay = Layout<M>;
+  constexpr int kWarps = warps_of(M), kThreads = kWarps * 32, kStages = stages_of(M);
   constexpr int NG = kWarps / M, S = kStages / NG;  // groups, stages of a group
-  static_assert(S <= 32, "a unit is looked up at most 32 ahead");
+  static_assert(S <= 24, "a unit is looked up at most 24 ahead");
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = warp / M, wig = warp % M;
-  uint64_t* const full = reinterpret_cast<uint64_t*>(sm + kBarOff) + group * S;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(sm + Lay::kBarOff) + group * S;
   uint64_t* const empty = full + kStages;
-  int64_t* const sums = reinterpret_cast<int64_t*>(sm + kSumOff);
-  int64_t* const seg = reinterpret_cast<int64_t*>(sm + kSegOff);
-  int64_t* const pref = reinterpret_cast<int64_t*>(sm + kPrefOff);
+  int64_t* const sums = reinterpret_cast<int64_t*>(sm + Lay::kSumOff);
+  int2* const seg = reinterpret_cast<int2*>(sm + Lay::kSegOff);
+  int4* const jobs = reinterpret_cast<int4*>(sm + Lay::kJobOff);  // [0].x: how many
+  int64_t* const pref = reinterpret_cast<int64_t*>(sm + Lay::kPrefOff);
   if (tid < kStages) {
-    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(sm + kBarOff) + tid), 1);
-    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(sm + kBarOff) + kStages + tid), M);
+    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(sm + Lay::kBarOff) + tid), 1);
+    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(sm + Lay::kBarOff) + kStages + tid), M);
     fence_barrier_init();
   }
   pdl_wait();
@@ -499,34 +565,31 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
   const int64_t u0 = cut.group_lo(blockIdx.x, group, NG);
   const int64_t n64 = cut.group_lo(blockIdx.x, group + 1, NG) - u0;
 
-  // ---- what unit u is: its tile, first token, page (-1: skipped) and scales
-  struct Unit {
-    int tile, tb, page, sc;
-    int i, n;  // number in its tile, units of the tile
+  // ---- what unit k of the range is: its tile, first token, KV head and the table's entry
+  struct Look {
+    int tile, tb, head, page;  // page: -2 where the unit is skipped
   };
-  auto resolve = [&](int64_t k) {
-    Unit r{0, 0, -1, 0, 0, 1};
+  auto look = [&](int k) {
+    Look r{0, 0, 0, -2};
     if (k >= n64) return r;
     const int64_t u = u0 + k;
-    int owner, head;
+    int owner;
     if (Lists) {
-      r.n = a.kb * kPageSubs;
-      const int64_t tile = u / r.n;
-      r.i = (int)(u - tile * r.n);
-      r.tile = (int)tile;
-      const Tile t = tile_of(a, tile);
-      owner = t.owner / a.Q;
-      head = t.head;
-      const int b = a.idx[(int64_t)t.owner * a.kb + r.i / kPageSubs];
-      if (b < 0) return r;
+      const uint32_t n = a.kb * kPageSubs;
+      r.tile = (u >> 31) ? (int)(u / n) : a.by_n((uint32_t)u);
+      const int i = (int)(u - (int64_t)r.tile * n);
+      const Tile t = tile_of(a, r.tile);
+      owner = a.by_q(t.owner);
+      r.head = t.head;
+      const int b = a.idx[(int64_t)t.owner * a.kb + i / kPageSubs];
       const int64_t L = a.seq_lens[owner];
-      const int64_t p = L - a.Q + t.owner % a.Q;
-      if (L < 0 || L > a.W * kPageTokens) return r;
+      const int64_t p = L - a.Q + (t.owner - owner * a.Q);
+      if (b < 0 || L < 0 || L > a.W * kPageTokens) return r;
       if (p < 0 || b > p / kPageTokens) {
         flag(a.status, MX4_STATUS_BAD_INDEX);
         return r;
       }
-      r.tb = b * kPageTokens + (r.i % kPageSubs) * kSub;
+      r.tb = b * kPageTokens + (i % kPageSubs) * kSub;
       if (r.tb > p) return r;
     } else {
       int lo = 0, hi = a.B - 1;
@@ -536,62 +599,108 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       }
       owner = lo;
       const int64_t before = lo ? pref[lo - 1] : 0;
-      r.n = (int)(pref[lo] - before);
-      const int64_t v = u - before * HR;
-      const int in = (int)(v / r.n);
-      r.i = (int)(v - (int64_t)in * r.n);
-      r.tile = lo * HR + in;
-      head = in / a.RT;
-      r.tb = r.i * kSub;
+      const uint32_t n = (uint32_t)(pref[lo] - before), v = (uint32_t)(u - before * HR);  // < 2^28
+      const uint32_t in = v / n;
+      r.tile = lo * HR + (int)in;
+      r.head = a.by_rt(in);
+      r.tb = (int)(v - in * n) * kSub;
     }
-    const int32_t page = a.table[(int64_t)owner * a.W + r.tb / kPageTokens];
-    if (page < 0 || page >= a.num_pages) {
-      flag(a.status, MX4_STATUS_BAD_PAGE);
-      return r;
-    }
-    r.page = page;
-    const int64_t at = ((int64_t)page * a.Hkv + head) * kPageSubs + (r.tb % kPageTokens) / kSub;
-    r.sc = a.ks[at] | (a.vs[at] << 8);
+    r.page = a.table[(int64_t)owner * a.W + r.tb / kPageTokens];
     return r;
+  };
+  // The unit as the loop reads it: tile, first token, page (-1: skipped), scales and head.
+  auto scales = [&](const Look& l) {  // K's, V's; (0, 0) where there is no page
+    int2 r = make_int2(0, 0);
+    if (l.page >= 0 && l.page < a.num_pages) {
+      const int64_t at = ((int64_t)l.page * a.Hkv + l.head) * kPageSubs + (l.tb % kPageTokens) / kSub;
+      r = make_int2(a.ks[at], a.vs[at]);
+    } else if (l.page != -2) {
+      flag(a.status, MX4_STATUS_BAD_PAGE);
+    }
+    return r;
+  };
+  auto entry = [&](const Look& l, int2 sc) {
+    return make_int4(l.tile, l.tb, l.page < a.num_pages ? max(l.page, -1) : -1, sc.x | (sc.y << 8) | (l.head << 16));
   };
 
   const int n = (int)n64;
-  Unit cur = resolve(lane), next = resolve(32 + lane);
-  int issued = 0;
-  bool dead = false;
   const uint32_t ring = smem_addr(sm) + group * S * kStepBytes;
-  // unit k's rows into its stage (k < 32 ahead of the current chunk's first unit); one warp of the
-  // group calls it
-  auto issue = [&](int k, int chunk) {
-    const bool in_next = k >= chunk + 32;
-    const int page = __shfl_sync(0xFFFFFFFFu, in_next ? next.page : cur.page, k & 31);
-    const int tb = __shfl_sync(0xFFFFFFFFu, in_next ? next.tb : cur.tb, k & 31);
-    const int tile = __shfl_sync(0xFFFFFFFFu, in_next ? next.tile : cur.tile, k & 31);
-    if (lane == 0) {
-      const int st = k % S;
-      const uint32_t bar = smem_addr(full + st), dst = ring + st * kStepBytes;
-      if (page >= 0) {
-        const int head = tile_of(a, tile).head;
-        mbar_arrive_expect_tx(bar, kStepBytes);
-        tensor_copy(dst, &a.kmap, tb % kPageTokens, head, page, bar);
-        tensor_copy(dst + kSub * kFp8Row, &a.vmap, tb % kPageTokens, head, page, bar);
-      } else {
-        mbar_arrive(bar);
-      }
+  auto issue = [&](int k, int page, int tb, int head) {  // unit k's rows into its stage
+    const int st = k % S;
+    const uint32_t bar = smem_addr(full + st), dst = ring + st * kStepBytes;
+    if (page >= 0) {
+      mbar_arrive_expect_tx(bar, kStepBytes);
+      tensor_copy(dst, &a.kmap, tb % kPageTokens, head, page, bar);
+      tensor_copy(dst + kSub * kFp8Row, &a.vmap, tb % kPageTokens, head, page, bar);
+    } else {
+      mbar_arrive(bar);
     }
-    issued = k + 1;
   };
-  if (wig == 0)
-    for (int k = 0; k < min(S, n); ++k) issue(k, 0);
 
-  Rows w;
+  Rows<q_shared(M)> w;
+  w.qs = smem_addr(sm) + Lay::kQOff + warp * 4096 + lane * 16;
   Tile tile{0, 0, 0};
-  int tile_id = -1, head_id = -1, first = 0;
   bool active = false;  // this warp has rows of the tile
+  uint4 q_raw[2][4];
+  auto begin_tile = [&](int id) {  // its queries on their way
+    tile = tile_of(a, id);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = tile.rt * 16 * M + wig * 16 + (lane >> 2) + 8 * h;
+      const bool real = r < a.R;
+      const uint4* const p =
+          reinterpret_cast<const uint4*>(a.q + (real ? row_of<Lists>(a, tile, r) : 0) * kHeadDim) + 4 * (lane & 3);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q_raw[h][i] = real ? p[i] : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto set_tile = [&]() {
+    const int s = Lists ? a.by_q(tile.owner) : tile.owner;
+    const int base = a.seq_lens[s] - a.Q + (Lists ? tile.owner - s * a.Q : 0);
+    const int r0 = tile.rt * 16 * M + wig * 16, r1 = min(r0 + 15, a.R - 1);
+    active = r0 < a.R;
+    w.clear();
+    w.min_lim = Lists ? base : base + a.by_g(r0);
+    w.max_lim = Lists ? base : base + a.by_g(max(r1, 0));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + (lane >> 2) + 8 * h;
+      w.lim[h] = r >= a.R ? -1 : Lists ? base : base + a.by_g(r);
+    }
+    w.set_q(q_raw, a.scale);
+  };
+
+  // Units are looked up 32 at a time, a lane each, and kept in a ring of 64.  At the start every
+  // lane sends for its own, before it waits for their scales and the queries.
+  int4* const units = reinterpret_cast<int4*>(sm + Lay::kUnitOff) + warp * 64;
+  int4 ahead = make_int4(0, 0, -1, 0);
+  int tile_id = -1, head_id = -1, issued = 0;
+  bool dead = false, fresh = false;  // fresh: the tile begins in this range
+  {
+    const Look l = look(lane);
+    tile_id = n > 0 ? __shfl_sync(0xFFFFFFFFu, l.tile, 0) : -1;
+    if (n > 0) begin_tile(tile_id);
+    const int2 sc = scales(l);  // (asked for ahead of the rows: behind them they came 3 us later)
+    if (wig == 0 && lane < min(S, n)) issue(lane, l.page < a.num_pages ? l.page : -1, l.tb, l.head);
+    units[lane] = entry(l, sc);
+    issued = min(S, n);
+    if (n > 0) {
+      int64_t x0;
+      if (Lists) {
+        x0 = (int64_t)tile_id * a.kb * kPageSubs;
+      } else {
+        const int64_t before = tile.owner ? pref[tile.owner - 1] : 0;
+        x0 = before * HR + (tile_id - tile.owner * HR) * (pref[tile.owner] - before);
+      }
+      fresh = u0 == x0;
+      set_tile();
+    }
+    __syncwarp();
+  }
   // rows of scratch memory, of this warp and of the CTA's first
   const int64_t cta_row = (int64_t)blockIdx.x * kWarps * 16, my_row = cta_row + warp * 16 + (lane >> 2);
-  float* const scratchmz = a.scratch + (int64_t)gridDim.x * kWarps * 16 * kHeadDim;
-  float* const recmz = a.rec + 2 * (int64_t)gridDim.x * 16 * M * kHeadDim;
+  float4* const scratchmz = reinterpret_cast<float4*>(a.scratch + (int64_t)gridDim.x * kWarps * 16 * kHeadDim);
+  float4* const recmz = reinterpret_cast<float4*>(a.rec + 2 * (int64_t)gridDim.x * 16 * M * kHeadDim);
 
   auto out_row = [&](int h) {  // this lane's row g + 8 h: its number among the owner's rows
     return tile.rt * 16 * M + wig * 16 + (lane >> 2) + 8 * h;
@@ -602,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       const int r = out_row(h);
       if (r >= a.R) continue;
       const int64_t at = row_of<Lists>(a, tile, r);
-      const float inv = w.z[h] == 0.f ? 0.f : 1.f / w.z[h];
+      const float inv = row_factor(w.z[h], (float)w.er);
       uint4* const p = reinterpret_cast<uint4*>(a.out + at * kHeadDim + 32 * (lane & 3));
 #pragma unroll
       for (int e = 0; e < 2; ++e)
@@ -618,111 +727,61 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
     }
   };
 
-  // The pieces of tile id in this CTA: the last tiles of `cnt` groups from gi on, then the first tile
-  // of group `tail` (-1: none).  to: 2 the result, else the piece of the CTA in rec.
-  auto join = [&](int64_t id, int gi, int cnt, int tail, int to) {
-    const Tile t = tile_of(a, id);
-    for (int r = warp; r < 16 * M; r += kWarps) {
-      const int row = t.rt * 16 * M + r;
-      if (row >= a.R) continue;
-      const float* const p = reinterpret_cast<const float*>(sm) + r * kRecRow;
-      const int64_t tr = cta_row + tail * M * 16 + r;
-      float m = tail >= 0 ? __ldcg(scratchmz + 2 * tr) : -INFINITY;
-      for (int x = gi; x < gi + cnt; ++x)
-        if (seg[3 * x] == id) m = fmaxf(m, p[x * 16 * M * kRecRow + kHeadDim]);
-      const float ref = m == -INFINITY ? 0.f : m;
-      float z = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = gi; x < gi + cnt; ++x) {
-        const float* const y = p + x * 16 * M * kRecRow;
-        if (seg[3 * x] == id)
-          add_piece(acc, z, *reinterpret_cast<const float4*>(y + 4 * lane), y[kHeadDim], y[kHeadDim + 1], ref);
-      }
-      if (tail >= 0)
-        add_piece(acc, z, __ldcg(reinterpret_cast<const float4*>(a.scratch + tr * kHeadDim) + lane),
-                  __ldcg(scratchmz + 2 * tr), __ldcg(scratchmz + 2 * tr + 1), ref);
-      if (to == 2) {
-        put_row<Lists>(a, t, row, acc, m, z, lane);
+  for (int k = 0; k < n; ++k) {
+    if ((k & 31) == 4 && k + 28 < n) {
+      const Look l = look(k + 28 + lane);
+      ahead = entry(l, scales(l));
+    }
+    if ((k & 31) == 8) {  // (its scales have had four units' time to arrive)
+      units[(k + 24 + lane) & 63] = ahead;
+      __syncwarp();
+    }
+    const int4 u = units[k & 63];
+    if (u.x != tile_id) {  // the tile in front ends inside this range: it is whole, or its last piece
+      w.sum_z();
+      if (fresh) {
+        if (active) write_out();
       } else {
-        const int64_t at = (2 * (int64_t)blockIdx.x + to) * 16 * M + r;
-        *reinterpret_cast<float4*>(a.rec + at * kHeadDim + 4 * lane) = acc;
-        if (lane == 0) *reinterpret_cast<float2*>(recmz + 2 * at) = make_float2(m, z);
-      }
-    }
-  };
-
-  int chunk = 0;
-  for (int k = 0; k < n && !dead; ++k) {
-    if (k - chunk == 32) {
-      chunk = k;
-      cur = next;
-      next = resolve(k + 32 + lane);
-    }
-    const int id = __shfl_sync(0xFFFFFFFFu, cur.tile, k & 31);
-    if (id != tile_id) {
-      if (tile_id >= 0) {  // the tile in front ends inside this range: it is whole, or its last piece
-        w.sum_z();
-        if (first == 0) {
-          if (active) write_out();
-        } else {
-          head_id = tile_id;
+        head_id = tile_id;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            w.put(h, a.scratch + (my_row + 8 * h) * kHeadDim, scratchmz + (my_row + 8 * h) * 2, lane);
-        }
+        for (int h = 0; h < 2; ++h)
+          w.put(h, a.scratch + (my_row + 8 * h) * kHeadDim, reinterpret_cast<float*>(scratchmz + my_row + 8 * h), lane);
       }
-      tile_id = id;
-      tile = tile_of(a, id);
-      first = __shfl_sync(0xFFFFFFFFu, cur.i, k & 31);
-      const int s = Lists ? tile.owner / a.Q : tile.owner;
-      const int base = a.seq_lens[s] - a.Q + (Lists ? tile.owner % a.Q : 0);
-      const int r0 = tile.rt * 16 * M + wig * 16, r1 = min(r0 + 15, a.R - 1);
-      active = r0 < a.R;
-      w.clear();
-      w.min_lim = Lists ? base : base + r0 / a.G;
-      w.max_lim = Lists ? base : base + max(r1, 0) / a.G;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = out_row(h);
-        const bool real = r < a.R;
-        w.lim[h] = !real ? -1 : Lists ? base : base + r / a.G;
-        w.load_q(a.q + (real ? row_of<Lists>(a, tile, r) : 0) * kHeadDim, real, h, a.scale, lane);
-      }
+      fresh = true;
+      tile_id = u.x;
+      begin_tile(tile_id);
+      set_tile();
     }
-    const int tb = __shfl_sync(0xFFFFFFFFu, cur.tb, k & 31);
-    const int page = __shfl_sync(0xFFFFFFFFu, cur.page, k & 31);
-    const int sc = __shfl_sync(0xFFFFFFFFu, cur.sc, k & 31);
     const int st = k % S;
-    if (!mbar_wait(smem_addr(full + st), (k / S) & 1)) dead = true;
-    dead = __any_sync(0xFFFFFFFFu, dead);
-    if (dead) {
-      if (lane == 0) flag(a.status, MX4_STATUS_TIMEOUT);
-      break;
-    }
-    if (page >= 0 && active) {
+    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(full + st), (k / S) & 1));
+    if (dead) break;
+    if (u.z >= 0 && active) {
       const uint32_t ka = ring + st * kStepBytes, va = ka + kSub * kFp8Row;
-      const float ek = e8m0_to_float(sc & 0xFF), ev = e8m0_to_float(sc >> 8);
-      if (tb + kSub - 1 <= w.min_lim)
-        w.template step<false>(ka, va, ek, ev, tb, lane);
+      const int kb = u.w & 0xFF, vb = (u.w >> 8) & 0xFF;
+      if (u.y + kSub - 1 <= w.min_lim && vb >= w.er + 127 - kFold && vb != 255)
+        w.template step<false>(ka, va, kb, vb, u.y, lane);
       else
-        w.template step<true>(ka, va, ek, ev, tb, lane);
+        w.template step<true>(ka, va, kb, vb, u.y, lane);
     }
     __syncwarp();
-    if (M == 1) {
-      if (k + S < n) issue(k + S, chunk);
-    } else {
+    int refill = k;  // the stage that is free
+    if (M > 1) {
       if (lane == 0) mbar_arrive(smem_addr(empty + st));
-      if (wig == 0 && k >= 1 && k - 1 + S < n) {  // the stage before: the others are done by now
-        const int e = k - 1;
-        if (!mbar_wait(smem_addr(empty + e % S), (e / S) & 1)) dead = true;
-        dead = __any_sync(0xFFFFFFFFu, dead);
-        if (!dead)
-          issue(e + S, chunk);
-        else if (lane == 0)
-          flag(a.status, MX4_STATUS_TIMEOUT);
+      refill = k - 1;  // the one before: the group's other warps are done with it by now
+    }
+    if (wig == 0 && refill >= 0 && refill + S < n) {
+      if (M > 1) {
+        dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(empty + refill % S), (refill / S) & 1));
+        if (dead) break;
       }
+      if (lane == 0) {
+        const int4 x = units[(refill + S) & 63];
+        issue(refill + S, x.z, x.y, x.w >> 16);
+      }
+      issued = refill + S + 1;
     }
   }
+  if (dead && lane == 0) flag(a.status, MX4_STATUS_TIMEOUT);
   // copies in flight land before their memory is used again (all have, but after a time-out)
   if (wig == 0 && lane == 0)
     for (int k = max(0, issued - S); k < issued; ++k)
@@ -730,49 +789,99 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
 
   // ---- pieces: each group's last tile is in registers, a tile that it ended inside its range but
   // did not begin in the scratch memory.  Pieces of one tile are joined, in the order of the units.
-  if (wig == 0 && lane == 0) {
-    seg[3 * group] = n > 0 ? tile_id : -1;
-    seg[3 * group + 1] = u0 + n;
-    seg[3 * group + 2] = head_id;
-  }
+  if (wig == 0 && lane == 0) seg[group] = make_int2(n > 0 ? tile_id : -1, head_id);
   if (n > 0) w.sum_z();
   __syncthreads();  // all stages are read
   float* const mine = reinterpret_cast<float*>(sm) + (warp * 16 + (lane >> 2)) * kRecRow;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     w.put(h, mine + h * 8 * kRecRow, mine + h * 8 * kRecRow + kHeadDim, lane);
-  if (tid == 0) a.meta[3 * blockIdx.x] = -1;
-  __syncthreads();
-  bool front = true;  // no group with units so far
-  for (int gi = 0; gi < NG; ++gi) {
-    if (seg[3 * gi] < 0) continue;
-    if (front && seg[3 * gi + 2] >= 0)  // the end of a tile that began in a CTA before
-      join(seg[3 * gi + 2], gi, 0, gi, 0);
-    front = false;
-    const int64_t id = seg[3 * gi];
-    int prev = gi - 1, last = gi, behind;
-    while (prev >= 0 && seg[3 * prev] < 0) --prev;
-    if (prev >= 0 && seg[3 * prev] == id) continue;  // joined by the first group of the tile
-    for (int x = gi + 1; x < NG; ++x)
-      if (seg[3 * x] == id) last = x;
-    for (behind = last + 1; behind < NG && seg[3 * behind] < 0;) ++behind;
-    const bool ends = behind < NG && seg[3 * behind + 2] == id;
-    const Tile t = tile_of(a, id);
-    int64_t x0, x1;  // the tile's units
-    if (Lists) {
-      x0 = id * a.kb * kPageSubs;
-      x1 = x0 + a.kb * kPageSubs;
-    } else {
-      const int64_t before = t.owner ? pref[t.owner - 1] : 0, units = pref[t.owner] - before;
-      x0 = before * HR + (id - (int64_t)t.owner * HR) * units;
-      x1 = x0 + units;
+  if (warp == 0) {
+    // Lane g has group g.  A job: tile, first and last group with it, the group behind whose first
+    // tile it is (or -1), and where the sum goes: 2 the result, else the CTA's piece in rec.
+    const int2 sg = lane < NG ? seg[lane] : make_int2(-1, -1);
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, sg.x >= 0);
+    const uint32_t below = some & ((1u << lane) - 1);
+    const int prev = below ? 31 - __clz(below) : -1;
+    const int prev_id = __shfl_sync(0xFFFFFFFFu, sg.x, max(prev, 0));
+    const bool lead = sg.x >= 0 && (prev < 0 || prev_id != sg.x);
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, sg.x);
+    const int end = 31 - __clz(same);
+    const uint32_t above = some & ~((2u << end) - 1);
+    const int next = above ? __ffs(above) - 1 : -1;
+    const int next_head = __shfl_sync(0xFFFFFFFFu, sg.y, max(next, 0));
+    const bool ends = next >= 0 && next_head == sg.x;  // the tile ends in the group behind
+    int to = 2, id = sg.x, until = -1;
+    if (lead) {
+      const int owner = a.by_hr(sg.x);
+      int64_t x0, x1;  // the tile's units
+      if (Lists) {
+        x0 = (int64_t)sg.x * a.kb * kPageSubs;
+        x1 = x0 + a.kb * kPageSubs;
+      } else {
+        const int64_t before = owner ? pref[owner - 1] : 0, units = pref[owner] - before;
+        x0 = before * HR + (sg.x - owner * HR) * units;
+        x1 = x0 + units;
+      }
+      const int64_t lo = cut.lo(blockIdx.x), hi = cut.lo(blockIdx.x + 1);
+      to = x0 < lo ? 0 : x1 > hi ? 1 : 2;
+      if (to == 1) until = (int)((x1 - 1) / cut.per);
     }
-    const bool begins = x0 >= cut.group_lo(blockIdx.x, gi, NG);
-    const bool whole = begins && (ends || seg[3 * last + 1] == x1);
-    join(id, gi, last - gi + 1, ends ? behind : -1, whole ? 2 : begins ? 1 : 0);
-    if (begins && !whole && tid == 0) {  // the second kernel joins it with those of the next CTAs
-      a.meta[3 * blockIdx.x] = id;
-      a.meta[3 * blockIdx.x + 1] = (x1 - 1) / cut.per;
+    const bool head = prev < 0 && sg.x >= 0 && sg.y >= 0;  // the end of a tile that began in a CTA before
+    const uint32_t leads = __ballot_sync(0xFFFFFFFFu, lead), heads = __ballot_sync(0xFFFFFFFFu, head);
+    const int at = 1 + __popc(leads & ((1u << lane) - 1)) + (heads ? 1 : 0);
+    if (lead) jobs[at] = make_int4(id, lane | (end << 8), ends ? next : -1, to);
+    if (head) jobs[1] = make_int4(sg.y, 1 | (0 << 8), lane, 0);
+    if (lane == 0) jobs[0].x = __popc(leads) + (heads ? 1 : 0);
+    const uint32_t open = __ballot_sync(0xFFFFFFFFu, lead && to == 1);  // at most one
+    if (open ? lane == __ffs(open) - 1 : lane == 0) {  // the second kernel joins it with the next CTAs'
+      a.meta[2 * blockIdx.x] = open ? id : -1;
+      a.meta[2 * blockIdx.x + 1] = until;
+    }
+  }
+  __syncthreads();
+  constexpr int kRows = 4;  // rows at a time: their loads are in flight together
+  const int items = jobs[0].x * (16 * M / kRows);
+  for (int i = warp; i < items; i += kWarps) {
+    const int4 job = jobs[1 + i / (16 * M / kRows)];
+    const int r0 = i % (16 * M / kRows) * kRows, g0 = job.y & 255, g1 = job.y >> 8, tail = job.z;
+    const Tile t = tile_of(a, job.x);
+    const float* const p = reinterpret_cast<const float*>(sm) + r0 * kRecRow;
+    const int64_t tr = cta_row + tail * M * 16 + r0;
+    Joined j[kRows];
+    float4 tail_mz[kRows], tail_o[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      tail_mz[r] = tail >= 0 ? __ldcg(scratchmz + tr + r) : make_float4(-INFINITY, 0.f, kNoScale, 0.f);
+      tail_o[r] = tail >= 0 ? __ldcg(reinterpret_cast<const float4*>(a.scratch + (tr + r) * kHeadDim) + lane)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int x = g0; x <= g1; ++x)  // (a group without units between them has none of the tile)
+      if (seg[x].x == job.x)
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+          j[r].see(*reinterpret_cast<const float4*>(p + (x * 16 * M + r) * kRecRow + kHeadDim));
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) j[r].see(tail_mz[r]);
+    for (int x = g0; x <= g1; ++x)
+      if (seg[x].x == job.x)
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const float* const y = p + (x * 16 * M + r) * kRecRow;
+          j[r].add(*reinterpret_cast<const float4*>(y + 4 * lane), *reinterpret_cast<const float4*>(y + kHeadDim));
+        }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      j[r].add(tail_o[r], tail_mz[r]);
+      const int row = t.rt * 16 * M + r0 + r;
+      if (row >= a.R) continue;
+      if (job.w == 2) {
+        put_row<Lists>(a, t, row, j[r], lane);
+      } else {
+        const int64_t at = (2 * (int64_t)blockIdx.x + job.w) * 16 * M + r0 + r;
+        *reinterpret_cast<float4*>(a.rec + at * kHeadDim + 4 * lane) = j[r].acc;
+        if (lane == 0) recmz[at] = make_float4(j[r].m, j[r].z, j[r].er, 0.f);
+      }
     }
   }
 }
@@ -782,47 +891,45 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
 template <int M, bool Lists>
 __global__ void __launch_bounds__(256) fp8_join_kernel(const __grid_constant__ DecodeArgs a, int ctas) {
   __shared__ float4 acc_s[8][32];
-  __shared__ float2 mz_s[8];
+  __shared__ float z_s[8];
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t id = a.meta[3 * blockIdx.x];
+  const int id = a.meta[2 * blockIdx.x];
   if (id < 0) return;
-  const int last = (int)a.meta[3 * blockIdx.x + 1];
+  const int last = a.meta[2 * blockIdx.x + 1];
   const Tile t = tile_of(a, id);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & 3;
   const int r = 2 * blockIdx.y + (warp >> 2), row = t.rt * 16 * M + r;
-  const float* const recmz = a.rec + 2 * (int64_t)ctas * 16 * M * kHeadDim;
+  const float4* const recmz = reinterpret_cast<const float4*>(a.rec + 2 * (int64_t)ctas * 16 * M * kHeadDim);
   auto slot = [&](int x) {  // CTA x's piece: its last tile's, or the one that it began in
-    return ((2 * (int64_t)x + (x == (int)blockIdx.x ? 1 : 0)) * 16 * M + r);
+    return (2 * (int64_t)x + (x == (int)blockIdx.x ? 1 : 0)) * 16 * M + r;
   };
-  float m = -INFINITY, z = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  Joined j;
   if (row < a.R) {
-    for (int x = blockIdx.x + lane; x <= last; x += 32) m = fmaxf(m, recmz[2 * slot(x)]);
+    for (int x = blockIdx.x + lane; x <= last; x += 32) j.see(recmz[slot(x)]);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-    for (int x = blockIdx.x + part; x <= last; x += 4) {
-      const float2 mz = *reinterpret_cast<const float2*>(recmz + 2 * slot(x));
-      const float4 v = *reinterpret_cast<const float4*>(a.rec + slot(x) * kHeadDim + 4 * lane);
-      add_piece(acc, z, v, mz.x, mz.y, ref);
+    for (int d = 16; d; d >>= 1) {
+      j.m = fmaxf(j.m, __shfl_xor_sync(0xFFFFFFFFu, j.m, d));
+      j.er = fmaxf(j.er, __shfl_xor_sync(0xFFFFFFFFu, j.er, d));
     }
+#pragma unroll 8
+    for (int x = blockIdx.x + part; x <= last; x += 4)
+      j.add(*reinterpret_cast<const float4*>(a.rec + slot(x) * kHeadDim + 4 * lane), recmz[slot(x)]);
   }
-  acc_s[warp][lane] = acc;
-  if (lane == 0) mz_s[warp] = make_float2(m, z);
+  acc_s[warp][lane] = j.acc;
+  if (lane == 0) z_s[warp] = j.z;
   __syncthreads();
   if (part != 0 || row >= a.R) return;
 #pragma unroll
   for (int i = 1; i < 4; ++i) {
     const float4 v = acc_s[warp + i][lane];
-    z += mz_s[warp + i].y;
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
+    j.z += z_s[warp + i];
+    j.acc.x += v.x;
+    j.acc.y += v.y;
+    j.acc.z += v.z;
+    j.acc.w += v.w;
   }
-  put_row<Lists>(a, t, row, acc, m, z, lane);
+  put_row<Lists>(a, t, row, j, lane);
 }
 
 cudaError_t kv_map(const uint8_t* pages, int64_t page_stride, int64_t head_stride, int64_t num_pages,
@@ -848,26 +955,30 @@ cudaError_t kv_map(const uint8_t* pages, int64_t page_stride, int64_t head_strid
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Workspace: pieces for the second kernel [2 CTAs][16 M][128], their m and z [2 CTAs][16 M][2],
-// scratch of the groups [8 CTAs][16][128] and [8 CTAs][16][2], meta [CTAs][3].
-size_t piece_floats(int rows_a_cta, int ctas) {
-  return (size_t)ctas * (2 * rows_a_cta + kWarps * 16) * (kHeadDim + 2);
-}
+// Workspace: pieces for the second kernel [2 CTAs][16 M][128], their m, z, Er [2 CTAs][16 M][4],
+// scratch of the groups [CTAs][warps][16] alike, meta [CTAs][2].
+size_t piece_floats(int M, int ctas) { return (size_t)ctas * 2 * 16 * M * kRecRow; }
+size_t scratch_floats(int M, int ctas) { return (size_t)ctas * warps_of(M) * 16 * kRecRow; }
 size_t ws_bytes(int M, int ctas) {
-  return piece_floats(16 * M, ctas) * 4 + (size_t)ctas * 3 * sizeof(int64_t);
+  return (piece_floats(M, ctas) + scratch_floats(M, ctas)) * 4 + (size_t)ctas * 2 * sizeof(int32_t);
 }
 
 // Rows a tile: the fewest warps whose 16 rows each hold all rows of an owner, at most eight.
-int warps_of(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
+int group_of(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
 
 template <int M, bool Lists>
 cudaError_t launch(DecodeArgs a, int64_t B, int num_sms, cudaStream_t stream) {
   auto kern = fp8_decode_kernel<M, Lists>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<M>::kBytes);
   if (e != cudaSuccess) return e;
   a.RT = (a.R + 16 * M - 1) / (16 * M);
-  a.scratch = a.rec + (size_t)num_sms * 2 * 16 * M * (kHeadDim + 2);
-  a.meta = reinterpret_cast<int64_t*>(a.rec + piece_floats(16 * M, num_sms));
+  a.by_hr = Div(a.Hkv * a.RT);
+  a.by_rt = Div(a.RT);
+  a.by_g = Div(a.G);
+  a.by_q = Div(a.Q);
+  a.by_n = Div(Lists ? a.kb * kPageSubs : 1);
+  a.scratch = a.rec + piece_floats(M, num_sms);
+  a.meta = reinterpret_cast<int32_t*>(a.scratch + scratch_floats(M, num_sms));
   const DecodeArgs all = a;
   const int64_t step = Lists ? B : kMaxOwners;  // lists take no prefix sums
   for (int64_t b0 = 0; b0 < B; b0 += step) {
@@ -878,7 +989,7 @@ cudaError_t launch(DecodeArgs a, int64_t B, int num_sms, cudaStream_t stream) {
     if (a.lse) a.lse += b0 * a.Q * a.H;
     a.table += b0 * a.W;
     a.seq_lens += b0;
-    e = launch_pdl(kern, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, a);
+    e = launch_pdl(kern, dim3(num_sms), dim3(warps_of(M) * 32), Layout<M>::kBytes, stream, a);
     if (e != cudaSuccess) return e;
     e = launch_pdl(fp8_join_kernel<M, Lists>, dim3(num_sms, 8 * M), dim3(256), 0, stream, a, num_sms);
     if (e != cudaSuccess) return e;
@@ -888,7 +999,7 @@ cudaError_t launch(DecodeArgs a, int64_t B, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-size_t fp8_decode_workspace_bytes(int rows, int num_sms) { return ws_bytes(warps_of(rows), num_sms); }
+size_t fp8_decode_workspace_bytes(int rows, int num_sms) { return ws_bytes(group_of(rows), num_sms); }
 
 cudaError_t launch_fp8_decode(const uint16_t* q, int64_t B, int Q, int H, int Hkv,
                               const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_scales,
@@ -920,7 +1031,7 @@ cudaError_t launch_fp8_decode(const uint16_t* q, int64_t B, int Q, int H, int Hk
   a.lse = lse;
   a.rec = static_cast<float*>(ws);
   a.status = status;
-  switch (warps_of(a.R)) {
+  switch (group_of(a.R)) {
     case 1: return block_idx ? launch<1, true>(a, B, num_sms, stream) : launch<1, false>(a, B, num_sms, stream);
     case 2: return block_idx ? launch<2, true>(a, B, num_sms, stream) : launch<2, false>(a, B, num_sms, stream);
     case 4: return block_idx ? launch<4, true>(a, B, num_sms, stream) : launch<4, false>(a, B, num_sms, stream);
