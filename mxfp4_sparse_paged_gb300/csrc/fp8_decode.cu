@@ -5,29 +5,30 @@
 //
 // over the visible tokens i, K_i = 2^Ek code, V_i = 2^Ev code with one E for 32 tokens and a head.
 //
-// Bound: HBM, 256 bytes a cached token and KV head, while a tile has up to about 40 rows (query
-// heads of one KV head, for all decode tokens of the sequence); the tensor pipe above.
+// Bound: HBM, 256 bytes a cached token and KV head, while a tile has up to 32 rows (query heads of
+// one KV head, for all decode tokens of the sequence); the tensor pipe above.
 //
-// Work.  A tile is 16 M rows of one KV head of one owner (a sequence; with block lists a token),
+// Work.  A tile is 8 NT M rows of one KV head of one owner (a sequence; with block lists a token),
 // a unit 32 cached tokens of it.  All units of all tiles form one list, cut into equal ranges, one
 // a CTA, and those into one for each group of M warps.  A group streams its units through a ring of
 // shared-memory stages by tensor copies (TMA, 128-byte swizzle); warps of different groups never
 // wait for one another before the end.  So the ragged lengths of a batch balance to within a unit.
 //
-// A unit in a warp (16 rows, everything in registers between the two products):
-//   S = q K^T on mma m16n8k16: E4M3 codes widen to f16 exactly, q (bf16, scaled by a power of two)
-//     too, so products are exact and sums fp32.  The k index of the fragments is a permutation of
-//     the head's dims that lets a lane read 32 consecutive bytes of a key; with the swizzle no two
-//     lanes of a quarter-warp meet in a bank.
+// A unit in a warp (8 NT rows, everything in registers between the two products; tokens, then dims
+// are the 16-row side of mma m16n8k16, so keys and values are widened once for all rows):
+//   S^T = K q^T: E4M3 codes widen to f16 exactly, q (bf16, scaled by a power of two) too, so products
+//     are exact and sums fp32.  The k index of the fragments is a permutation of the head's dims that
+//     lets a lane read 32 consecutive bytes of a key; with the swizzle no two lanes of a
+//     quarter-warp meet in a bank.
 //   p = 2^(S f - m + 8), f = scale log2(e) 2^Ek.  m moves only where a row's largest logit lies
 //     2^7 above it, so a unit costs one vote and no reduction.  z sums p in fp32; P is f16 (11
 //     bits: 2^-12 of a weight; weights down to 2^-22 of the largest keep all of them).
-//   O += P V: the accumulator fragment of S is the operand of the second product; a pair of tokens'
-//     bytes is put side by side by byte permutes and widened to f16x2, exact.  O is kept in units of
-//     2^Er, the largest 2^Ev met: 2^(Ev - Er) goes into the exponent of p (and out of z).  Units with
-//     Ev more than 6 below Er take the second form below, which scales their product in fp32, so
-//     scales of any two blocks may be any powers apart.
-// The tensor memory path (tcgen05) has no use here at 16 rows: it computes 128-row tiles from shared
+//   O^T += V^T P^T: weights of two rows are transposed in registers (movmatrix, 8 x 8); a pair of
+//     tokens' bytes is put side by side by byte permutes and widened to f16x2, exact.  O is kept in
+//     units of 2^Er, the largest 2^Ev met: 2^(Ev - Er) goes into the exponent of p (and out of z).
+//     Units with Ev more than 6 below Er take the second form below, which scales their product in
+//     fp32, so scales of any two blocks may be any powers apart.
+// The tensor memory path (tcgen05) has no use here at few rows: it computes 128-row tiles from shared
 // memory, and would put scores and weights through tensor and shared memory on the way.
 //
 // Units where some row does not see all 32 tokens (a sequence's end) take the second form of the step:
@@ -49,35 +50,27 @@ namespace mx4 {
 
 namespace {
 
-// Warps of a CTA by the warps of a group.  One: HBM is the limit, and stages of the ring count for
-// more than warps (256 ragged contexts: 163 us; 12 warps of two stages each 180).  Two and four:
-// three warps a scheduler hide the chain of a unit's products, exponentials and conversions; their
-// 168 registers leave no room for q, which they read from shared memory.
-constexpr int warps_of(int M) { return M == 1 || M == 8 ? 8 : 12; }
-constexpr bool q_shared(int M) { return M == 2 || M == 4; }
-constexpr int stages_of(int M) { return q_shared(M) ? 18 : 24; }  // of all groups of a CTA
-constexpr int kMaxWarps = 12;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 24;                      // of all groups of a CTA
 constexpr int kStepBytes = 2 * kSub * kFp8Row;   // K rows, V rows of a unit
 constexpr int kMaxOwners = 2048;                 // sequences of a launch (their prefix sums)
 constexpr int kRecRow = kHeadDim + 4;            // floats of a row in shared memory: O, m, z, Er
 constexpr int kFold = 6;                         // V scales this far below Er go into the weights
 constexpr int kNoScale = -1000;                  // Er before the first unit
+constexpr float kNoRef = -1e30f;                 // m before the first logit
 constexpr float kUp = 8.f;                       // weights are 2^kUp at the reference
 constexpr int64_t kMinUnits = 8;                 // of a CTA: one for each group of one warp
 
-// Shared memory, in bytes: stages | q fragments | barriers | sums | seg | jobs | units | prefix sums.
-template <int M>
-struct Layout {
-  static constexpr int kQOff = stages_of(M) * kStepBytes;  // [warp][8][32 lanes] of 16 bytes
-  static constexpr int kBarOff = kQOff + (q_shared(M) ? warps_of(M) * 4096 : 0);
-  static constexpr int kSumOff = kBarOff + 2 * stages_of(M) * 8;
-  static constexpr int kSegOff = kSumOff + kMaxWarps * 8;   // [group]: last tile, first tile if it began before
-  static constexpr int kJobOff = kSegOff + kMaxWarps * 8;   // tiles whose pieces are joined
-  static constexpr int kUnitOff = kJobOff + (kMaxWarps + 2) * 16;  // [warp][64]: units looked up ahead
-  static constexpr int kPrefOff = kUnitOff + kMaxWarps * 64 * 16;
-  static constexpr int kBytes = kPrefOff + kMaxOwners * 8 + 1024;  // 1024: the stages' alignment
-  static_assert(kUnitOff % 16 == 0 && kJobOff % 16 == 0 && kBytes <= 232448, "shared memory");
-};
+// Shared memory, in bytes: stages | barriers | sums | seg | jobs | units | prefix sums.
+constexpr int kBarOff = kStages * kStepBytes;
+constexpr int kSumOff = kBarOff + 2 * kStages * 8;
+constexpr int kSegOff = kSumOff + kWarps * 8;    // [group]: last tile, first tile if it began before
+constexpr int kJobOff = kSegOff + kWarps * 8;    // tiles whose pieces are joined
+constexpr int kUnitOff = kJobOff + (kWarps + 2) * 16;  // [warp][64]: units looked up ahead
+constexpr int kPrefOff = kUnitOff + kWarps * 64 * 16;
+constexpr int kSmemBytes = kPrefOff + kMaxOwners * 8 + 1024;  // 1024: the stages' alignment
+static_assert(kUnitOff % 16 == 0 && kJobOff % 16 == 0 && kSmemBytes <= 232448, "shared memory");
 
 // Division of numbers below 2^31 by d >= 1: (mulhi(x, mul) + x) >> shift.
 struct Div {
@@ -102,13 +95,13 @@ struct DecodeArgs {
   int kb;
   int64_t num_pages;
   int B, Q, H, Hkv, G;
-  int R, RT;                // rows of an owner and KV head, tiles they take
+  int R, TR, RT;            // rows of an owner and KV head, of a tile, tiles they take
   Div by_hr, by_rt, by_g, by_q, by_n;  // tiles of an owner, tiles of a head, G, Q, units of a list
   float scale;
   uint16_t* out;
   float* lse;
-  float* rec;               // pieces: [CTA][0: of a tile begun before, 1: begun here][16 M][128], m z Er
-  float* scratch;           // [CTA][warps][16][128], m z Er: tiles that a group ended but did not begin
+  float* rec;               // pieces: [CTA][0: of a tile begun before, 1: begun here][TR][128], m z Er
+  float* scratch;           // [CTA][8 warps][8 NT][128], m z Er: tiles that a group ended but did not begin
   int32_t* meta;            // [CTA][2]: the tile that begins here and ends in a later CTA (-1: none), that CTA
   uint32_t* status;
 };
@@ -166,6 +159,13 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {  // i known at
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+// An 8 x 8 matrix of halves, row lane / 4 in the lanes: its transpose alike.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, int row, int head,
                                             int page, uint32_t bar) {
   asm volatile(
@@ -175,186 +175,158 @@ __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// A warp's part of a tile: 16 rows, lane (g, c) = (lane / 4, lane % 4) holds rows g and g + 8,
-// dims 32 c .. 32 c + 31 of O (o[j]: dims 32 c + j and 32 c + 16 + j of row g, then of row g + 8).
-template <bool QS>
+// A warp's part of a tile: 8 NT rows.  Lane (g, c) = (lane / 4, lane % 4) holds, of rows 8 t + 2 c + e
+// (e = 0, 1), dims 16 g .. 16 g + 15 of O: o[j][t][e] dim 16 g + 2 j, o[j][t][2 + e] dim 16 g + 2 j + 1.
+template <int NT>
 struct Rows {
-  uint32_t qa[QS ? 1 : 8][4];
-  uint32_t qs;                    // QS: where the lane's fragments are, 512 bytes apart
-  float o[16][4];
-  float m[2], nb[2], z[2], f[2];  // reference, kUp - reference, sum, logit factor without 2^Ek
-  int er;                         // O is in units of 2^er
-  int lim[2];                     // last visible token of rows g, g + 8
-  int min_lim, max_lim;           // over the warp's rows
+  uint32_t qb[NT][8][2];              // row 8 t + g, dims 32 c + 4 j + {0, 1}, + {2, 3}
+  float o[8][NT][4];
+  float m[NT][2], z[NT][2], f[NT][2];  // reference, sum, logit factor without 2^Ek
+  int er;                              // O is in units of 2^er
+  int min_lim, max_lim;                // last visible token, least and most over the warp's rows
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      m[h] = -INFINITY;
-      nb[h] = 0.f;
-      z[h] = 0.f;
+      for (int j = 0; j < 8; ++j) o[j][t][0] = o[j][t][1] = o[j][t][2] = o[j][t][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[t][e] = kNoRef;
+        z[t][e] = 0.f;
+      }
     }
     er = kNoScale;
   }
 
   // q rows -> f16 fragments, scaled so that a row's largest element lies in [2^14, 2^15) (exact, but
-  // for elements 2^-29 of it; rows whose largest is below 2^-86 lose bits).  v: the lane's 32 dims.
-  __device__ __forceinline__ void set_q(const uint4 (&v)[2][4], float scale) {
-    float up[2];
+  // for elements 2^-29 of it; rows whose largest is below 2^-86 lose bits).  v: 32 dims of row 8 t + g.
+  __device__ __forceinline__ void set_q(const uint4 (&v)[NT][4], float scale, int lane) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int t = 0; t < NT; ++t) {
       uint32_t am = 0;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const uint32_t w = word(v[h][i >> 2], i & 3);
+        const uint32_t w = word(v[t][i >> 2], i & 3);
         am = max(am, max((w << 17) >> 1, w & 0x7FFF0000u));
       }
       am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
       am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
       const int sigma = am == 0u ? 0 : min(100, max(-113, 14 - ((int)(am >> 23) - 127)));
-      up[h] = __uint_as_float((uint32_t)(127 + sigma) << 23) * (scale < 0.f ? -1.f : 1.f);
-      f[h] = fabsf(scale) * 1.44269504f * __uint_as_float((uint32_t)(127 - sigma) << 23);
-    }
+      const float up = __uint_as_float((uint32_t)(127 + sigma) << 23) * (scale < 0.f ? -1.f : 1.f);
+      const float fr = fabsf(scale) * 1.44269504f * __uint_as_float((uint32_t)(127 - sigma) << 23);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t a[4];
+      for (int e = 0; e < 2; ++e) f[t][e] = __shfl_sync(0xFFFFFFFFu, fr, (2 * (lane & 3) + e) * 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w = word(v[i & 1][j >> 1], (2 * j + (i >> 1)) & 3);
-        a[i] = half2_bits(bf16_bits_to_float(w & 0xFFFFu) * up[i & 1], bf16_bits_to_float(w >> 16) * up[i & 1]);
-      }
-      if (QS)
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + j * 512), "r"(a[0]), "r"(a[1]),
-                     "r"(a[2]), "r"(a[3])
-                     : "memory");
-      else
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qa[QS ? 0 : j][i] = a[i];
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w = word(v[t][j >> 1], (2 * j + i) & 3);
+          qb[t][j][i] = half2_bits(bf16_bits_to_float(w & 0xFFFFu) * up, bf16_bits_to_float(w >> 16) * up);
+        }
     }
   }
 
   // One unit: 32 tokens from position tb on, K rows at ka and V rows at va (shared memory), scale
-  // bytes kb and vb.  General: some row does not see all of them, or Ev is far below er, or NaN.
-  template <bool General>
-  __device__ __forceinline__ void step(uint32_t ka, uint32_t va, int kb, int vb, int tb, int lane) {
+  // bytes kb and vb.  General: some row does not see all of them, or Ev is far below er, or NaN;
+  // lim(row of the warp) is then a row's last visible token.
+  template <bool General, class Lim>
+  __device__ __forceinline__ void step(uint32_t ka, uint32_t va, int kb, int vb, int tb, int lane, Lim lim) {
     const int g = lane >> 2, c = lane & 3;
-    float s[4][4];
-    constexpr int kN = QS ? 4 : 2;  // groups of eight tokens at a time
+    float s[2][NT][4];  // tokens 16 i + g (rows 2 c, 2 c + 1), then 16 i + g + 8
 #pragma unroll
-    for (int n = 0; n < 4; n += kN) {
-      uint4 x[kN][2];
+    for (int i = 0; i < 2; ++i) {
+      uint4 x[2][2];
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const uint32_t at = ka + (8 * (n + i) + g) * kFp8Row;
-        x[i][0] = lds128(at + (((2 * c) ^ g) << 4));
-        x[i][1] = lds128(at + (((2 * c + 1) ^ g) << 4));
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = ka + (16 * i + 8 * h + g) * kFp8Row;
+        x[h][0] = lds128(at + (((2 * c) ^ g) << 4));
+        x[h][1] = lds128(at + (((2 * c + 1) ^ g) << 4));
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        uint32_t q[4];
-        if (QS) {
-          const uint4 v = lds128(qs + j * 512);
-          q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
-        } else {
+        uint32_t k[4];
+        e4m3x4_f16x2(word(x[0][j >> 2], j & 3), k[0], k[2]);
+        e4m3x4_f16x2(word(x[1][j >> 2], j & 3), k[1], k[3]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) q[i] = qa[QS ? 0 : j][i];
-        }
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          uint32_t b0, b1;
-          e4m3x4_f16x2(word(x[i][j >> 2], j & 3), b0, b1);
-          if (j == 0) mma0(s[n + i], q, b0, b1); else mma(s[n + i], q, b0, b1);
-        }
+        for (int t = 0; t < NT; ++t)
+          if (j == 0) mma0(s[i][t], k, qb[t][j][0], qb[t][j][1]); else mma(s[i][t], k, qb[t][j][0], qb[t][j][1]);
       }
     }
-    const int rel0 = lim[0] - tb, rel1 = lim[1] - tb;  // last visible token of the unit
+    int rel[NT][2];  // last visible token of the unit
     if (General) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          if (8 * n + 2 * c + e > rel0) s[n][e] = -INFINITY;
-          if (8 * n + 2 * c + e > rel1) s[n][2 + e] = -INFINITY;
+          rel[t][e] = lim(8 * t + 2 * c + e) - tb;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (8 * i + g > rel[t][e]) s[i >> 1][t][2 * (i & 1) + e] = -INFINITY;
         }
     }
     // factors stay finite (a score of 0 is a logit of 0 whatever the scales) or NaN
     const float ek = e8m0_to_float(kb);
-    float f0 = f[0] * ek, f1 = f[1] * ek;
-    f0 = f0 > FLT_MAX ? FLT_MAX : f0;
-    f1 = f1 > FLT_MAX ? FLT_MAX : f1;
-    float mx0 = fmaxf(s[0][0], s[0][1]), mx1 = fmaxf(s[0][2], s[0][3]);
+    float fk[NT][2], top[NT][2];
+    bool above = false;
 #pragma unroll
-    for (int n = 1; n < 4; ++n) {
-      mx0 = fmaxf(mx0, fmaxf(s[n][0], s[n][1]));
-      mx1 = fmaxf(mx1, fmaxf(s[n][2], s[n][3]));
-    }
-    mx0 *= f0;
-    mx1 *= f1;
-    if (__any_sync(0xFFFFFFFFu, mx0 > m[0] + 7.f || mx1 > m[1] + 7.f)) {
-      float t[2] = {mx0, mx1};
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        t[h] = fmaxf(t[h], __shfl_xor_sync(0xFFFFFFFFu, t[h], 1));
-        t[h] = fmaxf(t[h], __shfl_xor_sync(0xFFFFFFFFu, t[h], 2));
-        if (t[h] > m[h] + 7.f) {
-          const float down = ex2(m[h] - t[h]);
-          m[h] = t[h];
-          nb[h] = kUp - t[h];
-          z[h] *= down;
+      for (int e = 0; e < 2; ++e) {
+        fk[t][e] = f[t][e] * ek;
+        fk[t][e] = fk[t][e] > FLT_MAX ? FLT_MAX : fk[t][e];
+        top[t][e] = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e])) * fk[t][e];
+        above |= top[t][e] > m[t][e] + 7.f;
+      }
+    if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            o[j][2 * h] *= down;
-            o[j][2 * h + 1] *= down;
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = top[t][e];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+          if (x > m[t][e] + 7.f) {
+            const float down = ex2(m[t][e] - x);
+            m[t][e] = x;
+            z[t][e] *= down;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              o[j][t][e] *= down;
+              o[j][t][2 + e] *= down;
+            }
           }
         }
-      }
     }
     if (vb - 127 > er && vb != 255) {  // O to the new unit (nothing is in it before the first)
       const float down = er == kNoScale ? 0.f : ex2((float)(er - vb + 127));
       er = vb - 127;
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] *= down;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][t][e] *= down;
     }
-    const float fold = General ? 0.f : (float)(vb - 127 - er);
-    uint32_t pa[2][4];
-    {
-      const float n0 = nb[0] + fold, n1 = nb[1] + fold;
-      float p[4][4], z0 = 0.f, z1 = 0.f;
+    const int fold = General ? 0 : vb - 127 - er;
+    const float up = kUp + (float)fold, back = __int_as_float((127 - fold) << 23);
+    uint32_t p[4][NT];  // tokens 8 i + 2 c, + 1 of row 8 t + g
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
+    for (int t = 0; t < NT; ++t) {
+      float w[2][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          p[n][e] = ex2(fmaf(s[n][e], f0, n0));
-          p[n][2 + e] = ex2(fmaf(s[n][2 + e], f1, n1));
-          if (General) {  // -inf times a factor of 0 or NaN is not -inf
-            if (8 * n + 2 * c + e > rel0) p[n][e] = 0.f;
-            if (8 * n + 2 * c + e > rel1) p[n][2 + e] = 0.f;
-          }
+      for (int e = 0; e < 2; ++e) {
+        const float n = up - m[t][e];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[e][i] = ex2(fmaf(s[i >> 1][t][2 * (i & 1) + e], fk[t][e], n));
+          // (-inf times a factor of 0 or NaN is not -inf)
+          if (General && 8 * i + g > rel[t][e]) w[e][i] = 0.f;
         }
-        z0 += p[n][0] + p[n][1];
-        z1 += p[n][2] + p[n][3];
+        z[t][e] = fmaf((w[e][0] + w[e][1]) + (w[e][2] + w[e][3]), back, z[t][e]);
       }
-      const float back = General ? 1.f : __int_as_float((127 - (vb - 127 - er)) << 23);
-      z[0] = fmaf(z0, back, z[0]);
-      z[1] = fmaf(z1, back, z[1]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        pa[k][0] = half2_bits(p[2 * k][0], p[2 * k][1]);
-        pa[k][1] = half2_bits(p[2 * k][2], p[2 * k][3]);
-        pa[k][2] = half2_bits(p[2 * k + 1][0], p[2 * k + 1][1]);
-        pa[k][3] = half2_bits(p[2 * k + 1][2], p[2 * k + 1][3]);
-      }
-    }
-    // a scale of NaN reaches only rows that see its tokens
-    float ev0 = 0.f, ev1 = 0.f;
-    if (General) {
-      const float ev = vb == 255 ? e8m0_to_float(255) : ex2((float)(vb - 127 - er));
-      ev0 = rel0 < 0 ? 0.f : ev;
-      ev1 = rel1 < 0 ? 0.f : ev;
+      for (int i = 0; i < 4; ++i) p[i][t] = transpose8(half2_bits(w[0][i], w[1][i]));
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -365,45 +337,41 @@ struct Rows {
         y[i] = lds128(va + r * kFp8Row + ((g ^ (2 * c + (i & 1))) << 4));
         if (General && tb + r > max_lim) y[i] = make_uint4(0, 0, 0, 0);
       }
-      uint32_t seen[4];
-      if (General) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t v[4];  // dims 2 j, 2 j + 1 of the lane's: first pair of tokens, second
+        const uint32_t sel = (j & 1) ? 0x7362 : 0x5140;
+        e4m3x4_f16x2(__byte_perm(word(y[0], j >> 1), word(y[1], j >> 1), sel), v[0], v[1]);
+        e4m3x4_f16x2(__byte_perm(word(y[2], j >> 1), word(y[3], j >> 1), sel), v[2], v[3]);
+        if (!General) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma(o[j][t], v, p[2 * k][t], p[2 * k + 1][t]);
+          continue;
+        }
+        uint32_t ind[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = 16 * k + 2 * c + 8 * (i >> 1), rel = (i & 1) ? rel1 : rel0;
-          seen[i] = (r <= rel ? 0x3C00u : 0u) | (r + 1 <= rel ? 0x3C000000u : 0u);
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t b[4][2];  // [dim of the word][token pair]
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t wa = word(y[2 * h], w), wb = word(y[2 * h + 1], w);
-          e4m3x4_f16x2(__byte_perm(wa, wb, 0x5140), b[0][h], b[1][h]);
-          e4m3x4_f16x2(__byte_perm(wa, wb, 0x7362), b[2][h], b[3][h]);
+          const __half2 x = *reinterpret_cast<const __half2*>(&v[i]);
+          const __half2 n = __hisnan2(x);
+          ind[i] = *reinterpret_cast<const uint32_t*>(&n);
+          v[i] &= ~(((ind[i] >> 10) & 0x00010001u) * 0xFFFFu);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float(&d)[4] = o[4 * w + i];
-          if (!General) {
-            mma(d, pa[k], b[i][0], b[i][1]);
-            continue;
-          }
-          float t[4], nan[4];
-          uint32_t ind[2];
+        for (int t = 0; t < NT; ++t) {
+          float x[4], nan[4];
+          uint32_t seen[2];
+          const int lr = lim(8 * t + g) - tb - 16 * k - 2 * c;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const __half2 v = *reinterpret_cast<const __half2*>(&b[i][h]);
-            const __half2 n = __hisnan2(v);
-            ind[h] = *reinterpret_cast<const uint32_t*>(&n);
-            b[i][h] &= ~(((ind[h] >> 10) & 0x00010001u) * 0xFFFFu);
-          }
-          mma0(nan, seen, ind[0], ind[1]);
-          mma0(t, pa[k], b[i][0], b[i][1]);
+          for (int i = 0; i < 2; ++i)
+            seen[i] = (8 * i <= lr ? 0x3C00u : 0u) | (8 * i + 1 <= lr ? 0x3C000000u : 0u);
+          mma0(nan, ind, seen[0], seen[1]);
+          mma0(x, v, p[2 * k][t], p[2 * k + 1][t]);
+          const float ev = vb == 255 ? e8m0_to_float(255) : ex2((float)(vb - 127 - er));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (nan[e] > 0.f) t[e] = __uint_as_float(0x7FC00000u);
-            d[e] = fmaf(e < 2 ? ev0 : ev1, t[e], d[e]);
+            if (nan[e] > 0.f) x[e] = __uint_as_float(0x7FC00000u);
+            // a scale of NaN reaches only rows that see its tokens
+            o[j][t][e] = fmaf(rel[t][e & 1] < 0 ? 0.f : ev, x[e], o[j][t][e]);
           }
         }
       }
@@ -412,22 +380,26 @@ struct Rows {
 
   __device__ __forceinline__ void sum_z() {  // over the lanes of a row
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      z[h] += __shfl_xor_sync(0xFFFFFFFFu, z[h], 1);
-      z[h] += __shfl_xor_sync(0xFFFFFFFFu, z[h], 2);
-    }
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) z[t][e] += __shfl_xor_sync(0xFFFFFFFFu, z[t][e], d);
   }
-  // row g + 8 h: O at p, its reference, sum and unit at mz
-  __device__ __forceinline__ void put(int h, float* p, float* mz, int lane) const {
-    const int c = lane & 3;
+  // rows of the warp: O to p (row_floats a row), reference, sum and unit to mz (mz_floats a row)
+  __device__ __forceinline__ void put(float* p, int row_floats, float* mz, int mz_floats, int lane) const {
+    const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(p + 32 * c + 16 * e + 4 * i) =
-            make_float4(o[4 * i][2 * h + e], o[4 * i + 1][2 * h + e], o[4 * i + 2][2 * h + e],
-                        o[4 * i + 3][2 * h + e]);
-    if (c == 0) *reinterpret_cast<float4*>(mz) = make_float4(m[h], z[h], (float)er, 0.f);
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * t + 2 * c + e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(p + r * row_floats + 16 * g + 4 * i) =
+              make_float4(o[2 * i][t][e], o[2 * i][t][2 + e], o[2 * i + 1][t][e], o[2 * i + 1][t][2 + e]);
+        if (g == 0) *reinterpret_cast<float4*>(mz + r * mz_floats) = make_float4(m[t][e], z[t][e], (float)er, 0.f);
+      }
   }
 };
 
@@ -462,15 +434,13 @@ __device__ __forceinline__ int64_t row_of(const DecodeArgs& a, const Tile& t, in
 // A row's sum of pieces, mz = (m, z, er, -) of each.
 struct Joined {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float z = 0.f, m = -INFINITY, er = kNoScale;
+  float z = 0.f, m = kNoRef, er = kNoScale;
   __device__ __forceinline__ void see(float4 mz) {  // all pieces, before the first is added
     m = fmaxf(m, mz.x);
     er = fmaxf(er, mz.z);
   }
   __device__ __forceinline__ void add(float4 v, float4 mz) {
-    // (a piece without a reference holds nothing, or NaN)
-    const float f = mz.x == -INFINITY ? (mz.y == 0.f ? 0.f : 1.f) : ex2(mz.x - m);
-    const float fo = f * ex2(mz.z - er);
+    const float f = ex2(mz.x - m), fo = f * ex2(mz.z - er);
     z = fmaf(f, mz.y, z);
     acc.x = fmaf(fo, v.x, acc.x);
     acc.y = fmaf(fo, v.y, acc.y);
@@ -489,26 +459,25 @@ __device__ __forceinline__ void put_row(const DecodeArgs& a, const Tile& t, int 
 
 // ---------------------------------------------------------------------------
 
-template <int M, bool Lists>
-__global__ void __launch_bounds__(warps_of(M) * 32, 1) fp8_decode_kernel(const __grid_constant__ DecodeArgs a) {
-  using Lay = Layout<M>;
-  constexpr int kWarps = warps_of(M), kThreads = kWarps * 32, kStages = stages_of(M);
+template <int M, int NT, bool Lists>
+__global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int NG = kWarps / M, S = kStages / NG;  // groups, stages of a group
+  constexpr int WR = 8 * NT, TR = M * WR;           // rows of a warp, of a tile
   static_assert(S <= 24, "a unit is looked up at most 24 ahead");
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = warp / M, wig = warp % M;
-  uint64_t* const full = reinterpret_cast<uint64_t*>(sm + Lay::kBarOff) + group * S;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(sm + kBarOff) + group * S;
   uint64_t* const empty = full + kStages;
-  int64_t* const sums = reinterpret_cast<int64_t*>(sm + Lay::kSumOff);
-  int2* const seg = reinterpret_cast<int2*>(sm + Lay::kSegOff);
-  int4* const jobs = reinterpret_cast<int4*>(sm + Lay::kJobOff);  // [0].x: how many
-  int64_t* const pref = reinterpret_cast<int64_t*>(sm + Lay::kPrefOff);
+  int64_t* const sums = reinterpret_cast<int64_t*>(sm + kSumOff);
+  int2* const seg = reinterpret_cast<int2*>(sm + kSegOff);
+  int4* const jobs = reinterpret_cast<int4*>(sm + kJobOff);  // [0].x: how many
+  int64_t* const pref = reinterpret_cast<int64_t*>(sm + kPrefOff);
   if (tid < kStages) {
-    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(sm + Lay::kBarOff) + tid), 1);
-    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(sm + Lay::kBarOff) + kStages + tid), M);
+    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(sm + kBarOff) + tid), 1);
+    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(sm + kBarOff) + kStages + tid), M);
     fence_barrier_init();
   }
   pdl_wait();
@@ -637,42 +606,42 @@ __global__ void __launch_bounds__(warps_of(M) * 32, 1) fp8_decode_kernel(const _
     }
   };
 
-  Rows<q_shared(M)> w;
-  w.qs = smem_addr(sm) + Lay::kQOff + warp * 4096 + lane * 16;
+  Rows<NT> w;
   Tile tile{0, 0, 0};
+  int base = 0;         // position of the tile's first decode token
   bool active = false;  // this warp has rows of the tile
-  uint4 q_raw[2][4];
+  uint4 q_raw[NT][4];
   auto begin_tile = [&](int id) {  // its queries on their way
     tile = tile_of(a, id);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = tile.rt * 16 * M + wig * 16 + (lane >> 2) + 8 * h;
+    for (int t = 0; t < NT; ++t) {
+      const int r = tile.rt * TR + wig * WR + 8 * t + (lane >> 2);
       const bool real = r < a.R;
       const uint4* const p =
           reinterpret_cast<const uint4*>(a.q + (real ? row_of<Lists>(a, tile, r) : 0) * kHeadDim) + 4 * (lane & 3);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q_raw[h][i] = real ? p[i] : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i) q_raw[t][i] = real ? p[i] : make_uint4(0, 0, 0, 0);
     }
+  };
+  // a row's last visible token (none of a padding row's; its number among the warp's)
+  auto lim = [&](int r) {
+    r += tile.rt * TR + wig * WR;
+    return r >= a.R ? -1 : Lists ? base : base + a.by_g(r);
   };
   auto set_tile = [&]() {
     const int s = Lists ? a.by_q(tile.owner) : tile.owner;
-    const int base = a.seq_lens[s] - a.Q + (Lists ? tile.owner - s * a.Q : 0);
-    const int r0 = tile.rt * 16 * M + wig * 16, r1 = min(r0 + 15, a.R - 1);
+    base = a.seq_lens[s] - a.Q + (Lists ? tile.owner - s * a.Q : 0);
+    const int r0 = tile.rt * TR + wig * WR;
     active = r0 < a.R;
     w.clear();
     w.min_lim = Lists ? base : base + a.by_g(r0);
-    w.max_lim = Lists ? base : base + a.by_g(max(r1, 0));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = r0 + (lane >> 2) + 8 * h;
-      w.lim[h] = r >= a.R ? -1 : Lists ? base : base + a.by_g(r);
-    }
-    w.set_q(q_raw, a.scale);
+    w.max_lim = Lists ? base : base + a.by_g(max(min(r0 + WR, a.R) - 1, 0));
+    w.set_q(q_raw, a.scale, lane);
   };
 
   // Units are looked up 32 at a time, a lane each, and kept in a ring of 64.  At the start every
   // lane sends for its own, before it waits for their scales and the queries.
-  int4* const units = reinterpret_cast<int4*>(sm + Lay::kUnitOff) + warp * 64;
+  int4* const units = reinterpret_cast<int4*>(sm + kUnitOff) + warp * 64;
   int4 ahead = make_int4(0, 0, -1, 0);
   int tile_id = -1, head_id = -1, issued = 0;
   bool dead = false, fresh = false;  // fresh: the tile begins in this range
@@ -697,34 +666,29 @@ __global__ void __launch_bounds__(warps_of(M) * 32, 1) fp8_decode_kernel(const _
     }
     __syncwarp();
   }
-  // rows of scratch memory, of this warp and of the CTA's first
-  const int64_t cta_row = (int64_t)blockIdx.x * kWarps * 16, my_row = cta_row + warp * 16 + (lane >> 2);
-  float4* const scratchmz = reinterpret_cast<float4*>(a.scratch + (int64_t)gridDim.x * kWarps * 16 * kHeadDim);
-  float4* const recmz = reinterpret_cast<float4*>(a.rec + 2 * (int64_t)gridDim.x * 16 * M * kHeadDim);
+  // the first row of the CTA in scratch memory
+  const int64_t cta_row = (int64_t)blockIdx.x * kWarps * WR;
+  float4* const scratchmz = reinterpret_cast<float4*>(a.scratch + (int64_t)gridDim.x * kWarps * WR * kHeadDim);
+  float4* const recmz = reinterpret_cast<float4*>(a.rec + 2 * (int64_t)gridDim.x * TR * kHeadDim);
 
-  auto out_row = [&](int h) {  // this lane's row g + 8 h: its number among the owner's rows
-    return tile.rt * 16 * M + wig * 16 + (lane >> 2) + 8 * h;
-  };
   auto write_out = [&]() {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = out_row(h);
-      if (r >= a.R) continue;
-      const int64_t at = row_of<Lists>(a, tile, r);
-      const float inv = row_factor(w.z[h], (float)w.er);
-      uint4* const p = reinterpret_cast<uint4*>(a.out + at * kHeadDim + 32 * (lane & 3));
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
+        const int r = tile.rt * TR + wig * WR + 8 * t + 2 * (lane & 3) + e;
+        if (r >= a.R) continue;
+        const int64_t at = row_of<Lists>(a, tile, r);
+        const float x = row_factor(w.z[t][e], (float)w.er);
+        uint4* const p = reinterpret_cast<uint4*>(a.out + at * kHeadDim + 16 * (lane >> 2));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int j = 8 * i, x = 2 * h + e;
-          p[2 * e + i] = make_uint4(bf16x2_bits(w.o[j][x] * inv, w.o[j + 1][x] * inv),
-                                    bf16x2_bits(w.o[j + 2][x] * inv, w.o[j + 3][x] * inv),
-                                    bf16x2_bits(w.o[j + 4][x] * inv, w.o[j + 5][x] * inv),
-                                    bf16x2_bits(w.o[j + 6][x] * inv, w.o[j + 7][x] * inv));
-        }
-      if (a.lse && (lane & 3) == 0) a.lse[at] = row_lse(w.m[h], w.z[h]);
-    }
+        for (int i = 0; i < 2; ++i)
+          p[i] = make_uint4(bf16x2_bits(w.o[4 * i][t][e] * x, w.o[4 * i][t][2 + e] * x),
+                            bf16x2_bits(w.o[4 * i + 1][t][e] * x, w.o[4 * i + 1][t][2 + e] * x),
+                            bf16x2_bits(w.o[4 * i + 2][t][e] * x, w.o[4 * i + 2][t][2 + e] * x),
+                            bf16x2_bits(w.o[4 * i + 3][t][e] * x, w.o[4 * i + 3][t][2 + e] * x));
+        if (a.lse && lane < 4) a.lse[at] = row_lse(w.m[t][e], w.z[t][e]);
+      }
   };
 
   for (int k = 0; k < n; ++k) {
@@ -743,9 +707,8 @@ __global__ void __launch_bounds__(warps_of(M) * 32, 1) fp8_decode_kernel(const _
         if (active) write_out();
       } else {
         head_id = tile_id;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          w.put(h, a.scratch + (my_row + 8 * h) * kHeadDim, reinterpret_cast<float*>(scratchmz + my_row + 8 * h), lane);
+        const int64_t row = cta_row + warp * WR;
+        w.put(a.scratch + row * kHeadDim, kHeadDim, reinterpret_cast<float*>(scratchmz + row), 4, lane);
       }
       fresh = true;
       tile_id = u.x;
@@ -759,9 +722,9 @@ __global__ void __launch_bounds__(warps_of(M) * 32, 1) fp8_decode_kernel(const _
       const uint32_t ka = ring + st * kStepBytes, va = ka + kSub * kFp8Row;
       const int kb = u.w & 0xFF, vb = (u.w >> 8) & 0xFF;
       if (u.y + kSub - 1 <= w.min_lim && vb >= w.er + 127 - kFold && vb != 255)
-        w.template step<false>(ka, va, kb, vb, u.y, lane);
+        w.template step<false>(ka, va, kb, vb, u.y, lane, lim);
       else
-        w.template step<true>(ka, va, kb, vb, u.y, lane);
+        w.template step<true>(ka, va, kb, vb, u.y, lane, lim);
     }
     __syncwarp();
     int refill = k;  // the stage that is free
@@ -792,10 +755,8 @@ __global__ void __launch_bounds__(warps_of(M) * 32, 1) fp8_decode_kernel(const _
   if (wig == 0 && lane == 0) seg[group] = make_int2(n > 0 ? tile_id : -1, head_id);
   if (n > 0) w.sum_z();
   __syncthreads();  // all stages are read
-  float* const mine = reinterpret_cast<float*>(sm) + (warp * 16 + (lane >> 2)) * kRecRow;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    w.put(h, mine + h * 8 * kRecRow, mine + h * 8 * kRecRow + kHeadDim, lane);
+  float* const mine = reinterpret_cast<float*>(sm) + warp * WR * kRecRow;
+  w.put(mine, kRecRow, mine + kHeadDim, kRecRow, lane);
   if (warp == 0) {
     // Lane g has group g.  A job: tile, first and last group with it, the group behind whose first
     // tile it is (or -1), and where the sum goes: 2 the result, else the CTA's piece in rec.
@@ -841,18 +802,18 @@ __global__ void __launch_bounds__(warps_of(M) * 32, 1) fp8_decode_kernel(const _
   }
   __syncthreads();
   constexpr int kRows = 4;  // rows at a time: their loads are in flight together
-  const int items = jobs[0].x * (16 * M / kRows);
+  const int items = jobs[0].x * (TR / kRows);
   for (int i = warp; i < items; i += kWarps) {
-    const int4 job = jobs[1 + i / (16 * M / kRows)];
-    const int r0 = i % (16 * M / kRows) * kRows, g0 = job.y & 255, g1 = job.y >> 8, tail = job.z;
+    const int4 job = jobs[1 + i / (TR / kRows)];
+    const int r0 = i % (TR / kRows) * kRows, g0 = job.y & 255, g1 = job.y >> 8, tail = job.z;
     const Tile t = tile_of(a, job.x);
     const float* const p = reinterpret_cast<const float*>(sm) + r0 * kRecRow;
-    const int64_t tr = cta_row + tail * M * 16 + r0;
+    const int64_t tr = cta_row + tail * TR + r0;
     Joined j[kRows];
     float4 tail_mz[kRows], tail_o[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      tail_mz[r] = tail >= 0 ? __ldcg(scratchmz + tr + r) : make_float4(-INFINITY, 0.f, kNoScale, 0.f);
+      tail_mz[r] = tail >= 0 ? __ldcg(scratchmz + tr + r) : make_float4(kNoRef, 0.f, kNoScale, 0.f);
       tail_o[r] = tail >= 0 ? __ldcg(reinterpret_cast<const float4*>(a.scratch + (tr + r) * kHeadDim) + lane)
                             : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -860,25 +821,25 @@ __global__ void __launch_bounds__(warps_of(M) * 32, 1) fp8_decode_kernel(const _
       if (seg[x].x == job.x)
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
-          j[r].see(*reinterpret_cast<const float4*>(p + (x * 16 * M + r) * kRecRow + kHeadDim));
+          j[r].see(*reinterpret_cast<const float4*>(p + (x * TR + r) * kRecRow + kHeadDim));
 #pragma unroll
     for (int r = 0; r < kRows; ++r) j[r].see(tail_mz[r]);
     for (int x = g0; x <= g1; ++x)
       if (seg[x].x == job.x)
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-          const float* const y = p + (x * 16 * M + r) * kRecRow;
+          const float* const y = p + (x * TR + r) * kRecRow;
           j[r].add(*reinterpret_cast<const float4*>(y + 4 * lane), *reinterpret_cast<const float4*>(y + kHeadDim));
         }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       j[r].add(tail_o[r], tail_mz[r]);
-      const int row = t.rt * 16 * M + r0 + r;
+      const int row = t.rt * TR + r0 + r;
       if (row >= a.R) continue;
       if (job.w == 2) {
         put_row<Lists>(a, t, row, j[r], lane);
       } else {
-        const int64_t at = (2 * (int64_t)blockIdx.x + job.w) * 16 * M + r0 + r;
+        const int64_t at = (2 * (int64_t)blockIdx.x + job.w) * TR + r0 + r;
         *reinterpret_cast<float4*>(a.rec + at * kHeadDim + 4 * lane) = j[r].acc;
         if (lane == 0) recmz[at] = make_float4(j[r].m, j[r].z, j[r].er, 0.f);
       }
@@ -888,7 +849,7 @@ __global__ void __launch_bounds__(warps_of(M) * 32, 1) fp8_decode_kernel(const _
 
 // Joins the pieces of the tiles that begin in CTA blockIdx.x of the first kernel and end in another:
 // two rows a CTA, four warps each.
-template <int M, bool Lists>
+template <bool Lists>
 __global__ void __launch_bounds__(256) fp8_join_kernel(const __grid_constant__ DecodeArgs a, int ctas) {
   __shared__ float4 acc_s[8][32];
   __shared__ float z_s[8];
@@ -899,10 +860,10 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(const __grid_constant__ D
   const int last = a.meta[2 * blockIdx.x + 1];
   const Tile t = tile_of(a, id);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & 3;
-  const int r = 2 * blockIdx.y + (warp >> 2), row = t.rt * 16 * M + r;
-  const float4* const recmz = reinterpret_cast<const float4*>(a.rec + 2 * (int64_t)ctas * 16 * M * kHeadDim);
+  const int r = 2 * blockIdx.y + (warp >> 2), row = t.rt * a.TR + r;
+  const float4* const recmz = reinterpret_cast<const float4*>(a.rec + 2 * (int64_t)ctas * a.TR * kHeadDim);
   auto slot = [&](int x) {  // CTA x's piece: its last tile's, or the one that it began in
-    return (2 * (int64_t)x + (x == (int)blockIdx.x ? 1 : 0)) * 16 * M + r;
+    return (2 * (int64_t)x + (x == (int)blockIdx.x ? 1 : 0)) * a.TR + r;
   };
   Joined j;
   if (row < a.R) {
@@ -955,30 +916,38 @@ cudaError_t kv_map(const uint8_t* pages, int64_t page_stride, int64_t head_strid
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Workspace: pieces for the second kernel [2 CTAs][16 M][128], their m, z, Er [2 CTAs][16 M][4],
-// scratch of the groups [CTAs][warps][16] alike, meta [CTAs][2].
-size_t piece_floats(int M, int ctas) { return (size_t)ctas * 2 * 16 * M * kRecRow; }
-size_t scratch_floats(int M, int ctas) { return (size_t)ctas * warps_of(M) * 16 * kRecRow; }
-size_t ws_bytes(int M, int ctas) {
-  return (piece_floats(M, ctas) + scratch_floats(M, ctas)) * 4 + (size_t)ctas * 2 * sizeof(int32_t);
+// Warps of a group and 8-row columns of a warp: the fewest that hold all rows of an owner and KV
+// head.  Three columns a warp at most: q, O and a unit's scores fill the registers.  128 rows a tile
+// at most.
+struct Shape {
+  int M, NT;
+};
+Shape shape_of(int rows) {
+  if (rows <= 24) return {1, (rows + 7) / 8};
+  if (rows <= 48) return {2, rows <= 32 ? 2 : 3};
+  if (rows <= 96) return {4, rows <= 64 ? 2 : 3};
+  return {8, 2};
 }
 
-// Rows a tile: the fewest warps whose 16 rows each hold all rows of an owner, at most eight.
-int group_of(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
+// Workspace: pieces for the second kernel [2 CTAs][TR][128], their m, z, Er [2 CTAs][TR][4],
+// scratch of the groups [CTAs][8][8 NT] alike, meta [CTAs][2].
+size_t piece_floats(Shape s, int ctas) { return (size_t)ctas * 2 * 8 * s.NT * s.M * kRecRow; }
+size_t scratch_floats(Shape s, int ctas) { return (size_t)ctas * kWarps * 8 * s.NT * kRecRow; }
 
-template <int M, bool Lists>
+template <int M, int NT, bool Lists>
 cudaError_t launch(DecodeArgs a, int64_t B, int num_sms, cudaStream_t stream) {
-  auto kern = fp8_decode_kernel<M, Lists>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<M>::kBytes);
+  auto kern = fp8_decode_kernel<M, NT, Lists>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  a.RT = (a.R + 16 * M - 1) / (16 * M);
+  a.TR = 8 * NT * M;
+  a.RT = (a.R + a.TR - 1) / a.TR;
   a.by_hr = Div(a.Hkv * a.RT);
   a.by_rt = Div(a.RT);
   a.by_g = Div(a.G);
   a.by_q = Div(a.Q);
   a.by_n = Div(Lists ? a.kb * kPageSubs : 1);
-  a.scratch = a.rec + piece_floats(M, num_sms);
-  a.meta = reinterpret_cast<int32_t*>(a.scratch + scratch_floats(M, num_sms));
+  a.scratch = a.rec + piece_floats({M, NT}, num_sms);
+  a.meta = reinterpret_cast<int32_t*>(a.scratch + scratch_floats({M, NT}, num_sms));
   const DecodeArgs all = a;
   const int64_t step = Lists ? B : kMaxOwners;  // lists take no prefix sums
   for (int64_t b0 = 0; b0 < B; b0 += step) {
@@ -989,17 +958,35 @@ cudaError_t launch(DecodeArgs a, int64_t B, int num_sms, cudaStream_t stream) {
     if (a.lse) a.lse += b0 * a.Q * a.H;
     a.table += b0 * a.W;
     a.seq_lens += b0;
-    e = launch_pdl(kern, dim3(num_sms), dim3(warps_of(M) * 32), Layout<M>::kBytes, stream, a);
+    e = launch_pdl(kern, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(fp8_join_kernel<M, Lists>, dim3(num_sms, 8 * M), dim3(256), 0, stream, a, num_sms);
+    e = launch_pdl(fp8_join_kernel<Lists>, dim3(num_sms, a.TR / 2), dim3(256), 0, stream, a, num_sms);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
+template <bool Lists>
+cudaError_t launch_shape(const DecodeArgs& a, int64_t B, int num_sms, cudaStream_t stream) {
+  const Shape s = shape_of(a.R);
+  switch (s.M * 8 + s.NT) {
+    case 8 + 1: return launch<1, 1, Lists>(a, B, num_sms, stream);
+    case 8 + 2: return launch<1, 2, Lists>(a, B, num_sms, stream);
+    case 8 + 3: return launch<1, 3, Lists>(a, B, num_sms, stream);
+    case 16 + 2: return launch<2, 2, Lists>(a, B, num_sms, stream);
+    case 16 + 3: return launch<2, 3, Lists>(a, B, num_sms, stream);
+    case 32 + 2: return launch<4, 2, Lists>(a, B, num_sms, stream);
+    case 32 + 3: return launch<4, 3, Lists>(a, B, num_sms, stream);
+    default: return launch<8, 2, Lists>(a, B, num_sms, stream);
+  }
+}
+
 }  // namespace
 
-size_t fp8_decode_workspace_bytes(int rows, int num_sms) { return ws_bytes(group_of(rows), num_sms); }
+size_t fp8_decode_workspace_bytes(int rows, int num_sms) { 
+  const Shape s = shape_of(rows);
+  return (piece_floats(s, num_sms) + scratch_floats(s, num_sms)) * 4 + (size_t)num_sms * 2 * sizeof(int32_t);
+}
 
 cudaError_t launch_fp8_decode(const uint16_t* q, int64_t B, int Q, int H, int Hkv,
                               const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_scales,
@@ -1031,12 +1018,7 @@ cudaError_t launch_fp8_decode(const uint16_t* q, int64_t B, int Q, int H, int Hk
   a.lse = lse;
   a.rec = static_cast<float*>(ws);
   a.status = status;
-  switch (group_of(a.R)) {
-    case 1: return block_idx ? launch<1, true>(a, B, num_sms, stream) : launch<1, false>(a, B, num_sms, stream);
-    case 2: return block_idx ? launch<2, true>(a, B, num_sms, stream) : launch<2, false>(a, B, num_sms, stream);
-    case 4: return block_idx ? launch<4, true>(a, B, num_sms, stream) : launch<4, false>(a, B, num_sms, stream);
-    default: return block_idx ? launch<8, true>(a, B, num_sms, stream) : launch<8, false>(a, B, num_sms, stream);
-  }
+  return block_idx ? launch_shape<true>(a, B, num_sms, stream) : launch_shape<false>(a, B, num_sms, stream);
 }
 
 }  // namespace mx4

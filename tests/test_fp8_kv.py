@@ -167,11 +167,13 @@ def test_c_refusals(lib, name, kw, code):
 
 
 def test_workspaces(lib):
-    # pieces of two tiles a CTA and of its warps' 16 rows (128 sums; a reference, a total, a unit and
-    # nothing), and two words; without a GPU the SM count is taken as 1024
+    # two pieces of a tile a CTA and one of each of its eight warps, rows of 132 floats (128 sums; a
+    # reference, a total, a unit and nothing), and two words; without a GPU the SM count is taken as
+    # 1024.  A tile's rows: M warps of NT times eight.
     sms = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 1024
-    for rows, M in ((1, 1), (16, 1), (17, 2), (40, 4), (65, 8), (1000, 8)):
-        want = sms * ((2 * 16 * M + 16 * (8 if M == 8 else 12)) * 132 * 4 + 8)
+    for rows, M, NT in ((1, 1, 1), (8, 1, 1), (16, 1, 2), (24, 1, 3), (25, 2, 2), (40, 2, 3), (64, 4, 2),
+                        (65, 4, 3), (128, 8, 2), (1000, 8, 2)):
+        want = sms * ((2 * 8 * NT * M + 8 * 8 * NT) * 132 * 4 + 8)
         if rows <= 128:
             assert m.fp8_block_decode_workspace(3, 16, rows, 1) == want
         if rows % 8 == 0:
