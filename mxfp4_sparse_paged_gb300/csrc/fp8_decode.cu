@@ -166,12 +166,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
+// The pages are read once a call: first to leave L2, where they would push out tables and code.
+__device__ __forceinline__ uint64_t read_once() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, int row, int head,
-                                            int page, uint32_t bar) {
+                                            int page, uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
-      "l"(map), "r"(0), "r"(row), "r"(head), "r"(page), "r"(bar)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n" ::"r"(dst),
+      "l"(map), "r"(0), "r"(row), "r"(head), "r"(page), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -594,13 +600,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
 
   const int n = (int)n64;
   const uint32_t ring = smem_addr(sm) + group * S * kStepBytes;
+  const uint64_t policy = read_once();
   auto issue = [&](int k, int page, int tb, int head) {  // unit k's rows into its stage
     const int st = k % S;
     const uint32_t bar = smem_addr(full + st), dst = ring + st * kStepBytes;
     if (page >= 0) {
       mbar_arrive_expect_tx(bar, kStepBytes);
-      tensor_copy(dst, &a.kmap, tb % kPageTokens, head, page, bar);
-      tensor_copy(dst + kSub * kFp8Row, &a.vmap, tb % kPageTokens, head, page, bar);
+      tensor_copy(dst, &a.kmap, tb % kPageTokens, head, page, bar, policy);
+      tensor_copy(dst + kSub * kFp8Row, &a.vmap, tb % kPageTokens, head, page, bar, policy);
     } else {
       mbar_arrive(bar);
     }
