@@ -26,14 +26,14 @@
 //   O^T += V^T P^T: weights of two rows are transposed in registers (movmatrix, 8 x 8); a pair of
 //     tokens' bytes is put side by side by byte permutes and widened to f16x2, exact.  O is kept in
 //     units of 2^Er, the largest 2^Ev met: 2^(Ev - Er) goes into the exponent of p (and out of z).
-//     Units with Ev more than 6 below Er take the second form below, which scales their product in
-//     fp32, so scales of any two blocks may be any powers apart.
+//     The product of a unit with Ev more than 6 below Er is scaled in fp32 before it is added, so
+//     scales of any two blocks may be any powers apart.
 // The tensor memory path (tcgen05) has no use here at few rows: it computes 128-row tiles from shared
 // memory, and would put scores and weights through tensor and shared memory on the way.
 //
-// Units where some row does not see all 32 tokens (a sequence's end) take the second form of the step:
-// scores are masked, values that no row sees are zeroed (rows past the length may hold anything), and
-// NaN codes that only some rows see reach those rows alone, by counting them in one more product.
+// Those, and units where some row does not see all 32 tokens (a sequence's end), take a second form of
+// the step: scores are masked, and values that no row sees, and NaN codes, are kept from the product
+// (clean() below).
 //
 // Ranges cut tiles.  A group keeps the tile it ends in until all groups of the CTA are done; then
 // pieces of the same tile are joined in shared memory.  Pieces of a tile in several CTAs go to the
@@ -159,6 +159,11 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {  // i known at
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+__device__ __forceinline__ void sts128(uint32_t at, int4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 // An 8 x 8 matrix of halves, row lane / 4 in the lanes: its transpose alike.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
@@ -189,7 +194,6 @@ struct Rows {
   float o[8][NT][4];
   float m[NT][2], z[NT][2], f[NT][2];  // reference, sum, logit factor without 2^Ek
   int er;                              // O is in units of 2^er
-  int min_lim, max_lim;                // last visible token, least and most over the warp's rows
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -235,9 +239,10 @@ struct Rows {
 
   // One unit: 32 tokens from position tb on, K rows at ka and V rows at va (shared memory), scale
   // bytes kb and vb.  General: some row does not see all of them, or Ev is far below er, or NaN;
-  // lim(row of the warp) is then a row's last visible token.
+  // lim(row of the warp) is then a row's last visible token, max_lim the last that any sees.
   template <bool General, class Lim>
-  __device__ __forceinline__ void step(uint32_t ka, uint32_t va, int kb, int vb, int tb, int lane, Lim lim) {
+  __device__ __forceinline__ void step(uint32_t ka, uint32_t va, int kb, int vb, int tb, int lane, Lim lim,
+                                       int max_lim) {
     const int g = lane >> 2, c = lane & 3;
     float s[2][NT][4];  // tokens 16 i + g (rows 2 c, 2 c + 1), then 16 i + g + 8
 #pragma unroll
@@ -259,28 +264,34 @@ struct Rows {
           if (j == 0) mma0(s[i][t], k, qb[t][j][0], qb[t][j][1]); else mma(s[i][t], k, qb[t][j][0], qb[t][j][1]);
       }
     }
-    int rel[NT][2];  // last visible token of the unit
-    if (General) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          rel[t][e] = lim(8 * t + 2 * c + e) - tb;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (8 * i + g > rel[t][e]) s[i >> 1][t][2 * (i & 1) + e] = -INFINITY;
-        }
-    }
     // factors stay finite (a score of 0 is a logit of 0 whatever the scales) or NaN
     const float ek = e8m0_to_float(kb);
     float fk[NT][2], top[NT][2];
-    bool above = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         fk[t][e] = f[t][e] * ek;
         fk[t][e] = fk[t][e] > FLT_MAX ? FLT_MAX : fk[t][e];
+      }
+    if constexpr (General) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rel = lim(8 * t + 2 * c + e) - tb;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (8 * i + g > rel) s[i >> 1][t][2 * (i & 1) + e] = -INFINITY;
+          // -inf stays -inf: no factor of 0, and no NaN from a scale that the row does not see
+          if (rel < 0 || fk[t][e] < FLT_MIN) fk[t][e] = FLT_MIN;
+        }
+    }
+    bool above = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
         top[t][e] = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e])) * fk[t][e];
         above |= top[t][e] > m[t][e] + 7.f;
       }
@@ -324,11 +335,7 @@ struct Rows {
       for (int e = 0; e < 2; ++e) {
         const float n = up - m[t][e];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[e][i] = ex2(fmaf(s[i >> 1][t][2 * (i & 1) + e], fk[t][e], n));
-          // (-inf times a factor of 0 or NaN is not -inf)
-          if (General && 8 * i + g > rel[t][e]) w[e][i] = 0.f;
-        }
+        for (int i = 0; i < 4; ++i) w[e][i] = ex2(fmaf(s[i >> 1][t][2 * (i & 1) + e], fk[t][e], n));
         z[t][e] = fmaf((w[e][0] + w[e][1]) + (w[e][2] + w[e][3]), back, z[t][e]);
       }
 #pragma unroll
@@ -338,50 +345,82 @@ struct Rows {
     for (int k = 0; k < 2; ++k) {
       uint4 y[4];  // tokens 16 k + 2 c + {0, 1, 8, 9}, dims 16 g .. 16 g + 15
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 16 * k + 2 * c + (i & 1) + 8 * (i >> 1);
-        y[i] = lds128(va + r * kFp8Row + ((g ^ (2 * c + (i & 1))) << 4));
-        if (General && tb + r > max_lim) y[i] = make_uint4(0, 0, 0, 0);
-      }
+      for (int i = 0; i < 4; ++i)
+        y[i] = lds128(va + (16 * k + 2 * c + (i & 1) + 8 * (i >> 1)) * kFp8Row + ((g ^ (2 * c + (i & 1))) << 4));
+      if constexpr (General) clean(y, 16 * k + 2 * c, tb, c, lim, max_lim);
+      if constexpr (!General) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t v[4];  // dims 2 j, 2 j + 1 of the lane's: first pair of tokens, second
-        const uint32_t sel = (j & 1) ? 0x7362 : 0x5140;
-        e4m3x4_f16x2(__byte_perm(word(y[0], j >> 1), word(y[1], j >> 1), sel), v[0], v[1]);
-        e4m3x4_f16x2(__byte_perm(word(y[2], j >> 1), word(y[3], j >> 1), sel), v[2], v[3]);
-        if (!General) {
+        for (int j = 0; j < 8; ++j) {
+          uint32_t v[4];
+          values(y, j, v);
 #pragma unroll
           for (int t = 0; t < NT; ++t) mma(o[j][t], v, p[2 * k][t], p[2 * k + 1][t]);
-          continue;
         }
-        uint32_t ind[4];
+      } else {
+        const float ev = vb == 255 ? e8m0_to_float(255) : ex2((float)(vb - 127 - er));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2 x = *reinterpret_cast<const __half2*>(&v[i]);
-          const __half2 n = __hisnan2(x);
-          ind[i] = *reinterpret_cast<const uint32_t*>(&n);
-          v[i] &= ~(((ind[i] >> 10) & 0x00010001u) * 0xFFFFu);
-        }
+        for (int j = 0; j < 8; ++j) {
+          uint32_t v[4];
+          values(y, j, v);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float x[4], nan[4];
-          uint32_t seen[2];
-          const int lr = lim(8 * t + g) - tb - 16 * k - 2 * c;
+          for (int t = 0; t < NT; ++t) {
+            float x[4];
+            mma0(x, v, p[2 * k][t], p[2 * k + 1][t]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            seen[i] = (8 * i <= lr ? 0x3C00u : 0u) | (8 * i + 1 <= lr ? 0x3C000000u : 0u);
-          mma0(nan, ind, seen[0], seen[1]);
-          mma0(x, v, p[2 * k][t], p[2 * k + 1][t]);
-          const float ev = vb == 255 ? e8m0_to_float(255) : ex2((float)(vb - 127 - er));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (nan[e] > 0.f) x[e] = __uint_as_float(0x7FC00000u);
-            // a scale of NaN reaches only rows that see its tokens
-            o[j][t][e] = fmaf(rel[t][e & 1] < 0 ? 0.f : ev, x[e], o[j][t][e]);
+            for (int e = 0; e < 4; ++e)  // a scale of NaN reaches only rows that see its tokens
+              o[j][t][e] = fmaf(lim(8 * t + 2 * c + (e & 1)) < tb ? 0.f : ev, x[e], o[j][t][e]);
           }
         }
       }
     }
+  }
+
+  // Dims 2 j, 2 j + 1 of the lane's as f16: tokens 2 c, 2 c + 1 of the four, then 2 c + 8, 2 c + 9.
+  __device__ __forceinline__ void values(const uint4 (&y)[4], int j, uint32_t (&v)[4]) const {
+    const uint32_t sel = (j & 1) ? 0x7362 : 0x5140;
+    e4m3x4_f16x2(__byte_perm(word(y[0], j >> 1), word(y[1], j >> 1), sel), v[0], v[1]);
+    e4m3x4_f16x2(__byte_perm(word(y[2], j >> 1), word(y[3], j >> 1), sel), v[2], v[3]);
+  }
+
+  // V rows of a tail (tokens r0 + {0, 1, 8, 9} of the unit): those that no row of the warp sees become
+  // zeros (they may hold anything), and so do NaN codes, whose weight of 0 would carry them to rows
+  // that do not see them; O of the rows that do becomes NaN here (a row sees a prefix of the tokens,
+  // so the first NaN of a dim decides).
+  template <class Lim>
+  __device__ __forceinline__ void clean(uint4 (&y)[4], int r0, int tb, int c, Lim lim, int max_lim) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (tb + r0 + (i & 1) + 8 * (i >> 1) > max_lim) y[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) any |= ((word(y[i], j) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    }
+    if (!__any_sync(0xFFFFFFFFu, any != 0)) return;
+#pragma unroll
+    for (int d = 0; d < 16; ++d) {
+      int first = 32;
+#pragma unroll
+      for (int i = 3; i >= 0; --i)
+        if (((word(y[i], d >> 2) >> (8 * (d & 3))) & 0x7F) == 0x7F) first = r0 + (i & 1) + 8 * (i >> 1);
+      first = min(first, __shfl_xor_sync(0xFFFFFFFFu, first, 1));
+      first = min(first, __shfl_xor_sync(0xFFFFFFFFu, first, 2));
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (first < 32 && tb + first <= lim(8 * t + 2 * c + e)) o[d >> 1][t][2 * (d & 1) + e] = __uint_as_float(0x7FC00000u);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i].x = drop_nan(y[i].x);
+      y[i].y = drop_nan(y[i].y);
+      y[i].z = drop_nan(y[i].z);
+      y[i].w = drop_nan(y[i].w);
+    }
+  }
+  static __device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
+    const uint32_t n = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    return w & ~((n >> 7) * 0xFFu);
   }
 
   __device__ __forceinline__ void sum_z() {  // over the lanes of a row
@@ -475,15 +514,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = warp / M, wig = warp % M;
-  uint64_t* const full = reinterpret_cast<uint64_t*>(sm + kBarOff) + group * S;
-  uint64_t* const empty = full + kStages;
+  const uint32_t base_at = smem_addr(sm), full = base_at + kBarOff + group * S * 8, empty = full + kStages * 8;
   int64_t* const sums = reinterpret_cast<int64_t*>(sm + kSumOff);
   int2* const seg = reinterpret_cast<int2*>(sm + kSegOff);
   int4* const jobs = reinterpret_cast<int4*>(sm + kJobOff);  // [0].x: how many
   int64_t* const pref = reinterpret_cast<int64_t*>(sm + kPrefOff);
   if (tid < kStages) {
-    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(sm + kBarOff) + tid), 1);
-    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(sm + kBarOff) + kStages + tid), M);
+    mbar_init(base_at + kBarOff + tid * 8, 1);
+    mbar_init(base_at + kBarOff + (kStages + tid) * 8, M);
     fence_barrier_init();
   }
   pdl_wait();
@@ -599,12 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
   };
 
   const int n = (int)n64;
-  const uint32_t ring = smem_addr(sm) + group * S * kStepBytes;
-  const uint64_t policy = read_once();
+  const uint32_t ring = base_at + group * S * kStepBytes;
   auto issue = [&](int k, int page, int tb, int head) {  // unit k's rows into its stage
     const int st = k % S;
-    const uint32_t bar = smem_addr(full + st), dst = ring + st * kStepBytes;
+    const uint32_t bar = full + st * 8, dst = ring + st * kStepBytes;
     if (page >= 0) {
+      const uint64_t policy = read_once();
       mbar_arrive_expect_tx(bar, kStepBytes);
       tensor_copy(dst, &a.kmap, tb % kPageTokens, head, page, bar, policy);
       tensor_copy(dst + kSub * kFp8Row, &a.vmap, tb % kPageTokens, head, page, bar, policy);
@@ -614,12 +652,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
   };
 
   Rows<NT> w;
-  Tile tile{0, 0, 0};
-  int base = 0;         // position of the tile's first decode token
-  bool active = false;  // this warp has rows of the tile
+  int tile_id = -1, min_lim = 0;  // of the warp's rows: the least last visible token
+  bool active = false;            // this warp has rows of the tile
   uint4 q_raw[NT][4];
-  auto begin_tile = [&](int id) {  // its queries on their way
-    tile = tile_of(a, id);
+  auto begin_tile = [&]() {  // its queries on their way
+    const Tile tile = tile_of(a, tile_id);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = tile.rt * TR + wig * WR + 8 * t + (lane >> 2);
@@ -630,43 +667,40 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       for (int i = 0; i < 4; ++i) q_raw[t][i] = real ? p[i] : make_uint4(0, 0, 0, 0);
     }
   };
-  // a row's last visible token (none of a padding row's; its number among the warp's)
-  auto lim = [&](int r) {
-    r += tile.rt * TR + wig * WR;
-    return r >= a.R ? -1 : Lists ? base : base + a.by_g(r);
+  auto base_of = [&](const Tile& tile) {  // position of the owner's first decode token
+    const int s = Lists ? a.by_q(tile.owner) : tile.owner;
+    return a.seq_lens[s] - a.Q + (Lists ? tile.owner - s * a.Q : 0);
   };
   auto set_tile = [&]() {
-    const int s = Lists ? a.by_q(tile.owner) : tile.owner;
-    base = a.seq_lens[s] - a.Q + (Lists ? tile.owner - s * a.Q : 0);
+    const Tile tile = tile_of(a, tile_id);
     const int r0 = tile.rt * TR + wig * WR;
     active = r0 < a.R;
     w.clear();
-    w.min_lim = Lists ? base : base + a.by_g(r0);
-    w.max_lim = Lists ? base : base + a.by_g(max(min(r0 + WR, a.R) - 1, 0));
+    min_lim = base_of(tile) + (Lists ? 0 : a.by_g(r0));
     w.set_q(q_raw, a.scale, lane);
   };
 
   // Units are looked up 32 at a time, a lane each, and kept in a ring of 64.  At the start every
   // lane sends for its own, before it waits for their scales and the queries.
-  int4* const units = reinterpret_cast<int4*>(sm + kUnitOff) + warp * 64;
-  int4 ahead = make_int4(0, 0, -1, 0);
-  int tile_id = -1, head_id = -1, issued = 0;
+  const uint32_t units = base_at + kUnitOff + warp * 1024;
+  int head_id = -1, issued = 0;
   bool dead = false, fresh = false;  // fresh: the tile begins in this range
   {
     const Look l = look(lane);
     tile_id = n > 0 ? __shfl_sync(0xFFFFFFFFu, l.tile, 0) : -1;
-    if (n > 0) begin_tile(tile_id);
+    if (n > 0) begin_tile();
     const int2 sc = scales(l);  // (asked for ahead of the rows: behind them they came 3 us later)
     if (wig == 0 && lane < min(S, n)) issue(lane, l.page < a.num_pages ? l.page : -1, l.tb, l.head);
-    units[lane] = entry(l, sc);
+    sts128(units + lane * 16, entry(l, sc));
     issued = min(S, n);
     if (n > 0) {
       int64_t x0;
       if (Lists) {
         x0 = (int64_t)tile_id * a.kb * kPageSubs;
       } else {
-        const int64_t before = tile.owner ? pref[tile.owner - 1] : 0;
-        x0 = before * HR + (tile_id - tile.owner * HR) * (pref[tile.owner] - before);
+        const int owner = a.by_hr(tile_id);
+        const int64_t before = owner ? pref[owner - 1] : 0;
+        x0 = before * HR + (tile_id - owner * HR) * (pref[owner] - before);
       }
       fresh = u0 == x0;
       set_tile();
@@ -679,6 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
   float4* const recmz = reinterpret_cast<float4*>(a.rec + 2 * (int64_t)gridDim.x * TR * kHeadDim);
 
   auto write_out = [&]() {
+    const Tile tile = tile_of(a, tile_id);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -699,15 +734,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
   };
 
   for (int k = 0; k < n; ++k) {
-    if ((k & 31) == 4 && k + 28 < n) {
-      const Look l = look(k + 28 + lane);
-      ahead = entry(l, scales(l));
-    }
-    if ((k & 31) == 8) {  // (its scales have had four units' time to arrive)
-      units[(k + 24 + lane) & 63] = ahead;
+    if ((k & 31) == 8 && k + 24 < n) {  // the next 32
+      const Look l = look(k + 24 + lane);
+      sts128(units + ((k + 24 + lane) & 63) * 16, entry(l, scales(l)));
       __syncwarp();
     }
-    const int4 u = units[k & 63];
+    const uint4 uu = lds128(units + (k & 63) * 16);
+    const int4 u = make_int4(uu.x, uu.y, uu.z, uu.w);
     if (u.x != tile_id) {  // the tile in front ends inside this range: it is whole, or its last piece
       w.sum_z();
       if (fresh) {
@@ -719,34 +752,38 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       }
       fresh = true;
       tile_id = u.x;
-      begin_tile(tile_id);
+      begin_tile();
       set_tile();
     }
     const int st = k % S;
-    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(full + st), (k / S) & 1));
+    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(full + st * 8, (k / S) & 1));
     if (dead) break;
     if (u.z >= 0 && active) {
       const uint32_t ka = ring + st * kStepBytes, va = ka + kSub * kFp8Row;
       const int kb = u.w & 0xFF, vb = (u.w >> 8) & 0xFF;
-      if (u.y + kSub - 1 <= w.min_lim && vb >= w.er + 127 - kFold && vb != 255)
-        w.template step<false>(ka, va, kb, vb, u.y, lane, lim);
-      else
-        w.template step<true>(ka, va, kb, vb, u.y, lane, lim);
+      if (u.y + kSub - 1 <= min_lim && vb >= w.er + 127 - kFold && vb != 255) {
+        w.template step<false>(ka, va, kb, vb, u.y, lane, 0, 0);
+      } else {
+        const Tile tile = tile_of(a, tile_id);
+        const int base = base_of(tile), r0 = tile.rt * TR + wig * WR;
+        auto lim = [&](int r) { return r0 + r >= a.R ? -1 : Lists ? base : base + a.by_g(r0 + r); };
+        w.template step<true>(ka, va, kb, vb, u.y, lane, lim, lim(min(WR, a.R - r0) - 1));
+      }
     }
     __syncwarp();
     int refill = k;  // the stage that is free
     if (M > 1) {
-      if (lane == 0) mbar_arrive(smem_addr(empty + st));
+      if (lane == 0) mbar_arrive(empty + st * 8);
       refill = k - 1;  // the one before: the group's other warps are done with it by now
     }
     if (wig == 0 && refill >= 0 && refill + S < n) {
       if (M > 1) {
-        dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(empty + refill % S), (refill / S) & 1));
+        dead = !__all_sync(0xFFFFFFFFu, mbar_wait(empty + refill % S * 8, (refill / S) & 1));
         if (dead) break;
       }
       if (lane == 0) {
-        const int4 x = units[(refill + S) & 63];
-        issue(refill + S, x.z, x.y, x.w >> 16);
+        const uint4 x = lds128(units + ((refill + S) & 63) * 16);
+        issue(refill + S, (int)x.z, (int)x.y, (int)x.w >> 16);
       }
       issued = refill + S + 1;
     }
@@ -755,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
   // copies in flight land before their memory is used again (all have, but after a time-out)
   if (wig == 0 && lane == 0)
     for (int k = max(0, issued - S); k < issued; ++k)
-      mbar_wait(smem_addr(full + k % S), (k / S) & 1);
+      mbar_wait(full + k % S * 8, (k / S) & 1);
 
   // ---- pieces: each group's last tile is in registers, a tile that it ended inside its range but
   // did not begin in the scratch memory.  Pieces of one tile are joined, in the order of the units.
