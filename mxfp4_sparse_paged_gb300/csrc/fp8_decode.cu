@@ -10,9 +10,11 @@
 //
 // Work.  A tile is 8 NT M rows of one KV head of one owner (a sequence; with block lists a token),
 // a unit 32 cached tokens of it.  All units of all tiles form one list, cut into equal ranges, one
-// a CTA, and those into one for each group of M warps.  A group streams its units through a ring of
-// shared-memory stages by tensor copies (TMA, 128-byte swizzle); warps of different groups never
-// wait for one another before the end.  So the ragged lengths of a batch balance to within a unit.
+// a CTA, and those into one for each group of M warps.  A group's units come through a ring of
+// shared-memory stages by tensor copies (TMA, 128-byte swizzle), sent for by four warps of their own
+// (looking a unit up and sending for it took a computing warp 700 of its 2700 cycles a unit); warps of
+// different groups never wait for one another before the end.  So the ragged lengths of a batch
+// balance to within a unit.
 //
 // A unit in a warp (8 NT rows, everything in registers between the two products; tokens, then dims
 // are the 16-row side of mma m16n8k16, so keys and values are widened once for all rows):
@@ -50,8 +52,10 @@ namespace mx4 {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 8;                        // that compute; four more bring the units
+constexpr int kThreads = (kWarps + 4) * 32;
+// Registers: 384 threads of 168 at the start, then 128 of 40 and 256 of 232 (the same 64512).
+constexpr int kLoadRegs = 40, kComputeRegs = 232;
 constexpr int kStages = 24;                      // of all groups of a CTA
 constexpr int kStepBytes = 2 * kSub * kFp8Row;   // K rows, V rows of a unit
 constexpr int kMaxOwners = 2048;                 // sequences of a launch (their prefix sums)
@@ -65,9 +69,9 @@ constexpr int64_t kMinUnits = 8;                 // of a CTA: one for each group
 // Shared memory, in bytes: stages | barriers | sums | seg | jobs | units | prefix sums.
 constexpr int kBarOff = kStages * kStepBytes;
 constexpr int kSumOff = kBarOff + 2 * kStages * 8;
-constexpr int kSegOff = kSumOff + kWarps * 8;    // [group]: last tile, first tile if it began before
+constexpr int kSegOff = kSumOff + 16 * 8;        // [group]: last tile, first tile if it began before
 constexpr int kJobOff = kSegOff + kWarps * 8;    // tiles whose pieces are joined
-constexpr int kUnitOff = kJobOff + (kWarps + 2) * 16;  // [warp][64]: units looked up ahead
+constexpr int kUnitOff = kJobOff + (kWarps + 2) * 16;  // [group][64]: units looked up ahead
 constexpr int kPrefOff = kUnitOff + kWarps * 64 * 16;
 constexpr int kSmemBytes = kPrefOff + kMaxOwners * 8 + 1024;  // 1024: the stages' alignment
 static_assert(kUnitOff % 16 == 0 && kJobOff % 16 == 0 && kSmemBytes <= 232448, "shared memory");
@@ -502,19 +506,178 @@ __device__ __forceinline__ void put_row(const DecodeArgs& a, const Tile& t, int 
   if (a.lse && lane == 0) a.lse[at] = row_lse(j.m, j.z);
 }
 
+// The owner that unit u belongs to: pref sums the owners' units, HR tiles each.
+__device__ __forceinline__ int owner_of(const int64_t* pref, int B, int HR, int64_t u) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pref[mid] * HR > u) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Unit u: its tile, first token, KV head and the table's entry (-2 where the unit is skipped).
+struct Look {
+  int tile, tb, head, page;
+};
+template <bool Lists>
+__device__ __forceinline__ Look look_up(const DecodeArgs& a, const int64_t* pref, int HR, int64_t u) {
+  Look r{0, 0, 0, -2};
+  int owner;
+  if (Lists) {
+    const uint32_t n = a.kb * kPageSubs;
+    r.tile = (u >> 31) ? (int)(u / n) : a.by_n((uint32_t)u);
+    const int i = (int)(u - (int64_t)r.tile * n);
+    const Tile t = tile_of(a, r.tile);
+    owner = a.by_q(t.owner);
+    r.head = t.head;
+    const int b = a.idx[(int64_t)t.owner * a.kb + i / kPageSubs];
+    const int64_t L = a.seq_lens[owner];
+    const int64_t p = L - a.Q + (t.owner - owner * a.Q);
+    if (b < 0 || L < 0 || L > a.W * kPageTokens) return r;
+    if (p < 0 || b > p / kPageTokens) {
+      flag(a.status, MX4_STATUS_BAD_INDEX);
+      return r;
+    }
+    r.tb = b * kPageTokens + (i % kPageSubs) * kSub;
+    if (r.tb > p) return r;
+  } else {
+    owner = owner_of(pref, a.B, HR, u);
+    const int64_t before = owner ? pref[owner - 1] : 0;
+    const uint32_t n = (uint32_t)(pref[owner] - before), v = (uint32_t)(u - before * HR);  // < 2^28
+    const uint32_t in = v / n;
+    r.tile = owner * HR + (int)in;
+    r.head = a.by_rt(in);
+    r.tb = (int)(v - in * n) * kSub;
+  }
+  r.page = a.table[(int64_t)owner * a.W + r.tb / kPageTokens];
+  if (r.page < 0 || r.page >= a.num_pages) {
+    flag(a.status, MX4_STATUS_BAD_PAGE);
+    r.page = -2;
+  }
+  return r;
+}
+
+// K's and V's scale of a looked-up unit; (0, 0) where it is skipped.
+__device__ __forceinline__ int2 scales_of(const DecodeArgs& a, const Look& l) {
+  if (l.page < 0) return make_int2(0, 0);
+  const int64_t at = ((int64_t)l.page * a.Hkv + l.head) * kPageSubs + (l.tb % kPageTokens) / kSub;
+  return make_int2(a.ks[at], a.vs[at]);
+}
+
+// The barrier's transactions, ahead of the arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {  // does not wait
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ void compute_sync() {  // the computing warps
+  asm volatile("bar.sync 1, %0;\n" ::"n"(kWarps * 32) : "memory");
+}
+
+// One warp brings the units of one or two groups: looks them up 32 at a time, a lane each, keeps them
+// in a ring of 64 for the group to read (tile, first token, page or -2, scales and head), and sends
+// for a unit's rows as soon as its stage is free.
+template <int M, bool Lists, int NG, int S>
+__device__ __forceinline__ void load_units(const DecodeArgs& a, const Cut& cut, const int64_t* pref, int HR,
+                                           uint32_t base_at, int which, int lane) {
+  constexpr int GP = NG > 4 ? 2 : 1;
+  if (which >= NG) return;
+  int64_t u0[GP];
+  int n[GP], next[GP];
+  auto full = [&](int j) { return base_at + kBarOff + (which + 4 * j) * S * 8; };
+  auto units = [&](int j) { return base_at + kUnitOff + (which + 4 * j) * 1024; };
+  auto send = [&](int j, int st, int page, int tb, int head) {
+    const uint64_t policy = read_once();
+    const uint32_t bar = full(j) + st * 8, dst = base_at + ((which + 4 * j) * S + st) * kStepBytes;
+    tensor_copy(dst, &a.kmap, tb % kPageTokens, head, page, bar, policy);
+    tensor_copy(dst + kSub * kFp8Row, &a.vmap, tb % kPageTokens, head, page, bar, policy);
+  };
+#pragma unroll
+  for (int j = 0; j < GP; ++j) {
+    u0[j] = cut.group_lo(blockIdx.x, which + 4 * j, NG);
+    n[j] = (int)(cut.group_lo(blockIdx.x, which + 4 * j + 1, NG) - u0[j]);
+    next[j] = min(S, n[j]);
+    Look l{0, 0, 0, -2};
+    if (lane < n[j]) l = look_up<Lists>(a, pref, HR, u0[j] + lane);
+    // The scales are asked for ahead of the rows (behind the rows of all SMs they came 3 us later); the
+    // arrival, which the group waits for, follows when they are there.
+    const int2 sc = scales_of(a, l);
+    if (lane < next[j] && l.page >= 0) {
+      mbar_expect_tx(full(j) + lane * 8, kStepBytes);
+      send(j, lane, l.page, l.tb, l.head);
+    }
+    sts128(units(j) + lane * 16, make_int4(l.tile, l.tb, l.page, sc.x | (sc.y << 8) | (l.head << 16)));
+    __syncwarp();
+    if (lane < next[j]) mbar_arrive(full(j) + lane * 8);
+  }
+  uint32_t idle = 0;
+  for (bool more = true; more;) {
+    more = false;
+    bool did = false;
+#pragma unroll
+    for (int j = 0; j < GP; ++j) {
+      const int k = next[j];
+      if (k >= n[j]) continue;
+      more = true;
+      const int st = k % S;
+      if (!__all_sync(0xFFFFFFFFu, mbar_done(full(j) + (kStages + st) * 8, (k / S - 1) & 1))) continue;
+      if ((k & 31) == 0) {  // the next 32
+        Look l{0, 0, 0, -2};
+        if (k + lane < n[j]) l = look_up<Lists>(a, pref, HR, u0[j] + k + lane);
+        const int2 sc = scales_of(a, l);
+        sts128(units(j) + ((k + lane) & 63) * 16, make_int4(l.tile, l.tb, l.page, sc.x | (sc.y << 8) | (l.head << 16)));
+        __syncwarp();
+      }
+      if (lane == 0) {
+        const uint4 x = lds128(units(j) + (k & 63) * 16);
+        const uint32_t bar = full(j) + st * 8;
+        if ((int)x.z >= 0) {
+          mbar_arrive_expect_tx(bar, kStepBytes);
+          send(j, st, (int)x.z, (int)x.y, (int)x.w >> 16);
+        } else {
+          mbar_arrive(bar);
+        }
+      }
+      __syncwarp();
+      next[j] = k + 1;
+      did = true;
+    }
+    idle = did ? 0 : idle + 1;
+    if (more && !did) {
+      if (idle > kWaitPolls) {
+        if (lane == 0) flag(a.status, MX4_STATUS_TIMEOUT);
+        break;
+      }
+      __nanosleep(32);
+    }
+  }
+  // copies in flight land before the CTA can end
+#pragma unroll
+  for (int j = 0; j < GP; ++j)
+    for (int k = max(0, next[j] - S); k < next[j]; ++k) mbar_wait(full(j) + k % S * 8, (k / S) & 1);
+}
+
 // ---------------------------------------------------------------------------
 
 template <int M, int NT, bool Lists>
 __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int NG = kWarps / M, S = kStages / NG;  // groups, stages of a group
   constexpr int WR = 8 * NT, TR = M * WR;           // rows of a warp, of a tile
-  static_assert(S <= 24, "a unit is looked up at most 24 ahead");
+  static_assert(S < 32, "the ring of looked-up units holds 64");
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int group = warp / M, wig = warp % M;
-  const uint32_t base_at = smem_addr(sm), full = base_at + kBarOff + group * S * 8, empty = full + kStages * 8;
+  const uint32_t base_at = smem_addr(sm);
   int64_t* const sums = reinterpret_cast<int64_t*>(sm + kSumOff);
   int2* const seg = reinterpret_cast<int2*>(sm + kSegOff);
   int4* const jobs = reinterpret_cast<int4*>(sm + kJobOff);  // [0].x: how many
@@ -575,81 +738,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       for (int i = tid; i < a.H; i += kThreads) a.lse[t * a.H + i] = -INFINITY;
   }
 
+  if (warp >= kWarps) {
+    // ================= units of groups warp - 8 and, with eight groups, warp - 4
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    load_units<M, Lists, NG, S>(a, cut, pref, HR, base_at, warp - kWarps, lane);
+    return;
+  }
+  // ================= computing
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+  const int group = warp / M, wig = warp % M;
+  const uint32_t full = base_at + kBarOff + group * S * 8, empty = full + kStages * 8;
+  const uint32_t ring = base_at + group * S * kStepBytes, units = base_at + kUnitOff + group * 1024;
   const int64_t u0 = cut.group_lo(blockIdx.x, group, NG);
-  const int64_t n64 = cut.group_lo(blockIdx.x, group + 1, NG) - u0;
-
-  // ---- what unit k of the range is: its tile, first token, KV head and the table's entry
-  struct Look {
-    int tile, tb, head, page;  // page: -2 where the unit is skipped
-  };
-  auto look = [&](int k) {
-    Look r{0, 0, 0, -2};
-    if (k >= n64) return r;
-    const int64_t u = u0 + k;
-    int owner;
-    if (Lists) {
-      const uint32_t n = a.kb * kPageSubs;
-      r.tile = (u >> 31) ? (int)(u / n) : a.by_n((uint32_t)u);
-      const int i = (int)(u - (int64_t)r.tile * n);
-      const Tile t = tile_of(a, r.tile);
-      owner = a.by_q(t.owner);
-      r.head = t.head;
-      const int b = a.idx[(int64_t)t.owner * a.kb + i / kPageSubs];
-      const int64_t L = a.seq_lens[owner];
-      const int64_t p = L - a.Q + (t.owner - owner * a.Q);
-      if (b < 0 || L < 0 || L > a.W * kPageTokens) return r;
-      if (p < 0 || b > p / kPageTokens) {
-        flag(a.status, MX4_STATUS_BAD_INDEX);
-        return r;
-      }
-      r.tb = b * kPageTokens + (i % kPageSubs) * kSub;
-      if (r.tb > p) return r;
-    } else {
-      int lo = 0, hi = a.B - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (pref[mid] * HR > u) hi = mid; else lo = mid + 1;
-      }
-      owner = lo;
-      const int64_t before = lo ? pref[lo - 1] : 0;
-      const uint32_t n = (uint32_t)(pref[lo] - before), v = (uint32_t)(u - before * HR);  // < 2^28
-      const uint32_t in = v / n;
-      r.tile = lo * HR + (int)in;
-      r.head = a.by_rt(in);
-      r.tb = (int)(v - in * n) * kSub;
-    }
-    r.page = a.table[(int64_t)owner * a.W + r.tb / kPageTokens];
-    return r;
-  };
-  // The unit as the loop reads it: tile, first token, page (-1: skipped), scales and head.
-  auto scales = [&](const Look& l) {  // K's, V's; (0, 0) where there is no page
-    int2 r = make_int2(0, 0);
-    if (l.page >= 0 && l.page < a.num_pages) {
-      const int64_t at = ((int64_t)l.page * a.Hkv + l.head) * kPageSubs + (l.tb % kPageTokens) / kSub;
-      r = make_int2(a.ks[at], a.vs[at]);
-    } else if (l.page != -2) {
-      flag(a.status, MX4_STATUS_BAD_PAGE);
-    }
-    return r;
-  };
-  auto entry = [&](const Look& l, int2 sc) {
-    return make_int4(l.tile, l.tb, l.page < a.num_pages ? max(l.page, -1) : -1, sc.x | (sc.y << 8) | (l.head << 16));
-  };
-
-  const int n = (int)n64;
-  const uint32_t ring = base_at + group * S * kStepBytes;
-  auto issue = [&](int k, int page, int tb, int head) {  // unit k's rows into its stage
-    const int st = k % S;
-    const uint32_t bar = full + st * 8, dst = ring + st * kStepBytes;
-    if (page >= 0) {
-      const uint64_t policy = read_once();
-      mbar_arrive_expect_tx(bar, kStepBytes);
-      tensor_copy(dst, &a.kmap, tb % kPageTokens, head, page, bar, policy);
-      tensor_copy(dst + kSub * kFp8Row, &a.vmap, tb % kPageTokens, head, page, bar, policy);
-    } else {
-      mbar_arrive(bar);
-    }
-  };
+  const int n = (int)(cut.group_lo(blockIdx.x, group + 1, NG) - u0);
 
   Rows<NT> w;
   int tile_id = -1, min_lim = 0;  // of the warp's rows: the least last visible token
@@ -680,32 +781,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
     w.set_q(q_raw, a.scale, lane);
   };
 
-  // Units are looked up 32 at a time, a lane each, and kept in a ring of 64.  At the start every
-  // lane sends for its own, before it waits for their scales and the queries.
-  const uint32_t units = base_at + kUnitOff + warp * 1024;
-  int head_id = -1, issued = 0;
+  int head_id = -1;
   bool dead = false, fresh = false;  // fresh: the tile begins in this range
-  {
-    const Look l = look(lane);
-    tile_id = n > 0 ? __shfl_sync(0xFFFFFFFFu, l.tile, 0) : -1;
-    if (n > 0) begin_tile();
-    const int2 sc = scales(l);  // (asked for ahead of the rows: behind them they came 3 us later)
-    if (wig == 0 && lane < min(S, n)) issue(lane, l.page < a.num_pages ? l.page : -1, l.tb, l.head);
-    sts128(units + lane * 16, entry(l, sc));
-    issued = min(S, n);
-    if (n > 0) {
-      int64_t x0;
-      if (Lists) {
-        x0 = (int64_t)tile_id * a.kb * kPageSubs;
-      } else {
-        const int owner = a.by_hr(tile_id);
-        const int64_t before = owner ? pref[owner - 1] : 0;
-        x0 = before * HR + (tile_id - owner * HR) * (pref[owner] - before);
-      }
-      fresh = u0 == x0;
-      set_tile();
+  if (n > 0) {
+    int64_t x0;
+    if (Lists) {
+      const uint32_t per = a.kb * kPageSubs;
+      tile_id = (u0 >> 31) ? (int)(u0 / per) : a.by_n((uint32_t)u0);
+      x0 = (int64_t)tile_id * per;
+    } else {
+      const int owner = owner_of(pref, a.B, HR, u0);
+      const int64_t before = owner ? pref[owner - 1] : 0;
+      const uint32_t per = (uint32_t)(pref[owner] - before), in = (uint32_t)(u0 - before * HR) / per;
+      tile_id = owner * HR + (int)in;
+      x0 = before * HR + (int64_t)in * per;
     }
-    __syncwarp();
+    fresh = u0 == x0;
+    begin_tile();
+    set_tile();
   }
   // the first row of the CTA in scratch memory
   const int64_t cta_row = (int64_t)blockIdx.x * kWarps * WR;
@@ -733,12 +826,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       }
   };
 
-  for (int k = 0; k < n; ++k) {
-    if ((k & 31) == 8 && k + 24 < n) {  // the next 32
-      const Look l = look(k + 24 + lane);
-      sts128(units + ((k + 24 + lane) & 63) * 16, entry(l, scales(l)));
-      __syncwarp();
-    }
+  for (int k = 0, st = 0, phase = 0; k < n; ++k) {
+    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(full + st * 8, phase));
+    if (dead) break;
     const uint4 uu = lds128(units + (k & 63) * 16);
     const int4 u = make_int4(uu.x, uu.y, uu.z, uu.w);
     if (u.x != tile_id) {  // the tile in front ends inside this range: it is whole, or its last piece
@@ -755,9 +845,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       begin_tile();
       set_tile();
     }
-    const int st = k % S;
-    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(full + st * 8, (k / S) & 1));
-    if (dead) break;
     if (u.z >= 0 && active) {
       const uint32_t ka = ring + st * kStepBytes, va = ka + kSub * kFp8Row;
       const int kb = u.w & 0xFF, vb = (u.w >> 8) & 0xFF;
@@ -771,34 +858,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       }
     }
     __syncwarp();
-    int refill = k;  // the stage that is free
-    if (M > 1) {
-      if (lane == 0) mbar_arrive(empty + st * 8);
-      refill = k - 1;  // the one before: the group's other warps are done with it by now
-    }
-    if (wig == 0 && refill >= 0 && refill + S < n) {
-      if (M > 1) {
-        dead = !__all_sync(0xFFFFFFFFu, mbar_wait(empty + refill % S * 8, (refill / S) & 1));
-        if (dead) break;
-      }
-      if (lane == 0) {
-        const uint4 x = lds128(units + ((refill + S) & 63) * 16);
-        issue(refill + S, (int)x.z, (int)x.y, (int)x.w >> 16);
-      }
-      issued = refill + S + 1;
+    if (lane == 0) mbar_arrive(empty + st * 8);
+    if (++st == S) {
+      st = 0;
+      phase ^= 1;
     }
   }
   if (dead && lane == 0) flag(a.status, MX4_STATUS_TIMEOUT);
-  // copies in flight land before their memory is used again (all have, but after a time-out)
-  if (wig == 0 && lane == 0)
-    for (int k = max(0, issued - S); k < issued; ++k)
-      mbar_wait(full + k % S * 8, (k / S) & 1);
 
   // ---- pieces: each group's last tile is in registers, a tile that it ended inside its range but
   // did not begin in the scratch memory.  Pieces of one tile are joined, in the order of the units.
   if (wig == 0 && lane == 0) seg[group] = make_int2(n > 0 ? tile_id : -1, head_id);
   if (n > 0) w.sum_z();
-  __syncthreads();  // all stages are read
+  compute_sync();  // all stages are read
   float* const mine = reinterpret_cast<float*>(sm) + warp * WR * kRecRow;
   w.put(mine, kRecRow, mine + kHeadDim, kRecRow, lane);
   if (warp == 0) {
@@ -844,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       a.meta[2 * blockIdx.x + 1] = until;
     }
   }
-  __syncthreads();
+  compute_sync();
   constexpr int kRows = 4;  // rows at a time: their loads are in flight together
   const int items = jobs[0].x * (TR / kRows);
   for (int i = warp; i < items; i += kWarps) {
