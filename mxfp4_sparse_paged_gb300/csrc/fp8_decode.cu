@@ -56,7 +56,10 @@ constexpr int kWarps = 8;                        // that compute; four more brin
 constexpr int kThreads = (kWarps + 4) * 32;
 // Registers: 384 threads of 168 at the start, then 128 of 40 and 256 of 232 (the same 64512).
 constexpr int kLoadRegs = 40, kComputeRegs = 232;
-constexpr int kStages = 24;                      // of all groups of a CTA
+// Three columns of queries do not fit the registers beside O: they are read from shared memory, which
+// leaves two stages a warp.
+constexpr bool q_shared(int NT) { return NT == 3; }
+constexpr int stages_of(int NT) { return q_shared(NT) ? 16 : 24; }  // of all groups of a CTA
 constexpr int kStepBytes = 2 * kSub * kFp8Row;   // K rows, V rows of a unit
 constexpr int kMaxOwners = 2048;                 // sequences of a launch (their prefix sums)
 constexpr int kRecRow = kHeadDim + 4;            // floats of a row in shared memory: O, m, z, Er
@@ -66,15 +69,19 @@ constexpr float kNoRef = -1e30f;                 // m before the first logit
 constexpr float kUp = 8.f;                       // weights are 2^kUp at the reference
 constexpr int64_t kMinUnits = 8;                 // of a CTA: one for each group of one warp
 
-// Shared memory, in bytes: stages | barriers | sums | seg | jobs | units | prefix sums.
-constexpr int kBarOff = kStages * kStepBytes;
-constexpr int kSumOff = kBarOff + 2 * kStages * 8;
-constexpr int kSegOff = kSumOff + 16 * 8;        // [group]: last tile, first tile if it began before
-constexpr int kJobOff = kSegOff + kWarps * 8;    // tiles whose pieces are joined
-constexpr int kUnitOff = kJobOff + (kWarps + 2) * 16;  // [group][64]: units looked up ahead
-constexpr int kPrefOff = kUnitOff + kWarps * 64 * 16;
-constexpr int kSmemBytes = kPrefOff + kMaxOwners * 8 + 1024;  // 1024: the stages' alignment
-static_assert(kUnitOff % 16 == 0 && kJobOff % 16 == 0 && kSmemBytes <= 232448, "shared memory");
+// Shared memory, in bytes: stages | queries | barriers | sums | seg | jobs | units | prefix sums.
+template <int NT>
+struct Layout {
+  static constexpr int kQOff = stages_of(NT) * kStepBytes;  // [warp][NT][4][32 lanes] of 16 bytes
+  static constexpr int kBarOff = kQOff + (q_shared(NT) ? kWarps * NT * 2048 : 0);
+  static constexpr int kSumOff = kBarOff + 2 * stages_of(NT) * 8;
+  static constexpr int kSegOff = kSumOff + 16 * 8;       // [group]: last tile, first tile if it began before
+  static constexpr int kJobOff = kSegOff + kWarps * 8;   // tiles whose pieces are joined
+  static constexpr int kUnitOff = kJobOff + (kWarps + 2) * 16;  // [group][64]: units looked up ahead
+  static constexpr int kPrefOff = kUnitOff + kWarps * 64 * 16;
+  static constexpr int kBytes = kPrefOff + kMaxOwners * 8 + 1024;  // 1024: the stages' alignment
+  static_assert(kUnitOff % 16 == 0 && kJobOff % 16 == 0 && kBytes <= 232448, "shared memory");
+};
 
 // Division of numbers below 2^31 by d >= 1: (mulhi(x, mul) + x) >> shift.
 struct Div {
@@ -194,7 +201,9 @@ __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map
 // (e = 0, 1), dims 16 g .. 16 g + 15 of O: o[j][t][e] dim 16 g + 2 j, o[j][t][2 + e] dim 16 g + 2 j + 1.
 template <int NT>
 struct Rows {
-  uint32_t qb[NT][8][2];              // row 8 t + g, dims 32 c + 4 j + {0, 1}, + {2, 3}
+  static constexpr bool QS = q_shared(NT);
+  uint32_t qb[QS ? 1 : NT][8][2];     // row 8 t + g, dims 32 c + 4 j + {0, 1}, + {2, 3}
+  uint32_t qs;                        // QS: where the lane's are, two j's together, 512 bytes apart
   float o[8][NT][4];
   float m[NT][2], z[NT][2], f[NT][2];  // reference, sum, logit factor without 2^Ek
   int er;                              // O is in units of 2^er
@@ -232,12 +241,19 @@ struct Rows {
 #pragma unroll
       for (int e = 0; e < 2; ++e) f[t][e] = __shfl_sync(0xFFFFFFFFu, fr, (2 * (lane & 3) + e) * 4);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 8; j += 2) {
+        uint32_t x[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t w = word(v[t][j >> 1], (2 * j + i) & 3);
-          qb[t][j][i] = half2_bits(bf16_bits_to_float(w & 0xFFFFu) * up, bf16_bits_to_float(w >> 16) * up);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = word(v[t][j >> 1], i);
+          x[i] = half2_bits(bf16_bits_to_float(w & 0xFFFFu) * up, bf16_bits_to_float(w >> 16) * up);
         }
+        if constexpr (QS) {
+          sts128(qs + (t * 4 + j / 2) * 512, make_int4(x[0], x[1], x[2], x[3]));
+        } else {
+          qb[t][j][0] = x[0], qb[t][j][1] = x[1], qb[t][j + 1][0] = x[2], qb[t][j + 1][1] = x[3];
+        }
+      }
     }
   }
 
@@ -249,23 +265,37 @@ struct Rows {
                                        int max_lim) {
     const int g = lane >> 2, c = lane & 3;
     float s[2][NT][4];  // tokens 16 i + g (rows 2 c, 2 c + 1), then 16 i + g + 8
+    constexpr int kI = QS ? 2 : 1;  // 16 tokens at a time, or all: queries are then read once
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint4 x[2][2];
+    for (int i0 = 0; i0 < 2; i0 += kI) {
+      uint4 x[kI][2][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t at = ka + (16 * i + 8 * h + g) * kFp8Row;
-        x[h][0] = lds128(at + (((2 * c) ^ g) << 4));
-        x[h][1] = lds128(at + (((2 * c + 1) ^ g) << 4));
-      }
+      for (int i = 0; i < kI; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = ka + (16 * (i0 + i) + 8 * h + g) * kFp8Row;
+          x[i][h][0] = lds128(at + (((2 * c) ^ g) << 4));
+          x[i][h][1] = lds128(at + (((2 * c + 1) ^ g) << 4));
+        }
+      uint4 q[NT];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        uint32_t k[4];
-        e4m3x4_f16x2(word(x[0][j >> 2], j & 3), k[0], k[2]);
-        e4m3x4_f16x2(word(x[1][j >> 2], j & 3), k[1], k[3]);
+        if constexpr (QS)
+          if (j % 2 == 0)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (j == 0) mma0(s[i][t], k, qb[t][j][0], qb[t][j][1]); else mma(s[i][t], k, qb[t][j][0], qb[t][j][1]);
+            for (int t = 0; t < NT; ++t) q[t] = lds128(qs + (t * 4 + j / 2) * 512);
+#pragma unroll
+        for (int i = 0; i < kI; ++i) {
+          uint32_t k[4];
+          e4m3x4_f16x2(word(x[i][0][j >> 2], j & 3), k[0], k[2]);
+          e4m3x4_f16x2(word(x[i][1][j >> 2], j & 3), k[1], k[3]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const uint32_t b0 = QS ? word(q[t], 2 * (j & 1)) : qb[QS ? 0 : t][j][0];
+            const uint32_t b1 = QS ? word(q[t], 2 * (j & 1) + 1) : qb[QS ? 0 : t][j][1];
+            if (j == 0) mma0(s[i0 + i][t], k, b0, b1); else mma(s[i0 + i][t], k, b0, b1);
+          }
+        }
       }
     }
     // factors stay finite (a score of 0 is a logit of 0 whatever the scales) or NaN
@@ -586,15 +616,16 @@ __device__ __forceinline__ void compute_sync() {  // the computing warps
 // One warp brings the units of one or two groups: looks them up 32 at a time, a lane each, keeps them
 // in a ring of 64 for the group to read (tile, first token, page or -2, scales and head), and sends
 // for a unit's rows as soon as its stage is free.
-template <int M, bool Lists, int NG, int S>
+template <int NT, bool Lists, int NG, int S>
 __device__ __forceinline__ void load_units(const DecodeArgs& a, const Cut& cut, const int64_t* pref, int HR,
                                            uint32_t base_at, int which, int lane) {
+  using Lay = Layout<NT>;
   constexpr int GP = NG > 4 ? 2 : 1;
   if (which >= NG) return;
   int64_t u0[GP];
   int n[GP], next[GP];
-  auto full = [&](int j) { return base_at + kBarOff + (which + 4 * j) * S * 8; };
-  auto units = [&](int j) { return base_at + kUnitOff + (which + 4 * j) * 1024; };
+  auto full = [&](int j) { return base_at + Lay::kBarOff + (which + 4 * j) * S * 8; };
+  auto units = [&](int j) { return base_at + Lay::kUnitOff + (which + 4 * j) * 1024; };
   auto send = [&](int j, int st, int page, int tb, int head) {
     const uint64_t policy = read_once();
     const uint32_t bar = full(j) + st * 8, dst = base_at + ((which + 4 * j) * S + st) * kStepBytes;
@@ -629,7 +660,7 @@ __device__ __forceinline__ void load_units(const DecodeArgs& a, const Cut& cut, 
       if (k >= n[j]) continue;
       more = true;
       const int st = k % S;
-      if (!__all_sync(0xFFFFFFFFu, mbar_done(full(j) + (kStages + st) * 8, (k / S - 1) & 1))) continue;
+      if (!__all_sync(0xFFFFFFFFu, mbar_done(full(j) + (stages_of(NT) + st) * 8, (k / S - 1) & 1))) continue;
       if ((k & 31) == 0) {  // the next 32
         Look l{0, 0, 0, -2};
         if (k + lane < n[j]) l = look_up<Lists>(a, pref, HR, u0[j] + k + lane);
@@ -670,7 +701,8 @@ __device__ __forceinline__ void load_units(const DecodeArgs& a, const Cut& cut, 
 
 template <int M, int NT, bool Lists>
 __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_constant__ DecodeArgs a) {
-  constexpr int NG = kWarps / M, S = kStages / NG;  // groups, stages of a group
+  using Lay = Layout<NT>;
+  constexpr int kStages = stages_of(NT), NG = kWarps / M, S = kStages / NG;  // groups, stages of a group
   constexpr int WR = 8 * NT, TR = M * WR;           // rows of a warp, of a tile
   static_assert(S < 32, "the ring of looked-up units holds 64");
   extern __shared__ uint8_t smem_dyn[];
@@ -678,13 +710,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base_at = smem_addr(sm);
-  int64_t* const sums = reinterpret_cast<int64_t*>(sm + kSumOff);
-  int2* const seg = reinterpret_cast<int2*>(sm + kSegOff);
-  int4* const jobs = reinterpret_cast<int4*>(sm + kJobOff);  // [0].x: how many
-  int64_t* const pref = reinterpret_cast<int64_t*>(sm + kPrefOff);
+  int64_t* const sums = reinterpret_cast<int64_t*>(sm + Lay::kSumOff);
+  int2* const seg = reinterpret_cast<int2*>(sm + Lay::kSegOff);
+  int4* const jobs = reinterpret_cast<int4*>(sm + Lay::kJobOff);  // [0].x: how many
+  int64_t* const pref = reinterpret_cast<int64_t*>(sm + Lay::kPrefOff);
   if (tid < kStages) {
-    mbar_init(base_at + kBarOff + tid * 8, 1);
-    mbar_init(base_at + kBarOff + (kStages + tid) * 8, M);
+    mbar_init(base_at + Lay::kBarOff + tid * 8, 1);
+    mbar_init(base_at + Lay::kBarOff + (kStages + tid) * 8, M);
     fence_barrier_init();
   }
   pdl_wait();
@@ -741,18 +773,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
   if (warp >= kWarps) {
     // ================= units of groups warp - 8 and, with eight groups, warp - 4
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    load_units<M, Lists, NG, S>(a, cut, pref, HR, base_at, warp - kWarps, lane);
+    load_units<NT, Lists, NG, S>(a, cut, pref, HR, base_at, warp - kWarps, lane);
     return;
   }
   // ================= computing
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
   const int group = warp / M, wig = warp % M;
-  const uint32_t full = base_at + kBarOff + group * S * 8, empty = full + kStages * 8;
-  const uint32_t ring = base_at + group * S * kStepBytes, units = base_at + kUnitOff + group * 1024;
+  const uint32_t full = base_at + Lay::kBarOff + group * S * 8, empty = full + kStages * 8;
+  const uint32_t ring = base_at + group * S * kStepBytes, units = base_at + Lay::kUnitOff + group * 1024;
   const int64_t u0 = cut.group_lo(blockIdx.x, group, NG);
   const int n = (int)(cut.group_lo(blockIdx.x, group + 1, NG) - u0);
 
   Rows<NT> w;
+  w.qs = base_at + Lay::kQOff + warp * NT * 2048 + lane * 16;
   int tile_id = -1, min_lim = 0;  // of the warp's rows: the least last visible token
   bool active = false;            // this warp has rows of the tile
   uint4 q_raw[NT][4];
@@ -776,9 +809,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
     const Tile tile = tile_of(a, tile_id);
     const int r0 = tile.rt * TR + wig * WR;
     active = r0 < a.R;
-    w.clear();
     min_lim = base_of(tile) + (Lists ? 0 : a.by_g(r0));
     w.set_q(q_raw, a.scale, lane);
+    w.clear();
   };
 
   int head_id = -1;
@@ -1053,7 +1086,7 @@ size_t scratch_floats(Shape s, int ctas) { return (size_t)ctas * kWarps * 8 * s.
 template <int M, int NT, bool Lists>
 cudaError_t launch(DecodeArgs a, int64_t B, int num_sms, cudaStream_t stream) {
   auto kern = fp8_decode_kernel<M, NT, Lists>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<NT>::kBytes);
   if (e != cudaSuccess) return e;
   a.TR = 8 * NT * M;
   a.RT = (a.R + a.TR - 1) / a.TR;
@@ -1074,7 +1107,7 @@ cudaError_t launch(DecodeArgs a, int64_t B, int num_sms, cudaStream_t stream) {
     if (a.lse) a.lse += b0 * a.Q * a.H;
     a.table += b0 * a.W;
     a.seq_lens += b0;
-    e = launch_pdl(kern, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, a);
+    e = launch_pdl(kern, dim3(num_sms), dim3(kThreads), Layout<NT>::kBytes, stream, a);
     if (e != cudaSuccess) return e;
     e = launch_pdl(fp8_join_kernel<Lists>, dim3(num_sms, a.TR / 2), dim3(256), 0, stream, a, num_sms);
     if (e != cudaSuccess) return e;
