@@ -1,14 +1,16 @@
 // block_topk: for each decode token the k blocks with the largest scores among its n visible ones,
 // the first and last few of them in any case; ties to the lower index, ascending, -1 padded.
 //
-// One CTA a token.  Scores become integers of the same order (score_key), those always taken the
-// largest.  Rows of up to 4096 blocks live in registers, consecutive blocks in a thread: the k-th
-// largest key is built from its top bit down, two bits a round, counting the keys that reach each of
-// three candidates; the start is the keys' common prefix.  One scan over the threads then gives
-// every taken block its place.  Longer rows are cut to the keys that matter first: a histogram over
-// equal steps of the score between the row's smallest and largest finds the step that holds the
-// k-th, and only that step's keys are searched, in shared memory.
-// Bound: latency (a row of 1024 scores is 4 KB).
+// A CTA a token, or a cluster of eight where a row has more than 4096 blocks.  Scores become integers
+// of the same order (score_key), those always taken the largest, and stay in registers, consecutive
+// blocks in a thread.  The k-th largest key is found byte by byte from the top: a histogram of the
+// keys that still match in shared memory (a cluster adds up its CTAs' histograms through distributed
+// shared memory, every CTA for itself), and the byte at which the count from above reaches k.  One
+// scan over the threads (and the CTAs' counts) then gives every taken block its place.
+// Bound: latency.  A row of 1024 scores is 4 KB; one of 65536 took a single CTA that went through it
+// five times 80 us.
+#include <cooperative_groups.h>
+
 #include "score_pipeline.cuh"
 
 namespace mx4 {
@@ -27,23 +29,6 @@ struct TopArgs {
 constexpr uint32_t kAlways = 0xFFFFFFFFu;  // above every score's key
 
 __device__ __forceinline__ uint32_t order_key(float x) { return x != x ? kNanKey : score_key(x); }
-
-// Sum over the CTA of a value whose total stays below 2^32, in every thread.
-template <int THREADS>
-__device__ __forceinline__ uint32_t cta_sum(uint32_t v, uint32_t* buf, int& turn) {
-  v = __reduce_add_sync(0xFFFFFFFFu, v);
-  uint32_t* const b = buf + (turn ^= 1) * (THREADS / 32);
-  if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
-  __syncthreads();
-  uint32_t s = 0;
-  if (THREADS <= 256) {
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) s += b[i];
-  } else {
-    s = __reduce_add_sync(0xFFFFFFFFu, b[threadIdx.x & (THREADS / 32 - 1)]);
-  }
-  return s;
-}
 
 // Exclusive prefix of a packed pair over the CTA's threads.
 template <int THREADS>
@@ -67,219 +52,91 @@ __device__ __forceinline__ uint64_t cta_prefix(uint64_t v, uint64_t* buf, uint64
   return before;
 }
 
-// The largest key that at least `want` (>= 1) of the CTA's keys reach, and how many exceed it.
-// get(i) for i < PER are the thread's keys; keys of 0 stand for none.
-template <int THREADS, int PER, class Get>
-__device__ __forceinline__ uint32_t kth_key(Get get, uint32_t want, uint32_t* buf, int& turn, uint32_t* above) {
-  uint32_t key = 0, over = 0;  // over: keys above the candidates with this prefix
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t cand = key | (1u << bit);
-    uint32_t c = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) c += get(i) >= cand;
-    c = cta_sum<THREADS>(c, buf, turn);
-    if (c >= want) key = cand; else over = c;
-  }
-  *above = over;
-  return key;
-}
-
-template <int THREADS, int PER>
+template <int THREADS, int PER, int CL>
 __global__ void __launch_bounds__(THREADS) block_topk_kernel(const TopArgs a) {
-  __shared__ uint32_t buf[2 * (THREADS / 32)];
+  namespace cg = cooperative_groups;
+  __shared__ uint32_t hist[2][256];
   __shared__ uint64_t buf64[THREADS / 32];
-  const int64_t t = blockIdx.x;
-  const int tid = threadIdx.x;
-  int turn = 0;
+  __shared__ uint32_t byte_s, above_s;
+  __shared__ uint64_t count_s;  // of this CTA: keys above the k-th, and equal to it
+  const int64_t t = blockIdx.x / CL;
+  const int tid = threadIdx.x, rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t L = a.seq_lens[t / a.Q], p = L - a.Q + t % a.Q;
+  const int64_t s = t / a.Q, L = a.seq_lens[s], p = L - a.Q + (t - s * a.Q);
   int32_t* const out = a.idx + t * a.k;
   int n = p >= 0 ? (int)(p / kPageTokens) + 1 : 0;
   if (L < 0 || n > a.ld) {
-    if (tid == 0) flag(a.status, MX4_STATUS_BAD_LEN);
+    if (tid == 0 && rank == 0) flag(a.status, MX4_STATUS_BAD_LEN);
     n = 0;
   }
   const int k = min(a.k, n);
-  for (int i = k + tid; i < a.k; i += THREADS) out[i] = -1;
-  if (k == n) {
-    for (int i = tid; i < n; i += THREADS) out[i] = i;
+  const int me = rank * THREADS + tid;
+  for (int i = k + me; i < a.k; i += CL * THREADS) out[i] = -1;
+  if (k == n) {  // (all CTAs of the cluster alike)
+    for (int i = me; i < n; i += CL * THREADS) out[i] = i;
     return;
   }
   const float* const x = a.scores + t * a.ld;
   uint32_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int b = tid * PER + i;
+    const int b = me * PER + i;
     key[i] = b >= n ? 0u : b < a.first || b >= n - a.last ? kAlways : order_key(x[b]);
   }
-  uint32_t above;
-  const uint32_t kth = kth_key<THREADS, PER>([&](int i) { return key[i]; }, k, buf, turn, &above);
+  uint32_t kth = 0, above = 0;  // keys that match kth's known bytes come after `above` larger ones
+#pragma unroll
+  for (int round = 0; round < 4; ++round) {
+    const int shift = 24 - 8 * round;
+    uint32_t* const h = hist[round & 1];
+    if (tid < 256) h[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)  // (a key of 0 is none)
+      if (key[i] != 0u && (round == 0 || (key[i] >> (shift + 8)) == (kth >> (shift + 8))))
+        atomicAdd(&h[(key[i] >> shift) & 255u], 1u);
+    // the histogram before the last one is read by no CTA any more once all are here
+    if (CL > 1) cg::this_cluster().sync(); else __syncthreads();
+    uint32_t c = 0;  // thread i has byte 255 - i
+    if (tid < 256) {
+      if (CL > 1) {
+#pragma unroll
+        for (int r = 0; r < CL; ++r) c += *cg::this_cluster().map_shared_rank(&h[255 - tid], r);
+      } else {
+        c = h[255 - tid];
+      }
+    }
+    uint64_t total;
+    const uint32_t before = above + (uint32_t)cta_prefix<THREADS>(c, buf64, &total);
+    if (before < (uint32_t)k && before + c >= (uint32_t)k) {  // one thread
+      byte_s = 255 - tid;
+      above_s = before;
+    }
+    __syncthreads();
+    kth |= byte_s << shift;
+    above = above_s;
+  }
   uint64_t mine = 0, total;  // keys above the k-th, and equal to it
 #pragma unroll
   for (int i = 0; i < PER; ++i) mine += (key[i] > kth ? 1ull << 32 : 0ull) + (key[i] == kth ? 1ull : 0ull);
-  const uint64_t before = cta_prefix<THREADS>(mine, buf64, &total);
+  uint64_t before = cta_prefix<THREADS>(mine, buf64, &total);
+  if (CL > 1) {
+    if (tid == 0) count_s = total;
+    cg::this_cluster().sync();
+    for (int r = 0; r < rank; ++r) before += *cg::this_cluster().map_shared_rank(&count_s, r);
+  }
   const uint32_t ties = k - above;
   uint32_t gt = (uint32_t)(before >> 32), eq = (uint32_t)before;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const uint32_t at = gt + min(eq, ties);
-    if (key[i] > kth || (key[i] == kth && eq < ties)) out[at] = tid * PER + i;
+    if (key[i] > kth || (key[i] == kth && eq < ties)) out[gt + min(eq, ties)] = me * PER + i;
     gt += key[i] > kth;
     eq += key[i] == kth;
   }
+  if (CL > 1) cg::this_cluster().sync();  // no CTA ends while another reads its counts
 }
 
-// Rows of more than 4096 blocks.
-constexpr int kBins = 4096;
-constexpr int kLongThreads = 1024;
-constexpr int kCands = 8192;  // keys of the step that holds the k-th (more: all keys are searched)
-struct LongSmem {
-  uint32_t hist[kBins];
-  uint32_t cand[kCands];
-  uint32_t buf[2 * (kLongThreads / 32)];
-  uint64_t buf64[kLongThreads / 32];
-  float lo[kLongThreads / 32], hi[kLongThreads / 32];
-  uint32_t n_cand, bin, above;
-};
-
-__global__ void __launch_bounds__(kLongThreads) block_topk_long_kernel(const TopArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  LongSmem& s = *reinterpret_cast<LongSmem*>(smem);
-  const int64_t t = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int turn = 0;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t L = a.seq_lens[t / a.Q], p = L - a.Q + t % a.Q;
-  int32_t* const out = a.idx + t * a.k;
-  int n = p >= 0 ? (int)(p / kPageTokens) + 1 : 0;
-  if (L < 0 || n > a.ld) {
-    if (tid == 0) flag(a.status, MX4_STATUS_BAD_LEN);
-    n = 0;
-  }
-  const int k = min(a.k, n);
-  for (int i = k + tid; i < a.k; i += kLongThreads) out[i] = -1;
-  if (k == n) {
-    for (int i = tid; i < n; i += kLongThreads) out[i] = i;
-    return;
-  }
-  const float* const x = a.scores + t * a.ld;
-  auto key_of = [&](int b) { return b < a.first || b >= n - a.last ? kAlways : order_key(x[b]); };
-
-  // ---- the range of the finite scores
-  float lo = INFINITY, hi = -INFINITY;
-  for (int i = tid; i < kBins; i += kLongThreads) s.hist[i] = 0;
-#pragma unroll 8
-  for (int b = tid; b < n; b += kLongThreads) {
-    const float v = x[b];
-    if (isfinite(v)) {
-      lo = fminf(lo, v);
-      hi = fmaxf(hi, v);
-    }
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, d));
-    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, d));
-  }
-  if (lane == 0) {
-    s.lo[warp] = lo;
-    s.hi[warp] = hi;
-  }
-  if (tid == 0) s.n_cand = 0;
-  __syncthreads();
-  lo = s.lo[lane];
-  hi = s.hi[lane];
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, d));
-    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, d));
-  }
-  // a step's number never falls as the key grows: both are monotone in the score
-  const float w = hi > lo ? (float)(kBins - 3) / (hi - lo) : 0.f;
-  auto bin_of = [&](float v) {
-    if (v != v || v == INFINITY) return kBins - 1;
-    if (v == -INFINITY) return 0;
-    const float f = (v - lo) * w;  // (a range beyond fp32, or one too small to divide by, is one step)
-    return 1 + (f < (float)(kBins - 3) ? (int)f : kBins - 3);
-  };
-  auto bin_at = [&](int b) { return b < a.first || b >= n - a.last ? kBins - 1 : bin_of(x[b]); };
-#pragma unroll 4
-  for (int b = tid; b < n; b += kLongThreads) atomicAdd(&s.hist[bin_at(b)], 1u);
-  __syncthreads();
-
-  // ---- the step that holds the k-th: thread i has steps 4 i .. 4 i + 3 counted from the top
-  {
-    uint32_t c[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum += c[i] = s.hist[kBins - 1 - (4 * tid + i)];
-    uint64_t total;
-    uint32_t before = (uint32_t)cta_prefix<kLongThreads>(sum, s.buf64, &total);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (before < (uint32_t)k && before + c[i] >= (uint32_t)k) {
-        s.bin = kBins - 1 - (4 * tid + i);
-        s.above = before;
-      }
-      before += c[i];
-    }
-  }
-  __syncthreads();
-  const int bin = s.bin;
-  const uint32_t over = s.above, held = s.hist[bin];
-
-  // ---- the k-th key
-  uint32_t kth, above;
-  if (held <= kCands) {
-#pragma unroll 4
-    for (int b = tid; b < n; b += kLongThreads)
-      if (bin_at(b) == bin) s.cand[atomicAdd(&s.n_cand, 1u)] = key_of(b);
-    __syncthreads();
-    uint32_t key[kCands / kLongThreads];
-#pragma unroll
-    for (int i = 0; i < kCands / kLongThreads; ++i)
-      key[i] = i * kLongThreads + tid < (int)held ? s.cand[i * kLongThreads + tid] : 0u;
-    kth = kth_key<kLongThreads, kCands / kLongThreads>([&](int i) { return key[i]; }, k - over, s.buf, turn, &above);
-    above += over;
-  } else {
-    kth = 0, above = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t cand = kth | (1u << bit);
-      uint32_t c = 0;
-#pragma unroll 4
-      for (int b = tid; b < n; b += kLongThreads) c += key_of(b) >= cand;
-      c = cta_sum<kLongThreads>(c, s.buf, turn);
-      if (c >= (uint32_t)k) kth = cand; else above = c;
-    }
-  }
-
-  // ---- taken blocks to their places, a tile of 4 a thread at a time
-  const uint32_t ties = k - above;
-  uint32_t gt0 = 0, eq0 = 0;
-  for (int base = 0; base < n && gt0 + min(eq0, ties) < (uint32_t)k; base += 4 * kLongThreads) {
-    uint32_t key[4];
-    uint64_t mine = 0, total;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = base + 4 * tid + i;
-      key[i] = b < n ? key_of(b) : 0u;
-      if (b < n) mine += (key[i] > kth ? 1ull << 32 : 0ull) + (key[i] == kth ? 1ull : 0ull);
-    }
-    const uint64_t before = cta_prefix<kLongThreads>(mine, s.buf64, &total);
-    uint32_t gt = gt0 + (uint32_t)(before >> 32), eq = eq0 + (uint32_t)before;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = base + 4 * tid + i;
-      if (b >= n) break;
-      if (key[i] > kth || (key[i] == kth && eq < ties)) out[gt + min(eq, ties)] = b;
-      gt += key[i] > kth;
-      eq += key[i] == kth;
-    }
-    gt0 += (uint32_t)(total >> 32);
-    eq0 += (uint32_t)total;
-  }
-}
+constexpr int kCluster = 8;
 
 }  // namespace
 
@@ -288,12 +145,20 @@ cudaError_t launch_block_topk(const float* scores, int64_t ld, const int32_t* se
                               cudaStream_t stream) {
   const TopArgs a{scores, ld, seq_lens, q, k, first, last, idx, status};
   const dim3 grid((unsigned)T);
-  if (ld <= 1024) return launch_pdl(block_topk_kernel<256, 4>, grid, dim3(256), 0, stream, a);
-  if (ld <= 4096) return launch_pdl(block_topk_kernel<256, 16>, grid, dim3(256), 0, stream, a);
-  cudaError_t e = cudaFuncSetAttribute(block_topk_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(LongSmem));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(block_topk_long_kernel, grid, dim3(kLongThreads), sizeof(LongSmem), stream, a);
+  if (ld <= 1024) return launch_pdl(block_topk_kernel<256, 4, 1>, grid, dim3(256), 0, stream, a);
+  if (ld <= 4096) return launch_pdl(block_topk_kernel<256, 16, 1>, grid, dim3(256), 0, stream, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(T * kCluster));
+  cfg.blockDim = dim3(512);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {kCluster, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, block_topk_kernel<512, 16, kCluster>, a);
 }
 
 }  // namespace mx4
