@@ -7,10 +7,15 @@
 // any size keep all bits that an fp32 angle in [-pi, pi) holds.
 //
 // Store.  A block of 32 cached tokens of a head shares the scale 2^E, the smallest with
-// amax <= 448 2^E (no value saturates), E >= -127.  One warp, or four where a sequence brings eight
-// new tokens or more on average (one warp goes through 32 rows twice: once for the largest, once to
-// store), takes the new rows of one block of K or V.  Where E grows the block's stored codes are
-// rounded to the new scale.  A power of two moves E4M3's normal values without rounding.
+// amax <= 448 2^E (no value saturates), E >= -127.  Where E grows the block's stored codes are rounded
+// to the new scale (a power of two moves E4M3's normal values without rounding).
+//
+// Work.  A decode step (fewer than eight new tokens a sequence on average): a warp a token and KV
+// head, K and V, whose rows are on their way before the sequence is looked up.  Prompts: four warps a
+// block of 32 tokens, K or V, four heads one after another, so that the sines of a token are computed
+// once for four heads (for each head they took 50 us of 136 with 13600 tokens of 8 + 40 heads).  q: a
+// warp a token and 8 to 32 heads.  A lane computes the sines of two of its four dims; its partner in
+// the pair has the others.
 //
 // Bound: latency for a decode batch, HBM for prompts.
 #include <cuda_fp8.h>
@@ -44,11 +49,13 @@ struct AppendArgs {
   uint8_t* ks;
   uint8_t* vs;
   uint16_t* q_out;
-  int64_t kv_tasks;  // (tokens, head, K or V); the q tasks (token, 8 heads) follow
+  int64_t kv_ctas;   // the q tasks (token, q_heads heads) follow them
+  int q_heads;
   uint32_t* status;
 };
 
-constexpr int kQHeads = 8;  // heads that share a token's sines
+constexpr int kQBatch = 8;   // q rows in flight
+constexpr int kKvHeads = 4;  // heads of a prompt's block, one after another
 
 template <typename E>
 __device__ __forceinline__ float4 load4(const E* p);
@@ -84,27 +91,42 @@ struct Turn {
 };
 __device__ __forceinline__ Turn turn_of(const AppendArgs& a, int64_t pos, int lane) {
   Turn t;
-  const int half = a.R / 2;
+  const int to = a.R / 8;  // neighbours: pairs 2 l, 2 l + 1.  halves: lanes l and l + R / 8, pairs 4 l .. 4 l + 3
+  const bool in = 4 * lane < a.R, upper = lane >= to;
+  const int i0 = a.interleaved ? 2 * lane : 4 * (upper ? lane - to : lane) + (upper ? 2 : 0);
+  float c[2], s[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int d = 4 * lane + e;
-    t.c[e] = 1.f;
-    t.s[e] = 0.f;
-    if (d < a.R) {
-      const int i = a.interleaved ? d >> 1 : d < half ? d : d - half;
-      const bool upper = a.interleaved ? d & 1 : d >= half;
-      const int32_t turns = (int32_t)(((uint64_t)pos * a.phases[i]) >> 32);  // of 2^-32
-      float s, c;
-      sincospif((float)turns * 0x1p-31f, &s, &c);
-      t.c[e] = c * a.factor;
-      t.s[e] = upper ? s * a.factor : -s * a.factor;
+  for (int e = 0; e < 2; ++e) {
+    c[e] = 1.f;
+    s[e] = 0.f;
+    if (in) {
+      const int32_t turns = (int32_t)(((uint64_t)pos * a.phases[i0 + e]) >> 32);  // of 2^-32
+      sincospif((float)turns * 0x1p-31f, &s[e], &c[e]);
+      c[e] *= a.factor;
+      s[e] *= a.factor;
+    }
+  }
+  if (a.interleaved) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      t.c[e] = c[e >> 1];
+      t.s[e] = (e & 1) ? s[e >> 1] : -s[e >> 1];
+    }
+  } else {
+    const int other = !in ? lane : upper ? lane - to : lane + to;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float oc = __shfl_sync(0xFFFFFFFFu, c[e], other), os = __shfl_sync(0xFFFFFFFFu, s[e], other);
+      t.c[e] = upper ? oc : c[e];
+      t.c[2 + e] = upper ? c[e] : oc;
+      t.s[e] = upper ? os : -s[e];
+      t.s[2 + e] = upper ? s[e] : -os;
     }
   }
   return t;
 }
 
 __device__ __forceinline__ float4 turned(const AppendArgs& a, float4 x, const Turn& t, int lane) {
-  if (a.R == 0) return x;
   float4 y;  // the pair's other element
   if (a.interleaved) {
     y = make_float4(x.y, x.x, x.w, x.z);
@@ -152,56 +174,36 @@ __device__ __forceinline__ int scale_exponent(uint32_t bits) {
   return max(e, -127);
 }
 
-// The rows of one block: cnt new rows from token t on, at row `at` of the block, of K (which = 0)
-// or V of head h; NW warps together, this one the wig-th.
-template <typename E, int NW>
-__device__ __forceinline__ void store_block(const AppendArgs& a, int64_t t, int cnt, int64_t pos0, int64_t page,
-                                            int h, int which, int wig, int lane, uint32_t* top_s) {
-  constexpr int kBatch = 8;
-  const E* const src = which ? static_cast<const E*>(a.v) + t * a.v_stride : static_cast<const E*>(a.k) + t * a.k_stride;
-  const int64_t stride = which ? a.v_stride : a.k_stride;
-  uint8_t* const pages = (which ? a.v_pages : a.k_pages) + page * a.page_stride + (int64_t)h * a.head_stride;
-  const int at = (int)(pos0 % kSub), first = (int)(pos0 % kPageTokens);  // row of the block, of the page
-  uint8_t* const scale = (which ? a.vs : a.ks) + (page * a.Hkv + h) * kPageSubs + first / kSub;
-  float4 x[kBatch];
-  auto rows = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      x[i] = b + i < cnt ? load4<E>(src + (b + i) * stride + h * kHeadDim + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (which == 0 && a.R > 0) {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (b + i >= cnt) break;
-        x[i] = turned(a, x[i], turn_of(a, a.positions ? a.positions[t + b + i] : pos0 + b + i, lane), lane);
-      }
-    }
-  };
-  const int old = at ? (int)*scale : 0;
-  uint32_t top = 0;
-  bool bad = false;
-  for (int b = wig * kBatch; b < cnt; b += NW * kBatch) {
-    rows(b);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      top = max(top, max(max(finite_bits(x[i].x), finite_bits(x[i].y)), max(finite_bits(x[i].z), finite_bits(x[i].w))));
-      bad |= !(isfinite(x[i].x) && isfinite(x[i].y) && isfinite(x[i].z) && isfinite(x[i].w));
-    }
-  }
-  if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) flag(a.status, MX4_STATUS_BAD_VALUE);
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if (NW > 1) {
-    __syncthreads();  // the block before has read its maxima
-    if (lane == 0) top_s[wig] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NW; ++i) top = max(top, top_s[i]);
-  }
-  // stored rows keep their scale or get a larger one; a scale of NaN (255) counts as the smallest
+// Where a block's rows go: its first new row's place and scale in K's or V's pool.
+struct Block {
+  uint8_t* rows;   // the block's first row
+  uint8_t* scale;
+  int at;          // its first new row
+};
+__device__ __forceinline__ Block block_of(const AppendArgs& a, int64_t page, int64_t pos, int h, int which) {
+  Block b;
+  const int sub = (int)(pos % kPageTokens) / kSub;
+  b.at = (int)(pos % kSub);
+  b.rows = (which ? a.v_pages : a.k_pages) + page * a.page_stride + (int64_t)h * a.head_stride + sub * kSub * kFp8Row;
+  b.scale = (which ? a.vs : a.ks) + (page * a.Hkv + h) * kPageSubs + sub;
+  return b;
+}
+
+__device__ __forceinline__ uint32_t largest(float4 x) {
+  return max(max(finite_bits(x.x), finite_bits(x.y)), max(finite_bits(x.z), finite_bits(x.w)));
+}
+__device__ __forceinline__ bool all_finite(float4 x) {
+  return isfinite(x.x) && isfinite(x.y) && isfinite(x.z) && isfinite(x.w);
+}
+
+// The block's exponent from the largest new value's bits and the stored scale byte (a scale of NaN,
+// 255, counts as the smallest); rows stored before move to it, i0 of n threads.
+__device__ __forceinline__ int grow(const Block& b, uint32_t top, int old, int i0, int n) {
   const int e_old = old == 255 ? -127 : old - 127;
-  const int e = max(scale_exponent(top), at ? e_old : -127);
-  if (at && e > e_old) {
-    uint4* const p = reinterpret_cast<uint4*>(pages + (first - at) * kFp8Row);
-    for (int i = wig * 32 + lane; i < at * (kFp8Row / 16); i += NW * 32) {
+  const int e = max(scale_exponent(top), b.at ? e_old : -127);
+  if (b.at && e > e_old) {
+    uint4* const p = reinterpret_cast<uint4*>(b.rows);
+    for (int i = i0; i < b.at * (kFp8Row / 16); i += n) {
       uint4 w = p[i];
       w.x = e4m3x4_down(w.x, e - e_old);
       w.y = e4m3x4_down(w.y, e - e_old);
@@ -210,105 +212,205 @@ __device__ __forceinline__ void store_block(const AppendArgs& a, int64_t t, int 
       p[i] = w;
     }
   }
-  if (wig == 0 && lane == 0) *scale = (uint8_t)(e + 127);
-  const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e, e in [-127, 120]
-  for (int b = wig * kBatch; b < cnt; b += NW * kBatch) {
-    if (cnt > NW * kBatch) rows(b);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (b + i >= cnt) break;
-      float4 y = x[i];
-      y = make_float4(y.x * down, y.y * down, y.z * down, y.w * down);
-      uint32_t w = e4m3x4(y);
-      if (bad) {  // what is not finite is stored as NaN
-        if (!isfinite(x[i].x)) w |= 0x7Fu;
-        if (!isfinite(x[i].y)) w |= 0x7F00u;
-        if (!isfinite(x[i].z)) w |= 0x7F0000u;
-        if (!isfinite(x[i].w)) w |= 0x7F000000u;
-      }
-      *reinterpret_cast<uint32_t*>(pages + (first + b + i) * kFp8Row + 4 * lane) = w;
-    }
-  }
+  if (i0 == 0) *b.scale = (uint8_t)(e + 127);
+  return e;
 }
 
-// NW = 1: a warp a task, one token's chance to be its block's first new one.  NW = 4: a CTA a task,
-// 32 tokens.
-template <typename E, int NW>
-__global__ void __launch_bounds__(128) fp8_append_kernel(const AppendArgs a) {
-  constexpr int kTokens = NW == 1 ? 1 : 32;
-  __shared__ uint32_t top_s[4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t kv_ctas = NW == 1 ? (a.kv_tasks + 3) / 4 : a.kv_tasks;
-  if (blockIdx.x < kv_ctas) {
-    const int64_t task = NW == 1 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
-    if (task >= a.kv_tasks) return;
-    const int per = 2 * a.Hkv;
-    const int64_t chunk = task / per;
-    const int hw = (int)(task - chunk * per), h = hw >> 1, which = hw & 1;
-    const int64_t end = min(a.T, (chunk + 1) * kTokens);
-    for (int64_t t = chunk * kTokens; t < end;) {
-      const int s = sequence_of(a, t, lane);
-      if (s < 0) {  // before the first sequence, or behind the last
-        if (t >= a.cu[0]) return;
-        t = a.cu[0];
-        continue;
-      }
-      const int64_t t0 = a.cu[s], t1 = a.cu[s + 1], L = a.seq_lens[s];
-      if (t1 > a.T || L < t1 - t0 || L > a.W * kPageTokens) {
-        if (lane == 0) flag(a.status, MX4_STATUS_BAD_LEN);
-        t = t1;
-        continue;
-      }
-      const int64_t pos = L - (t1 - t);
-      const int cnt = (int)min(t1 - t, (int64_t)kSub - pos % kSub);
-      if (t == t0 || pos % kSub == 0) {
-        const int32_t page = a.table[s * a.W + pos / kPageTokens];
-        if (page >= 0 && page < a.num_pages)
-          store_block<E, NW>(a, t, cnt, pos, page, h, which, NW == 1 ? 0 : warp, lane, top_s);
-        else if (lane == 0)
-          flag(a.status, MX4_STATUS_BAD_PAGE);
-      }
-      t += cnt;
-    }
-    return;
+__device__ __forceinline__ void store_row(const Block& b, int row, float4 x, int e, int lane) {
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e, e in [-127, 120]
+  uint32_t w = e4m3x4(make_float4(x.x * down, x.y * down, x.z * down, x.w * down));
+  if (!isfinite(x.x)) w |= 0x7Fu;  // what is not finite is stored as NaN
+  if (!isfinite(x.y)) w |= 0x7F00u;
+  if (!isfinite(x.z)) w |= 0x7F0000u;
+  if (!isfinite(x.w)) w |= 0x7F000000u;
+  *reinterpret_cast<uint32_t*>(b.rows + (b.at + row) * kFp8Row + 4 * lane) = w;
+}
+
+// New tokens t .. of sequence s, from t on up to the end of their block: position, count, page (-1:
+// none).  false: t belongs to no sequence, or to one that is skipped; `next` is then where to go on.
+struct Span {
+  int64_t pos, page, t0;
+  int cnt;
+};
+__device__ __forceinline__ bool span_of(const AppendArgs& a, int64_t t, int lane, Span* sp, int64_t* next) {
+  const int s = sequence_of(a, t, lane);
+  if (s < 0) {  // before the first sequence, or behind the last
+    const int64_t first = a.cu[0];
+    *next = t < first ? first : a.T;
+    return false;
   }
-  const int per = (a.H + kQHeads - 1) / kQHeads;
-  const int64_t task = (blockIdx.x - kv_ctas) * 4 + warp, t = task / per;
+  const int64_t t0 = a.cu[s], t1 = a.cu[s + 1], L = a.seq_lens[s];
+  if (t1 > a.T || L < t1 - t0 || L > a.W * kPageTokens) {
+    if (lane == 0) flag(a.status, MX4_STATUS_BAD_LEN);
+    *next = t1;
+    return false;
+  }
+  sp->t0 = t0;
+  sp->pos = L - (t1 - t);
+  sp->cnt = (int)min(t1 - t, (int64_t)kSub - sp->pos % kSub);
+  const int32_t page = a.table[s * a.W + sp->pos / kPageTokens];
+  sp->page = page >= 0 && page < a.num_pages ? page : -1;
+  *next = t + sp->cnt;
+  return true;
+}
+
+template <typename E>
+__device__ __forceinline__ void turn_q(const AppendArgs& a, int64_t task, int lane) {
+  const int per = (a.H + a.q_heads - 1) / a.q_heads;
+  const int64_t t = task / per;
   if (t >= a.T) return;
+  const int h0 = (int)(task - t * per) * a.q_heads, h1 = min(h0 + a.q_heads, a.H);
+  const E* const src = static_cast<const E*>(a.q) + t * a.q_stride + 4 * lane;
+  uint16_t* const dst = a.q_out + t * a.H * kHeadDim + 4 * lane;
+  float4 x[kQBatch];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < kQBatch; ++i)
+      x[i] = h + i < h1 ? load4<E>(src + (h + i) * kHeadDim) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  load(h0);  // (ahead of the look-up)
   const int s = sequence_of(a, t, lane);
   if (s < 0) return;
   const int64_t t1 = a.cu[s + 1], L = a.seq_lens[s];
   if (t1 > a.T || L < t1 - a.cu[s] || L > a.W * kPageTokens) return;  // (reported with its K)
   Turn turn;
   if (a.R > 0) turn = turn_of(a, a.positions ? a.positions[t] : L - (t1 - t), lane);
-  const int h0 = (int)(task - t * per) * kQHeads;
-  const E* const src = static_cast<const E*>(a.q) + t * a.q_stride + 4 * lane;
-  uint16_t* const dst = a.q_out + t * a.H * kHeadDim + 4 * lane;
-  float4 x[kQHeads];
+  for (int h = h0; h < h1; h += kQBatch) {
+    if (h > h0) load(h);
 #pragma unroll
-  for (int i = 0; i < kQHeads; ++i)
-    x[i] = h0 + i < a.H ? load4<E>(src + (h0 + i) * kHeadDim) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < kQHeads; ++i) {
-    if (h0 + i >= a.H) break;
-    const float4 y = turned(a, x[i], turn, lane);
-    uint2 w;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(y.y), "f"(y.x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(y.w), "f"(y.z));
-    *reinterpret_cast<uint2*>(dst + (h0 + i) * kHeadDim) = w;
+    for (int i = 0; i < kQBatch; ++i) {
+      if (h + i >= h1) break;
+      const float4 y = a.R > 0 ? turned(a, x[i], turn, lane) : x[i];
+      uint2 w;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(y.y), "f"(y.x));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(y.w), "f"(y.z));
+      *reinterpret_cast<uint2*>(dst + (h + i) * kHeadDim) = w;
+    }
   }
 }
 
+// A decode step: a warp a new token and KV head.  The first new token of a block takes the others of
+// its sequence in the block with it, two sweeps over them if there are any.
 template <typename E>
-cudaError_t launch(AppendArgs a, cudaStream_t stream) {
-  const bool wide = a.T >= 8 * (int64_t)a.B;
-  const int64_t q_ctas = a.q ? (a.T * ((a.H + kQHeads - 1) / kQHeads) + 3) / 4 : 0;
-  a.kv_tasks = (wide ? (a.T + 31) / 32 : a.T) * 2 * a.Hkv;
-  const int64_t grid = (wide ? a.kv_tasks : (a.kv_tasks + 3) / 4) + q_ctas;
-  return launch_pdl(wide ? fp8_append_kernel<E, 4> : fp8_append_kernel<E, 1>, dim3((unsigned)grid), dim3(128), 0,
-                    stream, a);
+__global__ void __launch_bounds__(128) fp8_append_step_kernel(const AppendArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (blockIdx.x >= a.kv_ctas) return turn_q<E>(a, (blockIdx.x - a.kv_ctas) * 4 + warp, lane);
+  const int64_t task = (int64_t)blockIdx.x * 4 + warp, t = task / a.Hkv;
+  if (t >= a.T) return;
+  const int h = (int)(task - t * a.Hkv);
+  const E* const src[2] = {static_cast<const E*>(a.k) + t * a.k_stride + h * kHeadDim + 4 * lane,
+                           static_cast<const E*>(a.v) + t * a.v_stride + h * kHeadDim + 4 * lane};
+  const int64_t stride[2] = {a.k_stride, a.v_stride};
+  const float4 first[2] = {load4<E>(src[0]), load4<E>(src[1])};  // (ahead of the look-up)
+  Span sp;
+  int64_t next;
+  if (!span_of(a, t, lane, &sp, &next)) return;
+  if (t != sp.t0 && sp.pos % kSub != 0) return;  // its block's first new token has it
+  if (sp.page < 0) {
+    if (lane == 0) flag(a.status, MX4_STATUS_BAD_PAGE);
+    return;
+  }
+  auto row = [&](int which, int r) {
+    float4 x = r == 0 ? first[which] : load4<E>(src[which] + r * stride[which]);
+    if (which == 0 && a.R > 0) x = turned(a, x, turn_of(a, a.positions ? a.positions[t + r] : sp.pos + r, lane), lane);
+    return x;
+  };
+  bool ok = true;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const Block b = block_of(a, sp.page, sp.pos, h, which);
+    const int old = b.at ? (int)*b.scale : 0;
+    float4 x = row(which, 0);
+    uint32_t top = largest(x);
+    ok &= all_finite(x);
+    for (int r = 1; r < sp.cnt; ++r) {
+      const float4 y = row(which, r);
+      top = max(top, largest(y));
+      ok &= all_finite(y);
+    }
+    const int e = grow(b, __reduce_max_sync(0xFFFFFFFFu, top), old, lane, 32);
+    store_row(b, 0, x, e, lane);
+    for (int r = 1; r < sp.cnt; ++r) store_row(b, r, row(which, r), e, lane);
+  }
+  if (!__all_sync(0xFFFFFFFFu, ok) && lane == 0) flag(a.status, MX4_STATUS_BAD_VALUE);
+}
+
+// Prompts: a CTA 32 new tokens, K or V, kKvHeads heads; a warp eight rows of a block.
+template <typename E>
+__global__ void __launch_bounds__(128) fp8_append_kernel(const AppendArgs a) {
+  __shared__ uint32_t top_s[2][4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (blockIdx.x >= a.kv_ctas) return turn_q<E>(a, (blockIdx.x - a.kv_ctas) * 4 + warp, lane);
+  const int groups = (a.Hkv + kKvHeads - 1) / kKvHeads;
+  const int64_t chunk = blockIdx.x / (2 * groups);
+  const int rest = (int)(blockIdx.x - chunk * 2 * groups), which = rest & 1;
+  const int h0 = (rest >> 1) * kKvHeads, h1 = min(h0 + kKvHeads, a.Hkv);
+  const int64_t stride = which ? a.v_stride : a.k_stride, end = min(a.T, (chunk + 1) * 32);
+  bool ok = true;
+  int turn_no = 0;
+  for (int64_t t = chunk * 32, next; t < end; t = next) {
+    Span sp;
+    if (!span_of(a, t, lane, &sp, &next)) continue;
+    if (t != sp.t0 && sp.pos % kSub != 0) continue;  // (the chunk before has this block)
+    if (sp.page < 0) {
+      if (threadIdx.x == 0) flag(a.status, MX4_STATUS_BAD_PAGE);
+      continue;
+    }
+    const int r0 = warp * 8, rows = min(8, sp.cnt - r0);  // of this warp
+    Turn turn[8];
+    const bool turns = which == 0 && a.R > 0;
+    if (turns) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < rows) turn[i] = turn_of(a, a.positions ? a.positions[t + r0 + i] : sp.pos + r0 + i, lane);
+    }
+    const E* const src =
+        (which ? static_cast<const E*>(a.v) : static_cast<const E*>(a.k)) + (t + r0) * stride + 4 * lane;
+    for (int h = h0; h < h1; ++h) {
+      const Block b = block_of(a, sp.page, sp.pos, h, which);
+      const int old = b.at ? (int)*b.scale : 0;
+      float4 x[8];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = i < rows ? load4<E>(src + i * stride + h * kHeadDim) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= rows) break;
+        if (turns) x[i] = turned(a, x[i], turn[i], lane);
+        top = max(top, largest(x[i]));
+        ok &= all_finite(x[i]);
+      }
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      uint32_t* const ts = top_s[turn_no++ & 1];
+      if (lane == 0) ts[warp] = top;
+      __syncthreads();  // (and all have read the stored scale; the next block's maxima go to the other row)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, ts[i]);
+      const int e = grow(b, top, old, threadIdx.x, 128);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= rows) break;
+        store_row(b, r0 + i, x[i], e, lane);
+      }
+    }
+  }
+  if (!__all_sync(0xFFFFFFFFu, ok) && lane == 0) flag(a.status, MX4_STATUS_BAD_VALUE);
+}
+
+template <typename E>
+cudaError_t launch(AppendArgs a, int num_sms, cudaStream_t stream) {
+  const bool prompts = a.T >= 8 * (int64_t)a.B;
+  a.kv_ctas = prompts ? (a.T + 31) / 32 * 2 * ((a.Hkv + kKvHeads - 1) / kKvHeads) : (a.T * a.Hkv + 3) / 4;
+  // more heads a q warp once there are warps enough: the sines are computed once for them
+  a.q_heads = kQBatch;
+  while (a.q_heads < 32 && a.q_heads < a.H && a.T * a.H / a.q_heads > 32 * (int64_t)num_sms) a.q_heads *= 2;
+  const int64_t q_ctas = a.q ? (a.T * ((a.H + a.q_heads - 1) / a.q_heads) + 3) / 4 : 0;
+  return launch_pdl(prompts ? fp8_append_kernel<E> : fp8_append_step_kernel<E>,
+                    dim3((unsigned)(a.kv_ctas + q_ctas)), dim3(128), 0, stream, a);
 }
 
 }  // namespace
@@ -319,11 +421,11 @@ cudaError_t launch_fp8_append(const void* q, const void* k, const void* v, int f
                               float factor, const int32_t* table, int64_t W, const int32_t* seq_lens,
                               uint8_t* k_pages, uint8_t* v_pages, int64_t page_stride, int64_t head_stride,
                               int64_t num_pages, uint8_t* k_scales, uint8_t* v_scales, uint16_t* q_out,
-                              uint32_t* status, cudaStream_t stream) {
+                              uint32_t* status, int num_sms, cudaStream_t stream) {
   AppendArgs a{q, k, v, strides[0], strides[1], strides[2], T, H, Hkv, cu, (int)B, positions,
                reinterpret_cast<const uint64_t*>(phases), rot, interleaved, factor, table, W, seq_lens,
-               k_pages, v_pages, page_stride, head_stride, num_pages, k_scales, v_scales, q_out, 0, status};
-  return fp32 ? launch<float>(a, stream) : launch<uint16_t>(a, stream);
+               k_pages, v_pages, page_stride, head_stride, num_pages, k_scales, v_scales, q_out, 0, 0, status};
+  return fp32 ? launch<float>(a, num_sms, stream) : launch<uint16_t>(a, num_sms, stream);
 }
 
 }  // namespace mx4

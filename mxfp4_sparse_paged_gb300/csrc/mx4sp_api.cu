@@ -70,7 +70,7 @@ cudaError_t launch_fp8_append(const void*, const void*, const void*, int, const 
                               int, int, const int32_t*, int64_t, const int64_t*, const int64_t*,
                               int, int, float, const int32_t*, int64_t, const int32_t*, uint8_t*,
                               uint8_t*, int64_t, int64_t, int64_t, uint8_t*, uint8_t*, uint16_t*,
-                              uint32_t*, cudaStream_t);
+                              uint32_t*, int, cudaStream_t);
 cudaError_t launch_fp8_decode(const uint16_t*, int64_t, int, int, int, const uint8_t*,
                               const uint8_t*, const uint8_t*, const uint8_t*, int64_t, int64_t,
                               int64_t, const int32_t*, int64_t, const int32_t*, const int32_t*,
@@ -1186,7 +1186,7 @@ extern "C" int fp8_rope_append(const void* q, int64_t q_stride, const void* k, i
       mx4::launch_fp8_append(q, k, v, fp32 ? 1 : 0, strides, T, H, Hkv, cu_new, B, positions,
                              phases, rot, interleaved ? 1 : 0, factor, block_table, bt_width,
                              seq_lens, k_pages, v_pages, kv_page_stride, kv_head_stride, num_pages,
-                             k_scales, v_scales, q_out, d->status,
+                             k_scales, v_scales, q_out, d->status, d->num_sms,
                              static_cast<cudaStream_t>(stream)),
       kName);
 }
