@@ -209,7 +209,13 @@ cudaError_t launch_index_score_fp8(const uint16_t* iq, int q, const uint8_t* pag
   }
 }
 
-// index_block_score_fp8: the largest score of each page (block mode of the pipeline).
+// index_block_score_fp8: the largest score of each page (block mode of the pipeline, a warp a page).
+struct Fp8Blocks : Fp8Fmt {
+  static constexpr int kConsumers = 3;
+  static constexpr int kStages = 6;
+  static constexpr int kEmptyCount = 1;
+};
+
 cudaError_t launch_index_block_score_fp8(const uint16_t* iq, int q, const uint8_t* pages,
                                          int64_t page_stride, int64_t num_pages,
                                          const int32_t* block_table, int B, int64_t bt_width,
@@ -218,7 +224,7 @@ cudaError_t launch_index_block_score_fp8(const uint16_t* iq, int q, const uint8_
                                          cudaStream_t stream) {
   const ScoreArgs a{iq, pages, page_stride, num_pages, block_table, B, bt_width, seq_lens,
                     scores, ld, status, scale};
-  return launch_score_q<Fp8Fmt, true>(q, a, num_sms, stream);
+  return launch_score_q<Fp8Blocks, true>(q, a, num_sms, stream);
 }
 
 }  // namespace mx4

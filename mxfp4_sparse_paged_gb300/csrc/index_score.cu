@@ -160,7 +160,14 @@ cudaError_t launch_index_score(const uint16_t* iq, int q, const uint8_t* idx_pag
   }
 }
 
-// index_block_score: the largest score of each page (block mode of the pipeline).
+// index_block_score: the largest score of each page (block mode of the pipeline, a warp a page).
+struct Mxfp4Blocks : Mxfp4Fmt {
+  static constexpr int kConsumers = 3;
+  static constexpr int kStages = 6;
+  static constexpr int kEmptyCount = 1;
+  static constexpr int ctas_per_sm(int Q) { return Q <= 4 ? 4 : 2; }
+};
+
 cudaError_t launch_index_block_score(const uint16_t* iq, int q, const uint8_t* idx_pages,
                                      int64_t idx_page_stride, int64_t num_pages,
                                      const int32_t* block_table, int B, int64_t bt_width,
@@ -168,7 +175,7 @@ cudaError_t launch_index_block_score(const uint16_t* iq, int q, const uint8_t* i
                                      uint32_t* status, int num_sms, cudaStream_t stream) {
   const ScoreArgs a{iq, idx_pages, idx_page_stride, num_pages, block_table, B, bt_width,
                     seq_lens, scores, ld, status, 1.f};
-  return launch_score_q<Mxfp4Fmt, true>(q, a, num_sms, stream);
+  return launch_score_q<Mxfp4Blocks, true>(q, a, num_sms, stream);
 }
 
 }  // namespace mx4

@@ -19,8 +19,9 @@
 // MX4_STATUS_TIMEOUT, stops, and drains the copies in flight before exiting.
 //
 // In block mode (Blocks) the scores stay in the kernel: a page's largest score for each query goes
-// out, scores[t][page], by an order-preserving integer maximum over lanes (one instruction), then
-// over the warps of the page in shared memory; the warp that comes last writes.
+// out, scores[t][page].  A warp takes a whole page, so that one order-preserving integer maximum over
+// its lanes a query and page (one instruction) is all that is added.  (Warps of one page meeting in
+// shared memory took 55 us for the 47 of this form on 256 ragged MXFP4 contexts.)
 //
 // A format whose tile math takes a whole page at once (kWholePage: the
 // block-scaled tensor-core scorer) gets a region of kExtraBytes of shared memory
@@ -70,7 +71,7 @@ struct ScoreArgs {
 
 // Shared-memory layout of the kernel, in bytes: format region | stages |
 // barriers | stage info | warp sums, flags | per-sequence page prefix [B].
-template <class F, int Q, bool Blocks = false>
+template <class F, int Q>
 struct ScoreLayout {
   static constexpr int kStageBytes =
       (F::kStageDataBytes + Q * kHeadDim * 2 + F::kStageAlign - 1) / F::kStageAlign * F::kStageAlign;
@@ -82,8 +83,7 @@ struct ScoreLayout {
   static constexpr int kInfoOff = kBarOff + 2 * F::kStages * 8;
   static constexpr int kWarpSumOff = kInfoOff + 4 * F::kStages * 4;
   static constexpr int kFlagOff = kWarpSumOff + 32 * 4;  // abort, issued
-  static constexpr int kKeyOff = (kFlagOff + 8 + 15) / 16 * 16;  // block mode: [S] keys of Q, count
-  static constexpr int kPrefOff = kKeyOff + (Blocks ? (F::kStages * (Q + 1) * 4 + 15) / 16 * 16 : 0);
+  static constexpr int kPrefOff = (kFlagOff + 8 + 15) / 16 * 16;
   // (plus the slack that aligns the dynamic shared memory to a stage alignment above 128)
   static size_t bytes(int B) {
     return (size_t)kPrefOff + (size_t)B * 4 + (F::kStageAlign > 128 ? F::kStageAlign : 0);
@@ -135,8 +135,11 @@ __device__ __forceinline__ PageRef resolve_page(const ScoreArgs& a, const int* p
 template <class F, int Q, bool Blocks = false>
 __global__ void __launch_bounds__((F::kConsumers + 1) * 32, F::ctas_per_sm(Q))
 score_kernel(const __grid_constant__ ScoreArgs a) {
-  using Lay = ScoreLayout<F, Q, Blocks>;
+  using Lay = ScoreLayout<F, Q>;
   constexpr int S = F::kStages, NC = F::kConsumers, NTHR = (NC + 1) * 32;
+  // (a warp that takes only some pages must own its stages: a parity tells a phase from the next, not
+  // from the one after, so rounds of a stage that go to different warps could be taken out of turn)
+  static_assert(!Blocks || S % NC == 0, "a stage's pages belong to one warp");
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   uint8_t* const smem_raw =
       F::kStageAlign > 128
@@ -199,9 +202,6 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
     *issued = 0;
     fence_barrier_init();
   }
-  uint32_t* const keys = reinterpret_cast<uint32_t*>(smem_raw + Lay::kKeyOff);
-  if constexpr (Blocks)
-    for (int i = tid; i < S * (Q + 1); i += NTHR) keys[i] = 0u;
   __syncthreads();
 
   const int total = B > 0 ? pref[B - 1] : 0;
@@ -272,7 +272,7 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
   } else {
     typename F::template Tile<Q> tile;
     int cur_seq = -1;
-    for (int kk = 0; kk < n; ++kk) {
+    for (int kk = Blocks ? warp : 0; kk < n; kk += Blocks ? NC : 1) {
       const int st = kk % S, round = kk / S;
       bool landed = false;
       for (uint32_t i = 0; i < kWaitPolls && !landed; ++i) {
@@ -316,32 +316,22 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
               a.scores[((int64_t)seq * Q + qq) * a.ld + i_g] = (i_g <= p) ? v : -INFINITY;
           }
         };
-#pragma unroll
-        for (int tt = 0; tt < kPageTokens / 16 / NC; ++tt)
-          tile.run(page, (warp + NC * tt) * 16, lane, emit);
         if constexpr (Blocks) {
-          uint32_t* const k = keys + st * (Q + 1);
+          for (int r0 = 0; r0 <= last0 + Q - 1 && r0 < kPageTokens; r0 += 16) tile.run(page, r0, lane, emit);
           uint32_t mine = 0u;
 #pragma unroll
           for (int qq = 0; qq < Q; ++qq) {
             const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best[qq]);
             if (lane == qq) mine = top;
           }
-          if (lane < Q) atomicMax(&k[lane], mine);
-          __threadfence_block();
-          __syncwarp();
-          uint32_t before = 0u;
-          if (lane == 0) before = atomicAdd(&k[Q], 1u);
-          if (__shfl_sync(0xFFFFFFFFu, before, 0) == NC - 1) {  // the page's last warp
-            __threadfence_block();
-            if (lane < Q) {
-              const uint32_t top = atomicExch(&k[lane], 0u);  // 0: the query sees nothing here
-              a.scores[((int64_t)seq * Q + lane) * a.ld + pg] = top ? key_score(top) : -INFINITY;
-            }
-            if (lane == 0) k[Q] = 0u;
-          }
+          if (lane < Q)  // 0: the query sees nothing here
+            a.scores[((int64_t)seq * Q + lane) * a.ld + pg] = mine ? key_score(mine) : -INFINITY;
+        } else {
+#pragma unroll
+          for (int tt = 0; tt < kPageTokens / 16 / NC; ++tt)
+            tile.run(page, (warp + NC * tt) * 16, lane, emit);
         }
-      } else if (Blocks && warp == 0 && lane < Q) {  // no page: no score
+      } else if (Blocks && lane < Q) {  // no page: no score
         a.scores[((int64_t)seq * Q + lane) * a.ld + pg] = -INFINITY;
       }
       __syncwarp();
@@ -383,7 +373,7 @@ inline cudaError_t resident_ctas(const void* kern, int threads, size_t smem, int
 // Launch over batches of at most kScoreMaxBatch sequences (the prefix array).
 template <class F, int Q, bool Blocks = false>
 cudaError_t launch_score(ScoreArgs a, int num_sms, cudaStream_t stream) {
-  using Lay = ScoreLayout<F, Q, Blocks>;
+  using Lay = ScoreLayout<F, Q>;
   auto kern = score_kernel<F, Q, Blocks>;
   const int B = a.B;
   const size_t smem = Lay::bytes(min(B, kScoreMaxBatch));
@@ -400,8 +390,7 @@ cudaError_t launch_score(ScoreArgs a, int num_sms, cudaStream_t stream) {
   // residency is taken from the SM's shared memory, registers and threads and the
   // kernel's own use of them.
   int resident = 0;
-  err = resident_ctas(reinterpret_cast<const void*>(kern), (F::kConsumers + 1) * 32, smem,
-                      &resident);
+  err = resident_ctas(reinterpret_cast<const void*>(kern), (F::kConsumers + 1) * 32, smem, &resident);
   if (err != cudaSuccess) return err;
   const int grid = num_sms * max(1, min(F::ctas_per_sm(Q), resident));
   for (int b0 = 0; b0 < B; b0 += kScoreMaxBatch) {

@@ -486,6 +486,36 @@ def test_block_scores_are_the_scorers_maxima(q, fp8):
     m.mx4_check_status()
 
 
+@pytest.mark.parametrize("fp8,q", [(False, 1), (False, 4), (True, 1), (True, 8)])
+def test_block_scores_of_many_pages(fp8, q):
+    """Every CTA goes round its ring many times (11000 pages), lengths ragged, three times over."""
+    g = torch.Generator().manual_seed(q)
+    lens = np.random.default_rng(q).integers(q, 11000, 256).tolist()
+    table, P = tables(g, lens)
+    iq = torch.randn((len(lens) * q, 128), generator=g).to(torch.bfloat16).to(DEV)
+    sl, td, W = torch.tensor(lens, dtype=torch.int32, device=DEV), table.to(DEV), table.shape[1]
+    sc = torch.full((len(lens) * q, W * 128), -math.inf, device=DEV)
+    gd = torch.Generator(DEV).manual_seed(q)
+    if fp8:
+        pages = torch.randn((P, 16384), generator=gd, device=DEV).mul_(100).to(E4M3).view(torch.uint8)
+        run = lambda f, out: f(iq, q, pages, td, sl, 0.03, out)
+        one, block = m.index_score_fp8, m.index_block_score_fp8
+    else:
+        pages = torch.randint(0, 256, (P, 8704), generator=gd, device=DEV, dtype=torch.uint8)
+        pages[:, 8192:] = torch.randint(115, 130, (P, 512), generator=gd, device=DEV, dtype=torch.uint8)
+        run = lambda f, out: f(iq, q, pages, td, sl, out)
+        one, block = m.index_score, m.index_block_score
+    run(one, sc)
+    want = sc.view(len(lens) * q, W, 128).amax(-1)
+    for _ in range(3):
+        bs = torch.full((len(lens) * q, W), -math.inf, device=DEV)
+        run(block, bs)
+        # (the fp8 rows hold a few NaN codes, values past the format: their blocks are NaN on both sides)
+        assert torch.equal(torch.isnan(bs), torch.isnan(want))
+        assert torch.equal(bs.nan_to_num(nan=0.0, neginf=-1e9), want.nan_to_num(nan=0.0, neginf=-1e9))
+    m.mx4_check_status()
+
+
 def test_block_scores_edges():
     """Sequences shorter than their queries, NaN scores, bad pages and lengths."""
     g = torch.Generator().manual_seed(0)
