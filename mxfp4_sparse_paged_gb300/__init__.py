@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -156,6 +157,8 @@ def _load():
                                          i64, P, P, i32, ctypes.c_float, P, P, P, sz, P]
         lib.fp8_block_decode_workspace.restype = sz
         lib.fp8_block_decode_workspace.argtypes = [i64, i32, i32, i32]
+        lib.mx4_call_words.restype = i32
+        lib.mx4_call_words.argtypes = [i32, ctypes.c_char_p]
         lib.mx4_check_status.restype = i32
         lib.mx4_check_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
         _lib = lib
@@ -781,37 +784,84 @@ def mx4_free_pages(tables, lens, ref_counts, free_list, free_count, stream=None)
 
 
 # ---- the 8-bit K/V cache
+#
+# Argument by argument a call of 30 took ctypes 8 us, so these go over as one array of words.  All
+# tensors of a call live on the current device, where it runs.
 
-def _one_device(*tensors):
-    """All of a call's CUDA tensors live on the current device (where the call runs)."""
-    seen = {t.get_device() for t in tensors if t is not None}
-    seen.discard(-1)  # a host tensor: refused with the call
-    if not seen:
-        return
-    here = torch.cuda.current_device()
-    if seen != {here}:
-        raise ValueError(f"the call runs on device {here}, its tensors are on {sorted(seen)}")
+def _words(which, layout):
+    return which, struct.Struct("=" + layout).pack
 
 
-def _fp8_kv_pools(k_pages, v_pages, k_scales, v_scales):
+_APPEND = _words(0, "16qd12q")
+_PAGED = _words(1, "16qd5q")
+_BLOCK = _words(2, "18qd5q")
+_TOPK = _words(3, "10q")
+_SCORE = _words(4, "13q")
+_SCORE_FP8 = _words(5, "10qd3q")
+
+
+def _call_words(how, *args):
+    try:
+        words = how[1](*args)
+    except struct.error:
+        for x in args:
+            if isinstance(x, _Host):
+                _ptr(x.t)
+        raise
+    rc = _load().mx4_call_words(how[0], words)
+    if rc != 0:
+        _check(rc)
+
+
+def _device() -> int:
+    try:
+        return torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError, AssertionError):  # no GPU, or not in this torch
+        return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
+def _address(t, dev, name):
+    """The address of a CUDA tensor of the current device."""
+    if t.get_device() == dev and dev >= 0:
+        return t.data_ptr()
+    if t.is_cuda:
+        raise ValueError(f"{name} is on device {t.get_device()}, the call runs on device {dev}")
+    return _Host(t)
+
+
+def _on(t, dtype, shape, name, dev):
+    """The address of a contiguous tensor of this type and shape (None sizes match)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0 and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, dtype, name)
+    _dims(t, name, *shape)
+    return _address(t, dev, name)
+
+
+def _stream_word(stream) -> int:
+    s = _stream(stream)
+    return 0 if s is None else s if type(s) is int else s.value or 0
+
+
+def _fp8_kv_pools(k_pages, v_pages, k_scales, v_scales, dev):
     """(K address, V address, page stride, head stride, pages), (scale addresses), KV heads."""
     s, st = k_pages.shape, k_pages.stride()
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if not (t.dtype is torch.uint8 and len(t.shape) == 3 and t.shape[2] == FP8_PAGE_BYTES and
-                t.stride(2) == 1):
+    if not (k_pages.dtype is torch.uint8 and v_pages.dtype is torch.uint8 and len(s) == 3 and
+            s[2] == FP8_PAGE_BYTES and st[2] == 1 and v_pages.shape == s and v_pages.stride() == st):
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
             _need(t, torch.uint8, name, contiguous=False)
-            raise ValueError(f"{name}: uint8 pages need shape [P, Hkv, {FP8_PAGE_BYTES}] with a "
-                             f"contiguous byte axis, got {tuple(t.shape)} strides {t.stride()}")
-    if v_pages.shape != s or v_pages.stride() != st:
+            if t.dim() != 3 or t.shape[2] != FP8_PAGE_BYTES or t.stride(2) != 1:
+                raise ValueError(f"{name}: uint8 pages need shape [P, Hkv, {FP8_PAGE_BYTES}] with a "
+                                 f"contiguous byte axis, got {tuple(t.shape)} strides {t.stride()}")
         raise ValueError("k_pages and v_pages must have the same shape and strides")
-    scales = (_arg(k_scales, torch.uint8, (s[0], s[1], 4), "k_scales"),
-              _arg(v_scales, torch.uint8, (s[0], s[1], 4), "v_scales"))
-    kp = k_pages.data_ptr() if k_pages.is_cuda else _Host(k_pages)
-    vp = v_pages.data_ptr() if v_pages.is_cuda else _Host(v_pages)
-    return (kp, vp, st[0], st[1], s[0]), scales, s[1]
+    P, Hkv = s[0], s[1]
+    scales = (_on(k_scales, torch.uint8, (P, Hkv, 4), "k_scales", dev),
+              _on(v_scales, torch.uint8, (P, Hkv, 4), "v_scales", dev))
+    return ((_address(k_pages, dev, "k_pages"), _address(v_pages, dev, "v_pages"), st[0], st[1], P),
+            scales, Hkv)
 
 
-def _head_rows(t, name, dtype, shape):
+def _head_rows(t, name, dtype, shape, dev):
     """(address, token stride) of [T, heads, 128] rows with contiguous heads."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -821,7 +871,7 @@ def _head_rows(t, name, dtype, shape):
     if st[2] != 1 or (shape[1] > 1 and st[1] != HEAD_DIM):
         raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {st}")
     # (the stride of a single token says nothing)
-    return t.data_ptr() if t.is_cuda else _Host(t), st[0] if shape[0] > 1 else shape[1] * HEAD_DIM
+    return _address(t, dev, name), st[0] if shape[0] > 1 else shape[1] * HEAD_DIM
 
 
 def fp8_rope_append(q, k, v, cu_new, block_table, seq_lens, k_pages, v_pages, k_scales, v_scales,
@@ -832,8 +882,8 @@ def fp8_rope_append(q, k, v, cu_new, block_table, seq_lens, k_pages, v_pages, k_
     with their scales uint8 [P, Hkv, 4].  q, k, v fp32 or bf16, heads contiguous, any token
     stride.  cu_new int32 [B + 1]: sequence s's rows, the last of its seq_lens int32 [B] tokens.
     q and q_out None: K and V alone."""
-    i32, i64 = torch.int32, torch.int64
-    T, Hkv, D = _sizes(k, "k", 3)
+    i32, i64, dev = torch.int32, torch.int64, _device()
+    T, Hkv, D = shape = _sizes(k, "k", 3)
     if D != HEAD_DIM:
         _dims(k, "k", None, None, HEAD_DIM)
     dtype = k.dtype
@@ -842,64 +892,71 @@ def fp8_rope_append(q, k, v, cu_new, block_table, seq_lens, k_pages, v_pages, k_
     B, W = _sizes(seq_lens, "seq_lens", 1)[0], _sizes(block_table, "block_table", 2)[1]
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    H, qp, qo = 0, (None, 0), None
+    H, qp, qs, qo = 0, 0, 0, 0
     if q is not None:
-        H = _sizes(q, "q", 3)[1]
-        qp = _head_rows(q, "q", dtype, (T, H, HEAD_DIM))
-        qo = _arg(q_out, torch.bfloat16, (T, H, HEAD_DIM), "q_out")
-    kr, vr = _head_rows(k, "k", dtype, (T, Hkv, HEAD_DIM)), _head_rows(v, "v", dtype, (T, Hkv, HEAD_DIM))
-    pools, scales, heads = _fp8_kv_pools(k_pages, v_pages, k_scales, v_scales)
+        qshape = _sizes(q, "q", 3)
+        H = qshape[1]
+        qp, qs = _head_rows(q, "q", dtype, (T, H, HEAD_DIM), dev)
+        qo = _on(q_out, torch.bfloat16, (T, H, HEAD_DIM), "q_out", dev)
+    kp, kst = _head_rows(k, "k", dtype, shape, dev)
+    vp, vst = _head_rows(v, "v", dtype, shape, dev)
+    pools, scales, heads = _fp8_kv_pools(k_pages, v_pages, k_scales, v_scales, dev)
     if heads != Hkv:
         raise ValueError(f"k_pages has {int(heads)} KV heads, k has {Hkv}")
-    rot = 0 if phases is None else 2 * _sizes(phases, "phases", 1)[0]
-    cu, pos = _arg(cu_new, i32, (B + 1,), "cu_new"), _opt(positions, i64, (T,), "positions")
-    ph = _arg(phases, i64, (rot // 2,), "phases") if rot else None
-    tables = _arg(block_table, i32, (B, W), "block_table"), W, _arg(seq_lens, i32, (B,), "seq_lens")
-    _one_device(q, k, v, cu_new, block_table, seq_lens, k_pages, v_pages, k_scales, v_scales, q_out,
-                phases, positions)
-    _call(_load().fp8_rope_append, *qp, *kr, *vr, dtype is torch.float32, T, H, Hkv, cu, B, pos, ph,
-          rot, bool(interleaved), factor, *tables, *pools, *scales, qo, _stream(stream))
+    cu = _on(cu_new, i32, (B + 1,), "cu_new", dev)
+    pos = 0 if positions is None else _on(positions, i64, (T,), "positions", dev)
+    rot = ph = 0
+    if phases is not None:
+        rot = 2 * _sizes(phases, "phases", 1)[0]
+        ph = _on(phases, i64, (rot // 2,), "phases", dev)
+    _call_words(_APPEND, qp, qs, kp, kst, vp, vst, dtype is torch.float32, T, H, Hkv, cu, B, pos, ph,
+                rot, bool(interleaved), factor, _on(block_table, i32, (B, W), "block_table", dev), W,
+                _on(seq_lens, i32, (B,), "seq_lens", dev), *pools, *scales, qo, _stream_word(stream))
+
+
+def _rows_on(t, dtype, rows, name, dev):
+    """The address of a contiguous matrix of at least this many rows."""
+    if _sizes(t, name, 2)[0] < rows:
+        _rows_at_least(t, rows, name)
+    return _on(t, dtype, t.shape, name, dev)
+
+
+def _block_score(how, iq, q_per_seq, pages, page_bytes, block_table, seq_lens, scores, stream, scale):
+    dev, i32 = _device(), torch.int32
+    B, W = _sizes(seq_lens, "seq_lens", 1)[0], _sizes(block_table, "block_table", 2)[1]
+    T, ld = B * int(q_per_seq), _sizes(scores, "scores", 2)[1]
+    if pages.dtype is not torch.uint8 or len(pages.shape) != 2 or pages.shape[1] != page_bytes or pages.stride(1) != 1:
+        _fp8_pages(pages, "pages") if page_bytes == FP8_PAGE_BYTES else _pages(pages, "idx_pages", 2)
+    _call_words(how, _on(iq, torch.bfloat16, (T, HEAD_DIM), "iq", dev), T, q_per_seq,
+                _address(pages, dev, "pages"), pages.stride(0), pages.shape[0],
+                _rows_on(block_table, i32, B, "block_table", dev), B, W,
+                _on(seq_lens, i32, (B,), "seq_lens", dev), *scale,
+                _rows_on(scores, torch.float32, T, "scores", dev), ld, _stream_word(stream))
 
 
 def index_block_score(iq, q_per_seq, idx_pages, block_table, seq_lens, scores, stream=None):
     """scores[t, b] = the largest index_score of the tokens of block b (128 tokens, one page) that
     decode token t sees, fp32 [T, ld], ld at least the most blocks of a sequence."""
-    _one_device(iq, idx_pages, block_table, seq_lens, scores)
-    _score_call("index_block_score", iq, q_per_seq, idx_pages, block_table, seq_lens, scores, stream)
+    _block_score(_SCORE, iq, q_per_seq, idx_pages, PAGE_BYTES, block_table, seq_lens, scores, stream, ())
 
 
 def index_block_score_fp8(iq, q_per_seq, pages, block_table, seq_lens, scale, scores, stream=None):
     """index_block_score over the fp8 index cache."""
-    _one_device(iq, pages, block_table, seq_lens, scores)
-    _need(iq, torch.bfloat16, "iq")
-    _need(block_table, torch.int32, "block_table")
-    _need(seq_lens, torch.int32, "seq_lens")
-    _need(scores, torch.float32, "scores")
-    _fp8_pages(pages, "pages")
-    _dims(seq_lens, "seq_lens", None)
-    B = int(seq_lens.shape[0])
-    _dims(iq, "iq", B * int(q_per_seq), HEAD_DIM)
-    _dims(block_table, "block_table", None, None)
-    _rows_at_least(block_table, B, "block_table")
-    _dims(scores, "scores", None, None)
-    _rows_at_least(scores, B * int(q_per_seq), "scores")
-    _check(_load().index_block_score_fp8(_ptr(iq), int(iq.shape[0]), int(q_per_seq), _ptr(pages),
-                                         pages.stride(0), int(pages.shape[0]), _ptr(block_table), B,
-                                         int(block_table.shape[1]), _ptr(seq_lens), float(scale),
-                                         _ptr(scores), scores.stride(0), _stream(stream)))
+    _block_score(_SCORE_FP8, iq, q_per_seq, pages, FP8_PAGE_BYTES, block_table, seq_lens, scores, stream,
+                 (scale,))
 
 
 def block_topk(scores, seq_lens, q_per_seq, block_idx, first=0, last=0, stream=None):
     """block_idx int32 [T, k]: for each decode token the first `first` and last `last` of its
     blocks and those with the largest scores (fp32 [T, ld]), ties to the lower index, ascending,
     -1 padded."""
+    dev = _device()
     B = _sizes(seq_lens, "seq_lens", 1)[0]
     T = B * int(q_per_seq)
     ld, k = _sizes(scores, "scores", 2)[1], _sizes(block_idx, "block_idx", 2)[1]
-    args = (_arg(scores, torch.float32, (T, ld), "scores"), ld, _arg(seq_lens, torch.int32, (B,), "seq_lens"),
-            B, q_per_seq, k, first, last, _arg(block_idx, torch.int32, (T, k), "block_idx"))
-    _one_device(scores, seq_lens, block_idx)
-    _call(_load().block_topk, *args, _stream(stream))
+    _call_words(_TOPK, _on(scores, torch.float32, (T, ld), "scores", dev), ld,
+                _on(seq_lens, torch.int32, (B,), "seq_lens", dev), B, q_per_seq, k, first, last,
+                _on(block_idx, torch.int32, (T, k), "block_idx", dev), _stream_word(stream))
 
 
 def fp8_paged_decode_workspace(T, q_per_seq, H, Hkv) -> int:
@@ -910,21 +967,29 @@ def fp8_block_decode_workspace(T, k, H, Hkv) -> int:
     return int(_load().fp8_block_decode_workspace(int(T), int(k), int(H), int(Hkv)))
 
 
-def _fp8_decode_args(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, out,
-                     lse, block_idx=None):
-    i32, bf = torch.int32, torch.bfloat16
+def _fp8_decode(how, q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, idx,
+                scale, out, ws, lse, stream):
+    i32, bf, dev = torch.int32, torch.bfloat16, _device()
     T, H, D = shape = _sizes(q, "q", 3)
     if D != HEAD_DIM:
         _dims(q, "q", None, None, HEAD_DIM)
     B, W = _sizes(seq_lens, "seq_lens", 1)[0], _sizes(block_table, "block_table", 2)[1]
     if T != B * q_per_seq:
         raise ValueError(f"q has {T} tokens, seq_lens gives {B} x {int(q_per_seq)}")
-    qp, op = _arg(q, bf, shape, "q"), _arg(out, bf, shape, "out")
-    lp = _opt(lse, torch.float32, (T, H), "lse")
-    pools, scales, heads = _fp8_kv_pools(k_pages, v_pages, k_scales, v_scales)
-    tables = (_arg(block_table, i32, (B, W), "block_table"), B, W, _arg(seq_lens, i32, (B,), "seq_lens"))
-    _one_device(q, out, lse, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, block_idx)
-    return (qp, T, q_per_seq, H, heads, *pools, *scales, *tables), (op, lp)
+    qp, op = _on(q, bf, shape, "q", dev), _on(out, bf, shape, "out", dev)
+    lp = 0 if lse is None else _on(lse, torch.float32, (T, H), "lse", dev)
+    pools, scales, heads = _fp8_kv_pools(k_pages, v_pages, k_scales, v_scales, dev)
+    lists = ()
+    if idx is not None:
+        kb = _sizes(idx, "block_idx", 2)[1]
+        lists = _on(idx, i32, (T, kb), "block_idx", dev), kb
+    wp, nw = (0, 0) if ws is None else (_address(ws, dev, "ws"), ws.numel() * ws.element_size())
+    if nw and not ws.is_contiguous():
+        raise ValueError("ws: must be contiguous")
+    _call_words(how, qp, T, q_per_seq, H, heads, *pools, *scales,
+                _on(block_table, i32, (B, W), "block_table", dev), B, W,
+                _on(seq_lens, i32, (B,), "seq_lens", dev), *lists, scale, op, lp, wp, nw,
+                _stream_word(stream))
 
 
 def fp8_paged_decode(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens,
@@ -932,20 +997,16 @@ def fp8_paged_decode(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_t
     """Attention of q bf16 [T, H, 128] (q_per_seq decode tokens a sequence, causal) over all cached
     tokens of the 8-bit pages uint8 [P, Hkv, 16384], scales uint8 [P, Hkv, 4]: out bf16 like q,
     lse fp32 [T, H] or None.  ws: uint8, fp8_paged_decode_workspace(T, q_per_seq, H, Hkv) bytes."""
-    args, outs = _fp8_decode_args(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table,
-                                  seq_lens, out, lse)
-    _call(_load().fp8_paged_decode, *args, scale, *outs, *_ws(ws), _stream(stream))
+    _fp8_decode(_PAGED, q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens,
+                None, scale, out, ws, lse, stream)
 
 
 def fp8_block_decode(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens,
                      block_idx, scale, out, ws, lse=None, stream=None):
     """fp8_paged_decode over the 128-token blocks that each token lists, block_idx int32 [T, k]
     (negative entries are skipped).  ws: fp8_block_decode_workspace(T, k, H, Hkv) bytes."""
-    args, outs = _fp8_decode_args(q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table,
-                                  seq_lens, out, lse, block_idx)
-    k = _sizes(block_idx, "block_idx", 2)[1]
-    idx = _arg(block_idx, torch.int32, (q.shape[0], k), "block_idx")
-    _call(_load().fp8_block_decode, *args, idx, k, scale, *outs, *_ws(ws), _stream(stream))
+    _fp8_decode(_BLOCK, q, q_per_seq, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens,
+                block_idx, scale, out, ws, lse, stream)
 
 
 def mx4_check_status(stream=None) -> int:

@@ -1235,3 +1235,50 @@ extern "C" int block_topk(const float* scores, int64_t ld_scores, const int32_t*
                                             static_cast<cudaStream_t>(stream)),
                      kName);
 }
+
+// The calls above from one array of 8-byte words, numbers and addresses in the order of their
+// arguments (floats as doubles): what the Python binding calls.  Converting 30 arguments one by one
+// took it longer than the kernels' launches.
+namespace {
+
+struct Words {
+  const int64_t* w;
+  template <class T>
+  operator T*() {
+    return reinterpret_cast<T*>(static_cast<uintptr_t>(*w++));
+  }
+  operator int64_t() { return *w++; }
+  operator int() { return static_cast<int>(*w++); }
+  operator size_t() { return static_cast<size_t>(*w++); }
+  operator float() {
+    double d;
+    memcpy(&d, w++, sizeof d);
+    return static_cast<float>(d);
+  }
+};
+
+// (braces: initialisers are evaluated from left to right)
+template <class... A>
+struct Call {
+  int rc;
+  Call(int (*f)(A...), A... a) : rc(f(a...)) {}
+};
+template <class... A>
+int call_words(int (*f)(A...), const int64_t* w) {
+  Words x{w};
+  return Call<A...>{f, static_cast<A>(x)...}.rc;
+}
+
+}  // namespace
+
+extern "C" int mx4_call_words(int which, const int64_t* w) {
+  switch (which) {
+    case 0: return call_words(fp8_rope_append, w);
+    case 1: return call_words(fp8_paged_decode, w);
+    case 2: return call_words(fp8_block_decode, w);
+    case 3: return call_words(block_topk, w);
+    case 4: return call_words(index_block_score, w);
+    case 5: return call_words(index_block_score_fp8, w);
+    default: return fail(MX4_ERR_INVALID, "mx4_call_words: which = %d", which);
+  }
+}

@@ -124,7 +124,15 @@ def _c(lib, name, **kw):
                                       scale=f(0.1), sc=p, ld=3, stream=None),
     }[name]
     assert set(kw) <= set(base)
-    return getattr(lib, name)(*{**base, **kw}.values())
+    args = list({**base, **kw}.values())
+    rc = getattr(lib, name)(*args)
+    # the binding's form of the call: one array of words
+    how = {"fp8_rope_append": m._APPEND, "fp8_paged_decode": m._PAGED, "fp8_block_decode": m._BLOCK,
+           "block_topk": m._TOPK, "index_block_score": m._SCORE, "index_block_score_fp8": m._SCORE_FP8}[name]
+    why = m.mx4_last_error()
+    words = how[1](*(0 if x is None else x.value if isinstance(x, f) else x for x in args))
+    assert lib.mx4_call_words(how[0], words) == rc and m.mx4_last_error() == why
+    return rc
 
 
 INF, NAN = ctypes.c_float(math.inf), ctypes.c_float(math.nan)
@@ -164,6 +172,10 @@ INF, NAN = ctypes.c_float(math.inf), ctypes.c_float(math.nan)
 def test_c_refusals(lib, name, kw, code):
     assert _c(lib, name, **kw) == code
     assert code == 0 or name in m.mx4_last_error()
+
+
+def test_call_of_words(lib):
+    assert lib.mx4_call_words(99, b"") == -1 and "99" in m.mx4_last_error()
 
 
 def test_workspaces(lib):
