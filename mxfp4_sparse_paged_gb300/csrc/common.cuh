@@ -132,6 +132,21 @@ __device__ __forceinline__ void bulk_copy_g2s(uint32_t dst, const void* src, uin
       : "memory");
 }
 
+// What is read once a call: first to leave L2, where it would push out tables, other inputs and code.
+__device__ __forceinline__ uint64_t read_once() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void bulk_copy_g2s_once(uint32_t dst, const void* src, uint32_t bytes,
+                                                   uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], "
+      "%2, [%3], %4;\n" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(read_once())
+      : "memory");
+}
+
 // The four bytes of w, each an e2m1 pair -> f16x2 (low nibble -> low half).
 // The hardware conversion gives the exact E2M1 grid value.
 __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&r)[4]) {

@@ -11,10 +11,9 @@
 // to the new scale (a power of two moves E4M3's normal values without rounding).
 //
 // Work.  A decode step (fewer than eight new tokens a sequence on average): a warp a token and KV
-// head, K and V, whose rows are on their way before the sequence is looked up.  Prompts: four warps a
-// block of 32 tokens, K or V, four heads one after another, so that the sines of a token are computed
-// once for four heads (for each head they took 50 us of 136 with 13600 tokens of 8 + 40 heads).  q: a
-// warp a token and 8 to 32 heads.  A lane computes the sines of two of its four dims; its partner in
+// head, K and V, whose rows are on their way before the sequence is looked up.  Prompts: sixteen warps
+// a block of 32 tokens, K or V, eight heads one after another, so that the sines of a token are
+// computed once for eight heads.  q: a warp a token and 8 to 64 heads.  A lane computes the sines of two of its four dims; its partner in
 // the pair has the others.
 //
 // Bound: latency for a decode batch, HBM for prompts.
@@ -55,7 +54,8 @@ struct AppendArgs {
 };
 
 constexpr int kQBatch = 8;   // q rows in flight
-constexpr int kKvHeads = 4;  // heads of a prompt's block, one after another
+constexpr int kKvHeads = 8;  // heads of a prompt's block, one after another
+constexpr int kPromptWarps = 16, kRows = kSub / kPromptWarps;  // and its rows
 
 template <typename E>
 __device__ __forceinline__ float4 load4(const E* p);
@@ -337,14 +337,15 @@ __global__ void __launch_bounds__(128) fp8_append_step_kernel(const AppendArgs a
   if (!__all_sync(0xFFFFFFFFu, ok) && lane == 0) flag(a.status, MX4_STATUS_BAD_VALUE);
 }
 
-// Prompts: a CTA 32 new tokens, K or V, kKvHeads heads; a warp eight rows of a block.
+// Prompts: a CTA 32 new tokens, K or V, kKvHeads heads; a warp two rows of a block (13600 tokens
+// of 40 + 8 fp32 heads: 105 us; four rows, and so half the warps, 121; four heads 114, two 138).
 template <typename E>
-__global__ void __launch_bounds__(128) fp8_append_kernel(const AppendArgs a) {
-  __shared__ uint32_t top_s[2][4];
+__global__ void __launch_bounds__(kPromptWarps * 32) fp8_append_kernel(const AppendArgs a) {
+  __shared__ uint32_t top_s[2][kPromptWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch_dependents();
   pdl_wait();
-  if (blockIdx.x >= a.kv_ctas) return turn_q<E>(a, (blockIdx.x - a.kv_ctas) * 4 + warp, lane);
+  if (blockIdx.x >= a.kv_ctas) return turn_q<E>(a, (blockIdx.x - a.kv_ctas) * kPromptWarps + warp, lane);
   const int groups = (a.Hkv + kKvHeads - 1) / kKvHeads;
   const int64_t chunk = blockIdx.x / (2 * groups);
   const int rest = (int)(blockIdx.x - chunk * 2 * groups), which = rest & 1;
@@ -360,12 +361,12 @@ __global__ void __launch_bounds__(128) fp8_append_kernel(const AppendArgs a) {
       if (threadIdx.x == 0) flag(a.status, MX4_STATUS_BAD_PAGE);
       continue;
     }
-    const int r0 = warp * 8, rows = min(8, sp.cnt - r0);  // of this warp
-    Turn turn[8];
+    const int r0 = warp * kRows, rows = min(kRows, sp.cnt - r0);  // of this warp
+    Turn turn[kRows];
     const bool turns = which == 0 && a.R > 0;
     if (turns) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < kRows; ++i)
         if (i < rows) turn[i] = turn_of(a, a.positions ? a.positions[t + r0 + i] : sp.pos + r0 + i, lane);
     }
     const E* const src =
@@ -373,12 +374,12 @@ __global__ void __launch_bounds__(128) fp8_append_kernel(const AppendArgs a) {
     for (int h = h0; h < h1; ++h) {
       const Block b = block_of(a, sp.page, sp.pos, h, which);
       const int old = b.at ? (int)*b.scale : 0;
-      float4 x[8];
+      float4 x[kRows];
       uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = i < rows ? load4<E>(src + i * stride + h * kHeadDim) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < kRows; ++i) x[i] = i < rows ? load4<E>(src + i * stride + h * kHeadDim) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         if (i >= rows) break;
         if (turns) x[i] = turned(a, x[i], turn[i], lane);
         top = max(top, largest(x[i]));
@@ -389,10 +390,10 @@ __global__ void __launch_bounds__(128) fp8_append_kernel(const AppendArgs a) {
       if (lane == 0) ts[warp] = top;
       __syncthreads();  // (and all have read the stored scale; the next block's maxima go to the other row)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, ts[i]);
-      const int e = grow(b, top, old, threadIdx.x, 128);
+      for (int i = 0; i < kPromptWarps; ++i) top = max(top, ts[i]);
+      const int e = grow(b, top, old, threadIdx.x, kPromptWarps * 32);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         if (i >= rows) break;
         store_row(b, r0 + i, x[i], e, lane);
       }
@@ -407,10 +408,11 @@ cudaError_t launch(AppendArgs a, int num_sms, cudaStream_t stream) {
   a.kv_ctas = prompts ? (a.T + 31) / 32 * 2 * ((a.Hkv + kKvHeads - 1) / kKvHeads) : (a.T * a.Hkv + 3) / 4;
   // more heads a q warp once there are warps enough: the sines are computed once for them
   a.q_heads = kQBatch;
-  while (a.q_heads < 32 && a.q_heads < a.H && a.T * a.H / a.q_heads > 32 * (int64_t)num_sms) a.q_heads *= 2;
-  const int64_t q_ctas = a.q ? (a.T * ((a.H + a.q_heads - 1) / a.q_heads) + 3) / 4 : 0;
+  while (a.q_heads < 64 && a.q_heads < a.H && a.T * a.H / a.q_heads > 32 * (int64_t)num_sms) a.q_heads *= 2;
+  const int warps = prompts ? kPromptWarps : 4;
+  const int64_t q_ctas = a.q ? (a.T * ((a.H + a.q_heads - 1) / a.q_heads) + warps - 1) / warps : 0;
   return launch_pdl(prompts ? fp8_append_kernel<E> : fp8_append_step_kernel<E>,
-                    dim3((unsigned)(a.kv_ctas + q_ctas)), dim3(128), 0, stream, a);
+                    dim3((unsigned)(a.kv_ctas + q_ctas)), dim3(warps * 32), 0, stream, a);
 }
 
 }  // namespace

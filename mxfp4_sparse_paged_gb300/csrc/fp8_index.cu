@@ -211,9 +211,10 @@ cudaError_t launch_index_score_fp8(const uint16_t* iq, int q, const uint8_t* pag
 
 // index_block_score_fp8: the largest score of each page (block mode of the pipeline, a warp a page).
 struct Fp8Blocks : Fp8Fmt {
-  static constexpr int kConsumers = 3;
-  static constexpr int kStages = 6;
+  static constexpr int kConsumers = 4;
+  static constexpr int kStages = 4;
   static constexpr int kEmptyCount = 1;
+  static constexpr int ctas_per_sm(int) { return 3; }  // (two of three warps and six stages: 55 us for 49)
 };
 
 cudaError_t launch_index_block_score_fp8(const uint16_t* iq, int q, const uint8_t* pages,

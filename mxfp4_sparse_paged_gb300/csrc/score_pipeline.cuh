@@ -242,7 +242,10 @@ score_kernel(const __grid_constant__ ScoreArgs a) {
               const uint32_t dst = smem_addr(smem_raw + Lay::kStagesOff + st * Lay::kStageBytes);
               if (okk) {
                 mbar_arrive_expect_tx(fb, F::kPageBytes + Q * kHeadDim * 2);
-                bulk_copy_g2s(dst, src, F::kPageBytes, fb);
+                if constexpr (Blocks)
+                  bulk_copy_g2s_once(dst, src, F::kPageBytes, fb);
+                else
+                  bulk_copy_g2s(dst, src, F::kPageBytes, fb);
                 bulk_copy_g2s(dst + F::kPageBytes, a.iq + (int64_t)seqk * Q * kHeadDim,
                               Q * kHeadDim * 2, fb);
               } else {
