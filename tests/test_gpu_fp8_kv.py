@@ -272,6 +272,50 @@ def test_decode_in_a_graph_and_on_a_stream():
         R.check_attention(out, lse, want)
 
 
+def test_two_streams_at_once():
+    """Calls on two streams with a workspace each, again and again: the bits of calls one by one."""
+    a = attention([9000, 30], 1, 16, 1, seed=20)
+    b = attention([3000] * 5, 2, 20, 4, seed=21)
+    wa, wb = (a[0].clone(), a[1].clone()), (b[0].clone(), b[1].clone())
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(s1):
+            a[3]()
+        with torch.cuda.stream(s2):
+            b[3]()
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], wa[0]) and torch.equal(a[1], wa[1])
+    assert torch.equal(b[0], wb[0]) and torch.equal(b[1], wb[1])
+
+
+def test_pages_past_32_bits():
+    """Pages whose bytes lie past 2^32 in the pool: append there and read back."""
+    g = torch.Generator().manual_seed(22)
+    P = (1 << 32) // 16384 + 100
+    kp, vp = (torch.empty((P, 1, 16384), dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = (torch.full((P, 1, 4), 255, dtype=torch.uint8, device=DEV) for _ in range(2))
+    L = 300
+    table = torch.tensor([[P - 1, P - 77, P - 3]], dtype=torch.int32)
+    i = dict(dtype=torch.int32, device=DEV)
+    k, v = (torch.randn((L, 1, 128), generator=g).to(torch.bfloat16) for _ in range(2))
+    m.fp8_rope_append(None, k.to(DEV), v.to(DEV), torch.tensor([0, L], **i), table.to(DEV), torch.tensor([L], **i),
+                      kp, vp, ks, vs, None)
+    q = torch.randn((1, 16, 128), generator=g).to(torch.bfloat16)
+    out, lse = torch.empty((1, 16, 128), dtype=torch.bfloat16, device=DEV), torch.empty((1, 16), device=DEV)
+    ws = torch.empty(m.fp8_paged_decode_workspace(1, 1, 16, 1), dtype=torch.uint8, device=DEV)
+    m.fp8_paged_decode(q.to(DEV), 1, kp, vp, ks, vs, table.to(DEV), torch.tensor([L], **i), 0.1, out, ws, lse=lse)
+    at = table[0].long().to(DEV)
+    rows = [R.values(x[at].cpu(), y[at].cpu()) for x, y in ((kp, ks), (vp, vs))]
+    small = torch.tensor([[0, 1, 2]], dtype=torch.int32)
+    R.check_attention(out, lse, R.attend(q, 1, *rows, small, [L], 0.1))
+    # stored values: within half a step of E4M3 (2^-4 of the value, 2^-10 of the scale) of the rows
+    got = rows[1][:, 0].reshape(-1, 128)[:L]
+    scale = torch.pow(2.0, vs[at].cpu().double() - 127).view(-1)[:, None].repeat_interleave(32, 0)[:L]
+    assert ((got - v[:, 0].double()).abs() <= v[:, 0].double().abs() * 2.0**-4 + scale * 2.0**-10).all()
+    m.mx4_check_status()
+
+
 # ------------------------------------------------------------------ append
 
 def append(lens, new, H, Hkv, dtype, rot, inter, seed, factor=1.0, shift=None, pad=0, fused=True, edit=None):
@@ -638,3 +682,36 @@ def test_steps_together(blocks, q, dtype):
         yq = R.turned(ins[0].cpu(), [lens[t // q] - q + t % q for t in range(T)], m.rope_phases(freq).tolist(),
                       False, grow)
         assert ((step.q_out.cpu().double() - yq).abs() <= 2.0**-8 * yq.abs() + band(ins[0].cpu().double(), 64, False, grow)).all()
+
+
+def test_chain_without_waits():
+    """Calls that read what the call before wrote, sixty steps without a wait between them: the bits
+    of the same steps with one after every call."""
+    from mxfp4_sparse_paged_gb300.fp8_step import Fp8Caches, Fp8Step
+    g = torch.Generator(DEV).manual_seed(0)
+    B, H, Hkv, prompt, steps = 24, 16, 2, 700, 60
+    table, P = tables(torch.Generator().manual_seed(1), [prompt + steps] * B)
+    ins = [(torch.randn((B, H, 128), generator=g, device=DEV).to(torch.bfloat16),
+            torch.randn((B, Hkv, 128), generator=g, device=DEV).to(torch.bfloat16),
+            torch.randn((B, Hkv, 128), generator=g, device=DEV).to(torch.bfloat16),
+            torch.randn((B, 128), generator=g, device=DEV).to(torch.bfloat16),
+            torch.randn((B, 128), generator=g, device=DEV)) for _ in range(steps)]
+    pk = torch.randn((2, B * prompt, Hkv, 128), generator=g, device=DEV).to(torch.bfloat16)
+    pi = torch.randn((B * prompt, 128), generator=g, device=DEV)
+    phases = m.rope_phases(m.rope_frequencies(128)[0]).to(DEV)
+
+    def go(wait):
+        caches = Fp8Caches(P, Hkv, index_scale=0.02)
+        step = Fp8Step(caches, table.to(DEV), torch.zeros(B, dtype=torch.int32, device=DEV), 1, H, 3, 1, 1, phases)
+        step.append(pk[0], pk[1], pi, torch.arange(0, B * prompt + 1, prompt, dtype=torch.int32, device=DEV), prompt)
+        outs = []
+        for x in ins:
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(step.run(*x).clone())
+            outs.append(step.block_idx.clone())
+        return outs + [t.clone() for t in caches.kv()]
+
+    quick, slow = go(False), go(True)
+    assert all(torch.equal(a, b) for a, b in zip(quick, slow))
+    m.mx4_check_status()
