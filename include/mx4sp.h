@@ -623,7 +623,7 @@ int fp8_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_st
  * order, a block listed twice counts twice, negative entries are skipped (the padding of
  * block_topk).  Tokens past p hold whatever they hold: they reach no result.  Logits, the sum and
  * the accumulator are fp32, weights 11 bits of f16 (relative to the largest of a row down to
- * 2^-22, absolute below).  A token that sees nothing (p < 0: a sequence shorter than q, down to
+ * 2^-16, absolute below).  A token that sees nothing (p < 0: a sequence shorter than q, down to
  * empty; no block) gets zeros and an lse of -inf.
  *
  *   q         bf16 [T, H, 128], contiguous, T = B * q_per_seq, 16-byte aligned

@@ -24,7 +24,7 @@
 //     quarter-warp meet in a bank.
 //   p = 2^(S f - m + 8), f = scale log2(e) 2^Ek.  m moves only where a row's largest logit lies
 //     2^7 above it, so a unit costs one vote and no reduction.  z sums p in fp32; P is f16 (11
-//     bits: 2^-12 of a weight; weights down to 2^-22 of the largest keep all of them).
+//     bits: 2^-12 of a weight; weights down to 2^-16 of the largest keep all of them).
 //   O^T += V^T P^T: weights of two rows are transposed in registers (movmatrix, 8 x 8); a pair of
 //     tokens' bytes is put side by side by byte permutes and widened to f16x2, exact.  O is kept in
 //     units of 2^Er, the largest 2^Ev met: 2^(Ev - Er) goes into the exponent of p (and out of z).
