@@ -596,7 +596,8 @@ int mx4_free_pages(const int32_t *tables, int64_t n, int64_t bt_width, const int
  *   q, k, v     fp32 (fp32 != 0) or bf16, [T, H, 128], [T, Hkv, 128] with q_stride, k_stride,
  *               v_stride elements a token (heads contiguous); row starts aligned to 4 elements.
  *               q may be NULL with q_out (K and V alone)
- *   q_out       bf16 [T, H, 128], contiguous, 8-byte aligned
+ *   q_out       bf16 [T, H, 128], contiguous, 8-byte aligned; may be q itself (bf16,
+ *               contiguous), may not overlap the inputs otherwise
  *   rot         0 (no turn; phases may be NULL) .. 128, a multiple of 8
  * A sequence with more new tokens than seq_len, seq_len > bt_width*128 or cu_new[s+1] > T is
  * skipped (MX4_STATUS_BAD_LEN), a block whose page id is outside the pool too
@@ -627,7 +628,7 @@ int fp8_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_st
  * empty; no block) gets zeros and an lse of -inf.
  *
  *   q         bf16 [T, H, 128], contiguous, T = B * q_per_seq, 16-byte aligned
- *   out       bf16 [T, H, 128], 16-byte aligned; lse fp32 [T, H] or NULL
+ *   out       bf16 [T, H, 128], 16-byte aligned, not overlapping q; lse fp32 [T, H] or NULL
  *   block_idx int32 [T, kb]
  *   ws        workspace of *_workspace(T, ...) bytes, 16-byte aligned; the size depends on the
  *             current device's SM count and may be shared by calls that follow one another on a
@@ -668,7 +669,8 @@ size_t fp8_block_decode_workspace(int64_t T, int kb, int H, int Hkv);
  * the first `first` and the last `last` (the token's own and those before it) always, then the
  * largest scores, ties to the lower index (NaN above all, -0.0 equal to +0.0); written in
  * ascending order to block_idx[t*k ..], -1 padded.
- *   scores fp32 [B * q_per_seq, ld_scores]; block_idx int32 [B * q_per_seq, k]
+ *   scores fp32 [B * q_per_seq, ld_scores]; block_idx int32 [B * q_per_seq, k] (not
+ *   overlapping the inputs)
  * 1 <= k <= 4096, first + last <= k, 1 <= ld_scores <= 65536, B <= 65535.  A negative seq_len or
  * one with n > ld_scores writes a row of -1 (MX4_STATUS_BAD_LEN).
  * ------------------------------------------------------------------------- */

@@ -1087,6 +1087,9 @@ int fp8_decode_entry(const char* name, const uint16_t* q, int64_t T, int q_per_s
     return fail(MX4_ERR_INVALID, "%s: misaligned buffer", name);
   if (!ws || !aligned(ws, 16))
     return fail(MX4_ERR_INVALID, "%s: workspace NULL or not 16-byte aligned", name);
+  // (parts of a token's attention read q after others have written theirs)
+  if (overlap(q, (size_t)T * H * 256, out, (size_t)T * H * 256))
+    return fail(MX4_ERR_INVALID, "%s: out overlaps q", name);
   if (bt_width < 1 || bt_width > (1 << 20))
     return fail(MX4_ERR_UNSUPPORTED, "%s: bt_width = %lld (1..2^20)", name, (long long)bt_width);
   DeviceInfo* d;
@@ -1179,6 +1182,14 @@ extern "C" int fp8_rope_append(const void* q, int64_t q_stride, const void* k, i
                                num_pages, k_scales, v_scales))
     return rc;
   if (bt_width < 1) return fail(MX4_ERR_INVALID, "%s: bt_width < 1", kName);
+  if (q) {
+    const size_t n = (size_t)T * H * 256;
+    auto bytes = [&](int64_t stride, int heads) { return ((T - 1) * stride + heads * 128) * (int64_t)e; };
+    const bool same = q == q_out && !fp32 && (T == 1 || q_stride == (int64_t)H * 128);  // row for row
+    if ((!same && overlap(q, bytes(q_stride, H), q_out, n)) || overlap(k, bytes(k_stride, Hkv), q_out, n) ||
+        overlap(v, bytes(v_stride, Hkv), q_out, n))
+      return fail(MX4_ERR_INVALID, "%s: q_out overlaps an input", kName);
+  }
   const int64_t strides[3] = {q_stride, k_stride, v_stride};
   DeviceInfo* d;
   if (int rc = device_info(&d)) return rc;
@@ -1228,6 +1239,9 @@ extern "C" int block_topk(const float* scores, int64_t ld_scores, const int32_t*
   if (!scores || !seq_lens || !block_idx) return fail(MX4_ERR_INVALID, "%s: NULL pointer", kName);
   if (!aligned(scores, 4) || !aligned(seq_lens, 4) || !aligned(block_idx, 4))
     return fail(MX4_ERR_INVALID, "%s: misaligned buffer", kName);
+  const size_t rows = (size_t)B * q_per_seq * 4;
+  if (overlap(block_idx, rows * k, scores, rows * ld_scores) || overlap(block_idx, rows * k, seq_lens, B * 4))
+    return fail(MX4_ERR_INVALID, "%s: block_idx overlaps an input", kName);
   DeviceInfo* d;
   if (int rc = device_info(&d)) return rc;
   return cuda_result(mx4::launch_block_topk(scores, ld_scores, seq_lens, B * q_per_seq, q_per_seq,

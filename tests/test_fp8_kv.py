@@ -104,20 +104,20 @@ def test_strides(lib):
 
 def _c(lib, name, **kw):
     """The C call with arguments that are fine but for kw; addresses are never read."""
-    p = 1 << 20
+    p, far = 1 << 20, 1 << 30
     f = ctypes.c_float
     base = {
         "fp8_rope_append": dict(q=p, qs=2048, k=p, kst=256, v=p, vst=256, fp32=0, T=4, H=16, Hkv=2,
                                 cu=p, B=4, pos=None, ph=p, rot=128, inter=0, factor=f(1.0), bt=p,
-                                W=3, sl=p, kp=p, vp=p, ps=32768, hs=16384, P=3, ks=p, vs=p, qo=p,
+                                W=3, sl=p, kp=p, vp=p, ps=32768, hs=16384, P=3, ks=p, vs=p, qo=far,
                                 stream=None),
         "fp8_paged_decode": dict(q=p, T=4, qps=1, H=16, Hkv=2, kp=p, vp=p, ps=32768, hs=16384, P=3,
-                                 ks=p, vs=p, bt=p, B=4, W=3, sl=p, scale=f(0.1), out=p, lse=p, ws=p,
+                                 ks=p, vs=p, bt=p, B=4, W=3, sl=p, scale=f(0.1), out=far, lse=p, ws=p,
                                  nws=1 << 40, stream=None),
         "fp8_block_decode": dict(q=p, T=4, qps=1, H=16, Hkv=2, kp=p, vp=p, ps=32768, hs=16384, P=3,
-                                 ks=p, vs=p, bt=p, B=4, W=3, sl=p, idx=p, kb=8, scale=f(0.1), out=p,
+                                 ks=p, vs=p, bt=p, B=4, W=3, sl=p, idx=p, kb=8, scale=f(0.1), out=far,
                                  lse=p, ws=p, nws=1 << 40, stream=None),
-        "block_topk": dict(sc=p, ld=3, sl=p, B=4, qps=1, k=8, first=1, last=2, idx=p, stream=None),
+        "block_topk": dict(sc=p, ld=3, sl=p, B=4, qps=1, k=8, first=1, last=2, idx=far, stream=None),
         "index_block_score": dict(iq=p, T=4, qps=1, ip=p, ps=8704, P=3, bt=p, B=4, W=3, sl=p, sc=p,
                                   ld=3, stream=None),
         "index_block_score_fp8": dict(iq=p, T=4, qps=1, ip=p, ps=16384, P=3, bt=p, B=4, W=3, sl=p,
@@ -157,6 +157,10 @@ INF, NAN = ctypes.c_float(math.inf), ctypes.c_float(math.nan)
     ("fp8_paged_decode", dict(ws=(1 << 20) + 8), -1), ("fp8_paged_decode", dict(out=None), -1),
     ("fp8_paged_decode", dict(q=(1 << 20) + 8), -1), ("fp8_paged_decode", dict(W=(1 << 20) + 1), -2),
     ("fp8_paged_decode", dict(B=65536, T=65536), -2), ("fp8_paged_decode", dict(B=0, T=0), 0),
+    ("fp8_paged_decode", dict(out=(1 << 20) + 4 * 16 * 256 - 16), -1),
+    ("fp8_rope_append", dict(qo=(1 << 20) + 4 * 2048 * 2 - 8), -1),
+    ("fp8_rope_append", dict(v=(1 << 30) + 4 * 16 * 256 - 8), -1),
+    ("block_topk", dict(idx=(1 << 20) + 8), -1),
     ("fp8_block_decode", dict(kb=0), -2), ("fp8_block_decode", dict(kb=4097), -2),
     ("fp8_block_decode", dict(idx=None), -1), ("fp8_block_decode", dict(kp=(1 << 20) + 8), -1),
     ("block_topk", dict(k=0), -2), ("block_topk", dict(k=4097), -2), ("block_topk", dict(first=-1), -1),

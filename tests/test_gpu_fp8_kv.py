@@ -272,6 +272,26 @@ def test_decode_in_a_graph_and_on_a_stream():
         R.check_attention(out, lse, want)
 
 
+def test_nothing_cached_and_full_tables():
+    """Empty sequences alone, and lengths that fill the table to its last token; no lse."""
+    for lens in ([0, 0, 0], [384, 384]):
+        out, lse, want, _ = attention(lens, 3, 16, 2, seed=30)
+        R.check_attention(out, lse, want)
+    g = torch.Generator().manual_seed(31)
+    table, P = tables(g, [384])
+    kp, ks = (x.to(DEV) for x in pool(g, P, 1))
+    q = torch.randn((1, 16, 128), generator=g).to(torch.bfloat16).to(DEV)
+    ws = torch.empty(m.fp8_paged_decode_workspace(1, 1, 16, 1), dtype=torch.uint8, device=DEV)
+    outs = []
+    for lse in (torch.empty((1, 16), device=DEV), None):
+        out = torch.empty_like(q)
+        m.fp8_paged_decode(q, 1, kp, kp, ks, ks, table.to(DEV), torch.tensor([384], dtype=torch.int32, device=DEV),
+                           0.1, out, ws, lse=lse)
+        outs.append(out)
+    assert torch.equal(*outs)
+    m.mx4_check_status()
+
+
 def test_two_streams_at_once():
     """Calls on two streams with a workspace each, again and again: the bits of calls one by one."""
     a = attention([9000, 30], 1, 16, 1, seed=20)
@@ -420,6 +440,7 @@ def check_pool(pages, scales, before, before_scales, rows, bands, table, lens, n
 @pytest.mark.parametrize("lens,new,H,Hkv,rot,inter", [
     ([777], [1], 16, 1, 128, False), ([1, 32, 33, 128, 129, 64], [1] * 6, 8, 2, 64, True),
     ([40, 300, 128, 5], [7, 1, 3, 5], 4, 1, 96, False), ([700, 129, 96, 0], [650, 129, 1, 0], 5, 1, 128, True),
+    ([9, 70], [1, 2], 2, 1, 8, False), ([90, 70], [50, 60], 2, 1, 24, False), ([33, 40], [33, 40], 3, 1, 120, True),
     ([100, 100], [40, 33], 3, 3, 0, False), ([257, 31], [256, 31], 16, 8, 16, False), ([64] * 9, [0] * 4 + [64] + [0] * 4, 1, 1, 8, True)])
 def test_append(lens, new, H, Hkv, rot, inter, dtype):
     append(lens, new, H, Hkv, dtype, rot, inter, seed=len(lens) + rot)
@@ -449,6 +470,26 @@ def test_append_special_values():
         x[5, -128:] = torch.tensor([3.0, -448.0, 1e-30, 0.0] * 32)
     append([1, 1, 1, 8, 1, 31], [1] * 6, 1, 1, torch.float32, 0, False, 4, edit=edit)
     m.mx4_check_status()
+
+
+def test_append_in_place():
+    """q_out may be q: the bits of a call into another tensor."""
+    g = torch.Generator().manual_seed(8)
+    i = dict(dtype=torch.int32, device=DEV)
+    for n in (3, 200):
+        q = torch.randn((n, 20, 128), generator=g).to(torch.bfloat16).to(DEV)
+        k = torch.randn((n, 1, 128), generator=g).to(torch.bfloat16).to(DEV)
+        pools = [torch.zeros((2, 1, 16384), dtype=torch.uint8, device=DEV) for _ in range(2)]
+        pools += [torch.zeros((2, 1, 4), dtype=torch.uint8, device=DEV) for _ in range(2)]
+        rest = (torch.tensor([0, n], **i), torch.tensor([[0, 1]], **i), torch.tensor([n], **i), *pools)
+        ph = m.rope_phases(m.rope_frequencies(128)[0]).to(DEV)
+        other = torch.empty_like(q)
+        m.fp8_rope_append(q, k, k, *rest, other, phases=ph)
+        m.fp8_rope_append(q, k, k, *rest, q, phases=ph)
+        assert torch.equal(q, other)
+        with pytest.raises(m.Mx4Error, match="overlaps"):
+            m.fp8_rope_append(q[:1], k[:1], k[:1], rest[0].clamp(max=1), *rest[1:], q.view(-1)[64:64 + 20 * 128].view(1, 20, 128),
+                              phases=ph)
 
 
 def test_append_non_finite():
@@ -557,6 +598,22 @@ def test_block_scores_of_many_pages(fp8, q):
         # (the fp8 rows hold a few NaN codes, values past the format: their blocks are NaN on both sides)
         assert torch.equal(torch.isnan(bs), torch.isnan(want))
         assert torch.equal(bs.nan_to_num(nan=0.0, neginf=-1e9), want.nan_to_num(nan=0.0, neginf=-1e9))
+    m.mx4_check_status()
+
+
+def test_block_scores_of_many_sequences():
+    """More sequences than a launch takes."""
+    g = torch.Generator().manual_seed(40)
+    lens = np.random.default_rng(3).integers(1, 400, 2100).tolist()
+    table, P = tables(g, lens)
+    pages = pool(g, P, 1)[0][:, 0].to(DEV)
+    iq = torch.randn((2100, 128), generator=g).to(torch.bfloat16).to(DEV)
+    sl, W = torch.tensor(lens, dtype=torch.int32, device=DEV), table.shape[1]
+    sc = torch.full((2100, W * 128), -math.inf, device=DEV)
+    bs = torch.full((2100, W), -math.inf, device=DEV)
+    m.index_score_fp8(iq, 1, pages, table.to(DEV), sl, 1.0, sc)
+    m.index_block_score_fp8(iq, 1, pages, table.to(DEV), sl, 1.0, bs)
+    assert torch.equal(bs, sc.view(2100, W, 128).amax(-1))
     m.mx4_check_status()
 
 
