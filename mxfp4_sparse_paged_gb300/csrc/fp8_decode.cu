@@ -30,12 +30,12 @@
 //     units of 2^Er, the largest 2^Ev met: 2^(Ev - Er) goes into the exponent of p (and out of z).
 //     The product of a unit with Ev more than 6 below Er is scaled in fp32 before it is added, so
 //     scales of any two blocks may be any powers apart.
-// The tensor memory path (tcgen05) has no use here at few rows: it computes 128-row tiles from shared
-// memory, and would put scores and weights through tensor and shared memory on the way.
-//
-// Those, and units where some row does not see all 32 tokens (a sequence's end), take a second form of
-// the step: scores are masked, and values that no row sees, and NaN codes, are kept from the product
+// Such units, and those where some row does not see all 32 tokens (a sequence's end), take a second form
+// of the step: scores are masked, and values that no row sees, and NaN codes, are kept from the product
 // (clean() below).
+// The tensor memory path (tcgen05) computes 128-row tiles from shared memory, and puts scores and weights
+// through tensor and shared memory on the way: a form with it took 116 us where this one takes 77
+// (32 sequences of 8192 to 16384 tokens, 64 rows of a KV head).
 //
 // Ranges cut tiles.  A group keeps the tile it ends in until all groups of the CTA are done; then
 // pieces of the same tile are joined in shared memory.  Pieces of a tile in several CTAs go to the

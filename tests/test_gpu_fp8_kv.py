@@ -150,6 +150,27 @@ def test_paged_decode_wide_scales():
     R.check_attention(out, lse, want)
 
 
+@pytest.mark.parametrize("q,H", [(3, 8), (5, 8), (4, 16), (6, 16), (8, 16), (3, 64)])
+def test_paged_decode_wide_scales_and_nan_many_rows(q, H):
+    """24 to 192 rows a sequence, in one to eight warps a tile: V scales 2^100 apart, and NaN values and
+    scales that only the last queries see."""
+    out, lse, want, _ = attention([300, 41, 700], q, H, 1, seed=20 + q, vlo=60, vhi=160)
+    R.check_attention(out, lse, want)
+
+    def edit(qq, kp, ks, vp, vs, table):
+        vp[table[0, 2]].view(1, 128, 128)[0, 299 - 256, 17] = 0x7F   # the last token
+        vp[table[1, 0]].view(1, 128, 128)[0, 97, 100] = 0xFF         # the one before it, of 99
+        vs[table[2, 1], 0, 0] = 255                                  # tokens 128 .. 129 of 130
+    out, lse, want, _ = attention([300, 99, 130], q, H, 1, seed=30 + q, edit=edit)
+    o = torch.isnan(out.cpu().float()).view(3, q, H, 128)
+    assert o[0, -1, :, 17].all() and int(o[0].sum()) == H
+    assert o[1, -2:, :, 100].all() and int(o[1].sum()) == 2 * H
+    assert o[2, -2:].all() and int(o[2].sum()) == 2 * H * 128
+    ok = ~torch.isnan(want[0]).any(-1).reshape(-1)
+    fin = [w.flatten(0, 1)[ok] if w.dim() == 3 else w.reshape(-1)[ok] for w in want]
+    R.check_attention(out.flatten(0, 1)[ok.to(DEV)], lse.reshape(-1)[ok.to(DEV)], fin)
+
+
 def test_paged_decode_large_and_small_queries():
     def edit(q, kp, ks, vp, vs, table):
         q[0] *= 2.0**90
@@ -670,6 +691,20 @@ def test_block_topk(lens, q, k, first, last, kind):
     idx = torch.full((len(lens) * q, k), 99, dtype=torch.int32, device=DEV)
     m.block_topk(x.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), q, idx, first=first, last=last)
     assert idx.tolist() == R.topk(x, lens, q, k, first, last)
+    m.mx4_check_status()
+
+
+@pytest.mark.parametrize("W", [1000, 4096, 9000])
+def test_block_topk_rows_off_16_bytes(W):
+    """Rows of a multiple of four scores that begin one, two, three floats off a 16-byte boundary."""
+    lens, q, k = [128 * W, 128 * W - 500, 128 * (W // 2)], 2, 33
+    x = torch.randn((len(lens) * q, W), generator=torch.Generator().manual_seed(W))
+    for off in range(4):
+        flat = torch.full((x.numel() + off,), math.inf, device=DEV)
+        rows = flat[off:].view(x.shape).copy_(x)
+        idx = torch.full((len(lens) * q, k), 99, dtype=torch.int32, device=DEV)
+        m.block_topk(rows, torch.tensor(lens, dtype=torch.int32, device=DEV), q, idx, first=1, last=2)
+        assert idx.tolist() == R.topk(x, lens, q, k, 1, 2)
     m.mx4_check_status()
 
 
