@@ -22,9 +22,12 @@
 //     are exact and sums fp32.  The k index of the fragments is a permutation of the head's dims that
 //     lets a lane read 32 consecutive bytes of a key; with the swizzle no two lanes of a
 //     quarter-warp meet in a bank.
-//   p = 2^(S f - m + 8), f = scale log2(e) 2^Ek.  m moves only where a row's largest logit lies
-//     2^7 above it, so a unit costs one vote and no reduction.  z sums p in fp32; P is f16 (11
-//     bits: 2^-12 of a weight; weights down to 2^-16 of the largest keep all of them).
+//   p = 2^((S g - m) f + 8), scale log2(e) 2^Ek = f g with f in [1, 2) and g a power of two: S g is
+//     exact, and so is its difference to a near reference m, however large the logits are (a fused
+//     multiply-add of S and the whole factor against a rounded product is off by 2^8 at logits of 9e7).
+//     m moves only where a row's largest logit lies 2^7 above it, so a unit costs one vote and no
+//     reduction.  z sums p in fp32; P is f16 (11 bits: 2^-12 of a weight; weights down to 2^-16 of the
+//     largest keep all of them).
 //   O^T += V^T P^T: weights of two rows are transposed in registers (movmatrix, 8 x 8); a pair of
 //     tokens' bytes is put side by side by byte permutes and widened to f16x2, exact.  O is kept in
 //     units of 2^Er, the largest 2^Ev met: 2^(Ev - Er) goes into the exponent of p (and out of z).
@@ -42,6 +45,7 @@
 // workspace and are joined by a second kernel, in the order of the list: results repeat bit for bit.
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
@@ -67,6 +71,7 @@ constexpr int kFold = 6;                         // V scales this far below Er g
 constexpr int kNoScale = -1000;                  // Er before the first unit
 constexpr float kNoRef = -1e30f;                 // m before the first logit
 constexpr float kUp = 8.f;                       // weights are 2^kUp at the reference
+constexpr float kLazy = 7.f;                     // a weight may grow by 2^kLazy before m moves
 constexpr int64_t kMinUnits = 8;                 // of a CTA: one for each group of one warp
 
 // Shared memory, in bytes: stages | queries | barriers | sums | seg | jobs | units | prefix sums.
@@ -108,7 +113,9 @@ struct DecodeArgs {
   int B, Q, H, Hkv, G;
   int R, TR, RT;            // rows of an owner and KV head, of a tile, tiles they take
   Div by_hr, by_rt, by_g, by_q, by_n;  // tiles of an owner, tiles of a head, G, Q, units of a list
-  float scale;
+  bool negative;            // |scale| log2(e) = fm 2^fe (1, and a zero's exponent, where that is 0)
+  float fm, lazy, fl;       // fm in [1, 2), kLazy / fm, fm ln 2
+  int fe;
   uint16_t* out;
   float* lse;
   float* rec;               // pieces: [CTA][0: of a tile begun before, 1: begun here][TR][128], m z Er
@@ -200,7 +207,8 @@ struct Rows {
   uint32_t qb[QS ? 1 : NT][8][2];     // row 8 t + g, dims 32 c + 4 j + {0, 1}, + {2, 3}
   uint32_t qs;                        // QS: where the lane's are, two j's together, 512 bytes apart
   float o[8][NT][4];
-  float m[NT][2], z[NT][2], f[NT][2];  // reference, sum, logit factor without 2^Ek
+  float m[NT][2], z[NT][2];            // reference (a score in units of g), sum
+  int fe[NT][2];                       // g = 2^(fe + Ek)
   int er;                              // O is in units of 2^er
 
   __device__ __forceinline__ void clear() {
@@ -219,7 +227,7 @@ struct Rows {
 
   // q rows -> f16 fragments, scaled so that a row's largest element lies in [2^14, 2^15) (exact, but
   // for elements 2^-29 of it; rows whose largest is below 2^-86 lose bits).  v: 32 dims of row 8 t + g.
-  __device__ __forceinline__ void set_q(const uint4 (&v)[NT][4], float scale, int lane) {
+  __device__ __forceinline__ void set_q(const uint4 (&v)[NT][4], const DecodeArgs& a, int lane) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       uint32_t am = 0;
@@ -231,10 +239,9 @@ struct Rows {
       am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
       am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
       const int sigma = am == 0u ? 0 : min(100, max(-113, 14 - ((int)(am >> 23) - 127)));
-      const float up = __uint_as_float((uint32_t)(127 + sigma) << 23) * (scale < 0.f ? -1.f : 1.f);
-      const float fr = fabsf(scale) * 1.44269504f * __uint_as_float((uint32_t)(127 - sigma) << 23);
+      const float up = __uint_as_float((uint32_t)(127 + sigma) << 23) * (a.negative ? -1.f : 1.f);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) f[t][e] = __shfl_sync(0xFFFFFFFFu, fr, (2 * (lane & 3) + e) * 4);
+      for (int e = 0; e < 2; ++e) fe[t][e] = __shfl_sync(0xFFFFFFFFu, a.fe - sigma, (2 * (lane & 3) + e) * 4);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         uint32_t x[4];
@@ -257,7 +264,7 @@ struct Rows {
   // lim(row of the warp) is then a row's last visible token, max_lim the last that any sees.
   template <bool General, class Lim>
   __device__ __forceinline__ void step(uint32_t ka, uint32_t va, int kb, int vb, int tb, int lane, Lim lim,
-                                       int max_lim) {
+                                       int max_lim, const DecodeArgs& a) {
     const int g = lane >> 2, c = lane & 3;
     float s[2][NT][4];  // tokens 16 i + g (rows 2 c, 2 c + 1), then 16 i + g + 8
     constexpr int kI = QS ? 2 : 1;  // 16 tokens at a time, or all: queries are then read once
@@ -293,16 +300,13 @@ struct Rows {
         }
       }
     }
-    // factors stay finite (a score of 0 is a logit of 0 whatever the scales) or NaN
-    const float ek = e8m0_to_float(kb);
-    float fk[NT][2], top[NT][2];
+    // factors stay normal numbers (a score of 0 is a logit of 0 whatever the scales) or NaN
+    float gk[NT][2], top[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        fk[t][e] = f[t][e] * ek;
-        fk[t][e] = fk[t][e] > FLT_MAX ? FLT_MAX : fk[t][e];
-      }
+      for (int e = 0; e < 2; ++e)
+        gk[t][e] = __int_as_float(kb == 255 ? 0x7FC00000 : min(max(fe[t][e] + kb, 1), 254) << 23);
     if constexpr (General) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -312,8 +316,7 @@ struct Rows {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (8 * i + g > rel) s[i >> 1][t][2 * (i & 1) + e] = -INFINITY;
-          // -inf stays -inf: no factor of 0, and no NaN from a scale that the row does not see
-          if (rel < 0 || fk[t][e] < FLT_MIN) fk[t][e] = FLT_MIN;
+          if (rel < 0) gk[t][e] = FLT_MIN;  // no NaN from a scale that the row does not see
         }
     }
     bool above = false;
@@ -321,8 +324,8 @@ struct Rows {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        top[t][e] = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e])) * fk[t][e];
-        above |= top[t][e] > m[t][e] + 7.f;
+        top[t][e] = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e])) * gk[t][e];
+        above |= top[t][e] - m[t][e] > a.lazy;
       }
     if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
@@ -332,8 +335,8 @@ struct Rows {
           float x = top[t][e];
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-          if (x > m[t][e] + 7.f) {
-            const float down = ex2(m[t][e] - x);
+          if (x - m[t][e] > a.lazy) {
+            const float down = ex2((m[t][e] - x) * a.fm);
             m[t][e] = x;
             z[t][e] *= down;
 #pragma unroll
@@ -362,9 +365,9 @@ struct Rows {
       float w[2][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float n = up - m[t][e];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[e][i] = ex2(fmaf(s[i >> 1][t][2 * (i & 1) + e], fk[t][e], n));
+        for (int i = 0; i < 4; ++i)
+          w[e][i] = ex2(fmaf(fmaf(s[i >> 1][t][2 * (i & 1) + e], gk[t][e], -m[t][e]), a.fm, up));
         z[t][e] = fmaf((w[e][0] + w[e][1]) + (w[e][2] + w[e][3]), back, z[t][e]);
       }
 #pragma unroll
@@ -481,8 +484,8 @@ struct Rows {
 __device__ __forceinline__ float row_factor(float z, float er) {
   return z == 0.f ? 0.f : (er < -127.f ? 0.f : e8m0_to_float((uint32_t)((int)er + 127))) / z;
 }
-__device__ __forceinline__ float row_lse(float m, float z) {
-  return z == 0.f ? -INFINITY : (m - kUp + log2f(z)) * 0.69314718f;
+__device__ __forceinline__ float row_lse(const DecodeArgs& a, float m, float z) {
+  return z == 0.f ? -INFINITY : fmaf(m, a.fl, (log2f(z) - kUp) * 0.69314718f);
 }
 
 struct Tile {
@@ -513,8 +516,8 @@ struct Joined {
     m = fmaxf(m, mz.x);
     er = fmaxf(er, mz.z);
   }
-  __device__ __forceinline__ void add(float4 v, float4 mz) {
-    const float f = ex2(mz.x - m), fo = f * ex2(mz.z - er);
+  __device__ __forceinline__ void add(float4 v, float4 mz, float fm) {
+    const float f = ex2((mz.x - m) * fm), fo = f * ex2(mz.z - er);
     z = fmaf(f, mz.y, z);
     acc.x = fmaf(fo, v.x, acc.x);
     acc.y = fmaf(fo, v.y, acc.y);
@@ -528,7 +531,7 @@ __device__ __forceinline__ void put_row(const DecodeArgs& a, const Tile& t, int 
   const int64_t at = row_of<Lists>(a, t, row);
   *reinterpret_cast<uint2*>(a.out + at * kHeadDim + 4 * lane) =
       make_uint2(bf16x2_bits(j.acc.x * f, j.acc.y * f), bf16x2_bits(j.acc.z * f, j.acc.w * f));
-  if (a.lse && lane == 0) a.lse[at] = row_lse(j.m, j.z);
+  if (a.lse && lane == 0) a.lse[at] = row_lse(a, j.m, j.z);
 }
 
 // The owner that unit u belongs to: pref sums the owners' units, HR tiles each.
@@ -805,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
     const int r0 = tile.rt * TR + wig * WR;
     active = r0 < a.R;
     min_lim = base_of(tile) + (Lists ? 0 : a.by_g(r0));
-    w.set_q(q_raw, a.scale, lane);
+    w.set_q(q_raw, a, lane);
     w.clear();
   };
 
@@ -850,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
                             bf16x2_bits(w.o[4 * i + 1][t][e] * x, w.o[4 * i + 1][t][2 + e] * x),
                             bf16x2_bits(w.o[4 * i + 2][t][e] * x, w.o[4 * i + 2][t][2 + e] * x),
                             bf16x2_bits(w.o[4 * i + 3][t][e] * x, w.o[4 * i + 3][t][2 + e] * x));
-        if (a.lse && lane < 4) a.lse[at] = row_lse(w.m[t][e], w.z[t][e]);
+        if (a.lse && lane < 4) a.lse[at] = row_lse(a, w.m[t][e], w.z[t][e]);
       }
   };
 
@@ -877,12 +880,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       const uint32_t ka = ring + st * kStepBytes, va = ka + kSub * kFp8Row;
       const int kb = u.w & 0xFF, vb = (u.w >> 8) & 0xFF;
       if (u.y + kSub - 1 <= min_lim && vb >= w.er + 127 - kFold && vb != 255) {
-        w.template step<false>(ka, va, kb, vb, u.y, lane, 0, 0);
+        w.template step<false>(ka, va, kb, vb, u.y, lane, 0, 0, a);
       } else {
         const Tile tile = tile_of(a, tile_id);
         const int base = base_of(tile), r0 = tile.rt * TR + wig * WR;
         auto lim = [&](int r) { return r0 + r >= a.R ? -1 : Lists ? base : base + a.by_g(r0 + r); };
-        w.template step<true>(ka, va, kb, vb, u.y, lane, lim, lim(min(WR, a.R - r0) - 1));
+        w.template step<true>(ka, va, kb, vb, u.y, lane, lim, lim(min(WR, a.R - r0) - 1), a);
       }
     }
     __syncwarp();
@@ -973,11 +976,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           const float* const y = p + (x * TR + r) * kRecRow;
-          j[r].add(*reinterpret_cast<const float4*>(y + 4 * lane), *reinterpret_cast<const float4*>(y + kHeadDim));
+          j[r].add(*reinterpret_cast<const float4*>(y + 4 * lane), *reinterpret_cast<const float4*>(y + kHeadDim), a.fm);
         }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      j[r].add(tail_o[r], tail_mz[r]);
+      j[r].add(tail_o[r], tail_mz[r], a.fm);
       const int row = t.rt * TR + r0 + r;
       if (row >= a.R) continue;
       if (job.w == 2) {
@@ -1019,7 +1022,7 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(const __grid_constant__ D
     }
 #pragma unroll 8
     for (int x = blockIdx.x + part; x <= last; x += 4)
-      j.add(*reinterpret_cast<const float4*>(a.rec + slot(x) * kHeadDim + 4 * lane), recmz[slot(x)]);
+      j.add(*reinterpret_cast<const float4*>(a.rec + slot(x) * kHeadDim + 4 * lane), recmz[slot(x)], a.fm);
   }
   acc_s[warp][lane] = j.acc;
   if (lane == 0) z_s[warp] = j.z;
@@ -1157,7 +1160,12 @@ cudaError_t launch_fp8_decode(const uint16_t* q, int64_t B, int Q, int H, int Hk
   a.Hkv = Hkv;
   a.G = H / Hkv;
   a.R = block_idx ? a.G : Q * a.G;
-  a.scale = scale;
+  a.negative = scale < 0.f;
+  const double factor = std::fabs((double)scale) * 1.4426950408889634;
+  a.fe = factor == 0.0 ? -4096 : std::ilogb(factor);
+  a.fm = factor == 0.0 ? 1.f : (float)std::scalbn(factor, -a.fe);
+  a.lazy = kLazy / a.fm;
+  a.fl = (float)((factor == 0.0 ? 1.0 : std::scalbn(factor, -a.fe)) * 0.6931471805599453);
   a.out = out;
   a.lse = lse;
   a.rec = static_cast<float*>(ws);

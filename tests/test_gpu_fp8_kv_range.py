@@ -1,0 +1,92 @@
+"""The 8-bit cache's attention and append where numbers leave the usual range: logits of any size,
+V scales any powers apart, results next to the least bf16, angles of slow pairs; against float64."""
+import math
+
+import pytest
+import torch
+
+import _fp8_ref as R
+import mxfp4_sparse_paged_gb300 as m
+from test_gpu_fp8_kv import append, attention, clean, tables  # noqa: F401 (clean: a fixture)
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F64, E4M3 = torch.float64, torch.float8_e4m3fn
+
+
+def codes(x):
+    return torch.as_tensor(x, dtype=torch.float32).to(E4M3).view(torch.uint8)
+
+
+def near(out, lse, want, exact=False):
+    """out: half a step of bf16 (2^-8 of the value, 2^-134 where it is subnormal), and of sum w |V| 2^-11
+    (weights of 11 bits, 2^-12 each, and fp32 sums) and twice the logits' error: 2^-18 of sum |q| |K| for
+    128 products summed in fp32, 0 where the sums are exact.  lse: that error, and fp32 of a logit (2^-22
+    holds its product and two sums).  Nothing absolute: a small result is held to its own size."""
+    w, wl, mag, big = want
+    out, lse = out.double().cpu(), lse.double().cpu()
+    dl = torch.zeros_like(big) if exact else 2.0**-18 * (big + 1)
+    tol = 2.0**-8 * w.abs() + (2.0**-11 + 2 * dl[..., None]) * mag + 2.0**-134
+    bad = ~((out - w).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4], out[bad][:4], w[bad][:4])
+    fin = torch.isfinite(wl)
+    assert torch.equal(lse == -math.inf, wl == -math.inf) and torch.isfinite(lse[fin]).all()
+    assert ((lse - wl).abs()[fin] <= 2.0**-22 * wl.abs()[fin] + 1e-6 + dl[fin]).all()
+
+
+# ------------------------------------------------------------------ logits
+
+def one_dim(size, sign, lo=1.0):
+    """Queries of one element, keys of E4M3 numbers in lo .. 448 there: every score is one exact
+    product, tokens of one code tie, others lie 2^-4 of the logit apart."""
+    def edit(q, kp, ks, vp, vs, table):
+        g = torch.Generator().manual_seed(1)
+        x = torch.exp2(torch.rand(kp.numel() // 128, generator=g) * math.log2(448 / lo)).mul_(lo).clamp_max_(448)
+        kp.view(-1, 128).zero_()
+        kp.view(-1, 128)[:, 5] = codes(x)
+        ks[:] = 127
+        q.zero_()
+        q[:, :, 5] = sign * size / 448 * math.sqrt(128)  # scale is 1 / sqrt(128)
+    return edit
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [9e7, 3e8, 5e8, 2e9, 1e12, 1e20])
+def test_large_logits(size, sign):
+    """Of logits far apart the largest alone counts, and those that tie with it, whatever its size."""
+    for q, H, Hkv in ((1, 16, 1), (4, 20, 4), (3, 8, 1), (4, 16, 1)):
+        out, lse, want, _ = attention([300, 40, 1, 129, 700], q, H, Hkv, seed=q, edit=one_dim(size, sign))
+        near(out, lse, want, exact=True)
+    m.mx4_check_status()
+
+
+def test_large_logits_long():
+    """Pieces of a row in many CTAs, and lists."""
+    for size, sign in ((5e8, 1), (2e9, -1)):
+        out, lse, want, _ = attention([30000, 5000], 1, 16, 1, seed=5, edit=one_dim(size, sign))
+        near(out, lse, want, exact=True)
+        blocks = [[3, 0, 30, 7], [5, 5, 2, 39]]
+        out, lse, want, _ = attention([30000, 5000], 1, 16, 1, seed=5, blocks=blocks, edit=one_dim(size, sign))
+        near(out, lse, want, exact=True)
+
+
+@pytest.mark.parametrize("size,unit", [(2.0**20, 1), (2.0**23, 1), (2.0**25, 4)])
+def test_logits_large_and_near(size, unit):
+    """Logits of 2^20 to 2^25 that differ by `unit` up to 12: two exact products whose sum has 24 bits,
+    so that the weights are as exact as those of small logits."""
+    def edit(q, kp, ks, vp, vs, table):
+        g = torch.Generator().manual_seed(2)
+        rows = kp.view(-1, 128)
+        rows.zero_()
+        # larger ones later: references move again and again
+        rank = torch.arange(rows.shape[0]) % 128 / 128.0
+        x = 12 * torch.rand(rows.shape[0], generator=g) * (0.2 + rank)
+        rows[:, 0] = codes(256.0)
+        rows[:, 7] = codes((x / unit).round().mul(unit).clamp(0, 12))
+        ks[:] = 127
+        q.zero_()
+        q[:, :, 0] = size / 256
+        q[:, :, 7] = 1.0
+    for q, H, Hkv in ((1, 16, 1), (4, 20, 4), (3, 8, 1)):
+        out, lse, want, _ = attention([700, 64, 2000], q, H, Hkv, seed=7, scale=1.0, edit=edit)
+        near(out, lse, want, exact=True)
