@@ -69,7 +69,7 @@ constexpr int kMaxOwners = 2048;                 // sequences of a launch (their
 constexpr int kRecRow = kHeadDim + 4;            // floats of a row in shared memory: O, m, z, Er
 constexpr int kFold = 6;                         // V scales this far below Er go into the weights
 constexpr int kNoScale = -1000;                  // Er before the first unit
-constexpr float kNoRef = -1e30f;                 // m before the first logit
+constexpr float kNoRef = -FLT_MAX;               // m before the first logit: no logit lies below it
 constexpr float kUp = 8.f;                       // weights are 2^kUp at the reference
 constexpr float kLazy = 7.f;                     // a weight may grow by 2^kLazy before m moves
 constexpr int64_t kMinUnits = 8;                 // of a CTA: one for each group of one warp

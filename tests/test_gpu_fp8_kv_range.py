@@ -51,7 +51,7 @@ def one_dim(size, sign, lo=1.0):
 
 
 @pytest.mark.parametrize("sign", [1, -1])
-@pytest.mark.parametrize("size", [9e7, 3e8, 5e8, 2e9, 1e12, 1e20])
+@pytest.mark.parametrize("size", [9e7, 3e8, 5e8, 2e9, 1e12, 1e20, 1e30, 1e36])
 def test_large_logits(size, sign):
     """Of logits far apart the largest alone counts, and those that tie with it, whatever its size."""
     for q, H, Hkv in ((1, 16, 1), (4, 20, 4), (3, 8, 1), (4, 16, 1)):
@@ -62,7 +62,7 @@ def test_large_logits(size, sign):
 
 def test_large_logits_long():
     """Pieces of a row in many CTAs, and lists."""
-    for size, sign in ((5e8, 1), (2e9, -1)):
+    for size, sign in ((5e8, 1), (2e9, -1), (1e31, -1)):
         out, lse, want, _ = attention([30000, 5000], 1, 16, 1, seed=5, edit=one_dim(size, sign))
         near(out, lse, want, exact=True)
         blocks = [[3, 0, 30, 7], [5, 5, 2, 39]]
