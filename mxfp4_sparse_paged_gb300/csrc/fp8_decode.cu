@@ -480,10 +480,18 @@ struct Rows {
   }
 };
 
-// A finished row from O (units 2^(m - kUp + er)), m and z: what O is multiplied by, and the lse.
-__device__ __forceinline__ float row_factor(float z, float er) {
-  return z == 0.f ? 0.f : (er < -127.f ? 0.f : e8m0_to_float((uint32_t)((int)er + 127))) / z;
-}
+// A finished row from O (units 2^(m - kUp + er)), m and z: O / z first, then its unit (2^er / z may lie
+// below fp32's range where the result does not), and the lse.
+struct Finish {
+  float inv, unit, rest;
+  __device__ __forceinline__ Finish(float z, float er) {
+    const int e = (int)er, e0 = min(max(e, -126), 127), e1 = max(e - e0, -126);
+    inv = z == 0.f ? 0.f : 1.f / z;
+    unit = __int_as_float((e0 + 127) << 23);
+    rest = __int_as_float((e1 + 127) << 23);
+  }
+  __device__ __forceinline__ float operator()(float o) const { return o * inv * unit * rest; }
+};
 __device__ __forceinline__ float row_lse(const DecodeArgs& a, float m, float z) {
   return z == 0.f ? -INFINITY : fmaf(m, a.fl, (log2f(z) - kUp) * 0.69314718f);
 }
@@ -527,10 +535,10 @@ struct Joined {
 };
 template <bool Lists>
 __device__ __forceinline__ void put_row(const DecodeArgs& a, const Tile& t, int row, const Joined& j, int lane) {
-  const float f = row_factor(j.z, j.er);
+  const Finish f(j.z, j.er);
   const int64_t at = row_of<Lists>(a, t, row);
   *reinterpret_cast<uint2*>(a.out + at * kHeadDim + 4 * lane) =
-      make_uint2(bf16x2_bits(j.acc.x * f, j.acc.y * f), bf16x2_bits(j.acc.z * f, j.acc.w * f));
+      make_uint2(bf16x2_bits(f(j.acc.x), f(j.acc.y)), bf16x2_bits(f(j.acc.z), f(j.acc.w)));
   if (a.lse && lane == 0) a.lse[at] = row_lse(a, j.m, j.z);
 }
 
@@ -845,14 +853,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
         const int r = tile.rt * TR + wig * WR + 8 * t + 2 * (lane & 3) + e;
         if (r >= a.R) continue;
         const int64_t at = row_of<Lists>(a, tile, r);
-        const float x = row_factor(w.z[t][e], (float)w.er);
+        const Finish f(w.z[t][e], (float)w.er);
         uint4* const p = reinterpret_cast<uint4*>(a.out + at * kHeadDim + 16 * (lane >> 2));
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          p[i] = make_uint4(bf16x2_bits(w.o[4 * i][t][e] * x, w.o[4 * i][t][2 + e] * x),
-                            bf16x2_bits(w.o[4 * i + 1][t][e] * x, w.o[4 * i + 1][t][2 + e] * x),
-                            bf16x2_bits(w.o[4 * i + 2][t][e] * x, w.o[4 * i + 2][t][2 + e] * x),
-                            bf16x2_bits(w.o[4 * i + 3][t][e] * x, w.o[4 * i + 3][t][2 + e] * x));
+          p[i] = make_uint4(bf16x2_bits(f(w.o[4 * i][t][e]), f(w.o[4 * i][t][2 + e])),
+                            bf16x2_bits(f(w.o[4 * i + 1][t][e]), f(w.o[4 * i + 1][t][2 + e])),
+                            bf16x2_bits(f(w.o[4 * i + 2][t][e]), f(w.o[4 * i + 2][t][2 + e])),
+                            bf16x2_bits(f(w.o[4 * i + 3][t][e]), f(w.o[4 * i + 3][t][2 + e])));
         if (a.lse && lane < 4) a.lse[at] = row_lse(a, w.m[t][e], w.z[t][e]);
       }
   };

@@ -90,3 +90,28 @@ def test_logits_large_and_near(size, unit):
     for q, H, Hkv in ((1, 16, 1), (4, 20, 4), (3, 8, 1)):
         out, lse, want, _ = attention([700, 64, 2000], q, H, Hkv, seed=7, scale=1.0, edit=edit)
         near(out, lse, want, exact=True)
+
+
+# ------------------------------------------------------------------ V scales
+
+@pytest.mark.parametrize("byte", [0, 1, 6, 12, 20])
+def test_small_results_of_long_contexts(byte):
+    """Near-equal weights of many tokens, values next to the least normal number."""
+    def edit(q, kp, ks, vp, vs, table):
+        vs[:] = byte
+        vp[:] = codes(100.0)
+        q.mul_(0.01)
+    for lens, q, H in (([12000], 1, 16), ([32768, 500], 1, 16), ([300, 40], 1, 16), ([9000], 4, 10)):
+        out, lse, want, _ = attention(lens, q, H, 1, seed=10, edit=edit)
+        near(out, lse, want)
+
+
+def test_usual_values_held_to_their_size():
+    """The bound without an absolute part on usual inputs, and on V scales of 2^-127."""
+    for q, H, Hkv in ((1, 16, 1), (2, 7, 1), (4, 20, 4), (3, 24, 4), (8, 16, 1)):
+        for v in (None, 0):
+            def edit(qq, kp, ks, vp, vs, table):
+                if v is not None:
+                    vs[:] = v
+            out, lse, want, _ = attention([0, 1, 33, 160, 700], q, H, Hkv, seed=q, edit=edit)
+            near(out, lse, want)
