@@ -31,11 +31,12 @@
 //   O^T += V^T P^T: weights of two rows are transposed in registers (movmatrix, 8 x 8); a pair of
 //     tokens' bytes is put side by side by byte permutes and widened to f16x2, exact.  O is kept in
 //     units of 2^Er, the largest 2^Ev met: 2^(Ev - Er) goes into the exponent of p (and out of z).
-//     The product of a unit with Ev more than 6 below Er is scaled in fp32 before it is added, so
-//     scales of any two blocks may be any powers apart.
+//     The product of a unit with Ev more than 6 below Er is scaled in fp32 before it is added.
 // Such units, and those where some row does not see all 32 tokens (a sequence's end), take a second form
 // of the step: scores are masked, and values that no row sees, and NaN codes, are kept from the product
-// (clean() below).
+// (clean() below).  Where Ev lies 2^30 above the first unit's, or 2^60 below Er, O gets a unit for which
+// it and the product both stay fp32 numbers, by what the rows hold and what they give weight (renorm()
+// below): a row keeps its sum beside blocks of any scale that it does not see, or gives no weight.
 // The tensor memory path (tcgen05) computes 128-row tiles from shared memory, and puts scores and weights
 // through tensor and shared memory on the way: a form with it took 116 us where this one takes 77
 // (32 sequences of 8192 to 16384 tokens, 64 rows of a KV head).
@@ -69,12 +70,17 @@ constexpr int kMaxOwners = 2048;                 // sequences of a launch (their
 constexpr int kRecRow = kHeadDim + 4;            // floats of a row in shared memory: O, m, z, Er
 constexpr int kFold = 6;                         // V scales this far below Er go into the weights
 constexpr int kNoScale = -1000;                  // Er before the first unit
+constexpr int kSpan = 30;                        // Er may grow by 2^kSpan beyond the first before renorm()
+constexpr int kFar = 60;                         // V scales this far below Er need it too
+constexpr int kTop = 100;                        // it leaves numbers up to 2^kTop
+constexpr int kMost = 29;                        // a unit's product is below 2^kMost: 32 weights of 2^15, 448
 constexpr float kNoRef = -FLT_MAX;               // m before the first logit: no logit lies below it
 constexpr float kUp = 8.f;                       // weights are 2^kUp at the reference
 constexpr float kLazy = 7.f;                     // a weight may grow by 2^kLazy before m moves
 constexpr int64_t kMinUnits = 8;                 // of a CTA: one for each group of one warp
 
-// Shared memory, in bytes: stages | queries | barriers | sums | seg | jobs | units | prefix sums.
+// Shared memory, in bytes: stages | queries | barriers | sums | seg | jobs | units | Er |
+// prefix sums.
 template <int NT>
 struct Layout {
   static constexpr int kQOff = stages_of(NT) * kStepBytes;  // [warp][NT][4][32 lanes] of 16 bytes
@@ -83,7 +89,8 @@ struct Layout {
   static constexpr int kSegOff = kSumOff + 16 * 8;       // [group]: last tile, first tile if it began before
   static constexpr int kJobOff = kSegOff + kWarps * 8;   // tiles whose pieces are joined
   static constexpr int kUnitOff = kJobOff + (kWarps + 2) * 16;  // [group][64]: units looked up ahead
-  static constexpr int kPrefOff = kUnitOff + kWarps * 64 * 16;
+  static constexpr int kErOff = kUnitOff + kWarps * 64 * 16;  // [warp][8 NT]: Er of rows, where they differ
+  static constexpr int kPrefOff = kErOff + kWarps * 8 * NT * 4;
   static constexpr int kBytes = kPrefOff + kMaxOwners * 8 + 1024;  // 1024: the stages' alignment
   static_assert(kUnitOff % 16 == 0 && kJobOff % 16 == 0 && kBytes <= 232448, "shared memory");
 };
@@ -210,6 +217,8 @@ struct Rows {
   float m[NT][2], z[NT][2];            // reference (a score in units of g), sum
   int fe[NT][2];                       // g = 2^(fe + Ek)
   int er;                              // O is in units of 2^er
+  int cap;                             // the largest scale byte that needs no renorm(); -1: rows have Er of
+  uint32_t er_at;                      // their own, here
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -223,6 +232,12 @@ struct Rows {
       }
     }
     er = kNoScale;
+    cap = 254;
+  }
+  __device__ __forceinline__ int row_er(int r) const {
+    int x = er;
+    if (cap < 0) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(x) : "r"(er_at + r * 4) : "memory");
+    return x;
   }
 
   // q rows -> f16 fragments, scaled so that a row's largest element lies in [2^14, 2^15) (exact, but
@@ -347,8 +362,10 @@ struct Rows {
           }
         }
     }
-    if (vb - 127 > er && vb != 255) {  // O to the new unit (nothing is in it before the first)
+    const bool far = General && vb != 255 && (vb > cap || vb - 127 < er - kFar);
+    if (vb - 127 > er && vb != 255 && !far) {  // O to the new unit (nothing is in it before the first)
       const float down = er == kNoScale ? 0.f : ex2((float)(er - vb + 127));
+      if (er == kNoScale) cap = min(254, vb + kSpan);
       er = vb - 127;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -373,6 +390,17 @@ struct Rows {
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[i][t] = transpose8(half2_bits(w[0][i], w[1][i]));
     }
+    float ev[General ? NT : 1][2];  // 2^(Ev - Er); 0 for rows that see none: a scale of NaN is not theirs
+    if constexpr (General) {
+      if (far) renorm(p, vb - 127, lane);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * t + 2 * c + e;
+          ev[t][e] = lim(r) < tb ? 0.f : vb == 255 ? e8m0_to_float(255) : ex2(fminf((float)(vb - 127 - row_er(r)), 127.f));
+        }
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       uint4 y[4];  // tokens 16 k + 2 c + {0, 1, 8, 9}, dims 16 g .. 16 g + 15
@@ -389,7 +417,6 @@ struct Rows {
           for (int t = 0; t < NT; ++t) mma(o[j][t], v, p[2 * k][t], p[2 * k + 1][t]);
         }
       } else {
-        const float ev = vb == 255 ? e8m0_to_float(255) : ex2((float)(vb - 127 - er));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           uint32_t v[4];
@@ -399,12 +426,71 @@ struct Rows {
             float x[4];
             mma0(x, v, p[2 * k][t], p[2 * k + 1][t]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)  // a scale of NaN reaches only rows that see its tokens
-              o[j][t][e] = fmaf(lim(8 * t + 2 * c + (e & 1)) < tb ? 0.f : ev, x[e], o[j][t][e]);
+            for (int e = 0; e < 4; ++e) o[j][t][e] = fmaf(ev[t][e & 1], x[e], o[j][t][e]);
           }
         }
       }
     }
+  }
+
+  // O to a unit in which it, and the product to come of weights p and values of scale 2^ev, is below
+  // 2^(kTop + 1): the least such unit, so that what is far smaller stays too.  One for all rows where
+  // theirs lie within 2^40, else one each; rows without weight here do not count the product.
+  __device__ __forceinline__ void renorm(const uint32_t (&p)[4][NT], int ev, int lane) {
+    const int c = lane & 3;
+    int want[NT][2], most = kNoScale, least = 1 << 20;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t any = p[0][t] | p[1][t] | p[2][t] | p[3][t];  // of row 8 t + g
+      any |= __shfl_xor_sync(0xFFFFFFFFu, any, 1);
+      any |= __shfl_xor_sync(0xFFFFFFFFu, any, 2);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool weight = __shfl_sync(0xFFFFFFFFu, any, (2 * c + e) * 4) != 0u;
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(o[j][t][e]), fabsf(o[j][t][2 + e])));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        int x = kNoScale;
+        if (top > 0.f) x = row_er(8 * t + 2 * c + e) + (int)(__float_as_uint(top) >> 23) - 127 - kTop;
+        if (weight) x = max(x, ev + kMost - kTop);
+        if (x != kNoScale) {
+          x = max(x, kNoScale / 2);  // (below any result)
+          least = min(least, x);
+        }
+        want[t][e] = x;
+        most = max(most, x);
+      }
+    }
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    least = __reduce_min_sync(0xFFFFFFFFu, least);
+    const bool same = most - least <= 40;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (same) want[t][e] = most;
+        const int r = 8 * t + 2 * c + e, old = row_er(r);
+        const int up = old == kNoScale || want[t][e] == kNoScale ? 0 : min(252, max(-252, old - want[t][e]));
+        const float f0 = __int_as_float((127 + up / 2) << 23), f1 = __int_as_float((127 + up - up / 2) << 23);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j][t][e] = o[j][t][e] * f0 * f1;
+          o[j][t][2 + e] = o[j][t][2 + e] * f0 * f1;
+        }
+      }
+    __syncwarp();
+    if (!same && lane < 4)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          asm volatile("st.shared.s32 [%0], %1;" ::"r"(er_at + (8 * t + 2 * c + e) * 4), "r"(want[t][e]) : "memory");
+    __syncwarp();
+    er = most;
+    // (what is now 2^60 to 2^kTop may go down by 2^101 before the next time)
+    cap = !same ? -1 : most == kNoScale ? 254 : min(254, most + 127 + kTop - kMost + kSpan);
   }
 
   // Dims 2 j, 2 j + 1 of the lane's as f16: tokens 2 c, 2 c + 1 of the four, then 2 c + 8, 2 c + 9.
@@ -475,7 +561,7 @@ struct Rows {
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<float4*>(p + r * row_floats + 16 * g + 4 * i) =
               make_float4(o[2 * i][t][e], o[2 * i][t][2 + e], o[2 * i + 1][t][e], o[2 * i + 1][t][2 + e]);
-        if (g == 0) *reinterpret_cast<float4*>(mz + r * mz_floats) = make_float4(m[t][e], z[t][e], (float)er, 0.f);
+        if (g == 0) *reinterpret_cast<float4*>(mz + r * mz_floats) = make_float4(m[t][e], z[t][e], (float)row_er(r), 0.f);
       }
   }
 };
@@ -520,17 +606,22 @@ __device__ __forceinline__ int64_t row_of(const DecodeArgs& a, const Tile& t, in
 struct Joined {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float z = 0.f, m = kNoRef, er = kNoScale;
-  __device__ __forceinline__ void see(float4 mz) {  // all pieces, before the first is added
-    m = fmaxf(m, mz.x);
-    er = fmaxf(er, mz.z);
+  // All pieces, before the first is added.  er: the largest of theirs, each less what its weights go
+  // down by, so that a large unit without weight takes nothing from the others.
+  __device__ __forceinline__ void see(float x, float unit, float fm) {
+    const float top = fmaxf(m, x);
+    er = fmaxf(er + (m - top) * fm, unit + (x - top) * fm);
+    m = top;
   }
+  __device__ __forceinline__ void see(float4 mz, float fm) { see(mz.x, mz.z, fm); }
+  __device__ __forceinline__ void seen() { er = rintf(fmaxf(er, (float)kNoScale)); }  // a whole power of two
   __device__ __forceinline__ void add(float4 v, float4 mz, float fm) {
-    const float f = ex2((mz.x - m) * fm), fo = f * ex2(mz.z - er);
-    z = fmaf(f, mz.y, z);
-    acc.x = fmaf(fo, v.x, acc.x);
-    acc.y = fmaf(fo, v.y, acc.y);
-    acc.z = fmaf(fo, v.z, acc.z);
-    acc.w = fmaf(fo, v.w, acc.w);
+    const float d = (mz.x - m) * fm, fo = ex2(0.5f * (d + (mz.z - er)));  // twice: large sums of small units
+    z = fmaf(ex2(d), mz.y, z);
+    acc.x = fmaf(fo, fo * v.x, acc.x);
+    acc.y = fmaf(fo, fo * v.y, acc.y);
+    acc.z = fmaf(fo, fo * v.z, acc.z);
+    acc.w = fmaf(fo, fo * v.w, acc.w);
   }
 };
 template <bool Lists>
@@ -792,6 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
 
   Rows<NT> w;
   w.qs = base_at + Lay::kQOff + warp * NT * 2048 + lane * 16;
+  w.er_at = base_at + Lay::kErOff + warp * WR * 4;
   int tile_id = -1, min_lim = 0;  // of the warp's rows: the least last visible token
   bool active = false;            // this warp has rows of the tile
   uint4 q_raw[NT][4];
@@ -853,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
         const int r = tile.rt * TR + wig * WR + 8 * t + 2 * (lane & 3) + e;
         if (r >= a.R) continue;
         const int64_t at = row_of<Lists>(a, tile, r);
-        const Finish f(w.z[t][e], (float)w.er);
+        const Finish f(w.z[t][e], (float)w.row_er(8 * t + 2 * (lane & 3) + e));
         uint4* const p = reinterpret_cast<uint4*>(a.out + at * kHeadDim + 16 * (lane >> 2));
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -887,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
     if (u.z >= 0 && active) {
       const uint32_t ka = ring + st * kStepBytes, va = ka + kSub * kFp8Row;
       const int kb = u.w & 0xFF, vb = (u.w >> 8) & 0xFF;
-      if (u.y + kSub - 1 <= min_lim && vb >= w.er + 127 - kFold && vb != 255) {
+      if (u.y + kSub - 1 <= min_lim && vb >= w.er + 127 - kFold && vb <= w.cap) {  // (255 is above it)
         w.template step<false>(ka, va, kb, vb, u.y, lane, 0, 0, a);
       } else {
         const Tile tile = tile_of(a, tile_id);
@@ -976,9 +1068,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
       if (seg[x].x == job.x)
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
-          j[r].see(*reinterpret_cast<const float4*>(p + (x * TR + r) * kRecRow + kHeadDim));
+          j[r].see(*reinterpret_cast<const float4*>(p + (x * TR + r) * kRecRow + kHeadDim), a.fm);
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) j[r].see(tail_mz[r]);
+    for (int r = 0; r < kRows; ++r) {
+      j[r].see(tail_mz[r], a.fm);
+      j[r].seen();
+    }
     for (int x = g0; x <= g1; ++x)
       if (seg[x].x == job.x)
 #pragma unroll
@@ -1022,12 +1117,13 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(const __grid_constant__ D
   };
   Joined j;
   if (row < a.R) {
-    for (int x = blockIdx.x + lane; x <= last; x += 32) j.see(recmz[slot(x)]);
+    for (int x = blockIdx.x + lane; x <= last; x += 32) j.see(recmz[slot(x)], a.fm);
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
-      j.m = fmaxf(j.m, __shfl_xor_sync(0xFFFFFFFFu, j.m, d));
-      j.er = fmaxf(j.er, __shfl_xor_sync(0xFFFFFFFFu, j.er, d));
+      const float x = __shfl_xor_sync(0xFFFFFFFFu, j.m, d);
+      j.see(x, __shfl_xor_sync(0xFFFFFFFFu, j.er, d), a.fm);
     }
+    j.seen();
 #pragma unroll 8
     for (int x = blockIdx.x + part; x <= last; x += 4)
       j.add(*reinterpret_cast<const float4*>(a.rec + slot(x) * kHeadDim + 4 * lane), recmz[slot(x)], a.fm);

@@ -94,6 +94,113 @@ def test_logits_large_and_near(size, unit):
 
 # ------------------------------------------------------------------ V scales
 
+def v_scale(blocks, low=20, rest=None):
+    """V scales `low`, and those of 32-token blocks (sequence, block) `blocks[...]`."""
+    def edit(q, kp, ks, vp, vs, table):
+        vs[:] = low
+        for (s, b), e in blocks.items():
+            vs[table[s, b // 4], :, b % 4] = e
+        if rest:
+            rest(q, kp, ks, vp, vs, table)
+    return edit
+
+
+@pytest.mark.parametrize("high", [150, 200, 247])
+@pytest.mark.parametrize("q,H,Hkv", [(2, 16, 1), (2, 4, 2), (8, 3, 1), (3, 16, 1), (8, 16, 1)])
+def test_a_large_scale_out_of_sight(q, H, Hkv, high):
+    """The last tokens begin a block whose V scale is far above the others: the queries before them
+    keep their small results."""
+    edit = v_scale({(0, 1): high, (1, 8): high, (2, 4): high})
+    out, lse, want, _ = attention([33, 257, 128 + q - 1], q, H, Hkv, seed=3, edit=edit)
+    near(out, lse, want)
+
+
+@pytest.mark.parametrize("low,high", [(0, 130), (0, 247), (20, 150), (60, 240)])
+@pytest.mark.parametrize("q,H,Hkv", [(1, 16, 1), (2, 12, 1), (4, 16, 1), (1, 8, 2)])
+def test_a_large_scale_without_weight(q, H, Hkv, low, high):
+    """Blocks of far larger V scales and logits 300 below the others' (weights of 2^-430), first, in the
+    middle and last; every other head gives them all its weight."""
+    def rest(qq, kp, ks, vp, vs, table):
+        rows = kp.view(*kp.shape[:2], 128, 128)
+        rows[..., 3] = 0
+        for s, b in far:
+            rows[table[s, b // 4], :, b % 4 * 32:b % 4 * 32 + 32, 3] = codes(-448.0)
+        qq[:, :, 3] = 1000.0
+        qq[:, 1::2, 3] = -1000.0
+    far = [(0, 0), (0, 5), (1, 7), (2, 40), (2, 93)]
+    edit = v_scale({x: high for x in far}, low, rest)
+    out, lse, want, _ = attention([300, 256, 3000], q, H, Hkv, seed=4, klo=120, khi=121, edit=edit)
+    near(out, lse, want)
+
+
+@pytest.mark.parametrize("high", [140, 247])
+def test_a_large_scale_in_another_piece(high):
+    """Pieces of a row in several CTAs, one with a block of a far larger V scale and no weight."""
+    def rest(qq, kp, ks, vp, vs, table):
+        rows = kp.view(*kp.shape[:2], 128, 128)
+        rows[..., 3] = 0
+        rows[table[0, 61], :, 64:96, 3] = codes(-448.0)
+        qq[:, :, 3] = 1000.0
+    edit = v_scale({(0, 61 * 4 + 2): high}, 8, rest)
+    for q in (1, 2):
+        out, lse, want, _ = attention([20000], q, 16, 1, seed=6, klo=120, khi=121, edit=edit)
+        near(out, lse, want)
+
+
+def test_scales_climb():
+    """V scales that grow by powers of 2^40 along a sequence, the weight on the first block."""
+    def rest(qq, kp, ks, vp, vs, table):
+        rows = kp.view(*kp.shape[:2], 128, 128)
+        rows[..., 3] = codes(-448.0)
+        rows[table[0, 0], :, :32, 3] = 0
+        qq[:, :, 3] = 1000.0
+    edit = v_scale({(0, b): 7 + 40 * b for b in range(1, 7)}, 10, rest)
+    for q, H in ((1, 16), (3, 8), (4, 16)):
+        out, lse, want, _ = attention([210], q, H, 1, seed=8, klo=120, khi=121, edit=edit)
+        near(out, lse, want)
+
+
+def test_some_weight_on_a_large_scale():
+    """A weight of 2^-14 on a block whose V scale is 2^70 and more above: it decides the result."""
+    def rest(qq, kp, ks, vp, vs, table):
+        rows = kp.view(*kp.shape[:2], 128, 128)
+        rows[..., 3] = 0
+        rows[table[0, 1], :, 32:64, 3] = codes(-9.0)
+        qq.zero_()
+        qq[:, :, 3] = 1.0
+    edit = v_scale({(0, 5): 180}, 90, rest)
+    for q, H in ((1, 16), (3, 8), (4, 16)):
+        out, lse, want, _ = attention([300], q, H, 1, seed=9, klo=127, khi=128, scale=1.0, edit=edit)
+        near(out, lse, want, exact=True)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("q,H,Hkv", [(1, 16, 1), (3, 8, 2), (3, 8, 1), (8, 16, 1), (2, 20, 4)])
+def test_scales_and_levels(q, H, Hkv, zeros):
+    """Each block's V scale is any power of two (or a third of the blocks are zeros of the least scale,
+    the others usual), its logits are about 0 or 309 above or below; odd heads see that upside down."""
+    def edit(qq, kp, ks, vp, vs, table):
+        g = torch.Generator().manual_seed(q)
+        level = torch.randint(-1, 2, (*ks.shape[:2], 4, 1), generator=g) * 448.0
+        rows = kp.view(*kp.shape[:2], 4, 32, 128)
+        rows[..., 3] = codes(level).expand(-1, -1, -1, 32)
+        if zeros:
+            at = torch.rand(vs.shape, generator=g) < 1 / 3
+            vs[at] = 0
+            vp.view(*vs.shape, 4096)[at] = 0
+        else:
+            vs[:] = torch.randint(0, 248, vs.shape, generator=g, dtype=torch.uint8)
+        qq[:, :, 3] = 1000.0
+        qq[:, 1::2, 3] = -1000.0
+    lens = [6000, 33, 700, 31, 64, 129]
+    out, lse, want, _ = attention(lens, q, H, Hkv, seed=q, klo=120, khi=121, edit=edit)
+    near(out, lse, want)
+    g = torch.Generator().manual_seed(q)
+    blocks = [torch.randperm((L - q + j) // 128 + 1, generator=g)[:12].tolist() for L in lens for j in range(q)]
+    out, lse, want, _ = attention(lens, q, H, Hkv, seed=q, blocks=blocks, klo=120, khi=121, edit=edit)
+    near(out, lse, want)
+
+
 @pytest.mark.parametrize("byte", [0, 1, 6, 12, 20])
 def test_small_results_of_long_contexts(byte):
     """Near-equal weights of many tokens, values next to the least normal number."""
