@@ -217,7 +217,8 @@ __device__ __forceinline__ int grow(const Block& b, uint32_t top, int old, int i
 }
 
 __device__ __forceinline__ void store_row(const Block& b, int row, float4 x, int e, int lane) {
-  const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e, e in [-127, 120]
+  // 2^-e, e in [-127, 127] (above 120 where the stored scale is): 2^-127 is no normal number
+  const float down = __uint_as_float(e < 127 ? (uint32_t)(127 - e) << 23 : 0x00400000u);
   uint32_t w = e4m3x4(make_float4(x.x * down, x.y * down, x.z * down, x.w * down));
   if (!isfinite(x.x)) w |= 0x7Fu;  // what is not finite is stored as NaN
   if (!isfinite(x.y)) w |= 0x7F00u;

@@ -222,3 +222,18 @@ def test_usual_values_held_to_their_size():
                     vs[:] = v
             out, lse, want, _ = attention([0, 1, 33, 160, 700], q, H, Hkv, seed=q, edit=edit)
             near(out, lse, want)
+
+
+# ------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("byte", [248, 251, 253, 254])
+def test_append_behind_a_large_scale(byte):
+    """A block that another writer gave a scale above 2^120 keeps it; new rows are its codes, in the
+    form for single tokens and in that for prompts."""
+    def edit(x, kp, ks, vp, vs, table):
+        ks[:] = byte
+        vs[:] = byte
+        x[:, -256:] = torch.tensor([2.0**120, -2.0**119, 2.0**125, 2.0**117, 1.75 * 2.0**127, 0.0, 1.0, -2.0**118] * 32)
+    for new in ([1, 2], [20, 9]):
+        append([30, 50], new, 1, 1, torch.float32, 0, False, byte, edit=edit)
+    m.mx4_check_status()
