@@ -3,8 +3,8 @@
 //
 // Turn.  Dims below R of a head form pairs (i, i + R/2), or (2 i, 2 i + 1); pair i turns by the
 // angle position * w_i.  w_i comes in turns a position, as a 64-bit binary fraction: the product
-// with the position wraps modulo one turn and is exact to 2^-64 * position turns, so positions of
-// any size keep all bits that an fp32 angle in [-pi, pi) holds.
+// with the position wraps modulo one turn and is exact to 2^-64 * position turns, and goes to the sine
+// as an fp32 number: positions of any size keep its 24 bits, small angles too.
 //
 // Store.  A block of 32 cached tokens of a head shares the scale 2^E, the smallest with
 // amax <= 448 2^E (no value saturates), E >= -127.  Where E grows the block's stored codes are rounded
@@ -100,8 +100,8 @@ __device__ __forceinline__ Turn turn_of(const AppendArgs& a, int64_t pos, int la
     c[e] = 1.f;
     s[e] = 0.f;
     if (in) {
-      const int32_t turns = (int32_t)(((uint64_t)pos * a.phases[i0 + e]) >> 32);  // of 2^-32
-      sincospif((float)turns * 0x1p-31f, &s[e], &c[e]);
+      const int64_t turns = (int64_t)((uint64_t)pos * a.phases[i0 + e]);  // of 2^-64
+      sincospif((float)turns * 0x1p-63f, &s[e], &c[e]);
       c[e] *= a.factor;
       s[e] *= a.factor;
     }

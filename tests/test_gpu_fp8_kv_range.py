@@ -237,3 +237,34 @@ def test_append_behind_a_large_scale(byte):
     for new in ([1, 2], [20, 9]):
         append([30, 50], new, 1, 1, torch.float32, 0, False, byte, edit=edit)
     m.mx4_check_status()
+
+
+@pytest.mark.parametrize("base", [1e4, 5e5, 1e7])
+@pytest.mark.parametrize("inter", [False, True])
+def test_slow_pairs(base, inter):
+    """Angles of pairs that turn by 1e-9 a position keep all bits of an fp32 number."""
+    T, R_ = 10, 128
+    f = m.rope_frequencies(R_, base, "linear", 8.0)[0]
+    ph = m.rope_phases(f)
+    x = torch.zeros((T, 1, 128))
+    a = 2 * torch.arange(64) if inter else torch.arange(64)
+    x[..., a] = 1.0
+    pos = torch.tensor([0, 1, 2, 3, 17, 1000, -1, -5, 123456, 2**31 + 7])
+    i = dict(dtype=torch.int32, device=DEV)
+    pools = [torch.zeros((1, 1, 16384), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    pools += [torch.zeros((1, 1, 4), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    qo = torch.zeros((T, 1, 128), dtype=torch.bfloat16, device=DEV)
+    m.fp8_rope_append(x.to(DEV), x.to(DEV), x.to(DEV), torch.tensor([0, T], **i), torch.zeros((1, 1), **i),
+                      torch.tensor([T], **i), *pools, qo, phases=ph.to(DEV), positions=pos.to(DEV),
+                      interleaved=inter)
+    want = R.turned(x, pos.tolist(), ph.tolist(), inter, 1.0)
+    # bf16; the angle (of -pi .. pi) as an fp32 number and times pi, 2^-23 of it; the sine's 2 ulp
+    turns = torch.tensor([[((int(w) * int(p) + 2**63) % 2**64 - 2**63) / 2.0**64 for w in ph.tolist()]
+                          for p in pos.tolist()], dtype=F64)
+    angle = 2 * math.pi * turns.abs()
+    tol = (2.0**-8 + 2.0**-21) * want.abs()
+    for d in (a, a + 1 if inter else a + 64):
+        tol[:, 0, d] += 2.0**-23 * angle
+    got = qo.cpu().double()
+    bad = (got - want).abs() > tol
+    assert not bad.any(), (bad.nonzero()[:5], got[bad][:5], want[bad][:5])
