@@ -48,10 +48,28 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     return freq.to(torch.float32), grow
 
 
+# 1 / (2 pi) to 144 bits, 24 at a time: a product with half of an fp64 frequency is exact in fp64.
+_TURNS = (10**49 << 144) // (2 * 31415926535897932384626433832795028841971693993751)
+_TURNS = [_TURNS >> (24 * (5 - j)) & 0xFFFFFF for j in range(6)]
+
+
 def rope_phases(frequencies: torch.Tensor) -> torch.Tensor:
     """int64 [n]: frequencies (radians a position) as turns a position, in units of 2^-64 modulo
-    one turn (the bits of an unsigned number), on the same device."""
-    turns = torch.remainder(frequencies.to(torch.float64) / (2 * math.pi), 1.0)
-    high = torch.floor(turns * 2.0**32)  # (powers of two: exact)
-    low = torch.floor((turns * 2.0**32 - high) * 2.0**32)
-    return (high.to(torch.int64) << 32) | low.to(torch.int64)
+    one turn (the bits of an unsigned number), right to a unit, on the same device."""
+    f = frequencies.to(torch.float64)
+    top = f.to(torch.float32).to(torch.float64)
+    high, low = (torch.zeros_like(f, dtype=torch.int64) for _ in range(2))  # units of 2^-32, 2^-64
+    rest = torch.zeros_like(f)
+    for j, digits in enumerate(_TURNS):
+        for part in (top, f - top):  # 24 and 29 bits
+            x = part * digits * 2.0 ** (-24 * (j + 1))
+            x = (x - x.trunc()) * 2.0**32
+            h = x.floor()
+            x = (x - h) * 2.0**32
+            high += h.to(torch.int64)
+            low += x.floor().to(torch.int64)
+            rest += x - x.floor()
+    low += rest.round().to(torch.int64)
+    high += low >> 32
+    high = (high + 2**31) % 2**32 - 2**31
+    return high * 2**32 + (low & 0xFFFFFFFF)

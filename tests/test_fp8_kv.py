@@ -247,3 +247,21 @@ def test_slots():
     step.seq_lens = torch.tensor([258, 400], dtype=torch.int32)
     got = step.slots(cu, 6)
     assert got[0].item() == 5 * 128 + 127 and (got[1:5] >= 7 * 128).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64])
+def test_phases_are_exact(dtype):
+    """Phases to a unit of 2^-64 turns, so that a position of 2^36 keeps an angle to 2^-28 turns:
+    against integers, pi to 60 digits."""
+    from fractions import Fraction
+    pi = Fraction(3141592653589793238462643383279502884197169399375105820974944, 10**60)
+    g = torch.Generator().manual_seed(0)
+    f = torch.cat([m.rope_frequencies(128, b, s, 8.0)[0].to(dtype) for b in (1e4, 1e7) for s in (None, "linear")] + [
+        torch.exp2(40 * torch.rand(200, generator=g, dtype=torch.float64) - 35).to(dtype),
+        torch.tensor([0.0, 1.0, -1.0, -1e-9, 2 * math.pi, 0.3, -0.7, 3.5, 1e4, 2.0**-60, -2.0**-70], dtype=dtype)])
+    got = m.rope_phases(f)
+    assert got.dtype == torch.int64
+    for x, p in zip(f.tolist(), got.tolist()):
+        want = Fraction(x) / (2 * pi) * 2**64
+        d = (want - p + 2**63) % 2**64 - 2**63
+        assert abs(d) <= 1, (x, p, float(d))
