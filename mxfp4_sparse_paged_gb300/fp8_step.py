@@ -51,6 +51,7 @@ class Fp8Step:
         self.blocks, self.first, self.last = blocks, first, last
         self.phases, self.interleaved, self.factor = phases, interleaved, factor
         self.seq_lens = seq_lens.clone()
+        self.now = torch.empty_like(self.seq_lens)  # with the step's tokens; seq_lens follows at its end
         T, Hkv = B * q_per_seq, caches.k_pages.shape[1]
         self.cu_step = torch.arange(0, T + 1, q_per_seq, dtype=torch.int32, device=dev)
         self.q_out = torch.empty((T, heads, HEAD_DIM), dtype=torch.bfloat16, device=dev)
@@ -63,16 +64,17 @@ class Fp8Step:
             need = fp8_block_decode_workspace(T, blocks, heads, Hkv)
         self.ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
 
-    def slots(self, cu_new, T: int) -> torch.Tensor:
-        """int64 [T] page-128 slots of the rows that cu_new gives the sequences' last positions, -1
-        for rows of none.  A row past the table, or where that has no page, gets a slot past the
-        pool, which the insert reports (bad-slot)."""
+    def slots(self, cu_new, T: int, lens=None) -> torch.Tensor:
+        """int64 [T] page-128 slots of the rows that cu_new gives the sequences' last positions (of
+        `lens`, None: seq_lens), -1 for rows of none.  A row past the table, or where that has no
+        page, gets a slot past the pool, which the insert reports (bad-slot)."""
+        lens = self.seq_lens if lens is None else lens
         (B, W), dev = self.block_table.shape, self.block_table.device
         t = torch.arange(T, device=dev, dtype=cu_new.dtype)
         s = torch.searchsorted(cu_new, t, right=True).sub_(1)
         live = (s >= 0) & (s < B)
         s = s.clamp_(0, B - 1)
-        pos = self.seq_lens[s].long() - cu_new[s + 1] + t
+        pos = lens[s].long() - cu_new[s + 1] + t
         page = self.block_table[s, (pos // PAGE_TOKENS).clamp(0, W - 1)].long()
         there = (pos >= 0) & (pos < W * PAGE_TOKENS) & (page >= 0)
         page = torch.where(there, page, self.caches.num_pages)
@@ -80,26 +82,35 @@ class Fp8Step:
 
     def append(self, k, v, idx_k, cu_new, new, q=None, q_out=None, positions=None):
         """`new` (int32 [B]) more tokens a sequence, the rows of k, v [T, Hkv, 128] and idx_k fp32
-        [T, 128] that cu_new (int32 [B + 1]) gives it; q [T, H, 128] turned into q_out."""
+        [T, 128] that cu_new (int32 [B + 1]) gives it; q [T, H, 128] turned into q_out.  A call
+        that is refused (an exception) leaves the lengths as they were."""
+        self._write(k, v, idx_k, cu_new, new, q, q_out, positions)
+        self.seq_lens.copy_(self.now)
+
+    def _write(self, k, v, idx_k, cu_new, new, q, q_out, positions):
+        """The rows of an append; `now` has the lengths with them."""
         c = self.caches
-        self.seq_lens.add_(new)
-        fp8_rope_append(q, k, v, cu_new, self.block_table, self.seq_lens, *c.kv(), q_out,
+        torch.add(self.seq_lens, new, out=self.now)
+        # (index rows first: they can be written again, a block's scale does not go back)
+        fp8_index_insert(idx_k, self.slots(cu_new, k.shape[0], self.now), c.index_scale, c.idx_pages)
+        fp8_rope_append(q, k, v, cu_new, self.block_table, self.now, *c.kv(), q_out,
                         phases=self.phases, positions=positions, interleaved=self.interleaved,
                         factor=self.factor)
-        fp8_index_insert(idx_k, self.slots(cu_new, k.shape[0]), c.index_scale, c.idx_pages)
 
     def run(self, q, k, v, iq, idx_k, positions=None):
         """One step: q [T, H, 128], k, v [T, Hkv, 128] (fp32 or bf16, before the turn), iq bf16 and
-        idx_k fp32 [T, 128].  Returns out, bf16 [T, H, 128]."""
-        c, cached = self.caches, (self.block_table, self.seq_lens)
-        self.append(k, v, idx_k, self.cu_step, self.q, q, self.q_out, positions)
+        idx_k fp32 [T, 128].  Returns out, bf16 [T, H, 128].  A step that is refused (an exception)
+        leaves the lengths as they were: it can be run again."""
+        c, cached = self.caches, (self.block_table, self.now)
+        self._write(k, v, idx_k, self.cu_step, self.q, q, self.q_out, positions)
         if not self.blocks:
             fp8_paged_decode(self.q_out, self.q, *c.kv(), *cached, self.scale, self.out, self.ws,
                              lse=self.lse)
-            return self.out
-        index_block_score_fp8(iq, self.q, c.idx_pages, *cached, c.index_scale, self.scores)
-        block_topk(self.scores, self.seq_lens, self.q, self.block_idx, first=self.first,
-                   last=self.last)
-        fp8_block_decode(self.q_out, self.q, *c.kv(), *cached, self.block_idx, self.scale, self.out,
-                         self.ws, lse=self.lse)
+        else:
+            index_block_score_fp8(iq, self.q, c.idx_pages, *cached, c.index_scale, self.scores)
+            block_topk(self.scores, self.now, self.q, self.block_idx, first=self.first,
+                       last=self.last)
+            fp8_block_decode(self.q_out, self.q, *c.kv(), *cached, self.block_idx, self.scale,
+                             self.out, self.ws, lse=self.lse)
+        self.seq_lens.copy_(self.now)
         return self.out
