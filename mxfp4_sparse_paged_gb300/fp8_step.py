@@ -40,13 +40,15 @@ class Fp8Step:
     """Buffers and calls of decode steps of `block_table`'s sequences, q_per_seq tokens each.
 
     seq_lens (int32 [B], device): tokens cached so far.  blocks: how many blocks a token reads, the
-    first `first` and last `last` in any case (0: all tokens).  phases (int64, rope_phases): how the
+    first `first` and last `last` in any case (0: all tokens, `first` and `last` unused).  phases (int64, rope_phases): how the
     heads turn, None: not at all."""
 
     def __init__(self, caches: Fp8Caches, block_table, seq_lens, q_per_seq: int = 1, heads: int = 16,
                  blocks: int = 16, first: int = 1, last: int = 2, phases=None, interleaved=False,
                  factor: float = 1.0, scale: float = 1.0 / math.sqrt(HEAD_DIM)):
         dev, (B, W) = block_table.device, block_table.shape
+        if blocks < 0 or (blocks > 0 and (first < 0 or last < 0 or first + last > blocks)):
+            raise ValueError(f"blocks = {blocks}, of which the first {first} and the last {last} in any case")
         self.caches, self.block_table, self.q, self.scale = caches, block_table, q_per_seq, scale
         self.blocks, self.first, self.last = blocks, first, last
         self.phases, self.interleaved, self.factor = phases, interleaved, factor

@@ -36,3 +36,16 @@ def test_refused_calls_leave_the_lengths():
             step.append(k, v, idx_k, torch.tensor([0, 3, 5], dtype=torch.int32),
                         torch.tensor([3, 2], dtype=torch.int32))
         assert step.seq_lens.tolist() == [130, 257]
+
+
+@pytest.mark.parametrize("kw", [dict(blocks=2), dict(blocks=1, first=0, last=2), dict(blocks=-1),
+                                dict(blocks=4, first=-1), dict(blocks=4, last=-1), dict(blocks=4, first=3, last=2)])
+def test_choices_of_blocks_are_refused_at_once(kw):
+    with pytest.raises(ValueError, match="blocks"):
+        step_of(**kw)
+
+
+@pytest.mark.parametrize("kw", [dict(blocks=3), dict(blocks=0), dict(blocks=1, first=0, last=1),
+                                dict(blocks=5, first=3, last=2), dict(blocks=2, first=0, last=0)])
+def test_choices_of_blocks(kw):
+    assert step_of(**kw).blocks == kw["blocks"]
