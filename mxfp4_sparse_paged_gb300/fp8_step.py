@@ -8,6 +8,10 @@ which every sequence brings q tokens: their K heads turn by their positions and 
 for each of them (index_block_score_fp8, block_topk), and attention reads those (fp8_block_decode),
 or everything (fp8_paged_decode).  All on the current stream; lengths stay on the device, so a step
 can be captured into a CUDA graph.
+
+A sequence with a new token that has no page (past the table, or no entry of the pool there) sits a
+step or an append out: its length and its K/V rows stay, its results are zeros, and mx4_check_status
+reports it (bad-slot, bad-len).
 """
 from __future__ import annotations
 
@@ -53,9 +57,12 @@ class Fp8Step:
         self.blocks, self.first, self.last = blocks, first, last
         self.phases, self.interleaved, self.factor = phases, interleaved, factor
         self.seq_lens = seq_lens.clone()
-        self.now = torch.empty_like(self.seq_lens)  # with the step's tokens; seq_lens follows at its end
+        self.now = torch.empty_like(self.seq_lens)   # with a step's tokens, 0 where it is sat out
+        self.next = torch.empty_like(self.seq_lens)  # what seq_lens is after it
         T, Hkv = B * q_per_seq, caches.k_pages.shape[1]
         self.cu_step = torch.arange(0, T + 1, q_per_seq, dtype=torch.int32, device=dev)
+        t = torch.arange(T, device=dev)
+        self.row_seq, self.row_back = t // q_per_seq, t % q_per_seq - q_per_seq  # of a step's rows
         self.q_out = torch.empty((T, heads, HEAD_DIM), dtype=torch.bfloat16, device=dev)
         self.out = torch.empty_like(self.q_out)
         self.lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
@@ -71,30 +78,42 @@ class Fp8Step:
         `lens`, None: seq_lens), -1 for rows of none.  A row past the table, or where that has no
         page, gets a slot past the pool, which the insert reports (bad-slot)."""
         lens = self.seq_lens if lens is None else lens
-        (B, W), dev = self.block_table.shape, self.block_table.device
+        B, dev = self.block_table.shape[0], self.block_table.device
         t = torch.arange(T, device=dev, dtype=cu_new.dtype)
         s = torch.searchsorted(cu_new, t, right=True).sub_(1)
         live = (s >= 0) & (s < B)
         s = s.clamp_(0, B - 1)
-        pos = lens[s].long() - cu_new[s + 1] + t
-        page = self.block_table[s, (pos // PAGE_TOKENS).clamp(0, W - 1)].long()
+        return torch.where(live, self._slots(s, t - cu_new[s + 1], lens), -1)
+
+    def _slots(self, seq, back, lens):
+        """Slots of the rows of sequences `seq` at lens + back, past the pool where there is no page."""
+        W = self.block_table.shape[1]
+        pos = lens[seq].long() + back
+        page = self.block_table[seq, (pos // PAGE_TOKENS).clamp(0, W - 1)].long()
         there = (pos >= 0) & (pos < W * PAGE_TOKENS) & (page >= 0)
-        page = torch.where(there, page, self.caches.num_pages)
-        return torch.where(live, page * PAGE_TOKENS + pos % PAGE_TOKENS, -1)
+        return torch.where(there, page, self.caches.num_pages) * PAGE_TOKENS + pos % PAGE_TOKENS
 
     def append(self, k, v, idx_k, cu_new, new, q=None, q_out=None, positions=None):
         """`new` (int32 [B]) more tokens a sequence, the rows of k, v [T, Hkv, 128] and idx_k fp32
         [T, 128] that cu_new (int32 [B + 1]) gives it; q [T, H, 128] turned into q_out.  A call
         that is refused (an exception) leaves the lengths as they were."""
-        self._write(k, v, idx_k, cu_new, new, q, q_out, positions)
-        self.seq_lens.copy_(self.now)
-
-    def _write(self, k, v, idx_k, cu_new, new, q, q_out, positions):
-        """The rows of an append; `now` has the lengths with them."""
-        c = self.caches
         torch.add(self.seq_lens, new, out=self.now)
+        T = k.shape[0]
+        slots = self.slots(cu_new, T, self.now)
+        # rows without a page ahead of each row; a sequence whose rows cross one, or the end, is out
+        before = torch.nn.functional.pad((slots >= self.caches.num_pages * PAGE_TOKENS).cumsum(0), (1, 0))
+        at = cu_new.long()
+        n = before[at.clamp(0, T)]
+        self._write(k, v, idx_k, cu_new, q, q_out, positions, slots, (n[1:] != n[:-1]) | (at[1:] > T))
+        self.seq_lens.copy_(self.next)
+
+    def _write(self, k, v, idx_k, cu_new, q, q_out, positions, slots, out):
+        """The rows of an append to `now` but for the sequences `out`; `next` is what follows."""
+        c = self.caches
+        torch.where(out, self.seq_lens, self.now, out=self.next)
+        self.now.masked_fill_(out, 0)
         # (index rows first: they can be written again, a block's scale does not go back)
-        fp8_index_insert(idx_k, self.slots(cu_new, k.shape[0], self.now), c.index_scale, c.idx_pages)
+        fp8_index_insert(idx_k, slots, c.index_scale, c.idx_pages)
         fp8_rope_append(q, k, v, cu_new, self.block_table, self.now, *c.kv(), q_out,
                         phases=self.phases, positions=positions, interleaved=self.interleaved,
                         factor=self.factor)
@@ -104,7 +123,10 @@ class Fp8Step:
         idx_k fp32 [T, 128].  Returns out, bf16 [T, H, 128].  A step that is refused (an exception)
         leaves the lengths as they were: it can be run again."""
         c, cached = self.caches, (self.block_table, self.now)
-        self._write(k, v, idx_k, self.cu_step, self.q, q, self.q_out, positions)
+        torch.add(self.seq_lens, self.q, out=self.now)
+        slots = self._slots(self.row_seq, self.row_back, self.now)
+        lost = (slots >= c.num_pages * PAGE_TOKENS).view(-1, self.q).any(1)
+        self._write(k, v, idx_k, self.cu_step, q, self.q_out, positions, slots, lost)
         if not self.blocks:
             fp8_paged_decode(self.q_out, self.q, *c.kv(), *cached, self.scale, self.out, self.ws,
                              lse=self.lse)
@@ -114,5 +136,5 @@ class Fp8Step:
                        last=self.last)
             fp8_block_decode(self.q_out, self.q, *c.kv(), *cached, self.block_idx, self.scale,
                              self.out, self.ws, lse=self.lse)
-        self.seq_lens.copy_(self.now)
+        self.seq_lens.copy_(self.next)
         return self.out
