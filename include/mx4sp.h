@@ -545,6 +545,7 @@ int mx4_accept_rows(const int32_t *path, const int32_t *n_accepted, const int32_
  * child_lens[i] = seq_lens[r].  Children take pages in order, child 0 from the top.  A
  * child that finds no page has length 0, a row of -1 and no references
  * (MX4_STATUS_NO_PAGES); so has one of a bad row (MX4_STATUS_BAD_INDEX) or length.
+ * MXFP4 pages alone: those of the 8-bit K/V cache and their scales are not copied.
  *
  * mx4_free_pages: every page of the rows' first ceil(lens / 128) entries loses a
  * reference; pages that reach 0 go on the stack, ascending by id.  The table rows keep

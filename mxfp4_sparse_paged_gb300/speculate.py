@@ -17,7 +17,7 @@ import math
 
 import torch
 
-from . import (HEAD_DIM, PAGE_TOKENS, mx4_accept_rows, mx4_fork_pages, mx4_free_pages,
+from . import (HEAD_DIM, PAGE_BYTES, PAGE_TOKENS, mx4_accept_rows, mx4_fork_pages, mx4_free_pages,
                tree_paged_decode, tree_paged_decode_workspace, verify_drafts)
 
 
@@ -127,6 +127,9 @@ class PageBook:
 
     def fork(self, rows, block_table, seq_lens, caches):
         """(tables int32 [n, W], lens int32 [n]) of children of block_table's rows."""
+        if caches.k_pages.shape[-1] != PAGE_BYTES:
+            raise ValueError("MXFP4 pages alone fork: a page being filled is copied row by row, without "
+                             "the scales that an 8-bit cache keeps beside its pages")
         if caches.fp8_idx_pages is not None:
             raise ValueError("caches with a second index pool do not fork")
         n = rows.shape[0]

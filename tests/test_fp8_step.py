@@ -49,3 +49,14 @@ def test_choices_of_blocks_are_refused_at_once(kw):
                                 dict(blocks=5, first=3, last=2), dict(blocks=2, first=0, last=0)])
 def test_choices_of_blocks(kw):
     assert step_of(**kw).blocks == kw["blocks"]
+
+
+def test_8_bit_caches_do_not_fork():
+    """mx4_fork_pages copies MXFP4 rows: children of an 8-bit cache are refused, not left with a page
+    whose rows and scales are another's."""
+    from mxfp4_sparse_paged_gb300.speculate import PageBook
+    table = torch.tensor([[0, 1]], dtype=torch.int32)
+    book = PageBook(4, table)
+    with pytest.raises(ValueError, match="MXFP4"):
+        book.fork(torch.zeros(2, dtype=torch.int32), table, torch.tensor([130], dtype=torch.int32),
+                  Fp8Caches(4, device="cpu"))
