@@ -5,6 +5,7 @@
 // with a trailing 8704-byte contiguous axis, else an error; "vllm.models.
 // minimax_m3.amd.mono.dispatch", _step_refusal: a reason string instead of a
 // wrong result), the per-device status word, and the kernel launches.
+#include <climits>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -1262,7 +1263,10 @@ struct Words {
     return reinterpret_cast<T*>(static_cast<uintptr_t>(*w++));
   }
   operator int64_t() { return *w++; }
-  operator int() { return static_cast<int>(*w++); }
+  operator int() {  // (past an int: its end, which the calls refuse)
+    const int64_t x = *w++;
+    return static_cast<int>(x < INT_MIN ? INT_MIN : x > INT_MAX ? INT_MAX : x);
+  }
   operator size_t() { return static_cast<size_t>(*w++); }
   operator float() {
     double d;

@@ -265,3 +265,29 @@ def test_phases_are_exact(dtype):
         want = Fraction(x) / (2 * pi) * 2**64
         d = (want - p + 2**63) % 2**64 - 2**63
         assert abs(d) <= 1, (x, p, float(d))
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("block_topk", dict(first=1 << 32)), ("block_topk", dict(last=(1 << 32) + 1)), ("block_topk", dict(k=(1 << 32) + 8)),
+    ("block_topk", dict(qps=(1 << 32) + 1)), ("fp8_rope_append", dict(rot=(1 << 32) + 128)),
+    ("fp8_rope_append", dict(H=(1 << 40) + 16)), ("fp8_rope_append", dict(Hkv=2 - (1 << 32))),
+    ("fp8_block_decode", dict(kb=(1 << 32) + 8)), ("fp8_paged_decode", dict(qps=1 - (1 << 32))),
+    ("index_block_score", dict(qps=(1 << 33) + 1))])
+def test_numbers_past_32_bits_are_refused(lib, name, kw):
+    """The array of words: numbers that would be others in 32 bits."""
+    p, far, third = 1 << 20, 1 << 30, 0.1
+    how, words = {
+        "fp8_rope_append": (m._APPEND, dict(q=p, qs=2048, k=p, kst=256, v=p, vst=256, fp32=0, T=4, H=16, Hkv=2, cu=p, B=4,
+                                            pos=0, ph=p, rot=128, inter=0, factor=1.0, bt=p, W=3, sl=p, kp=p, vp=p,
+                                            ps=32768, hs=16384, P=3, ks=p, vs=p, qo=far, stream=0)),
+        "fp8_paged_decode": (m._PAGED, dict(q=p, T=4, qps=1, H=16, Hkv=2, kp=p, vp=p, ps=32768, hs=16384, P=3, ks=p, vs=p,
+                                            bt=p, B=4, W=3, sl=p, scale=third, out=far, lse=p, ws=p, nws=1 << 40, stream=0)),
+        "fp8_block_decode": (m._BLOCK, dict(q=p, T=4, qps=1, H=16, Hkv=2, kp=p, vp=p, ps=32768, hs=16384, P=3, ks=p, vs=p,
+                                            bt=p, B=4, W=3, sl=p, idx=p, kb=8, scale=third, out=far, lse=p, ws=p,
+                                            nws=1 << 40, stream=0)),
+        "block_topk": (m._TOPK, dict(sc=p, ld=3, sl=p, B=4, qps=1, k=8, first=1, last=2, idx=far, stream=0)),
+        "index_block_score": (m._SCORE, dict(iq=p, T=4, qps=1, ip=p, ps=8704, P=3, bt=p, B=4, W=3, sl=p, sc=p, ld=3, stream=0)),
+    }[name]
+    assert set(kw) <= set(words)
+    assert lib.mx4_call_words(how[0], how[1](*{**words, **kw}.values())) in (-1, -2)
+    assert name in m.mx4_last_error()
