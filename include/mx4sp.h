@@ -687,6 +687,16 @@ int block_topk(const float *scores, int64_t ld_scores, const int32_t *seq_lens, 
                int q_per_seq, int k, int first, int last, int32_t *block_idx, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * mx4_call_words -- a call of the 8-bit cache from one array of 8-byte words, one for each of its
+ * arguments in their order: numbers as int64_t (past an int's range they are refused), addresses as
+ * uint64_t, floats as doubles.  For bindings that convert arguments one by one.
+ *   which  0 fp8_rope_append, 1 fp8_paged_decode, 2 fp8_block_decode, 3 block_topk,
+ *          4 index_block_score, 5 index_block_score_fp8; others are refused
+ * Returns what the call returns.
+ * ------------------------------------------------------------------------- */
+int mx4_call_words(int which, const int64_t *words);
+
+/* ---------------------------------------------------------------------------
  * mx4_check_status -- synchronise `stream`, return MX4_OK if no kernel of this
  * library has flagged bad data on the current device since the last check,
  * else MX4_ERR_BOUNDS with the flagged MX4_STATUS_* bits in *bits (if bits is

@@ -291,3 +291,14 @@ def test_numbers_past_32_bits_are_refused(lib, name, kw):
     assert set(kw) <= set(words)
     assert lib.mx4_call_words(how[0], how[1](*{**words, **kw}.values())) in (-1, -2)
     assert name in m.mx4_last_error()
+
+
+def test_every_exported_call_is_declared(lib):
+    """What the binding calls is in the header."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "mx4sp.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    binding = open(m.__file__).read()
+    for name in set(re.findall(r"lib\.(\w+)\.argtypes", binding)) | set(re.findall(r"_load\(\)\.(\w+)\(", binding)):
+        assert re.search(rf"\b{name}\s*\(", src), name
