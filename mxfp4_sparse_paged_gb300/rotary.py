@@ -58,18 +58,13 @@ def rope_phases(frequencies: torch.Tensor) -> torch.Tensor:
     one turn (the bits of an unsigned number), right to a unit, on the same device."""
     f = frequencies.to(torch.float64)
     top = f.to(torch.float32).to(torch.float64)
-    high, low = (torch.zeros_like(f, dtype=torch.int64) for _ in range(2))  # units of 2^-32, 2^-64
-    rest = torch.zeros_like(f)
-    for j, digits in enumerate(_TURNS):
-        for part in (top, f - top):  # 24 and 29 bits
-            x = part * digits * 2.0 ** (-24 * (j + 1))
-            x = (x - x.trunc()) * 2.0**32
-            h = x.floor()
-            x = (x - h) * 2.0**32
-            high += h.to(torch.int64)
-            low += x.floor().to(torch.int64)
-            rest += x - x.floor()
-    low += rest.round().to(torch.int64)
-    high += low >> 32
-    high = (high + 2**31) % 2**32 - 2**31
-    return high * 2**32 + (low & 0xFFFFFFFF)
+    x = torch.stack([part * (digits * 2.0 ** (-24 * (j + 1)))  # of 24 and 29 bits
+                     for j, digits in enumerate(_TURNS) for part in (top, f - top)])
+    x = (x - x.trunc()) * 2.0**32
+    high = x.floor()
+    x = (x - high) * 2.0**32
+    low = x.floor()
+    rest = (x - low).sum(0).round().to(torch.int64)
+    low = low.to(torch.int64).sum(0) + rest
+    high = high.to(torch.int64).sum(0) + (low >> 32)
+    return ((high + 2**31) % 2**32 - 2**31) * 2**32 + (low & 0xFFFFFFFF)
