@@ -34,9 +34,11 @@
 //     The product of a unit with Ev more than 6 below Er is scaled in fp32 before it is added.
 // Such units, and those where some row does not see all 32 tokens (a sequence's end), take a second form
 // of the step: scores are masked, and values that no row sees, and NaN codes, are kept from the product
-// (clean() below).  Where Ev lies 2^30 above the first unit's, or 2^60 below Er, O gets a unit for which
-// it and the product both stay fp32 numbers, by what the rows hold and what they give weight (renorm()
-// below): a row keeps its sum beside blocks of any scale that it does not see, or gives no weight.
+// (clean() below).  Where Ev lies 2^30 above the first unit's, or 2^60 below Er and the sums have become
+// small against Er, O gets a unit for which it and the product both stay fp32 numbers, by what the rows
+// hold and what they give weight (renorm() below): a row keeps its sum beside blocks of any scale that it
+// does not see, or gives no weight.  The second form is then rare; batches of which a third of the blocks
+// have scales 2^20 below the others take 210 us for 158, of scales 2^119 below 231.
 // The tensor memory path (tcgen05) computes 128-row tiles from shared memory, and puts scores and weights
 // through tensor and shared memory on the way: a form with it took 116 us where this one takes 77
 // (32 sequences of 8192 to 16384 tokens, 64 rows of a KV head).
@@ -71,7 +73,8 @@ constexpr int kRecRow = kHeadDim + 4;            // floats of a row in shared me
 constexpr int kFold = 6;                         // V scales this far below Er go into the weights
 constexpr int kNoScale = -1000;                  // Er before the first unit
 constexpr int kSpan = 30;                        // Er may grow by 2^kSpan beyond the first before renorm()
-constexpr int kFar = 60;                         // V scales this far below Er need it too
+constexpr int kFar = 60;                         // V scales this far below Er need it too, where sums
+constexpr float kHold = 40.f;                    // may have gone down by more than 2^kHold against Er
 constexpr int kTop = 100;                        // it leaves numbers up to 2^kTop
 constexpr int kMost = 29;                        // a unit's product is below 2^kMost: 32 weights of 2^15, 448
 constexpr float kNoRef = -FLT_MAX;               // m before the first logit: no logit lies below it
@@ -219,6 +222,7 @@ struct Rows {
   int er;                              // O is in units of 2^er
   int cap;                             // the largest scale byte that needs no renorm(); -1: rows have Er of
   uint32_t er_at;                      // their own, here
+  float hold;                          // what a row's sum has gone down by against er, at most (log2)
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -233,6 +237,7 @@ struct Rows {
     }
     er = kNoScale;
     cap = 254;
+    hold = 0.f;
   }
   __device__ __forceinline__ int row_er(int r) const {
     int x = er;
@@ -343,6 +348,7 @@ struct Rows {
         above |= top[t][e] - m[t][e] > a.lazy;
       }
     if (__any_sync(0xFFFFFFFFu, above)) {
+      float most = 0.f;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -351,7 +357,8 @@ struct Rows {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
           if (x - m[t][e] > a.lazy) {
-            const float down = ex2((m[t][e] - x) * a.fm);
+            const float by = (x - m[t][e]) * a.fm, down = ex2(-by);
+            if (m[t][e] != kNoRef) most = fmaxf(most, by);
             m[t][e] = x;
             z[t][e] *= down;
 #pragma unroll
@@ -361,10 +368,13 @@ struct Rows {
             }
           }
         }
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+      hold += fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
     }
-    const bool far = General && vb != 255 && (vb > cap || vb - 127 < er - kFar);
+    const bool far = General && vb != 255 && (vb > cap || (vb - 127 < er - kFar && hold > kHold));
     if (vb - 127 > er && vb != 255 && !far) {  // O to the new unit (nothing is in it before the first)
       const float down = er == kNoScale ? 0.f : ex2((float)(er - vb + 127));
+      hold = er == kNoScale ? 0.f : hold + (float)(vb - 127 - er);
       if (er == kNoScale) cap = min(254, vb + kSpan);
       er = vb - 127;
 #pragma unroll
@@ -392,14 +402,19 @@ struct Rows {
     }
     float ev[General ? NT : 1][2];  // 2^(Ev - Er); 0 for rows that see none: a scale of NaN is not theirs
     if constexpr (General) {
-      if (far) renorm(p, vb - 127, lane);
+      if (far) renorm(p, vb - 127, lane, lim);
+      const float all = vb == 255 ? e8m0_to_float(255) : ex2(fminf((float)(vb - 127 - er), 127.f));
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 8 * t + 2 * c + e;
-          ev[t][e] = lim(r) < tb ? 0.f : vb == 255 ? e8m0_to_float(255) : ex2(fminf((float)(vb - 127 - row_er(r)), 127.f));
-        }
+        for (int e = 0; e < 2; ++e) ev[t][e] = lim(8 * t + 2 * c + e) < tb ? 0.f : all;
+      if (cap < 0 && vb != 255) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (lim(8 * t + 2 * c + e) >= tb) ev[t][e] = ex2(fminf((float)(vb - 127 - row_er(8 * t + 2 * c + e)), 127.f));
+      }
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -435,10 +450,12 @@ struct Rows {
 
   // O to a unit in which it, and the product to come of weights p and values of scale 2^ev, is below
   // 2^(kTop + 1): the least such unit, so that what is far smaller stays too.  One for all rows where
-  // theirs lie within 2^40, else one each; rows without weight here do not count the product.
-  __device__ __forceinline__ void renorm(const uint32_t (&p)[4][NT], int ev, int lane) {
+  // theirs lie within 2^90, else one each; rows without weight here do not count the product, and
+  // those that see nothing at all (lim) count for nothing.
+  template <class Lim>
+  __device__ __forceinline__ void renorm(const uint32_t (&p)[4][NT], int ev, int lane, Lim lim) {
     const int c = lane & 3;
-    int want[NT][2], most = kNoScale, least = 1 << 20;
+    int want[NT][2], most = kNoScale, least = 1 << 20, held = 1 << 20;  // held: sums are 2^held at least
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       uint32_t any = p[0][t] | p[1][t] | p[2][t] | p[3][t];  // of row 8 t + g
@@ -453,11 +470,15 @@ struct Rows {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
         int x = kNoScale;
-        if (top > 0.f) x = row_er(8 * t + 2 * c + e) + (int)(__float_as_uint(top) >> 23) - 127 - kTop;
-        if (weight) x = max(x, ev + kMost - kTop);
-        if (x != kNoScale) {
-          x = max(x, kNoScale / 2);  // (below any result)
-          least = min(least, x);
+        if (lim(8 * t + 2 * c + e) >= 0) {
+          if (top > 0.f) {  // (kNoScale / 2: below any result)
+            x = max(row_er(8 * t + 2 * c + e) + (int)(__float_as_uint(top) >> 23) - 127 - kTop, kNoScale / 2);
+            held = min(held, x + kTop);
+          } else if (weight) {
+            held = min(held, ev - 33);  // a weight of 2^-24 and a code of 2^-9
+          }
+          if (weight) x = max(x, ev + kMost - kTop);
+          if (x != kNoScale) least = min(least, x);
         }
         want[t][e] = x;
         most = max(most, x);
@@ -465,7 +486,8 @@ struct Rows {
     }
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     least = __reduce_min_sync(0xFFFFFFFFu, least);
-    const bool same = most - least <= 40;
+    held = __reduce_min_sync(0xFFFFFFFFu, held);
+    const bool same = most - least <= 90;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -489,7 +511,8 @@ struct Rows {
           asm volatile("st.shared.s32 [%0], %1;" ::"r"(er_at + (8 * t + 2 * c + e) * 4), "r"(want[t][e]) : "memory");
     __syncwarp();
     er = most;
-    // (what is now 2^60 to 2^kTop may go down by 2^101 before the next time)
+    hold = (float)(most - held);
+    // (sums of 2^10 and more may go down by 2^101 before the next time)
     cap = !same ? -1 : most == kNoScale ? 254 : min(254, most + 127 + kTop - kMost + kSpan);
   }
 
