@@ -127,7 +127,7 @@ class PageBook:
 
     def fork(self, rows, block_table, seq_lens, caches):
         """(tables int32 [n, W], lens int32 [n]) of children of block_table's rows."""
-        if caches.k_pages.shape[-1] != PAGE_BYTES:
+        if caches.k_pages is not None and caches.k_pages.shape[-1] != PAGE_BYTES:
             raise ValueError("MXFP4 pages alone fork: a page being filled is copied row by row, without "
                              "the scales that an 8-bit cache keeps beside its pages")
         if caches.fp8_idx_pages is not None:
