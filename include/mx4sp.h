@@ -624,10 +624,11 @@ int fp8_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_st
  * block_idx[t*kb ..] lists: block b is tokens 128 b .. 128 b + 127.  Entries may come in any
  * order, a block listed twice counts twice, negative entries are skipped (the padding of
  * block_topk).  Tokens past p hold whatever they hold: they reach no result.  Logits, the sum and
- * the accumulator are fp32 (logits past its range make their row NaN), weights 11 bits of f16
+ * the accumulator are fp32 (a logit of 2^127 and more makes its row NaN), weights 11 bits of f16
  * (relative to the largest of a row down to 2^-16, absolute below; in out one below 2^-27 may count
- * as 0, whatever the scale of its block).  Scales of any two blocks may be any powers apart.  A token that sees nothing (p < 0: a sequence shorter than q, down to
- * empty; no block) gets zeros and an lse of -inf.
+ * as 0, whatever the scale of its block).  Scales of any two blocks may be any powers apart.  A token
+ * that sees nothing (p < 0: a sequence shorter than q, down to empty; no block) gets zeros and an
+ * lse of -inf.
  *
  *   q         bf16 [T, H, 128], contiguous, T = B * q_per_seq, 16-byte aligned
  *   out       bf16 [T, H, 128], 16-byte aligned, not overlapping q; lse fp32 [T, H] or NULL
